@@ -598,6 +598,132 @@ ob_status ob_codec_step(ob_ctx* ctx, int bits, uint64_t t, const void* const* gr
                         void* smsg, float* smsg_scales, const float* v_frozen, float* p,
                         ob_stream_t stream);
 
+/* ----------------------------------------------------------------------
+ * The model's side of a training step.  The calls above take a model's
+ * gradients; these are the operators around its matrix products that
+ * produce them: dropout, the learned relative position bias, and the
+ * attention that uses both, each with its backward pass.  No counterpart
+ * in the pages.  They need no ctx; results are the same bits on every run.
+ * ---------------------------------------------------------------------- */
+
+#define OB_TYPE_F32 0
+#define OB_TYPE_BF16 1
+#define OB_TYPE_F16 2
+
+/* Keep bits.  Element e of an array (its row-major index) belongs to call
+ * e / 8 of Philox4x32-10 with key = seed and counter = (e / 8, offset) as
+ * two 64-bit halves; u = the lowest 15 bits of halfword e % 8 of its output
+ * (low half of word 0 first).  T = p * 32768 rounded to the nearest whole
+ * number (ties to even): the element is dropped iff u < T, a kept one is
+ * scaled by 32768 / (32768 - T), so the mean is exact for the probability
+ * that is really applied.  p = 0 keeps, p = 1 drops everything.  Calls that
+ * must be independent take different offsets. */
+
+/* y[r][c] = residual[r][c] + (kept ? x[r][c] * scale : 0), the keep bit that
+ * of element r * cols + c; residual may be NULL (0).  One rounding to the
+ * type.  A dropped x is not used, whatever it holds.  The mask is never
+ * stored: the backward pass is the same call on dy with the same p, seed and
+ * offset and no residual (whose own gradient is dy).
+ * type: OB_TYPE_*, of all three arrays.  Rows start ldx, ldr and ldy elements
+ * apart (each >= cols); pointers aligned to the element, 16 bytes (and rows
+ * that are multiples of 16 bytes, or contiguous) for the fast path.  y may be
+ * x or residual itself, but must not overlap them otherwise.  rows * cols
+ * < 2^40; 0 is allowed. */
+ob_status ob_dropout(const void* x, size_t ldx, const void* residual, size_t ldr, void* y,
+                     size_t ldy, size_t rows, size_t cols, int type, double p, uint64_t seed,
+                     uint64_t offset, ob_stream_t stream);
+
+/* Buckets of a learned relative position bias.  For the distance d = key -
+ * query: two-sided, num_buckets / 2 buckets for d <= 0, then as many for
+ * d > 0, n = |d|; one-sided, n = max(-d, 0).  With `side` buckets a side and
+ * E = side / 2: bucket n for n < E, then E + floor((side - E) * log(n / E) /
+ * log(max_distance / E)), at most side - 1, evaluated in whole numbers.
+ * first[b]: the first n of bucket b of a side (where neighbours share it,
+ * the upper one holds).  Filled by ob_relpos_init; read only afterwards. */
+#define OB_RELPOS_MAX_SIDE 128
+typedef struct {
+  int num_buckets, max_distance, two_sided, side;
+  int first[OB_RELPOS_MAX_SIDE];
+} ob_relpos;
+
+/* Host only.  num_buckets: 2..128 one-sided, even and 4..256 two-sided;
+ * max_distance in (side / 2, 2^20]. */
+ob_status ob_relpos_init(int num_buckets, int max_distance, int two_sided, ob_relpos* rp);
+
+/* out[h][i][j] = table[bucket(j - i - q_offset)][h], rounded once to
+ * out_type.  table: [num_buckets][H] of table_type, contiguous.  out: H
+ * heads of Lq rows of Lk elements, stride_h and stride_l elements apart.
+ * q_offset: position of query 0 among the keys.  H, Lq and Lk may be 0.
+ * Lq, Lk < 2^30, |q_offset| < 2^30. */
+ob_status ob_relpos_bias(const ob_relpos* rp, const void* table, int table_type, int H,
+                         int64_t Lq, int64_t Lk, int64_t q_offset, void* out, int out_type,
+                         int64_t stride_h, int64_t stride_l, ob_stream_t stream);
+
+/* Its gradient: dtable[b][h] = sum of dout[n][h][i][j] over the N entries
+ * that shared the bias and the pairs of bucket b, summed in fp32 in a fixed
+ * order and rounded once to table_type; every entry is written.
+ * workspace: ob_relpos_workspace_bytes(), 16-byte aligned, contents free. */
+ob_status ob_relpos_workspace_bytes(const ob_relpos* rp, int64_t N, int H, int64_t Lq,
+                                    int64_t Lk, size_t* bytes);
+ob_status ob_relpos_bias_bwd(const ob_relpos* rp, const void* dout, int out_type, int64_t N,
+                             int H, int64_t Lq, int64_t Lk, int64_t stride_n, int64_t stride_h,
+                             int64_t stride_l, int64_t q_offset, void* dtable, int table_type,
+                             void* workspace, size_t workspace_bytes, ob_stream_t stream);
+
+/* Attention over H query heads that share Hkv key/value heads (head h reads
+ * h / (H / Hkv)), for query i and key j of batch entry b on the pairs with
+ * j < kv_len[b] (all of Lk if kv_len is NULL; values outside [0, Lk] are
+ * clamped) and, if causal, j <= i + q_offset:
+ *   S = scale q.k + table[bucket(j - i - q_offset)][h],  P = softmax(S)
+ *   Z = kept ? P * 32768 / (32768 - T) : 0,              o = Z v
+ *   lse = log sum exp S (natural; -inf for a row without keys)
+ * and, given do:
+ *   dv = Z^T do,  dS = P (kept-scaled do.v - rowsum(do o)),
+ *   dq = scale dS k,  dk = scale dS^T q,  dtable = dS summed by buckets.
+ * A row without keys gives o = 0 and adds nothing to any gradient.  K and V
+ * past kv_len are never used, whatever they hold; their dk and dv are 0.
+ * The keep bits are those of an array [B][H][Lq][Lk rounded up to a multiple
+ * of 8] (offset and seed as for ob_dropout).
+ * Products take the inputs' type with fp32 accumulation; softmax statistics
+ * and dtable's sums are fp32; P and dS are rounded to the type as operands of
+ * their products, as is o before rowsum(do o). */
+typedef struct {
+  int type;               /* OB_TYPE_BF16 or OB_TYPE_F16: q, k, v, o, their gradients, table */
+  int B, H, Hkv, D;       /* H a multiple of Hkv; D a multiple of 8, 8..128 */
+  int64_t Lq, Lk;         /* < 2^24; B, Lq or Lk may be 0 */
+  float scale;            /* > 0 */
+  int causal;
+  int64_t q_offset;       /* position of query 0 among the keys, |q_offset| < 2^24 */
+  const ob_relpos* relpos; /* NULL: no bias; max_distance <= OB_ATTN_MAX_DISTANCE */
+  const void* table;      /* [num_buckets][H], contiguous */
+  const int32_t* kv_len;  /* [B], on the device, or NULL */
+  double p;               /* in [0, 1) */
+  uint64_t seed, offset;
+} ob_attn;
+#define OB_ATTN_MAX_DISTANCE 2048
+
+/* Rows of D contiguous elements; entry b, row i, head h starts at
+ * data + b * stride_b + i * stride_l + h * stride_h (elements).  data is
+ * 16-byte aligned and the strides are multiples of 8, positive where their
+ * extent is over 1. */
+typedef struct {
+  void* data;
+  int64_t stride_b, stride_l, stride_h;
+} ob_heads;
+
+/* o and lse [B][H][Lq] (fp32, contiguous; NULL: not written). */
+ob_status ob_attn_fwd(const ob_attn* a, const ob_heads* q, const ob_heads* k, const ob_heads* v,
+                      const ob_heads* o, float* lse, ob_stream_t stream);
+
+/* dq, dk, dv and, with a bias, dtable (NULL: not computed) from do and the
+ * forward pass's o and lse.  workspace: ob_attn_workspace_bytes(), 256-byte
+ * aligned, contents free. */
+ob_status ob_attn_workspace_bytes(const ob_attn* a, size_t* bytes);
+ob_status ob_attn_bwd(const ob_attn* a, const ob_heads* grad_o, const ob_heads* q,
+                      const ob_heads* k, const ob_heads* v, const ob_heads* o, const float* lse,
+                      const ob_heads* dq, const ob_heads* dk, const ob_heads* dv, void* dtable,
+                      void* workspace, size_t workspace_bytes, ob_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -7,6 +7,10 @@ and torch's current CUDA stream becomes the stream handle; every step of
 the path runs in the CUDA kernels of libob.so.  There is no CPU fallback:
 if libob.so is missing or cannot be loaded, `lib()` raises.
 
+The model's side of a training step -- dropout, the bucketed relative
+position bias and the attention that uses both -- is here under its C names
+too; model.py wraps it for torch's autograd.
+
 Two layers:
   * `ob_*` functions with the C names, taking an `ob_ctx` handle, tensors
     (or lists of tensors) and an optional stream;
@@ -15,6 +19,7 @@ Two layers:
     in the order of the method.
 """
 import ctypes as ct
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -24,6 +29,9 @@ OB_OK, OB_ERR_INVALID, OB_ERR_ALIGN, OB_ERR_UNSUPPORTED, OB_ERR_CUDA, OB_ERR_STA
 OB_GRAD_F32, OB_GRAD_BF16 = 0, 1
 OB_MODE_ADAM, OB_MODE_LAMB = 0, 1
 OB_MAX_WORKERS = 64
+OB_TYPE_F32, OB_TYPE_BF16, OB_TYPE_F16 = 0, 1, 2
+OB_RELPOS_MAX_SIDE = 128  # buckets a side of a relative position bias
+OB_ATTN_MAX_DISTANCE = 2048  # max_distance of a bias inside the attention
 OB_NOALLOC_SCRATCH_BYTES = 4 << 20  # the static scratch of ob_compress_noalloc
 OB_FLAG_NO_RATIO_EF = 1 << 0
 OB_FLAG_FROZEN_C = 1 << 1
@@ -40,6 +48,8 @@ EXPORTS = (
     "ob_compress_signm_ls", "ob_server_reduce_db", "ob_lamb_step_signm", "ob_step_db",
     "ob_noalloc_device_error", "ob_error_norm", "ob_plan_step", "ob_codec_step",
     "ob_compress_worker", "ob_server_reduce_part", "ob_reset_errors_rank",
+    "ob_dropout", "ob_relpos_init", "ob_relpos_bias", "ob_relpos_workspace_bytes",
+    "ob_relpos_bias_bwd", "ob_attn_fwd", "ob_attn_workspace_bytes", "ob_attn_bwd",
 )
 
 
@@ -76,6 +86,26 @@ class ob_plan(ct.Structure):
 class ob_layer_state(ct.Structure):
     _fields_ = [(k, ct.c_void_p) for k in
                 ("s", "c_avg", "r_prev", "c_prev", "c_prev2", "c_sum", "c_t")]
+
+
+class ob_relpos(ct.Structure):
+    """The buckets of a relative position bias (ob_relpos_init fills it)."""
+    _fields_ = [("num_buckets", ct.c_int), ("max_distance", ct.c_int), ("two_sided", ct.c_int),
+                ("side", ct.c_int), ("first", ct.c_int * OB_RELPOS_MAX_SIDE)]
+
+
+class ob_attn(ct.Structure):
+    _fields_ = [("type", ct.c_int), ("B", ct.c_int), ("H", ct.c_int), ("Hkv", ct.c_int),
+                ("D", ct.c_int), ("Lq", ct.c_int64), ("Lk", ct.c_int64), ("scale", ct.c_float),
+                ("causal", ct.c_int), ("q_offset", ct.c_int64),
+                ("relpos", ct.POINTER(ob_relpos)), ("table", ct.c_void_p),
+                ("kv_len", ct.c_void_p), ("p", ct.c_double), ("seed", ct.c_uint64),
+                ("offset", ct.c_uint64)]
+
+
+class ob_heads(ct.Structure):
+    _fields_ = [("data", ct.c_void_p), ("stride_b", ct.c_int64), ("stride_l", ct.c_int64),
+                ("stride_h", ct.c_int64)]
 
 
 _lib = None
@@ -132,6 +162,16 @@ def lib():
         L.ob_server_reduce_db.argtypes = [vp] * 10
         L.ob_lamb_step_signm.argtypes = [vp] * 10
         L.ob_step_db.argtypes = [vp] * 15
+        f64, i64 = ct.c_double, ct.c_int64
+        L.ob_dropout.argtypes = [vp, sz, vp, sz, vp, sz, sz, sz, i32, f64, u64, u64, vp]
+        L.ob_relpos_init.argtypes = [i32, i32, i32, vp]
+        L.ob_relpos_bias.argtypes = [vp, vp, i32, i32, i64, i64, i64, vp, i32, i64, i64, vp]
+        L.ob_relpos_workspace_bytes.argtypes = [vp, i64, i32, i64, i64, ct.POINTER(sz)]
+        L.ob_relpos_bias_bwd.argtypes = [vp, vp, i32, i64, i32, i64, i64, i64, i64, i64, i64, vp,
+                                         i32, vp, sz, vp]
+        L.ob_attn_fwd.argtypes = [vp] * 7
+        L.ob_attn_workspace_bytes.argtypes = [vp, ct.POINTER(sz)]
+        L.ob_attn_bwd.argtypes = [vp] * 12 + [sz, vp]
         for name in EXPORTS:
             if name != "ob_last_error":
                 getattr(L, name).restype = ct.c_int
@@ -497,6 +537,241 @@ def ob_adam_step_f16(ctx, send, hs, v_frozen, m, p, stream=None):
     """Adam update from the FP16 server message (m = 0, p unchanged when not sent)."""
     _check(lib().ob_adam_step_f16(ctx, int(bool(send)), _ptr(hs), _ptr(v_frozen), _ptr(m),
                                   _ptr(p), _stream(stream)), ctx)
+
+
+# ---------------------------------------------------------------------------
+# The model's side: dropout, relative position bias, attention
+# ---------------------------------------------------------------------------
+
+@functools.lru_cache(None)
+def _types():
+    import torch
+    return {torch.float32: OB_TYPE_F32, torch.bfloat16: OB_TYPE_BF16,
+            torch.float16: OB_TYPE_F16}
+
+
+def _refuse(what):
+    raise OBError(OB_ERR_INVALID, what)
+
+
+def _type(t, name):
+    code = _types().get(t.dtype)
+    if code is None:
+        _refuse(f"{name}: {t.dtype} is not float32, bfloat16 or float16")
+    return code
+
+
+def _on_device(*named):
+    for name, t in named:
+        if t is not None and not t.is_cuda:
+            _refuse(f"{name} is not a CUDA tensor")
+
+
+def _scratch(nbytes, like, stream):
+    """Device scratch of one call, kept by torch's allocator until `stream` is done with it."""
+    import torch
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if stream is not None:
+        ws.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    return ws
+
+
+def _rows(t, name):
+    """(rows, cols, elements between rows) of a tensor whose last dimension is
+    contiguous and whose leading dimensions are one run of rows."""
+    if t.dim() < 2:
+        if t.dim() == 1 and t.shape[0] > 1 and t.stride(0) != 1:
+            _refuse(f"{name}: the last dimension must be contiguous")
+        return 1, t.numel(), t.numel()
+    cols = t.shape[-1]
+    if cols > 1 and t.stride(-1) != 1:
+        _refuse(f"{name}: the last dimension must be contiguous")
+    rows, ld = 1, None
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = stride
+        elif stride != rows * ld:
+            _refuse(f"{name}: the leading dimensions must be one run of rows")
+        rows *= size
+    return rows, cols, cols if ld is None else ld
+
+
+def ob_dropout(x, y, p, seed, offset, residual=None, stream=None):
+    """y = residual + dropout(x): the mask is drawn from (seed, offset) and
+    never stored; with dy for x and no residual it is the backward pass."""
+    type_ = _type(x, "x")
+    _on_device(("x", x), ("y", y), ("residual", residual))
+    if y.shape != x.shape or y.dtype != x.dtype:
+        _refuse("y must have the shape and the type of x")
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
+        _refuse("residual must have the shape and the type of x")
+    if x.is_contiguous() and y.is_contiguous() and (residual is None or residual.is_contiguous()):
+        rows, ldr = 1, x.numel()
+        cols = ldx = ldy = ldr
+    else:
+        rows, cols, ldx = _rows(x, "x")
+        ldy = _rows(y, "y")[2]
+        ldr = cols if residual is None else _rows(residual, "residual")[2]
+    _check(lib().ob_dropout(x.data_ptr(), ldx, _ptr(residual), ldr, y.data_ptr(), ldy, rows, cols,
+                            type_, p, seed, offset, _stream(stream)))
+
+
+@functools.lru_cache(256)
+def ob_relpos_init(num_buckets, max_distance, two_sided):
+    """The buckets of a relative position bias (host only; the same object for
+    the same arguments: do not write to it)."""
+    rp = ob_relpos()
+    _check(lib().ob_relpos_init(num_buckets, max_distance, int(two_sided), ct.byref(rp)))
+    return rp
+
+
+def _check_table(table, relpos, H, name="table"):
+    if tuple(table.shape) != (relpos.num_buckets, H) or not table.is_contiguous():
+        _refuse(f"{name} must be a contiguous ({relpos.num_buckets}, {H}) tensor, got "
+                f"{tuple(table.shape)}")
+
+
+def _last_contiguous(t, name):
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        _refuse(f"{name}: the last dimension must be contiguous")
+
+
+def ob_relpos_bias(relpos, table, out, q_offset=0, stream=None):
+    """out[h, i, j] = table[bucket(j - i - q_offset), h] for out [H, Lq, Lk]."""
+    _on_device(("table", table), ("out", out))
+    if out.dim() != 3:
+        _refuse("out must be [H, Lq, Lk]")
+    H, Lq, Lk = out.shape
+    _check_table(table, relpos, H)
+    _last_contiguous(out, "out")
+    _check(lib().ob_relpos_bias(ct.byref(relpos), table.data_ptr(), _type(table, "table"), H, Lq,
+                                Lk, q_offset, out.data_ptr(), _type(out, "out"), out.stride(0),
+                                out.stride(1), _stream(stream)))
+
+
+def ob_relpos_workspace_bytes(relpos, N, H, Lq, Lk):
+    """Bytes of scratch ob_relpos_bias_bwd needs."""
+    b = ct.c_size_t()
+    _check(lib().ob_relpos_workspace_bytes(ct.byref(relpos), N, H, Lq, Lk, ct.byref(b)))
+    return b.value
+
+
+def ob_relpos_bias_bwd(relpos, dout, dtable, q_offset=0, workspace=None, stream=None):
+    """dtable[b, h] = the sum of dout [N, H, Lq, Lk] (or [H, Lq, Lk]) over N and the
+    pairs of bucket b.  workspace: a uint8 tensor, or None for one of torch's
+    allocator."""
+    _on_device(("dout", dout), ("dtable", dtable))
+    if dout.dim() == 3:
+        dout = dout.unsqueeze(0)
+    if dout.dim() != 4:
+        _refuse("dout must be [N, H, Lq, Lk] or [H, Lq, Lk]")
+    N, H, Lq, Lk = dout.shape
+    _check_table(dtable, relpos, H, "dtable")
+    _last_contiguous(dout, "dout")
+    if workspace is None:
+        workspace = _scratch(ob_relpos_workspace_bytes(relpos, N, H, Lq, Lk), dout, stream)
+    sn, sh, sl = dout.stride()[:3]
+    _check(lib().ob_relpos_bias_bwd(ct.byref(relpos), dout.data_ptr(), _type(dout, "dout"), N, H,
+                                    Lq, Lk, sn, sh, sl, q_offset, dtable.data_ptr(),
+                                    _type(dtable, "dtable"), _ptr(workspace) or None,
+                                    workspace.numel() * workspace.element_size(),
+                                    _stream(stream)))
+
+
+def _heads(t):
+    b, l, h, _ = t.stride()
+    return ob_heads(t.data_ptr(), b, l, h)
+
+
+def _attn(q, k, v, named, scale, causal, q_offset, relpos, table, kv_len, p, seed, offset):
+    """The ob_attn of a call; `named`: the arrays beside q, k, v and whether each is
+    shaped as the queries (True) or the keys."""
+    if q.dim() != 4 or k.dim() != 4:
+        _refuse("q, k and v must be [batch, length, heads, D]")
+    B, Lq, H, D = q.shape
+    _, Lk, Hkv, _ = k.shape
+    for name, t, as_q in (("q", q, True), ("k", k, False), ("v", v, False)) + named:
+        if t.shape != (q.shape if as_q else (B, Lk, Hkv, D)) or t.dtype != q.dtype:
+            _refuse(f"{name}: {tuple(t.shape)} {t.dtype} does not go with q {tuple(q.shape)} "
+                    f"{q.dtype} and k {tuple(k.shape)}")
+        if not t.is_cuda:
+            _refuse(f"{name} is not a CUDA tensor")
+        if t.stride(3) != 1 and D > 1:
+            _refuse(f"{name}: the last dimension must be contiguous")
+    if (relpos is None) != (table is None):
+        _refuse("relpos and table go together")
+    a = ob_attn(_type(q, "q"), B, H, Hkv, D, Lq, Lk, D ** -0.5 if scale is None else scale,
+                int(causal), Lk - Lq if q_offset is None else q_offset, None, None, None, p, seed,
+                offset)
+    if table is not None:
+        _check_table(table, relpos, H)
+        if table.dtype != q.dtype or not table.is_cuda:
+            _refuse("table must be a CUDA tensor of the type of q")
+        a.relpos, a.table = ct.pointer(relpos), table.data_ptr()
+    if kv_len is not None:
+        import torch
+        if kv_len.shape != (B,) or kv_len.dtype != torch.int32 or not kv_len.is_cuda \
+                or not kv_len.is_contiguous():
+            _refuse("kv_len must be a contiguous int32 CUDA tensor of one length a batch entry")
+        a.kv_len = kv_len.data_ptr()
+    return a
+
+
+def _check_lse(lse, q):
+    import torch
+    B, Lq, H, _ = q.shape
+    if tuple(lse.shape) != (B, H, Lq) or lse.dtype != torch.float32 or not lse.is_cuda \
+            or not lse.is_contiguous():
+        _refuse("lse must be a contiguous float32 CUDA tensor [batch, heads, queries]")
+
+
+def ob_attn_fwd(q, k, v, o, lse=None, scale=None, causal=False, q_offset=None, relpos=None,
+                table=None, kv_len=None, p=0.0, seed=0, offset=0, stream=None):
+    """o = dropout(softmax(scale q k^T + bias)) v for q, o [B, Lq, H, D] and k, v
+    [B, Lk, Hkv, D]; lse [B, H, Lq] is what the backward pass needs.  scale: D ** -0.5
+    by default; q_offset: Lk - Lq."""
+    a = _attn(q, k, v, (("o", o, True),), scale, causal, q_offset, relpos, table, kv_len, p, seed,
+              offset)
+    if lse is not None:
+        _check_lse(lse, q)
+    _check(lib().ob_attn_fwd(ct.byref(a), ct.byref(_heads(q)), ct.byref(_heads(k)),
+                             ct.byref(_heads(v)), ct.byref(_heads(o)), _ptr(lse),
+                             _stream(stream)))
+
+
+def ob_attn_bwd(grad_o, q, k, v, o, lse, dq, dk, dv, dtable=None, scale=None, causal=False,
+                q_offset=None, relpos=None, table=None, kv_len=None, p=0.0, seed=0, offset=0,
+                workspace=None, stream=None):
+    """dq, dk, dv and dtable from grad_o, with the forward call's arguments, o and
+    lse.  workspace: a uint8 tensor, or None for one of torch's allocator."""
+    a = _attn(q, k, v, (("grad_o", grad_o, True), ("o", o, True), ("dq", dq, True),
+                        ("dk", dk, False), ("dv", dv, False)),
+              scale, causal, q_offset, relpos, table, kv_len, p, seed, offset)
+    _check_lse(lse, q)
+    if dtable is not None:
+        if relpos is None:
+            _refuse("dtable is given, but there is no bias")
+        _check_table(dtable, relpos, q.shape[2], "dtable")
+        if dtable.dtype != q.dtype or not dtable.is_cuda:
+            _refuse("dtable must be a CUDA tensor of the type of q")
+    if workspace is None:
+        b = ct.c_size_t()
+        _check(lib().ob_attn_workspace_bytes(ct.byref(a), ct.byref(b)))
+        workspace = _scratch(b.value, q, stream)
+    _check(lib().ob_attn_bwd(ct.byref(a), *(ct.byref(_heads(t)) for t in (grad_o, q, k, v, o)),
+                             lse.data_ptr(), *(ct.byref(_heads(t)) for t in (dq, dk, dv)),
+                             _ptr(dtable), _ptr(workspace) or None,
+                             workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def ob_attn_workspace_bytes(q, k, relpos=None, table=None):
+    """Bytes of scratch ob_attn_bwd needs for these shapes."""
+    a = _attn(q, k, k, (), None, False, 0, relpos, table, None, 0.0, 0, 0)
+    b = ct.c_size_t()
+    _check(lib().ob_attn_workspace_bytes(ct.byref(a), ct.byref(b)))
+    return b.value
 
 
 # ---------------------------------------------------------------------------

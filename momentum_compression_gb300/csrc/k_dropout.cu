@@ -1,0 +1,176 @@
+// Dropout with a mask that is never stored: y = residual + keep * x * scale.
+//
+// Two (with a residual three) streams of elements and one Philox call per
+// eight of them: ten rounds of two wide products and two three-way xors,
+// about 60 issue slots a call, 8 an element with loads and conversions.  At
+// 2 bytes an element and 6.8 TB/s an SM has to issue about 90 of its 128
+// lanes' slots a clock; HBM is the bound for every type.
+#include "elem.cuh"
+#include "keep.cuh"
+#include "model.cuh"
+
+namespace ob {
+namespace {
+
+constexpr int kDropThreads = 256;
+
+// Eight elements in fp32, from and to 16-byte aligned memory.
+template <typename T>
+struct Eight {
+  uint4 a[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+    const uint4* q = reinterpret_cast<const uint4*>(p);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) a[i] = __ldcs(q + i);
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    uint4* q = reinterpret_cast<uint4*>(p);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) q[i] = a[i];
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    if constexpr (sizeof(T) == 4) {
+      memcpy(v, a, 32);
+    } else {
+      const uint32_t w[4] = {a[0].x, a[0].y, a[0].z, a[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2<T>(w[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    if constexpr (sizeof(T) == 4)
+      memcpy(a, v, 32);
+    else
+      a[0] = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]),
+                        pack2<T>(v[6], v[7]));
+  }
+};
+
+__device__ __forceinline__ float drop1(float x, float r, bool keep, float scale) {
+  return keep ? __fmaf_rn(x, scale, r) : r;
+}
+
+// Groups of eight that are 16-byte aligned in every array: one row, or rows
+// of a multiple of eight elements whose starts are aligned.  A thread takes
+// two groups a block apart, so that its loads and two Philox chains overlap.
+template <typename T, bool RES>
+__global__ void __launch_bounds__(kDropThreads) k_dropout_vec(const DropoutArgs a) {
+  const uint64_t groups = (a.n + 7) / 8;
+  const uint64_t g0 = (uint64_t)blockIdx.x * (2 * kDropThreads) + threadIdx.x;
+  const T* x = static_cast<const T*>(a.x);
+  const T* res = static_cast<const T*>(a.residual);
+  T* y = static_cast<T*>(a.y);
+  const uint64_t per_row = a.cols / 8;
+  uint64_t xo[2], ro[2], yo[2];
+  Eight<T> xv[2], rv[2];
+  bool full[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint64_t g = g0 + (uint64_t)u * kDropThreads;
+    if (a.rows == 1) {
+      xo[u] = ro[u] = yo[u] = g * 8;
+    } else {
+      const uint64_t r = groups <= 0xffffffffull ? (uint32_t)g / (uint32_t)per_row : g / per_row;
+      const uint64_t c = (g - r * per_row) * 8;
+      xo[u] = r * a.ldx + c;
+      ro[u] = r * a.ldr + c;
+      yo[u] = r * a.ldy + c;
+    }
+    full[u] = g * 8 + 8 <= a.n;
+    if (full[u]) {
+      xv[u].load(x + xo[u]);
+      if (RES) rv[u].load(res + ro[u]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint64_t g = g0 + (uint64_t)u * kDropThreads;
+    if (g >= groups) break;
+    uint4 w = make_uint4(~0u, ~0u, ~0u, ~0u);
+    if (a.keep.T) w = keep_words(a.keep, g);
+    if (full[u]) {
+      float v[8], r[8];
+      xv[u].get(v);
+      if (RES) rv[u].get(r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = drop1(v[i], RES ? r[i] : 0.0f, kept(w, i, a.keep.T), a.keep.scale);
+      xv[u].set(v);
+      xv[u].store(y + yo[u]);
+    } else {  // the last group of one row
+      const uint32_t b = keep_byte(w, a.keep.T);
+      for (int i = 0; g * 8 + i < a.n; ++i)
+        y[yo[u] + i] = from_f32<T>(drop1(to_f32(x[xo[u] + i]), RES ? to_f32(res[ro[u] + i]) : 0.0f,
+                                         b >> i & 1, a.keep.scale));
+    }
+  }
+}
+
+// Any strides and alignment: a warp takes 256 elements, lane l draws the keep
+// bits of its l-th eight, and in step k the lanes handle elements 32k..32k+31
+// (consecutive addresses) with the bits fetched from the lane that drew them.
+template <typename T, bool RES>
+__global__ void __launch_bounds__(kDropThreads) k_dropout_any(const DropoutArgs a) {
+  const int lane = threadIdx.x & 31;
+  const uint64_t e0 =
+      ((uint64_t)blockIdx.x * (kDropThreads / 32) + threadIdx.x / 32) * 256;
+  if (e0 >= a.n) return;
+  const T* x = static_cast<const T*>(a.x);
+  const T* res = static_cast<const T*>(a.residual);
+  T* y = static_cast<T*>(a.y);
+  float v[8], r[8];
+  uint64_t yo[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint64_t e = e0 + 32 * k + lane;
+    if (e >= a.n) break;
+    const uint64_t row = a.cols == 1 ? e : a.small ? __umul64hi(e, a.magic) : e / a.cols;
+    const uint64_t c = e - row * a.cols;
+    v[k] = to_f32(x[row * a.ldx + c]);
+    r[k] = RES ? to_f32(res[row * a.ldr + c]) : 0.0f;
+    yo[k] = row * a.ldy + c;
+  }
+  uint32_t byte = 0xffu;
+  if (a.keep.T) byte = keep_byte(keep_words(a.keep, e0 / 8 + lane), a.keep.T);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t b = __shfl_sync(0xffffffffu, byte, 4 * k + (lane >> 3));
+    if (e0 + 32 * k + lane < a.n)
+      y[yo[k]] = from_f32<T>(drop1(v[k], r[k], b >> (lane & 7) & 1, a.keep.scale));
+  }
+}
+
+template <typename T>
+cudaError_t launch(const DropoutArgs& a, cudaStream_t s) {
+  auto aligned = [&](const void* p, uint64_t ld) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.rows == 1 || ld % 8 == 0);
+  };
+  const bool vec = aligned(a.x, a.ldx) && aligned(a.y, a.ldy) &&
+                   (!a.residual || aligned(a.residual, a.ldr)) &&
+                   (a.rows == 1 || a.cols % 8 == 0);
+  const uint64_t per = vec ? 16ull * kDropThreads : 8ull * kDropThreads;
+  const dim3 grid((unsigned)((a.n + per - 1) / per));
+  if (vec && a.residual)
+    k_dropout_vec<T, true><<<grid, kDropThreads, 0, s>>>(a);
+  else if (vec)
+    k_dropout_vec<T, false><<<grid, kDropThreads, 0, s>>>(a);
+  else if (a.residual)
+    k_dropout_any<T, true><<<grid, kDropThreads, 0, s>>>(a);
+  else
+    k_dropout_any<T, false><<<grid, kDropThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_dropout(const DropoutArgs& a, int type, cudaStream_t s) {
+  if (type == OB_TYPE_F32) return launch<float>(a, s);
+  if (type == OB_TYPE_BF16) return launch<__nv_bfloat16>(a, s);
+  return launch<__half>(a, s);
+}
+
+}  // namespace ob
