@@ -700,7 +700,7 @@ typedef struct {
   double p;               /* in [0, 1) */
   uint64_t seed, offset;
 } ob_attn;
-#define OB_ATTN_MAX_DISTANCE 2048
+#define OB_ATTN_MAX_DISTANCE 512 /* the staged bias and the bucket sums fit beside the tiles */
 
 /* Rows of D contiguous elements; entry b, row i, head h starts at
  * data + b * stride_b + i * stride_l + h * stride_h (elements).  data is
@@ -723,6 +723,13 @@ ob_status ob_attn_bwd(const ob_attn* a, const ob_heads* grad_o, const ob_heads* 
                       const ob_heads* k, const ob_heads* v, const ob_heads* o, const float* lse,
                       const ob_heads* dq, const ob_heads* dk, const ob_heads* dv, void* dtable,
                       void* workspace, size_t workspace_bytes, ob_stream_t stream);
+
+/* The attention's kernels wait on shared-memory barriers for copies and
+ * products; every wait is bounded (about a second).  One that runs out leaves
+ * a code (as for ob_device_error) in a device word of the library, and its
+ * block's outputs are not valid.  Reads and clears that word (0 = none).
+ * Synchronises `stream`. */
+ob_status ob_attn_device_error(unsigned* code, ob_stream_t stream);
 
 #ifdef __cplusplus
 }

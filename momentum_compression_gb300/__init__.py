@@ -31,7 +31,7 @@ OB_MODE_ADAM, OB_MODE_LAMB = 0, 1
 OB_MAX_WORKERS = 64
 OB_TYPE_F32, OB_TYPE_BF16, OB_TYPE_F16 = 0, 1, 2
 OB_RELPOS_MAX_SIDE = 128  # buckets a side of a relative position bias
-OB_ATTN_MAX_DISTANCE = 2048  # max_distance of a bias inside the attention
+OB_ATTN_MAX_DISTANCE = 512  # max_distance of a bias inside the attention
 OB_NOALLOC_SCRATCH_BYTES = 4 << 20  # the static scratch of ob_compress_noalloc
 OB_FLAG_NO_RATIO_EF = 1 << 0
 OB_FLAG_FROZEN_C = 1 << 1
@@ -50,6 +50,7 @@ EXPORTS = (
     "ob_compress_worker", "ob_server_reduce_part", "ob_reset_errors_rank",
     "ob_dropout", "ob_relpos_init", "ob_relpos_bias", "ob_relpos_workspace_bytes",
     "ob_relpos_bias_bwd", "ob_attn_fwd", "ob_attn_workspace_bytes", "ob_attn_bwd",
+    "ob_attn_device_error",
 )
 
 
@@ -171,6 +172,7 @@ def lib():
                                          i32, vp, sz, vp]
         L.ob_attn_fwd.argtypes = [vp] * 7
         L.ob_attn_workspace_bytes.argtypes = [vp, ct.POINTER(sz)]
+        L.ob_attn_device_error.argtypes = [ct.POINTER(ct.c_uint), vp]
         L.ob_attn_bwd.argtypes = [vp] * 12 + [sz, vp]
         for name in EXPORTS:
             if name != "ob_last_error":
@@ -764,6 +766,13 @@ def ob_attn_bwd(grad_o, q, k, v, o, lse, dq, dk, dv, dtable=None, scale=None, ca
                              lse.data_ptr(), *(ct.byref(_heads(t)) for t in (dq, dk, dv)),
                              _ptr(dtable), _ptr(workspace) or None,
                              workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def ob_attn_device_error(stream=None):
+    """Reads and clears the attention's device error word (0 = none)."""
+    v = ct.c_uint()
+    _check(lib().ob_attn_device_error(ct.byref(v), _stream(stream)))
+    return v.value
 
 
 def ob_attn_workspace_bytes(q, k, relpos=None, table=None):

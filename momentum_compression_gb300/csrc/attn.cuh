@@ -1,6 +1,10 @@
-// Argument block and launchers of the attention.
+// What the attention's forward and backward kernels share: the argument
+// block, the tensor maps of its arrays, the staged bias, the keep bits.
 #pragma once
 
+#include <cuda.h>
+
+#include "elem.cuh"
 #include "model.cuh"
 
 namespace ob {
@@ -27,5 +31,74 @@ struct AttnArgs {
 size_t attn_workspace_bytes(const AttnArgs& a);
 cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_bwd(const AttnArgs& a, cudaStream_t s);
+
+// The device word where a wait that ran out leaves its code.
+cudaError_t attn_error_word(unsigned** word);
+
+// A map of one array whose boxes are `rows` rows of 64 elements of one head:
+// elements past D and rows past L read as zero.
+cudaError_t attn_tensor_map(CUtensorMap* map, const Heads& t, int type, int D, int L, int H, int B,
+                            int rows);
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+#ifdef __CUDACC__
+
+__device__ __forceinline__ int key_count(const int32_t* kv_len, int Lk, int b) {
+  return kv_len ? max(0, min(Lk, kv_len[b])) : Lk;
+}
+
+// ---------------------------------------------------------------------------
+// Bias.  Distances up to -left share one bucket and so do those from right on;
+// between them (and kBiasMargin past either end, so that a block of 32 x 32
+// that touches the range is covered whole) the values of one head, times
+// log2(e), are staged in shared memory.
+// ---------------------------------------------------------------------------
+
+constexpr int kBiasMargin = 64;
+
+constexpr int kBiasMostBytes = 4 * (2 * OB_ATTN_MAX_DISTANCE + 2 * kBiasMargin + 1);
+
+struct BiasSpan {
+  int left, right;
+};
+__host__ __device__ inline BiasSpan bias_span(const ob_relpos& rp) {
+  const int last = rp.first[rp.side - 1];
+  return BiasSpan{last, rp.two_sided ? last : 0};
+}
+__host__ __device__ inline int bias_floats(const ob_relpos& rp) {
+  const BiasSpan s = bias_span(rp);
+  return s.left + s.right + 2 * kBiasMargin + 1;
+}
+
+// tab[d + left + margin], by threads tid of n.
+template <typename T>
+__device__ __forceinline__ void stage_bias(float* tab, const ob_relpos& rp, const int* first,
+                                           const T* table, int H, int h, int tid, int n) {
+  const BiasSpan s = bias_span(rp);
+  const int count = s.left + s.right + 2 * kBiasMargin + 1;
+  for (int t = tid; t < count; t += n) {
+    const int b = bucket_of(first, rp.side, rp.two_sided, t - s.left - kBiasMargin);
+    tab[t] = to_f32(table[(size_t)b * H + h]) * kLog2e;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Keep bits, eight a call: pair t of a call's words as two masks of 16 bits.
+// As fp16 bit patterns u < T can be compared by the packed half pipe, NaN
+// patterns (u > 0x7c00) counting as kept; T itself must then be a number.
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t keep_mask2(uint32_t w, uint32_t T2) {
+  uint32_t m;
+  asm("set.geu.u32.f16x2 %0, %1, %2;" : "=r"(m) : "r"(w & 0x7fff7fffu), "r"(T2));
+  return m;
+}
+__device__ __forceinline__ uint32_t keep_mask2_any(uint32_t w, uint32_t T) {
+  return ((w & 0x7fffu) >= T ? 0xffffu : 0u) | ((w >> 16 & 0x7fffu) >= T ? 0xffff0000u : 0u);
+}
+
+#endif
 
 }  // namespace ob

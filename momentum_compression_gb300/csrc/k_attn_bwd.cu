@@ -38,63 +38,12 @@ __device__ __forceinline__ float dot(const float* x, const T* y, int D) {
   return s;
 }
 
-__device__ __forceinline__ int key_count(const AttnArgs& a, int b) {
-  if (!a.kv_len) return a.Lk;
-  return max(0, min(a.Lk, a.kv_len[b]));
-}
-
 // Whether the pair's weight is kept.
 __device__ __forceinline__ bool pair_kept(const AttnArgs& a, int bh, int i, int j) {
   if (!a.keep.T) return true;
   const uint64_t per_row = (uint64_t)((a.Lk + 7) / 8);
   const uint4 w = keep_words(a.keep, ((uint64_t)bh * a.Lq + i) * per_row + (j >> 3));
   return keep_byte(w, a.keep.T) >> (j & 7) & 1;
-}
-
-template <typename T>
-__global__ void k_fwd(const __grid_constant__ AttnArgs a) {
-  __shared__ int first[OB_RELPOS_MAX_SIDE];
-  __shared__ float qs[kWarps][kMaxD];
-  for (int b = threadIdx.x; b < a.rp.side; b += blockDim.x) first[b] = a.rp.first[b];
-  __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i = blockIdx.x * kWarps + warp, bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
-  if (i >= a.Lq) return;
-  const int hk = h / (a.H / a.Hkv), n = key_count(a, b);
-  for (int d = lane; d < a.D; d += 32) qs[warp][d] = to_f32(row<T>(a.q, b, i, h)[d]);
-  __syncwarp();
-  float m = -INFINITY, l = 0.0f, acc[4] = {0, 0, 0, 0};
-  for (int j0 = 0; j0 < n; j0 += 32) {
-    const int j = j0 + lane;
-    const bool live = j < n && (!a.causal || j <= i + a.q_offset);
-    float s = -INFINITY;
-    if (live) {
-      s = dot(qs[warp], row<T>(a.k, b, j, hk), a.D) * a.scale;
-      if (a.biased)
-        s += load_as_f32(a.table,
-                         (size_t)bucket_of(first, a.rp.side, a.rp.two_sided, j - i - a.q_offset) *
-                                 a.H + h,
-                         a.type);
-    }
-    const float top = fmaxf(m, warp_max(s));
-    const float base = top == -INFINITY ? 0.0f : top;  // nothing yet, or NaN alone
-    const float p = live ? expf(s - base) : 0.0f, less = expf(m - base);
-    m = top;
-    l = l * less + warp_sum(p);
-    const float z = live && pair_kept(a, bh, i, j) ? p : 0.0f;
-    for (int t = 0; t < 4; ++t) acc[t] *= less;
-    for (int k = 0; k < 32 && j0 + k < n; ++k) {
-      const float zk = __shfl_sync(0xffffffffu, z, k);
-      if (zk == 0.0f) continue;
-      const T* v = row<T>(a.v, b, j0 + k, hk);
-      for (int t = 0; t < 4; ++t)
-        if (lane + 32 * t < a.D) acc[t] = __fmaf_rn(zk, to_f32(v[lane + 32 * t]), acc[t]);
-    }
-  }
-  const float inv = l > 0.0f || l != l ? a.keep.scale / l : 0.0f;
-  for (int t = 0; t < 4; ++t)
-    if (lane + 32 * t < a.D) row_out<T>(a.o, b, i, h)[lane + 32 * t] = from_f32<T>(acc[t] * inv);
-  if (a.lse && lane == 0) a.lse[(size_t)bh * a.Lq + i] = l != 0.0f ? m + logf(l) : -INFINITY;
 }
 
 // dq and the bucket sums of its row, part i of partial[h].
@@ -109,7 +58,7 @@ __global__ void k_dq(const __grid_constant__ AttnArgs a) {
   __syncthreads();
   const int i = blockIdx.x * kWarps + warp, bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
   if (i >= a.Lq) return;
-  const int hk = h / (a.H / a.Hkv), n = key_count(a, b);
+  const int hk = h / (a.H / a.Hkv), n = key_count(a.kv_len, a.Lk, b);
   float delta = 0.0f, acc[4] = {0, 0, 0, 0};
   for (int d = lane; d < a.D; d += 32) {
     qs[warp][d] = to_f32(row<T>(a.q, b, i, h)[d]);
@@ -163,7 +112,7 @@ __global__ void k_dkv(const __grid_constant__ AttnArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int j = blockIdx.x * kWarps + warp, b = blockIdx.y / a.Hkv, hk = blockIdx.y % a.Hkv;
   if (j >= a.Lk) return;
-  const int group = a.H / a.Hkv, n = key_count(a, b);
+  const int group = a.H / a.Hkv, n = key_count(a.kv_len, a.Lk, b);
   float dk[4] = {0, 0, 0, 0}, dv[4] = {0, 0, 0, 0};
   if (j < n) {
     for (int d = lane; d < a.D; d += 32) {
@@ -214,12 +163,6 @@ __global__ void k_dkv(const __grid_constant__ AttnArgs a) {
 }
 
 template <typename T>
-cudaError_t fwd(const AttnArgs& a, cudaStream_t s) {
-  k_fwd<T><<<dim3((a.Lq + kWarps - 1) / kWarps, a.B * a.H), 32 * kWarps, 0, s>>>(a);
-  return cudaGetLastError();
-}
-
-template <typename T>
 cudaError_t bwd(const AttnArgs& a, cudaStream_t s) {
   if (a.B && a.Lq)
     k_dq<T><<<dim3((a.Lq + kWarps - 1) / kWarps, a.B * a.H), 32 * kWarps, 0, s>>>(a);
@@ -237,10 +180,6 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t s) {
 
 size_t attn_workspace_bytes(const AttnArgs& a) {
   return a.biased ? (size_t)a.B * a.H * a.Lq * a.rp.num_buckets * sizeof(float) : 0;
-}
-
-cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s) {
-  return a.type == OB_TYPE_BF16 ? fwd<__nv_bfloat16>(a, s) : fwd<__half>(a, s);
 }
 
 cudaError_t launch_attn_bwd(const AttnArgs& a, cudaStream_t s) {

@@ -1,0 +1,430 @@
+// Attention, forward.
+//
+// A block takes 256 queries of one head, 128 for each of two warpgroups (a
+// thread a query), and walks over the keys in tiles of BN.  One thread issues
+// the products on the tensor cores and one the TMA copies:
+//   S = Q K^T        128 x BN in tensor memory, both operands in shared memory
+//   P = softmax-to-be of S, dropped and rounded, over S in tensor memory
+//   O += P V         P from tensor memory, V as it lies (rows are the sum)
+// S of one warpgroup is worked on while the tensor cores run the other's.
+// The softmax is on line: weights are taken relative to a reference m that a
+// row raises (with its sum and its O) only when a score passes it by more
+// than 2^8, so O is hardly ever touched outside the products.
+#include <cmath>
+#include <type_traits>
+
+#include "attn.cuh"
+#include "ob_internal.cuh"
+#include "tc.cuh"
+
+namespace ob {
+namespace {
+
+__device__ unsigned g_attn_error;
+
+constexpr int kRows = 128;      // queries of a warpgroup
+constexpr int kGroups = 2;      // warpgroups
+constexpr int kCompute = kGroups * 128;
+constexpr int kThreads = kCompute + 64;  // and a warp each for products and copies
+constexpr float kRaise = 8.0f;
+
+struct FwdArgs {
+  CUtensorMap q, k, v;
+  int B, H, Hkv, D, Lq, Lk, causal, q_offset, biased, stages;
+  float scale2;  // scale * log2(e)
+  ob_relpos rp;
+  const void* table;
+  const int32_t* kv_len;
+  Keep keep;
+  Heads o;
+  float* lse;
+};
+
+template <int DP, int BN>
+struct FwdShape {
+  static constexpr int kStages = DP == 64 ? 3 : 2;
+  static constexpr uint32_t kQ = kRows * DP * 2;  // bytes of one warpgroup's Q
+  static constexpr uint32_t kTile = BN * DP * 2;
+  static constexpr uint32_t kCols = 2 * BN + 2 * DP;  // tensor memory: S, S, O, O
+  static constexpr uint32_t kAlloc = kCols <= 256 ? 256 : 512;
+  static constexpr uint32_t kBias = kGroups * kQ + 2 * kStages * kTile;  // offset of the bias
+};
+
+struct FwdBars {
+  uint64_t q_full, k_full[3], v_full[3], k_empty[3], v_empty[3], s_full[kGroups], p_full[kGroups];
+  uint64_t drain;
+  uint32_t tmem;
+  int dead;
+  int first[OB_RELPOS_MAX_SIDE];
+};
+
+// All lanes of a warp wait and take the same decision.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, &g_attn_error, kErrWaitFull));
+}
+
+template <typename T, int DP, int BN>
+__global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
+    k_attn_fwd(const __grid_constant__ FwdArgs a) {
+  using S = FwdShape<DP, BN>;
+  constexpr bool kBf16 = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ uint8_t raw[];
+  __shared__ FwdBars bar;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~1023ull);
+  float* bias = reinterpret_cast<float*>(smem + S::kBias);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hkv);
+  // The last queries see the most keys: they start first.
+  const int q0 = ((int)gridDim.x - 1 - (int)blockIdx.x) * (kGroups * kRows);
+  const int keys = key_count(a.kv_len, a.Lk, b);
+  int tiles[kGroups], most = 0;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const int qg = q0 + g * kRows;
+    int n = keys;
+    if (a.causal) n = min(n, min(qg + kRows, a.Lq) + a.q_offset);
+    tiles[g] = qg < a.Lq && n > 0 ? (n + BN - 1) / BN : 0;
+    most = max(most, tiles[g]);
+  }
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bar.q_full, 1);
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&bar.k_full[i], 1);
+      mbar_init(&bar.v_full[i], 1);
+      mbar_init(&bar.k_empty[i], 1);
+      mbar_init(&bar.v_empty[i], 1);
+    }
+    for (int g = 0; g < kGroups; ++g) {
+      mbar_init(&bar.s_full[g], 1);
+      mbar_init(&bar.p_full[g], kRows);
+    }
+    mbar_init(&bar.drain, 1);
+    bar.dead = 0;
+    fence_barrier_init();
+  }
+  if (warp == kCompute / 32) tmem_alloc(&bar.tmem, S::kAlloc);
+  if (a.biased) {
+    for (int i = threadIdx.x; i < a.rp.side; i += kThreads) bar.first[i] = a.rp.first[i];
+    __syncthreads();
+    stage_bias(bias, a.rp, bar.first, static_cast<const T*>(a.table), a.H, h, threadIdx.x, kThreads);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem;
+  volatile int* dead = &bar.dead;
+
+  if (warp == kCompute / 32 + 1) {
+    // ----- copies --------------------------------------------------------
+    if (lane == 0 && most > 0) {
+      uint32_t groups = 0;
+      for (int g = 0; g < kGroups; ++g) groups += tiles[g] > 0;
+      mbar_arrive_expect_tx(&bar.q_full, groups * S::kQ);
+      for (int g = 0; g < kGroups; ++g)
+        if (tiles[g] > 0)
+          for (int x = 0; x < DP / 64; ++x)
+            tma_load4(smem + g * S::kQ + x * (kRows * 128), &a.q, 64 * x, q0 + g * kRows, h, b,
+                      &bar.q_full);
+      int n = 0;
+      for (; n < most; ++n) {
+        const int st = n % S::kStages;
+        const uint32_t par = (n / S::kStages + 1) & 1;
+        uint8_t* kt = smem + kGroups * S::kQ + 2 * st * S::kTile;
+        if (n >= S::kStages && (!mbar_wait(&bar.k_empty[st], par, &g_attn_error, kErrWaitEmpty) || *dead)) break;
+        mbar_arrive_expect_tx(&bar.k_full[st], S::kTile);
+        for (int x = 0; x < DP / 64; ++x)
+          tma_load4(kt + x * (BN * 128), &a.k, 64 * x, n * BN, hk, b, &bar.k_full[st]);
+        if (n >= S::kStages && (!mbar_wait(&bar.v_empty[st], par, &g_attn_error, kErrWaitEmpty) || *dead)) break;
+        mbar_arrive_expect_tx(&bar.v_full[st], S::kTile);
+        for (int x = 0; x < DP / 64; ++x)
+          tma_load4(kt + S::kTile + x * (BN * 128), &a.v, 64 * x, n * BN, hk, b, &bar.v_full[st]);
+      }
+      if (n < most) {  // a wait ran out: let what is in flight land before the block ends
+        *dead = 1;
+        mbar_wait(&bar.q_full, 0, &g_attn_error, kErrDrain);
+        for (int i = max(0, n - S::kStages); i <= n; ++i) {
+          mbar_wait(&bar.k_full[i % S::kStages], (i / S::kStages) & 1, &g_attn_error, kErrDrain);
+          if (i < n)
+            mbar_wait(&bar.v_full[i % S::kStages], (i / S::kStages) & 1, &g_attn_error, kErrDrain);
+        }
+      }
+    }
+  } else if (warp == kCompute / 32) {
+    // ----- products ------------------------------------------------------
+    if (lane == 0 && most > 0) {
+      constexpr uint32_t kShapeS = mma_shape(kBf16, BN, false);
+      constexpr uint32_t kShapeO = mma_shape(kBf16, DP, true);
+      const uint32_t qs = smem_u32(smem), kv = qs + kGroups * S::kQ;
+      const int ksteps = (a.D + 15) / 16;
+      bool ok = mbar_wait(&bar.q_full, 0, &g_attn_error, kErrWaitFull);
+      auto scores = [&](int g, int n) {
+        const uint32_t kt = kv + 2 * (n % S::kStages) * S::kTile;
+        for (int s = 0; s < ksteps; ++s)
+          mma_ss(tmem + g * BN,
+                 desc_k(qs + g * S::kQ + (s >> 2) * (kRows * 128) + (s & 3) * 32),
+                 desc_k(kt + (s >> 2) * (BN * 128) + (s & 3) * 32), kShapeS, s > 0);
+      };
+      ok = ok && mbar_wait(&bar.k_full[0], 0, &g_attn_error, kErrWaitFull);
+      if (ok) {
+        tc_fence_after();
+        for (int g = 0; g < kGroups; ++g)
+          if (tiles[g] > 0) {
+            scores(g, 0);
+            mma_commit(&bar.s_full[g]);
+          }
+        if (S::kStages < most) mma_commit(&bar.k_empty[0]);
+      }
+      for (int n = 0; ok && n < most; ++n) {
+        const int st = n % S::kStages, next = (n + 1) % S::kStages;
+        ok = mbar_wait(&bar.v_full[st], (n / S::kStages) & 1, &g_attn_error, kErrWaitFull);
+        if (ok && n + 1 < most)
+          ok = mbar_wait(&bar.k_full[next], ((n + 1) / S::kStages) & 1, &g_attn_error, kErrWaitFull);
+        const uint32_t vt = kv + (2 * st + 1) * S::kTile;
+        for (int g = 0; ok && g < kGroups; ++g) {
+          if (n >= tiles[g]) continue;
+          ok = mbar_wait(&bar.p_full[g], n & 1, &g_attn_error, kErrWaitFull) && !*dead;
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int s = 0; s < BN / 16; ++s)
+            mma_ts(tmem + 2 * BN + g * DP, tmem + g * BN + s * 8,
+                   desc_mn(vt + s * 2048, BN * 128), kShapeO, n > 0 || s > 0);
+          if (n + 1 < tiles[g]) scores(g, n + 1);
+          mma_commit(&bar.s_full[g]);
+        }
+        // Only where a later copy waits for it: nothing may arrive after the block's end.
+        if (ok && n + 1 + S::kStages < most) mma_commit(&bar.k_empty[next]);
+        if (ok && n + S::kStages < most) mma_commit(&bar.v_empty[st]);
+      }
+      if (!ok) {
+        *dead = 1;
+        mma_commit(&bar.drain);
+        mbar_wait(&bar.drain, 0, &g_attn_error, kErrDrain);
+      }
+    }
+  } else {
+    // ----- softmax: a thread a query -------------------------------------
+    const int g = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const int i = q0 + g * kRows + row;
+    const int wi = q0 + g * kRows + (warp & 3) * 32;  // the warp's first query
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + g * BN, to = tmem + lanes + 2 * BN + g * DP;
+    const int limit = a.causal ? min(keys, i + a.q_offset + 1) : keys;  // keys of this row
+    const int warp_limit = a.causal ? min(keys, wi + a.q_offset + 1) : keys;  // of the first
+    const uint32_t T2 = a.keep.T * 0x10001u;
+    const uint64_t call0 = ((uint64_t)bh * a.Lq + i) * (uint32_t)((a.Lk + 7) / 8);
+    const BiasSpan span = a.biased ? bias_span(a.rp) : BiasSpan{0, 0};
+    const float far_left = a.biased ? bias[0] : 0.0f;
+    const float far_right = a.biased ? bias[span.left + span.right + 2 * kBiasMargin] : 0.0f;
+    float m = -INFINITY, l = 0.0f;
+    bool ok = true;
+
+    // Columns 32 c .. 32 c + 31 of tile n: scores times log2(e), bias, masks.
+    auto scores = [&](float (&x)[32], int n, int c) {
+      uint32_t r[32];
+      tmem_ld32(r, ts + 32 * c);
+      tmem_wait_ld(r);
+      const int j = n * BN + 32 * c;
+      float far = 0.0f;
+      bool near = false;
+      if (a.biased) {
+        const int d = j - wi - a.q_offset;  // of the warp's first row and the first column
+        near = d + 31 > -span.left && d - 31 < span.right;
+        far = d > 0 ? far_right : far_left;
+      }
+      if (near) {
+        const float* t = bias + (j - i - a.q_offset) + span.left + kBiasMargin;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = __fmaf_rn(__uint_as_float(r[k]), a.scale2, t[k]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = __fmaf_rn(__uint_as_float(r[k]), a.scale2, far);
+      }
+      if (j + 32 > warp_limit) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = j + k < limit ? x[k] : -INFINITY;
+      }
+    };
+
+    for (int n = 0; n < tiles[g]; ++n) {
+      ok = warp_wait(&bar.s_full[g], n & 1);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t p[BN / 2];
+      float sum, top;
+      // The first tile is looked over for its maximum; the others are taken
+      // relative to m at once, and again in the rare case that m is passed.
+      bool draw = n > 0;
+#pragma unroll 1
+      for (int pass = 0;; ++pass) {
+        const float base = m == -INFINITY ? 0.0f : m;
+        sum = 0.0f;
+        top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) {
+          float x[32];
+          scores(x, n, c);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) top = fmaxf(top, x[k]);
+          if (!draw) continue;
+          float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            x[k] = exp2_approx(x[k] - base);
+            part[k & 3] += x[k];
+          }
+          sum += (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) p[16 * c + k] = pack2<T>(x[2 * k], x[2 * k + 1]);
+          if (a.keep.T) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint4 w = keep_words(a.keep, call0 + (uint32_t)(n * (BN / 8) + 4 * c + k));
+              const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+              if (a.keep.T <= 0x7c00u) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[16 * c + 4 * k + e] &= keep_mask2(u[e], T2);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[16 * c + 4 * k + e] &= keep_mask2_any(u[e], a.keep.T);
+              }
+            }
+          }
+        }
+        if (pass == 1 || (draw && !__any_sync(0xffffffffu, top > m + kRaise))) break;
+        const float up = fmaxf(m, top);
+        const float less = m == -INFINITY ? 0.0f : exp2_approx(m - up);
+        m = up;
+        l *= less;
+        if (n > 0) {
+#pragma unroll
+          for (int c = 0; c < DP / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld32(r, to + 32 * c);
+            tmem_wait_ld(r);
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              r[k] = __float_as_uint(__uint_as_float(r[k]) * less);
+            tmem_st32(to + 32 * c, r);
+          }
+        }
+        draw = true;
+      }
+      l += sum;
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) tmem_st16(ts + 16 * c, p + 16 * c);
+      tmem_wait_st();
+      if (keys < a.Lk && (n + 1) * BN > keys) {
+        // Rows of V past the length have weight zero, but may hold anything.
+        const int st = n % S::kStages;
+        ok = warp_wait(&bar.v_full[st], (n / S::kStages) & 1);
+        if (!ok) break;
+        uint8_t* vt = smem + kGroups * S::kQ + (2 * st + 1) * S::kTile;
+        const int from = keys - n * BN;  // > 0: the tile holds a key
+        for (int t = threadIdx.x & 127; t < (BN - from) * 8 * (DP / 64); t += 128) {
+          const int r = from + (t >> 3) % (BN - from), x = (t >> 3) / (BN - from);
+          *reinterpret_cast<uint4*>(vt + x * (BN * 128) + r * 128 + (t & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_async_shared();
+      }
+      tc_fence_before();
+      mbar_arrive(&bar.p_full[g]);
+    }
+    if (ok && tiles[g] > 0)
+      ok = warp_wait(&bar.s_full[g], tiles[g] & 1);
+    if (!ok) *dead = 1;
+    tc_fence_after();
+    // ----- o = O / l -------------------------------------------------------
+    const float inv = l > 0.0f || l != l ? a.keep.scale / l : 0.0f;
+    T* out = static_cast<T*>(a.o.data) + b * a.o.b + (int64_t)i * a.o.l + h * a.o.h;
+#pragma unroll
+    for (int c = 0; c < DP / 32; ++c) {
+      uint32_t r[32];
+      if (tiles[g] > 0) {
+        tmem_ld32(r, to + 32 * c);
+        tmem_wait_ld(r);
+      }
+      if (i < a.Lq) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (32 * c + 8 * k >= a.D) break;
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (inv != 0.0f) {
+            uint32_t* u = &w.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              u[e] = pack2<T>(__uint_as_float(r[8 * k + 2 * e]) * inv,
+                              __uint_as_float(r[8 * k + 2 * e + 1]) * inv);
+          }
+          *reinterpret_cast<uint4*>(out + 32 * c + 8 * k) = w;
+        }
+      }
+    }
+    if (a.lse && i < a.Lq)
+      a.lse[(size_t)bh * a.Lq + i] = l != 0.0f ? __fmaf_rn(m, kLn2, logf(l)) : -INFINITY;
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == kCompute / 32) {
+    tc_fence_after();
+    tmem_free(tmem, S::kAlloc);
+  }
+}
+
+template <typename T, int DP, int BN>
+cudaError_t fwd(const AttnArgs& a, cudaStream_t s) {
+  using S = FwdShape<DP, BN>;
+  FwdArgs f{};
+  cudaError_t e = attn_tensor_map(&f.q, a.q, a.type, a.D, a.Lq, a.H, a.B, kRows);
+  // Without keys nothing is read through these; the map still needs an address.
+  if (e == cudaSuccess)
+    e = attn_tensor_map(&f.k, a.Lk ? a.k : a.q, a.type, a.D, a.Lk ? a.Lk : 1, a.Lk ? a.Hkv : 1,
+                        a.Lk ? a.B : 1, BN);
+  if (e == cudaSuccess)
+    e = attn_tensor_map(&f.v, a.Lk ? a.v : a.q, a.type, a.D, a.Lk ? a.Lk : 1, a.Lk ? a.Hkv : 1,
+                        a.Lk ? a.B : 1, BN);
+  if (e != cudaSuccess) return e;
+  f.B = a.B;
+  f.H = a.H;
+  f.Hkv = a.Hkv;
+  f.D = a.D;
+  f.Lq = a.Lq;
+  f.Lk = a.Lk;
+  f.causal = a.causal;
+  f.q_offset = a.q_offset;
+  f.biased = a.biased;
+  f.scale2 = a.scale * kLog2e;
+  f.rp = a.rp;
+  f.table = a.table;
+  f.kv_len = a.kv_len;
+  f.keep = a.keep;
+  f.o = a.o;
+  f.lse = a.lse;
+  const size_t bytes = 1024 + S::kBias + (a.biased ? bias_floats(a.rp) * sizeof(float) : 0);
+  static PerDeviceOnce once;
+  e = once.run([] {
+    return cudaFuncSetAttribute(k_attn_fwd<T, DP, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                1024 + S::kBias + kBiasMostBytes);
+  });
+  if (e != cudaSuccess) return e;
+  const dim3 grid((a.Lq + kGroups * kRows - 1) / (kGroups * kRows), a.B * a.H);
+  k_attn_fwd<T, DP, BN><<<grid, kThreads, bytes, s>>>(f);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t attn_error_word(unsigned** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_attn_error);
+}
+
+cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s) {
+  if (a.type == OB_TYPE_BF16)
+    return a.D <= 64 ? fwd<__nv_bfloat16, 64, 64>(a, s) : fwd<__nv_bfloat16, 128, 128>(a, s);
+  return a.D <= 64 ? fwd<__half, 64, 64>(a, s) : fwd<__half, 128, 128>(a, s);
+}
+
+}  // namespace ob

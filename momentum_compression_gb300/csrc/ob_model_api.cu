@@ -392,4 +392,19 @@ ob_status ob_attn_bwd(const ob_attn* at, const ob_heads* grad_o, const ob_heads*
   return launched(ob::launch_attn_bwd(a, reinterpret_cast<cudaStream_t>(stream)), "attn_bwd");
 }
 
+ob_status ob_attn_device_error(unsigned* code, ob_stream_t stream) {
+  OB_TRACE();
+  if (!code) return failf(OB_ERR_INVALID, "attn_device_error: code is NULL");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  unsigned* word = nullptr;
+  unsigned v = 0;
+  cudaError_t e = ob::attn_error_word(&word);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&v, word, sizeof v, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof v, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return launched(e, "attn_device_error");
+  *code = v;
+  return OB_OK;
+}
+
 }  // extern "C"

@@ -221,6 +221,7 @@ def _attn_run(q, k, v, do, kw):
             got["dtable"] = nan(kw["table"])
         ob.ob_attn_bwd(do, q, k, v, got["o"], got["lse"], got["dq"], got["dk"], got["dv"],
                        dtable=got.get("dtable"), **kw)
+    assert ob.ob_attn_device_error() == 0
     return got
 
 
@@ -251,7 +252,9 @@ CASES = {
     "bias": dict(Lq=128, Lk=128, bias=T5),
     "bias_far": dict(H=1, Lq=600, Lk=700, bias=T5, q_offset=0),
     "bias_16": dict(H=3, Lq=257, Lk=257, bias=(16, 64, True), D=80, dtype=F16),
-    "bias_wide": dict(H=1, Lq=300, Lk=2100, bias=(64, 2048, False), q_offset=1800),
+    "bias_wide": dict(H=1, Lq=300, Lk=2100, bias=(64, 512, False), q_offset=1800),
+    "bias_wide_two": dict(H=1, Lq=900, Lk=1100, bias=(128, 512, True), q_offset=100),
+    "drop_almost_all": dict(Lq=40, Lk=600, p=0.998, dtype=F16),
     "causal": dict(Lq=300, Lk=300, causal=True, D=128),
     "causal_more_keys": dict(Lq=65, Lk=400, causal=True, p=0.2, bias=ONE),
     "causal_fewer_keys": dict(Lq=400, Lk=65, causal=True, p=0.2, bias=ONE),
