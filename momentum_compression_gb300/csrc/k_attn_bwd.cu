@@ -269,49 +269,68 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     }
   } else if (warp == kProducts) {
     // ----- products ------------------------------------------------------
-    if (lane == 0 && total > 0) {
+    if (total > 0) {
       constexpr uint32_t kShapeS = mma_shape(kBf16, kTileRows, false);
       constexpr uint32_t kShapeA = mma_shape(kBf16, DP, true);
-      const uint32_t xs = smem_u32(smem), ys = xs + S::kX, us = xs + 2 * S::kX;
+      const uint32_t leader = elect_lane();
+      const uint32_t xs = smem_u32(smem), us = xs + 2 * S::kX;
+      const uint64_t x_desc = desc_k(xs), u_desc = desc_k(us),
+                     u_rows = desc_mn(us, kTileRows * 128);
       const int ksteps = (a.D + 15) / 16;
-      bool ok = mbar_wait(&bar.x_full, 0, a.err, kErrWaitFull);
-      auto scores = [&](int t) {
-        const int st = t % S::kStages, g = t % G;
-        ok = mbar_wait(&bar.full[st], (t / S::kStages) & 1, a.err, kErrWaitFull) && !*dead;
+      bool ok = warp_wait(&bar.x_full, 0, a.err);
+      // S and dP of a tile: stage st, its phase, group g.
+      auto scores = [&](int st, int par, int g) {
+        ok = warp_wait(&bar.full[st], par, a.err) && !*dead;
         if (!ok) return;
         tc_fence_after();
-        const uint32_t u = us + st * S::kStage, w = u + S::kTile;
-        for (int s = 0; s < ksteps; ++s)
-          mma_ss(tmem + g * 128, desc_k(xs + (s >> 2) * (kRows * 128) + (s & 3) * 32),
-                 desc_k(u + (s >> 2) * (kTileRows * 128) + (s & 3) * 32), kShapeS, s > 0);
-        for (int s = 0; s < ksteps; ++s)
-          mma_ss(tmem + g * 128 + 64, desc_k(ys + (s >> 2) * (kRows * 128) + (s & 3) * 32),
-                 desc_k(w + (s >> 2) * (kTileRows * 128) + (s & 3) * 32), kShapeS, s > 0);
-        mma_commit(&bar.s_full[g]);
+        const uint64_t ud = u_desc + (uint32_t)st * (S::kStage >> 4);
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int s = 0; s < DP / 16; ++s)
+            if (s < ksteps)
+              mma_ss(leader, tmem + g * 128 + 64 * y,
+                     x_desc + ((y * S::kX + (s >> 2) * (kRows * 128) + (s & 3) * 32) >> 4),
+                     ud + ((y * S::kTile + (s >> 2) * (kTileRows * 128) + (s & 3) * 32) >> 4),
+                     kShapeS, s > 0);
+        mma_commit(leader, &bar.s_full[g]);
       };
-      for (int t = 0; ok && t < G && t < total; ++t) scores(t);
+      int lst = 0, lpar = 0, lg = 0;  // of the next tile to score
+      auto advance = [&](int& st, int& par, int& g) {
+        if (++st == S::kStages) st = 0, par ^= 1;
+        if (++g == G) g = 0;
+      };
+      for (int t = 0; ok && t < G && t < total; ++t) {
+        scores(lst, lpar, lg);
+        advance(lst, lpar, lg);
+      }
+      int st = 0, par = 0, g = 0, gpar = 0;
       for (int t = 0; ok && t < total; ++t) {
-        const int st = t % S::kStages, g = t % G;
-        ok = mbar_wait(&bar.p_full[g], (t / G) & 1, a.err, kErrWaitFull) && !*dead;
+        ok = warp_wait(&bar.p_full[g], gpar, a.err) && !*dead;
         if (!ok) break;
         tc_fence_after();
-        const uint32_t u = us + st * S::kStage, w = u + S::kTile;
+        const uint64_t ud = u_rows + (uint32_t)st * (S::kStage >> 4);
+        if (!DQ) {
 #pragma unroll
-        for (int s = 0; s < kTileRows / 16; ++s) {
-          if (!DQ)
-            mma_ts(tmem + S::kAcc, tmem + g * 128 + s * 8, desc_mn(w + s * 2048, kTileRows * 128),
-                   kShapeA, t > 0 || s > 0);
+          for (int s = 0; s < kTileRows / 16; ++s)
+            mma_ts(leader, tmem + S::kAcc, tmem + g * 128 + s * 8,
+                   ud + ((S::kTile + s * 2048) >> 4), kShapeA, t > 0 || s > 0);
         }
 #pragma unroll
         for (int s = 0; s < kTileRows / 16; ++s)
-          mma_ts(tmem + S::kAcc + (DQ ? 0 : DP), tmem + g * 128 + 64 + s * 8,
-                 desc_mn(u + s * 2048, kTileRows * 128), kShapeA, t > 0 || s > 0);
+          mma_ts(leader, tmem + S::kAcc + (DQ ? 0 : DP), tmem + g * 128 + 64 + s * 8,
+                 ud + (s * 2048 >> 4), kShapeA, t > 0 || s > 0);
         // Only where a later copy waits for it: nothing may arrive after the block's end.
-        if (t + S::kStages < total) mma_commit(&bar.empty[st]);
-        if (t + G < total) scores(t + G);
+        if (t + S::kStages < total) mma_commit(leader, &bar.empty[st]);
+        if (t + G < total) {
+          scores(lst, lpar, lg);
+          advance(lst, lpar, lg);
+        }
+        advance(st, par, g);
+        if (g == 0) gpar ^= 1;
       }
       if (!ok) *dead = 1;
-      mma_commit(&bar.done);
+      mma_commit(leader, &bar.done);
       if (!ok) mbar_wait(&bar.done, 0, a.err, kErrDrain);
     }
   } else {

@@ -152,60 +152,69 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
     }
   } else if (warp == kCompute / 32) {
     // ----- products ------------------------------------------------------
-    if (lane == 0 && most > 0) {
+    if (most > 0) {
       constexpr uint32_t kShapeS = mma_shape(kBf16, BN, false);
       constexpr uint32_t kShapeO = mma_shape(kBf16, DP, true);
+      const uint32_t leader = elect_lane();
       const uint32_t qs = smem_u32(smem), kv = qs + kGroups * S::kQ;
+      const uint64_t q_desc = desc_k(qs), k_desc = desc_k(kv),
+                     v_desc = desc_mn(kv + S::kTile, BN * 128);
       const int ksteps = (a.D + 15) / 16;
-      bool ok = mbar_wait(&bar.q_full, 0, &g_attn_error, kErrWaitFull);
-      auto scores = [&](int g, int n) {
-        const uint32_t kt = kv + 2 * (n % S::kStages) * S::kTile;
-        for (int s = 0; s < ksteps; ++s)
-          mma_ss(tmem + g * BN,
-                 desc_k(qs + g * S::kQ + (s >> 2) * (kRows * 128) + (s & 3) * 32),
-                 desc_k(kt + (s >> 2) * (BN * 128) + (s & 3) * 32), kShapeS, s > 0);
+      bool ok = warp_wait(&bar.q_full, 0);
+      auto scores = [&](int g, int st) {
+        const uint64_t qd = q_desc + (uint32_t)g * (S::kQ >> 4);
+        const uint64_t kd = k_desc + (uint32_t)st * (2 * S::kTile >> 4);
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s)
+          if (s < ksteps)
+            mma_ss(leader, tmem + g * BN, qd + (((s >> 2) * (kRows * 128) + (s & 3) * 32) >> 4),
+                   kd + (((s >> 2) * (BN * 128) + (s & 3) * 32) >> 4), kShapeS, s > 0);
       };
-      ok = ok && mbar_wait(&bar.k_full[0], 0, &g_attn_error, kErrWaitFull);
+      ok = ok && warp_wait(&bar.k_full[0], 0);
       if (ok) {
         tc_fence_after();
+#pragma unroll
         for (int g = 0; g < kGroups; ++g)
           if (tiles[g] > 0) {
             scores(g, 0);
-            mma_commit(&bar.s_full[g]);
+            mma_commit(leader, &bar.s_full[g]);
           }
-        if (S::kStages < most) mma_commit(&bar.k_empty[0]);
+        if (S::kStages < most) mma_commit(leader, &bar.k_empty[0]);
       }
+      int st = 0, par = 0;  // of tile n
       for (int n = 0; ok && n < most; ++n) {
-        const int st = n % S::kStages, next = (n + 1) % S::kStages;
-        ok = mbar_wait(&bar.v_full[st], (n / S::kStages) & 1, &g_attn_error, kErrWaitFull);
-        if (ok && n + 1 < most)
-          ok = mbar_wait(&bar.k_full[next], ((n + 1) / S::kStages) & 1, &g_attn_error, kErrWaitFull);
-        const uint32_t vt = kv + (2 * st + 1) * S::kTile;
-        for (int g = 0; ok && g < kGroups; ++g) {
-          if (n >= tiles[g]) continue;
-          ok = mbar_wait(&bar.p_full[g], n & 1, &g_attn_error, kErrWaitFull) && !*dead;
-          if (!ok) break;
+        const int next = st + 1 == S::kStages ? 0 : st + 1, next_par = next ? par : par ^ 1;
+        ok = warp_wait(&bar.v_full[st], par);
+        if (ok && n + 1 < most) ok = warp_wait(&bar.k_full[next], next_par);
+        const uint64_t vd = v_desc + (uint32_t)st * (2 * S::kTile >> 4);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          if (!ok || n >= tiles[g]) continue;
+          ok = warp_wait(&bar.p_full[g], n & 1) && !*dead;
+          if (!ok) continue;
           tc_fence_after();
 #pragma unroll
           for (int s = 0; s < BN / 16; ++s)
-            mma_ts(tmem + 2 * BN + g * DP, tmem + g * BN + s * 8,
-                   desc_mn(vt + s * 2048, BN * 128), kShapeO, n > 0 || s > 0);
-          if (n + 1 < tiles[g]) scores(g, n + 1);
-          mma_commit(&bar.s_full[g]);
+            mma_ts(leader, tmem + 2 * BN + g * DP, tmem + g * BN + s * 8, vd + s * (2048 >> 4),
+                   kShapeO, n > 0 || s > 0);
+          if (n + 1 < tiles[g]) scores(g, next);
+          mma_commit(leader, &bar.s_full[g]);
         }
         // Only where a later copy waits for it: nothing may arrive after the block's end.
-        if (ok && n + 1 + S::kStages < most) mma_commit(&bar.k_empty[next]);
-        if (ok && n + S::kStages < most) mma_commit(&bar.v_empty[st]);
+        if (ok && n + 1 + S::kStages < most) mma_commit(leader, &bar.k_empty[next]);
+        if (ok && n + S::kStages < most) mma_commit(leader, &bar.v_empty[st]);
+        st = next;
+        par = next_par;
       }
       if (!ok) {
         *dead = 1;
-        mma_commit(&bar.drain);
+        mma_commit(leader, &bar.drain);
         mbar_wait(&bar.drain, 0, &g_attn_error, kErrDrain);
       }
     }
   } else {
     // ----- softmax: a thread a query -------------------------------------
-    const int g = warp >> 2;
+    const int g = warp >> 2, mine = g ? tiles[1] : tiles[0];
     const int row = (warp & 3) * 32 + lane;
     const int i = q0 + g * kRows + row;
     const int wi = q0 + g * kRows + (warp & 3) * 32;  // the warp's first query
@@ -248,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
       }
     };
 
-    for (int n = 0; n < tiles[g]; ++n) {
+    for (int n = 0; n < mine; ++n) {
       ok = warp_wait(&bar.s_full[g], n & 1);
       if (!ok) break;
       tc_fence_after();
@@ -333,8 +342,8 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
       tc_fence_before();
       mbar_arrive(&bar.p_full[g]);
     }
-    if (ok && tiles[g] > 0)
-      ok = warp_wait(&bar.s_full[g], tiles[g] & 1);
+    if (ok && mine > 0)
+      ok = warp_wait(&bar.s_full[g], mine & 1);
     if (!ok) *dead = 1;
     tc_fence_after();
     // ----- o = O / l -------------------------------------------------------
@@ -343,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
 #pragma unroll
     for (int c = 0; c < DP / 32; ++c) {
       uint32_t r[32];
-      if (tiles[g] > 0) {
+      if (mine > 0) {
         tmem_ld32(r, to + 32 * c);
         tmem_wait_ld(r);
       }
