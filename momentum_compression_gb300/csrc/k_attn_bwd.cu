@@ -36,7 +36,8 @@ struct GradArgs {
   const void* table;
   const int32_t* kv_len;
   Keep keep;
-  float2* rows;    // [B * H][Lqp]: lse * log2(e) (+inf: no weight), rowsum(do o) / keep.scale
+  float* rows;     // of each tile of 64 queries: 64 times -lse * log2(e) (-inf: no weight),
+                   // then 64 times -rowsum(do o) / keep.scale
   int Lqp;
   Heads out1, out2;  // dq: out2 = dq; dkv: out1 = dv, out2 = dk
   float* partial;    // [H][B * blocks][num_buckets], or null
@@ -48,13 +49,19 @@ struct RowArgs {
   Heads o, grad_o;
   const float* lse;
   float inv_keep;
-  float2* rows;
+  float* rows;
 };
 
 // ---------------------------------------------------------------------------
-// lse and rowsum(do o): 16 lanes a row.  Rows past Lq and rows without keys get
-// lse = +inf, which makes every weight exp2(s - lse) zero.
+// -lse and -rowsum(do o): 16 lanes a row.  Rows past Lq and rows without keys
+// get -lse = -inf, which makes every weight exp2(s - lse) zero.
 // ---------------------------------------------------------------------------
+
+// Where query i of head bh has the first of its two values; the second is
+// kTileRows further.
+__device__ __forceinline__ int64_t row_at(int bh, int Lqp, int i) {
+  return (int64_t)bh * Lqp * 2 + (int64_t)(i / kTileRows) * (2 * kTileRows) + i % kTileRows;
+}
 
 template <typename T>
 __global__ void __launch_bounds__(16 * kRowsPerBlock) k_rows(const RowArgs a) {
@@ -80,12 +87,14 @@ __global__ void __launch_bounds__(16 * kRowsPerBlock) k_rows(const RowArgs a) {
 #pragma unroll
   for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (l == 0) {
-    float lse = INFINITY;
+    float nlse = -INFINITY;
     if (i < a.Lq) {
       const float x = a.lse[(int64_t)bh * a.Lq + i];
-      if (x != -INFINITY) lse = x * kLog2e;
+      if (x != -INFINITY) nlse = -x * kLog2e;
     }
-    a.rows[at] = make_float2(lse, lse == INFINITY ? 0.0f : sum * a.inv_keep);
+    float* to = a.rows + row_at(bh, a.Lqp, i);
+    to[0] = nlse;
+    to[kTileRows] = nlse == -INFINITY ? 0.0f : -sum * a.inv_keep;
   }
 }
 
@@ -257,7 +266,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           tma_load4(to + S::kTile + x * (kTileRows * 128), &a.w, 64 * x, r, hu, b, &bar.full[st]);
         }
         if (!DQ)
-          bulk_g2s(to + 2 * S::kTile, a.rows + (int64_t)(b * a.H + hu) * a.Lqp + r, kTileRows * 8,
+          bulk_g2s(to + 2 * S::kTile, a.rows + row_at(b * a.H + hu, a.Lqp, r), kTileRows * 8,
                    &bar.full[st]);
       }
       if (t < total) {  // a wait ran out: let what is in flight land before the block ends
@@ -340,8 +349,12 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + g * 128, tp = ts + 64;
     const uint64_t per_row = (uint32_t)((a.Lk + 7) / 8);
-    float2 mine = make_float2(INFINITY, 0.0f);
-    if (DQ) mine = a.rows[(int64_t)(b * a.H + h0) * a.Lqp + x];  // Lqp covers every row of the block
+    float nlse = 0.0f, ndelta = 0.0f;  // of the row's query
+    if (DQ) {  // Lqp covers every row of the block
+      const float* r = a.rows + row_at(b * a.H + h0, a.Lqp, x);
+      nlse = r[0];
+      ndelta = r[kTileRows];
+    }
     // The live columns of the row: DQ: below `limit`; else from `limit` on.
     int limit, warp_limit;
     if (DQ) {
@@ -370,19 +383,27 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       const uint64_t rows0 = (uint64_t)(b * a.H + h) * a.Lq;
       for (; ok && t < (hh + 1) * per; t += G) {
         const int st = t % S::kStages;
+        const int c0 = (from + t - hh * per) * kTileRows;  // first column (key or query)
+        uint8_t* stage = smem + 2 * S::kX + st * S::kStage;
+        // The keep bits do not wait for the scores.
+        uint32_t kept[2] = {~0u, ~0u};
+        if (!DQ && a.keep.T) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            kept[u] = keep_column(
+                a.keep,
+                (rows0 + (uint32_t)(c0 + 32 * u + (lane & 7))) * per_row + (uint32_t)(x >> 3),
+                per_row, lane);
+        }
         ok = warp_wait(&bar.s_full[g], (t / G) & 1, a.err);
         if (!ok) break;
         tc_fence_after();
-        const int c0 = (from + t - hh * per) * kTileRows;  // first column (key or query)
-        uint8_t* stage = smem + 2 * S::kX + st * S::kStage;
-        const float4* qrow = reinterpret_cast<const float4*>(stage + 2 * S::kTile);
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          const int col = c0 + 32 * c;
-          uint32_t rs[32], rp[32];
-          float p[32], ds[32];
-          tmem_ld32(rs, ts + 32 * c);
-          tmem_ld32(rp, tp + 32 * c);
+        uint32_t rs[2][16], rp[2][16];
+        tmem_ld16(rs[0], ts);
+        tmem_ld16(rp[0], tp);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {  // 32 columns at a time
+          const int col = c0 + 32 * u;
           // distance of the warp's first row and the first column
           const int d = DQ ? col - wx - a.q_offset : wx - col - a.q_offset;
           bool near = false;
@@ -391,94 +412,120 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
             near = d + 31 > -span.left && d - 31 < span.right;
             far = d > 0 ? far_right : far_left;
           }
-          uint32_t kept = ~0u;
-          if (!DQ && a.keep.T)
-            kept = keep_column(a.keep,
-                               (rows0 + (uint32_t)(col + (lane & 7))) * per_row + (uint32_t)(x >> 3),
-                               per_row, lane);
-          tmem_wait_ld(rs);
-          if (near) {
-            const float* tb = bias + (DQ ? col - x : x - col) - a.q_offset + span.left + kBiasMargin;
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              p[k] = __fmaf_rn(__uint_as_float(rs[k]), a.scale2, DQ ? tb[k] : tb[-k]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) p[k] = __fmaf_rn(__uint_as_float(rs[k]), a.scale2, far);
-          }
-          tmem_wait_ld(rp);
           const bool masked = DQ ? col + 32 > warp_limit : col < warp_limit;
-          if (DQ) {
+          const float* tb = bias + (DQ ? col - x : x - col) - a.q_offset + span.left + kBiasMargin;
+          float ds[32];
+          uint64_t mass = 0;  // sums of p, two lanes of them
 #pragma unroll
-            for (int k = 0; k < 32; ++k) p[k] = exp2_approx(p[k] - mine.x);
+          for (int hf = 0; hf < 2; ++hf) {
+            const int cc = 2 * u + hf;  // 16 columns; the next 16 are on their way meanwhile
+            tmem_wait_ld(rs[cc & 1]);
+            tmem_wait_ld(rp[cc & 1]);
+            if (cc < 3) {
+              tmem_ld16(rs[~cc & 1], ts + 16 * (cc + 1));
+              tmem_ld16(rp[~cc & 1], tp + 16 * (cc + 1));
+            }
+            const uint32_t(&vs)[16] = rs[cc & 1];
+            const uint32_t(&vp)[16] = rp[cc & 1];
+            const uint64_t scale2 = pair(a.scale2, a.scale2);
+            uint64_t shift[8];  // bias - lse
+            if (near) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int n = 16 * hf + 2 * k;
+                shift[k] = DQ ? pair(tb[n], tb[n + 1]) : pair(tb[-n], tb[-n - 1]);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) shift[k] = pair(far, far);
+            }
+            float p[16], z[16];
+            const ulonglong2* qlse =
+                reinterpret_cast<const ulonglong2*>(stage + 2 * S::kTile) + 4 * cc;
+            const ulonglong2* qdelta = qlse + kTileRows / 4;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              uint64_t nl = pair(nlse, nlse);
+              if (!DQ) {
+                const ulonglong2 four = qlse[k >> 1];
+                nl = k & 1 ? four.y : four.x;
+              }
+              const uint64_t e =
+                  fma2(pair(vs[2 * k], vs[2 * k + 1]), scale2, add2(shift[k], nl));
+              unpair(e, &p[2 * k], &p[2 * k + 1]);
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) p[k] = exp2_approx(p[k]);
             if (masked) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) p[k] = col + k < limit ? p[k] : 0.0f;
+              for (int k = 0; k < 16; ++k)
+                p[k] = (DQ ? col + 16 * hf + k < limit : col + 16 * hf + k >= limit) ? p[k] : 0.0f;
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float z[8];
+            for (int k = 0; k < 16; ++k) z[k] = p[k];
+            if (a.keep.T) {
+              if (DQ) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) z[e] = p[8 * k + e];
-              if (a.keep.T) {
-                const uint4 w = keep_words(
-                    a.keep, (rows0 + (uint32_t)x) * per_row + (uint32_t)((col >> 3) + k));
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                for (int k = 0; k < 2; ++k) {
+                  const uint4 w = keep_words(a.keep, (rows0 + (uint32_t)x) * per_row +
+                                                         (uint32_t)((col >> 3) + 2 * hf + k));
+                  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  keep_pair(u[e], a.keep.T, z[2 * e], z[2 * e + 1], &z[2 * e], &z[2 * e + 1]);
+                  for (int e = 0; e < 4; ++e)
+                    keep_pair(v[e], a.keep.T, p[8 * k + 2 * e], p[8 * k + 2 * e + 1],
+                              &z[8 * k + 2 * e], &z[8 * k + 2 * e + 1]);
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) z[k] = kept[u] >> (16 * hf + k) & 1 ? p[k] : 0.0f;
               }
+            }
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                ds[8 * k + e] = __fmaf_rn(z[e], __uint_as_float(rp[8 * k + e]),
-                                          -(p[8 * k + e] * mine.y));
+            for (int k = 0; k < 8; ++k) {
+              uint64_t nd = pair(ndelta, ndelta);
+              if (!DQ) {
+                const ulonglong2 four = qdelta[k >> 1];
+                nd = k & 1 ? four.y : four.x;
+              }
+              const uint64_t pp = pair(p[2 * k], p[2 * k + 1]);
+              unpair(fma2(pair(z[2 * k], z[2 * k + 1]), pair(vp[2 * k], vp[2 * k + 1]), mul2(pp, nd)),
+                     &ds[16 * hf + 2 * k], &ds[16 * hf + 2 * k + 1]);
+              if (sums && !near) mass = add2(mass, pp);
             }
             if (masked) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) ds[k] = col + k < limit ? ds[k] : 0.0f;
-            }
-          } else {
-            float z[32];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float4 r = qrow[16 * c + k];  // two queries
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int n = 2 * k + e;
-                const float lse = e ? r.z : r.x, delta = e ? r.w : r.y;
-                p[n] = exp2_approx(p[n] - lse);
-                if (masked) p[n] = col + n >= limit ? p[n] : 0.0f;
-                z[n] = kept >> n & 1 ? p[n] : 0.0f;
-                ds[n] = __fmaf_rn(z[n], __uint_as_float(rp[n]), -(p[n] * delta));
-                if (masked) ds[n] = col + n >= limit ? ds[n] : 0.0f;
+              for (int k = 0; k < 16; ++k) {
+                float& e = ds[16 * hf + k];
+                e = (DQ ? col + 16 * hf + k < limit : col + 16 * hf + k >= limit) ? e : 0.0f;
               }
             }
-            uint32_t o[16];
+            uint32_t o[8];
+            if (!DQ) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
-            tmem_st16(ts + 16 * c, o);
+              for (int k = 0; k < 8; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
+              tmem_st8(ts + 8 * cc, o);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              o[k] = pack2<T>(ds[16 * hf + 2 * k], ds[16 * hf + 2 * k + 1]);
+            tmem_st8(tp + 8 * cc, o);
           }
-          uint32_t o[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = pack2<T>(ds[2 * k], ds[2 * k + 1]);
-          tmem_st16(tp + 16 * c, o);
           if (sums) {
-            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            uint64_t s2 = 0;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) s[k & 3] += ds[k];
-            const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+            for (int k = 0; k < 16; ++k) s2 = add2(s2, pair(ds[2 * k], ds[2 * k + 1]));
+            float s0, s1;
+            unpair(s2, &s0, &s1);
+            const float sum = s0 + s1;
             eps += sum;
             if (!near) {
-              float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-              for (int k = 0; k < 32; ++k) w[k & 3] += p[k];
-              const float mass = (w[0] + w[1]) + (w[2] + w[3]);
+              unpair(mass, &s0, &s1);
               if (d > 0) {
                 far_r += sum;
-                mass_r += mass;
+                mass_r += s0 + s1;
               } else {
                 far_l += sum;
-                mass_l += mass;
+                mass_l += s0 + s1;
               }
             } else {
               // Sums down the diagonals of the 32 x 32 block: a running sum moves one
@@ -558,7 +605,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
 #pragma unroll
       for (int k = 0; k < G; ++k) e += bar.eps[k][row];
       if (g == 0)
-        a.rows[(int64_t)(b * a.H + h0) * a.Lqp + x] = make_float2(mine.x, mine.y + e);
+        a.rows[row_at(b * a.H + h0, a.Lqp, x) + kTileRows] = ndelta - e;
       far_l -= e * mass_l;
       far_r -= e * mass_r;
 #pragma unroll
@@ -636,7 +683,7 @@ cudaError_t grad(const AttnArgs& a, GradArgs f, cudaStream_t s) {
 int padded(int Lq) { return (Lq + kRows - 1) / kRows * kRows; }
 
 size_t rows_bytes(const AttnArgs& a) {
-  return ((size_t)a.B * a.H * padded(a.Lq) * sizeof(float2) + 255) / 256 * 256;
+  return ((size_t)a.B * a.H * padded(a.Lq) * 2 * sizeof(float) + 255) / 256 * 256;
 }
 
 template <typename T>
@@ -659,7 +706,7 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t s) {
   f.table = a.table;
   f.kv_len = a.kv_len;
   f.keep = a.keep;
-  f.rows = static_cast<float2*>(a.workspace);
+  f.rows = static_cast<float*>(a.workspace);
   f.Lqp = padded(a.Lq);
   if (a.Lq) {
     RowArgs r{a.B, a.H, a.D, a.Lq, f.Lqp, a.o, a.grad_o, a.lse, 1.0f / a.keep.scale, f.rows};
