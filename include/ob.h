@@ -697,7 +697,7 @@ typedef struct {
   const ob_relpos* relpos; /* NULL: no bias; max_distance <= OB_ATTN_MAX_DISTANCE */
   const void* table;      /* [num_buckets][H], contiguous */
   const int32_t* kv_len;  /* [B], on the device, or NULL */
-  double p;               /* in [0, 1) */
+  double p;               /* in [0, 255/256] */
   uint64_t seed, offset;
 } ob_attn;
 #define OB_ATTN_MAX_DISTANCE 512 /* the staged bias and the bucket sums fit beside the tiles */

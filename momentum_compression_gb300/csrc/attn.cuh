@@ -85,18 +85,18 @@ __device__ __forceinline__ void stage_bias(float* tab, const ob_relpos& rp, cons
 }
 
 // ---------------------------------------------------------------------------
-// Keep bits, eight a call: pair t of a call's words as two masks of 16 bits.
-// As fp16 bit patterns u < T can be compared by the packed half pipe, NaN
-// patterns (u > 0x7c00) counting as kept; T itself must then be a number.
+// Keep bits, eight a call: a word's two as masks of 16 bits.  Non-negative
+// bf16 patterns are ordered like whole numbers, so u < T is one compare of the
+// packed 16-bit pipe for both; the NaN patterns, above every number, count as
+// kept (geu), and T is at most infinity's, 0x7f80.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t keep_mask2(uint32_t w, uint32_t T2) {
   uint32_t m;
-  asm("set.geu.u32.f16x2 %0, %1, %2;" : "=r"(m) : "r"(w & 0x7fff7fffu), "r"(T2));
+  asm("{\n\t.reg .b32 u;\n\tabs.bf16x2 u, %1;\n\tset.geu.u32.bf16x2 %0, u, %2;\n\t}"
+      : "=r"(m)
+      : "r"(w), "r"(T2));
   return m;
-}
-__device__ __forceinline__ uint32_t keep_mask2_any(uint32_t w, uint32_t T) {
-  return ((w & 0x7fffu) >= T ? 0xffffu : 0u) | ((w >> 16 & 0x7fffu) >= T ? 0xffff0000u : 0u);
 }
 
 #endif

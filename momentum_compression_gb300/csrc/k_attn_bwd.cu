@@ -132,19 +132,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsign
 }
 
 // The pair of weights whose halfwords are w, dropped ones as zero.
-__device__ __forceinline__ void keep_pair(uint32_t w, uint32_t T, float p0, float p1, float* z0,
+__device__ __forceinline__ void keep_pair(uint32_t w, uint32_t T2, float p0, float p1, float* z0,
                                           float* z1) {
-  if (T <= 0x7c00u) {
-    asm("{\n\t.reg .pred a, b;\n\t"
-        "setp.geu.f16x2 a|b, %2, %3;\n\t"
-        "selp.f32 %0, %4, 0f00000000, a;\n\t"
-        "selp.f32 %1, %5, 0f00000000, b;\n\t}"
-        : "=f"(*z0), "=f"(*z1)
-        : "r"(w & 0x7fff7fffu), "r"(T * 0x10001u), "f"(p0), "f"(p1));
-  } else {
-    *z0 = (w & 0x7fffu) >= T ? p0 : 0.0f;
-    *z1 = (w >> 16 & 0x7fffu) >= T ? p1 : 0.0f;
-  }
+  asm("{\n\t.reg .pred a, b;\n\t.reg .b32 u;\n\t"
+      "abs.bf16x2 u, %2;\n\t"
+      "setp.geu.bf16x2 a|b, u, %3;\n\t"
+      "selp.f32 %0, %4, 0f00000000, a;\n\t"
+      "selp.f32 %1, %5, 0f00000000, b;\n\t}"
+      : "=f"(*z0), "=f"(*z1)
+      : "r"(w), "r"(T2), "f"(p0), "f"(p1));
 }
 
 // Keep bits of 32 queries for the thread's key, from calls that hold eight
@@ -162,9 +158,7 @@ __device__ __forceinline__ uint32_t keep_column(const Keep& keep, uint64_t call0
     uint32_t& to = k < 2 ? x : y;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint32_t m = keep.T <= 0x7c00u ? keep_mask2(u[e], keep.T * 0x10001u)
-                                           : keep_mask2_any(u[e], keep.T);
-      to |= m & (0x00020001u << (2 * e + 8 * (k & 1)));
+      to |= keep_mask2(u[e], keep.T * 0x10001u) & (0x00020001u << (2 * e + 8 * (k & 1)));
     }
   }
   // even keys are in the low halves, odd ones in the high halves
@@ -179,7 +173,7 @@ __device__ __forceinline__ uint32_t keep_column(const Keep& keep, uint64_t call0
   return v;
 }
 
-template <typename T, int DP, bool DQ>
+template <typename T, int DP, bool DQ, bool DROP>
 __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     k_attn_grad(const __grid_constant__ GradArgs a) {
   using S = GradShape<DP, DQ>;
@@ -355,6 +349,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       nlse = r[0];
       ndelta = r[kTileRows];
     }
+    const uint32_t T2 = a.keep.T * 0x10001u;
     // The live columns of the row: DQ: below `limit`; else from `limit` on.
     int limit, warp_limit;
     if (DQ) {
@@ -387,7 +382,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
         uint8_t* stage = smem + 2 * S::kX + st * S::kStage;
         // The keep bits do not wait for the scores.
         uint32_t kept[2] = {~0u, ~0u};
-        if (!DQ && a.keep.T) {
+        if (!DQ && DROP) {
 #pragma unroll
           for (int u = 0; u < 2; ++u)
             kept[u] = keep_column(
@@ -428,31 +423,35 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
             const uint32_t(&vs)[16] = rs[cc & 1];
             const uint32_t(&vp)[16] = rp[cc & 1];
             const uint64_t scale2 = pair(a.scale2, a.scale2);
-            uint64_t shift[8];  // bias - lse
+            const ulonglong2* qlse =  // two pairs of queries each
+                reinterpret_cast<const ulonglong2*>(stage + 2 * S::kTile) + 4 * cc;
+            const ulonglong2* qdelta = qlse + kTileRows / 4;
+            float p[16];
+            auto score = [&](int k, uint64_t shift) {
+              unpair(fma2(pair(vs[2 * k], vs[2 * k + 1]), scale2, shift), &p[2 * k], &p[2 * k + 1]);
+            };
             if (near) {
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const int n = 16 * hf + 2 * k;
-                shift[k] = DQ ? pair(tb[n], tb[n + 1]) : pair(tb[-n], tb[-n - 1]);
+                const uint64_t bias2 = DQ ? pair(tb[n], tb[n + 1]) : pair(tb[-n], tb[-n - 1]);
+                if (DQ) {
+                  score(k, add2(bias2, pair(nlse, nlse)));
+                } else {
+                  const ulonglong2 four = qlse[k >> 1];
+                  score(k, add2(bias2, k & 1 ? four.y : four.x));
+                }
               }
+            } else if (DQ) {
+              const float f = far + nlse;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) score(k, pair(f, f));
             } else {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) shift[k] = pair(far, far);
-            }
-            float p[16], z[16];
-            const ulonglong2* qlse =
-                reinterpret_cast<const ulonglong2*>(stage + 2 * S::kTile) + 4 * cc;
-            const ulonglong2* qdelta = qlse + kTileRows / 4;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              uint64_t nl = pair(nlse, nlse);
-              if (!DQ) {
+              for (int k = 0; k < 8; ++k) {
                 const ulonglong2 four = qlse[k >> 1];
-                nl = k & 1 ? four.y : four.x;
+                score(k, add2(pair(far, far), k & 1 ? four.y : four.x));
               }
-              const uint64_t e =
-                  fma2(pair(vs[2 * k], vs[2 * k + 1]), scale2, add2(shift[k], nl));
-              unpair(e, &p[2 * k], &p[2 * k + 1]);
             }
 #pragma unroll
             for (int k = 0; k < 16; ++k) p[k] = exp2_approx(p[k]);
@@ -461,36 +460,36 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
               for (int k = 0; k < 16; ++k)
                 p[k] = (DQ ? col + 16 * hf + k < limit : col + 16 * hf + k >= limit) ? p[k] : 0.0f;
             }
+            float z[16];
+            if (DROP && DQ) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) z[k] = p[k];
-            if (a.keep.T) {
-              if (DQ) {
+              for (int k = 0; k < 2; ++k) {
+                const uint4 w = keep_words(a.keep, (rows0 + (uint32_t)x) * per_row +
+                                                       (uint32_t)((col >> 3) + 2 * hf + k));
+                const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const uint4 w = keep_words(a.keep, (rows0 + (uint32_t)x) * per_row +
-                                                         (uint32_t)((col >> 3) + 2 * hf + k));
-                  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    keep_pair(v[e], a.keep.T, p[8 * k + 2 * e], p[8 * k + 2 * e + 1],
-                              &z[8 * k + 2 * e], &z[8 * k + 2 * e + 1]);
-                }
-              } else {
-#pragma unroll
-                for (int k = 0; k < 16; ++k) z[k] = kept[u] >> (16 * hf + k) & 1 ? p[k] : 0.0f;
+                for (int e = 0; e < 4; ++e)
+                  keep_pair(v[e], T2, p[8 * k + 2 * e], p[8 * k + 2 * e + 1],
+                            &z[8 * k + 2 * e], &z[8 * k + 2 * e + 1]);
               }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                z[k] = !DROP || (kept[u] >> (16 * hf + k) & 1) ? p[k] : 0.0f;
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              uint64_t nd = pair(ndelta, ndelta);
-              if (!DQ) {
+              uint64_t nd;
+              if (DQ) {
+                nd = pair(ndelta, ndelta);
+              } else {
                 const ulonglong2 four = qdelta[k >> 1];
                 nd = k & 1 ? four.y : four.x;
               }
               const uint64_t pp = pair(p[2 * k], p[2 * k + 1]);
               unpair(fma2(pair(z[2 * k], z[2 * k + 1]), pair(vp[2 * k], vp[2 * k + 1]), mul2(pp, nd)),
                      &ds[16 * hf + 2 * k], &ds[16 * hf + 2 * k + 1]);
-              if (sums && !near) mass = add2(mass, pp);
+              if (DQ) mass = add2(mass, pp);
             }
             if (masked) {
 #pragma unroll
@@ -649,8 +648,8 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
   }
 }
 
-template <typename T, int DP, bool DQ>
-cudaError_t grad(const AttnArgs& a, GradArgs f, cudaStream_t s) {
+template <typename T, int DP, bool DQ, bool DROP>
+cudaError_t grad_of(const AttnArgs& a, GradArgs f, cudaStream_t s) {
   using S = GradShape<DP, DQ>;
   // An empty side is never read; its map still needs an address and an extent.
   auto map = [&](CUtensorMap* m, const Heads& t, int L, int heads, int rows) {
@@ -671,13 +670,20 @@ cudaError_t grad(const AttnArgs& a, GradArgs f, cudaStream_t s) {
                        (a.biased ? bias_floats(a.rp) * 4 * (f.partial ? 1 + S::kWarps : 1) : 0);
   static PerDeviceOnce once;
   e = once.run([] {
-    return cudaFuncSetAttribute(k_attn_grad<T, DP, DQ>,
+    return cudaFuncSetAttribute(k_attn_grad<T, DP, DQ, DROP>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   });
   if (e != cudaSuccess) return e;
   const dim3 grid((Lx + kRows - 1) / kRows, a.B * Hx);
-  k_attn_grad<T, DP, DQ><<<grid, S::kThreads, bytes, s>>>(f);
+  k_attn_grad<T, DP, DQ, DROP><<<grid, S::kThreads, bytes, s>>>(f);
   return cudaGetLastError();
+}
+
+template <typename T, bool DQ>
+cudaError_t grad(const AttnArgs& a, const GradArgs& f, cudaStream_t s) {
+  if (a.D <= 64)
+    return a.keep.T ? grad_of<T, 64, DQ, true>(a, f, s) : grad_of<T, 64, DQ, false>(a, f, s);
+  return a.keep.T ? grad_of<T, 128, DQ, true>(a, f, s) : grad_of<T, 128, DQ, false>(a, f, s);
 }
 
 int padded(int Lq) { return (Lq + kRows - 1) / kRows * kRows; }
@@ -715,7 +721,7 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t s) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (a.dtable) f.partial = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + rows_bytes(a));
-    e = a.D <= 64 ? grad<T, 64, true>(a, f, s) : grad<T, 128, true>(a, f, s);
+    e = grad<T, true>(a, f, s);
     if (e != cudaSuccess) return e;
     if (a.dtable) {
       e = launch_bucket_sums(f.partial, a.B * ((a.Lq + kRows - 1) / kRows), a.H, a.rp.num_buckets,
@@ -724,7 +730,7 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t s) {
       f.partial = nullptr;
     }
   }
-  if (a.Lk) e = a.D <= 64 ? grad<T, 64, false>(a, f, s) : grad<T, 128, false>(a, f, s);
+  if (a.Lk) e = grad<T, false>(a, f, s);
   return e;
 }
 

@@ -63,11 +63,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, &g_attn_error, kErrWaitFull));
 }
 
-template <typename T, int DP, int BN>
+template <typename T, int DP, int BN, bool DROP>
 __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
     k_attn_fwd(const __grid_constant__ FwdArgs a) {
   using S = FwdShape<DP, BN>;
-  constexpr bool kBf16 = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  // Registers for the next columns' scores while these are worked on: with four
+  // warps a scheduler the other warps cover that latency.
+  constexpr bool kAhead = DP > 64;
   extern __shared__ uint8_t raw[];
   __shared__ FwdBars bar;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~1023ull);
@@ -230,96 +233,96 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
 
-    // Columns 32 c .. 32 c + 31 of tile n: scores times log2(e), bias, masks.
-    auto scores = [&](float (&x)[32], int n, int c) {
-      uint32_t r[32];
-      tmem_ld32(r, ts + 32 * c);
-      tmem_wait_ld(r);
-      const int j = n * BN + 32 * c;
-      float far = 0.0f;
-      bool near = false;
-      if (a.biased) {
-        const int d = j - wi - a.q_offset;  // of the warp's first row and the first column
-        near = d + 31 > -span.left && d - 31 < span.right;
-        far = d > 0 ? far_right : far_left;
-      }
-      if (near) {
-        const float* t = bias + (j - i - a.q_offset) + span.left + kBiasMargin;
-#pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = __fmaf_rn(__uint_as_float(r[k]), a.scale2, t[k]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = __fmaf_rn(__uint_as_float(r[k]), a.scale2, far);
-      }
-      if (j + 32 > warp_limit) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = j + k < limit ? x[k] : -INFINITY;
-      }
-    };
+    const uint64_t scale2 = pair(a.scale2, a.scale2);
 
     for (int n = 0; n < mine; ++n) {
+      // The keep bits do not wait for the scores: as masks of the packed weights.
+      uint32_t p[BN / 2];
+      auto draw = [&] {
+#pragma unroll
+        for (int k = 0; k < BN / 8; ++k) {
+          const uint4 w = keep_words(a.keep, call0 + (uint32_t)(n * (BN / 8) + k));
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[4 * k + e] = keep_mask2(u[e], T2);
+        }
+      };
+      if (DROP) draw();
       ok = warp_wait(&bar.s_full[g], n & 1);
       if (!ok) break;
       tc_fence_after();
-      uint32_t p[BN / 2];
       float sum, top;
       // The first tile is looked over for its maximum; the others are taken
       // relative to m at once, and again in the rare case that m is passed.
-      bool draw = n > 0;
+      bool weigh = n > 0;
 #pragma unroll 1
       for (int pass = 0;; ++pass) {
         const float base = m == -INFINITY ? 0.0f : m;
-        sum = 0.0f;
-        top = -INFINITY;
+        uint64_t sum2 = 0;
+        top = -INFINITY;  // relative to base
+        uint32_t r[kAhead ? 2 : 1][16];
+        if (kAhead) tmem_ld16(r[0], ts);
 #pragma unroll
-        for (int c = 0; c < BN / 32; ++c) {
-          float x[32];
-          scores(x, n, c);
+        for (int c = 0; c < BN / 16; ++c) {  // 16 columns at a time
+          uint32_t(&v)[16] = r[kAhead ? c & 1 : 0];
+          if (!kAhead) tmem_ld16(v, ts + 16 * c);
+          tmem_wait_ld(v);
+          if (kAhead && c + 1 < BN / 16) tmem_ld16(r[~c & 1], ts + 16 * (c + 1));
+          const int j = n * BN + 16 * c;
+          float x[16];  // scores times log2(e), less base
+          const int d = j - wi - a.q_offset;  // distance of the warp's first row, first column
+          if (a.biased && d + 15 > -span.left && d - 31 < span.right) {
+            const float* t = bias + (j - i - a.q_offset) + span.left + kBiasMargin;
+            const uint64_t less = pair(-base, -base);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) top = fmaxf(top, x[k]);
-          if (!draw) continue;
-          float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int k = 0; k < 8; ++k)
+              unpair(fma2(pair(v[2 * k], v[2 * k + 1]), scale2,
+                          add2(pair(t[2 * k], t[2 * k + 1]), less)),
+                     &x[2 * k], &x[2 * k + 1]);
+          } else {
+            const float f = (a.biased ? d > 0 ? far_right : far_left : 0.0f) - base;
+            const uint64_t far = pair(f, f);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            x[k] = exp2_approx(x[k] - base);
-            part[k & 3] += x[k];
+            for (int k = 0; k < 8; ++k)
+              unpair(fma2(pair(v[2 * k], v[2 * k + 1]), scale2, far), &x[2 * k], &x[2 * k + 1]);
           }
-          sum += (part[0] + part[1]) + (part[2] + part[3]);
+          if (j + 16 > warp_limit) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) p[16 * c + k] = pack2<T>(x[2 * k], x[2 * k + 1]);
-          if (a.keep.T) {
+            for (int k = 0; k < 16; ++k) x[k] = j + k < limit ? x[k] : -INFINITY;
+          }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint4 w = keep_words(a.keep, call0 + (uint32_t)(n * (BN / 8) + 4 * c + k));
-              const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-              if (a.keep.T <= 0x7c00u) {
+          for (int k = 0; k < 16; k += 2) top = fmaxf(top, fmaxf(x[k], x[k + 1]));
+          if (!weigh) continue;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[16 * c + 4 * k + e] &= keep_mask2(u[e], T2);
-              } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) p[16 * c + 4 * k + e] &= keep_mask2_any(u[e], a.keep.T);
-              }
-            }
+          for (int k = 0; k < 8; ++k) {
+            x[2 * k] = exp2_approx(x[2 * k]);
+            x[2 * k + 1] = exp2_approx(x[2 * k + 1]);
+            sum2 = add2(sum2, pair(x[2 * k], x[2 * k + 1]));
+            const uint32_t w = pack2<T>(x[2 * k], x[2 * k + 1]);
+            p[8 * c + k] = DROP ? p[8 * c + k] & w : w;
           }
         }
-        if (pass == 1 || (draw && !__any_sync(0xffffffffu, top > m + kRaise))) break;
-        const float up = fmaxf(m, top);
+        float s0, s1;
+        unpair(sum2, &s0, &s1);
+        sum = s0 + s1;
+        if (pass == 1 || (weigh && !__any_sync(0xffffffffu, top > kRaise))) break;
+        const float up = fmaxf(m, base + top);
         const float less = m == -INFINITY ? 0.0f : exp2_approx(m - up);
         m = up;
         l *= less;
         if (n > 0) {
 #pragma unroll
-          for (int c = 0; c < DP / 32; ++c) {
-            uint32_t r[32];
-            tmem_ld32(r, to + 32 * c);
-            tmem_wait_ld(r);
+          for (int c = 0; c < DP / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(o, to + 16 * c);
+            tmem_wait_ld(o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              r[k] = __float_as_uint(__uint_as_float(r[k]) * less);
-            tmem_st32(to + 32 * c, r);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * less);
+            tmem_st16(to + 16 * c, o);
           }
+          if (DROP) draw();
         }
-        draw = true;
+        weigh = true;
       }
       l += sum;
 #pragma unroll
@@ -383,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
   }
 }
 
-template <typename T, int DP, int BN>
+template <typename T, int DP, int BN, bool DROP>
 cudaError_t fwd(const AttnArgs& a, cudaStream_t s) {
   using S = FwdShape<DP, BN>;
   FwdArgs f{};
@@ -415,12 +418,12 @@ cudaError_t fwd(const AttnArgs& a, cudaStream_t s) {
   const size_t bytes = 1024 + S::kBias + (a.biased ? bias_floats(a.rp) * sizeof(float) : 0);
   static PerDeviceOnce once;
   e = once.run([] {
-    return cudaFuncSetAttribute(k_attn_fwd<T, DP, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(k_attn_fwd<T, DP, BN, DROP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 1024 + S::kBias + kBiasMostBytes);
   });
   if (e != cudaSuccess) return e;
   const dim3 grid((a.Lq + kGroups * kRows - 1) / (kGroups * kRows), a.B * a.H);
-  k_attn_fwd<T, DP, BN><<<grid, kThreads, bytes, s>>>(f);
+  k_attn_fwd<T, DP, BN, DROP><<<grid, kThreads, bytes, s>>>(f);
   return cudaGetLastError();
 }
 
@@ -431,9 +434,13 @@ cudaError_t attn_error_word(unsigned** word) {
 }
 
 cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s) {
-  if (a.type == OB_TYPE_BF16)
-    return a.D <= 64 ? fwd<__nv_bfloat16, 64, 64>(a, s) : fwd<__nv_bfloat16, 128, 128>(a, s);
-  return a.D <= 64 ? fwd<__half, 64, 64>(a, s) : fwd<__half, 128, 128>(a, s);
+  auto by_type = [&](auto zero) {
+    using T = decltype(zero);
+    if (a.D <= 64)
+      return a.keep.T ? fwd<T, 64, 64, true>(a, s) : fwd<T, 64, 64, false>(a, s);
+    return a.keep.T ? fwd<T, 128, 128, true>(a, s) : fwd<T, 128, 128, false>(a, s);
+  };
+  return a.type == OB_TYPE_BF16 ? by_type(__nv_bfloat16()) : by_type(__half());
 }
 
 }  // namespace ob

@@ -112,7 +112,8 @@ ob_status check_attn(const ob_attn* a) {
   if (ob_status st = check_lengths(a->Lq, a->Lk, a->q_offset, 1ll << 24)) return st;
   if (!(a->scale > 0.0f) || !std::isfinite(a->scale))
     return failf(OB_ERR_INVALID, "scale = %g must be positive", (double)a->scale);
-  if (!(a->p >= 0.0 && a->p < 1.0)) return failf(OB_ERR_INVALID, "p = %g must be in [0, 1)", a->p);
+  if (!(a->p >= 0.0 && a->p <= 255.0 / 256))
+    return failf(OB_ERR_INVALID, "p = %g must be in [0, 255/256]", a->p);
   if (a->relpos) {
     if (ob_status st = check_relpos(a->relpos)) return st;
     if (a->relpos->max_distance > OB_ATTN_MAX_DISTANCE)
