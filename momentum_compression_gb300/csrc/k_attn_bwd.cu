@@ -14,6 +14,14 @@
 //   acc1 += Z W (dv), acc2 += dS U (dq or dk)    first operand from tensor memory
 // The warpgroups of a block take turns over the tiles, so one's arithmetic
 // runs beside another's products.
+//
+// A block stays on its SM and takes one piece of work (128 rows of X) after
+// another from a counter, the products of the next begun before the last of
+// this one are in.  Which block takes what changes no result.  Beside the
+// warpgroups it has a warp each that issues the products of S and dP, those
+// of the accumulators, and the copies (and clears the rows of pieces without
+// pairs), and one that stages the bias of the next head and adds up the bias
+// table's sums of the last.
 #include <cmath>
 #include <type_traits>
 
@@ -31,6 +39,8 @@ constexpr int kRowsPerBlock = 16;  // of k_rows
 struct GradArgs {
   CUtensorMap x, y, u, w;
   int B, H, Hkv, D, Lq, Lk, causal, q_offset, biased;
+  int blocks, items;  // 128-row blocks of a head; blocks * batch * heads
+  int sum_bufs;       // buffers of the bias table's sums, 0: none are wanted
   float scale, scale2;  // scale2 = scale * log2(e)
   ob_relpos rp;
   const void* table;
@@ -40,7 +50,8 @@ struct GradArgs {
                    // then 64 times -rowsum(do o) / keep.scale
   int Lqp;
   Heads out1, out2;  // dq: out2 = dq; dkv: out1 = dv, out2 = dk
-  float* partial;    // [H][B * blocks][num_buckets], or null
+  float* partial;    // [H][B * blocks][num_buckets]
+  unsigned* next;    // the counter of this launch, 0 at its start
   unsigned* err;
 };
 
@@ -50,6 +61,7 @@ struct RowArgs {
   const float* lse;
   float inv_keep;
   float* rows;
+  unsigned* next;  // two counters to clear
 };
 
 // ---------------------------------------------------------------------------
@@ -65,10 +77,11 @@ __device__ __forceinline__ int64_t row_at(int bh, int Lqp, int i) {
 
 template <typename T>
 __global__ void __launch_bounds__(16 * kRowsPerBlock) k_rows(const RowArgs a) {
+  if (blockIdx.x == 0 && threadIdx.x < 2) a.next[threadIdx.x] = 0;
   const int l = threadIdx.x & 15;
   const int64_t at = (int64_t)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 4);
+  if (at >= (int64_t)a.B * a.H * a.Lqp) return;
   const int bh = (int)(at / a.Lqp), i = (int)(at % a.Lqp), b = bh / a.H, h = bh % a.H;
-  if (bh >= a.B * a.H) return;
   float sum = 0.0f;
   if (i < a.Lq && 8 * l < a.D) {
     const uint4 x = *reinterpret_cast<const uint4*>(
@@ -106,30 +119,39 @@ template <int DP, bool DQ>
 struct GradShape {
   static constexpr int kGroups = DP == 64 ? 3 : 2;
   static constexpr int kStages = DP == 64 ? 5 : 3;
+  static constexpr int kXBufs = DP == 64 ? 2 : 1;
   static constexpr int kWarps = 4 * kGroups;
-  static constexpr int kThreads = 128 * kGroups + 64;
+  static constexpr int kThreads = 32 * (kWarps + 4);  // and the four warps of the other roles
   static constexpr uint32_t kX = kRows * DP * 2;
   static constexpr uint32_t kTile = kTileRows * DP * 2;
   static constexpr uint32_t kStage = 2 * kTile + (DQ ? 0 : 1024);  // U, W and the queries' rows
-  static constexpr uint32_t kBias = 2 * kX + kStages * kStage;     // offset of the bias
+  static constexpr uint32_t kRing = kXBufs * 2 * kX;               // offset of the stages
+  static constexpr uint32_t kBias = kRing + kStages * kStage;      // of two biases, then the sums
   // tensor memory: S and dP of each group, the accumulators
   static constexpr uint32_t kAcc = 128 * kGroups;
+  // floats of one buffer of sums: by distance for each warp, and of each
+  // group's rows eps, far left and right, mass left and right
+  __host__ __device__ static constexpr int sum_floats(int nbias) {
+    return kWarps * nbias + 5 * kGroups * kRows;
+  }
+};
+
+constexpr int kSlots = 8;
+
+struct Item {
+  int x0, b, hx, keys, from, per;  // x0 < 0: no more
 };
 
 template <int G, int S>
 struct GradBars {
-  uint64_t x_full, full[S], empty[S], s_full[G], p_full[G], done;
+  uint64_t item_full[kSlots], item_empty[kSlots];
+  uint64_t x_full[2], x_empty[2], full[S], empty[S], s_full[G], p_full[G], acc_full, acc_free;
+  uint64_t bias_full[2], bias_empty[2], sums_full[2], sums_empty[2], drain[2];
+  Item item[kSlots];
   uint32_t tmem;
-  int dead;
   int first[OB_RELPOS_MAX_SIDE];
-  float eps[G][kRows];        // sums of a row's dS
-  float far[4 * G][2];        // the warps' sums over the far buckets
   float carry[4 * G][32];
 };
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned* err) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, kErrWaitFull));
-}
 
 // The pair of weights whose halfwords are w, dropped ones as zero.
 __device__ __forceinline__ void keep_pair(uint32_t w, uint32_t T2, float p0, float p1, float* z0,
@@ -151,15 +173,15 @@ __device__ __forceinline__ void keep_pair(uint32_t w, uint32_t T2, float p0, flo
 __device__ __forceinline__ uint32_t keep_column(const Keep& keep, uint64_t call0, uint64_t step,
                                                 int lane) {
   uint32_t x = 0, y = 0;  // queries 8 k + l % 8 for k = 0, 1 and for k = 2, 3
+  uint4 w[4];
+  keep_words_n(keep, call0, 8 * step, w);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint4 w = keep_words(keep, call0 + (uint64_t)(8 * k) * step);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
     uint32_t& to = k < 2 ? x : y;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 4; ++e)
       to |= keep_mask2(u[e], keep.T * 0x10001u) & (0x00020001u << (2 * e + 8 * (k & 1)));
-    }
   }
   // even keys are in the low halves, odd ones in the high halves
   uint32_t v = __byte_perm(x, y, 0x5410) | __byte_perm(x, y, 0x7632);
@@ -178,468 +200,636 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     k_attn_grad(const __grid_constant__ GradArgs a) {
   using S = GradShape<DP, DQ>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr int G = S::kGroups, kProducts = 4 * G, kCopies = 4 * G + 1;
+  constexpr int G = S::kGroups, kScores = 4 * G, kProducts = kScores + 1, kCopies = kScores + 2;
   extern __shared__ uint8_t raw[];
   __shared__ GradBars<G, S::kStages> bar;
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~1023ull);
-  float* bias = reinterpret_cast<float*>(smem + S::kBias);
+  uint8_t* smem = align_shared(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const BiasSpan span = a.biased ? bias_span(a.rp) : BiasSpan{0, 0};
   const int nbias = a.biased ? bias_floats(a.rp) : 0;
-  const bool sums = DQ && a.partial;
-  float* by_d = bias + nbias;  // the warps' sums by distance, nbias each
-
-  // DQ: x0 is a query of head h.  Else a key of head hk, and the tiles run over
-  // the queries from `from` on of the heads h0 .. h0 + heads - 1.
-  const int group = a.H / a.Hkv;
-  const int b = blockIdx.y / (DQ ? a.H : a.Hkv), hx = blockIdx.y % (DQ ? a.H : a.Hkv);
-  const int h0 = DQ ? hx : hx * group, hk = DQ ? hx / group : hx, heads = DQ ? 1 : group;
-  const int keys = key_count(a.kv_len, a.Lk, b);
-  // Causal: the last queries see the most keys, the first keys the most queries.
-  const int x0 = (DQ ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x) * kRows;
-  int from = 0, per;  // tiles of a head: from, ..., from + per - 1
-  if (DQ) {
-    int n = keys;
-    if (a.causal) n = min(n, min(x0 + kRows, a.Lq) + a.q_offset);
-    per = n > 0 ? (n + kTileRows - 1) / kTileRows : 0;
-  } else {
-    if (a.causal) from = max(0, x0 - a.q_offset) / kTileRows;
-    per = x0 < keys ? max(0, (a.Lq + kTileRows - 1) / kTileRows - from) : 0;
-  }
-  const int total = heads * per;
+  const int group = a.H / a.Hkv, heads_x = DQ ? a.H : a.Hkv, heads = DQ ? 1 : group;
+  float* biases = reinterpret_cast<float*>(smem + S::kBias);
+  float* sums = biases + 2 * nbias;  // sum_bufs buffers of S::sum_floats(nbias)
 
   if (threadIdx.x == 0) {
-    mbar_init(&bar.x_full, 1);
-    mbar_init(&bar.done, 1);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&bar.item_full[i], 1);
+      mbar_init(&bar.item_empty[i], 2 + S::kWarps + (a.biased ? 1 : 0));
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.x_full[i], 1);
+      mbar_init(&bar.x_empty[i], 1);
+      mbar_init(&bar.bias_full[i], 1);
+      mbar_init(&bar.bias_empty[i], S::kWarps);
+      mbar_init(&bar.sums_full[i], S::kWarps);
+      mbar_init(&bar.sums_empty[i], 1);
+      mbar_init(&bar.drain[i], 1);
+    }
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&bar.full[i], 1);
       mbar_init(&bar.empty[i], 1);
     }
     for (int g = 0; g < G; ++g) {
       mbar_init(&bar.s_full[g], 1);
-      mbar_init(&bar.p_full[g], 128);
+      mbar_init(&bar.p_full[g], 4);
     }
-    bar.dead = 0;
+    mbar_init(&bar.acc_full, 1);
+    mbar_init(&bar.acc_free, S::kWarps);
     fence_barrier_init();
   }
   if (warp == kProducts) tmem_alloc(&bar.tmem, 512);
   if (a.biased) {
     for (int i = threadIdx.x; i < a.rp.side; i += S::kThreads) bar.first[i] = a.rp.first[i];
-    if (sums)
-      for (int i = threadIdx.x; i < S::kWarps * nbias; i += S::kThreads) by_d[i] = 0.0f;
-    __syncthreads();
-    if (DQ)
-      stage_bias(bias, a.rp, bar.first, static_cast<const T*>(a.table), a.H, h0, threadIdx.x,
-                 S::kThreads);
+    for (int i = threadIdx.x; i < a.sum_bufs * S::sum_floats(nbias); i += S::kThreads)
+      sums[i] = 0.0f;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
-  volatile int* dead = &bar.dead;
+
+  // The k-th piece of work of this block, for one of the roles that follow it:
+  // false after the last, or when the wait ran out.
+  auto take = [&](int k, Item& it) {
+    const int slot = k % kSlots;
+    if (!warp_wait(&bar.item_full[slot], (k / kSlots) & 1, a.err)) return false;
+    it = bar.item[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.item_empty[slot]);
+    return it.x0 >= 0;
+  };
 
   if (warp == kCopies) {
     // ----- copies --------------------------------------------------------
-    if (lane == 0 && total > 0) {
-      mbar_arrive_expect_tx(&bar.x_full, 2 * S::kX);
-      for (int x = 0; x < DP / 64; ++x) {
-        tma_load4(smem + x * (kRows * 128), &a.x, 64 * x, x0, hx, b, &bar.x_full);
-        tma_load4(smem + S::kX + x * (kRows * 128), &a.y, 64 * x, x0, hx, b, &bar.x_full);
-      }
-      int t = 0;
-      for (; t < total; ++t) {
-        const int st = t % S::kStages;
-        if (t >= S::kStages &&
-            (!mbar_wait(&bar.empty[st], (t / S::kStages + 1) & 1, a.err, kErrWaitEmpty) || *dead))
-          break;
-        uint8_t* to = smem + 2 * S::kX + st * S::kStage;
-        const int r = (from + t % per) * kTileRows, hu = DQ ? hk : h0 + t / per;
-        mbar_arrive_expect_tx(&bar.full[st], 2 * S::kTile + (DQ ? 0 : kTileRows * 8));
-        for (int x = 0; x < DP / 64; ++x) {
-          tma_load4(to + x * (kTileRows * 128), &a.u, 64 * x, r, hu, b, &bar.full[st]);
-          tma_load4(to + S::kTile + x * (kTileRows * 128), &a.w, 64 * x, r, hu, b, &bar.full[st]);
+    // DQ: x0 is a query of head hx.  Else a key of head hx, and the tiles run over
+    // the queries from tile `from` on of the heads that share it.
+    int idx = blockIdx.x, k = 0, nx = 0, nt = 0;  // pieces, X buffers and tiles issued so far
+    bool ok = true;
+    // Finds the next piece with pairs, clearing the rows of those without, and
+    // hands it to the other roles.
+    auto hand_out = [&] {
+      Item it{-1, 0, 0, 0, 0, 0};
+      while (idx < a.items) {
+        // Causal: the last queries see the most keys, the first keys the most queries.
+        const int blk = idx / (a.B * heads_x), bh = idx % (a.B * heads_x);
+        const int x0 = (DQ ? a.blocks - 1 - blk : blk) * kRows, b = bh / heads_x, hx = bh % heads_x;
+        unsigned n = 0;
+        if (lane == 0) n = gridDim.x + atomicAdd(a.next, 1u);
+        const int keys = key_count(a.kv_len, a.Lk, b);
+        int from = 0, per;
+        if (DQ) {
+          int last = keys;
+          if (a.causal) last = min(last, min(x0 + kRows, a.Lq) + a.q_offset);
+          per = last > 0 ? (last + kTileRows - 1) / kTileRows : 0;
+        } else {
+          if (a.causal) from = max(0, x0 - a.q_offset) / kTileRows;
+          per = x0 < keys ? max(0, (a.Lq + kTileRows - 1) / kTileRows - from) : 0;
         }
-        if (!DQ)
-          bulk_g2s(to + 2 * S::kTile, a.rows + row_at(b * a.H + hu, a.Lqp, r), kTileRows * 8,
-                   &bar.full[st]);
+        idx = (int)__shfl_sync(0xffffffffu, n, 0);
+        if (per > 0) {
+          it = Item{x0, b, hx, keys, from, per};
+          break;
+        }
+        for (int r = 0; r < kRows && x0 + r < (DQ ? a.Lq : a.Lk); ++r)
+          for (int o = DQ ? 1 : 0; o < 2; ++o) {
+            const Heads& out = o ? a.out2 : a.out1;
+            T* to = static_cast<T*>(out.data) + b * out.b + (int64_t)(x0 + r) * out.l + hx * out.h;
+            if (8 * lane < a.D) *reinterpret_cast<uint4*>(to + 8 * lane) = make_uint4(0, 0, 0, 0);
+          }
+        if (DQ && a.sum_bufs) {
+          float* to = a.partial + (((int64_t)hx * a.B + b) * a.blocks + x0 / kRows) * a.rp.num_buckets;
+          for (int i = lane; i < a.rp.num_buckets; i += 32) to[i] = 0.0f;
+        }
       }
-      if (t < total) {  // a wait ran out: let what is in flight land before the block ends
-        *dead = 1;
-        mbar_wait(&bar.x_full, 0, a.err, kErrDrain);
-        for (int i = max(0, t - S::kStages); i < t; ++i)
-          mbar_wait(&bar.full[i % S::kStages], (i / S::kStages) & 1, a.err, kErrDrain);
+      const int slot = k % kSlots;
+      if (k >= kSlots) ok = warp_wait(&bar.item_empty[slot], (k / kSlots + 1) & 1, a.err, kErrWaitEmpty);
+      if (ok && lane == 0) {
+        bar.item[slot] = it;
+        mbar_arrive(&bar.item_full[slot]);
       }
+      ++k;
+      return it;
+    };
+    Item it = hand_out();
+    while (ok && it.x0 >= 0) {
+      const Item after = hand_out();  // known to all well before its turn
+      const int xb = nx % S::kXBufs;
+      if (ok && nx >= S::kXBufs) ok = warp_wait(&bar.x_empty[xb], (nx / S::kXBufs + 1) & 1, a.err, kErrWaitEmpty);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bar.x_full[xb], 2 * S::kX);
+        for (int x = 0; x < DP / 64; ++x) {
+          uint8_t* to = smem + xb * 2 * S::kX + x * (kRows * 128);
+          tma_load4(to, &a.x, 64 * x, it.x0, it.hx, it.b, &bar.x_full[xb]);
+          tma_load4(to + S::kX, &a.y, 64 * x, it.x0, it.hx, it.b, &bar.x_full[xb]);
+        }
+      }
+      ++nx;
+      for (int hh = 0; ok && hh < heads; ++hh) {
+        const int hu = DQ ? it.hx / group : it.hx * group + hh;
+        for (int t = 0; t < it.per; ++t, ++nt) {
+          const int st = nt % S::kStages;
+          if (nt >= S::kStages) ok = warp_wait(&bar.empty[st], (nt / S::kStages + 1) & 1, a.err, kErrWaitEmpty);
+          if (!ok) break;
+          uint8_t* to = smem + S::kRing + st * S::kStage;
+          const int r = (it.from + t) * kTileRows;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bar.full[st], 2 * S::kTile + (DQ ? 0 : kTileRows * 8));
+            for (int x = 0; x < DP / 64; ++x) {
+              tma_load4(to + x * (kTileRows * 128), &a.u, 64 * x, r, hu, it.b, &bar.full[st]);
+              tma_load4(to + S::kTile + x * (kTileRows * 128), &a.w, 64 * x, r, hu, it.b,
+                        &bar.full[st]);
+            }
+            if (!DQ)
+              bulk_g2s(to + 2 * S::kTile, a.rows + row_at(it.b * a.H + hu, a.Lqp, r),
+                       kTileRows * 8, &bar.full[st]);
+          }
+        }
+      }
+      it = after;
     }
-  } else if (warp == kProducts) {
-    // ----- products ------------------------------------------------------
-    if (total > 0) {
-      constexpr uint32_t kShapeS = mma_shape(kBf16, kTileRows, false);
-      constexpr uint32_t kShapeA = mma_shape(kBf16, DP, true);
-      const uint32_t leader = elect_lane();
-      const uint32_t xs = smem_u32(smem), us = xs + 2 * S::kX;
-      const uint64_t x_desc = desc_k(xs), u_desc = desc_k(us),
-                     u_rows = desc_mn(us, kTileRows * 128);
-      const int ksteps = (a.D + 15) / 16;
-      bool ok = warp_wait(&bar.x_full, 0, a.err);
-      // S and dP of a tile: stage st, its phase, group g.
-      auto scores = [&](int st, int par, int g) {
-        ok = warp_wait(&bar.full[st], par, a.err) && !*dead;
-        if (!ok) return;
+    if (!ok) {  // a wait ran out: let what is in flight land before the block ends
+      for (int i = max(0, nx - S::kXBufs); i < nx; ++i)
+        mbar_wait(&bar.x_full[i % S::kXBufs], (i / S::kXBufs) & 1, a.err, kErrDrain);
+      for (int i = max(0, nt - S::kStages); i < nt; ++i)
+        mbar_wait(&bar.full[i % S::kStages], (i / S::kStages) & 1, a.err, kErrDrain);
+    }
+  } else if (warp == kScores) {
+    // ----- S and dP -------------------------------------------------------
+    constexpr uint32_t kShapeS = mma_shape(kBf16, kTileRows, false);
+    const uint32_t leader = elect_lane();
+    const uint64_t x_desc = desc_k(smem_u32(smem)), u_desc = desc_k(smem_u32(smem) + S::kRing);
+    const int ksteps = (a.D + 15) / 16;
+    bool ok = true;
+    int st = 0, par = 0, g = 0;     // stage, its phase, group of the tile
+    int fst = 0, fpar = 0, nt = 0;  // stage and phase of the tile that had the group last
+    Item it;
+    for (int k = 0; ok && take(k, it); ++k) {
+      const int xb = k % S::kXBufs;
+      ok = warp_wait(&bar.x_full[xb], (k / S::kXBufs) & 1, a.err);
+      const uint64_t xd = x_desc + (uint32_t)xb * (2 * S::kX >> 4);
+      const int total = heads * it.per;
+      for (int t = 0; ok && t < total; ++t, ++nt) {
+        ok = warp_wait(&bar.full[st], par, a.err);
+        // Once that tile's products are done, its P and dS may be written over.
+        if (ok && nt >= G) {
+          ok = warp_wait(&bar.empty[fst], fpar, a.err, kErrWaitEmpty);
+          if (++fst == S::kStages) fst = 0, fpar ^= 1;
+        }
+        if (!ok) break;
         tc_fence_after();
         const uint64_t ud = u_desc + (uint32_t)st * (S::kStage >> 4);
+        const uint32_t d = tmem + g * 128;
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
           for (int s = 0; s < DP / 16; ++s)
             if (s < ksteps)
-              mma_ss(leader, tmem + g * 128 + 64 * y,
-                     x_desc + ((y * S::kX + (s >> 2) * (kRows * 128) + (s & 3) * 32) >> 4),
+              mma_ss(leader, d + 64 * y,
+                     xd + ((y * S::kX + (s >> 2) * (kRows * 128) + (s & 3) * 32) >> 4),
                      ud + ((y * S::kTile + (s >> 2) * (kTileRows * 128) + (s & 3) * 32) >> 4),
                      kShapeS, s > 0);
         mma_commit(leader, &bar.s_full[g]);
-      };
-      int lst = 0, lpar = 0, lg = 0;  // of the next tile to score
-      auto advance = [&](int& st, int& par, int& g) {
         if (++st == S::kStages) st = 0, par ^= 1;
         if (++g == G) g = 0;
-      };
-      for (int t = 0; ok && t < G && t < total; ++t) {
-        scores(lst, lpar, lg);
-        advance(lst, lpar, lg);
       }
-      int st = 0, par = 0, g = 0, gpar = 0;
-      for (int t = 0; ok && t < total; ++t) {
-        ok = warp_wait(&bar.p_full[g], gpar, a.err) && !*dead;
+      mma_commit(leader, &bar.x_empty[xb]);
+    }
+    // Nothing may arrive after the block's end.
+    mma_commit(leader, &bar.drain[0]);
+    mbar_wait(&bar.drain[0], 0, a.err, kErrDrain);
+  } else if (warp == kProducts) {
+    // ----- the accumulators -----------------------------------------------------
+    constexpr uint32_t kShapeA = mma_shape(kBf16, DP, true);
+    const uint32_t leader = elect_lane();
+    const uint64_t u_rows = desc_mn(smem_u32(smem) + S::kRing, kTileRows * 128);
+    bool ok = true;
+    int st = 0, g = 0, gpar = 0;
+    Item it;
+    for (int k = 0; ok && take(k, it); ++k) {
+      const int total = heads * it.per;
+      for (int t = 0; t < total; ++t) {
+        ok = warp_wait(&bar.p_full[g], gpar, a.err);
+        if (ok && t == 0 && k > 0) ok = warp_wait(&bar.acc_free, (k + 1) & 1, a.err, kErrWaitEmpty);
         if (!ok) break;
         tc_fence_after();
         const uint64_t ud = u_rows + (uint32_t)st * (S::kStage >> 4);
+        const uint32_t p = tmem + g * 128;
         if (!DQ) {
 #pragma unroll
           for (int s = 0; s < kTileRows / 16; ++s)
-            mma_ts(leader, tmem + S::kAcc, tmem + g * 128 + s * 8,
-                   ud + ((S::kTile + s * 2048) >> 4), kShapeA, t > 0 || s > 0);
+            mma_ts(leader, tmem + S::kAcc, p + s * 8, ud + ((S::kTile + s * 2048) >> 4), kShapeA,
+                   t > 0 || s > 0);
         }
 #pragma unroll
         for (int s = 0; s < kTileRows / 16; ++s)
-          mma_ts(leader, tmem + S::kAcc + (DQ ? 0 : DP), tmem + g * 128 + 64 + s * 8,
-                 ud + (s * 2048 >> 4), kShapeA, t > 0 || s > 0);
-        // Only where a later copy waits for it: nothing may arrive after the block's end.
-        if (t + S::kStages < total) mma_commit(leader, &bar.empty[st]);
-        if (t + G < total) {
-          scores(lst, lpar, lg);
-          advance(lst, lpar, lg);
-        }
-        advance(st, par, g);
-        if (g == 0) gpar ^= 1;
+          mma_ts(leader, tmem + S::kAcc + (DQ ? 0 : DP), p + 64 + s * 8, ud + (s * 2048 >> 4),
+                 kShapeA, t > 0 || s > 0);
+        mma_commit(leader, &bar.empty[st]);
+        if (++st == S::kStages) st = 0;
+        if (++g == G) g = 0, gpar ^= 1;
       }
-      if (!ok) *dead = 1;
-      mma_commit(leader, &bar.done);
-      if (!ok) mbar_wait(&bar.done, 0, a.err, kErrDrain);
+      if (ok) mma_commit(leader, &bar.acc_full);
+    }
+    mma_commit(leader, &bar.drain[1]);
+    mbar_wait(&bar.drain[1], 0, a.err, kErrDrain);
+  } else if (warp > kCopies) {
+    // ----- helper: the biases ahead, the bias table's sums behind -----------------
+    if (a.biased) {
+      int k = 0, nb = 0;  // pieces taken, biases staged
+      bool ok = true;
+      Item it, prev;
+      bool have = take(k, it), had = false;
+      int done = 0;  // pieces whose sums are out
+      while (ok && (have || had)) {
+        if (have) {
+          ++k;
+          for (int hh = 0; ok && hh < heads; ++hh, ++nb) {
+            if (nb >= 2) ok = warp_wait(&bar.bias_empty[nb & 1], (nb / 2 + 1) & 1, a.err, kErrWaitEmpty);
+            if (!ok) break;
+            stage_bias(biases + (nb & 1) * nbias, a.rp, bar.first, static_cast<const T*>(a.table),
+                       a.H, DQ ? it.hx : it.hx * group + hh, lane, 32);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.bias_full[nb & 1]);
+          }
+        }
+        if (had && ok && DQ && a.sum_bufs) {
+          const int sb = done % a.sum_bufs;
+          ok = warp_wait(&bar.sums_full[sb], (done / a.sum_bufs) & 1, a.err);
+          if (!ok) break;
+          float* by_d = sums + sb * S::sum_floats(nbias);
+          float* row = by_d + S::kWarps * nbias;  // [5][G][kRows]
+          // A row's dS sums to zero; what it sums to is the error of rowsum(do o),
+          // taken from the rounded o.  It is taken out of the far buckets, whose
+          // weight would multiply it, and out of the row's entry for dk.
+          float far_l = 0.0f, far_r = 0.0f;
+          for (int r = lane; r < kRows; r += 32) {
+            float v[5] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 5; ++i)
+#pragma unroll
+              for (int g = 0; g < G; ++g) v[i] += row[(i * G + g) * kRows + r];
+            far_l += v[1] - v[0] * v[3];
+            far_r += v[2] - v[0] * v[4];
+            a.rows[row_at(prev.b * a.H + prev.hx, a.Lqp, prev.x0 + r) + kTileRows] -= v[0];
+          }
+#pragma unroll
+          for (int o = 16; o; o >>= 1) {
+            far_l += __shfl_xor_sync(0xffffffffu, far_l, o);
+            far_r += __shfl_xor_sync(0xffffffffu, far_r, o);
+          }
+          // The warps' sums of a distance into the first warp's, the others cleared.
+          for (int i = lane; i < nbias; i += 32) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < S::kWarps; ++w) {
+              sum += by_d[w * nbias + i];
+              if (w) by_d[w * nbias + i] = 0.0f;
+            }
+            by_d[i] = sum;
+          }
+          __syncwarp();
+          float* to = a.partial + (((int64_t)prev.hx * a.B + prev.b) * a.blocks + prev.x0 / kRows) *
+                                      a.rp.num_buckets;
+          for (int n = lane; n < a.rp.num_buckets; n += 32) {
+            int64_t lo, hi;
+            bucket_range(bar.first, a.rp.side, a.rp.two_sided, n, -(span.left + kBiasMargin),
+                         span.right + kBiasMargin, &lo, &hi);
+            float sum = n == a.rp.side - 1 ? far_l : 0.0f;
+            if (n == (a.rp.two_sided ? a.rp.num_buckets - 1 : 0)) sum += far_r;
+            for (int i = (int)lo; i < (int)hi; ++i) sum += by_d[i + span.left + kBiasMargin];
+            to[n] = sum * a.keep.scale;
+          }
+          __syncwarp();
+          for (int i = lane; i < nbias; i += 32) by_d[i] = 0.0f;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.sums_empty[sb]);
+          ++done;
+        }
+        had = have;
+        prev = it;
+        have = have && take(k, it);
+      }
     }
   } else {
     // ----- arithmetic: a thread a row of X ----------------------------------
-    const int g = warp >> 2, row = (warp & 3) * 32 + lane, x = x0 + row;
-    const int wx = x0 + (warp & 3) * 32;  // the warp's first row
+    const int g = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + g * 128, tp = ts + 64;
     const uint64_t per_row = (uint32_t)((a.Lk + 7) / 8);
+    const uint32_t T2 = a.keep.T * 0x10001u;
+    bool ok = true;
+    int nt = 0, next = g, nb = 0;  // tiles of earlier pieces, this group's next tile, biases used
     float nlse = 0.0f, ndelta = 0.0f;  // of the row's query
-    if (DQ) {  // Lqp covers every row of the block
-      const float* r = a.rows + row_at(b * a.H + h0, a.Lqp, x);
+    auto fetch = [&](const Item& of) {
+      if (!DQ) return;  // Lqp covers every row of the block
+      const float* r = a.rows + row_at(of.b * a.H + of.hx, a.Lqp, of.x0 + row);
       nlse = r[0];
       ndelta = r[kTileRows];
-    }
-    const uint32_t T2 = a.keep.T * 0x10001u;
-    // The live columns of the row: DQ: below `limit`; else from `limit` on.
-    int limit, warp_limit;
-    if (DQ) {
-      limit = a.causal ? min(keys, x + a.q_offset + 1) : keys;
-      warp_limit = a.causal ? min(keys, wx + a.q_offset + 1) : keys;
-    } else {
-      limit = x >= keys ? INT32_MAX : a.causal ? x - a.q_offset : INT32_MIN;
-      warp_limit = wx + 31 >= keys ? INT32_MAX : a.causal ? wx + 31 - a.q_offset : INT32_MIN;
-    }
-    float eps = 0.0f, far_l = 0.0f, far_r = 0.0f, mass_l = 0.0f, mass_r = 0.0f;
-    float far_left = 0.0f, far_right = 0.0f;
-    bool ok = true;
-    int t = g;  // this group's next tile
-    for (int hh = 0; hh < heads; ++hh) {
-      const int h = h0 + hh;
-      if (a.biased) {
-        if (!DQ) {  // the head's bias; every group passes here once a head
-          named_sync(1, 128 * G);
-          stage_bias(bias, a.rp, bar.first, static_cast<const T*>(a.table), a.H, h, threadIdx.x,
-                     128 * G);
-          named_sync(1, 128 * G);
-        }
-        far_left = bias[0];
-        far_right = bias[nbias - 1];
+    };
+    Item it;
+    bool have = take(0, it);
+    if (have) fetch(it);
+    for (int k = 0; ok && have; ++k) {
+      const int x = it.x0 + row, wx = it.x0 + (warp & 3) * 32;  // the warp's first row
+      const int h0 = DQ ? it.hx : it.hx * group, keys = it.keys;
+      // The live columns of the row: DQ: below `limit`; else from `limit` on.
+      int limit, warp_limit;
+      if (DQ) {
+        limit = a.causal ? min(keys, x + a.q_offset + 1) : keys;
+        warp_limit = a.causal ? min(keys, wx + a.q_offset + 1) : keys;
+      } else {
+        limit = x >= keys ? INT32_MAX : a.causal ? x - a.q_offset : INT32_MIN;
+        warp_limit = wx + 31 >= keys ? INT32_MAX : a.causal ? wx + 31 - a.q_offset : INT32_MIN;
       }
-      const uint64_t rows0 = (uint64_t)(b * a.H + h) * a.Lq;
-      for (; ok && t < (hh + 1) * per; t += G) {
-        const int st = t % S::kStages;
-        const int c0 = (from + t - hh * per) * kTileRows;  // first column (key or query)
-        uint8_t* stage = smem + 2 * S::kX + st * S::kStage;
-        // The keep bits do not wait for the scores.
-        uint32_t kept[2] = {~0u, ~0u};
-        if (!DQ && DROP) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            kept[u] = keep_column(
-                a.keep,
-                (rows0 + (uint32_t)(c0 + 32 * u + (lane & 7))) * per_row + (uint32_t)(x >> 3),
-                per_row, lane);
-        }
-        ok = warp_wait(&bar.s_full[g], (t / G) & 1, a.err);
+      float eps = 0.0f, far_l = 0.0f, far_r = 0.0f, mass_l = 0.0f, mass_r = 0.0f;
+      float* by_d = sums;
+      if (DQ && a.sum_bufs) {
+        const int sb = k % a.sum_bufs;
+        if (k >= a.sum_bufs) ok = warp_wait(&bar.sums_empty[sb], (k / a.sum_bufs + 1) & 1, a.err, kErrWaitEmpty);
         if (!ok) break;
-        tc_fence_after();
-        uint32_t rs[2][16], rp[2][16];
-        tmem_ld16(rs[0], ts);
-        tmem_ld16(rp[0], tp);
+        by_d = sums + sb * S::sum_floats(nbias);
+      }
+      for (int hh = 0; ok && hh < heads; ++hh) {
+        const float* bias = biases + (nb & 1) * nbias;
+        float far_left = 0.0f, far_right = 0.0f;
+        if (a.biased) {
+          ok = warp_wait(&bar.bias_full[nb & 1], (nb / 2) & 1, a.err);
+          if (!ok) break;
+          far_left = bias[0];
+          far_right = bias[nbias - 1];
+        }
+        const uint64_t rows0 = (uint64_t)(it.b * a.H + h0 + hh) * a.Lq;
+        for (; ok && next < nt + (hh + 1) * it.per; next += G) {
+          const int st = next % S::kStages;
+          const int c0 = (it.from + next - nt - hh * it.per) * kTileRows;  // first column (key or query)
+          uint8_t* stage = smem + S::kRing + st * S::kStage;
+          // The keep bits do not wait for the scores.
+          uint32_t kept[2] = {~0u, ~0u};
+          if (!DQ && DROP) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {  // 32 columns at a time
-          const int col = c0 + 32 * u;
-          // distance of the warp's first row and the first column
-          const int d = DQ ? col - wx - a.q_offset : wx - col - a.q_offset;
-          bool near = false;
-          float far = 0.0f;
-          if (a.biased) {
-            near = d + 31 > -span.left && d - 31 < span.right;
-            far = d > 0 ? far_right : far_left;
+            for (int u = 0; u < 2; ++u)
+              kept[u] = keep_column(
+                  a.keep,
+                  (rows0 + (uint32_t)(c0 + 32 * u + (lane & 7))) * per_row + (uint32_t)(x >> 3),
+                  per_row, lane);
           }
-          const bool masked = DQ ? col + 32 > warp_limit : col < warp_limit;
-          const float* tb = bias + (DQ ? col - x : x - col) - a.q_offset + span.left + kBiasMargin;
-          float ds[32];
-          uint64_t mass = 0;  // sums of p, two lanes of them
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const int cc = 2 * u + hf;  // 16 columns; the next 16 are on their way meanwhile
-            tmem_wait_ld(rs[cc & 1]);
-            tmem_wait_ld(rp[cc & 1]);
-            if (cc < 3) {
-              tmem_ld16(rs[~cc & 1], ts + 16 * (cc + 1));
-              tmem_ld16(rp[~cc & 1], tp + 16 * (cc + 1));
-            }
-            const uint32_t(&vs)[16] = rs[cc & 1];
-            const uint32_t(&vp)[16] = rp[cc & 1];
+          uint4 words[4];  // DQ: of 32 columns
+          if (DQ && DROP)
+            keep_words_n(a.keep, (rows0 + (uint32_t)x) * per_row + (uint32_t)(c0 >> 3), 1, words);
+          ok = warp_wait(&bar.s_full[g], (next / G) & 1, a.err);
+          if (!ok) break;
+          tc_fence_after();
+          // Distances of the warp's rows and the tile's columns: [low, high].
+          const int low = (DQ ? c0 - wx - 31 : wx - c0 - 63) - a.q_offset, high = low + 94;
+          const bool near = a.biased && high > -span.left && low < span.right;
+          const float far = !a.biased ? 0.0f : low > 0 ? far_right : far_left;
+          const bool masked = DQ ? c0 + 64 > warp_limit : c0 < warp_limit;
+
+          // Z and dS of the tile.  Branch-free inside, for the scheduler's sake: a
+          // body each for tiles of one bias value, tiles across several, and tiles
+          // with masked pairs (of either kind).
+          auto weigh = [&](auto several_t, auto mask_t) {
+            constexpr bool kSeveral = decltype(several_t)::value, kMask = decltype(mask_t)::value;
+            // The bias of column n of the row: tb[n * step].
+            const int step = (kSeveral || near) ? (DQ ? 1 : -1) : 0;
+            const float* tb =
+                (kSeveral || near)
+                    ? bias + (DQ ? c0 - x : x - c0) - a.q_offset + span.left + kBiasMargin
+                    : bias + (low > 0 ? nbias - 1 : 0);
             const uint64_t scale2 = pair(a.scale2, a.scale2);
-            const ulonglong2* qlse =  // two pairs of queries each
-                reinterpret_cast<const ulonglong2*>(stage + 2 * S::kTile) + 4 * cc;
-            const ulonglong2* qdelta = qlse + kTileRows / 4;
-            float p[16];
-            auto score = [&](int k, uint64_t shift) {
-              unpair(fma2(pair(vs[2 * k], vs[2 * k + 1]), scale2, shift), &p[2 * k], &p[2 * k + 1]);
-            };
-            if (near) {
+            uint32_t rs[2][16], rp[2][16];
+            tmem_ld16(rs[0], ts);
+            tmem_ld16(rp[0], tp);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const int n = 16 * hf + 2 * k;
-                const uint64_t bias2 = DQ ? pair(tb[n], tb[n + 1]) : pair(tb[-n], tb[-n - 1]);
-                if (DQ) {
-                  score(k, add2(bias2, pair(nlse, nlse)));
+            for (int u = 0; u < 2; ++u) {  // 32 columns at a time
+              const int col = c0 + 32 * u;
+              if (DQ && DROP && u)
+                keep_words_n(a.keep, (rows0 + (uint32_t)x) * per_row + (uint32_t)(col >> 3), 1,
+                             words);
+              float ds[32];
+              uint64_t mass = 0;  // sums of p, two lanes of them
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                const int cc = 2 * u + hf;  // 16 columns; the next 16 are on their way meanwhile
+                const uint32_t(&vs)[16] = rs[hf];
+                const uint32_t(&vp)[16] = rp[hf];
+                tmem_wait_ld(rs[hf]);
+                tmem_wait_ld(rp[hf]);
+                if (cc < 3) {
+                  tmem_ld16(rs[1 - hf], ts + 16 * (cc + 1));
+                  tmem_ld16(rp[1 - hf], tp + 16 * (cc + 1));
+                }
+                const ulonglong2* qlse =  // two pairs of queries each
+                    reinterpret_cast<const ulonglong2*>(stage + 2 * S::kTile) + 4 * cc;
+                const ulonglong2* qdelta = qlse + kTileRows / 4;
+                float p[16], z[16];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  uint64_t shift;  // bias - lse
+                  if (DQ && !kSeveral && !kMask) {
+                    shift = pair(far + nlse, far + nlse);
+                  } else {
+                    uint64_t nl;
+                    if (DQ) {
+                      nl = pair(nlse, nlse);
+                    } else {
+                      const ulonglong2 four = qlse[k >> 1];
+                      nl = k & 1 ? four.y : four.x;
+                    }
+                    const int n = 16 * cc + 2 * k;
+                    if (kSeveral)
+                      shift = add2(DQ ? pair(tb[n], tb[n + 1]) : pair(tb[-n], tb[-n - 1]), nl);
+                    else if (kMask && a.biased)
+                      shift = add2(pair(tb[n * step], tb[(n + 1) * step]), nl);
+                    else
+                      shift = add2(pair(far, far), nl);
+                  }
+                  unpair(fma2(pair(vs[2 * k], vs[2 * k + 1]), scale2, shift), &p[2 * k],
+                         &p[2 * k + 1]);
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  p[k] = exp2_approx(p[k]);
+                  const int n = c0 + 16 * cc + k;
+                  if (kMask) p[k] = (DQ ? n < limit : n >= limit) ? p[k] : 0.0f;
+                }
+                if (DROP && DQ) {
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    const uint4& w = words[2 * hf + k];
+                    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                      keep_pair(v[e], T2, p[8 * k + 2 * e], p[8 * k + 2 * e + 1],
+                                &z[8 * k + 2 * e], &z[8 * k + 2 * e + 1]);
+                  }
                 } else {
-                  const ulonglong2 four = qlse[k >> 1];
-                  score(k, add2(bias2, k & 1 ? four.y : four.x));
+#pragma unroll
+                  for (int k = 0; k < 16; ++k)
+                    z[k] = !DROP || (kept[u] >> (16 * hf + k) & 1) ? p[k] : 0.0f;
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  uint64_t nd;
+                  if (DQ) {
+                    nd = pair(ndelta, ndelta);
+                  } else {
+                    const ulonglong2 four = qdelta[k >> 1];
+                    nd = k & 1 ? four.y : four.x;
+                  }
+                  const uint64_t pp = pair(p[2 * k], p[2 * k + 1]);
+                  float &d0 = ds[16 * hf + 2 * k], &d1 = ds[16 * hf + 2 * k + 1];
+                  unpair(fma2(pair(z[2 * k], z[2 * k + 1]), pair(vp[2 * k], vp[2 * k + 1]),
+                              mul2(pp, nd)),
+                         &d0, &d1);
+                  if (DQ && !kSeveral) mass = add2(mass, pp);
+                  if (kMask) {
+                    const int n = c0 + 16 * cc + 2 * k;
+                    d0 = (DQ ? n < limit : n >= limit) ? d0 : 0.0f;
+                    d1 = (DQ ? n + 1 < limit : n + 1 >= limit) ? d1 : 0.0f;
+                  }
+                }
+                uint32_t o[8];
+                if (!DQ) {
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
+                  tmem_st8(ts + 8 * cc, o);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  o[k] = pack2<T>(ds[16 * hf + 2 * k], ds[16 * hf + 2 * k + 1]);
+                tmem_st8(tp + 8 * cc, o);
+              }
+              if (DQ && a.sum_bufs) {
+                uint64_t s2 = 0;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) s2 = add2(s2, pair(ds[2 * k], ds[2 * k + 1]));
+                float s0, s1;
+                unpair(s2, &s0, &s1);
+                const float sum = s0 + s1;
+                eps += sum;
+                if (!kSeveral && !(kMask && near)) {
+                  unpair(mass, &s0, &s1);
+                  if (low > 0) {
+                    far_r += sum;
+                    mass_r += s0 + s1;
+                  } else {
+                    far_l += sum;
+                    mass_l += s0 + s1;
+                  }
+                } else {
+                  // Sums down the diagonals of the 32 x 32 block: a running sum moves one
+                  // lane (row) on with every column; what lane 31 holds is complete.
+                  // Two runs of 16 columns side by side: what the first ends with belongs
+                  // to diagonals that the second goes on with.
+                  float run0 = 0.0f, run1 = 0.0f;
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) {
+                    const float up0 = __shfl_up_sync(0xffffffffu, run0, 1);
+                    const float up1 = __shfl_up_sync(0xffffffffu, run1, 1);
+                    run0 = lane ? up0 + ds[k] : ds[k];
+                    run1 = lane ? up1 + ds[16 + k] : ds[16 + k];
+                    if (lane == 31) {
+                      bar.carry[warp][k] = run0;
+                      bar.carry[warp][16 + k] = run1;
+                    }
+                  }
+                  __syncwarp();
+                  const float lo = __shfl_up_sync(0xffffffffu, run0, 16);
+                  const float hi = __shfl_sync(0xffffffffu, run0, 46 - lane);
+                  // of the diagonal of the warp's first row and the block's first column
+                  float* to = by_d + warp * nbias + low + 31 + 32 * u + span.left + kBiasMargin;
+                  if (lane < 31) to[lane - 31] += bar.carry[warp][lane] + (lane >= 16 ? hi : 0.0f);
+                  __syncwarp();
+                  to[31 - lane] += run1 + (lane >= 16 ? lo : 0.0f);
+                  __syncwarp();
                 }
               }
-            } else if (DQ) {
-              const float f = far + nlse;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) score(k, pair(f, f));
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const ulonglong2 four = qlse[k >> 1];
-                score(k, add2(pair(far, far), k & 1 ? four.y : four.x));
-              }
             }
-#pragma unroll
-            for (int k = 0; k < 16; ++k) p[k] = exp2_approx(p[k]);
-            if (masked) {
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                p[k] = (DQ ? col + 16 * hf + k < limit : col + 16 * hf + k >= limit) ? p[k] : 0.0f;
+          };
+          using Yes = std::true_type;
+          using No = std::false_type;
+          if (masked)
+            weigh(No(), Yes());
+          else if (near)
+            weigh(Yes(), No());
+          else
+            weigh(No(), No());
+          tmem_wait_st();
+          if (DQ && keys < a.Lk && c0 + kTileRows > keys) {
+            // Rows of K past the length have dS = 0, but may hold anything.
+            const int live = keys - c0;
+            for (int k = threadIdx.x & 127; k < (kTileRows - live) * 8 * (DP / 64); k += 128) {
+              const int r = live + (k >> 3) % (kTileRows - live), y = (k >> 3) / (kTileRows - live);
+              *reinterpret_cast<uint4*>(stage + y * (kTileRows * 128) + r * 128 + (k & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
             }
-            float z[16];
-            if (DROP && DQ) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint4 w = keep_words(a.keep, (rows0 + (uint32_t)x) * per_row +
-                                                       (uint32_t)((col >> 3) + 2 * hf + k));
-                const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  keep_pair(v[e], T2, p[8 * k + 2 * e], p[8 * k + 2 * e + 1],
-                            &z[8 * k + 2 * e], &z[8 * k + 2 * e + 1]);
-              }
-            } else {
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                z[k] = !DROP || (kept[u] >> (16 * hf + k) & 1) ? p[k] : 0.0f;
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              uint64_t nd;
-              if (DQ) {
-                nd = pair(ndelta, ndelta);
-              } else {
-                const ulonglong2 four = qdelta[k >> 1];
-                nd = k & 1 ? four.y : four.x;
-              }
-              const uint64_t pp = pair(p[2 * k], p[2 * k + 1]);
-              unpair(fma2(pair(z[2 * k], z[2 * k + 1]), pair(vp[2 * k], vp[2 * k + 1]), mul2(pp, nd)),
-                     &ds[16 * hf + 2 * k], &ds[16 * hf + 2 * k + 1]);
-              if (DQ) mass = add2(mass, pp);
-            }
-            if (masked) {
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                float& e = ds[16 * hf + k];
-                e = (DQ ? col + 16 * hf + k < limit : col + 16 * hf + k >= limit) ? e : 0.0f;
-              }
-            }
-            uint32_t o[8];
-            if (!DQ) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
-              tmem_st8(ts + 8 * cc, o);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              o[k] = pack2<T>(ds[16 * hf + 2 * k], ds[16 * hf + 2 * k + 1]);
-            tmem_st8(tp + 8 * cc, o);
+            fence_async_shared();
           }
-          if (sums) {
-            uint64_t s2 = 0;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) s2 = add2(s2, pair(ds[2 * k], ds[2 * k + 1]));
-            float s0, s1;
-            unpair(s2, &s0, &s1);
-            const float sum = s0 + s1;
-            eps += sum;
-            if (!near) {
-              unpair(mass, &s0, &s1);
-              if (d > 0) {
-                far_r += sum;
-                mass_r += s0 + s1;
-              } else {
-                far_l += sum;
-                mass_l += s0 + s1;
-              }
-            } else {
-              // Sums down the diagonals of the 32 x 32 block: a running sum moves one
-              // lane (row) on with every column; what lane 31 holds is complete.
-              float run = 0.0f;
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                const float up = __shfl_up_sync(0xffffffffu, run, 1);
-                run = lane ? up + ds[k] : ds[k];
-                if (lane == 31) bar.carry[warp][k] = run;
-              }
-              __syncwarp();
-              float* to = by_d + warp * nbias + d + span.left + kBiasMargin;
-              if (lane < 31) to[lane - 31] += bar.carry[warp][lane];
-              __syncwarp();
-              to[31 - lane] += run;
-              __syncwarp();
-            }
-          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.p_full[g]);
         }
-        tmem_wait_st();
-        if (DQ && keys < a.Lk && c0 + kTileRows > keys) {
-          // Rows of K past the length have dS = 0, but may hold anything.
-          const int live = keys - c0;
-          for (int k = threadIdx.x & 127; k < (kTileRows - live) * 8 * (DP / 64); k += 128) {
-            const int r = live + (k >> 3) % (kTileRows - live), y = (k >> 3) / (kTileRows - live);
-            *reinterpret_cast<uint4*>(stage + y * (kTileRows * 128) + r * 128 + (k & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
-          fence_async_shared();
+        if (a.biased) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.bias_empty[nb & 1]);
+          ++nb;
         }
-        tc_fence_before();
-        mbar_arrive(&bar.p_full[g]);
-      }
-    }
-    if (ok && total > 0) ok = warp_wait(&bar.done, 0, a.err);
-    if (!ok) *dead = 1;
-    tc_fence_after();
-
-    // ----- results --------------------------------------------------------------
-    const int rows_x = DQ ? a.Lq : a.Lk;
-    const bool none = total == 0 || (!DQ && x >= keys);
-#pragma unroll 1
-    for (int c = g; c < (DQ ? 1 : 2) * DP / 32; c += G) {
-      uint32_t r[32];
-      if (total > 0) {
-        tmem_ld32(r, tmem + lanes + S::kAcc + 32 * c);
-        tmem_wait_ld(r);
-      }
-      const bool second = DQ || c >= DP / 32;
-      const Heads& out = second ? a.out2 : a.out1;
-      const int col = 32 * (DQ ? c : c % (DP / 32));
-      const float mul = second ? a.scale * a.keep.scale : a.keep.scale;
-      T* to = static_cast<T*>(out.data) + b * out.b + (int64_t)x * out.l + hx * out.h + col;
-      if (x < rows_x) {
+        }
+      nt += heads * it.per;
+      if (DQ && a.sum_bufs && ok) {
+        float* r = by_d + S::kWarps * nbias + g * kRows + row;
+        const float v[5] = {eps, far_l, far_r, mass_l, mass_r};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (col + 8 * k >= a.D) break;
-          uint32_t o[4] = {0, 0, 0, 0};
-          if (!none) {
+        for (int i = 0; i < 5; ++i) r[i * G * kRows] = v[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.sums_full[k % a.sum_bufs]);
+      }
+      if (!ok) break;
+      const Item done = it;
+      have = take(k + 1, it);
+      if (have) fetch(it);  // on its way meanwhile
+      ok = warp_wait(&bar.acc_full, k & 1, a.err);
+      if (!ok) break;
+      tc_fence_after();
+      // ----- results: 32 columns at a time, the groups in turn ----------------------
+      constexpr int kChunks = (DQ ? 1 : 2) * DP / 32, kMine = (kChunks + G - 1) / G;
+      uint32_t r[kMine][32];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              o[e] = pack2<T>(__uint_as_float(r[8 * k + 2 * e]) * mul,
-                              __uint_as_float(r[8 * k + 2 * e + 1]) * mul);
+      for (int i = 0; i < kMine; ++i)
+        if (g + i * G < kChunks) tmem_ld32(r[i], tmem + lanes + S::kAcc + 32 * (g + i * G));
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) tmem_wait_ld(r[i]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.acc_free);
+      const bool none = !DQ && x >= keys;
+      if (x < (DQ ? a.Lq : a.Lk)) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int c = g + i * G;
+          if (c >= kChunks) break;
+          const bool second = DQ || c >= DP / 32;
+          const Heads& out = second ? a.out2 : a.out1;
+          const int col = 32 * (DQ ? c : c % (DP / 32));
+          const float mul = second ? a.scale * a.keep.scale : a.keep.scale;
+          T* to = static_cast<T*>(out.data) + done.b * out.b + (int64_t)x * out.l + done.hx * out.h + col;
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            if (col + 8 * n >= a.D) break;
+            uint32_t o[4] = {0, 0, 0, 0};
+            if (!none) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                o[e] = pack2<T>(__uint_as_float(r[i][8 * n + 2 * e]) * mul,
+                                __uint_as_float(r[i][8 * n + 2 * e + 1]) * mul);
+            }
+            *reinterpret_cast<uint4*>(to + 8 * n) = make_uint4(o[0], o[1], o[2], o[3]);
           }
-          *reinterpret_cast<uint4*>(to + 8 * k) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
     }
-    if (sums) {
-      // A row's dS sums to zero; what it sums to is the error of rowsum(do o),
-      // taken from the rounded o.  It is taken out of the far buckets, whose
-      // weight would multiply it, and out of the row's entry for dk.
-      bar.eps[g][row] = eps;
-      named_sync(1, 128 * G);
-      float e = 0.0f;
-#pragma unroll
-      for (int k = 0; k < G; ++k) e += bar.eps[k][row];
-      if (g == 0)
-        a.rows[row_at(b * a.H + h0, a.Lqp, x) + kTileRows] = ndelta - e;
-      far_l -= e * mass_l;
-      far_r -= e * mass_r;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        far_l += __shfl_xor_sync(0xffffffffu, far_l, o);
-        far_r += __shfl_xor_sync(0xffffffffu, far_r, o);
-      }
-      if (lane == 0) {
-        bar.far[warp][0] = far_l;
-        bar.far[warp][1] = far_r;
-      }
-      named_sync(1, 128 * G);
-      const int last_l = a.rp.side - 1, last_r = a.rp.two_sided ? a.rp.num_buckets - 1 : 0;
-      float* to = a.partial + (((int64_t)h0 * a.B + b) * gridDim.x + blockIdx.x) * a.rp.num_buckets;
-      for (int k = warp; k < a.rp.num_buckets; k += S::kWarps) {
-        int64_t lo, hi;
-        bucket_range(bar.first, a.rp.side, a.rp.two_sided, k, -(span.left + kBiasMargin),
-                     span.right + kBiasMargin, &lo, &hi);
-        float sum = 0.0f;
-        for (int i = (int)lo + span.left + kBiasMargin + lane;
-             i < (int)hi + span.left + kBiasMargin; i += 32)
-#pragma unroll
-          for (int w = 0; w < S::kWarps; ++w) sum += by_d[w * nbias + i];
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) {
-          for (int w = 0; w < S::kWarps; ++w) {
-            if (k == last_l) sum += bar.far[w][0];
-            if (k == last_r) sum += bar.far[w][1];
-          }
-          to[k] = sum * a.keep.scale;
-        }
-      }
-    }
-    tc_fence_before();
   }
   __syncthreads();
   if (warp == kProducts) {
@@ -665,17 +855,35 @@ cudaError_t grad_of(const AttnArgs& a, GradArgs f, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   f.out1 = DQ ? a.dq : a.dv;
   f.out2 = DQ ? a.dq : a.dk;
-  constexpr size_t most = 1024 + S::kBias + kBiasMostBytes * (DQ ? 1 + S::kWarps : 1);
-  const size_t bytes = 1024 + S::kBias +
-                       (a.biased ? bias_floats(a.rp) * 4 * (f.partial ? 1 + S::kWarps : 1) : 0);
+  f.blocks = (Lx + kRows - 1) / kRows;
+  f.items = f.blocks * a.B * Hx;
+  f.next += DQ ? 0 : 1;
+  constexpr size_t most = 227 * 1024 - 256 - sizeof(GradBars<S::kGroups, S::kStages>);
+  size_t bytes = 1024 + S::kBias;
+  if (a.biased) {
+    const int n = bias_floats(a.rp);
+    bytes += 2 * n * sizeof(float);
+    if (DQ && f.partial) {
+      // Two buffers, so that the sums of a piece are added up beside the next
+      // one; a wide bias (over some 300 distances a side) leaves room for one.
+      const size_t one = S::sum_floats(n) * sizeof(float);
+      f.sum_bufs = bytes + 2 * one <= most ? 2 : 1;
+      bytes += f.sum_bufs * one;
+    }
+  }
+  static_assert(1024 + S::kBias + 2 * kBiasMostBytes + (DQ ? S::kWarps * kBiasMostBytes + 5 * S::kGroups * kRows * 4 : 0) <= most,
+                "the widest bias must fit");
   static PerDeviceOnce once;
   e = once.run([] {
     return cudaFuncSetAttribute(k_attn_grad<T, DP, DQ, DROP>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   });
   if (e != cudaSuccess) return e;
-  const dim3 grid((Lx + kRows - 1) / kRows, a.B * Hx);
-  k_attn_grad<T, DP, DQ, DROP><<<grid, S::kThreads, bytes, s>>>(f);
+  int dev = 0, sms = 0;
+  e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  k_attn_grad<T, DP, DQ, DROP><<<f.items < sms ? f.items : sms, S::kThreads, bytes, s>>>(f);
   return cudaGetLastError();
 }
 
@@ -685,6 +893,8 @@ cudaError_t grad(const AttnArgs& a, const GradArgs& f, cudaStream_t s) {
     return a.keep.T ? grad_of<T, 64, DQ, true>(a, f, s) : grad_of<T, 64, DQ, false>(a, f, s);
   return a.keep.T ? grad_of<T, 128, DQ, true>(a, f, s) : grad_of<T, 128, DQ, false>(a, f, s);
 }
+
+constexpr size_t kCounterBytes = 256;
 
 int padded(int Lq) { return (Lq + kRows - 1) / kRows * kRows; }
 
@@ -712,15 +922,16 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t s) {
   f.table = a.table;
   f.kv_len = a.kv_len;
   f.keep = a.keep;
-  f.rows = static_cast<float*>(a.workspace);
+  f.next = static_cast<unsigned*>(a.workspace);
+  f.rows = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounterBytes);
   f.Lqp = padded(a.Lq);
+  RowArgs r{a.B, a.H, a.D, a.Lq, f.Lqp, a.o, a.grad_o, a.lse, 1.0f / a.keep.scale, f.rows, f.next};
+  const int64_t rows = (int64_t)a.B * a.H * f.Lqp;
+  k_rows<T><<<(unsigned)(rows ? rows / kRowsPerBlock : 1), 16 * kRowsPerBlock, 0, s>>>(r);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   if (a.Lq) {
-    RowArgs r{a.B, a.H, a.D, a.Lq, f.Lqp, a.o, a.grad_o, a.lse, 1.0f / a.keep.scale, f.rows};
-    const int64_t rows = (int64_t)a.B * a.H * f.Lqp;
-    k_rows<T><<<(unsigned)((rows + kRowsPerBlock - 1) / kRowsPerBlock), 16 * kRowsPerBlock, 0, s>>>(r);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    if (a.dtable) f.partial = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + rows_bytes(a));
+    if (a.dtable) f.partial = f.rows + rows_bytes(a) / sizeof(float);
     e = grad<T, true>(a, f, s);
     if (e != cudaSuccess) return e;
     if (a.dtable) {
@@ -737,7 +948,7 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 size_t attn_workspace_bytes(const AttnArgs& a) {
-  size_t n = rows_bytes(a);
+  size_t n = kCounterBytes + rows_bytes(a);
   if (a.biased)
     n += (size_t)a.B * a.H * ((a.Lq + kRows - 1) / kRows) * a.rp.num_buckets * sizeof(float);
   return n;

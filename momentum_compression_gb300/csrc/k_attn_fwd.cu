@@ -54,14 +54,8 @@ struct FwdBars {
   uint64_t q_full, k_full[3], v_full[3], k_empty[3], v_empty[3], s_full[kGroups], p_full[kGroups];
   uint64_t drain;
   uint32_t tmem;
-  int dead;
   int first[OB_RELPOS_MAX_SIDE];
 };
-
-// All lanes of a warp wait and take the same decision.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, &g_attn_error, kErrWaitFull));
-}
 
 template <typename T, int DP, int BN, bool DROP>
 __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
@@ -73,7 +67,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
   constexpr bool kAhead = DP > 64;
   extern __shared__ uint8_t raw[];
   __shared__ FwdBars bar;
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~1023ull);
+  uint8_t* smem = align_shared(raw);
   float* bias = reinterpret_cast<float*>(smem + S::kBias);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hkv);
@@ -103,7 +97,6 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
       mbar_init(&bar.p_full[g], kRows);
     }
     mbar_init(&bar.drain, 1);
-    bar.dead = 0;
     fence_barrier_init();
   }
   if (warp == kCompute / 32) tmem_alloc(&bar.tmem, S::kAlloc);
@@ -116,41 +109,50 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
-  volatile int* dead = &bar.dead;
 
   if (warp == kCompute / 32 + 1) {
     // ----- copies --------------------------------------------------------
-    if (lane == 0 && most > 0) {
-      uint32_t groups = 0;
-      for (int g = 0; g < kGroups; ++g) groups += tiles[g] > 0;
-      mbar_arrive_expect_tx(&bar.q_full, groups * S::kQ);
-      for (int g = 0; g < kGroups; ++g)
-        if (tiles[g] > 0)
-          for (int x = 0; x < DP / 64; ++x)
-            tma_load4(smem + g * S::kQ + x * (kRows * 128), &a.q, 64 * x, q0 + g * kRows, h, b,
-                      &bar.q_full);
-      int n = 0;
-      for (; n < most; ++n) {
+    if (most > 0) {
+      if (lane == 0) {
+        uint32_t groups = 0;
+        for (int g = 0; g < kGroups; ++g) groups += tiles[g] > 0;
+        mbar_arrive_expect_tx(&bar.q_full, groups * S::kQ);
+        for (int g = 0; g < kGroups; ++g)
+          if (tiles[g] > 0)
+            for (int x = 0; x < DP / 64; ++x)
+              tma_load4(smem + g * S::kQ + x * (kRows * 128), &a.q, 64 * x, q0 + g * kRows, h, b,
+                        &bar.q_full);
+      }
+      bool ok = true;
+      int n = 0, nv = 0;  // tiles of K and V asked for
+      for (; n < most; ++n, ++nv) {
         const int st = n % S::kStages;
         const uint32_t par = (n / S::kStages + 1) & 1;
         uint8_t* kt = smem + kGroups * S::kQ + 2 * st * S::kTile;
-        if (n >= S::kStages && (!mbar_wait(&bar.k_empty[st], par, &g_attn_error, kErrWaitEmpty) || *dead)) break;
-        mbar_arrive_expect_tx(&bar.k_full[st], S::kTile);
-        for (int x = 0; x < DP / 64; ++x)
-          tma_load4(kt + x * (BN * 128), &a.k, 64 * x, n * BN, hk, b, &bar.k_full[st]);
-        if (n >= S::kStages && (!mbar_wait(&bar.v_empty[st], par, &g_attn_error, kErrWaitEmpty) || *dead)) break;
-        mbar_arrive_expect_tx(&bar.v_full[st], S::kTile);
-        for (int x = 0; x < DP / 64; ++x)
-          tma_load4(kt + S::kTile + x * (BN * 128), &a.v, 64 * x, n * BN, hk, b, &bar.v_full[st]);
-      }
-      if (n < most) {  // a wait ran out: let what is in flight land before the block ends
-        *dead = 1;
-        mbar_wait(&bar.q_full, 0, &g_attn_error, kErrDrain);
-        for (int i = max(0, n - S::kStages); i <= n; ++i) {
-          mbar_wait(&bar.k_full[i % S::kStages], (i / S::kStages) & 1, &g_attn_error, kErrDrain);
-          if (i < n)
-            mbar_wait(&bar.v_full[i % S::kStages], (i / S::kStages) & 1, &g_attn_error, kErrDrain);
+        if (n >= S::kStages) ok = warp_wait(&bar.k_empty[st], par, &g_attn_error, kErrWaitEmpty);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar.k_full[st], S::kTile);
+          for (int x = 0; x < DP / 64; ++x)
+            tma_load4(kt + x * (BN * 128), &a.k, 64 * x, n * BN, hk, b, &bar.k_full[st]);
         }
+        if (n >= S::kStages) ok = warp_wait(&bar.v_empty[st], par, &g_attn_error, kErrWaitEmpty);
+        if (!ok) {
+          ++n;
+          break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar.v_full[st], S::kTile);
+          for (int x = 0; x < DP / 64; ++x)
+            tma_load4(kt + S::kTile + x * (BN * 128), &a.v, 64 * x, n * BN, hk, b, &bar.v_full[st]);
+        }
+      }
+      if (!ok) {  // a wait ran out: let what is in flight land before the block ends
+        mbar_wait(&bar.q_full, 0, &g_attn_error, kErrDrain);
+        for (int i = max(0, n - S::kStages); i < n; ++i)
+          mbar_wait(&bar.k_full[i % S::kStages], (i / S::kStages) & 1, &g_attn_error, kErrDrain);
+        for (int i = max(0, nv - S::kStages); i < nv; ++i)
+          mbar_wait(&bar.v_full[i % S::kStages], (i / S::kStages) & 1, &g_attn_error, kErrDrain);
       }
     }
   } else if (warp == kCompute / 32) {
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
       const uint64_t q_desc = desc_k(qs), k_desc = desc_k(kv),
                      v_desc = desc_mn(kv + S::kTile, BN * 128);
       const int ksteps = (a.D + 15) / 16;
-      bool ok = warp_wait(&bar.q_full, 0);
+      bool ok = warp_wait(&bar.q_full, 0, &g_attn_error);
       auto scores = [&](int g, int st) {
         const uint64_t qd = q_desc + (uint32_t)g * (S::kQ >> 4);
         const uint64_t kd = k_desc + (uint32_t)st * (2 * S::kTile >> 4);
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
             mma_ss(leader, tmem + g * BN, qd + (((s >> 2) * (kRows * 128) + (s & 3) * 32) >> 4),
                    kd + (((s >> 2) * (BN * 128) + (s & 3) * 32) >> 4), kShapeS, s > 0);
       };
-      ok = ok && warp_wait(&bar.k_full[0], 0);
+      ok = ok && warp_wait(&bar.k_full[0], 0, &g_attn_error);
       if (ok) {
         tc_fence_after();
 #pragma unroll
@@ -187,13 +189,13 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
       int st = 0, par = 0;  // of tile n
       for (int n = 0; ok && n < most; ++n) {
         const int next = st + 1 == S::kStages ? 0 : st + 1, next_par = next ? par : par ^ 1;
-        ok = warp_wait(&bar.v_full[st], par);
-        if (ok && n + 1 < most) ok = warp_wait(&bar.k_full[next], next_par);
+        ok = warp_wait(&bar.v_full[st], par, &g_attn_error);
+        if (ok && n + 1 < most) ok = warp_wait(&bar.k_full[next], next_par, &g_attn_error);
         const uint64_t vd = v_desc + (uint32_t)st * (2 * S::kTile >> 4);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
           if (!ok || n >= tiles[g]) continue;
-          ok = warp_wait(&bar.p_full[g], n & 1) && !*dead;
+          ok = warp_wait(&bar.p_full[g], n & 1, &g_attn_error);
           if (!ok) continue;
           tc_fence_after();
 #pragma unroll
@@ -210,7 +212,6 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
         par = next_par;
       }
       if (!ok) {
-        *dead = 1;
         mma_commit(leader, &bar.drain);
         mbar_wait(&bar.drain, 0, &g_attn_error, kErrDrain);
       }
@@ -240,15 +241,20 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
       uint32_t p[BN / 2];
       auto draw = [&] {
 #pragma unroll
-        for (int k = 0; k < BN / 8; ++k) {
-          const uint4 w = keep_words(a.keep, call0 + (uint32_t)(n * (BN / 8) + k));
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        for (int k = 0; k < BN / 8; k += 4) {
+          uint4 w[4];
+          keep_words_n(a.keep, call0 + (uint32_t)(n * (BN / 8) + k), 1, w);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[4 * k + e] = keep_mask2(u[e], T2);
+          for (int q = 0; q < 4; ++q) {
+            p[4 * (k + q)] = keep_mask2(w[q].x, T2);
+            p[4 * (k + q) + 1] = keep_mask2(w[q].y, T2);
+            p[4 * (k + q) + 2] = keep_mask2(w[q].z, T2);
+            p[4 * (k + q) + 3] = keep_mask2(w[q].w, T2);
+          }
         }
       };
       if (DROP) draw();
-      ok = warp_wait(&bar.s_full[g], n & 1);
+      ok = warp_wait(&bar.s_full[g], n & 1, &g_attn_error);
       if (!ok) break;
       tc_fence_after();
       float sum, top;
@@ -331,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
       if (keys < a.Lk && (n + 1) * BN > keys) {
         // Rows of V past the length have weight zero, but may hold anything.
         const int st = n % S::kStages;
-        ok = warp_wait(&bar.v_full[st], (n / S::kStages) & 1);
+        ok = warp_wait(&bar.v_full[st], (n / S::kStages) & 1, &g_attn_error);
         if (!ok) break;
         uint8_t* vt = smem + kGroups * S::kQ + (2 * st + 1) * S::kTile;
         const int from = keys - n * BN;  // > 0: the tile holds a key
@@ -346,8 +352,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
       mbar_arrive(&bar.p_full[g]);
     }
     if (ok && mine > 0)
-      ok = warp_wait(&bar.s_full[g], mine & 1);
-    if (!ok) *dead = 1;
+      ok = warp_wait(&bar.s_full[g], mine & 1, &g_attn_error);
     tc_fence_after();
     // ----- o = O / l -------------------------------------------------------
     const float inv = l > 0.0f || l != l ? a.keep.scale / l : 0.0f;

@@ -35,6 +35,26 @@ __device__ __forceinline__ uint4 keep_words(const Keep& k, uint64_t call) {
                        k.keys);
 }
 
+// The words of N calls, `step` calls apart: N independent chains side by side,
+// so that one lane's dependent multiplies overlap.
+template <int N>
+__device__ __forceinline__ void keep_words_n(const Keep& k, uint64_t call, uint64_t step,
+                                             uint4 (&w)[N]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const uint64_t c = call + n * step;
+    w[n] = make_uint4((uint32_t)c, (uint32_t)(c >> 32), k.off_lo, k.off_hi);
+  }
+#pragma unroll
+  for (int r = 0; r < 10; ++r)
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const uint64_t p0 = (uint64_t)0xD2511F53u * w[n].x, p1 = (uint64_t)0xCD9E8D57u * w[n].z;
+      w[n] = make_uint4((uint32_t)(p1 >> 32) ^ w[n].y ^ k.keys.k0[r], (uint32_t)p1,
+                        (uint32_t)(p0 >> 32) ^ w[n].w ^ k.keys.k1[r], (uint32_t)p0);
+    }
+}
+
 // Whether element i (0..7) of a call's eight is kept.
 __device__ __forceinline__ bool kept(const uint4& w, int i, uint32_t T) {
   const uint32_t x = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
