@@ -694,13 +694,16 @@ typedef struct {
   float scale;            /* > 0 */
   int causal;
   int64_t q_offset;       /* position of query 0 among the keys, |q_offset| < 2^24 */
-  const ob_relpos* relpos; /* NULL: no bias; max_distance <= OB_ATTN_MAX_DISTANCE */
+  const ob_relpos* relpos; /* NULL: no bias; span <= OB_ATTN_MAX_SPAN */
   const void* table;      /* [num_buckets][H], contiguous */
   const int32_t* kv_len;  /* [B], on the device, or NULL */
   double p;               /* in [0, 255/256] */
   uint64_t seed, offset;
 } ob_attn;
-#define OB_ATTN_MAX_DISTANCE 512 /* the staged bias and the bucket sums fit beside the tiles */
+/* The span of a bias: the distances between its outermost buckets,
+ * first[side - 1] one-sided and twice that two-sided (182 for 32 two-sided
+ * buckets up to 128).  A head's values over the span stay in shared memory. */
+#define OB_ATTN_MAX_SPAN 512
 
 /* Rows of D contiguous elements; entry b, row i, head h starts at
  * data + b * stride_b + i * stride_l + h * stride_h (elements).  data is

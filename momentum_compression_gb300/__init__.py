@@ -31,7 +31,7 @@ OB_MODE_ADAM, OB_MODE_LAMB = 0, 1
 OB_MAX_WORKERS = 64
 OB_TYPE_F32, OB_TYPE_BF16, OB_TYPE_F16 = 0, 1, 2
 OB_RELPOS_MAX_SIDE = 128  # buckets a side of a relative position bias
-OB_ATTN_MAX_DISTANCE = 512  # max_distance of a bias inside the attention
+OB_ATTN_MAX_SPAN = 512  # distances between the outermost buckets of a bias inside the attention
 OB_NOALLOC_SCRATCH_BYTES = 4 << 20  # the static scratch of ob_compress_noalloc
 OB_FLAG_NO_RATIO_EF = 1 << 0
 OB_FLAG_FROZEN_C = 1 << 1

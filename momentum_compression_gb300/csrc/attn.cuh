@@ -51,14 +51,14 @@ __device__ __forceinline__ int key_count(const int32_t* kv_len, int Lk, int b) {
 
 // ---------------------------------------------------------------------------
 // Bias.  Distances up to -left share one bucket and so do those from right on;
-// between them (and kBiasMargin past either end, so that a block of 32 rows
-// and 64 columns that touches the range is covered whole) the values of one
-// head, times log2(e), are staged in shared memory.
+// between them (and kBiasMargin past either end, so that a block of 32 x 32
+// that touches the range is covered whole) the values of one head, times
+// log2(e), are staged in shared memory.
 // ---------------------------------------------------------------------------
 
-constexpr int kBiasMargin = 96;
-
-constexpr int kBiasMostBytes = 4 * (2 * OB_ATTN_MAX_DISTANCE + 2 * kBiasMargin + 1);
+constexpr int kBiasMargin = 64;
+constexpr int kBiasMost = OB_ATTN_MAX_SPAN + 2 * kBiasMargin + 1;  // floats
+constexpr int kBiasMostBytes = 4 * kBiasMost;
 
 struct BiasSpan {
   int left, right;
@@ -72,16 +72,19 @@ __host__ __device__ inline int bias_floats(const ob_relpos& rp) {
   return s.left + s.right + 2 * kBiasMargin + 1;
 }
 
-// tab[d + left + margin], by threads tid of n.
-template <typename T>
-__device__ __forceinline__ void stage_bias(float* tab, const ob_relpos& rp, const int* first,
-                                           const T* table, int H, int h, int tid, int n) {
+// Buckets of the staged distances (entry t: distance t - left - margin), by
+// threads tid of n; rp is the kernel's parameter.
+__device__ __forceinline__ void stage_buckets(uint8_t* map, const ob_relpos& rp, int tid, int n) {
   const BiasSpan s = bias_span(rp);
   const int count = s.left + s.right + 2 * kBiasMargin + 1;
-  for (int t = tid; t < count; t += n) {
-    const int b = bucket_of(first, rp.side, rp.two_sided, t - s.left - kBiasMargin);
-    tab[t] = to_f32(table[(size_t)b * H + h]) * kLog2e;
-  }
+  for (int t = tid; t < count; t += n)
+    map[t] = (uint8_t)bucket_of(rp.first, rp.side, rp.two_sided, t - s.left - kBiasMargin);
+}
+template <typename T>
+__device__ __forceinline__ void stage_bias(float* tab, const uint8_t* map, int count,
+                                           const T* table, int H, int h, int tid, int n) {
+#pragma unroll 4
+  for (int t = tid; t < count; t += n) tab[t] = to_f32(table[(size_t)map[t] * H + h]) * kLog2e;
 }
 
 // ---------------------------------------------------------------------------

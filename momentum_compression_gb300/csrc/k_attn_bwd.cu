@@ -12,8 +12,10 @@
 //   S = X U^T, dP = Y W^T   128 x 64 each in tensor memory
 //   Z, dS                   from them in registers, rounded over S and dP
 //   acc1 += Z W (dv), acc2 += dS U (dq or dk)    first operand from tensor memory
-// The warpgroups of a block take turns over the tiles, so one's arithmetic
-// runs beside another's products.
+// Two tiles are in work at a time, each by two warpgroups (32 columns each), so
+// one's arithmetic runs beside the other's products: sixteen warps that work,
+// since a single one's dependent instructions leave three of four issue slots
+// empty.
 //
 // A block stays on its SM and takes one piece of work (128 rows of X) after
 // another from a counter, the products of the next begun before the last of
@@ -117,8 +119,8 @@ __global__ void __launch_bounds__(16 * kRowsPerBlock) k_rows(const RowArgs a) {
 
 template <int DP, bool DQ>
 struct GradShape {
-  static constexpr int kGroups = DP == 64 ? 3 : 2;
-  static constexpr int kStages = DP == 64 ? 5 : 3;
+  static constexpr int kGroups = 4, kSlots = 2;  // warpgroups, tiles in work
+  static constexpr int kStages = DP == 64 ? 4 : 3;
   static constexpr int kXBufs = DP == 64 ? 2 : 1;
   static constexpr int kWarps = 4 * kGroups;
   static constexpr int kThreads = 32 * (kWarps + 4);  // and the four warps of the other roles
@@ -127,8 +129,9 @@ struct GradShape {
   static constexpr uint32_t kStage = 2 * kTile + (DQ ? 0 : 1024);  // U, W and the queries' rows
   static constexpr uint32_t kRing = kXBufs * 2 * kX;               // offset of the stages
   static constexpr uint32_t kBias = kRing + kStages * kStage;      // of two biases, then the sums
-  // tensor memory: S and dP of each group, the accumulators
-  static constexpr uint32_t kAcc = 128 * kGroups;
+  // tensor memory: S and dP of each slot, one or two sets of accumulators
+  static constexpr uint32_t kAcc = 128 * kSlots, kAccCols = DQ ? DP : 2 * DP;
+  static constexpr int kAccBufs = (512 - kAcc) / kAccCols >= 2 ? 2 : 1;
   // floats of one buffer of sums: by distance for each warp, and of each
   // group's rows eps, far left and right, mass left and right
   __host__ __device__ static constexpr int sum_floats(int nbias) {
@@ -136,21 +139,22 @@ struct GradShape {
   }
 };
 
-constexpr int kSlots = 8;
+constexpr int kItems = 8;  // pieces handed out at a time
 
 struct Item {
   int x0, b, hx, keys, from, per;  // x0 < 0: no more
 };
 
-template <int G, int S>
+template <int W, int S>
 struct GradBars {
-  uint64_t item_full[kSlots], item_empty[kSlots];
-  uint64_t x_full[2], x_empty[2], full[S], empty[S], s_full[G], p_full[G], acc_full, acc_free;
+  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t x_full[2], x_empty[2], full[S], empty[S], s_full[2], p_full[2], acc_full[2], acc_free[2];
   uint64_t bias_full[2], bias_empty[2], sums_full[2], sums_empty[2], drain[2];
-  Item item[kSlots];
+  Item item[kItems];
   uint32_t tmem;
   int first[OB_RELPOS_MAX_SIDE];
-  float carry[4 * G][32];
+  uint8_t bucket[kBiasMost];
+  float carry[W][32];
 };
 
 // The pair of weights whose halfwords are w, dropped ones as zero.
@@ -200,9 +204,9 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     k_attn_grad(const __grid_constant__ GradArgs a) {
   using S = GradShape<DP, DQ>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr int G = S::kGroups, kScores = 4 * G, kProducts = kScores + 1, kCopies = kScores + 2;
+  constexpr int G = S::kGroups, K = S::kSlots, kScores = 4 * G, kProducts = kScores + 1, kCopies = kScores + 2;
   extern __shared__ uint8_t raw[];
-  __shared__ GradBars<G, S::kStages> bar;
+  __shared__ GradBars<S::kWarps, S::kStages> bar;
   uint8_t* smem = align_shared(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const BiasSpan span = a.biased ? bias_span(a.rp) : BiasSpan{0, 0};
@@ -212,7 +216,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
   float* sums = biases + 2 * nbias;  // sum_bufs buffers of S::sum_floats(nbias)
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) {
+    for (int i = 0; i < kItems; ++i) {
       mbar_init(&bar.item_full[i], 1);
       mbar_init(&bar.item_empty[i], 2 + S::kWarps + (a.biased ? 1 : 0));
     }
@@ -224,22 +228,21 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       mbar_init(&bar.sums_full[i], S::kWarps);
       mbar_init(&bar.sums_empty[i], 1);
       mbar_init(&bar.drain[i], 1);
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], S::kWarps / K);
+      mbar_init(&bar.acc_full[i], 1);
+      mbar_init(&bar.acc_free[i], S::kWarps);
     }
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&bar.full[i], 1);
       mbar_init(&bar.empty[i], 1);
     }
-    for (int g = 0; g < G; ++g) {
-      mbar_init(&bar.s_full[g], 1);
-      mbar_init(&bar.p_full[g], 4);
-    }
-    mbar_init(&bar.acc_full, 1);
-    mbar_init(&bar.acc_free, S::kWarps);
     fence_barrier_init();
   }
   if (warp == kProducts) tmem_alloc(&bar.tmem, 512);
   if (a.biased) {
     for (int i = threadIdx.x; i < a.rp.side; i += S::kThreads) bar.first[i] = a.rp.first[i];
+    stage_buckets(bar.bucket, a.rp, threadIdx.x, S::kThreads);
     for (int i = threadIdx.x; i < a.sum_bufs * S::sum_floats(nbias); i += S::kThreads)
       sums[i] = 0.0f;
   }
@@ -251,8 +254,8 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
   // The k-th piece of work of this block, for one of the roles that follow it:
   // false after the last, or when the wait ran out.
   auto take = [&](int k, Item& it) {
-    const int slot = k % kSlots;
-    if (!warp_wait(&bar.item_full[slot], (k / kSlots) & 1, a.err)) return false;
+    const int slot = k % kItems;
+    if (!warp_wait(&bar.item_full[slot], (k / kItems) & 1, a.err)) return false;
     it = bar.item[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar.item_empty[slot]);
@@ -301,8 +304,8 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           for (int i = lane; i < a.rp.num_buckets; i += 32) to[i] = 0.0f;
         }
       }
-      const int slot = k % kSlots;
-      if (k >= kSlots) ok = warp_wait(&bar.item_empty[slot], (k / kSlots + 1) & 1, a.err, kErrWaitEmpty);
+      const int slot = k % kItems;
+      if (k >= kItems) ok = warp_wait(&bar.item_empty[slot], (k / kItems + 1) & 1, a.err, kErrWaitEmpty);
       if (ok && lane == 0) {
         bar.item[slot] = it;
         mbar_arrive(&bar.item_full[slot]);
@@ -361,8 +364,8 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     const uint64_t x_desc = desc_k(smem_u32(smem)), u_desc = desc_k(smem_u32(smem) + S::kRing);
     const int ksteps = (a.D + 15) / 16;
     bool ok = true;
-    int st = 0, par = 0, g = 0;     // stage, its phase, group of the tile
-    int fst = 0, fpar = 0, nt = 0;  // stage and phase of the tile that had the group last
+    int st = 0, par = 0, g = 0;     // stage, its phase, slot of the tile
+    int fst = 0, fpar = 0, nt = 0;  // stage and phase of the tile that had the slot last
     Item it;
     for (int k = 0; ok && take(k, it); ++k) {
       const int xb = k % S::kXBufs;
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       for (int t = 0; ok && t < total; ++t, ++nt) {
         ok = warp_wait(&bar.full[st], par, a.err);
         // Once that tile's products are done, its P and dS may be written over.
-        if (ok && nt >= G) {
+        if (ok && nt >= K) {
           ok = warp_wait(&bar.empty[fst], fpar, a.err, kErrWaitEmpty);
           if (++fst == S::kStages) fst = 0, fpar ^= 1;
         }
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
                      kShapeS, s > 0);
         mma_commit(leader, &bar.s_full[g]);
         if (++st == S::kStages) st = 0, par ^= 1;
-        if (++g == G) g = 0;
+        if (++g == K) g = 0;
       }
       mma_commit(leader, &bar.x_empty[xb]);
     }
@@ -407,29 +410,32 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     int st = 0, g = 0, gpar = 0;
     Item it;
     for (int k = 0; ok && take(k, it); ++k) {
-      const int total = heads * it.per;
+      const int total = heads * it.per, ab = k % S::kAccBufs;
+      const uint32_t acc = tmem + S::kAcc + ab * S::kAccCols;
       for (int t = 0; t < total; ++t) {
         ok = warp_wait(&bar.p_full[g], gpar, a.err);
-        if (ok && t == 0 && k > 0) ok = warp_wait(&bar.acc_free, (k + 1) & 1, a.err, kErrWaitEmpty);
+        if (ok && t == 0 && k >= S::kAccBufs)
+          ok = warp_wait(&bar.acc_free[ab], (k / S::kAccBufs + 1) & 1, a.err, kErrWaitEmpty);
         if (!ok) break;
         tc_fence_after();
         const uint64_t ud = u_rows + (uint32_t)st * (S::kStage >> 4);
         const uint32_t p = tmem + g * 128;
+        // The slot's warpgroups each left 32 rows of the sum over their own columns.
         if (!DQ) {
 #pragma unroll
           for (int s = 0; s < kTileRows / 16; ++s)
-            mma_ts(leader, tmem + S::kAcc, p + s * 8, ud + ((S::kTile + s * 2048) >> 4), kShapeA,
-                   t > 0 || s > 0);
+            mma_ts(leader, acc, p + (s >> 1) * 32 + (s & 1) * 8,
+                   ud + ((S::kTile + s * 2048) >> 4), kShapeA, t > 0 || s > 0);
         }
 #pragma unroll
         for (int s = 0; s < kTileRows / 16; ++s)
-          mma_ts(leader, tmem + S::kAcc + (DQ ? 0 : DP), p + 64 + s * 8, ud + (s * 2048 >> 4),
-                 kShapeA, t > 0 || s > 0);
+          mma_ts(leader, acc + (DQ ? 0 : DP), p + 64 + (s >> 1) * 32 + (s & 1) * 8,
+                 ud + (s * 2048 >> 4), kShapeA, t > 0 || s > 0);
         mma_commit(leader, &bar.empty[st]);
         if (++st == S::kStages) st = 0;
-        if (++g == G) g = 0, gpar ^= 1;
+        if (++g == K) g = 0, gpar ^= 1;
       }
-      if (ok) mma_commit(leader, &bar.acc_full);
+      if (ok) mma_commit(leader, &bar.acc_full[ab]);
     }
     mma_commit(leader, &bar.drain[1]);
     mbar_wait(&bar.drain[1], 0, a.err, kErrDrain);
@@ -447,7 +453,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           for (int hh = 0; ok && hh < heads; ++hh, ++nb) {
             if (nb >= 2) ok = warp_wait(&bar.bias_empty[nb & 1], (nb / 2 + 1) & 1, a.err, kErrWaitEmpty);
             if (!ok) break;
-            stage_bias(biases + (nb & 1) * nbias, a.rp, bar.first, static_cast<const T*>(a.table),
+            stage_bias(biases + (nb & 1) * nbias, bar.bucket, nbias, static_cast<const T*>(a.table),
                        a.H, DQ ? it.hx : it.hx * group + hh, lane, 32);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.bias_full[nb & 1]);
@@ -497,6 +503,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
                          span.right + kBiasMargin, &lo, &hi);
             float sum = n == a.rp.side - 1 ? far_l : 0.0f;
             if (n == (a.rp.two_sided ? a.rp.num_buckets - 1 : 0)) sum += far_r;
+#pragma unroll 4
             for (int i = (int)lo; i < (int)hi; ++i) sum += by_d[i + span.left + kBiasMargin];
             to[n] = sum * a.keep.scale;
           }
@@ -513,13 +520,13 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     }
   } else {
     // ----- arithmetic: a thread a row of X ----------------------------------
-    const int g = warp >> 2, row = (warp & 3) * 32 + lane;
+    const int g = warp >> 2, slot = g >> 1, half = g & 1, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + g * 128, tp = ts + 64;
+    const uint32_t ts = tmem + lanes + slot * 128 + half * 32, tp = ts + 64;
     const uint64_t per_row = (uint32_t)((a.Lk + 7) / 8);
     const uint32_t T2 = a.keep.T * 0x10001u;
     bool ok = true;
-    int nt = 0, next = g, nb = 0;  // tiles of earlier pieces, this group's next tile, biases used
+    int nt = 0, next = slot, nb = 0;  // tiles of earlier pieces, the slot's next tile, biases used
     float nlse = 0.0f, ndelta = 0.0f;  // of the row's query
     auto fetch = [&](const Item& of) {
       if (!DQ) return;  // Lqp covers every row of the block
@@ -560,35 +567,32 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           far_right = bias[nbias - 1];
         }
         const uint64_t rows0 = (uint64_t)(it.b * a.H + h0 + hh) * a.Lq;
-        for (; ok && next < nt + (hh + 1) * it.per; next += G) {
+        for (; ok && next < nt + (hh + 1) * it.per; next += K) {
           const int st = next % S::kStages;
-          const int c0 = (it.from + next - nt - hh * it.per) * kTileRows;  // first column (key or query)
+          // first of the group's 32 columns (keys or queries)
+          const int c0 = (it.from + next - nt - hh * it.per) * kTileRows + 32 * half;
           uint8_t* stage = smem + S::kRing + st * S::kStage;
           // The keep bits do not wait for the scores.
-          uint32_t kept[2] = {~0u, ~0u};
-          if (!DQ && DROP) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              kept[u] = keep_column(
-                  a.keep,
-                  (rows0 + (uint32_t)(c0 + 32 * u + (lane & 7))) * per_row + (uint32_t)(x >> 3),
-                  per_row, lane);
-          }
-          uint4 words[4];  // DQ: of 32 columns
+          uint32_t kept = ~0u;
+          uint4 words[4];
+          if (!DQ && DROP)
+            kept = keep_column(a.keep,
+                               (rows0 + (uint32_t)(c0 + (lane & 7))) * per_row + (uint32_t)(x >> 3),
+                               per_row, lane);
           if (DQ && DROP)
             keep_words_n(a.keep, (rows0 + (uint32_t)x) * per_row + (uint32_t)(c0 >> 3), 1, words);
-          ok = warp_wait(&bar.s_full[g], (next / G) & 1, a.err);
+          ok = warp_wait(&bar.s_full[slot], (next / K) & 1, a.err);
           if (!ok) break;
           tc_fence_after();
-          // Distances of the warp's rows and the tile's columns: [low, high].
-          const int low = (DQ ? c0 - wx - 31 : wx - c0 - 63) - a.q_offset, high = low + 94;
-          const bool near = a.biased && high > -span.left && low < span.right;
+          // Distances of the warp's rows and the columns: [low, low + 62].
+          const int low = (DQ ? c0 - wx - 31 : wx - c0 - 31) - a.q_offset;
+          const bool near = a.biased && low + 62 > -span.left && low < span.right;
           const float far = !a.biased ? 0.0f : low > 0 ? far_right : far_left;
-          const bool masked = DQ ? c0 + 64 > warp_limit : c0 < warp_limit;
+          const bool masked = DQ ? c0 + 32 > warp_limit : c0 < warp_limit;
 
-          // Z and dS of the tile.  Branch-free inside, for the scheduler's sake: a
-          // body each for tiles of one bias value, tiles across several, and tiles
-          // with masked pairs (of either kind).
+          // Z and dS of the block.  Branch-free inside, for the scheduler's sake: a
+          // body each for blocks of one bias value, blocks across several, and
+          // blocks with masked pairs (of either kind).
           auto weigh = [&](auto several_t, auto mask_t) {
             constexpr bool kSeveral = decltype(several_t)::value, kMask = decltype(mask_t)::value;
             // The bias of column n of the row: tb[n * step].
@@ -601,150 +605,134 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
             uint32_t rs[2][16], rp[2][16];
             tmem_ld16(rs[0], ts);
             tmem_ld16(rp[0], tp);
+            uint64_t mass = 0, sum2 = 0;  // sums of p and dS, two lanes of them
+            float run[2] = {0.0f, 0.0f};
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {  // 32 columns at a time
-              const int col = c0 + 32 * u;
-              if (DQ && DROP && u)
-                keep_words_n(a.keep, (rows0 + (uint32_t)x) * per_row + (uint32_t)(col >> 3), 1,
-                             words);
-              float ds[32];
-              uint64_t mass = 0;  // sums of p, two lanes of them
+            for (int c = 0; c < 2; ++c) {  // 16 columns; the next are on their way meanwhile
+              const uint32_t(&vs)[16] = rs[c];
+              const uint32_t(&vp)[16] = rp[c];
+              tmem_wait_ld(rs[c]);
+              tmem_wait_ld(rp[c]);
+              if (c == 0) {
+                tmem_ld16(rs[1], ts + 16);
+                tmem_ld16(rp[1], tp + 16);
+              }
+              const ulonglong2* qlse =  // two pairs of queries each
+                  reinterpret_cast<const ulonglong2*>(stage + 2 * S::kTile) + 8 * half + 4 * c;
+              const ulonglong2* qdelta = qlse + kTileRows / 4;
+              float p[16], z[16], ds[16];
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                const int cc = 2 * u + hf;  // 16 columns; the next 16 are on their way meanwhile
-                const uint32_t(&vs)[16] = rs[hf];
-                const uint32_t(&vp)[16] = rp[hf];
-                tmem_wait_ld(rs[hf]);
-                tmem_wait_ld(rp[hf]);
-                if (cc < 3) {
-                  tmem_ld16(rs[1 - hf], ts + 16 * (cc + 1));
-                  tmem_ld16(rp[1 - hf], tp + 16 * (cc + 1));
-                }
-                const ulonglong2* qlse =  // two pairs of queries each
-                    reinterpret_cast<const ulonglong2*>(stage + 2 * S::kTile) + 4 * cc;
-                const ulonglong2* qdelta = qlse + kTileRows / 4;
-                float p[16], z[16];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  uint64_t shift;  // bias - lse
-                  if (DQ && !kSeveral && !kMask) {
-                    shift = pair(far + nlse, far + nlse);
+              for (int k = 0; k < 8; ++k) {
+                uint64_t shift;  // bias - lse
+                if (DQ && !kSeveral && !kMask) {
+                  shift = pair(far + nlse, far + nlse);
+                } else {
+                  uint64_t nl;
+                  if (DQ) {
+                    nl = pair(nlse, nlse);
                   } else {
-                    uint64_t nl;
-                    if (DQ) {
-                      nl = pair(nlse, nlse);
-                    } else {
-                      const ulonglong2 four = qlse[k >> 1];
-                      nl = k & 1 ? four.y : four.x;
-                    }
-                    const int n = 16 * cc + 2 * k;
-                    if (kSeveral)
-                      shift = add2(DQ ? pair(tb[n], tb[n + 1]) : pair(tb[-n], tb[-n - 1]), nl);
-                    else if (kMask && a.biased)
-                      shift = add2(pair(tb[n * step], tb[(n + 1) * step]), nl);
-                    else
-                      shift = add2(pair(far, far), nl);
+                    const ulonglong2 four = qlse[k >> 1];
+                    nl = k & 1 ? four.y : four.x;
                   }
-                  unpair(fma2(pair(vs[2 * k], vs[2 * k + 1]), scale2, shift), &p[2 * k],
-                         &p[2 * k + 1]);
+                  const int n = 16 * c + 2 * k;
+                  if (kSeveral)
+                    shift = add2(DQ ? pair(tb[n], tb[n + 1]) : pair(tb[-n], tb[-n - 1]), nl);
+                  else if (kMask && a.biased)
+                    shift = add2(pair(tb[n * step], tb[(n + 1) * step]), nl);
+                  else
+                    shift = add2(pair(far, far), nl);
                 }
+                unpair(fma2(pair(vs[2 * k], vs[2 * k + 1]), scale2, shift), &p[2 * k], &p[2 * k + 1]);
+              }
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                p[k] = exp2_approx(p[k]);
+                const int n = c0 + 16 * c + k;
+                if (kMask) p[k] = (DQ ? n < limit : n >= limit) ? p[k] : 0.0f;
+              }
+              if (DROP && DQ) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const uint4& w = words[2 * c + k];
+                  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    keep_pair(v[e], T2, p[8 * k + 2 * e], p[8 * k + 2 * e + 1], &z[8 * k + 2 * e],
+                              &z[8 * k + 2 * e + 1]);
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                  z[k] = !DROP || (kept >> (16 * c + k) & 1) ? p[k] : 0.0f;
+              }
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                uint64_t nd;
+                if (DQ) {
+                  nd = pair(ndelta, ndelta);
+                } else {
+                  const ulonglong2 four = qdelta[k >> 1];
+                  nd = k & 1 ? four.y : four.x;
+                }
+                const uint64_t pp = pair(p[2 * k], p[2 * k + 1]);
+                float &d0 = ds[2 * k], &d1 = ds[2 * k + 1];
+                unpair(fma2(pair(z[2 * k], z[2 * k + 1]), pair(vp[2 * k], vp[2 * k + 1]),
+                            mul2(pp, nd)),
+                       &d0, &d1);
+                if (DQ && !kSeveral) mass = add2(mass, pp);
+                if (kMask) {
+                  const int n = c0 + 16 * c + 2 * k;
+                  d0 = (DQ ? n < limit : n >= limit) ? d0 : 0.0f;
+                  d1 = (DQ ? n + 1 < limit : n + 1 >= limit) ? d1 : 0.0f;
+                }
+                if (DQ) sum2 = add2(sum2, pair(d0, d1));
+              }
+              uint32_t o[8];
+              if (!DQ) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
+                tmem_st8(ts + 8 * c, o);
+              }
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[k] = pack2<T>(ds[2 * k], ds[2 * k + 1]);
+              tmem_st8(tp + 8 * c, o);
+              if (DQ && a.sum_bufs && (kSeveral || (kMask && near))) {
+                // Sums down the diagonals: a running sum moves one lane (row) on with
+                // every column; what lane 31 holds is complete.
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                  p[k] = exp2_approx(p[k]);
-                  const int n = c0 + 16 * cc + k;
-                  if (kMask) p[k] = (DQ ? n < limit : n >= limit) ? p[k] : 0.0f;
+                  const float up = __shfl_up_sync(0xffffffffu, run[c], 1);
+                  run[c] = lane ? up + ds[k] : ds[k];
+                  if (lane == 31) bar.carry[warp][16 * c + k] = run[c];
                 }
-                if (DROP && DQ) {
-#pragma unroll
-                  for (int k = 0; k < 2; ++k) {
-                    const uint4& w = words[2 * hf + k];
-                    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                      keep_pair(v[e], T2, p[8 * k + 2 * e], p[8 * k + 2 * e + 1],
-                                &z[8 * k + 2 * e], &z[8 * k + 2 * e + 1]);
-                  }
-                } else {
-#pragma unroll
-                  for (int k = 0; k < 16; ++k)
-                    z[k] = !DROP || (kept[u] >> (16 * hf + k) & 1) ? p[k] : 0.0f;
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  uint64_t nd;
-                  if (DQ) {
-                    nd = pair(ndelta, ndelta);
-                  } else {
-                    const ulonglong2 four = qdelta[k >> 1];
-                    nd = k & 1 ? four.y : four.x;
-                  }
-                  const uint64_t pp = pair(p[2 * k], p[2 * k + 1]);
-                  float &d0 = ds[16 * hf + 2 * k], &d1 = ds[16 * hf + 2 * k + 1];
-                  unpair(fma2(pair(z[2 * k], z[2 * k + 1]), pair(vp[2 * k], vp[2 * k + 1]),
-                              mul2(pp, nd)),
-                         &d0, &d1);
-                  if (DQ && !kSeveral) mass = add2(mass, pp);
-                  if (kMask) {
-                    const int n = c0 + 16 * cc + 2 * k;
-                    d0 = (DQ ? n < limit : n >= limit) ? d0 : 0.0f;
-                    d1 = (DQ ? n + 1 < limit : n + 1 >= limit) ? d1 : 0.0f;
-                  }
-                }
-                uint32_t o[8];
-                if (!DQ) {
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
-                  tmem_st8(ts + 8 * cc, o);
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  o[k] = pack2<T>(ds[16 * hf + 2 * k], ds[16 * hf + 2 * k + 1]);
-                tmem_st8(tp + 8 * cc, o);
               }
-              if (DQ && a.sum_bufs) {
-                uint64_t s2 = 0;
-#pragma unroll
-                for (int k = 0; k < 16; ++k) s2 = add2(s2, pair(ds[2 * k], ds[2 * k + 1]));
-                float s0, s1;
-                unpair(s2, &s0, &s1);
-                const float sum = s0 + s1;
-                eps += sum;
-                if (!kSeveral && !(kMask && near)) {
-                  unpair(mass, &s0, &s1);
-                  if (low > 0) {
-                    far_r += sum;
-                    mass_r += s0 + s1;
-                  } else {
-                    far_l += sum;
-                    mass_l += s0 + s1;
-                  }
+            }
+            if (DQ && a.sum_bufs) {
+              float s0, s1;
+              unpair(sum2, &s0, &s1);
+              const float sum = s0 + s1;
+              eps += sum;
+              if (!kSeveral && !(kMask && near)) {
+                unpair(mass, &s0, &s1);
+                if (low > 0) {
+                  far_r += sum;
+                  mass_r += s0 + s1;
                 } else {
-                  // Sums down the diagonals of the 32 x 32 block: a running sum moves one
-                  // lane (row) on with every column; what lane 31 holds is complete.
-                  // Two runs of 16 columns side by side: what the first ends with belongs
-                  // to diagonals that the second goes on with.
-                  float run0 = 0.0f, run1 = 0.0f;
-#pragma unroll
-                  for (int k = 0; k < 16; ++k) {
-                    const float up0 = __shfl_up_sync(0xffffffffu, run0, 1);
-                    const float up1 = __shfl_up_sync(0xffffffffu, run1, 1);
-                    run0 = lane ? up0 + ds[k] : ds[k];
-                    run1 = lane ? up1 + ds[16 + k] : ds[16 + k];
-                    if (lane == 31) {
-                      bar.carry[warp][k] = run0;
-                      bar.carry[warp][16 + k] = run1;
-                    }
-                  }
-                  __syncwarp();
-                  const float lo = __shfl_up_sync(0xffffffffu, run0, 16);
-                  const float hi = __shfl_sync(0xffffffffu, run0, 46 - lane);
-                  // of the diagonal of the warp's first row and the block's first column
-                  float* to = by_d + warp * nbias + low + 31 + 32 * u + span.left + kBiasMargin;
-                  if (lane < 31) to[lane - 31] += bar.carry[warp][lane] + (lane >= 16 ? hi : 0.0f);
-                  __syncwarp();
-                  to[31 - lane] += run1 + (lane >= 16 ? lo : 0.0f);
-                  __syncwarp();
+                  far_l += sum;
+                  mass_l += s0 + s1;
                 }
+              } else {
+                // What the run over the first 16 columns ends with belongs to
+                // diagonals that the second run went on with.
+                __syncwarp();
+                const float lo = __shfl_up_sync(0xffffffffu, run[0], 16);
+                const float hi = __shfl_sync(0xffffffffu, run[0], 46 - lane);
+                // of the diagonal of the warp's first row and first column
+                float* to = by_d + warp * nbias + low + 31 + span.left + kBiasMargin;
+                if (lane < 31) to[lane - 31] += bar.carry[warp][lane] + (lane >= 16 ? hi : 0.0f);
+                __syncwarp();
+                to[31 - lane] += run[1] + (lane >= 16 ? lo : 0.0f);
+                __syncwarp();
               }
             }
           };
@@ -757,11 +745,11 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           else
             weigh(No(), No());
           tmem_wait_st();
-          if (DQ && keys < a.Lk && c0 + kTileRows > keys) {
+          if (DQ && keys < a.Lk && c0 + 32 > keys) {
             // Rows of K past the length have dS = 0, but may hold anything.
-            const int live = keys - c0;
-            for (int k = threadIdx.x & 127; k < (kTileRows - live) * 8 * (DP / 64); k += 128) {
-              const int r = live + (k >> 3) % (kTileRows - live), y = (k >> 3) / (kTileRows - live);
+            const int live = max(0, keys - c0);  // of the group's 32
+            for (int k = threadIdx.x & 127; k < (32 - live) * 8 * (DP / 64); k += 128) {
+              const int r = 32 * half + live + (k >> 3) % (32 - live), y = (k >> 3) / (32 - live);
               *reinterpret_cast<uint4*>(stage + y * (kTileRows * 128) + r * 128 + (k & 7) * 16) =
                   make_uint4(0, 0, 0, 0);
             }
@@ -769,7 +757,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.p_full[g]);
+          if (lane == 0) mbar_arrive(&bar.p_full[slot]);
         }
         if (a.biased) {
           __syncwarp();
@@ -790,43 +778,39 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       const Item done = it;
       have = take(k + 1, it);
       if (have) fetch(it);  // on its way meanwhile
-      ok = warp_wait(&bar.acc_full, k & 1, a.err);
+      const int ab = k % S::kAccBufs;
+      ok = warp_wait(&bar.acc_full[ab], (k / S::kAccBufs) & 1, a.err);
       if (!ok) break;
       tc_fence_after();
-      // ----- results: 32 columns at a time, the groups in turn ----------------------
-      constexpr int kChunks = (DQ ? 1 : 2) * DP / 32, kMine = (kChunks + G - 1) / G;
-      uint32_t r[kMine][32];
+      // ----- results: 16 columns at a time, the groups in turn ----------------------
+      constexpr int kMine = S::kAccCols / 16 / G;
+      const bool none = !DQ && x >= keys;
+      uint32_t o[kMine][8];
 #pragma unroll
-      for (int i = 0; i < kMine; ++i)
-        if (g + i * G < kChunks) tmem_ld32(r[i], tmem + lanes + S::kAcc + 32 * (g + i * G));
+      for (int i = 0; i < kMine; ++i) {
+        const int c = g + i * G;
+        uint32_t r[16];
+        tmem_ld16(r, tmem + lanes + S::kAcc + ab * S::kAccCols + 16 * c);
+        tmem_wait_ld(r);
+        const float mul = DQ || c >= DP / 16 ? a.scale * a.keep.scale : a.keep.scale;
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) tmem_wait_ld(r[i]);
+        for (int n = 0; n < 8; ++n)
+          o[i][n] = none ? 0u
+                         : pack2<T>(__uint_as_float(r[2 * n]) * mul,
+                                    __uint_as_float(r[2 * n + 1]) * mul);
+      }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.acc_free);
-      const bool none = !DQ && x >= keys;
+      if (lane == 0) mbar_arrive(&bar.acc_free[ab]);
       if (x < (DQ ? a.Lq : a.Lk)) {
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-          const int c = g + i * G;
-          if (c >= kChunks) break;
-          const bool second = DQ || c >= DP / 32;
-          const Heads& out = second ? a.out2 : a.out1;
-          const int col = 32 * (DQ ? c : c % (DP / 32));
-          const float mul = second ? a.scale * a.keep.scale : a.keep.scale;
+          const int c = g + i * G, col = 16 * (DQ ? c : c % (DP / 16));
+          const Heads& out = DQ || c >= DP / 16 ? a.out2 : a.out1;
           T* to = static_cast<T*>(out.data) + done.b * out.b + (int64_t)x * out.l + done.hx * out.h + col;
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            if (col + 8 * n >= a.D) break;
-            uint32_t o[4] = {0, 0, 0, 0};
-            if (!none) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                o[e] = pack2<T>(__uint_as_float(r[i][8 * n + 2 * e]) * mul,
-                                __uint_as_float(r[i][8 * n + 2 * e + 1]) * mul);
-            }
-            *reinterpret_cast<uint4*>(to + 8 * n) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
+          if (col < a.D) *reinterpret_cast<uint4*>(to) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
+          if (col + 8 < a.D)
+            *reinterpret_cast<uint4*>(to + 8) = make_uint4(o[i][4], o[i][5], o[i][6], o[i][7]);
         }
       }
     }
@@ -858,14 +842,14 @@ cudaError_t grad_of(const AttnArgs& a, GradArgs f, cudaStream_t s) {
   f.blocks = (Lx + kRows - 1) / kRows;
   f.items = f.blocks * a.B * Hx;
   f.next += DQ ? 0 : 1;
-  constexpr size_t most = 227 * 1024 - 256 - sizeof(GradBars<S::kGroups, S::kStages>);
+  constexpr size_t most = 227 * 1024 - 256 - sizeof(GradBars<S::kWarps, S::kStages>);
   size_t bytes = 1024 + S::kBias;
   if (a.biased) {
     const int n = bias_floats(a.rp);
     bytes += 2 * n * sizeof(float);
     if (DQ && f.partial) {
       // Two buffers, so that the sums of a piece are added up beside the next
-      // one; a wide bias (over some 300 distances a side) leaves room for one.
+      // one; a wide bias may leave room for one.
       const size_t one = S::sum_floats(n) * sizeof(float);
       f.sum_bufs = bytes + 2 * one <= most ? 2 : 1;
       bytes += f.sum_bufs * one;

@@ -54,7 +54,7 @@ struct FwdBars {
   uint64_t q_full, k_full[3], v_full[3], k_empty[3], v_empty[3], s_full[kGroups], p_full[kGroups];
   uint64_t drain;
   uint32_t tmem;
-  int first[OB_RELPOS_MAX_SIDE];
+  uint8_t bucket[kBiasMost];
 };
 
 template <typename T, int DP, int BN, bool DROP>
@@ -101,9 +101,10 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
   }
   if (warp == kCompute / 32) tmem_alloc(&bar.tmem, S::kAlloc);
   if (a.biased) {
-    for (int i = threadIdx.x; i < a.rp.side; i += kThreads) bar.first[i] = a.rp.first[i];
+    stage_buckets(bar.bucket, a.rp, threadIdx.x, kThreads);
     __syncthreads();
-    stage_bias(bias, a.rp, bar.first, static_cast<const T*>(a.table), a.H, h, threadIdx.x, kThreads);
+    stage_bias(bias, bar.bucket, bias_floats(a.rp), static_cast<const T*>(a.table), a.H, h,
+               threadIdx.x, kThreads);
   }
   tc_fence_before();
   __syncthreads();

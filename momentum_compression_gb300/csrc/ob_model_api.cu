@@ -116,9 +116,10 @@ ob_status check_attn(const ob_attn* a) {
     return failf(OB_ERR_INVALID, "p = %g must be in [0, 255/256]", a->p);
   if (a->relpos) {
     if (ob_status st = check_relpos(a->relpos)) return st;
-    if (a->relpos->max_distance > OB_ATTN_MAX_DISTANCE)
-      return failf(OB_ERR_UNSUPPORTED, "max_distance = %d: attention takes up to %d",
-                   a->relpos->max_distance, OB_ATTN_MAX_DISTANCE);
+    const int last = a->relpos->first[a->relpos->side - 1];
+    if (last * (a->relpos->two_sided ? 2 : 1) > OB_ATTN_MAX_SPAN)
+      return failf(OB_ERR_UNSUPPORTED, "a bias whose buckets span %d distances: attention takes %d",
+                   last * (a->relpos->two_sided ? 2 : 1), OB_ATTN_MAX_SPAN);
     OB_MODEL_PTR(a->table, 2, "table");
   } else if (a->table) {
     return failf(OB_ERR_INVALID, "table is given without relpos");

@@ -12,39 +12,10 @@
 
 namespace ob {
 
-// ---------------------------------------------------------------------------
-// Waits.  A waiting warp is suspended by the hardware for up to kSuspendNs at
-// a time, not left polling: the polls of a block's waiting warps would take
-// issue slots from those that work (half of all instructions, measured on the
-// backward kernels before).  Bounded like mbar_wait.  All lanes of the warp
-// wait and take the same decision.
-// ---------------------------------------------------------------------------
-
-constexpr uint32_t kSuspendNs = 20000;
-
-__device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
-      : "memory");
-  return done != 0;
-}
+// A whole warp waits (bounded, as mbar_wait) and takes one decision.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned* err,
                                           unsigned code = kErrWaitFull) {
-  bool ok = mbar_try_wait_for(bar, parity);
-  if (!__all_sync(0xffffffffu, ok)) {
-    const long long t0 = clock64();
-    while (!ok && !(ok = mbar_try_wait_for(bar, parity)) && clock64() - t0 <= kWaitCycles) {
-    }
-    if (!ok) atomicCAS(err, 0u, code);
-    ok = __all_sync(0xffffffffu, ok);
-    return ok;
-  }
-  return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, code));
 }
 
 // The start of dynamic shared memory, rounded up to 1024 bytes (which the

@@ -252,8 +252,8 @@ CASES = {
     "bias": dict(Lq=128, Lk=128, bias=T5),
     "bias_far": dict(H=1, Lq=600, Lk=700, bias=T5, q_offset=0),
     "bias_16": dict(H=3, Lq=257, Lk=257, bias=(16, 64, True), D=80, dtype=F16),
-    "bias_wide": dict(H=1, Lq=300, Lk=2100, bias=(64, 512, False), q_offset=1800),
-    "bias_wide_two": dict(H=1, Lq=900, Lk=1100, bias=(128, 512, True), q_offset=100),
+    "bias_wide": dict(H=1, Lq=300, Lk=2100, bias=(64, 520, False), q_offset=1800),
+    "bias_wide_two": dict(H=1, Lq=900, Lk=1100, bias=(128, 260, True), q_offset=100),
     "drop_almost_all": dict(Lq=40, Lk=600, p=255 / 256, dtype=F16),
     "causal": dict(Lq=300, Lk=300, causal=True, D=128),
     "causal_more_keys": dict(Lq=65, Lk=400, causal=True, p=0.2, bias=ONE),

@@ -106,7 +106,7 @@ def _attn(**over):
 def test_attention_refuses():
     L = ob.lib()
     rp = ob.ob_relpos_init(32, 128, True)
-    far = ob.ob_relpos_init(32, 4096, True)
+    far = ob.ob_relpos_init(32, 800, True)
     q = ob.ob_heads(0x1000, 4096, 256, 64)
     kv = ob.ob_heads(0x2000, 4096, 128, 64)
     o = ob.ob_heads(0x3000, 4096, 256, 64)
