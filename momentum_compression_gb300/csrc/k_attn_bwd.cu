@@ -119,8 +119,12 @@ __global__ void __launch_bounds__(16 * kRowsPerBlock) k_rows(const RowArgs a) {
 
 template <int DP, bool DQ>
 struct GradShape {
-  static constexpr int kGroups = 4, kSlots = 2;  // warpgroups, tiles in work
-  static constexpr int kStages = DP == 64 ? 4 : 3;
+  static constexpr int kGroups = 4;  // warpgroups, two a tile
+  // Tiles whose S and dP are in tensor memory: with a third, the scores of a
+  // pair's next tile are there when it is done with one (64 x 2048 backward 702
+  // -> XXX us).  At 128 there is no room for it, or for its stage.
+  static constexpr int kSlots = DP == 64 ? 3 : 2;
+  static constexpr int kStages = DP == 64 ? 5 : 3;
   static constexpr int kXBufs = DP == 64 ? 2 : 1;
   static constexpr int kWarps = 4 * kGroups;
   static constexpr int kThreads = 32 * (kWarps + 4);  // and the four warps of the other roles
@@ -148,7 +152,7 @@ struct Item {
 template <int W, int S>
 struct GradBars {
   uint64_t item_full[kItems], item_empty[kItems];
-  uint64_t x_full[2], x_empty[2], full[S], empty[S], s_full[2], p_full[2], acc_full[2], acc_free[2];
+  uint64_t x_full[2], x_empty[2], full[S], empty[S], s_full[3], p_full[3], acc_full[2], acc_free[2];
   uint64_t bias_full[2], bias_empty[2], sums_full[2], sums_empty[2], drain[2];
   Item item[kItems];
   uint32_t tmem;
@@ -228,10 +232,12 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       mbar_init(&bar.sums_full[i], S::kWarps);
       mbar_init(&bar.sums_empty[i], 1);
       mbar_init(&bar.drain[i], 1);
-      mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], S::kWarps / K);
       mbar_init(&bar.acc_full[i], 1);
       mbar_init(&bar.acc_free[i], S::kWarps);
+    }
+    for (int i = 0; i < K; ++i) {
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], S::kWarps / 2);
     }
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&bar.full[i], 1);
@@ -420,7 +426,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
         tc_fence_after();
         const uint64_t ud = u_rows + (uint32_t)st * (S::kStage >> 4);
         const uint32_t p = tmem + g * 128;
-        // The slot's warpgroups each left 32 rows of the sum over their own columns.
+        // The tile's warpgroups each left 32 rows of the sum over their own columns.
         if (!DQ) {
 #pragma unroll
           for (int s = 0; s < kTileRows / 16; ++s)
@@ -520,13 +526,12 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     }
   } else {
     // ----- arithmetic: a thread a row of X ----------------------------------
-    const int g = warp >> 2, slot = g >> 1, half = g & 1, row = (warp & 3) * 32 + lane;
+    const int g = warp >> 2, half = g & 1, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + slot * 128 + half * 32, tp = ts + 64;
     const uint64_t per_row = (uint32_t)((a.Lk + 7) / 8);
     const uint32_t T2 = a.keep.T * 0x10001u;
     bool ok = true;
-    int nt = 0, next = slot, nb = 0;  // tiles of earlier pieces, the slot's next tile, biases used
+    int nt = 0, next = g >> 1, nb = 0;  // tiles of earlier pieces, the pair's next tile, biases used
     float nlse = 0.0f, ndelta = 0.0f;  // of the row's query
     auto fetch = [&](const Item& of) {
       if (!DQ) return;  // Lqp covers every row of the block
@@ -567,8 +572,9 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           far_right = bias[nbias - 1];
         }
         const uint64_t rows0 = (uint64_t)(it.b * a.H + h0 + hh) * a.Lq;
-        for (; ok && next < nt + (hh + 1) * it.per; next += K) {
-          const int st = next % S::kStages;
+        for (; ok && next < nt + (hh + 1) * it.per; next += 2) {
+          const int st = next % S::kStages, slot = next % K;
+          const uint32_t ts = tmem + lanes + slot * 128 + half * 32, tp = ts + 64;
           // first of the group's 32 columns (keys or queries)
           const int c0 = (it.from + next - nt - hh * it.per) * kTileRows + 32 * half;
           uint8_t* stage = smem + S::kRing + st * S::kStage;
