@@ -202,7 +202,8 @@ def _ptr_array(xs):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle torch.cuda.current_stream() wraps, without making the wrapper
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -682,26 +683,27 @@ def ob_relpos_bias_bwd(relpos, dout, dtable, q_offset=0, workspace=None, stream=
                                     _stream(stream)))
 
 
-def _heads(t):
-    b, l, h, _ = t.stride()
-    return ob_heads(t.data_ptr(), b, l, h)
-
-
 def _attn(q, k, v, named, scale, causal, q_offset, relpos, table, kv_len, p, seed, offset):
-    """The ob_attn of a call; `named`: the arrays beside q, k, v and whether each is
-    shaped as the queries (True) or the keys."""
+    """The ob_attn of a call and the ob_heads of q, k, v and `named`, the arrays beside
+    them with their names and whether each is shaped as the queries (True) or the keys."""
     if q.dim() != 4 or k.dim() != 4:
         _refuse("q, k and v must be [batch, length, heads, D]")
-    B, Lq, H, D = q.shape
-    _, Lk, Hkv, _ = k.shape
+    qs, ks, dtype = q.shape, k.shape, q.dtype
+    B, Lq, H, D = qs
+    _, Lk, Hkv, _ = ks
+    if ks[0] != B or ks[3] != D:
+        _refuse(f"k: {tuple(ks)} does not go with q {tuple(qs)}")
+    heads = []
     for name, t, as_q in (("q", q, True), ("k", k, False), ("v", v, False)) + named:
-        if t.shape != (q.shape if as_q else (B, Lk, Hkv, D)) or t.dtype != q.dtype:
-            _refuse(f"{name}: {tuple(t.shape)} {t.dtype} does not go with q {tuple(q.shape)} "
-                    f"{q.dtype} and k {tuple(k.shape)}")
+        if t.shape != (qs if as_q else ks) or t.dtype != dtype:
+            _refuse(f"{name}: {tuple(t.shape)} {t.dtype} does not go with q {tuple(qs)} "
+                    f"{dtype} and k {tuple(ks)}")
         if not t.is_cuda:
             _refuse(f"{name} is not a CUDA tensor")
-        if t.stride(3) != 1 and D > 1:
+        b, l, h, d = t.stride()
+        if d != 1 and D > 1:
             _refuse(f"{name}: the last dimension must be contiguous")
+        heads.append(ob_heads(t.data_ptr(), b, l, h))
     if (relpos is None) != (table is None):
         _refuse("relpos and table go together")
     a = ob_attn(_type(q, "q"), B, H, Hkv, D, Lq, Lk, D ** -0.5 if scale is None else scale,
@@ -709,7 +711,7 @@ def _attn(q, k, v, named, scale, causal, q_offset, relpos, table, kv_len, p, see
                 offset)
     if table is not None:
         _check_table(table, relpos, H)
-        if table.dtype != q.dtype or not table.is_cuda:
+        if table.dtype != dtype or not table.is_cuda:
             _refuse("table must be a CUDA tensor of the type of q")
         a.relpos, a.table = ct.pointer(relpos), table.data_ptr()
     if kv_len is not None:
@@ -718,7 +720,7 @@ def _attn(q, k, v, named, scale, causal, q_offset, relpos, table, kv_len, p, see
                 or not kv_len.is_contiguous():
             _refuse("kv_len must be a contiguous int32 CUDA tensor of one length a batch entry")
         a.kv_len = kv_len.data_ptr()
-    return a
+    return a, heads
 
 
 def _check_lse(lse, q):
@@ -734,13 +736,11 @@ def ob_attn_fwd(q, k, v, o, lse=None, scale=None, causal=False, q_offset=None, r
     """o = dropout(softmax(scale q k^T + bias)) v for q, o [B, Lq, H, D] and k, v
     [B, Lk, Hkv, D]; lse [B, H, Lq] is what the backward pass needs.  scale: D ** -0.5
     by default; q_offset: Lk - Lq."""
-    a = _attn(q, k, v, (("o", o, True),), scale, causal, q_offset, relpos, table, kv_len, p, seed,
-              offset)
+    a, heads = _attn(q, k, v, (("o", o, True),), scale, causal, q_offset, relpos, table, kv_len, p,
+                     seed, offset)
     if lse is not None:
         _check_lse(lse, q)
-    _check(lib().ob_attn_fwd(ct.byref(a), ct.byref(_heads(q)), ct.byref(_heads(k)),
-                             ct.byref(_heads(v)), ct.byref(_heads(o)), _ptr(lse),
-                             _stream(stream)))
+    _check(lib().ob_attn_fwd(ct.byref(a), *map(ct.byref, heads), _ptr(lse), _stream(stream)))
 
 
 def ob_attn_bwd(grad_o, q, k, v, o, lse, dq, dk, dv, dtable=None, scale=None, causal=False,
@@ -748,9 +748,10 @@ def ob_attn_bwd(grad_o, q, k, v, o, lse, dq, dk, dv, dtable=None, scale=None, ca
                 workspace=None, stream=None):
     """dq, dk, dv and dtable from grad_o, with the forward call's arguments, o and
     lse.  workspace: a uint8 tensor, or None for one of torch's allocator."""
-    a = _attn(q, k, v, (("grad_o", grad_o, True), ("o", o, True), ("dq", dq, True),
-                        ("dk", dk, False), ("dv", dv, False)),
-              scale, causal, q_offset, relpos, table, kv_len, p, seed, offset)
+    a, (hq, hk, hv, *rest) = _attn(
+        q, k, v, (("grad_o", grad_o, True), ("o", o, True), ("dq", dq, True), ("dk", dk, False),
+                  ("dv", dv, False)),
+        scale, causal, q_offset, relpos, table, kv_len, p, seed, offset)
     _check_lse(lse, q)
     if dtable is not None:
         if relpos is None:
@@ -762,9 +763,9 @@ def ob_attn_bwd(grad_o, q, k, v, o, lse, dq, dk, dv, dtable=None, scale=None, ca
         b = ct.c_size_t()
         _check(lib().ob_attn_workspace_bytes(ct.byref(a), ct.byref(b)))
         workspace = _scratch(b.value, q, stream)
-    _check(lib().ob_attn_bwd(ct.byref(a), *(ct.byref(_heads(t)) for t in (grad_o, q, k, v, o)),
-                             lse.data_ptr(), *(ct.byref(_heads(t)) for t in (dq, dk, dv)),
-                             _ptr(dtable), _ptr(workspace) or None,
+    hg, ho, *grads = rest
+    _check(lib().ob_attn_bwd(ct.byref(a), *map(ct.byref, (hg, hq, hk, hv, ho)), lse.data_ptr(),
+                             *map(ct.byref, grads), _ptr(dtable), _ptr(workspace) or None,
                              workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
@@ -777,7 +778,7 @@ def ob_attn_device_error(stream=None):
 
 def ob_attn_workspace_bytes(q, k, relpos=None, table=None):
     """Bytes of scratch ob_attn_bwd needs for these shapes."""
-    a = _attn(q, k, k, (), None, False, 0, relpos, table, None, 0.0, 0, 0)
+    a, _ = _attn(q, k, k, (), None, False, 0, relpos, table, None, 0.0, 0, 0)
     b = ct.c_size_t()
     _check(lib().ob_attn_workspace_bytes(ct.byref(a), ct.byref(b)))
     return b.value

@@ -3,7 +3,7 @@
 // The bias depends on the distance d = j - i - q_offset alone, so a tile of R
 // rows and C columns holds R + C - 1 different values: the forward kernel
 // looks those up once into shared memory and then only writes (bound: HBM
-// writes).  The gradient adds along diagonals: a lane keeps the running sums
+// writes; 16 x 2048 x 2048 bf16 at XXX us).  The gradient adds along diagonals: a lane keeps the running sums
 // of its columns' diagonals in registers while it walks down the rows, and
 // hands the one that leaves its columns to the next lane, so an element
 // costs one load and one addition (bound: HBM reads).
@@ -20,6 +20,10 @@ constexpr int kBiasRows = 64;
 // Forward
 // ---------------------------------------------------------------------------
 
+// Distances between the outermost buckets up to which the buckets are looked
+// up in a map; a wider bias searches its edges for every distance.
+constexpr int kMapSpan = 2048;
+
 // Block (column chunk, row strip, head).  VEC: 8 columns a thread in 16-byte
 // stores (32 for fp32), one new value a row (the other seven move up); else
 // one column a thread and step, any alignment.
@@ -27,21 +31,32 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(kBiasThreads) k_relpos_bias(const __grid_constant__ RelposArgs a) {
   constexpr int kCols = 8 * kBiasThreads;
   __shared__ int first[OB_RELPOS_MAX_SIDE];
+  __shared__ T head[2 * OB_RELPOS_MAX_SIDE];
+  __shared__ uint8_t map[kMapSpan + 1];
   __shared__ T val[kBiasRows + kCols];
+  const int last = a.rp.first[a.rp.side - 1], left = last, right = a.rp.two_sided ? last : 0;
+  const bool mapped = left + right <= kMapSpan;
+  for (int b = threadIdx.x; b < a.rp.side; b += kBiasThreads) first[b] = a.rp.first[b];
+  __syncthreads();
+  if (mapped)
+    for (int t = threadIdx.x; t <= left + right; t += kBiasThreads)
+      map[t] = (uint8_t)bucket_of(first, a.rp.side, a.rp.two_sided, t - left);
   const int64_t c0 = (int64_t)blockIdx.x * kCols;
   const int ncols = (int)min((int64_t)kCols, a.Lk - c0);
   for (int64_t strip = blockIdx.y; strip * kBiasRows < a.Lq; strip += gridDim.y) {
     const int64_t i0 = strip * kBiasRows;
     const int nrows = (int)min((int64_t)kBiasRows, a.Lq - i0);
     for (int h = blockIdx.z; h < a.H; h += gridDim.z) {
-      __syncthreads();  // the previous tile's readers are done
-      for (int b = threadIdx.x; b < a.rp.side; b += kBiasThreads) first[b] = a.rp.first[b];
-      __syncthreads();
+      for (int b = threadIdx.x; b < a.rp.num_buckets; b += kBiasThreads)
+        head[b] = from_f32<T>(load_as_f32(a.table, (size_t)b * a.H + h, a.table_type));
+      __syncthreads();  // and the previous tile's readers are done with val
       // val[t]: distance dmin + t, dmin of the last row and the first column
       const int64_t dmin = c0 - (i0 + nrows - 1) - a.q_offset;
+#pragma unroll 4
       for (int t = threadIdx.x; t < nrows + ncols - 1; t += kBiasThreads) {
-        const int b = bucket_of(first, a.rp.side, a.rp.two_sided, dmin + t);
-        val[t] = from_f32<T>(load_as_f32(a.table, (size_t)b * a.H + h, a.table_type));
+        const int64_t d = dmin + t;
+        val[t] = head[mapped ? map[(int)max((int64_t)-left, min((int64_t)right, d)) + left]
+                             : bucket_of(first, a.rp.side, a.rp.two_sided, d)];
       }
       __syncthreads();
       T* out = static_cast<T*>(a.out) + (int64_t)h * a.stride_h + i0 * a.stride_l + c0;
@@ -139,43 +154,66 @@ __global__ void __launch_bounds__(32 * kGradWarps)
     float acc[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = 0.0f;
+    // kBatch rows at a time: their loads are all on the way before the first is
+    // added in.
+    constexpr int kBatch = V == 8 ? 4 : 8;
+    for (int r0 = 0; r0 < nrows; r0 += kBatch) {
+      float v[kBatch][V];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[i][k] = 0.0f;
+      const T* q = p + (int64_t)r0 * a.stride_l;
 #pragma unroll 2
-    for (int r = 0; r < nrows; ++r) {
-      if (r) {  // one row down a diagonal is one column to the right
-        const float left = __shfl_up_sync(0xffffffffu, acc[V - 1], 1);
-        if (lane == 31) by_d[warp][nrows - r + kWarpCols - 1] = acc[V - 1];
-#pragma unroll
-        for (int k = V - 1; k > 0; --k) acc[k] = acc[k - 1];
-        acc[0] = lane ? left : 0.0f;
-      }
-      const T* q = p + (int64_t)r * a.stride_l;
-      if (in) {
+      for (int n = 0; n < nn; ++n, q += a.stride_n) {
         if constexpr (V == 8) {
-#pragma unroll 4
-          for (int n = 0; n < nn; ++n, q += a.stride_n) {
-            uint4 w[sizeof(T) / 2];
+          uint4 w[kBatch][sizeof(T) / 2];
 #pragma unroll
-            for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
-              w[i] = __ldcs(reinterpret_cast<const uint4*>(q) + i);
+          for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int j = 0; j < (int)(sizeof(T) / 2); ++j)
+              w[i][j] = in && r0 + i < nrows
+                            ? __ldcs(reinterpret_cast<const uint4*>(q + i * a.stride_l) + j)
+                            : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
             if constexpr (sizeof(T) == 4) {
-              float v[8];
-              memcpy(v, w, 32);
+              float f[8];
+              memcpy(f, w[i], 32);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) acc[k] += v[k];
+              for (int k = 0; k < 8; ++k) v[i][k] += f[k];
             } else {
-              const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+              const uint32_t u[4] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w};
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const float2 f = unpack2<T>(u[k]);
-                acc[2 * k] += f.x;
-                acc[2 * k + 1] += f.y;
+                v[i][2 * k] += f.x;
+                v[i][2 * k + 1] += f.y;
               }
             }
           }
         } else {
-#pragma unroll 4
-          for (int n = 0; n < nn; ++n, q += a.stride_n) acc[0] += to_f32(*q);
+          float f[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            f[i] = in && r0 + i < nrows ? to_f32(q[i * a.stride_l]) : 0.0f;
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) v[i][0] += f[i];
         }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + i;
+        if (r >= nrows) break;
+        if (r) {  // one row down a diagonal is one column to the right
+          const float left = __shfl_up_sync(0xffffffffu, acc[V - 1], 1);
+          if (lane == 31) by_d[warp][nrows - r + kWarpCols - 1] = acc[V - 1];
+#pragma unroll
+          for (int k = V - 1; k > 0; --k) acc[k] = acc[k - 1];
+          acc[0] = lane ? left : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] += v[i][k];
       }
     }
     // the last row's diagonals, from column c0 on (those of columns past Lk hold
@@ -184,19 +222,29 @@ __global__ void __launch_bounds__(32 * kGradWarps)
     for (int k = 0; k < V; ++k) by_d[warp][lane * V + k] = acc[k];
   }
   __syncwarp();
-  // Diagonals to buckets: the distances of a bucket are a range.
-  const int64_t dmin = c0 - (i0 + nrows - 1) - a.q_offset;
-  for (int b = 0; b < a.rp.num_buckets; ++b) {
-    int64_t lo, hi;
-    bucket_range(first, a.rp.side, a.rp.two_sided, b, dmin, dmin + nrows + kWarpCols - 2, &lo,
-                 &hi);
-    float sum = 0.0f;
-    if (live && lo < hi) {
-      for (int t = (int)(lo - dmin) + lane; t < (int)(hi - dmin); t += 32) sum += by_d[warp][t];
+  // Diagonals to buckets: the distances of a bucket are a range.  All in one
+  // bucket (most tiles): the warp adds them up; else a lane a bucket.
+  const int64_t dmin = c0 - (i0 + nrows - 1) - a.q_offset, dmax = dmin + nrows + kWarpCols - 2;
+  const int b0 = bucket_of(first, a.rp.side, a.rp.two_sided, dmin);
+  const bool one = b0 == bucket_of(first, a.rp.side, a.rp.two_sided, dmax);
+  float all = 0.0f;
+  if (live && one) {
+#pragma unroll 4
+    for (int t = lane; t <= (int)(dmax - dmin); t += 32) all += by_d[warp][t];
 #pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  for (int b = lane; b < a.rp.num_buckets; b += 32) {
+    float sum = 0.0f;
+    if (live && one) {
+      if (b == b0) sum = all;
+    } else if (live) {
+      int64_t lo, hi;
+      bucket_range(first, a.rp.side, a.rp.two_sided, b, dmin, dmax, &lo, &hi);
+#pragma unroll 4
+      for (int t = (int)(lo - dmin); t < (int)(hi - dmin); ++t) sum += by_d[warp][t];
     }
-    if (lane == 0) by_b[warp][b] = sum;
+    by_b[warp][b] = sum;
   }
   __syncthreads();
   for (int b = threadIdx.x; b < a.rp.num_buckets; b += 32 * kGradWarps) {
