@@ -79,6 +79,7 @@ __device__ __forceinline__ int64_t row_at(int bh, int Lqp, int i) {
 
 template <typename T>
 __global__ void __launch_bounds__(16 * kRowsPerBlock) k_rows(const RowArgs a) {
+  grid_release();
   if (blockIdx.x == 0 && threadIdx.x < 2) a.next[threadIdx.x] = 0;
   const int l = threadIdx.x & 15;
   const int64_t at = (int64_t)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 4);
@@ -256,6 +257,8 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
+  grid_wait();
+  grid_release();
 
   // The k-th piece of work of this block, for one of the roles that follow it:
   // false after the last, or when the wait ran out.
@@ -873,8 +876,8 @@ cudaError_t grad_of(const AttnArgs& a, GradArgs f, cudaStream_t s) {
   e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  k_attn_grad<T, DP, DQ, DROP><<<f.items < sms ? f.items : sms, S::kThreads, bytes, s>>>(f);
-  return cudaGetLastError();
+  return launch_behind(k_attn_grad<T, DP, DQ, DROP>, dim3(f.items < sms ? f.items : sms),
+                       dim3(S::kThreads), bytes, s, f);
 }
 
 template <typename T, bool DQ>

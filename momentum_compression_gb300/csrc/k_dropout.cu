@@ -124,15 +124,24 @@ __global__ void __launch_bounds__(kDropThreads) k_dropout_any(const DropoutArgs 
   T* y = static_cast<T*>(a.y);
   float v[8], r[8];
   uint64_t yo[8];
+  // Row and column of the lane's first element; 32 columns on for each next.
+  const uint64_t first = e0 + lane;
+  uint64_t row = a.small ? __umul64hi(first, a.magic) : first / a.cols;
+  if (a.cols == 1) row = first;
+  uint64_t c = first - row * a.cols;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const uint64_t e = e0 + 32 * k + lane;
-    if (e >= a.n) break;
-    const uint64_t row = a.cols == 1 ? e : a.small ? __umul64hi(e, a.magic) : e / a.cols;
-    const uint64_t c = e - row * a.cols;
+    if (first + 32 * k >= a.n) break;
     v[k] = to_f32(x[row * a.ldx + c]);
     r[k] = RES ? to_f32(res[row * a.ldr + c]) : 0.0f;
     yo[k] = row * a.ldy + c;
+    c += 32;
+    if (a.cols >= 32) {
+      if (c >= a.cols) c -= a.cols, ++row;
+    } else {
+      row += c / (uint32_t)a.cols;
+      c %= (uint32_t)a.cols;
+    }
   }
   uint32_t byte = 0xffu;
   if (a.keep.T) byte = keep_byte(keep_words(a.keep, e0 / 8 + lane), a.keep.T);

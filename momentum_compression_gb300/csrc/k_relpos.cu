@@ -9,6 +9,7 @@
 // costs one load and one addition (bound: HBM reads).
 #include "elem.cuh"
 #include "model.cuh"
+#include "ob_internal.cuh"
 
 namespace ob {
 namespace {
@@ -119,15 +120,36 @@ constexpr int kGradRows = 32;  // rows of a block's strip
 // else 1.  A warp takes kGradRows rows of 32 V columns; a block's warps lie
 // side by side over warps_c column strips (a power of two, no more than the
 // columns fill) and one below the other in the rest, and add n_per entries.
+//
+// V = 8: the loads go through shared memory (each lane reads back what it
+// copied itself), kGradStages batches of four rows ahead, so that a warp
+// always has some 10 KB on the way; in registers there was room for one batch,
+// and its latency stood between every two (BERT-base, 201 MB: 61 us).
+// V = 1: a batch of eight rows in registers.
+template <int V>
+constexpr int kGradResident = V == 8 ? 2 : 5;  // blocks an SM
+constexpr int kGradBatch = 4;
+template <typename T>
+constexpr int kGradStages = sizeof(T) == 2 ? 6 : 3;
+
+__device__ __forceinline__ void copy16_async(void* dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src), "r"(valid ? 16 : 0)
+               : "memory");
+}
+
 template <typename T, int V>
-__global__ void __launch_bounds__(32 * kGradWarps)
+__global__ void __launch_bounds__(32 * kGradWarps, kGradResident<V>)
     k_relpos_grad(const __grid_constant__ RelposBwdArgs a) {
   constexpr int kWarpCols = 32 * V;
   constexpr int kDist = kGradRows + kWarpCols;  // distances of a warp's tile, and one spare
   __shared__ int first[OB_RELPOS_MAX_SIDE];
   __shared__ float by_d[kGradWarps][kDist];
   __shared__ float by_b[kGradWarps][2 * OB_RELPOS_MAX_SIDE];
+  extern __shared__ uint4 ring[];  // V = 8: [warp][stage][row][16-byte part][lane]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_release();
   for (int b = threadIdx.x; b < a.rp.side; b += 32 * kGradWarps) first[b] = a.rp.first[b];
   __syncthreads();
   int bl = blockIdx.x;
@@ -154,45 +176,87 @@ __global__ void __launch_bounds__(32 * kGradWarps)
     float acc[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = 0.0f;
-    // kBatch rows at a time: their loads are all on the way before the first is
-    // added in.
-    constexpr int kBatch = V == 8 ? 4 : 8;
-    for (int r0 = 0; r0 < nrows; r0 += kBatch) {
-      float v[kBatch][V];
+    // One row further: what each column's diagonal has so far moves one column to
+    // the right, and the row's values are added.
+    auto row = [&](int r, const float (&v)[V]) {
+      if (r) {
+        const float left = __shfl_up_sync(0xffffffffu, acc[V - 1], 1);
+        if (lane == 31) by_d[warp][nrows - r + kWarpCols - 1] = acc[V - 1];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
+        for (int k = V - 1; k > 0; --k) acc[k] = acc[k - 1];
+        acc[0] = lane ? left : 0.0f;
+      }
 #pragma unroll
-        for (int k = 0; k < V; ++k) v[i][k] = 0.0f;
-      const T* q = p + (int64_t)r0 * a.stride_l;
-#pragma unroll 2
-      for (int n = 0; n < nn; ++n, q += a.stride_n) {
-        if constexpr (V == 8) {
-          uint4 w[kBatch][sizeof(T) / 2];
+      for (int k = 0; k < V; ++k) acc[k] += v[k];
+    };
+    if constexpr (V == 8) {
+      constexpr int kParts = sizeof(T) / 2, kStages = kGradStages<T>;
+      uint4* mine = ring + warp * (kStages * kGradBatch * kParts * 32) + lane;
+      const int steps = (nrows + kGradBatch - 1) / kGradBatch * nn;  // a batch of one entry each
+      int fr = 0, fn = 0, fs = 0;  // row, entry and stage of the next copies
+      auto fetch = [&] {
+        if (fr < nrows) {
+          const T* q = p + (int64_t)fr * a.stride_l + (int64_t)fn * a.stride_n;
+          uint4* to = mine + fs * (kGradBatch * kParts * 32);
 #pragma unroll
-          for (int i = 0; i < kBatch; ++i)
+          for (int i = 0; i < kGradBatch; ++i)
 #pragma unroll
-            for (int j = 0; j < (int)(sizeof(T) / 2); ++j)
-              w[i][j] = in && r0 + i < nrows
-                            ? __ldcs(reinterpret_cast<const uint4*>(q + i * a.stride_l) + j)
-                            : make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < kParts; ++j) {
+              const bool valid = in && fr + i < nrows;
+              copy16_async(to + (i * kParts + j) * 32,
+                           valid ? reinterpret_cast<const uint4*>(q + i * a.stride_l) + j
+                                 : static_cast<const void*>(a.dout),
+                           valid);
+            }
+          if (++fn == nn) fn = 0, fr += kGradBatch;
+        }
+        if (++fs == kStages) fs = 0;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      for (int i = 0; i < kStages - 1; ++i) fetch();
+      float v[kGradBatch][8];
+      int r0 = 0, n = 0, st = 0;
+      for (int step = 0; step < steps; ++step) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        const uint4* from = mine + st * (kGradBatch * kParts * 32);
 #pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            if constexpr (sizeof(T) == 4) {
-              float f[8];
-              memcpy(f, w[i], 32);
+        for (int i = 0; i < kGradBatch; ++i) {
+          float f[8];
+          if constexpr (kParts == 2) {
+            const uint4 w[2] = {from[i * 64], from[i * 64 + 32]};
+            memcpy(f, w, 32);
+          } else {
+            const uint4 w = from[i * 32];
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-              for (int k = 0; k < 8; ++k) v[i][k] += f[k];
-            } else {
-              const uint32_t u[4] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float2 f = unpack2<T>(u[k]);
-                v[i][2 * k] += f.x;
-                v[i][2 * k + 1] += f.y;
-              }
+            for (int k = 0; k < 4; ++k) {
+              const float2 g = unpack2<T>(u[k]);
+              f[2 * k] = g.x;
+              f[2 * k + 1] = g.y;
             }
           }
-        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[i][k] = n ? v[i][k] + f[k] : f[k];
+        }
+        if (++st == kStages) st = 0;
+        fetch();
+        if (++n == nn) {
+#pragma unroll
+          for (int i = 0; i < kGradBatch; ++i)
+            if (r0 + i < nrows) row(r0 + i, v[i]);
+          n = 0;
+          r0 += kGradBatch;
+        }
+      }
+    } else {
+      constexpr int kBatch = 8;
+      for (int r0 = 0; r0 < nrows; r0 += kBatch) {
+        float v[kBatch][1];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) v[i][0] = 0.0f;
+        const T* q = p + (int64_t)r0 * a.stride_l;
+#pragma unroll 1
+        for (int n = 0; n < nn; ++n, q += a.stride_n) {
           float f[kBatch];
 #pragma unroll
           for (int i = 0; i < kBatch; ++i)
@@ -200,20 +264,9 @@ __global__ void __launch_bounds__(32 * kGradWarps)
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) v[i][0] += f[i];
         }
-      }
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = r0 + i;
-        if (r >= nrows) break;
-        if (r) {  // one row down a diagonal is one column to the right
-          const float left = __shfl_up_sync(0xffffffffu, acc[V - 1], 1);
-          if (lane == 31) by_d[warp][nrows - r + kWarpCols - 1] = acc[V - 1];
-#pragma unroll
-          for (int k = V - 1; k > 0; --k) acc[k] = acc[k - 1];
-          acc[0] = lane ? left : 0.0f;
-        }
-#pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] += v[i][k];
+        for (int i = 0; i < kBatch; ++i)
+          if (r0 + i < nrows) row(r0 + i, v[i]);
       }
     }
     // the last row's diagonals, from column c0 on (those of columns past Lk hold
@@ -260,6 +313,7 @@ __global__ void __launch_bounds__(32 * kGradWarps)
 __global__ void __launch_bounds__(1024)
     k_bucket_sums(const float* partial, int parts, int H, int nb, void* dtable, int type) {
   __shared__ float s[32][33];
+  grid_wait();
   const int h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int b0 = 0; b0 < nb; b0 += 32) {
     const int b = b0 + lane;
@@ -282,10 +336,19 @@ __global__ void __launch_bounds__(1024)
 template <typename T>
 cudaError_t launch_grad(const RelposBwdArgs& a, bool aligned, cudaStream_t s) {
   const dim3 grid((unsigned)(a.blocks_l * a.blocks_c * a.blocks_n), (unsigned)a.H);
-  if (aligned)
-    k_relpos_grad<T, 8><<<grid, 32 * kGradWarps, 0, s>>>(a);
-  else
+  if (aligned) {
+    constexpr int bytes =
+        kGradWarps * kGradStages<T> * kGradBatch * (int)(sizeof(T) / 2) * 32 * (int)sizeof(uint4);
+    static PerDeviceOnce once;
+    const cudaError_t e = once.run([] {
+      return cudaFuncSetAttribute(k_relpos_grad<T, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  bytes);
+    });
+    if (e != cudaSuccess) return e;
+    k_relpos_grad<T, 8><<<grid, 32 * kGradWarps, bytes, s>>>(a);
+  } else {
     k_relpos_grad<T, 1><<<grid, 32 * kGradWarps, 0, s>>>(a);
+  }
   return cudaGetLastError();
 }
 
@@ -304,10 +367,11 @@ void plan_relpos_bwd(RelposBwdArgs& a, bool aligned) {
   const int64_t rows = kGradRows * (kGradWarps / a.warps_c);
   a.blocks_l = (int)((a.Lq + rows - 1) / rows);
   a.blocks_c = (int)((strips + a.warps_c - 1) / a.warps_c);
-  // Entries are split over blocks until the card is covered four times (152
-  // SMs of eight resident blocks).
+  // Entries are split over as many blocks as are resident at once on 152 SMs:
+  // more would start a second wave that leaves most of the card idle.
   const int64_t tiles = (int64_t)a.blocks_l * a.blocks_c * a.H;
-  int64_t split = (4 * 152 + tiles - 1) / tiles;
+  const int64_t resident = 152 * (aligned ? kGradResident<8> : kGradResident<1>);
+  int64_t split = resident / tiles;
   if (split > a.N) split = a.N;
   if (split < 1) split = 1;
   a.n_per = (int)((a.N + split - 1) / split);
@@ -326,8 +390,8 @@ cudaError_t launch_relpos_bias_bwd(const RelposBwdArgs& a, int out_type, bool al
 
 cudaError_t launch_bucket_sums(const float* partial, int parts, int H, int num_buckets,
                                void* dtable, int type, cudaStream_t s) {
-  k_bucket_sums<<<(unsigned)H, 1024, 0, s>>>(partial, parts, H, num_buckets, dtable, type);
-  return cudaGetLastError();
+  return launch_behind(k_bucket_sums, dim3((unsigned)H), dim3(1024), 0, s, partial, parts, H,
+                       num_buckets, dtable, type);
 }
 
 }  // namespace ob

@@ -58,6 +58,30 @@ cudaError_t launch_bucket_sums(const float* partial, int parts, int H, int num_b
                                void* dtable, int type, cudaStream_t s);
 
 #ifdef __CUDACC__
+// Launches a kernel that may start while the one before it on the stream still
+// runs (its launch and prologue overlap that one's end): it calls grid_wait()
+// before it touches anything the others write or read, and the one before
+// calls grid_release() when the next may start.
+template <typename... P, typename... A>
+inline cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                                 cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------
 // Buckets.  `first` is ob_relpos.first of a side, staged in shared memory.
 // ---------------------------------------------------------------------------
