@@ -302,12 +302,18 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           it = Item{x0, b, hx, keys, from, per};
           break;
         }
-        for (int r = 0; r < kRows && x0 + r < (DQ ? a.Lq : a.Lk); ++r)
-          for (int o = DQ ? 1 : 0; o < 2; ++o) {
-            const Heads& out = o ? a.out2 : a.out1;
-            T* to = static_cast<T*>(out.data) + b * out.b + (int64_t)(x0 + r) * out.l + hx * out.h;
-            if (8 * lane < a.D) *reinterpret_cast<uint4*>(to + 8 * lane) = make_uint4(0, 0, 0, 0);
+        const int chunks = a.D / 8, rows = min(kRows, (DQ ? a.Lq : a.Lk) - x0);
+#pragma unroll 4
+        for (int t = lane; t < rows * chunks; t += 32) {
+          const int64_t r = x0 + t / chunks;
+          const int d = t % chunks * 8;
+          T* to = static_cast<T*>(a.out2.data) + b * a.out2.b + r * a.out2.l + hx * a.out2.h + d;
+          *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
+          if (!DQ) {
+            to = static_cast<T*>(a.out1.data) + b * a.out1.b + r * a.out1.l + hx * a.out1.h + d;
+            *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
           }
+        }
         if (DQ && a.sum_bufs) {
           float* to = a.partial + (((int64_t)hx * a.B + b) * a.blocks + x0 / kRows) * a.rp.num_buckets;
           for (int i = lane; i < a.rp.num_buckets; i += 32) to[i] = 0.0f;
