@@ -328,11 +328,10 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       ++k;
       return it;
     };
-    Item it = hand_out();
+    Item it = hand_out(), after{-1, 0, 0, 0, 0, 0};
     while (ok && it.x0 >= 0) {
-      const Item after = hand_out();  // known to all well before its turn
       const int xb = nx % S::kXBufs;
-      if (ok && nx >= S::kXBufs) ok = warp_wait(&bar.x_empty[xb], (nx / S::kXBufs + 1) & 1, a.err, kErrWaitEmpty);
+      if (nx >= S::kXBufs) ok = warp_wait(&bar.x_empty[xb], (nx / S::kXBufs + 1) & 1, a.err, kErrWaitEmpty);
       if (!ok) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(&bar.x_full[xb], 2 * S::kX);
@@ -361,6 +360,12 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
             if (!DQ)
               bulk_g2s(to + 2 * S::kTile, a.rows + row_at(it.b * a.H + hu, a.Lqp, r),
                        kTileRows * 8, &bar.full[st]);
+          }
+          // The next piece is found while the first tiles are on their way.
+          if (hh == 0 && t == min(it.per, 2) - 1) after = hand_out();
+          if (!ok) {
+            ++nt;
+            break;
           }
         }
       }
@@ -587,141 +592,125 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           // first of the group's 32 columns (keys or queries)
           const int c0 = (it.from + next - nt - hh * it.per) * kTileRows + 32 * half;
           uint8_t* stage = smem + S::kRing + st * S::kStage;
-          // The keep bits do not wait for the scores.
           uint32_t kept = ~0u;
-          uint4 words[4];
-          if (!DQ && DROP)
-            kept = keep_column(a.keep,
-                               (rows0 + (uint32_t)(c0 + (lane & 7))) * per_row + (uint32_t)(x >> 3),
-                               per_row, lane);
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {  // 16 columns at a time
+          const int col = c0 + 16 * c;
+          // The keep bits do not wait for the scores.
+          uint4 words[2];
           if (DQ && DROP)
-            keep_words_n(a.keep, (rows0 + (uint32_t)x) * per_row + (uint32_t)(c0 >> 3), 1, words);
-          ok = warp_wait(&bar.s_full[slot], (next / K) & 1, a.err);
-          if (!ok) break;
-          tc_fence_after();
-          // Distances of the warp's rows and the columns: [low, low + 62].
-          const int low = (DQ ? c0 - wx - 31 : wx - c0 - 31) - a.q_offset;
-          const bool near = a.biased && low + 62 > -span.left && low < span.right;
-          const float far = !a.biased ? 0.0f : low > 0 ? far_right : far_left;
-          const bool masked = DQ ? c0 + 32 > warp_limit : c0 < warp_limit;
+            keep_words_n(a.keep, (rows0 + (uint32_t)x) * per_row + (uint32_t)(col >> 3), 1, words);
+          if (c == 0) {
+            if (!DQ && DROP)
+              kept = keep_column(
+                  a.keep, (rows0 + (uint32_t)(c0 + (lane & 7))) * per_row + (uint32_t)(x >> 3),
+                  per_row, lane);
+            ok = warp_wait(&bar.s_full[slot], (next / K) & 1, a.err);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          uint32_t vs[16], vp[16];
+          tmem_ld16(vs, ts + 16 * c);
+          tmem_ld16(vp, tp + 16 * c);
+          // Distances of the warp's rows and the columns: [low, low + 46].
+          const int low = (DQ ? col - wx - 31 : wx - col - 15) - a.q_offset;
+          const bool near = a.biased && low + 46 > -span.left && low < span.right;
+          const float far = !a.biased ? 0.0f : low >= span.right ? far_right : far_left;
+          const bool masked = DQ ? col + 16 > warp_limit : col < warp_limit;
 
-          // Z and dS of the block.  Branch-free inside, for the scheduler's sake: a
+          // Z and dS of the columns.  Branch-free inside, for the scheduler's sake: a
           // body each for blocks of one bias value, blocks across several, and
-          // blocks with masked pairs (of either kind).
+          // blocks with masked pairs (of either kind).  No more is unrolled than
+          // this: the warps of a block are all at different places of the code,
+          // and more of it than the instruction caches hold costs more than it
+          // saves.
           auto weigh = [&](auto several_t, auto mask_t) {
             constexpr bool kSeveral = decltype(several_t)::value, kMask = decltype(mask_t)::value;
             // The bias of column n of the row: tb[n * step].
             const int step = (kSeveral || near) ? (DQ ? 1 : -1) : 0;
             const float* tb =
                 (kSeveral || near)
-                    ? bias + (DQ ? c0 - x : x - c0) - a.q_offset + span.left + kBiasMargin
-                    : bias + (low > 0 ? nbias - 1 : 0);
+                    ? bias + (DQ ? col - x : x - col) - a.q_offset + span.left + kBiasMargin
+                    : bias + (low >= span.right ? nbias - 1 : 0);
             const uint64_t scale2 = pair(a.scale2, a.scale2);
-            uint32_t rs[2][16], rp[2][16];
-            tmem_ld16(rs[0], ts);
-            tmem_ld16(rp[0], tp);
+            const ulonglong2* qlse =  // two pairs of queries each
+                reinterpret_cast<const ulonglong2*>(stage + 2 * S::kTile) + 8 * half + 4 * c;
+            const ulonglong2* qdelta = qlse + kTileRows / 4;
+            float p[16], z[16], ds[16];
             uint64_t mass = 0, sum2 = 0;  // sums of p and dS, two lanes of them
-            float run[2] = {0.0f, 0.0f};
+            tmem_wait_ld(vs);
+            tmem_wait_ld(vp);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {  // 16 columns; the next are on their way meanwhile
-              const uint32_t(&vs)[16] = rs[c];
-              const uint32_t(&vp)[16] = rp[c];
-              tmem_wait_ld(rs[c]);
-              tmem_wait_ld(rp[c]);
-              if (c == 0) {
-                tmem_ld16(rs[1], ts + 16);
-                tmem_ld16(rp[1], tp + 16);
-              }
-              const ulonglong2* qlse =  // two pairs of queries each
-                  reinterpret_cast<const ulonglong2*>(stage + 2 * S::kTile) + 8 * half + 4 * c;
-              const ulonglong2* qdelta = qlse + kTileRows / 4;
-              float p[16], z[16], ds[16];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                uint64_t shift;  // bias - lse
-                if (DQ && !kSeveral && !kMask) {
-                  shift = pair(far + nlse, far + nlse);
-                } else {
-                  uint64_t nl;
-                  if (DQ) {
-                    nl = pair(nlse, nlse);
-                  } else {
-                    const ulonglong2 four = qlse[k >> 1];
-                    nl = k & 1 ? four.y : four.x;
-                  }
-                  const int n = 16 * c + 2 * k;
-                  if (kSeveral)
-                    shift = add2(DQ ? pair(tb[n], tb[n + 1]) : pair(tb[-n], tb[-n - 1]), nl);
-                  else if (kMask && a.biased)
-                    shift = add2(pair(tb[n * step], tb[(n + 1) * step]), nl);
-                  else
-                    shift = add2(pair(far, far), nl);
-                }
-                unpair(fma2(pair(vs[2 * k], vs[2 * k + 1]), scale2, shift), &p[2 * k], &p[2 * k + 1]);
-              }
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                p[k] = exp2_approx(p[k]);
-                const int n = c0 + 16 * c + k;
-                if (kMask) p[k] = (DQ ? n < limit : n >= limit) ? p[k] : 0.0f;
-              }
-              if (DROP && DQ) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const uint4& w = words[2 * c + k];
-                  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    keep_pair(v[e], T2, p[8 * k + 2 * e], p[8 * k + 2 * e + 1], &z[8 * k + 2 * e],
-                              &z[8 * k + 2 * e + 1]);
-                }
+            for (int k = 0; k < 8; ++k) {
+              uint64_t shift;  // bias - lse
+              if (DQ && !kSeveral && !kMask) {
+                shift = pair(far + nlse, far + nlse);
               } else {
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                  z[k] = !DROP || (kept >> (16 * c + k) & 1) ? p[k] : 0.0f;
-              }
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                uint64_t nd;
+                uint64_t nl;
                 if (DQ) {
-                  nd = pair(ndelta, ndelta);
+                  nl = pair(nlse, nlse);
                 } else {
-                  const ulonglong2 four = qdelta[k >> 1];
-                  nd = k & 1 ? four.y : four.x;
+                  const ulonglong2 four = qlse[k >> 1];
+                  nl = k & 1 ? four.y : four.x;
                 }
-                const uint64_t pp = pair(p[2 * k], p[2 * k + 1]);
-                float &d0 = ds[2 * k], &d1 = ds[2 * k + 1];
-                unpair(fma2(pair(z[2 * k], z[2 * k + 1]), pair(vp[2 * k], vp[2 * k + 1]),
-                            mul2(pp, nd)),
-                       &d0, &d1);
-                if (DQ && !kSeveral) mass = add2(mass, pp);
-                if (kMask) {
-                  const int n = c0 + 16 * c + 2 * k;
-                  d0 = (DQ ? n < limit : n >= limit) ? d0 : 0.0f;
-                  d1 = (DQ ? n + 1 < limit : n + 1 >= limit) ? d1 : 0.0f;
-                }
-                if (DQ) sum2 = add2(sum2, pair(d0, d1));
+                if (kSeveral)
+                  shift = add2(DQ ? pair(tb[2 * k], tb[2 * k + 1]) : pair(tb[-2 * k], tb[-2 * k - 1]),
+                               nl);
+                else if (kMask && a.biased)
+                  shift = add2(pair(tb[2 * k * step], tb[(2 * k + 1) * step]), nl);
+                else
+                  shift = add2(pair(far, far), nl);
               }
-              uint32_t o[8];
-              if (!DQ) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
-                tmem_st8(ts + 8 * c, o);
-              }
-#pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] = pack2<T>(ds[2 * k], ds[2 * k + 1]);
-              tmem_st8(tp + 8 * c, o);
-              if (DQ && a.sum_bufs && (kSeveral || (kMask && near))) {
-                // Sums down the diagonals: a running sum moves one lane (row) on with
-                // every column; what lane 31 holds is complete.
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                  const float up = __shfl_up_sync(0xffffffffu, run[c], 1);
-                  run[c] = lane ? up + ds[k] : ds[k];
-                  if (lane == 31) bar.carry[warp][16 * c + k] = run[c];
-                }
-              }
+              unpair(fma2(pair(vs[2 * k], vs[2 * k + 1]), scale2, shift), &p[2 * k], &p[2 * k + 1]);
             }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              p[k] = exp2_approx(p[k]);
+              if (kMask) p[k] = (DQ ? col + k < limit : col + k >= limit) ? p[k] : 0.0f;
+            }
+            if (DROP && DQ) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t v[4] = {words[k].x, words[k].y, words[k].z, words[k].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  keep_pair(v[e], T2, p[8 * k + 2 * e], p[8 * k + 2 * e + 1], &z[8 * k + 2 * e],
+                            &z[8 * k + 2 * e + 1]);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) z[k] = !DROP || (kept >> k & 1) ? p[k] : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              uint64_t nd;
+              if (DQ) {
+                nd = pair(ndelta, ndelta);
+              } else {
+                const ulonglong2 four = qdelta[k >> 1];
+                nd = k & 1 ? four.y : four.x;
+              }
+              const uint64_t pp = pair(p[2 * k], p[2 * k + 1]);
+              float &d0 = ds[2 * k], &d1 = ds[2 * k + 1];
+              unpair(fma2(pair(z[2 * k], z[2 * k + 1]), pair(vp[2 * k], vp[2 * k + 1]), mul2(pp, nd)),
+                     &d0, &d1);
+              if (DQ && !kSeveral) mass = add2(mass, pp);
+              if (kMask) {
+                const int n = col + 2 * k;
+                d0 = (DQ ? n < limit : n >= limit) ? d0 : 0.0f;
+                d1 = (DQ ? n + 1 < limit : n + 1 >= limit) ? d1 : 0.0f;
+              }
+              if (DQ) sum2 = add2(sum2, pair(d0, d1));
+            }
+            uint32_t o[8];
+            if (!DQ) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
+              tmem_st8(ts + 8 * c, o);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = pack2<T>(ds[2 * k], ds[2 * k + 1]);
+            tmem_st8(tp + 8 * c, o);
             if (DQ && a.sum_bufs) {
               float s0, s1;
               unpair(sum2, &s0, &s1);
@@ -729,7 +718,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
               eps += sum;
               if (!kSeveral && !(kMask && near)) {
                 unpair(mass, &s0, &s1);
-                if (low > 0) {
+                if (low >= span.right) {
                   far_r += sum;
                   mass_r += s0 + s1;
                 } else {
@@ -737,16 +726,21 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
                   mass_l += s0 + s1;
                 }
               } else {
-                // What the run over the first 16 columns ends with belongs to
-                // diagonals that the second run went on with.
+                // Sums down the diagonals of the 32 x 16 block: a running sum moves one
+                // lane (row) on with every column; what lane 31 holds is complete.
+                float run = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  const float up = __shfl_up_sync(0xffffffffu, run, 1);
+                  run = lane ? up + ds[k] : ds[k];
+                  if (lane == 31) bar.carry[warp][k] = run;
+                }
                 __syncwarp();
-                const float lo = __shfl_up_sync(0xffffffffu, run[0], 16);
-                const float hi = __shfl_sync(0xffffffffu, run[0], 46 - lane);
                 // of the diagonal of the warp's first row and first column
                 float* to = by_d + warp * nbias + low + 31 + span.left + kBiasMargin;
-                if (lane < 31) to[lane - 31] += bar.carry[warp][lane] + (lane >= 16 ? hi : 0.0f);
+                if (lane < 15) to[lane - 31] += bar.carry[warp][lane];
                 __syncwarp();
-                to[31 - lane] += run[1] + (lane >= 16 ? lo : 0.0f);
+                to[15 - lane] += run;
                 __syncwarp();
               }
             }
@@ -759,6 +753,9 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
             weigh(Yes(), No());
           else
             weigh(No(), No());
+          kept >>= 16;
+          }
+          if (!ok) break;
           tmem_wait_st();
           if (DQ && keys < a.Lk && c0 + 32 > keys) {
             // Rows of K past the length have dS = 0, but may hold anything.
