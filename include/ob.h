@@ -690,10 +690,10 @@ ob_status ob_relpos_bias_bwd(const ob_relpos* rp, const void* dout, int out_type
 typedef struct {
   int type;               /* OB_TYPE_BF16 or OB_TYPE_F16: q, k, v, o, their gradients, table */
   int B, H, Hkv, D;       /* H a multiple of Hkv; D a multiple of 8, 8..128 */
-  int64_t Lq, Lk;         /* < 2^24; B, Lq or Lk may be 0 */
+  int64_t Lq, Lk;         /* < 2^23; B, Lq or Lk may be 0 */
   float scale;            /* > 0 */
   int causal;
-  int64_t q_offset;       /* position of query 0 among the keys, |q_offset| < 2^24 */
+  int64_t q_offset;       /* position of query 0 among the keys, |q_offset| < 2^23 */
   const ob_relpos* relpos; /* NULL: no bias; span <= OB_ATTN_MAX_SPAN */
   const void* table;      /* [num_buckets][H], contiguous */
   const int32_t* kv_len;  /* [B], on the device, or NULL */

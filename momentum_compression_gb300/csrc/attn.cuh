@@ -51,12 +51,12 @@ __device__ __forceinline__ int key_count(const int32_t* kv_len, int Lk, int b) {
 
 // ---------------------------------------------------------------------------
 // Bias.  Distances up to -left share one bucket and so do those from right on;
-// between them (and kBiasMargin past either end, so that a block of 32 x 32
+// between them (and kBiasMargin past either end, so that a block of 32 x 64
 // that touches the range is covered whole) the values of one head, times
 // log2(e), are staged in shared memory.
 // ---------------------------------------------------------------------------
 
-constexpr int kBiasMargin = 64;
+constexpr int kBiasMargin = 96;
 constexpr int kBiasMost = OB_ATTN_MAX_SPAN + 2 * kBiasMargin + 1;  // floats
 constexpr int kBiasMostBytes = 4 * kBiasMost;
 

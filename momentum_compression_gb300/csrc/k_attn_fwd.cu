@@ -1,12 +1,15 @@
 // Attention, forward.
 //
 // A block takes 256 queries of one head, 128 for each of two warpgroups (a
-// thread a query), and walks over the keys in tiles of BN.  One thread issues
+// thread a query), and walks over the keys in tiles of 64.  One warp issues
 // the products on the tensor cores and one the TMA copies:
-//   S = Q K^T        128 x BN in tensor memory, both operands in shared memory
+//   S = Q K^T        128 x 64 in tensor memory, both operands in shared memory
 //   P = softmax-to-be of S, dropped and rounded, over S in tensor memory
 //   O += P V         P from tensor memory, V as it lies (rows are the sum)
-// S of one warpgroup is worked on while the tensor cores run the other's.
+// With head sizes up to 64 two blocks share an SM, and one's products run
+// beside the other's arithmetic.  Above, one block fills the SM's tensor
+// memory, and a warpgroup's S has two buffers: the scores of the next tile are
+// there when it is done with one.
 // The softmax is on line: weights are taken relative to a reference m that a
 // row raises (with its sum and its O) only when a score passes it by more
 // than 2^8, so O is hardly ever touched outside the products.
@@ -26,6 +29,7 @@ constexpr int kRows = 128;      // queries of a warpgroup
 constexpr int kGroups = 2;      // warpgroups
 constexpr int kCompute = kGroups * 128;
 constexpr int kThreads = kCompute + 64;  // and a warp each for products and copies
+constexpr int BN = 64;          // keys of a tile
 constexpr float kRaise = 8.0f;
 
 struct FwdArgs {
@@ -40,39 +44,41 @@ struct FwdArgs {
   float* lse;
 };
 
-template <int DP, int BN>
+template <int DP>
 struct FwdShape {
-  static constexpr int kStages = DP == 64 ? 3 : 2;
+  static constexpr int kStages = DP == 64 ? 3 : 4;
+  static constexpr int kBufs = DP == 64 ? 1 : 2;  // buffers of a warpgroup's S
   static constexpr uint32_t kQ = kRows * DP * 2;  // bytes of one warpgroup's Q
   static constexpr uint32_t kTile = BN * DP * 2;
-  static constexpr uint32_t kCols = 2 * BN + 2 * DP;  // tensor memory: S, S, O, O
-  static constexpr uint32_t kAlloc = kCols <= 256 ? 256 : 512;
+  // tensor memory: the S, then the O
+  static constexpr uint32_t kO = kGroups * kBufs * BN, kAlloc = DP == 64 ? 256 : 512;
+  static_assert(kO + kGroups * DP <= kAlloc, "");
   static constexpr uint32_t kBias = kGroups * kQ + 2 * kStages * kTile;  // offset of the bias
 };
 
 struct FwdBars {
-  uint64_t q_full, k_full[3], v_full[3], k_empty[3], v_empty[3], s_full[kGroups], p_full[kGroups];
+  uint64_t q_full, k_full[4], v_full[4], k_empty[4], v_empty[4];
+  // By a tile's number modulo 2: with two buffers of S a warpgroup may be a tile
+  // ahead of its products, and one barrier's phases would pass each other.
+  uint64_t s_full[kGroups][2], p_full[kGroups][2], o_done[kGroups][2];
   uint64_t drain;
   uint32_t tmem;
   uint8_t bucket[kBiasMost];
 };
 
-template <typename T, int DP, int BN, bool DROP>
+template <typename T, int DP, bool DROP>
 __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
     k_attn_fwd(const __grid_constant__ FwdArgs a) {
-  using S = FwdShape<DP, BN>;
+  using S = FwdShape<DP>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  // Registers for the next columns' scores while these are worked on: with four
-  // warps a scheduler the other warps cover that latency.
-  constexpr bool kAhead = DP > 64;
   extern __shared__ uint8_t raw[];
   __shared__ FwdBars bar;
   uint8_t* smem = align_shared(raw);
   float* bias = reinterpret_cast<float*>(smem + S::kBias);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hkv);
-  // The last queries see the most keys: they start first.
-  const int q0 = ((int)gridDim.x - 1 - (int)blockIdx.x) * (kGroups * kRows);
+  const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hkv);
+  // The last queries see the most keys: they start first, those of all heads.
+  const int q0 = ((int)gridDim.y - 1 - (int)blockIdx.y) * (kGroups * kRows);
   const int keys = key_count(a.kv_len, a.Lk, b);
   int tiles[kGroups], most = 0;
 #pragma unroll
@@ -93,19 +99,16 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
       mbar_init(&bar.v_empty[i], 1);
     }
     for (int g = 0; g < kGroups; ++g) {
-      mbar_init(&bar.s_full[g], 1);
-      mbar_init(&bar.p_full[g], kRows);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bar.s_full[g][i], 1);
+        mbar_init(&bar.p_full[g][i], kRows / 32);
+        mbar_init(&bar.o_done[g][i], 1);
+      }
     }
     mbar_init(&bar.drain, 1);
     fence_barrier_init();
   }
   if (warp == kCompute / 32) tmem_alloc(&bar.tmem, S::kAlloc);
-  if (a.biased) {
-    stage_buckets(bar.bucket, a.rp, threadIdx.x, kThreads);
-    __syncthreads();
-    stage_bias(bias, bar.bucket, bias_floats(a.rp), static_cast<const T*>(a.table), a.H, h,
-               threadIdx.x, kThreads);
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -167,50 +170,56 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
                      v_desc = desc_mn(kv + S::kTile, BN * 128);
       const int ksteps = (a.D + 15) / 16;
       bool ok = warp_wait(&bar.q_full, 0, &g_attn_error);
-      auto scores = [&](int g, int st) {
+      int kst = 0, kpar = 0, kn = 0;  // stage, phase and number of the next tile of K
+      // S of tile kn for both groups; its buffer's P has been issued to O.
+      auto scores = [&](int g) {
         const uint64_t qd = q_desc + (uint32_t)g * (S::kQ >> 4);
-        const uint64_t kd = k_desc + (uint32_t)st * (2 * S::kTile >> 4);
+        const uint64_t kd = k_desc + (uint32_t)kst * (2 * S::kTile >> 4);
+        const uint32_t d = tmem + (g * S::kBufs + kn % S::kBufs) * BN;
 #pragma unroll
         for (int s = 0; s < DP / 16; ++s)
           if (s < ksteps)
-            mma_ss(leader, tmem + g * BN, qd + (((s >> 2) * (kRows * 128) + (s & 3) * 32) >> 4),
+            mma_ss(leader, d, qd + (((s >> 2) * (kRows * 128) + (s & 3) * 32) >> 4),
                    kd + (((s >> 2) * (BN * 128) + (s & 3) * 32) >> 4), kShapeS, s > 0);
+        mma_commit(leader, &bar.s_full[g][kn & 1]);
       };
-      ok = ok && warp_wait(&bar.k_full[0], 0, &g_attn_error);
-      if (ok) {
+      auto next_k = [&] {  // that tile of K is issued for both
+        // Only where a later copy waits for it: nothing may arrive after the block's end.
+        if (kn + S::kStages < most) mma_commit(leader, &bar.k_empty[kst]);
+        ++kn;
+        if (++kst == S::kStages) kst = 0, kpar ^= 1;
+      };
+      for (int i = 0; ok && i < S::kBufs && i < most; ++i) {
+        ok = warp_wait(&bar.k_full[kst], kpar, &g_attn_error);
+        if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int g = 0; g < kGroups; ++g)
-          if (tiles[g] > 0) {
-            scores(g, 0);
-            mma_commit(leader, &bar.s_full[g]);
-          }
-        if (S::kStages < most) mma_commit(leader, &bar.k_empty[0]);
+          if (kn < tiles[g]) scores(g);
+        next_k();
       }
-      int st = 0, par = 0;  // of tile n
+      int st = 0, par = 0;  // of tile n of V
       for (int n = 0; ok && n < most; ++n) {
-        const int next = st + 1 == S::kStages ? 0 : st + 1, next_par = next ? par : par ^ 1;
         ok = warp_wait(&bar.v_full[st], par, &g_attn_error);
-        if (ok && n + 1 < most) ok = warp_wait(&bar.k_full[next], next_par, &g_attn_error);
+        if (ok && kn < most) ok = warp_wait(&bar.k_full[kst], kpar, &g_attn_error);
         const uint64_t vd = v_desc + (uint32_t)st * (2 * S::kTile >> 4);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
           if (!ok || n >= tiles[g]) continue;
-          ok = warp_wait(&bar.p_full[g], n & 1, &g_attn_error);
+          ok = warp_wait(&bar.p_full[g][n & 1], (n >> 1) & 1, &g_attn_error);
           if (!ok) continue;
           tc_fence_after();
+          const uint32_t p = tmem + (g * S::kBufs + n % S::kBufs) * BN;
 #pragma unroll
           for (int s = 0; s < BN / 16; ++s)
-            mma_ts(leader, tmem + 2 * BN + g * DP, tmem + g * BN + s * 8, vd + s * (2048 >> 4),
-                   kShapeO, n > 0 || s > 0);
-          if (n + 1 < tiles[g]) scores(g, next);
-          mma_commit(leader, &bar.s_full[g]);
+            mma_ts(leader, tmem + S::kO + g * DP, p + s * 8, vd + s * (2048 >> 4), kShapeO,
+                   n > 0 || s > 0);
+          mma_commit(leader, &bar.o_done[g][n & 1]);
+          if (kn < tiles[g]) scores(g);
         }
-        // Only where a later copy waits for it: nothing may arrive after the block's end.
-        if (ok && n + 1 + S::kStages < most) mma_commit(leader, &bar.k_empty[next]);
         if (ok && n + S::kStages < most) mma_commit(leader, &bar.v_empty[st]);
-        st = next;
-        par = next_par;
+        if (ok && kn < most) next_k();
+        if (++st == S::kStages) st = 0, par ^= 1;
       }
       if (!ok) {
         mma_commit(leader, &bar.drain);
@@ -219,25 +228,33 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
     }
   } else {
     // ----- softmax: a thread a query -------------------------------------
+    if (a.biased) {  // while the first copies are on their way
+      stage_buckets(bar.bucket, a.rp, threadIdx.x, kCompute);
+      named_sync(1, kCompute);
+      stage_bias(bias, bar.bucket, bias_floats(a.rp), static_cast<const T*>(a.table), a.H, h,
+                 threadIdx.x, kCompute);
+      named_sync(1, kCompute);
+    }
     const int g = warp >> 2, mine = g ? tiles[1] : tiles[0];
     const int row = (warp & 3) * 32 + lane;
     const int i = q0 + g * kRows + row;
     const int wi = q0 + g * kRows + (warp & 3) * 32;  // the warp's first query
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + g * BN, to = tmem + lanes + 2 * BN + g * DP;
+    const uint32_t to = tmem + lanes + S::kO + g * DP;
     const int limit = a.causal ? min(keys, i + a.q_offset + 1) : keys;  // keys of this row
     const int warp_limit = a.causal ? min(keys, wi + a.q_offset + 1) : keys;  // of the first
     const uint32_t T2 = a.keep.T * 0x10001u;
     const uint64_t call0 = ((uint64_t)bh * a.Lq + i) * (uint32_t)((a.Lk + 7) / 8);
     const BiasSpan span = a.biased ? bias_span(a.rp) : BiasSpan{0, 0};
-    const float far_left = a.biased ? bias[0] : 0.0f;
-    const float far_right = a.biased ? bias[span.left + span.right + 2 * kBiasMargin] : 0.0f;
+    const int nbias = a.biased ? bias_floats(a.rp) : 0;
+    const float far_left = a.biased ? bias[0] : 0.0f, far_right = a.biased ? bias[nbias - 1] : 0.0f;
+    const uint64_t scale2 = pair(a.scale2, a.scale2);
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
 
-    const uint64_t scale2 = pair(a.scale2, a.scale2);
-
     for (int n = 0; n < mine; ++n) {
+      const uint32_t ts = tmem + lanes + (g * S::kBufs + n % S::kBufs) * BN;
+      const int j0 = n * BN;
       // The keep bits do not wait for the scores: as masks of the packed weights.
       uint32_t p[BN / 2];
       auto draw = [&] {
@@ -255,51 +272,76 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
         }
       };
       if (DROP) draw();
-      ok = warp_wait(&bar.s_full[g], n & 1, &g_attn_error);
+      ok = warp_wait(&bar.s_full[g][n & 1], (n >> 1) & 1, &g_attn_error);
       if (!ok) break;
       tc_fence_after();
-      float sum, top;
-      // The first tile is looked over for its maximum; the others are taken
-      // relative to m at once, and again in the rare case that m is passed.
-      bool weigh = n > 0;
+      // Distances of the warp's rows and the tile's columns: [low, low + 94].
+      const int low = j0 - wi - 31 - a.q_offset;
+      const bool near = a.biased && low + 94 > -span.left && low < span.right;
+      const float far = low >= span.right ? far_right : far_left;
+      const bool masked = j0 + BN > warp_limit;
+
+      // The largest score of the tile, times log2(e).
+      auto peak = [&] {
+        const int step = near ? 1 : 0;
+        const float* t = near ? bias + (j0 - i - a.q_offset) + span.left + kBiasMargin
+                              : bias + (low >= span.right ? nbias - 1 : 0);
+        float top = -INFINITY;
 #pragma unroll 1
-      for (int pass = 0;; ++pass) {
-        const float base = m == -INFINITY ? 0.0f : m;
-        uint64_t sum2 = 0;
-        top = -INFINITY;  // relative to base
-        uint32_t r[kAhead ? 2 : 1][16];
-        if (kAhead) tmem_ld16(r[0], ts);
-#pragma unroll
-        for (int c = 0; c < BN / 16; ++c) {  // 16 columns at a time
-          uint32_t(&v)[16] = r[kAhead ? c & 1 : 0];
-          if (!kAhead) tmem_ld16(v, ts + 16 * c);
+        for (int c = 0; c < BN; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(v, ts + c);
           tmem_wait_ld(v);
-          if (kAhead && c + 1 < BN / 16) tmem_ld16(r[~c & 1], ts + 16 * (c + 1));
-          const int j = n * BN + 16 * c;
-          float x[16];  // scores times log2(e), less base
-          const int d = j - wi - a.q_offset;  // distance of the warp's first row, first column
-          if (a.biased && d + 15 > -span.left && d - 31 < span.right) {
-            const float* t = bias + (j - i - a.q_offset) + span.left + kBiasMargin;
-            const uint64_t less = pair(-base, -base);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              unpair(fma2(pair(v[2 * k], v[2 * k + 1]), scale2,
-                          add2(pair(t[2 * k], t[2 * k + 1]), less)),
-                     &x[2 * k], &x[2 * k + 1]);
-          } else {
-            const float f = (a.biased ? d > 0 ? far_right : far_left : 0.0f) - base;
-            const uint64_t far = pair(f, f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              unpair(fma2(pair(v[2 * k], v[2 * k + 1]), scale2, far), &x[2 * k], &x[2 * k + 1]);
+          for (int k = 0; k < 16; ++k) {
+            const float s = __uint_as_float(v[k]);
+            float x = a.biased ? __fmaf_rn(s, a.scale2, t[(c + k) * step]) : s * a.scale2;
+            x = j0 + c + k < limit ? x : -INFINITY;
+            top = fmaxf(top, x);
           }
-          if (j + 16 > warp_limit) {
+        }
+        return top;
+      };
+      float sum, top;  // top: relative to base
+      // The weights relative to base, into p (dropped ones as zero), their sum and
+      // their largest score.  Branch-free inside, for the scheduler's sake: a body
+      // each for tiles of one bias value, tiles across several, and tiles with
+      // masked pairs (of either kind).
+      auto weigh = [&](auto several_t, auto mask_t, float base) {
+        constexpr bool kSeveral = decltype(several_t)::value, kMask = decltype(mask_t)::value;
+        const int step = kSeveral || near ? 1 : 0;
+        const float* t = kSeveral || near
+                             ? bias + (j0 - i - a.q_offset) + span.left + kBiasMargin
+                             : bias + (low >= span.right ? nbias - 1 : 0);
+        const uint64_t less = pair(-base, -base);
+        const float f = (a.biased ? far : 0.0f) - base;
+        uint64_t sum2 = 0;
+        top = -INFINITY;
+        uint32_t r[2][16];
+        tmem_ld16(r[0], ts);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = j + k < limit ? x[k] : -INFINITY;
+        for (int c = 0; c < BN / 16; ++c) {  // 16 columns; the next are on their way meanwhile
+          uint32_t(&v)[16] = r[c & 1];
+          tmem_wait_ld(v);
+          if (c + 1 < BN / 16) tmem_ld16(r[~c & 1], ts + 16 * (c + 1));
+          float x[16];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int n0 = 16 * c + 2 * k;
+            uint64_t shift;  // bias - base
+            if (kSeveral)
+              shift = add2(pair(t[n0], t[n0 + 1]), less);
+            else if (kMask && a.biased)
+              shift = add2(pair(t[n0 * step], t[(n0 + 1) * step]), less);
+            else
+              shift = pair(f, f);
+            unpair(fma2(pair(v[2 * k], v[2 * k + 1]), scale2, shift), &x[2 * k], &x[2 * k + 1]);
+            if (kMask) {
+              x[2 * k] = j0 + n0 < limit ? x[2 * k] : -INFINITY;
+              x[2 * k + 1] = j0 + n0 + 1 < limit ? x[2 * k + 1] : -INFINITY;
+            }
+            top = fmaxf(top, fmaxf(x[2 * k], x[2 * k + 1]));
           }
-#pragma unroll
-          for (int k = 0; k < 16; k += 2) top = fmaxf(top, fmaxf(x[k], x[k + 1]));
-          if (!weigh) continue;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             x[2 * k] = exp2_approx(x[2 * k]);
@@ -312,36 +354,55 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
         float s0, s1;
         unpair(sum2, &s0, &s1);
         sum = s0 + s1;
-        if (pass == 1 || (weigh && !__any_sync(0xffffffffu, top > kRaise))) break;
+      };
+      using Yes = std::true_type;
+      using No = std::false_type;
+      // The first tile is looked over for its maximum; the others are taken
+      // relative to m at once, and again in the rare case that m is passed.
+      if (n == 0) m = peak();
+#pragma unroll 1
+      for (int pass = 0;; ++pass) {
+        const float base = m == -INFINITY ? 0.0f : m;
+        if (masked)
+          weigh(No(), Yes(), base);
+        else if (near)
+          weigh(Yes(), No(), base);
+        else
+          weigh(No(), No(), base);
+        const bool over = m == -INFINITY ? top > -INFINITY : top > kRaise;
+        if (pass == 1 || !__any_sync(0xffffffffu, over)) break;
         const float up = fmaxf(m, base + top);
         const float less = m == -INFINITY ? 0.0f : exp2_approx(m - up);
         m = up;
         l *= less;
         if (n > 0) {
-#pragma unroll
-          for (int c = 0; c < DP / 16; ++c) {
+          ok = warp_wait(&bar.o_done[g][(n - 1) & 1], ((n - 1) >> 1) & 1, &g_attn_error);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < DP; c += 16) {
             uint32_t o[16];
-            tmem_ld16(o, to + 16 * c);
+            tmem_ld16(o, to + c);
             tmem_wait_ld(o);
 #pragma unroll
             for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * less);
-            tmem_st16(to + 16 * c, o);
+            tmem_st16(to + c, o);
           }
-          if (DROP) draw();
         }
-        weigh = true;
+        if (DROP) draw();
       }
+      if (!ok) break;
       l += sum;
 #pragma unroll
       for (int c = 0; c < BN / 32; ++c) tmem_st16(ts + 16 * c, p + 16 * c);
       tmem_wait_st();
-      if (keys < a.Lk && (n + 1) * BN > keys) {
+      if (keys < a.Lk && j0 + BN > keys) {
         // Rows of V past the length have weight zero, but may hold anything.
         const int st = n % S::kStages;
         ok = warp_wait(&bar.v_full[st], (n / S::kStages) & 1, &g_attn_error);
         if (!ok) break;
         uint8_t* vt = smem + kGroups * S::kQ + (2 * st + 1) * S::kTile;
-        const int from = keys - n * BN;  // > 0: the tile holds a key
+        const int from = keys - j0;  // > 0: the tile holds a key
         for (int t = threadIdx.x & 127; t < (BN - from) * 8 * (DP / 64); t += 128) {
           const int r = from + (t >> 3) % (BN - from), x = (t >> 3) / (BN - from);
           *reinterpret_cast<uint4*>(vt + x * (BN * 128) + r * 128 + (t & 7) * 16) =
@@ -350,10 +411,11 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
         fence_async_shared();
       }
       tc_fence_before();
-      mbar_arrive(&bar.p_full[g]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.p_full[g][n & 1]);
     }
     if (ok && mine > 0)
-      ok = warp_wait(&bar.s_full[g], mine & 1, &g_attn_error);
+      ok = warp_wait(&bar.o_done[g][(mine - 1) & 1], ((mine - 1) >> 1) & 1, &g_attn_error);
     tc_fence_after();
     // ----- o = O / l -------------------------------------------------------
     const float inv = l > 0.0f || l != l ? a.keep.scale / l : 0.0f;
@@ -392,9 +454,9 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
   }
 }
 
-template <typename T, int DP, int BN, bool DROP>
+template <typename T, int DP, bool DROP>
 cudaError_t fwd(const AttnArgs& a, cudaStream_t s) {
-  using S = FwdShape<DP, BN>;
+  using S = FwdShape<DP>;
   FwdArgs f{};
   cudaError_t e = attn_tensor_map(&f.q, a.q, a.type, a.D, a.Lq, a.H, a.B, kRows);
   // Without keys nothing is read through these; the map still needs an address.
@@ -424,12 +486,12 @@ cudaError_t fwd(const AttnArgs& a, cudaStream_t s) {
   const size_t bytes = 1024 + S::kBias + (a.biased ? bias_floats(a.rp) * sizeof(float) : 0);
   static PerDeviceOnce once;
   e = once.run([] {
-    return cudaFuncSetAttribute(k_attn_fwd<T, DP, BN, DROP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(k_attn_fwd<T, DP, DROP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 1024 + S::kBias + kBiasMostBytes);
   });
   if (e != cudaSuccess) return e;
-  const dim3 grid((a.Lq + kGroups * kRows - 1) / (kGroups * kRows), a.B * a.H);
-  k_attn_fwd<T, DP, BN, DROP><<<grid, kThreads, bytes, s>>>(f);
+  const dim3 grid(a.B * a.H, (a.Lq + kGroups * kRows - 1) / (kGroups * kRows));
+  k_attn_fwd<T, DP, DROP><<<grid, kThreads, bytes, s>>>(f);
   return cudaGetLastError();
 }
 
@@ -443,8 +505,8 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t s) {
   auto by_type = [&](auto zero) {
     using T = decltype(zero);
     if (a.D <= 64)
-      return a.keep.T ? fwd<T, 64, 64, true>(a, s) : fwd<T, 64, 64, false>(a, s);
-    return a.keep.T ? fwd<T, 128, 128, true>(a, s) : fwd<T, 128, 128, false>(a, s);
+      return a.keep.T ? fwd<T, 64, true>(a, s) : fwd<T, 64, false>(a, s);
+    return a.keep.T ? fwd<T, 128, true>(a, s) : fwd<T, 128, false>(a, s);
   };
   return a.type == OB_TYPE_BF16 ? by_type(__nv_bfloat16()) : by_type(__half());
 }

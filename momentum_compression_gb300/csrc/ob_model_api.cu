@@ -109,7 +109,7 @@ ob_status check_attn(const ob_attn* a) {
                  a->H, a->Hkv);
   if (a->D < 8 || a->D > 128 || a->D % 8)
     return failf(OB_ERR_UNSUPPORTED, "D = %d must be a multiple of 8 in [8, 128]", a->D);
-  if (ob_status st = check_lengths(a->Lq, a->Lk, a->q_offset, 1ll << 24)) return st;
+  if (ob_status st = check_lengths(a->Lq, a->Lk, a->q_offset, 1ll << 23)) return st;
   if (!(a->scale > 0.0f) || !std::isfinite(a->scale))
     return failf(OB_ERR_INVALID, "scale = %g must be positive", (double)a->scale);
   if (!(a->p >= 0.0 && a->p <= 255.0 / 256))

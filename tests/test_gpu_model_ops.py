@@ -270,6 +270,8 @@ CASES = {
     "odd": dict(B=3, H=3, Lq=333, Lk=517, p=0.1, bias=T5),
     "peaked": dict(Lq=200, Lk=200, spread=8.0, p=0.1),
     "scale": dict(Lq=100, Lk=100, scale=0.5, bias=T5),
+    "many_blocks": dict(B=8, H=16, Lq=700, Lk=700, D=128),
+    "many_blocks_causal": dict(B=8, H=16, Hkv=4, Lq=520, Lk=700, D=72, causal=True, p=0.1, bias=ONE),
     "long": dict(H=1, Lq=1111, Lk=1300, D=128, causal=True, p=0.1, bias=ONE),
     "long_64": dict(H=2, Lq=1025, Lk=1025, p=0.1, bias=T5),
 }
