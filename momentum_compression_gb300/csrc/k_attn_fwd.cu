@@ -71,6 +71,9 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
     k_attn_fwd(const __grid_constant__ FwdArgs a) {
   using S = FwdShape<DP>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  // The next columns' scores on their way while these are worked on, where the
+  // registers last for it.
+  constexpr bool kAhead = DP > 64 || !DROP;
   extern __shared__ uint8_t raw[];
   __shared__ FwdBars bar;
   uint8_t* smem = align_shared(raw);
@@ -317,13 +320,14 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
         const float f = (a.biased ? far : 0.0f) - base;
         uint64_t sum2 = 0;
         top = -INFINITY;
-        uint32_t r[2][16];
-        tmem_ld16(r[0], ts);
+        uint32_t r[kAhead ? 2 : 1][16];
+        if (kAhead) tmem_ld16(r[0], ts);
 #pragma unroll
-        for (int c = 0; c < BN / 16; ++c) {  // 16 columns; the next are on their way meanwhile
-          uint32_t(&v)[16] = r[c & 1];
+        for (int c = 0; c < BN / 16; ++c) {  // 16 columns
+          uint32_t(&v)[16] = r[kAhead ? c & 1 : 0];
+          if (!kAhead) tmem_ld16(v, ts + 16 * c);
           tmem_wait_ld(v);
-          if (c + 1 < BN / 16) tmem_ld16(r[~c & 1], ts + 16 * (c + 1));
+          if (kAhead && c + 1 < BN / 16) tmem_ld16(r[~c & 1], ts + 16 * (c + 1));
           float x[16];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
