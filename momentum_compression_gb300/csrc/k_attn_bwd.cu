@@ -155,7 +155,7 @@ struct GradBars {
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t x_full[2], x_empty[2], full[S], empty[S], s_full[3], p_full[3], acc_full[2], acc_free[2];
   uint64_t bias_full[2], bias_empty[2], sums_full[2], sums_empty[2], drain[2];
-  Item item[kItems];
+  Item item[kItems], done[W];  // done: the piece whose results a warp still has to take
   uint32_t tmem;
   int first[OB_RELPOS_MAX_SIDE];
   uint8_t bucket[kBiasMost];
@@ -179,7 +179,7 @@ __device__ __forceinline__ void keep_pair(uint32_t w, uint32_t T2, float p0, flo
 // query further every `step` calls) for the eight keys of its eight lanes,
 // and an 8 x 8 transposition of bits among those lanes turns query numbers
 // into bit numbers.  Bit r: query r.
-__device__ __forceinline__ uint32_t keep_column(const Keep& keep, uint64_t call0, uint64_t step,
+__device__ __forceinline__ uint32_t keep_column(const Keep& keep, uint64_t call0, uint32_t step,
                                                 int lane) {
   uint32_t x = 0, y = 0;  // queries 8 k + l % 8 for k = 0, 1 and for k = 2, 3
   uint4 w[4];
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     // ----- arithmetic: a thread a row of X ----------------------------------
     const int g = warp >> 2, half = g & 1, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint64_t per_row = (uint32_t)((a.Lk + 7) / 8);
+    const uint32_t per_row = (uint32_t)((a.Lk + 7) / 8);
     const uint32_t T2 = a.keep.T * 0x10001u;
     bool ok = true;
     int nt = 0, next = g >> 1, nb = 0;  // tiles of earlier pieces, the pair's next tile, biases used
@@ -553,10 +553,52 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       nlse = r[0];
       ndelta = r[kTileRows];
     };
+    // The results of piece kp, 16 columns at a time, the groups in turn.
+    auto finish = [&](int kp) {
+      const int ab = kp % S::kAccBufs;
+      ok = warp_wait(&bar.acc_full[ab], (kp / S::kAccBufs) & 1, a.err);
+      if (!ok) return;
+      tc_fence_after();
+      const Item done = bar.done[warp];
+      const int x = done.x0 + row;
+      const bool none = !DQ && x >= done.keys;
+      constexpr int kMine = S::kAccCols / 16 / G;
+      uint32_t o[kMine][8];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int c = g + i * G;
+        uint32_t r[16];
+        tmem_ld16(r, tmem + lanes + S::kAcc + ab * S::kAccCols + 16 * c);
+        tmem_wait_ld(r);
+        const float mul = DQ || c >= DP / 16 ? a.scale * a.keep.scale : a.keep.scale;
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+          o[i][n] = none ? 0u
+                         : pack2<T>(__uint_as_float(r[2 * n]) * mul,
+                                    __uint_as_float(r[2 * n + 1]) * mul);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.acc_free[ab]);
+      if (x < (DQ ? a.Lq : a.Lk)) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int c = g + i * G, col = 16 * (DQ ? c : c % (DP / 16));
+          const Heads& out = DQ || c >= DP / 16 ? a.out2 : a.out1;
+          T* to = static_cast<T*>(out.data) + done.b * out.b + (int64_t)x * out.l + done.hx * out.h + col;
+          if (col < a.D) *reinterpret_cast<uint4*>(to) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
+          if (col + 8 < a.D)
+            *reinterpret_cast<uint4*>(to + 8) = make_uint4(o[i][4], o[i][5], o[i][6], o[i][7]);
+        }
+      }
+    };
+    // A piece's results are taken after the first tile of the next: until then the
+    // other groups' last tiles and their products would be waited for.
     Item it;
-    bool have = take(0, it);
+    bool have = take(0, it), pending = false;
     if (have) fetch(it);
-    for (int k = 0; ok && have; ++k) {
+    for (int k = 0; ok && (have || pending); ++k) {
+      if (have) {
       const int x = it.x0 + row, wx = it.x0 + (warp & 3) * 32;  // the warp's first row
       const int h0 = DQ ? it.hx : it.hx * group, keys = it.keys;
       // The live columns of the row: DQ: below `limit`; else from `limit` on.
@@ -585,7 +627,10 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           far_left = bias[0];
           far_right = bias[nbias - 1];
         }
-        const uint64_t rows0 = (uint64_t)(it.b * a.H + h0 + hh) * a.Lq;
+        // Keep bits: the call of the row's first key, or of its key and query lane % 8.
+        const uint64_t call0 =
+            DQ ? ((uint64_t)(it.b * a.H + h0 + hh) * a.Lq + x) * per_row
+               : ((uint64_t)(it.b * a.H + h0 + hh) * a.Lq + (lane & 7)) * per_row + (x >> 3);
         for (; ok && next < nt + (hh + 1) * it.per; next += 2) {
           const int st = next % S::kStages, slot = next % K;
           const uint32_t ts = tmem + lanes + slot * 128 + half * 32, tp = ts + 64;
@@ -599,12 +644,10 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           // The keep bits do not wait for the scores.
           uint4 words[2];
           if (DQ && DROP)
-            keep_words_n(a.keep, (rows0 + (uint32_t)x) * per_row + (uint32_t)(col >> 3), 1, words);
+            keep_words_n(a.keep, call0 + (uint32_t)(col >> 3), 1, words);
           if (c == 0) {
             if (!DQ && DROP)
-              kept = keep_column(
-                  a.keep, (rows0 + (uint32_t)(c0 + (lane & 7))) * per_row + (uint32_t)(x >> 3),
-                  per_row, lane);
+              kept = keep_column(a.keep, call0 + (uint64_t)(uint32_t)c0 * per_row, per_row, lane);
             ok = warp_wait(&bar.s_full[slot], (next / K) & 1, a.err);
             if (!ok) break;
             tc_fence_after();
@@ -770,6 +813,10 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.p_full[slot]);
+          if (pending) {
+            pending = false;
+            finish(k - 1);
+          }
         }
         if (a.biased) {
           __syncwarp();
@@ -786,45 +833,15 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.sums_full[k % a.sum_bufs]);
       }
-      if (!ok) break;
-      const Item done = it;
+      }
+      if (ok && pending) finish(k - 1);
+      pending = have;
+      if (!ok || !have) break;
+      __syncwarp();
+      if (lane == 0) bar.done[warp] = it;
+      __syncwarp();
       have = take(k + 1, it);
       if (have) fetch(it);  // on its way meanwhile
-      const int ab = k % S::kAccBufs;
-      ok = warp_wait(&bar.acc_full[ab], (k / S::kAccBufs) & 1, a.err);
-      if (!ok) break;
-      tc_fence_after();
-      // ----- results: 16 columns at a time, the groups in turn ----------------------
-      constexpr int kMine = S::kAccCols / 16 / G;
-      const bool none = !DQ && x >= keys;
-      uint32_t o[kMine][8];
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int c = g + i * G;
-        uint32_t r[16];
-        tmem_ld16(r, tmem + lanes + S::kAcc + ab * S::kAccCols + 16 * c);
-        tmem_wait_ld(r);
-        const float mul = DQ || c >= DP / 16 ? a.scale * a.keep.scale : a.keep.scale;
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-          o[i][n] = none ? 0u
-                         : pack2<T>(__uint_as_float(r[2 * n]) * mul,
-                                    __uint_as_float(r[2 * n + 1]) * mul);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.acc_free[ab]);
-      if (x < (DQ ? a.Lq : a.Lk)) {
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const int c = g + i * G, col = 16 * (DQ ? c : c % (DP / 16));
-          const Heads& out = DQ || c >= DP / 16 ? a.out2 : a.out1;
-          T* to = static_cast<T*>(out.data) + done.b * out.b + (int64_t)x * out.l + done.hx * out.h + col;
-          if (col < a.D) *reinterpret_cast<uint4*>(to) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
-          if (col + 8 < a.D)
-            *reinterpret_cast<uint4*>(to + 8) = make_uint4(o[i][4], o[i][5], o[i][6], o[i][7]);
-        }
-      }
     }
   }
   __syncthreads();
