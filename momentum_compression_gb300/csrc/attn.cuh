@@ -83,7 +83,7 @@ __device__ __forceinline__ void stage_buckets(uint8_t* map, const ob_relpos& rp,
 template <typename T>
 __device__ __forceinline__ void stage_bias(float* tab, const uint8_t* map, int count,
                                            const T* table, int H, int h, int tid, int n) {
-#pragma unroll 4
+#pragma unroll 8
   for (int t = tid; t < count; t += n) tab[t] = to_f32(table[(size_t)map[t] * H + h]) * kLog2e;
 }
 

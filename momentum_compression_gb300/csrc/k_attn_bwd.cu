@@ -139,10 +139,14 @@ struct GradShape {
   static constexpr int kAccBufs = (512 - kAcc) / kAccCols >= 2 ? 2 : 1;
   // floats of one buffer of sums: by distance for each warp, and of each
   // group's rows eps, far left and right, mass left and right
-  __host__ __device__ static constexpr int sum_floats(int nbias) {
-    return kWarps * nbias + 5 * kGroups * kRows;
+  __host__ __device__ static constexpr int sum_floats(int ndist) {
+    return kWarps * ndist + 5 * kGroups * kRows;
   }
 };
+
+// Sums by distance cover this much past the outermost buckets' edges: all that
+// a block of 32 x 16 touches when it touches what lies between them.
+constexpr int kSumMargin = 48;
 
 constexpr int kItems = 8;  // pieces handed out at a time
 
@@ -216,9 +220,10 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const BiasSpan span = a.biased ? bias_span(a.rp) : BiasSpan{0, 0};
   const int nbias = a.biased ? bias_floats(a.rp) : 0;
+  const int ndist = nbias - 2 * (kBiasMargin - kSumMargin);
   const int group = a.H / a.Hkv, heads_x = DQ ? a.H : a.Hkv, heads = DQ ? 1 : group;
   float* biases = reinterpret_cast<float*>(smem + S::kBias);
-  float* sums = biases + 2 * nbias;  // sum_bufs buffers of S::sum_floats(nbias)
+  float* sums = biases + 2 * nbias;  // sum_bufs buffers of S::sum_floats(ndist)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kItems; ++i) {
@@ -250,7 +255,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
   if (a.biased) {
     for (int i = threadIdx.x; i < a.rp.side; i += S::kThreads) bar.first[i] = a.rp.first[i];
     stage_buckets(bar.bucket, a.rp, threadIdx.x, S::kThreads);
-    for (int i = threadIdx.x; i < a.sum_bufs * S::sum_floats(nbias); i += S::kThreads)
+    for (int i = threadIdx.x; i < a.sum_bufs * S::sum_floats(ndist); i += S::kThreads)
       sums[i] = 0.0f;
   }
   tc_fence_before();
@@ -483,8 +488,8 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           const int sb = done % a.sum_bufs;
           ok = warp_wait(&bar.sums_full[sb], (done / a.sum_bufs) & 1, a.err);
           if (!ok) break;
-          float* by_d = sums + sb * S::sum_floats(nbias);
-          float* row = by_d + S::kWarps * nbias;  // [5][G][kRows]
+          float* by_d = sums + sb * S::sum_floats(ndist);
+          float* row = by_d + S::kWarps * ndist;  // [5][G][kRows]
           // A row's dS sums to zero; what it sums to is the error of rowsum(do o),
           // taken from the rounded o.  It is taken out of the far buckets, whose
           // weight would multiply it, and out of the row's entry for dk.
@@ -497,7 +502,8 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
               for (int g = 0; g < G; ++g) v[i] += row[(i * G + g) * kRows + r];
             far_l += v[1] - v[0] * v[3];
             far_r += v[2] - v[0] * v[4];
-            a.rows[row_at(prev.b * a.H + prev.hx, a.Lqp, prev.x0 + r) + kTileRows] -= v[0];
+            // The only addition to this entry: its order is no question.
+            atomicAdd(&a.rows[row_at(prev.b * a.H + prev.hx, a.Lqp, prev.x0 + r) + kTileRows], -v[0]);
           }
 #pragma unroll
           for (int o = 16; o; o >>= 1) {
@@ -505,30 +511,34 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
             far_r += __shfl_xor_sync(0xffffffffu, far_r, o);
           }
           // The warps' sums of a distance into the first warp's, the others cleared.
-          for (int i = lane; i < nbias; i += 32) {
-            float sum = 0.0f;
+          for (int i = lane; i < ndist; i += 32) {
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int w = 0; w < S::kWarps; ++w) {
-              sum += by_d[w * nbias + i];
-              if (w) by_d[w * nbias + i] = 0.0f;
-            }
-            by_d[i] = sum;
+            for (int w = 0; w < S::kWarps; ++w) sum[w & 3] += by_d[w * ndist + i];
+#pragma unroll
+            for (int w = 1; w < S::kWarps; ++w) by_d[w * ndist + i] = 0.0f;
+            by_d[i] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
           }
           __syncwarp();
           float* to = a.partial + (((int64_t)prev.hx * a.B + prev.b) * a.blocks + prev.x0 / kRows) *
                                       a.rp.num_buckets;
           for (int n = lane; n < a.rp.num_buckets; n += 32) {
             int64_t lo, hi;
-            bucket_range(bar.first, a.rp.side, a.rp.two_sided, n, -(span.left + kBiasMargin),
-                         span.right + kBiasMargin, &lo, &hi);
-            float sum = n == a.rp.side - 1 ? far_l : 0.0f;
-            if (n == (a.rp.two_sided ? a.rp.num_buckets - 1 : 0)) sum += far_r;
-#pragma unroll 4
-            for (int i = (int)lo; i < (int)hi; ++i) sum += by_d[i + span.left + kBiasMargin];
-            to[n] = sum * a.keep.scale;
+            bucket_range(bar.first, a.rp.side, a.rp.two_sided, n, -(span.left + kSumMargin),
+                         span.right + kSumMargin, &lo, &hi);
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (n == a.rp.side - 1) sum[0] = far_l;
+            if (n == (a.rp.two_sided ? a.rp.num_buckets - 1 : 0)) sum[1] = far_r;
+            const float* from = by_d + span.left + kSumMargin;
+            int i = (int)lo;
+            for (; i + 4 <= (int)hi; i += 4)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) sum[j] += from[i + j];
+            for (; i < (int)hi; ++i) sum[2] += from[i];
+            to[n] = ((sum[0] + sum[1]) + (sum[2] + sum[3])) * a.keep.scale;
           }
           __syncwarp();
-          for (int i = lane; i < nbias; i += 32) by_d[i] = 0.0f;
+          for (int i = lane; i < ndist; i += 32) by_d[i] = 0.0f;
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.sums_empty[sb]);
           ++done;
@@ -616,7 +626,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
         const int sb = k % a.sum_bufs;
         if (k >= a.sum_bufs) ok = warp_wait(&bar.sums_empty[sb], (k / a.sum_bufs + 1) & 1, a.err, kErrWaitEmpty);
         if (!ok) break;
-        by_d = sums + sb * S::sum_floats(nbias);
+        by_d = sums + sb * S::sum_floats(ndist);
       }
       for (int hh = 0; ok && hh < heads; ++hh) {
         const float* bias = biases + (nb & 1) * nbias;
@@ -780,7 +790,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
                 }
                 __syncwarp();
                 // of the diagonal of the warp's first row and first column
-                float* to = by_d + warp * nbias + low + 31 + span.left + kBiasMargin;
+                float* to = by_d + warp * ndist + low + 31 + span.left + kSumMargin;
                 if (lane < 15) to[lane - 31] += bar.carry[warp][lane];
                 __syncwarp();
                 to[15 - lane] += run;
@@ -826,7 +836,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
         }
       nt += heads * it.per;
       if (DQ && a.sum_bufs && ok) {
-        float* r = by_d + S::kWarps * nbias + g * kRows + row;
+        float* r = by_d + S::kWarps * ndist + g * kRows + row;
         const float v[5] = {eps, far_l, far_r, mass_l, mass_r};
 #pragma unroll
         for (int i = 0; i < 5; ++i) r[i * G * kRows] = v[i];
@@ -879,12 +889,12 @@ cudaError_t grad_of(const AttnArgs& a, GradArgs f, cudaStream_t s) {
     if (DQ && f.partial) {
       // Two buffers, so that the sums of a piece are added up beside the next
       // one; a wide bias may leave room for one.
-      const size_t one = S::sum_floats(n) * sizeof(float);
+      const size_t one = S::sum_floats(n - 2 * (kBiasMargin - kSumMargin)) * sizeof(float);
       f.sum_bufs = bytes + 2 * one <= most ? 2 : 1;
       bytes += f.sum_bufs * one;
     }
   }
-  static_assert(1024 + S::kBias + 2 * kBiasMostBytes + (DQ ? S::kWarps * kBiasMostBytes + 5 * S::kGroups * kRows * 4 : 0) <= most,
+  static_assert(1024 + S::kBias + 2 * kBiasMostBytes + (DQ ? 4 * S::sum_floats(kBiasMost - 2 * (kBiasMargin - kSumMargin)) : 0) <= most,
                 "the widest bias must fit");
   static PerDeviceOnce once;
   e = once.run([] {
