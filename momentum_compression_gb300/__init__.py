@@ -582,6 +582,9 @@ def _scratch(nbytes, like, stream):
 def _rows(t, name):
     """(rows, cols, elements between rows) of a tensor whose last dimension is
     contiguous and whose leading dimensions are one run of rows."""
+    if t.dim() == 2 and t.stride(1) == 1:
+        rows, cols = t.shape
+        return rows, cols, t.stride(0) if rows > 1 else cols
     if t.dim() < 2:
         if t.dim() == 1 and t.shape[0] > 1 and t.stride(0) != 1:
             _refuse(f"{name}: the last dimension must be contiguous")
@@ -686,20 +689,17 @@ def ob_relpos_bias_bwd(relpos, dout, dtable, q_offset=0, workspace=None, stream=
 def _attn(q, k, v, named, scale, causal, q_offset, relpos, table, kv_len, p, seed, offset):
     """The ob_attn of a call and the ob_heads of q, k, v and `named`, the arrays beside
     them with their names and whether each is shaped as the queries (True) or the keys."""
-    if q.dim() != 4 or k.dim() != 4:
-        _refuse("q, k and v must be [batch, length, heads, D]")
     qs, ks, dtype = q.shape, k.shape, q.dtype
+    if len(qs) != 4 or len(ks) != 4 or ks[0] != qs[0] or ks[3] != qs[3]:
+        _refuse(f"q {tuple(qs)} and k {tuple(ks)} must be [batch, length, heads, D] of one batch "
+                "and D")
     B, Lq, H, D = qs
     _, Lk, Hkv, _ = ks
-    if ks[0] != B or ks[3] != D:
-        _refuse(f"k: {tuple(ks)} does not go with q {tuple(qs)}")
     heads = []
     for name, t, as_q in (("q", q, True), ("k", k, False), ("v", v, False)) + named:
-        if t.shape != (qs if as_q else ks) or t.dtype != dtype:
-            _refuse(f"{name}: {tuple(t.shape)} {t.dtype} does not go with q {tuple(qs)} "
-                    f"{dtype} and k {tuple(ks)}")
-        if not t.is_cuda:
-            _refuse(f"{name} is not a CUDA tensor")
+        if t.shape != (qs if as_q else ks) or t.dtype != dtype or not t.is_cuda:
+            _refuse(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device} does not go with q "
+                    f"{tuple(qs)} {dtype} and k {tuple(ks)} on a CUDA device")
         b, l, h, d = t.stride()
         if d != 1 and D > 1:
             _refuse(f"{name}: the last dimension must be contiguous")

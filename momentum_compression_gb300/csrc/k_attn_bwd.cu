@@ -52,7 +52,10 @@ struct GradArgs {
                    // then 64 times -rowsum(do o) / keep.scale
   int Lqp;
   Heads out1, out2;  // dq: out2 = dq; dkv: out1 = dv, out2 = dk
-  float* partial;    // [H][B * blocks][num_buckets]
+  float* partial;    // [H][sum_parts][num_buckets]: dq writes them, dkv adds them into dtable
+  int sum_parts;     // B * the blocks of dq
+  void* dtable;      // dkv: or null
+  float* join;       // dkv, split over the heads that share keys: [dv, dk][B][H][Lk][D], or null
   unsigned* next;    // the counter of this launch, 0 at its start
   unsigned* err;
 };
@@ -221,7 +224,10 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
   const BiasSpan span = a.biased ? bias_span(a.rp) : BiasSpan{0, 0};
   const int nbias = a.biased ? bias_floats(a.rp) : 0;
   const int ndist = nbias - 2 * (kBiasMargin - kSumMargin);
-  const int group = a.H / a.Hkv, heads_x = DQ ? a.H : a.Hkv, heads = DQ ? 1 : group;
+  // A piece's heads: its X, the first and the number of those on the other side.
+  const int group = a.H / a.Hkv;
+  const bool single = DQ || a.join;
+  const int heads_x = single ? a.H : a.Hkv, heads = single ? 1 : group;
   float* biases = reinterpret_cast<float*>(smem + S::kBias);
   float* sums = biases + 2 * nbias;  // sum_bufs buffers of S::sum_floats(ndist)
 
@@ -308,16 +314,24 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           break;
         }
         const int chunks = a.D / 8, rows = min(kRows, (DQ ? a.Lq : a.Lk) - x0);
+        const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll 4
         for (int t = lane; t < rows * chunks; t += 32) {
           const int64_t r = x0 + t / chunks;
           const int d = t % chunks * 8;
-          T* to = static_cast<T*>(a.out2.data) + b * a.out2.b + r * a.out2.l + hx * a.out2.h + d;
-          *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
-          if (!DQ) {
-            to = static_cast<T*>(a.out1.data) + b * a.out1.b + r * a.out1.l + hx * a.out1.h + d;
-            *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
+          if (!DQ && a.join) {
+            for (int o = 0; o < 2; ++o) {
+              uint4* to = reinterpret_cast<uint4*>(
+                  a.join + (((int64_t)(o * a.B + b) * a.H + hx) * a.Lk + r) * a.D + d);
+              to[0] = to[1] = zero;
+            }
+            continue;
           }
+          *reinterpret_cast<uint4*>(static_cast<T*>(a.out2.data) + b * a.out2.b + r * a.out2.l +
+                                    hx * a.out2.h + d) = zero;
+          if (!DQ)
+            *reinterpret_cast<uint4*>(static_cast<T*>(a.out1.data) + b * a.out1.b + r * a.out1.l +
+                                      hx * a.out1.h + d) = zero;
         }
         if (DQ && a.sum_bufs) {
           float* to = a.partial + (((int64_t)hx * a.B + b) * a.blocks + x0 / kRows) * a.rp.num_buckets;
@@ -342,13 +356,14 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
         mbar_arrive_expect_tx(&bar.x_full[xb], 2 * S::kX);
         for (int x = 0; x < DP / 64; ++x) {
           uint8_t* to = smem + xb * 2 * S::kX + x * (kRows * 128);
-          tma_load4(to, &a.x, 64 * x, it.x0, it.hx, it.b, &bar.x_full[xb]);
-          tma_load4(to + S::kX, &a.y, 64 * x, it.x0, it.hx, it.b, &bar.x_full[xb]);
+          const int h = !DQ && a.join ? it.hx / group : it.hx;
+          tma_load4(to, &a.x, 64 * x, it.x0, h, it.b, &bar.x_full[xb]);
+          tma_load4(to + S::kX, &a.y, 64 * x, it.x0, h, it.b, &bar.x_full[xb]);
         }
       }
       ++nx;
       for (int hh = 0; ok && hh < heads; ++hh) {
-        const int hu = DQ ? it.hx / group : it.hx * group + hh;
+        const int hu = DQ ? it.hx / group : a.join ? it.hx : it.hx * group + hh;
         for (int t = 0; t < it.per; ++t, ++nt) {
           const int st = nt % S::kStages;
           if (nt >= S::kStages) ok = warp_wait(&bar.empty[st], (nt / S::kStages + 1) & 1, a.err, kErrWaitEmpty);
@@ -479,7 +494,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
             if (nb >= 2) ok = warp_wait(&bar.bias_empty[nb & 1], (nb / 2 + 1) & 1, a.err, kErrWaitEmpty);
             if (!ok) break;
             stage_bias(biases + (nb & 1) * nbias, bar.bucket, nbias, static_cast<const T*>(a.table),
-                       a.H, DQ ? it.hx : it.hx * group + hh, lane, 32);
+                       a.H, single ? it.hx : it.hx * group + hh, lane, 32);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.bias_full[nb & 1]);
           }
@@ -547,6 +562,18 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
         prev = it;
         have = have && take(k, it);
       }
+      // The bias table's gradient from the sums that dq left: a lane a bucket, in
+      // order, beside the last piece's arithmetic.
+      if (!DQ && a.dtable)
+        for (int h = blockIdx.x; h < a.H; h += gridDim.x)
+          for (int n = lane; n < a.rp.num_buckets; n += 32) {
+            const float* from = a.partial + (int64_t)h * a.sum_parts * a.rp.num_buckets + n;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+            for (int i = 0; i < a.sum_parts; ++i) sum[i & 3] += from[(int64_t)i * a.rp.num_buckets];
+            static_cast<T*>(a.dtable)[(size_t)n * a.H + h] =
+                from_f32<T>((sum[0] + sum[1]) + (sum[2] + sum[3]));
+          }
     }
   } else {
     // ----- arithmetic: a thread a row of X ----------------------------------
@@ -573,14 +600,43 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       const int x = done.x0 + row;
       const bool none = !DQ && x >= done.keys;
       constexpr int kMine = S::kAccCols / 16 / G;
+      const uint32_t acc = tmem + lanes + S::kAcc + ab * S::kAccCols;
+      // Of chunk c: whether it is of the second output, and its first column.
+      auto second = [](int c) { return DQ || c >= DP / 16; };
+      auto column = [](int c) { return 16 * (DQ ? c : c % (DP / 16)); };
+      if (!DQ && a.join) {
+#pragma unroll 1
+        for (int i = 0; i < kMine; ++i) {
+          const int c = g + i * G;
+          uint32_t r[16];
+          tmem_ld16(r, acc + 16 * c);
+          tmem_wait_ld(r);
+          const float mul = none ? 0.0f : second(c) ? a.scale * a.keep.scale : a.keep.scale;
+          float* to = a.join +
+                      (((int64_t)(second(c) * a.B + done.b) * a.H + done.hx) * a.Lk + x) * a.D +
+                      column(c);
+#pragma unroll
+          for (int n = 0; n < 16; n += 4)
+            if (x < a.Lk && column(c) + n < a.D)
+              *reinterpret_cast<float4*>(to + n) =
+                  none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                       : make_float4(__uint_as_float(r[n]) * mul, __uint_as_float(r[n + 1]) * mul,
+                                     __uint_as_float(r[n + 2]) * mul,
+                                     __uint_as_float(r[n + 3]) * mul);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.acc_free[ab]);
+        return;
+      }
       uint32_t o[kMine][8];
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         const int c = g + i * G;
         uint32_t r[16];
-        tmem_ld16(r, tmem + lanes + S::kAcc + ab * S::kAccCols + 16 * c);
+        tmem_ld16(r, acc + 16 * c);
         tmem_wait_ld(r);
-        const float mul = DQ || c >= DP / 16 ? a.scale * a.keep.scale : a.keep.scale;
+        const float mul = second(c) ? a.scale * a.keep.scale : a.keep.scale;
 #pragma unroll
         for (int n = 0; n < 8; ++n)
           o[i][n] = none ? 0u
@@ -593,8 +649,8 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       if (x < (DQ ? a.Lq : a.Lk)) {
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-          const int c = g + i * G, col = 16 * (DQ ? c : c % (DP / 16));
-          const Heads& out = DQ || c >= DP / 16 ? a.out2 : a.out1;
+          const int c = g + i * G, col = column(c);
+          const Heads& out = second(c) ? a.out2 : a.out1;
           T* to = static_cast<T*>(out.data) + done.b * out.b + (int64_t)x * out.l + done.hx * out.h + col;
           if (col < a.D) *reinterpret_cast<uint4*>(to) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
           if (col + 8 < a.D)
@@ -610,7 +666,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     for (int k = 0; ok && (have || pending); ++k) {
       if (have) {
       const int x = it.x0 + row, wx = it.x0 + (warp & 3) * 32;  // the warp's first row
-      const int h0 = DQ ? it.hx : it.hx * group, keys = it.keys;
+      const int h0 = single ? it.hx : it.hx * group, keys = it.keys;
       // The live columns of the row: DQ: below `limit`; else from `limit` on.
       int limit, warp_limit;
       if (DQ) {
@@ -879,14 +935,14 @@ cudaError_t grad_of(const AttnArgs& a, GradArgs f, cudaStream_t s) {
   f.out1 = DQ ? a.dq : a.dv;
   f.out2 = DQ ? a.dq : a.dk;
   f.blocks = (Lx + kRows - 1) / kRows;
-  f.items = f.blocks * a.B * Hx;
+  f.items = f.blocks * a.B * (DQ || f.join ? a.H : Hx);
   f.next += DQ ? 0 : 1;
   constexpr size_t most = 227 * 1024 - 256 - sizeof(GradBars<S::kWarps, S::kStages>);
   size_t bytes = 1024 + S::kBias;
   if (a.biased) {
     const int n = bias_floats(a.rp);
     bytes += 2 * n * sizeof(float);
-    if (DQ && f.partial) {
+    if (DQ && f.dtable) {
       // Two buffers, so that the sums of a piece are added up beside the next
       // one; a wide bias may leave room for one.
       const size_t one = S::sum_floats(n - 2 * (kBiasMargin - kSumMargin)) * sizeof(float);
@@ -919,10 +975,66 @@ cudaError_t grad(const AttnArgs& a, const GradArgs& f, cudaStream_t s) {
 
 constexpr size_t kCounterBytes = 256;
 
-int padded(int Lq) { return (Lq + kRows - 1) / kRows * kRows; }
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+int blocks_of(int L) { return (L + kRows - 1) / kRows; }
 
 size_t rows_bytes(const AttnArgs& a) {
-  return ((size_t)a.B * a.H * padded(a.Lq) * 2 * sizeof(float) + 255) / 256 * 256;
+  return up256((size_t)a.B * a.H * blocks_of(a.Lq) * kRows * 2 * sizeof(float));
+}
+
+size_t partial_bytes(const AttnArgs& a) {
+  return a.biased ? up256((size_t)a.B * a.H * blocks_of(a.Lq) * a.rp.num_buckets * sizeof(float))
+                  : 0;
+}
+
+// Whether dk and dv are worked out for every query head on its own, in fp32,
+// and joined by a kernel after: where shared heads leave fewer pieces than the
+// card has SMs (152), each as long as its group is large (3 x 517 keys, 2 heads
+// shared by 8: backward 66 -> XXX us).
+bool splits(const AttnArgs& a) {
+  return a.H != a.Hkv && (int64_t)blocks_of(a.Lk) * a.B * a.Hkv < 152;
+}
+
+size_t join_bytes(const AttnArgs& a) {
+  return splits(a) ? 2 * sizeof(float) * (size_t)a.B * a.H * a.Lk * a.D : 0;
+}
+
+// dk and dv: the sums of their group's heads, in order.
+struct JoinArgs {
+  const float* join;
+  int B, H, Hkv, Lk, D;
+  Heads dv, dk;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) k_join(const JoinArgs a) {
+  grid_wait();
+  const int chunks = a.D / 8, group = a.H / a.Hkv;
+  int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int d = (int)(t % chunks) * 8;
+  t /= chunks;
+  const int j = (int)(t % a.Lk);
+  t /= a.Lk;
+  const int hk = (int)(t % a.Hkv);
+  t /= a.Hkv;
+  const int b = (int)(t % a.B), which = (int)(t / a.B);
+  if (which > 1) return;
+  float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int g = 0; g < group; ++g) {
+    const float4* p = reinterpret_cast<const float4*>(
+        a.join + (((int64_t)(which * a.B + b) * a.H + hk * group + g) * a.Lk + j) * a.D + d);
+    const float4 x = p[0], y = p[1];
+    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] += v[i];
+  }
+  const Heads& out = which ? a.dk : a.dv;
+  *reinterpret_cast<uint4*>(static_cast<T*>(out.data) + b * out.b + (int64_t)j * out.l +
+                            hk * out.h + d) =
+      make_uint4(pack2<T>(s[0], s[1]), pack2<T>(s[2], s[3]), pack2<T>(s[4], s[5]),
+                 pack2<T>(s[6], s[7]));
 }
 
 template <typename T>
@@ -945,40 +1057,36 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t s) {
   f.table = a.table;
   f.kv_len = a.kv_len;
   f.keep = a.keep;
-  f.next = static_cast<unsigned*>(a.workspace);
-  f.rows = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounterBytes);
-  f.Lqp = padded(a.Lq);
+  char* ws = static_cast<char*>(a.workspace);
+  f.next = reinterpret_cast<unsigned*>(ws);
+  f.rows = reinterpret_cast<float*>(ws + kCounterBytes);
+  f.partial = reinterpret_cast<float*>(ws + kCounterBytes + rows_bytes(a));
+  f.Lqp = blocks_of(a.Lq) * kRows;
+  f.sum_parts = a.B * blocks_of(a.Lq);
+  f.dtable = a.dtable;
   RowArgs r{a.B, a.H, a.D, a.Lq, f.Lqp, a.o, a.grad_o, a.lse, 1.0f / a.keep.scale, f.rows, f.next};
   const int64_t rows = (int64_t)a.B * a.H * f.Lqp;
   k_rows<T><<<(unsigned)(rows ? rows / kRowsPerBlock : 1), 16 * kRowsPerBlock, 0, s>>>(r);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  if (a.Lq) {
-    if (a.dtable) f.partial = f.rows + rows_bytes(a) / sizeof(float);
-    e = grad<T, true>(a, f, s);
-    if (e != cudaSuccess) return e;
-    if (a.dtable) {
-      e = launch_bucket_sums(f.partial, a.B * ((a.Lq + kRows - 1) / kRows), a.H, a.rp.num_buckets,
-                             a.dtable, a.type, s);
-      if (e != cudaSuccess) return e;
-      f.partial = nullptr;
-    }
-  }
-  if (a.Lk) e = grad<T, false>(a, f, s);
-  return e;
+  if (e == cudaSuccess && a.Lq) e = grad<T, true>(a, f, s);
+  if (e != cudaSuccess || !a.Lk) return e;
+  if (!a.Lq) f.dtable = nullptr;
+  if (splits(a)) f.join = reinterpret_cast<float*>(ws + kCounterBytes + rows_bytes(a) + partial_bytes(a));
+  e = grad<T, false>(a, f, s);
+  if (e != cudaSuccess || !f.join) return e;
+  const JoinArgs j{f.join, a.B, a.H, a.Hkv, a.Lk, a.D, a.dv, a.dk};
+  const int64_t threads = 2ll * a.B * a.Hkv * a.Lk * (a.D / 8);
+  return launch_behind(k_join<T>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, j);
 }
 
 }  // namespace
 
 size_t attn_workspace_bytes(const AttnArgs& a) {
-  size_t n = kCounterBytes + rows_bytes(a);
-  if (a.biased)
-    n += (size_t)a.B * a.H * ((a.Lq + kRows - 1) / kRows) * a.rp.num_buckets * sizeof(float);
-  return n;
+  return kCounterBytes + rows_bytes(a) + partial_bytes(a) + join_bytes(a);
 }
 
 cudaError_t launch_attn_bwd(const AttnArgs& a, cudaStream_t s) {
-  if (a.dtable && (a.B == 0 || a.Lq == 0)) {
+  if (a.dtable && (a.B == 0 || a.Lq == 0 || a.Lk == 0)) {
     const cudaError_t e = cudaMemsetAsync(a.dtable, 0, (size_t)a.rp.num_buckets * a.H * 2, s);
     if (e != cudaSuccess) return e;
   }
