@@ -39,7 +39,7 @@ constexpr int kTileRows = 64;
 constexpr int kRowsPerBlock = 16;  // of k_rows
 
 struct GradArgs {
-  CUtensorMap x, y, u, w;
+  CUtensorMap q, grad_o, k, v;  // boxes of 64 rows
   int B, H, Hkv, D, Lq, Lk, causal, q_offset, biased;
   int blocks, items;  // 128-row blocks of a head; blocks * batch * heads
   int sum_bufs;       // buffers of the bias table's sums, 0: none are wanted
@@ -354,12 +354,14 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       if (!ok) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(&bar.x_full[xb], 2 * S::kX);
-        for (int x = 0; x < DP / 64; ++x) {
-          uint8_t* to = smem + xb * 2 * S::kX + x * (kRows * 128);
-          const int h = !DQ && a.join ? it.hx / group : it.hx;
-          tma_load4(to, &a.x, 64 * x, it.x0, h, it.b, &bar.x_full[xb]);
-          tma_load4(to + S::kX, &a.y, 64 * x, it.x0, h, it.b, &bar.x_full[xb]);
-        }
+        const int h = !DQ && a.join ? it.hx / group : it.hx;
+        for (int x = 0; x < DP / 64; ++x)
+          for (int r = 0; r < kRows; r += kTileRows) {
+            uint8_t* to = smem + xb * 2 * S::kX + x * (kRows * 128) + r * 128;
+            tma_load4(to, DQ ? &a.q : &a.k, 64 * x, it.x0 + r, h, it.b, &bar.x_full[xb]);
+            tma_load4(to + S::kX, DQ ? &a.grad_o : &a.v, 64 * x, it.x0 + r, h, it.b,
+                      &bar.x_full[xb]);
+          }
       }
       ++nx;
       for (int hh = 0; ok && hh < heads; ++hh) {
@@ -373,8 +375,9 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           if (lane == 0) {
             mbar_arrive_expect_tx(&bar.full[st], 2 * S::kTile + (DQ ? 0 : kTileRows * 8));
             for (int x = 0; x < DP / 64; ++x) {
-              tma_load4(to + x * (kTileRows * 128), &a.u, 64 * x, r, hu, it.b, &bar.full[st]);
-              tma_load4(to + S::kTile + x * (kTileRows * 128), &a.w, 64 * x, r, hu, it.b,
+              tma_load4(to + x * (kTileRows * 128), DQ ? &a.k : &a.q, 64 * x, r, hu, it.b,
+                        &bar.full[st]);
+              tma_load4(to + S::kTile + x * (kTileRows * 128), DQ ? &a.v : &a.grad_o, 64 * x, r, hu, it.b,
                         &bar.full[st]);
             }
             if (!DQ)
@@ -920,22 +923,11 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
 template <typename T, int DP, bool DQ, bool DROP>
 cudaError_t grad_of(const AttnArgs& a, GradArgs f, cudaStream_t s) {
   using S = GradShape<DP, DQ>;
-  // An empty side is never read; its map still needs an address and an extent.
-  auto map = [&](CUtensorMap* m, const Heads& t, int L, int heads, int rows) {
-    return L ? attn_tensor_map(m, t, a.type, a.D, L, heads, a.B, rows)
-             : attn_tensor_map(m, DQ ? a.q : a.k, a.type, a.D, 1, 1, 1, rows);
-  };
-  const int Lx = DQ ? a.Lq : a.Lk, Lu = DQ ? a.Lk : a.Lq;
-  const int Hx = DQ ? a.H : a.Hkv, Hu = DQ ? a.Hkv : a.H;
-  cudaError_t e = map(&f.x, DQ ? a.q : a.k, Lx, Hx, kRows);
-  if (e == cudaSuccess) e = map(&f.y, DQ ? a.grad_o : a.v, Lx, Hx, kRows);
-  if (e == cudaSuccess) e = map(&f.u, DQ ? a.k : a.q, Lu, Hu, kTileRows);
-  if (e == cudaSuccess) e = map(&f.w, DQ ? a.v : a.grad_o, Lu, Hu, kTileRows);
-  if (e != cudaSuccess) return e;
+  const int Lx = DQ ? a.Lq : a.Lk, Hx = DQ ? a.H : a.Hkv;
   f.out1 = DQ ? a.dq : a.dv;
   f.out2 = DQ ? a.dq : a.dk;
   f.blocks = (Lx + kRows - 1) / kRows;
-  f.items = f.blocks * a.B * (DQ || f.join ? a.H : Hx);
+  f.items = f.blocks * a.B * (f.join ? a.H : Hx);
   f.next += DQ ? 0 : 1;
   constexpr size_t most = 227 * 1024 - 256 - sizeof(GradBars<S::kWarps, S::kStages>);
   size_t bytes = 1024 + S::kBias;
@@ -953,7 +945,7 @@ cudaError_t grad_of(const AttnArgs& a, GradArgs f, cudaStream_t s) {
   static_assert(1024 + S::kBias + 2 * kBiasMostBytes + (DQ ? 4 * S::sum_floats(kBiasMost - 2 * (kBiasMargin - kSumMargin)) : 0) <= most,
                 "the widest bias must fit");
   static PerDeviceOnce once;
-  e = once.run([] {
+  cudaError_t e = once.run([] {
     return cudaFuncSetAttribute(k_attn_grad<T, DP, DQ, DROP>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   });
@@ -1064,6 +1056,18 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t s) {
   f.Lqp = blocks_of(a.Lq) * kRows;
   f.sum_parts = a.B * blocks_of(a.Lq);
   f.dtable = a.dtable;
+  // An empty side is never read; its map still needs an address and an extent.
+  auto map = [&](CUtensorMap* m, const Heads& t, int L, int heads) {
+    return L ? attn_tensor_map(m, t, a.type, a.D, L, heads, a.B, kTileRows)
+             : attn_tensor_map(m, a.Lq ? a.q : a.k, a.type, a.D, 1, 1, 1, kTileRows);
+  };
+  if (a.Lq || a.Lk) {
+    e = map(&f.q, a.q, a.Lq, a.H);
+    if (e == cudaSuccess) e = map(&f.grad_o, a.grad_o, a.Lq, a.H);
+    if (e == cudaSuccess) e = map(&f.k, a.k, a.Lk, a.Hkv);
+    if (e == cudaSuccess) e = map(&f.v, a.v, a.Lk, a.Hkv);
+    if (e != cudaSuccess) return e;
+  }
   RowArgs r{a.B, a.H, a.D, a.Lq, f.Lqp, a.o, a.grad_o, a.lse, 1.0f / a.keep.scale, f.rows, f.next};
   const int64_t rows = (int64_t)a.B * a.H * f.Lqp;
   k_rows<T><<<(unsigned)(rows ? rows / kRowsPerBlock : 1), 16 * kRowsPerBlock, 0, s>>>(r);
