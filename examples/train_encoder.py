@@ -105,7 +105,8 @@ def train(steps=200, warmup=100, W=2, lr=1e-3, log=print):
         opt.warmup_step(grads) if t < warmup else opt.compressed_step(grads)
         losses.append(loss)
         if t % 20 == 0:
-            log(f"step {t:4d} {'warmup    ' if t < warmup else 'compressed'} loss {loss.item():.4f}")
+            phase = "warmup    " if t < warmup else "compressed"
+            log(f"step {t:4d} {phase} loss {loss.item():.4f}")
     torch.cuda.synchronize()
     opt.close()
     return [x.item() for x in losses]

@@ -546,11 +546,15 @@ def ob_adam_step_f16(ctx, send, hs, v_frozen, m, p, stream=None):
 # The model's side: dropout, relative position bias, attention
 # ---------------------------------------------------------------------------
 
-@functools.lru_cache(None)
+_type_codes = {}
+
+
 def _types():
-    import torch
-    return {torch.float32: OB_TYPE_F32, torch.bfloat16: OB_TYPE_BF16,
-            torch.float16: OB_TYPE_F16}
+    if not _type_codes:
+        import torch
+        _type_codes.update({torch.float32: OB_TYPE_F32, torch.bfloat16: OB_TYPE_BF16,
+                            torch.float16: OB_TYPE_F16})
+    return _type_codes
 
 
 def _refuse(what):
@@ -568,6 +572,14 @@ def _on_device(*named):
     for name, t in named:
         if t is not None and not t.is_cuda:
             _refuse(f"{name} is not a CUDA tensor")
+
+
+def _stream_of(t, stream):
+    """The stream's handle; for None, torch's current one on the tensor's device."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _stream(stream)
 
 
 def _scratch(nbytes, like, stream):
@@ -607,21 +619,30 @@ def _rows(t, name):
 def ob_dropout(x, y, p, seed, offset, residual=None, stream=None):
     """y = residual + dropout(x): the mask is drawn from (seed, offset) and
     never stored; with dy for x and no residual it is the backward pass."""
+    dtype, shape = x.dtype, x.shape
     type_ = _type(x, "x")
-    _on_device(("x", x), ("y", y), ("residual", residual))
-    if y.shape != x.shape or y.dtype != x.dtype:
+    if y.shape != shape or y.dtype != dtype:
         _refuse("y must have the shape and the type of x")
-    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
-        _refuse("residual must have the shape and the type of x")
-    if x.is_contiguous() and y.is_contiguous() and (residual is None or residual.is_contiguous()):
-        rows, ldr = 1, x.numel()
-        cols = ldx = ldy = ldr
+    if not (x.is_cuda and y.is_cuda):
+        _refuse("x and y must be CUDA tensors")
+    pr = None
+    whole = x.is_contiguous() and y.is_contiguous()
+    if residual is not None:
+        if residual.shape != shape or residual.dtype != dtype or not residual.is_cuda:
+            _refuse("residual must be a CUDA tensor of the shape and the type of x")
+        pr = residual.data_ptr()
+        whole = whole and residual.is_contiguous()
+    if whole:
+        rows, cols = 1, x.numel()
+        ldx = ldy = ldr = cols
     else:
         rows, cols, ldx = _rows(x, "x")
         ldy = _rows(y, "y")[2]
         ldr = cols if residual is None else _rows(residual, "residual")[2]
-    _check(lib().ob_dropout(x.data_ptr(), ldx, _ptr(residual), ldr, y.data_ptr(), ldy, rows, cols,
-                            type_, p, seed, offset, _stream(stream)))
+    status = lib().ob_dropout(x.data_ptr(), ldx, pr, ldr, y.data_ptr(), ldy, rows, cols, type_, p,
+                              seed, offset, _stream_of(x, stream))
+    if status:
+        _check(status)
 
 
 @functools.lru_cache(256)
@@ -654,7 +675,7 @@ def ob_relpos_bias(relpos, table, out, q_offset=0, stream=None):
     _last_contiguous(out, "out")
     _check(lib().ob_relpos_bias(ct.byref(relpos), table.data_ptr(), _type(table, "table"), H, Lq,
                                 Lk, q_offset, out.data_ptr(), _type(out, "out"), out.stride(0),
-                                out.stride(1), _stream(stream)))
+                                out.stride(1), _stream_of(out, stream)))
 
 
 def ob_relpos_workspace_bytes(relpos, N, H, Lq, Lk):
@@ -662,6 +683,12 @@ def ob_relpos_workspace_bytes(relpos, N, H, Lq, Lk):
     b = ct.c_size_t()
     _check(lib().ob_relpos_workspace_bytes(ct.byref(relpos), N, H, Lq, Lk, ct.byref(b)))
     return b.value
+
+
+@functools.lru_cache(1024)
+def _relpos_scratch(num_buckets, max_distance, two_sided, N, H, Lq, Lk):
+    return ob_relpos_workspace_bytes(ob_relpos_init(num_buckets, max_distance, two_sided), N, H,
+                                     Lq, Lk)
 
 
 def ob_relpos_bias_bwd(relpos, dout, dtable, q_offset=0, workspace=None, stream=None):
@@ -677,13 +704,14 @@ def ob_relpos_bias_bwd(relpos, dout, dtable, q_offset=0, workspace=None, stream=
     _check_table(dtable, relpos, H, "dtable")
     _last_contiguous(dout, "dout")
     if workspace is None:
-        workspace = _scratch(ob_relpos_workspace_bytes(relpos, N, H, Lq, Lk), dout, stream)
+        workspace = _scratch(_relpos_scratch(relpos.num_buckets, relpos.max_distance,
+                                             bool(relpos.two_sided), N, H, Lq, Lk), dout, stream)
     sn, sh, sl = dout.stride()[:3]
     _check(lib().ob_relpos_bias_bwd(ct.byref(relpos), dout.data_ptr(), _type(dout, "dout"), N, H,
                                     Lq, Lk, sn, sh, sl, q_offset, dtable.data_ptr(),
                                     _type(dtable, "dtable"), _ptr(workspace) or None,
                                     workspace.numel() * workspace.element_size(),
-                                    _stream(stream)))
+                                    _stream_of(dout, stream)))
 
 
 def _attn(q, k, v, named, scale, causal, q_offset, relpos, table, kv_len, p, seed, offset):
@@ -731,6 +759,18 @@ def _check_lse(lse, q):
         _refuse("lse must be a contiguous float32 CUDA tensor [batch, heads, queries]")
 
 
+@functools.lru_cache(1024)
+def _attn_scratch(type_, B, H, Hkv, D, Lq, Lk, buckets):
+    """ob_attn_workspace_bytes of the sizes it goes by."""
+    a = ob_attn(type_, B, H, Hkv, D, Lq, Lk, 1.0, 0, 0, None, None, None, 0.0, 0, 0)
+    if buckets is not None:
+        a.relpos = ct.pointer(ob_relpos_init(*buckets))
+        a.table = 2  # any: only the sizes count
+    b = ct.c_size_t()
+    _check(lib().ob_attn_workspace_bytes(ct.byref(a), ct.byref(b)))
+    return b.value
+
+
 def ob_attn_fwd(q, k, v, o, lse=None, scale=None, causal=False, q_offset=None, relpos=None,
                 table=None, kv_len=None, p=0.0, seed=0, offset=0, stream=None):
     """o = dropout(softmax(scale q k^T + bias)) v for q, o [B, Lq, H, D] and k, v
@@ -740,7 +780,8 @@ def ob_attn_fwd(q, k, v, o, lse=None, scale=None, causal=False, q_offset=None, r
                      seed, offset)
     if lse is not None:
         _check_lse(lse, q)
-    _check(lib().ob_attn_fwd(ct.byref(a), *map(ct.byref, heads), _ptr(lse), _stream(stream)))
+    _check(lib().ob_attn_fwd(ct.byref(a), *map(ct.byref, heads), _ptr(lse),
+                             _stream_of(q, stream)))
 
 
 def ob_attn_bwd(grad_o, q, k, v, o, lse, dq, dk, dv, dtable=None, scale=None, causal=False,
@@ -760,13 +801,15 @@ def ob_attn_bwd(grad_o, q, k, v, o, lse, dq, dk, dv, dtable=None, scale=None, ca
         if dtable.dtype != q.dtype or not dtable.is_cuda:
             _refuse("dtable must be a CUDA tensor of the type of q")
     if workspace is None:
-        b = ct.c_size_t()
-        _check(lib().ob_attn_workspace_bytes(ct.byref(a), ct.byref(b)))
-        workspace = _scratch(b.value, q, stream)
+        workspace = _scratch(_attn_scratch(a.type, a.B, a.H, a.Hkv, a.D, a.Lq, a.Lk,
+                                           None if relpos is None else
+                                           (relpos.num_buckets, relpos.max_distance,
+                                            bool(relpos.two_sided))), q, stream)
     hg, ho, *grads = rest
     _check(lib().ob_attn_bwd(ct.byref(a), *map(ct.byref, (hg, hq, hk, hv, ho)), lse.data_ptr(),
                              *map(ct.byref, grads), _ptr(dtable), _ptr(workspace) or None,
-                             workspace.numel() * workspace.element_size(), _stream(stream)))
+                             workspace.numel() * workspace.element_size(),
+                             _stream_of(q, stream)))
 
 
 def ob_attn_device_error(stream=None):

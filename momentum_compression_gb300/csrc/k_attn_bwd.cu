@@ -1,21 +1,28 @@
 // Attention, backward.
 //
-// Three kernels.  k_rows: lse and rowsum(do o) of every query.  k_attn_grad
-// twice: for 128 queries at a time over the keys (dq and the bias table's
-// sums), and for 128 keys at a time over the queries of the heads that share
-// them (dk, dv).  Both recompute S and dP on the tensor cores and need no
-// atomics: seven products instead of the five of a single pass, for results
-// that are the same bits on every run.
+//   P = exp(S scale + bias - lse), Z = P kept (0 or P), dP = do V^T
+//   delta = rowsum(do o) / keep scale,  dS = Z dP - P delta
+//   dv = keep scale Z^T do,  dq = scale keep scale dS K,  dk = ... dS^T Q
+//   dtable[n][h] = keep scale * the sum of dS over the pairs of bucket n
+//
+// Three kernels, and a fourth for shared heads.  k_rows: -lse and -delta of
+// every query.  k_attn_grad twice: for 128 queries at a time over the keys (dq
+// and the bias table's sums), and for 128 keys at a time over the queries of
+// the heads that share them (dk, dv).  Both recompute S and dP on the tensor
+// cores and need no atomics: seven products instead of the five of a single
+// pass, for results that are the same bits on every run.  k_join adds up heads
+// that share keys where they were worked out one by one.
 //
 // A block holds its 128 rows X, Y in shared memory (q, do or k, v) and walks
-// over tiles of 64 of the other side, U, W.  With a thread a row:
+// over tiles of 64 of the other side, U, W:
 //   S = X U^T, dP = Y W^T   128 x 64 each in tensor memory
 //   Z, dS                   from them in registers, rounded over S and dP
 //   acc1 += Z W (dv), acc2 += dS U (dq or dk)    first operand from tensor memory
-// Two tiles are in work at a time, each by two warpgroups (32 columns each), so
-// one's arithmetic runs beside the other's products: sixteen warps that work,
-// since a single one's dependent instructions leave three of four issue slots
-// empty.
+// Z and dS are rounded to the inputs' type, as the matrix unit wants them; all
+// that is summed, and the bias table's sums, are fp32.  Two tiles are in work at
+// a time, each by two warpgroups (a thread a row of 32 columns), so one's
+// arithmetic runs beside the other's products: sixteen warps that work, since a
+// single one's dependent instructions leave three of four issue slots empty.
 //
 // A block stays on its SM and takes one piece of work (128 rows of X) after
 // another from a counter, the products of the next begun before the last of
@@ -24,6 +31,12 @@
 // of the accumulators, and the copies (and clears the rows of pieces without
 // pairs), and one that stages the bias of the next head and adds up the bias
 // table's sums of the last.
+//
+// What bounds it is the issue of the arithmetic, not the matrix unit: without
+// bias and dropout 866 TFLOP/s (five products counted) at d 128 x 8192 in
+// 3.2 ms, 624 at d 64 x 2048 in 0.55 ms; with both, at 32 x 12 x 512 of
+// d 64, 0.31 ms full (the two passes' keep bits alone are 48 us of every
+// scheduler) and 0.27 ms over ragged lengths.
 #include <cmath>
 #include <type_traits>
 
@@ -125,8 +138,8 @@ template <int DP, bool DQ>
 struct GradShape {
   static constexpr int kGroups = 4;  // warpgroups, two a tile
   // Tiles whose S and dP are in tensor memory: with a third, the scores of a
-  // pair's next tile are there when it is done with one (64 x 2048 backward 702
-  // -> XXX us).  At 128 there is no room for it, or for its stage.
+  // pair's next tile are there when it is done with one (d 64 x 2048 backward
+  // 702 -> 565 us).  At 128 there is no room for it, or for its stage.
   static constexpr int kSlots = DP == 64 ? 3 : 2;
   static constexpr int kStages = DP == 64 ? 5 : 3;
   static constexpr int kXBufs = DP == 64 ? 2 : 1;
@@ -216,7 +229,8 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     k_attn_grad(const __grid_constant__ GradArgs a) {
   using S = GradShape<DP, DQ>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr int G = S::kGroups, K = S::kSlots, kScores = 4 * G, kProducts = kScores + 1, kCopies = kScores + 2;
+  constexpr int G = S::kGroups, K = S::kSlots;
+  constexpr int kScores = 4 * G, kProducts = kScores + 1, kCopies = kScores + 2;
   extern __shared__ uint8_t raw[];
   __shared__ GradBars<S::kWarps, S::kStages> bar;
   uint8_t* smem = align_shared(raw);
@@ -334,12 +348,14 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
                                       hx * a.out1.h + d) = zero;
         }
         if (DQ && a.sum_bufs) {
-          float* to = a.partial + (((int64_t)hx * a.B + b) * a.blocks + x0 / kRows) * a.rp.num_buckets;
+          float* to =
+              a.partial + (((int64_t)hx * a.B + b) * a.blocks + x0 / kRows) * a.rp.num_buckets;
           for (int i = lane; i < a.rp.num_buckets; i += 32) to[i] = 0.0f;
         }
       }
       const int slot = k % kItems;
-      if (k >= kItems) ok = warp_wait(&bar.item_empty[slot], (k / kItems + 1) & 1, a.err, kErrWaitEmpty);
+      if (k >= kItems)
+        ok = warp_wait(&bar.item_empty[slot], (k / kItems + 1) & 1, a.err, kErrWaitEmpty);
       if (ok && lane == 0) {
         bar.item[slot] = it;
         mbar_arrive(&bar.item_full[slot]);
@@ -350,7 +366,8 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     Item it = hand_out(), after{-1, 0, 0, 0, 0, 0};
     while (ok && it.x0 >= 0) {
       const int xb = nx % S::kXBufs;
-      if (nx >= S::kXBufs) ok = warp_wait(&bar.x_empty[xb], (nx / S::kXBufs + 1) & 1, a.err, kErrWaitEmpty);
+      if (nx >= S::kXBufs)
+        ok = warp_wait(&bar.x_empty[xb], (nx / S::kXBufs + 1) & 1, a.err, kErrWaitEmpty);
       if (!ok) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(&bar.x_full[xb], 2 * S::kX);
@@ -368,7 +385,8 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
         const int hu = DQ ? it.hx / group : a.join ? it.hx : it.hx * group + hh;
         for (int t = 0; t < it.per; ++t, ++nt) {
           const int st = nt % S::kStages;
-          if (nt >= S::kStages) ok = warp_wait(&bar.empty[st], (nt / S::kStages + 1) & 1, a.err, kErrWaitEmpty);
+          if (nt >= S::kStages)
+            ok = warp_wait(&bar.empty[st], (nt / S::kStages + 1) & 1, a.err, kErrWaitEmpty);
           if (!ok) break;
           uint8_t* to = smem + S::kRing + st * S::kStage;
           const int r = (it.from + t) * kTileRows;
@@ -377,8 +395,8 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
             for (int x = 0; x < DP / 64; ++x) {
               tma_load4(to + x * (kTileRows * 128), DQ ? &a.k : &a.q, 64 * x, r, hu, it.b,
                         &bar.full[st]);
-              tma_load4(to + S::kTile + x * (kTileRows * 128), DQ ? &a.v : &a.grad_o, 64 * x, r, hu, it.b,
-                        &bar.full[st]);
+              tma_load4(to + S::kTile + x * (kTileRows * 128), DQ ? &a.v : &a.grad_o, 64 * x, r,
+                        hu, it.b, &bar.full[st]);
             }
             if (!DQ)
               bulk_g2s(to + 2 * S::kTile, a.rows + row_at(it.b * a.H + hu, a.Lqp, r),
@@ -494,7 +512,8 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
         if (have) {
           ++k;
           for (int hh = 0; ok && hh < heads; ++hh, ++nb) {
-            if (nb >= 2) ok = warp_wait(&bar.bias_empty[nb & 1], (nb / 2 + 1) & 1, a.err, kErrWaitEmpty);
+            if (nb >= 2)
+              ok = warp_wait(&bar.bias_empty[nb & 1], (nb / 2 + 1) & 1, a.err, kErrWaitEmpty);
             if (!ok) break;
             stage_bias(biases + (nb & 1) * nbias, bar.bucket, nbias, static_cast<const T*>(a.table),
                        a.H, single ? it.hx : it.hx * group + hh, lane, 32);
@@ -521,7 +540,8 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
             far_l += v[1] - v[0] * v[3];
             far_r += v[2] - v[0] * v[4];
             // The only addition to this entry: its order is no question.
-            atomicAdd(&a.rows[row_at(prev.b * a.H + prev.hx, a.Lqp, prev.x0 + r) + kTileRows], -v[0]);
+            const int64_t at = row_at(prev.b * a.H + prev.hx, a.Lqp, prev.x0 + r);
+            atomicAdd(&a.rows[at + kTileRows], -v[0]);
           }
 #pragma unroll
           for (int o = 16; o; o >>= 1) {
@@ -585,7 +605,8 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     const uint32_t per_row = (uint32_t)((a.Lk + 7) / 8);
     const uint32_t T2 = a.keep.T * 0x10001u;
     bool ok = true;
-    int nt = 0, next = g >> 1, nb = 0;  // tiles of earlier pieces, the pair's next tile, biases used
+    // tiles of earlier pieces, the pair's next tile, biases used
+    int nt = 0, next = g >> 1, nb = 0;
     float nlse = 0.0f, ndelta = 0.0f;  // of the row's query
     auto fetch = [&](const Item& of) {
       if (!DQ) return;  // Lqp covers every row of the block
@@ -654,8 +675,10 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
         for (int i = 0; i < kMine; ++i) {
           const int c = g + i * G, col = column(c);
           const Heads& out = second(c) ? a.out2 : a.out1;
-          T* to = static_cast<T*>(out.data) + done.b * out.b + (int64_t)x * out.l + done.hx * out.h + col;
-          if (col < a.D) *reinterpret_cast<uint4*>(to) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
+          T* to = static_cast<T*>(out.data) + done.b * out.b + (int64_t)x * out.l +
+                  done.hx * out.h + col;
+          if (col < a.D)
+            *reinterpret_cast<uint4*>(to) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
           if (col + 8 < a.D)
             *reinterpret_cast<uint4*>(to + 8) = make_uint4(o[i][4], o[i][5], o[i][6], o[i][7]);
         }
@@ -668,240 +691,246 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     if (have) fetch(it);
     for (int k = 0; ok && (have || pending); ++k) {
       if (have) {
-      const int x = it.x0 + row, wx = it.x0 + (warp & 3) * 32;  // the warp's first row
-      const int h0 = single ? it.hx : it.hx * group, keys = it.keys;
-      // The live columns of the row: DQ: below `limit`; else from `limit` on.
-      int limit, warp_limit;
-      if (DQ) {
-        limit = a.causal ? min(keys, x + a.q_offset + 1) : keys;
-        warp_limit = a.causal ? min(keys, wx + a.q_offset + 1) : keys;
-      } else {
-        limit = x >= keys ? INT32_MAX : a.causal ? x - a.q_offset : INT32_MIN;
-        warp_limit = wx + 31 >= keys ? INT32_MAX : a.causal ? wx + 31 - a.q_offset : INT32_MIN;
-      }
-      float eps = 0.0f, far_l = 0.0f, far_r = 0.0f, mass_l = 0.0f, mass_r = 0.0f;
-      float* by_d = sums;
-      if (DQ && a.sum_bufs) {
-        const int sb = k % a.sum_bufs;
-        if (k >= a.sum_bufs) ok = warp_wait(&bar.sums_empty[sb], (k / a.sum_bufs + 1) & 1, a.err, kErrWaitEmpty);
-        if (!ok) break;
-        by_d = sums + sb * S::sum_floats(ndist);
-      }
-      for (int hh = 0; ok && hh < heads; ++hh) {
-        const float* bias = biases + (nb & 1) * nbias;
-        float far_left = 0.0f, far_right = 0.0f;
-        if (a.biased) {
-          ok = warp_wait(&bar.bias_full[nb & 1], (nb / 2) & 1, a.err);
-          if (!ok) break;
-          far_left = bias[0];
-          far_right = bias[nbias - 1];
+        const int x = it.x0 + row, wx = it.x0 + (warp & 3) * 32;  // the warp's first row
+        const int h0 = single ? it.hx : it.hx * group, keys = it.keys;
+        // The live columns of the row: DQ: below `limit`; else from `limit` on.
+        int limit, warp_limit;
+        if (DQ) {
+          limit = a.causal ? min(keys, x + a.q_offset + 1) : keys;
+          warp_limit = a.causal ? min(keys, wx + a.q_offset + 1) : keys;
+        } else {
+          limit = x >= keys ? INT32_MAX : a.causal ? x - a.q_offset : INT32_MIN;
+          warp_limit = wx + 31 >= keys ? INT32_MAX : a.causal ? wx + 31 - a.q_offset : INT32_MIN;
         }
-        // Keep bits: the call of the row's first key, or of its key and query lane % 8.
-        const uint64_t call0 =
-            DQ ? ((uint64_t)(it.b * a.H + h0 + hh) * a.Lq + x) * per_row
-               : ((uint64_t)(it.b * a.H + h0 + hh) * a.Lq + (lane & 7)) * per_row + (x >> 3);
-        for (; ok && next < nt + (hh + 1) * it.per; next += 2) {
-          const int st = next % S::kStages, slot = next % K;
-          const uint32_t ts = tmem + lanes + slot * 128 + half * 32, tp = ts + 64;
-          // first of the group's 32 columns (keys or queries)
-          const int c0 = (it.from + next - nt - hh * it.per) * kTileRows + 32 * half;
-          uint8_t* stage = smem + S::kRing + st * S::kStage;
-          uint32_t kept = ~0u;
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {  // 16 columns at a time
-          const int col = c0 + 16 * c;
-          // The keep bits do not wait for the scores.
-          uint4 words[2];
-          if (DQ && DROP)
-            keep_words_n(a.keep, call0 + (uint32_t)(col >> 3), 1, words);
-          if (c == 0) {
-            if (!DQ && DROP)
-              kept = keep_column(a.keep, call0 + (uint64_t)(uint32_t)c0 * per_row, per_row, lane);
-            ok = warp_wait(&bar.s_full[slot], (next / K) & 1, a.err);
+        float eps = 0.0f, far_l = 0.0f, far_r = 0.0f, mass_l = 0.0f, mass_r = 0.0f;
+        float* by_d = sums;
+        if (DQ && a.sum_bufs) {
+          const int sb = k % a.sum_bufs;
+          if (k >= a.sum_bufs)
+            ok = warp_wait(&bar.sums_empty[sb], (k / a.sum_bufs + 1) & 1, a.err, kErrWaitEmpty);
+          if (!ok) break;
+          by_d = sums + sb * S::sum_floats(ndist);
+        }
+        for (int hh = 0; ok && hh < heads; ++hh) {
+          const float* bias = biases + (nb & 1) * nbias;
+          float far_left = 0.0f, far_right = 0.0f;
+          if (a.biased) {
+            ok = warp_wait(&bar.bias_full[nb & 1], (nb / 2) & 1, a.err);
             if (!ok) break;
-            tc_fence_after();
+            far_left = bias[0];
+            far_right = bias[nbias - 1];
           }
-          uint32_t vs[16], vp[16];
-          tmem_ld16(vs, ts + 16 * c);
-          tmem_ld16(vp, tp + 16 * c);
-          // Distances of the warp's rows and the columns: [low, low + 46].
-          const int low = (DQ ? col - wx - 31 : wx - col - 15) - a.q_offset;
-          const bool near = a.biased && low + 46 > -span.left && low < span.right;
-          const float far = !a.biased ? 0.0f : low >= span.right ? far_right : far_left;
-          const bool masked = DQ ? col + 16 > warp_limit : col < warp_limit;
+          // Keep bits: the call of the row's first key, or of its key and query lane % 8.
+          const uint64_t call0 =
+              DQ ? ((uint64_t)(it.b * a.H + h0 + hh) * a.Lq + x) * per_row
+                 : ((uint64_t)(it.b * a.H + h0 + hh) * a.Lq + (lane & 7)) * per_row + (x >> 3);
+          for (; ok && next < nt + (hh + 1) * it.per; next += 2) {
+            const int st = next % S::kStages, slot = next % K;
+            const uint32_t ts = tmem + lanes + slot * 128 + half * 32, tp = ts + 64;
+            // first of the group's 32 columns (keys or queries)
+            const int c0 = (it.from + next - nt - hh * it.per) * kTileRows + 32 * half;
+            uint8_t* stage = smem + S::kRing + st * S::kStage;
+            uint32_t kept = ~0u;
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {  // 16 columns at a time
+              const int col = c0 + 16 * c;
+              // The keep bits do not wait for the scores.
+              uint4 words[2];
+              if (DQ && DROP)
+                keep_words_n(a.keep, call0 + (uint32_t)(col >> 3), 1, words);
+              if (c == 0) {
+                if (!DQ && DROP)
+                  kept = keep_column(a.keep, call0 + (uint64_t)(uint32_t)c0 * per_row, per_row,
+                                     lane);
+                ok = warp_wait(&bar.s_full[slot], (next / K) & 1, a.err);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              uint32_t vs[16], vp[16];
+              tmem_ld16(vs, ts + 16 * c);
+              tmem_ld16(vp, tp + 16 * c);
+              // Distances of the warp's rows and the columns: [low, low + 46].
+              const int low = (DQ ? col - wx - 31 : wx - col - 15) - a.q_offset;
+              const bool near = a.biased && low + 46 > -span.left && low < span.right;
+              const float far = !a.biased ? 0.0f : low >= span.right ? far_right : far_left;
+              const bool masked = DQ ? col + 16 > warp_limit : col < warp_limit;
 
-          // Z and dS of the columns.  Branch-free inside, for the scheduler's sake: a
-          // body each for blocks of one bias value, blocks across several, and
-          // blocks with masked pairs (of either kind).  No more is unrolled than
-          // this: the warps of a block are all at different places of the code,
-          // and more of it than the instruction caches hold costs more than it
-          // saves.
-          auto weigh = [&](auto several_t, auto mask_t) {
-            constexpr bool kSeveral = decltype(several_t)::value, kMask = decltype(mask_t)::value;
-            // The bias of column n of the row: tb[n * step].
-            const int step = (kSeveral || near) ? (DQ ? 1 : -1) : 0;
-            const float* tb =
-                (kSeveral || near)
-                    ? bias + (DQ ? col - x : x - col) - a.q_offset + span.left + kBiasMargin
-                    : bias + (low >= span.right ? nbias - 1 : 0);
-            const uint64_t scale2 = pair(a.scale2, a.scale2);
-            const ulonglong2* qlse =  // two pairs of queries each
-                reinterpret_cast<const ulonglong2*>(stage + 2 * S::kTile) + 8 * half + 4 * c;
-            const ulonglong2* qdelta = qlse + kTileRows / 4;
-            float p[16], z[16], ds[16];
-            uint64_t mass = 0, sum2 = 0;  // sums of p and dS, two lanes of them
-            tmem_wait_ld(vs);
-            tmem_wait_ld(vp);
+              // Z and dS of the columns.  Branch-free inside, for the scheduler's sake: a
+              // body each for blocks of one bias value, blocks across several, and
+              // blocks with masked pairs (of either kind).  No more is unrolled than
+              // this: the warps of a block are all at different places of the code,
+              // and more of it than the instruction caches hold costs more than it
+              // saves.
+              auto weigh = [&](auto several_t, auto mask_t) {
+                constexpr bool kSeveral = decltype(several_t)::value;
+                constexpr bool kMask = decltype(mask_t)::value;
+                // The bias of column n of the row: tb[n * step].
+                const int step = (kSeveral || near) ? (DQ ? 1 : -1) : 0;
+                const float* tb =
+                    (kSeveral || near)
+                        ? bias + (DQ ? col - x : x - col) - a.q_offset + span.left + kBiasMargin
+                        : bias + (low >= span.right ? nbias - 1 : 0);
+                const uint64_t scale2 = pair(a.scale2, a.scale2);
+                const ulonglong2* qlse =  // two pairs of queries each
+                    reinterpret_cast<const ulonglong2*>(stage + 2 * S::kTile) + 8 * half + 4 * c;
+                const ulonglong2* qdelta = qlse + kTileRows / 4;
+                float p[16], z[16], ds[16];
+                uint64_t mass = 0, sum2 = 0;  // sums of p and dS, two lanes of them
+                tmem_wait_ld(vs);
+                tmem_wait_ld(vp);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              uint64_t shift;  // bias - lse
-              if (DQ && !kSeveral && !kMask) {
-                shift = pair(far + nlse, far + nlse);
-              } else {
-                uint64_t nl;
-                if (DQ) {
-                  nl = pair(nlse, nlse);
-                } else {
-                  const ulonglong2 four = qlse[k >> 1];
-                  nl = k & 1 ? four.y : four.x;
+                for (int k = 0; k < 8; ++k) {
+                  uint64_t shift;  // bias - lse
+                  if (DQ && !kSeveral && !kMask) {
+                    shift = pair(far + nlse, far + nlse);
+                  } else {
+                    uint64_t nl;
+                    if (DQ) {
+                      nl = pair(nlse, nlse);
+                    } else {
+                      const ulonglong2 four = qlse[k >> 1];
+                      nl = k & 1 ? four.y : four.x;
+                    }
+                    if (kSeveral)
+                      shift = add2(DQ ? pair(tb[2 * k], tb[2 * k + 1])
+                                      : pair(tb[-2 * k], tb[-2 * k - 1]),
+                                   nl);
+                    else if (kMask && a.biased)
+                      shift = add2(pair(tb[2 * k * step], tb[(2 * k + 1) * step]), nl);
+                    else
+                      shift = add2(pair(far, far), nl);
+                  }
+                  unpair(fma2(pair(vs[2 * k], vs[2 * k + 1]), scale2, shift), &p[2 * k],
+                         &p[2 * k + 1]);
                 }
-                if (kSeveral)
-                  shift = add2(DQ ? pair(tb[2 * k], tb[2 * k + 1]) : pair(tb[-2 * k], tb[-2 * k - 1]),
-                               nl);
-                else if (kMask && a.biased)
-                  shift = add2(pair(tb[2 * k * step], tb[(2 * k + 1) * step]), nl);
-                else
-                  shift = add2(pair(far, far), nl);
-              }
-              unpair(fma2(pair(vs[2 * k], vs[2 * k + 1]), scale2, shift), &p[2 * k], &p[2 * k + 1]);
-            }
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              p[k] = exp2_approx(p[k]);
-              if (kMask) p[k] = (DQ ? col + k < limit : col + k >= limit) ? p[k] : 0.0f;
-            }
-            if (DROP && DQ) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint32_t v[4] = {words[k].x, words[k].y, words[k].z, words[k].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  keep_pair(v[e], T2, p[8 * k + 2 * e], p[8 * k + 2 * e + 1], &z[8 * k + 2 * e],
-                            &z[8 * k + 2 * e + 1]);
-              }
-            } else {
-#pragma unroll
-              for (int k = 0; k < 16; ++k) z[k] = !DROP || (kept >> k & 1) ? p[k] : 0.0f;
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              uint64_t nd;
-              if (DQ) {
-                nd = pair(ndelta, ndelta);
-              } else {
-                const ulonglong2 four = qdelta[k >> 1];
-                nd = k & 1 ? four.y : four.x;
-              }
-              const uint64_t pp = pair(p[2 * k], p[2 * k + 1]);
-              float &d0 = ds[2 * k], &d1 = ds[2 * k + 1];
-              unpair(fma2(pair(z[2 * k], z[2 * k + 1]), pair(vp[2 * k], vp[2 * k + 1]), mul2(pp, nd)),
-                     &d0, &d1);
-              if (DQ && !kSeveral) mass = add2(mass, pp);
-              if (kMask) {
-                const int n = col + 2 * k;
-                d0 = (DQ ? n < limit : n >= limit) ? d0 : 0.0f;
-                d1 = (DQ ? n + 1 < limit : n + 1 >= limit) ? d1 : 0.0f;
-              }
-              if (DQ) sum2 = add2(sum2, pair(d0, d1));
-            }
-            uint32_t o[8];
-            if (!DQ) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
-              tmem_st8(ts + 8 * c, o);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = pack2<T>(ds[2 * k], ds[2 * k + 1]);
-            tmem_st8(tp + 8 * c, o);
-            if (DQ && a.sum_bufs) {
-              float s0, s1;
-              unpair(sum2, &s0, &s1);
-              const float sum = s0 + s1;
-              eps += sum;
-              if (!kSeveral && !(kMask && near)) {
-                unpair(mass, &s0, &s1);
-                if (low >= span.right) {
-                  far_r += sum;
-                  mass_r += s0 + s1;
-                } else {
-                  far_l += sum;
-                  mass_l += s0 + s1;
-                }
-              } else {
-                // Sums down the diagonals of the 32 x 16 block: a running sum moves one
-                // lane (row) on with every column; what lane 31 holds is complete.
-                float run = 0.0f;
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                  const float up = __shfl_up_sync(0xffffffffu, run, 1);
-                  run = lane ? up + ds[k] : ds[k];
-                  if (lane == 31) bar.carry[warp][k] = run;
+                  p[k] = exp2_approx(p[k]);
+                  if (kMask) p[k] = (DQ ? col + k < limit : col + k >= limit) ? p[k] : 0.0f;
                 }
-                __syncwarp();
-                // of the diagonal of the warp's first row and first column
-                float* to = by_d + warp * ndist + low + 31 + span.left + kSumMargin;
-                if (lane < 15) to[lane - 31] += bar.carry[warp][lane];
-                __syncwarp();
-                to[15 - lane] += run;
-                __syncwarp();
-              }
-            }
-          };
-          using Yes = std::true_type;
-          using No = std::false_type;
-          if (masked)
-            weigh(No(), Yes());
-          else if (near)
-            weigh(Yes(), No());
-          else
-            weigh(No(), No());
-          kept >>= 16;
-          }
-          if (!ok) break;
-          tmem_wait_st();
-          if (DQ && keys < a.Lk && c0 + 32 > keys) {
-            // Rows of K past the length have dS = 0, but may hold anything.
-            const int live = max(0, keys - c0);  // of the group's 32
-            for (int k = threadIdx.x & 127; k < (32 - live) * 8 * (DP / 64); k += 128) {
-              const int r = 32 * half + live + (k >> 3) % (32 - live), y = (k >> 3) / (32 - live);
-              *reinterpret_cast<uint4*>(stage + y * (kTileRows * 128) + r * 128 + (k & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-            }
-            fence_async_shared();
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.p_full[slot]);
-          if (pending) {
-            pending = false;
-            finish(k - 1);
-          }
-        }
-        if (a.biased) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.bias_empty[nb & 1]);
-          ++nb;
-        }
-        }
-      nt += heads * it.per;
-      if (DQ && a.sum_bufs && ok) {
-        float* r = by_d + S::kWarps * ndist + g * kRows + row;
-        const float v[5] = {eps, far_l, far_r, mass_l, mass_r};
+                if (DROP && DQ) {
 #pragma unroll
-        for (int i = 0; i < 5; ++i) r[i * G * kRows] = v[i];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.sums_full[k % a.sum_bufs]);
-      }
+                  for (int k = 0; k < 2; ++k) {
+                    const uint32_t v[4] = {words[k].x, words[k].y, words[k].z, words[k].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                      keep_pair(v[e], T2, p[8 * k + 2 * e], p[8 * k + 2 * e + 1],
+                                &z[8 * k + 2 * e], &z[8 * k + 2 * e + 1]);
+                  }
+                } else {
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) z[k] = !DROP || (kept >> k & 1) ? p[k] : 0.0f;
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  uint64_t nd;
+                  if (DQ) {
+                    nd = pair(ndelta, ndelta);
+                  } else {
+                    const ulonglong2 four = qdelta[k >> 1];
+                    nd = k & 1 ? four.y : four.x;
+                  }
+                  const uint64_t pp = pair(p[2 * k], p[2 * k + 1]);
+                  float &d0 = ds[2 * k], &d1 = ds[2 * k + 1];
+                  unpair(fma2(pair(z[2 * k], z[2 * k + 1]), pair(vp[2 * k], vp[2 * k + 1]),
+                              mul2(pp, nd)),
+                         &d0, &d1);
+                  if (DQ && !kSeveral) mass = add2(mass, pp);
+                  if (kMask) {
+                    const int n = col + 2 * k;
+                    d0 = (DQ ? n < limit : n >= limit) ? d0 : 0.0f;
+                    d1 = (DQ ? n + 1 < limit : n + 1 >= limit) ? d1 : 0.0f;
+                  }
+                  if (DQ) sum2 = add2(sum2, pair(d0, d1));
+                }
+                uint32_t o[8];
+                if (!DQ) {
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
+                  tmem_st8(ts + 8 * c, o);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] = pack2<T>(ds[2 * k], ds[2 * k + 1]);
+                tmem_st8(tp + 8 * c, o);
+                if (DQ && a.sum_bufs) {
+                  float s0, s1;
+                  unpair(sum2, &s0, &s1);
+                  const float sum = s0 + s1;
+                  eps += sum;
+                  if (!kSeveral && !(kMask && near)) {
+                    unpair(mass, &s0, &s1);
+                    if (low >= span.right) {
+                      far_r += sum;
+                      mass_r += s0 + s1;
+                    } else {
+                      far_l += sum;
+                      mass_l += s0 + s1;
+                    }
+                  } else {
+                    // Sums down the diagonals of the 32 x 16 block: a running sum moves one
+                    // lane (row) on with every column; what lane 31 holds is complete.
+                    float run = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                      const float up = __shfl_up_sync(0xffffffffu, run, 1);
+                      run = lane ? up + ds[k] : ds[k];
+                      if (lane == 31) bar.carry[warp][k] = run;
+                    }
+                    __syncwarp();
+                    // of the diagonal of the warp's first row and first column
+                    float* to = by_d + warp * ndist + low + 31 + span.left + kSumMargin;
+                    if (lane < 15) to[lane - 31] += bar.carry[warp][lane];
+                    __syncwarp();
+                    to[15 - lane] += run;
+                    __syncwarp();
+                  }
+                }
+              };
+              using Yes = std::true_type;
+              using No = std::false_type;
+              if (masked)
+                weigh(No(), Yes());
+              else if (near)
+                weigh(Yes(), No());
+              else
+                weigh(No(), No());
+              kept >>= 16;
+            }
+            if (!ok) break;
+            tmem_wait_st();
+            if (DQ && keys < a.Lk && c0 + 32 > keys) {
+              // Rows of K past the length have dS = 0, but may hold anything.
+              const int live = max(0, keys - c0);  // of the group's 32
+              for (int k = threadIdx.x & 127; k < (32 - live) * 8 * (DP / 64); k += 128) {
+                const int r = 32 * half + live + (k >> 3) % (32 - live), y = (k >> 3) / (32 - live);
+                *reinterpret_cast<uint4*>(stage + y * (kTileRows * 128) + r * 128 + (k & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+              }
+              fence_async_shared();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.p_full[slot]);
+            if (pending) {
+              pending = false;
+              finish(k - 1);
+            }
+          }
+          if (a.biased) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.bias_empty[nb & 1]);
+            ++nb;
+          }
+        }
+        nt += heads * it.per;
+        if (DQ && a.sum_bufs && ok) {
+          float* r = by_d + S::kWarps * ndist + g * kRows + row;
+          const float v[5] = {eps, far_l, far_r, mass_l, mass_r};
+#pragma unroll
+          for (int i = 0; i < 5; ++i) r[i * G * kRows] = v[i];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.sums_full[k % a.sum_bufs]);
+        }
       }
       if (ok && pending) finish(k - 1);
       pending = have;
@@ -942,7 +971,8 @@ cudaError_t grad_of(const AttnArgs& a, GradArgs f, cudaStream_t s) {
       bytes += f.sum_bufs * one;
     }
   }
-  static_assert(1024 + S::kBias + 2 * kBiasMostBytes + (DQ ? 4 * S::sum_floats(kBiasMost - 2 * (kBiasMargin - kSumMargin)) : 0) <= most,
+  constexpr size_t widest = S::sum_floats(kBiasMost - 2 * (kBiasMargin - kSumMargin));
+  static_assert(1024 + S::kBias + 2 * kBiasMostBytes + (DQ ? sizeof(float) * widest : 0) <= most,
                 "the widest bias must fit");
   static PerDeviceOnce once;
   cudaError_t e = once.run([] {
@@ -983,7 +1013,7 @@ size_t partial_bytes(const AttnArgs& a) {
 // Whether dk and dv are worked out for every query head on its own, in fp32,
 // and joined by a kernel after: where shared heads leave fewer pieces than the
 // card has SMs (152), each as long as its group is large (3 x 517 keys, 2 heads
-// shared by 8: backward 66 -> XXX us).
+// shared by 8: backward 66 -> 46 us).
 bool splits(const AttnArgs& a) {
   return a.H != a.Hkv && (int64_t)blocks_of(a.Lk) * a.B * a.Hkv < 152;
 }
@@ -1075,7 +1105,8 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t s) {
   if (e == cudaSuccess && a.Lq) e = grad<T, true>(a, f, s);
   if (e != cudaSuccess || !a.Lk) return e;
   if (!a.Lq) f.dtable = nullptr;
-  if (splits(a)) f.join = reinterpret_cast<float*>(ws + kCounterBytes + rows_bytes(a) + partial_bytes(a));
+  if (splits(a))
+    f.join = reinterpret_cast<float*>(ws + kCounterBytes + rows_bytes(a) + partial_bytes(a));
   e = grad<T, false>(a, f, s);
   if (e != cudaSuccess || !f.join) return e;
   const JoinArgs j{f.join, a.B, a.H, a.Hkv, a.Lk, a.D, a.dv, a.dk};

@@ -12,7 +12,15 @@
 // there when it is done with one.
 // The softmax is on line: weights are taken relative to a reference m that a
 // row raises (with its sum and its O) only when a score passes it by more
-// than 2^8, so O is hardly ever touched outside the products.
+// than 2^8, so O is hardly ever touched outside the products.  P is rounded to
+// the inputs' type, as the matrix unit wants it; its row sum is of the values
+// before that, in fp32.
+//
+// What bounds it: at d 128 the matrix unit and the softmax beside it (8192
+// keys 0.83 ms, 1330 TFLOP/s; 8 x 2048 causal 0.15 ms, 914), at d 64 the
+// exponentials and the rest of a row's arithmetic (2048 keys 860 TFLOP/s),
+// with dropout the drawing of the keep bits, 72 issue cycles of a scheduler
+// for 256 pairs (32 x 12 x 512 of d 64 96 us, without dropout 59).
 #include <cmath>
 #include <type_traits>
 
@@ -490,7 +498,8 @@ cudaError_t fwd(const AttnArgs& a, cudaStream_t s) {
   const size_t bytes = 1024 + S::kBias + (a.biased ? bias_floats(a.rp) * sizeof(float) : 0);
   static PerDeviceOnce once;
   e = once.run([] {
-    return cudaFuncSetAttribute(k_attn_fwd<T, DP, DROP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(k_attn_fwd<T, DP, DROP>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 1024 + S::kBias + kBiasMostBytes);
   });
   if (e != cudaSuccess) return e;

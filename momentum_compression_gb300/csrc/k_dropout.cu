@@ -1,10 +1,14 @@
 // Dropout with a mask that is never stored: y = residual + keep * x * scale.
 //
 // Two (with a residual three) streams of elements and one Philox call per
-// eight of them: ten rounds of two wide products and two three-way xors,
-// about 60 issue slots a call, 8 an element with loads and conversions.  At
-// 2 bytes an element and 6.8 TB/s an SM has to issue about 90 of its 128
-// lanes' slots a clock; HBM is the bound for every type.
+// eight of them: ten rounds of two wide products and two three-way xors, 72
+// issue cycles of a scheduler for a warp's 256 elements.  Four schedulers of
+// 152 SMs draw for 4.2e12 elements a second, where HBM brings at most 1.7e12
+// of the smallest type: HBM is the bound (65536 x 2048 bf16 with a residual in
+// 117.4 us, 6.86 TB/s; 16384 x 1024 in 18.5 us, 5.45 TB/s, the launch and the
+// tail included).  Arrays that are not 16-byte aligned or have rows of odd
+// lengths take an element a lane and step: 16.4 MB in 10 us, where addresses
+// and 2-byte accesses are the bound.
 #include "elem.cuh"
 #include "keep.cuh"
 #include "model.cuh"
@@ -119,37 +123,43 @@ __global__ void __launch_bounds__(kDropThreads) k_dropout_any(const DropoutArgs 
   const uint64_t e0 =
       ((uint64_t)blockIdx.x * (kDropThreads / 32) + threadIdx.x / 32) * 256;
   if (e0 >= a.n) return;
-  const T* x = static_cast<const T*>(a.x);
-  const T* res = static_cast<const T*>(a.residual);
-  T* y = static_cast<T*>(a.y);
-  float v[8], r[8];
-  uint64_t yo[8];
-  // Row and column of the lane's first element; 32 columns on for each next.
+  // The lane's first element; the next ones are 32 columns on, and where that
+  // passes the end of a row, in the next.
   const uint64_t first = e0 + lane;
   uint64_t row = a.small ? __umul64hi(first, a.magic) : first / a.cols;
   if (a.cols == 1) row = first;
   uint64_t c = first - row * a.cols;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx + c;
+  const T* res = RES ? static_cast<const T*>(a.residual) + row * a.ldr + c : nullptr;
+  T* y = static_cast<T*>(a.y) + row * a.ldy + c;
+  float v[8], r[8];
+  T* to[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     if (first + 32 * k >= a.n) break;
-    v[k] = to_f32(x[row * a.ldx + c]);
-    r[k] = RES ? to_f32(res[row * a.ldr + c]) : 0.0f;
-    yo[k] = row * a.ldy + c;
+    v[k] = to_f32(*x);
+    r[k] = RES ? to_f32(*res) : 0.0f;
+    to[k] = y;
     c += 32;
+    uint32_t rows = 0;
     if (a.cols >= 32) {
-      if (c >= a.cols) c -= a.cols, ++row;
+      rows = c >= a.cols;
+      if (rows) c -= a.cols;
     } else {
-      row += c / (uint32_t)a.cols;
-      c %= (uint32_t)a.cols;
+      rows = (uint32_t)c / (uint32_t)a.cols;
+      c -= rows * (uint32_t)a.cols;
     }
+    x += 32 + rows * (a.ldx - a.cols);
+    if (RES) res += 32 + rows * (a.ldr - a.cols);
+    y += 32 + rows * (a.ldy - a.cols);
   }
   uint32_t byte = 0xffu;
   if (a.keep.T) byte = keep_byte(keep_words(a.keep, e0 / 8 + lane), a.keep.T);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const uint32_t b = __shfl_sync(0xffffffffu, byte, 4 * k + (lane >> 3));
-    if (e0 + 32 * k + lane < a.n)
-      y[yo[k]] = from_f32<T>(drop1(v[k], r[k], b >> (lane & 7) & 1, a.keep.scale));
+    if (first + 32 * k < a.n)
+      *to[k] = from_f32<T>(drop1(v[k], r[k], b >> (lane & 7) & 1, a.keep.scale));
   }
 }
 

@@ -310,8 +310,9 @@ ob_status ob_relpos_bias_bwd(const ob_relpos* rp, const void* dout, int out_type
   OB_MODEL_PTR(dtable, type_bytes(table_type), "dtable");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (N == 0 || Lq == 0 || Lk == 0)
-    return launched(cudaMemsetAsync(dtable, 0, (size_t)rp->num_buckets * H * type_bytes(table_type), s),
-                    "relpos_bias_bwd");
+    return launched(
+        cudaMemsetAsync(dtable, 0, (size_t)rp->num_buckets * H * type_bytes(table_type), s),
+        "relpos_bias_bwd");
   OB_MODEL_PTR(dout, type_bytes(out_type), "dout");
   ob::RelposBwdArgs a{};
   a.rp = *rp;
