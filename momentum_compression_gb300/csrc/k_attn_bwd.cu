@@ -32,11 +32,16 @@
 // pairs), and one that stages the bias of the next head and adds up the bias
 // table's sums of the last.
 //
+// dq and the pass for dk and dv need nothing of one another (but the bias
+// table's sums): the second's blocks start as the first's end (12 heads x 128
+// queries x 128 keys 24.6 -> 16.2 us, BERT-base full 512 309 -> 294 us).
+//
 // What bounds it is the issue of the arithmetic, not the matrix unit: without
-// bias and dropout 866 TFLOP/s (five products counted) at d 128 x 8192 in
-// 3.2 ms, 624 at d 64 x 2048 in 0.55 ms; with both, at 32 x 12 x 512 of
-// d 64, 0.31 ms full (the two passes' keep bits alone are 48 us of every
-// scheduler) and 0.27 ms over ragged lengths.
+// bias and dropout 888 TFLOP/s (five products counted) at d 128 x 8192 in
+// 3.1 ms, 644 at d 64 x 2048 in 0.53 ms; with both, at 32 x 12 x 512 of
+// d 64, 0.29 ms full (the two passes' keep bits alone are 48 us of every
+// scheduler) and 0.26 ms over ragged lengths, where the start and the end of
+// the many short pieces weigh more.
 #include <cmath>
 #include <type_traits>
 
@@ -70,6 +75,7 @@ struct GradArgs {
   void* dtable;      // dkv: or null
   float* join;       // dkv, split over the heads that share keys: [dv, dk][B][H][Lk][D], or null
   unsigned* next;    // the counter of this launch, 0 at its start
+  bool behind_dq;    // dkv: launched behind dq
   unsigned* err;
 };
 
@@ -282,7 +288,9 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
-  grid_wait();
+  // dk and dv need nothing of dq's before the bias table's sums: they start as
+  // its blocks end, which have all waited for the rows.
+  if (DQ || !a.behind_dq) grid_wait();
   grid_release();
 
   // The k-th piece of work of this block, for one of the roles that follow it:
@@ -529,7 +537,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           float* row = by_d + S::kWarps * ndist;  // [5][G][kRows]
           // A row's dS sums to zero; what it sums to is the error of rowsum(do o),
           // taken from the rounded o.  It is taken out of the far buckets, whose
-          // weight would multiply it, and out of the row's entry for dk.
+          // weight would multiply it.
           float far_l = 0.0f, far_r = 0.0f;
           for (int r = lane; r < kRows; r += 32) {
             float v[5] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
@@ -539,9 +547,6 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
               for (int g = 0; g < G; ++g) v[i] += row[(i * G + g) * kRows + r];
             far_l += v[1] - v[0] * v[3];
             far_r += v[2] - v[0] * v[4];
-            // The only addition to this entry: its order is no question.
-            const int64_t at = row_at(prev.b * a.H + prev.hx, a.Lqp, prev.x0 + r);
-            atomicAdd(&a.rows[at + kTileRows], -v[0]);
           }
 #pragma unroll
           for (int o = 16; o; o >>= 1) {
@@ -587,6 +592,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       }
       // The bias table's gradient from the sums that dq left: a lane a bucket, in
       // order, beside the last piece's arithmetic.
+      if (!DQ) grid_wait();
       if (!DQ && a.dtable)
         for (int h = blockIdx.x; h < a.H; h += gridDim.x)
           for (int n = lane; n < a.rp.num_buckets; n += 32) {
@@ -947,6 +953,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     tc_fence_after();
     tmem_free(tmem, 512);
   }
+  if (!DQ) grid_wait();  // so that this grid's end is that of all before it
 }
 
 template <typename T, int DP, bool DQ, bool DROP>
@@ -1105,6 +1112,7 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t s) {
   if (e == cudaSuccess && a.Lq) e = grad<T, true>(a, f, s);
   if (e != cudaSuccess || !a.Lk) return e;
   if (!a.Lq) f.dtable = nullptr;
+  f.behind_dq = a.Lq != 0;
   if (splits(a))
     f.join = reinterpret_cast<float*>(ws + kCounterBytes + rows_bytes(a) + partial_bytes(a));
   e = grad<T, false>(a, f, s);
