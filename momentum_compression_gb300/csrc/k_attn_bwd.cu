@@ -34,13 +34,13 @@
 //
 // dq and the pass for dk and dv need nothing of one another (but the bias
 // table's sums): the second's blocks start as the first's end (12 heads x 128
-// queries x 128 keys 24.6 -> 16.2 us, BERT-base full 512 309 -> 294 us).
+// queries x 128 keys 24.6 -> 16.2 us, 32 x 12 x 512 of d 64 309 -> 294 us).
 //
 // What bounds it is the issue of the arithmetic, not the matrix unit: without
-// bias and dropout 888 TFLOP/s (five products counted) at d 128 x 8192 in
-// 3.1 ms, 644 at d 64 x 2048 in 0.53 ms; with both, at 32 x 12 x 512 of
-// d 64, 0.29 ms full (the two passes' keep bits alone are 48 us of every
-// scheduler) and 0.26 ms over ragged lengths, where the start and the end of
+// bias and dropout 897 TFLOP/s (five products counted) at d 128 x 8192 in
+// 3.1 ms, 668 at d 64 x 2048 in 0.51 ms; with both, at 32 x 12 x 512 of
+// d 64, 0.27 ms full (the two passes' keep bits alone are 48 us of every
+// scheduler) and 0.24 ms over ragged lengths, where the start and the end of
 // the many short pieces weigh more.
 #include <cmath>
 #include <type_traits>
@@ -54,7 +54,7 @@ namespace {
 
 constexpr int kRows = 128;  // rows of X, Y
 constexpr int kTileRows = 64;
-constexpr int kRowsPerBlock = 16;  // of k_rows
+constexpr int kRowThreads = 256;   // of k_rows
 
 struct GradArgs {
   CUtensorMap q, grad_o, k, v;  // boxes of 64 rows
@@ -89,8 +89,10 @@ struct RowArgs {
 };
 
 // ---------------------------------------------------------------------------
-// -lse and -rowsum(do o): 16 lanes a row.  Rows past Lq and rows without keys
-// get -lse = -inf, which makes every weight exp2(s - lse) zero.
+// -lse and -rowsum(do o): a block takes 128 queries of a head, LANES lanes a
+// row, all rows' loads on their way at once (32 x 12 x 512 of d 64, 50 MB, in
+// 11 us; with a row at a time 23).  Rows past Lq and rows without keys get
+// -lse = -inf, which makes every weight exp2(s - lse) zero.
 // ---------------------------------------------------------------------------
 
 // Where query i of head bh has the first of its two values; the second is
@@ -99,40 +101,50 @@ __device__ __forceinline__ int64_t row_at(int bh, int Lqp, int i) {
   return (int64_t)bh * Lqp * 2 + (int64_t)(i / kTileRows) * (2 * kTileRows) + i % kTileRows;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(16 * kRowsPerBlock) k_rows(const RowArgs a) {
+template <typename T, int LANES>
+__global__ void __launch_bounds__(kRowThreads) k_rows(const RowArgs a) {
   grid_release();
   if (blockIdx.x == 0 && threadIdx.x < 2) a.next[threadIdx.x] = 0;
-  const int l = threadIdx.x & 15;
-  const int64_t at = (int64_t)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 4);
-  if (at >= (int64_t)a.B * a.H * a.Lqp) return;
-  const int bh = (int)(at / a.Lqp), i = (int)(at % a.Lqp), b = bh / a.H, h = bh % a.H;
-  float sum = 0.0f;
-  if (i < a.Lq && 8 * l < a.D) {
-    const uint4 x = *reinterpret_cast<const uint4*>(
-        static_cast<const T*>(a.o.data) + b * a.o.b + (int64_t)i * a.o.l + h * a.o.h + 8 * l);
-    const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.grad_o.data) +
-                                                    b * a.grad_o.b + (int64_t)i * a.grad_o.l +
-                                                    h * a.grad_o.h + 8 * l);
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+  const int heads = a.B * a.H;
+  if (heads == 0 || a.Lq == 0) return;
+  constexpr int kPass = kRowThreads / LANES, N = kRows / kPass;
+  const int l = threadIdx.x % LANES, r0 = (int)(blockIdx.x / heads) * kRows + threadIdx.x / LANES;
+  const int bh = blockIdx.x % heads, b = bh / a.H, h = bh % a.H;
+  const T* o = static_cast<const T*>(a.o.data) + b * a.o.b + h * a.o.h + 8 * l;
+  const T* g = static_cast<const T*>(a.grad_o.data) + b * a.grad_o.b + h * a.grad_o.h + 8 * l;
+  uint4 x[N], y[N];
+  float lse[N];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = unpack2<T>(xs[k]), g = unpack2<T>(ys[k]);
-      sum = __fmaf_rn(f.x, g.x, sum);
-      sum = __fmaf_rn(f.y, g.y, sum);
+  for (int n = 0; n < N; ++n) {
+    const int i = r0 + n * kPass;
+    x[n] = y[n] = make_uint4(0, 0, 0, 0);
+    lse[n] = -INFINITY;
+    if (i >= a.Lq) continue;
+    if (8 * l < a.D) {
+      x[n] = *reinterpret_cast<const uint4*>(o + (int64_t)i * a.o.l);
+      y[n] = *reinterpret_cast<const uint4*>(g + (int64_t)i * a.grad_o.l);
     }
+    lse[n] = a.lse[(int64_t)bh * a.Lq + i];
   }
 #pragma unroll
-  for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (l == 0) {
-    float nlse = -INFINITY;
-    if (i < a.Lq) {
-      const float x = a.lse[(int64_t)bh * a.Lq + i];
-      if (x != -INFINITY) nlse = -x * kLog2e;
+  for (int n = 0; n < N; ++n) {
+    const uint32_t xs[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+    const uint32_t ys[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = unpack2<T>(xs[k]), e = unpack2<T>(ys[k]);
+      sum = __fmaf_rn(f.x, e.x, sum);
+      sum = __fmaf_rn(f.y, e.y, sum);
     }
-    float* to = a.rows + row_at(bh, a.Lqp, i);
-    to[0] = nlse;
-    to[kTileRows] = nlse == -INFINITY ? 0.0f : -sum * a.inv_keep;
+#pragma unroll
+    for (int k = LANES / 2; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    if (l == 0) {
+      const bool none = lse[n] == -INFINITY;
+      float* to = a.rows + row_at(bh, a.Lqp, r0 + n * kPass);
+      to[0] = none ? -INFINITY : -lse[n] * kLog2e;
+      to[kTileRows] = none ? 0.0f : -sum * a.inv_keep;
+    }
   }
 }
 
@@ -170,7 +182,7 @@ struct GradShape {
 // a block of 32 x 16 touches when it touches what lies between them.
 constexpr int kSumMargin = 48;
 
-constexpr int kItems = 8;  // pieces handed out at a time
+constexpr int kItems = 4;  // pieces handed out at a time
 
 struct Item {
   int x0, b, hx, keys, from, per;  // x0 < 0: no more
@@ -182,10 +194,11 @@ struct GradBars {
   uint64_t x_full[2], x_empty[2], full[S], empty[S], s_full[3], p_full[3], acc_full[2], acc_free[2];
   uint64_t bias_full[2], bias_empty[2], sums_full[2], sums_empty[2], drain[2];
   Item item[kItems], done[W];  // done: the piece whose results a warp still has to take
+  alignas(16) float rows[kItems][2 * kRows];  // dq: of the piece's queries, as in global memory
   uint32_t tmem;
   int first[OB_RELPOS_MAX_SIDE];
   uint8_t bucket[kBiasMost];
-  float carry[W][32];
+  alignas(16) float carry[W][16];
 };
 
 // The pair of weights whose halfwords are w, dropped ones as zero.
@@ -198,6 +211,15 @@ __device__ __forceinline__ void keep_pair(uint32_t w, uint32_t T2, float p0, flo
       "selp.f32 %1, %5, 0f00000000, b;\n\t}"
       : "=f"(*z0), "=f"(*z1)
       : "r"(w), "r"(T2), "f"(p0), "f"(p1));
+}
+
+// v += what the lane below (lane - 1) has in u; in lane 0 nothing.
+__device__ __forceinline__ void add_from_below(float* v, float u) {
+  asm volatile("{\n\t.reg .pred in;\n\t.reg .f32 t;\n\t"
+               "shfl.sync.up.b32 t|in, %1, 1, 0, 0xffffffff;\n\t"
+               "@in add.f32 %0, %0, t;\n\t}"
+               : "+f"(*v)
+               : "f"(u));
 }
 
 // Keep bits of 32 queries for the thread's key, from calls that hold eight
@@ -295,10 +317,11 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
 
   // The k-th piece of work of this block, for one of the roles that follow it:
   // false after the last, or when the wait ran out.
-  auto take = [&](int k, Item& it) {
+  auto take = [&](int k, Item& it, auto&& use) {
     const int slot = k % kItems;
     if (!warp_wait(&bar.item_full[slot], (k / kItems) & 1, a.err)) return false;
     it = bar.item[slot];
+    use(slot);
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar.item_empty[slot]);
     return it.x0 >= 0;
@@ -309,6 +332,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     // DQ: x0 is a query of head hx.  Else a key of head hx, and the tiles run over
     // the queries from tile `from` on of the heads that share it.
     int idx = blockIdx.x, k = 0, nx = 0, nt = 0;  // pieces, X buffers and tiles issued so far
+    int given = 0;                                // of the pieces, those that were handed out
     bool ok = true;
     // Finds the next piece with pairs, clearing the rows of those without, and
     // hands it to the other roles.
@@ -335,25 +359,26 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           it = Item{x0, b, hx, keys, from, per};
           break;
         }
-        const int chunks = a.D / 8, rows = min(kRows, (DQ ? a.Lq : a.Lk) - x0);
+        // 16 bytes a lane, as many rows at a time as a warp has lanes for.
+        const int chunks = a.D / 8, each = 32 / chunks, d = lane % chunks * 8;
+        const int rows = lane < each * chunks ? min(kRows, (DQ ? a.Lq : a.Lk) - x0) : 0;
         const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 4
-        for (int t = lane; t < rows * chunks; t += 32) {
-          const int64_t r = x0 + t / chunks;
-          const int d = t % chunks * 8;
-          if (!DQ && a.join) {
-            for (int o = 0; o < 2; ++o) {
-              uint4* to = reinterpret_cast<uint4*>(
-                  a.join + (((int64_t)(o * a.B + b) * a.H + hx) * a.Lk + r) * a.D + d);
-              to[0] = to[1] = zero;
+        if (!DQ && a.join) {
+          float* dv = a.join + (((int64_t)b * a.H + hx) * a.Lk + x0) * a.D + d;
+          float* dk = dv + (int64_t)a.B * a.H * a.Lk * a.D;
+          for (int r = lane / chunks; r < rows; r += each)
+            for (int half = 0; half < 8; half += 4) {
+              *reinterpret_cast<uint4*>(dv + r * a.D + half) = zero;
+              *reinterpret_cast<uint4*>(dk + r * a.D + half) = zero;
             }
-            continue;
+        } else {
+          T* to2 = static_cast<T*>(a.out2.data) + b * a.out2.b + x0 * a.out2.l + hx * a.out2.h + d;
+          T* to1 = static_cast<T*>(a.out1.data) + b * a.out1.b + x0 * a.out1.l + hx * a.out1.h + d;
+#pragma unroll 4
+          for (int r = lane / chunks; r < rows; r += each) {
+            *reinterpret_cast<uint4*>(to2 + r * a.out2.l) = zero;
+            if (!DQ) *reinterpret_cast<uint4*>(to1 + r * a.out1.l) = zero;
           }
-          *reinterpret_cast<uint4*>(static_cast<T*>(a.out2.data) + b * a.out2.b + r * a.out2.l +
-                                    hx * a.out2.h + d) = zero;
-          if (!DQ)
-            *reinterpret_cast<uint4*>(static_cast<T*>(a.out1.data) + b * a.out1.b + r * a.out1.l +
-                                      hx * a.out1.h + d) = zero;
         }
         if (DQ && a.sum_bufs) {
           float* to =
@@ -364,9 +389,17 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       const int slot = k % kItems;
       if (k >= kItems)
         ok = warp_wait(&bar.item_empty[slot], (k / kItems + 1) & 1, a.err, kErrWaitEmpty);
+      if (ok) given = k + 1;
       if (ok && lane == 0) {
         bar.item[slot] = it;
-        mbar_arrive(&bar.item_full[slot]);
+        if (DQ && it.x0 >= 0) {
+          constexpr uint32_t bytes = 2 * kRows * sizeof(float);  // Lqp covers every row
+          mbar_arrive_expect_tx(&bar.item_full[slot], bytes);
+          bulk_g2s(bar.rows[slot], a.rows + row_at(it.b * a.H + it.hx, a.Lqp, it.x0), bytes,
+                   &bar.item_full[slot]);
+        } else {
+          mbar_arrive(&bar.item_full[slot]);
+        }
       }
       ++k;
       return it;
@@ -420,12 +453,13 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       }
       it = after;
     }
-    if (!ok) {  // a wait ran out: let what is in flight land before the block ends
-      for (int i = max(0, nx - S::kXBufs); i < nx; ++i)
-        mbar_wait(&bar.x_full[i % S::kXBufs], (i / S::kXBufs) & 1, a.err, kErrDrain);
-      for (int i = max(0, nt - S::kStages); i < nt; ++i)
-        mbar_wait(&bar.full[i % S::kStages], (i / S::kStages) & 1, a.err, kErrDrain);
-    }
+    // Whatever became of the others: what is in flight lands before the block ends.
+    for (int i = max(0, nx - S::kXBufs); i < nx; ++i)
+      mbar_wait(&bar.x_full[i % S::kXBufs], (i / S::kXBufs) & 1, a.err, kErrDrain);
+    for (int i = max(0, nt - S::kStages); i < nt; ++i)
+      mbar_wait(&bar.full[i % S::kStages], (i / S::kStages) & 1, a.err, kErrDrain);
+    for (int i = max(0, given - kItems); i < given; ++i)
+      mbar_wait(&bar.item_full[i % kItems], (i / kItems) & 1, a.err, kErrDrain);
   } else if (warp == kScores) {
     // ----- S and dP -------------------------------------------------------
     constexpr uint32_t kShapeS = mma_shape(kBf16, kTileRows, false);
@@ -436,7 +470,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     int st = 0, par = 0, g = 0;     // stage, its phase, slot of the tile
     int fst = 0, fpar = 0, nt = 0;  // stage and phase of the tile that had the slot last
     Item it;
-    for (int k = 0; ok && take(k, it); ++k) {
+    for (int k = 0; ok && take(k, it, [](int) {}); ++k) {
       const int xb = k % S::kXBufs;
       ok = warp_wait(&bar.x_full[xb], (k / S::kXBufs) & 1, a.err);
       const uint64_t xd = x_desc + (uint32_t)xb * (2 * S::kX >> 4);
@@ -478,7 +512,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     bool ok = true;
     int st = 0, g = 0, gpar = 0;
     Item it;
-    for (int k = 0; ok && take(k, it); ++k) {
+    for (int k = 0; ok && take(k, it, [](int) {}); ++k) {
       const int total = heads * it.per, ab = k % S::kAccBufs;
       const uint32_t acc = tmem + S::kAcc + ab * S::kAccCols;
       for (int t = 0; t < total; ++t) {
@@ -514,7 +548,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       int k = 0, nb = 0;  // pieces taken, biases staged
       bool ok = true;
       Item it, prev;
-      bool have = take(k, it), had = false;
+      bool have = take(k, it, [](int) {}), had = false;
       int done = 0;  // pieces whose sums are out
       while (ok && (have || had)) {
         if (have) {
@@ -588,7 +622,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
         }
         had = have;
         prev = it;
-        have = have && take(k, it);
+        have = have && take(k, it, [](int) {});
       }
       // The bias table's gradient from the sums that dq left: a lane a bucket, in
       // order, beside the last piece's arithmetic.
@@ -614,9 +648,9 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     // tiles of earlier pieces, the pair's next tile, biases used
     int nt = 0, next = g >> 1, nb = 0;
     float nlse = 0.0f, ndelta = 0.0f;  // of the row's query
-    auto fetch = [&](const Item& of) {
-      if (!DQ) return;  // Lqp covers every row of the block
-      const float* r = a.rows + row_at(of.b * a.H + of.hx, a.Lqp, of.x0 + row);
+    auto fetch = [&](int slot) {
+      if (!DQ) return;
+      const float* r = bar.rows[slot] + row_at(0, 0, row);
       nlse = r[0];
       ndelta = r[kTileRows];
     };
@@ -693,8 +727,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     // A piece's results are taken after the first tile of the next: until then the
     // other groups' last tiles and their products would be waited for.
     Item it;
-    bool have = take(0, it), pending = false;
-    if (have) fetch(it);
+    bool have = take(0, it, fetch), pending = false;
     for (int k = 0; ok && (have || pending); ++k) {
       if (have) {
         const int x = it.x0 + row, wx = it.x0 + (warp & 3) * 32;  // the warp's first row
@@ -874,20 +907,21 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
                     }
                   } else {
                     // Sums down the diagonals of the 32 x 16 block: a running sum moves one
-                    // lane (row) on with every column; what lane 31 holds is complete.
-                    float run = 0.0f;
+                    // lane (row) on with every column; what lane 31 then holds is complete.
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                      const float up = __shfl_up_sync(0xffffffffu, run, 1);
-                      run = lane ? up + ds[k] : ds[k];
-                      if (lane == 31) bar.carry[warp][k] = run;
+                    for (int k = 1; k < 16; ++k) add_from_below(&ds[k], ds[k - 1]);
+                    if (lane == 31) {
+#pragma unroll
+                      for (int k = 0; k < 16; k += 4)
+                        *reinterpret_cast<float4*>(bar.carry[warp] + k) =
+                            make_float4(ds[k], ds[k + 1], ds[k + 2], ds[k + 3]);
                     }
                     __syncwarp();
                     // of the diagonal of the warp's first row and first column
                     float* to = by_d + warp * ndist + low + 31 + span.left + kSumMargin;
                     if (lane < 15) to[lane - 31] += bar.carry[warp][lane];
                     __syncwarp();
-                    to[15 - lane] += run;
+                    to[15 - lane] += ds[15];
                     __syncwarp();
                   }
                 }
@@ -944,8 +978,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       __syncwarp();
       if (lane == 0) bar.done[warp] = it;
       __syncwarp();
-      have = take(k + 1, it);
-      if (have) fetch(it);  // on its way meanwhile
+      have = take(k + 1, it, fetch);
     }
   }
   __syncthreads();
@@ -1106,8 +1139,12 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   RowArgs r{a.B, a.H, a.D, a.Lq, f.Lqp, a.o, a.grad_o, a.lse, 1.0f / a.keep.scale, f.rows, f.next};
-  const int64_t rows = (int64_t)a.B * a.H * f.Lqp;
-  k_rows<T><<<(unsigned)(rows ? rows / kRowsPerBlock : 1), 16 * kRowsPerBlock, 0, s>>>(r);
+  const int64_t blocks = (int64_t)a.B * a.H * blocks_of(a.Lq);
+  const unsigned grid_rows = (unsigned)(blocks ? blocks : 1);  // one clears the counters
+  if (a.D <= 64)
+    k_rows<T, 8><<<grid_rows, kRowThreads, 0, s>>>(r);
+  else
+    k_rows<T, 16><<<grid_rows, kRowThreads, 0, s>>>(r);
   e = cudaGetLastError();
   if (e == cudaSuccess && a.Lq) e = grad<T, true>(a, f, s);
   if (e != cudaSuccess || !a.Lk) return e;
