@@ -39,8 +39,8 @@
 // What bounds it is the issue of the arithmetic, not the matrix unit: without
 // bias and dropout 897 TFLOP/s (five products counted) at d 128 x 8192 in
 // 3.1 ms, 668 at d 64 x 2048 in 0.51 ms; with both, at 32 x 12 x 512 of
-// d 64, 0.27 ms full (the two passes' keep bits alone are 48 us of every
-// scheduler) and 0.24 ms over ragged lengths, where the start and the end of
+// d 64, 0.26 ms full (the two passes' keep bits alone are 48 us of every
+// scheduler) and 0.23 ms over ragged lengths, where the start and the end of
 // the many short pieces weigh more.
 #include <cmath>
 #include <type_traits>
@@ -182,6 +182,13 @@ struct GradShape {
 // a block of 32 x 16 touches when it touches what lies between them.
 constexpr int kSumMargin = 48;
 
+// Floats of a staged bias of n distances, and distances of the sums that go
+// with it: in whole float4.
+__host__ __device__ constexpr int bias_room(int n) { return (n + 3) / 4 * 4; }
+__host__ __device__ constexpr int sum_dists(int n) {
+  return (n - 2 * (kBiasMargin - kSumMargin) + 3) / 4 * 4;
+}
+
 constexpr int kItems = 4;  // pieces handed out at a time
 
 struct Item {
@@ -265,13 +272,14 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const BiasSpan span = a.biased ? bias_span(a.rp) : BiasSpan{0, 0};
   const int nbias = a.biased ? bias_floats(a.rp) : 0;
-  const int ndist = nbias - 2 * (kBiasMargin - kSumMargin);
+  const int bias_step = DQ ? bias_room(nbias) : nbias;  // the sums behind them are read as float4
+  const int ndist = a.biased ? sum_dists(nbias) : 0;
   // A piece's heads: its X, the first and the number of those on the other side.
   const int group = a.H / a.Hkv;
   const bool single = DQ || a.join;
   const int heads_x = single ? a.H : a.Hkv, heads = single ? 1 : group;
   float* biases = reinterpret_cast<float*>(smem + S::kBias);
-  float* sums = biases + 2 * nbias;  // sum_bufs buffers of S::sum_floats(ndist)
+  float* sums = biases + 2 * bias_step;  // sum_bufs buffers of S::sum_floats(ndist)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kItems; ++i) {
@@ -550,6 +558,15 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       Item it, prev;
       bool have = take(k, it, [](int) {}), had = false;
       int done = 0;  // pieces whose sums are out
+      // The distances of bucket n, and those of the lane's first.
+      auto distances = [&](int n) {
+        int64_t lo, hi;
+        bucket_range(bar.first, a.rp.side, a.rp.two_sided, n, -(span.left + kSumMargin),
+                     span.right + kSumMargin, &lo, &hi);
+        return make_int2((int)lo, (int)hi);
+      };
+      int2 mine = make_int2(0, 0);
+      if (DQ && a.sum_bufs && lane < a.rp.num_buckets) mine = distances(lane);
       while (ok && (have || had)) {
         if (have) {
           ++k;
@@ -557,8 +574,9 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
             if (nb >= 2)
               ok = warp_wait(&bar.bias_empty[nb & 1], (nb / 2 + 1) & 1, a.err, kErrWaitEmpty);
             if (!ok) break;
-            stage_bias(biases + (nb & 1) * nbias, bar.bucket, nbias, static_cast<const T*>(a.table),
-                       a.H, single ? it.hx : it.hx * group + hh, lane, 32);
+            stage_bias(biases + (nb & 1) * bias_step, bar.bucket, nbias,
+                       static_cast<const T*>(a.table), a.H, single ? it.hx : it.hx * group + hh,
+                       lane, 32);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.bias_full[nb & 1]);
           }
@@ -588,30 +606,35 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
             far_r += __shfl_xor_sync(0xffffffffu, far_r, o);
           }
           // The warps' sums of a distance into the first warp's, the others cleared.
-          for (int i = lane; i < ndist; i += 32) {
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          for (int i = lane; i < ndist / 4; i += 32) {
+            float4* d = reinterpret_cast<float4*>(by_d) + i;
+            float4 sum[2] = {d[0], d[ndist / 4]};
 #pragma unroll
-            for (int w = 0; w < S::kWarps; ++w) sum[w & 3] += by_d[w * ndist + i];
+            for (int w = 2; w < S::kWarps; ++w) {
+              const float4 v = d[w * (ndist / 4)];
+              float4& to = sum[w & 1];
+              to = make_float4(to.x + v.x, to.y + v.y, to.z + v.z, to.w + v.w);
+            }
 #pragma unroll
-            for (int w = 1; w < S::kWarps; ++w) by_d[w * ndist + i] = 0.0f;
-            by_d[i] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            for (int w = 1; w < S::kWarps; ++w)
+              d[w * (ndist / 4)] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            d[0] = make_float4(sum[0].x + sum[1].x, sum[0].y + sum[1].y, sum[0].z + sum[1].z,
+                               sum[0].w + sum[1].w);
           }
           __syncwarp();
           float* to = a.partial + (((int64_t)prev.hx * a.B + prev.b) * a.blocks + prev.x0 / kRows) *
                                       a.rp.num_buckets;
           for (int n = lane; n < a.rp.num_buckets; n += 32) {
-            int64_t lo, hi;
-            bucket_range(bar.first, a.rp.side, a.rp.two_sided, n, -(span.left + kSumMargin),
-                         span.right + kSumMargin, &lo, &hi);
+            const int2 of = n == lane ? mine : distances(n);
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             if (n == a.rp.side - 1) sum[0] = far_l;
             if (n == (a.rp.two_sided ? a.rp.num_buckets - 1 : 0)) sum[1] = far_r;
             const float* from = by_d + span.left + kSumMargin;
-            int i = (int)lo;
-            for (; i + 4 <= (int)hi; i += 4)
+            int i = of.x;
+            for (; i + 4 <= of.y; i += 4)
 #pragma unroll
               for (int j = 0; j < 4; ++j) sum[j] += from[i + j];
-            for (; i < (int)hi; ++i) sum[2] += from[i];
+            for (; i < of.y; ++i) sum[2] += from[i];
             to[n] = ((sum[0] + sum[1]) + (sum[2] + sum[3])) * a.keep.scale;
           }
           __syncwarp();
@@ -751,7 +774,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           by_d = sums + sb * S::sum_floats(ndist);
         }
         for (int hh = 0; ok && hh < heads; ++hh) {
-          const float* bias = biases + (nb & 1) * nbias;
+          const float* bias = biases + (nb & 1) * bias_step;
           float far_left = 0.0f, far_right = 0.0f;
           if (a.biased) {
             ok = warp_wait(&bar.bias_full[nb & 1], (nb / 2) & 1, a.err);
@@ -909,19 +932,26 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
                     // Sums down the diagonals of the 32 x 16 block: a running sum moves one
                     // lane (row) on with every column; what lane 31 then holds is complete.
 #pragma unroll
-                    for (int k = 1; k < 16; ++k) add_from_below(&ds[k], ds[k - 1]);
+                    for (int k = 1; k < 8; ++k) {  // in two chains, of eight columns
+                      add_from_below(&ds[k], ds[k - 1]);
+                      add_from_below(&ds[8 + k], ds[7 + k]);
+                    }
                     if (lane == 31) {
 #pragma unroll
                       for (int k = 0; k < 16; k += 4)
                         *reinterpret_cast<float4*>(bar.carry[warp] + k) =
                             make_float4(ds[k], ds[k + 1], ds[k + 2], ds[k + 3]);
                     }
+                    // Eight columns on, the first chain's rows meet the second's; its last
+                    // eight rows leave the block.
+                    const float first = __shfl_up_sync(0xffffffffu, ds[7], 8);
                     __syncwarp();
                     // of the diagonal of the warp's first row and first column
                     float* to = by_d + warp * ndist + low + 31 + span.left + kSumMargin;
-                    if (lane < 15) to[lane - 31] += bar.carry[warp][lane];
+                    if (lane < 15 && lane != 7) to[lane - 31] += bar.carry[warp][lane];
                     __syncwarp();
-                    to[15 - lane] += ds[15];
+                    to[15 - lane] += lane < 8 ? ds[15] : ds[15] + first;
+                    if (lane >= 24) to[7 - lane] += ds[7];
                     __syncwarp();
                   }
                 }
@@ -1002,17 +1032,17 @@ cudaError_t grad_of(const AttnArgs& a, GradArgs f, cudaStream_t s) {
   size_t bytes = 1024 + S::kBias;
   if (a.biased) {
     const int n = bias_floats(a.rp);
-    bytes += 2 * n * sizeof(float);
+    bytes += 2 * bias_room(n) * sizeof(float);
     if (DQ && f.dtable) {
       // Two buffers, so that the sums of a piece are added up beside the next
       // one; a wide bias may leave room for one.
-      const size_t one = S::sum_floats(n - 2 * (kBiasMargin - kSumMargin)) * sizeof(float);
+      const size_t one = S::sum_floats(sum_dists(n)) * sizeof(float);
       f.sum_bufs = bytes + 2 * one <= most ? 2 : 1;
       bytes += f.sum_bufs * one;
     }
   }
-  constexpr size_t widest = S::sum_floats(kBiasMost - 2 * (kBiasMargin - kSumMargin));
-  static_assert(1024 + S::kBias + 2 * kBiasMostBytes + (DQ ? sizeof(float) * widest : 0) <= most,
+  constexpr size_t widest = S::sum_floats(sum_dists(kBiasMost)) * sizeof(float);
+  static_assert(1024 + S::kBias + 8 * bias_room(kBiasMost) + (DQ ? widest : 0) <= most,
                 "the widest bias must fit");
   static PerDeviceOnce once;
   cudaError_t e = once.run([] {
