@@ -90,7 +90,7 @@ struct RowArgs {
 
 // ---------------------------------------------------------------------------
 // -lse and -rowsum(do o): a block takes 128 queries of a head, LANES lanes a
-// row, all rows' loads on their way at once (32 x 12 x 512 of d 64, 50 MB, in
+// row, four rows' loads on their way at once (32 x 12 x 512 of d 64, 50 MB, in
 // 11 us; with a row at a time 23).  Rows past Lq and rows without keys get
 // -lse = -inf, which makes every weight exp2(s - lse) zero.
 // ---------------------------------------------------------------------------
@@ -107,43 +107,46 @@ __global__ void __launch_bounds__(kRowThreads) k_rows(const RowArgs a) {
   if (blockIdx.x == 0 && threadIdx.x < 2) a.next[threadIdx.x] = 0;
   const int heads = a.B * a.H;
   if (heads == 0 || a.Lq == 0) return;
-  constexpr int kPass = kRowThreads / LANES, N = kRows / kPass;
+  constexpr int kPass = kRowThreads / LANES, N = 4;
   const int l = threadIdx.x % LANES, r0 = (int)(blockIdx.x / heads) * kRows + threadIdx.x / LANES;
   const int bh = blockIdx.x % heads, b = bh / a.H, h = bh % a.H;
   const T* o = static_cast<const T*>(a.o.data) + b * a.o.b + h * a.o.h + 8 * l;
   const T* g = static_cast<const T*>(a.grad_o.data) + b * a.grad_o.b + h * a.grad_o.h + 8 * l;
-  uint4 x[N], y[N];
-  float lse[N];
+#pragma unroll 1
+  for (int p = r0; p < r0 / kRows * kRows + kRows; p += N * kPass) {
+    uint4 x[N], y[N];
+    float lse[N];
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const int i = r0 + n * kPass;
-    x[n] = y[n] = make_uint4(0, 0, 0, 0);
-    lse[n] = -INFINITY;
-    if (i >= a.Lq) continue;
-    if (8 * l < a.D) {
-      x[n] = *reinterpret_cast<const uint4*>(o + (int64_t)i * a.o.l);
-      y[n] = *reinterpret_cast<const uint4*>(g + (int64_t)i * a.grad_o.l);
-    }
-    lse[n] = a.lse[(int64_t)bh * a.Lq + i];
-  }
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const uint32_t xs[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
-    const uint32_t ys[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
-    float sum = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = unpack2<T>(xs[k]), e = unpack2<T>(ys[k]);
-      sum = __fmaf_rn(f.x, e.x, sum);
-      sum = __fmaf_rn(f.y, e.y, sum);
+    for (int n = 0; n < N; ++n) {
+      const int i = p + n * kPass;
+      x[n] = y[n] = make_uint4(0, 0, 0, 0);
+      lse[n] = -INFINITY;
+      if (i >= a.Lq) continue;
+      if (8 * l < a.D) {
+        x[n] = *reinterpret_cast<const uint4*>(o + (int64_t)i * a.o.l);
+        y[n] = *reinterpret_cast<const uint4*>(g + (int64_t)i * a.grad_o.l);
+      }
+      lse[n] = a.lse[(int64_t)bh * a.Lq + i];
     }
 #pragma unroll
-    for (int k = LANES / 2; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-    if (l == 0) {
-      const bool none = lse[n] == -INFINITY;
-      float* to = a.rows + row_at(bh, a.Lqp, r0 + n * kPass);
-      to[0] = none ? -INFINITY : -lse[n] * kLog2e;
-      to[kTileRows] = none ? 0.0f : -sum * a.inv_keep;
+    for (int n = 0; n < N; ++n) {
+      const uint32_t xs[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+      const uint32_t ys[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
+      float sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = unpack2<T>(xs[k]), e = unpack2<T>(ys[k]);
+        sum = __fmaf_rn(f.x, e.x, sum);
+        sum = __fmaf_rn(f.y, e.y, sum);
+      }
+#pragma unroll
+      for (int k = LANES / 2; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+      if (l == 0) {
+        const bool none = lse[n] == -INFINITY;
+        float* to = a.rows + row_at(bh, a.Lqp, p + n * kPass);
+        to[0] = none ? -INFINITY : -lse[n] * kLog2e;
+        to[kTileRows] = none ? 0.0f : -sum * a.inv_keep;
+      }
     }
   }
 }

@@ -7,7 +7,7 @@
 // along diagonals: a lane keeps the running sums of its columns' diagonals in
 // registers while it walks down the rows, and hands the one that leaves its
 // columns to the next lane, so an element costs one load and one addition
-// (bound: HBM reads; 32 x 12 x 512 x 512 bf16, 201 MB, in 43 us, 4.7 TB/s with
+// (bound: HBM reads; 32 x 12 x 512 x 512 bf16, 201 MB, in 42.5 us, 4.7 TB/s with
 // the launch of the second kernel).
 #include "elem.cuh"
 #include "model.cuh"
@@ -149,9 +149,15 @@ __global__ void __launch_bounds__(32 * kGradWarps, kGradResident<V>)
   constexpr int kDist = kGradRows + kWarpCols;  // distances of a warp's tile, and one spare
   __shared__ int first[OB_RELPOS_MAX_SIDE];
   __shared__ float by_d[kGradWarps][kDist];
-  __shared__ float by_b[kGradWarps][2 * OB_RELPOS_MAX_SIDE];
   extern __shared__ uint4 ring[];  // V = 8: [warp][stage][row][16-byte part][lane]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // A warp's sums by bucket: with V = 8 over its part of the ring, once that is
+  // read (else two blocks miss fitting an SM by a kilobyte).
+  __shared__ float apart[V == 8 ? 1 : kGradWarps * 2 * OB_RELPOS_MAX_SIDE];
+  constexpr int kPart = V == 8 ? kGradStages<T> * kGradBatch * (int)sizeof(T) / 2 * 32 * 4
+                               : 2 * OB_RELPOS_MAX_SIDE;  // floats
+  static_assert(kPart >= 2 * OB_RELPOS_MAX_SIDE, "");
+  float* by_b = V == 8 ? reinterpret_cast<float*>(ring) : apart;
   grid_release();
   for (int b = threadIdx.x; b < a.rp.side; b += 32 * kGradWarps) first[b] = a.rp.first[b];
   __syncthreads();
@@ -300,13 +306,13 @@ __global__ void __launch_bounds__(32 * kGradWarps, kGradResident<V>)
 #pragma unroll 4
       for (int t = (int)(lo - dmin); t < (int)(hi - dmin); ++t) sum += by_d[warp][t];
     }
-    by_b[warp][b] = sum;
+    by_b[warp * kPart + b] = sum;
   }
   __syncthreads();
   for (int b = threadIdx.x; b < a.rp.num_buckets; b += 32 * kGradWarps) {
     float sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kGradWarps; ++w) sum += by_b[w][b];
+    for (int w = 0; w < kGradWarps; ++w) sum += by_b[w * kPart + b];
     a.partial[((int64_t)h * gridDim.x + blockIdx.x) * a.rp.num_buckets + b] = sum;
   }
 }
