@@ -6,9 +6,12 @@
 // 152 SMs draw for 4.2e12 elements a second, where HBM brings at most 1.7e12
 // of the smallest type: HBM is the bound (65536 x 2048 bf16 with a residual in
 // 117.4 us, 6.86 TB/s; 16384 x 1024 in 18.5 us, 5.45 TB/s, the launch and the
-// tail included).  Arrays that are not 16-byte aligned or have rows of odd
-// lengths take an element a lane and step: 16.4 MB in 10 us, where addresses
-// and 2-byte accesses are the bound.
+// tail included).  Rows at any alignment into one aligned run are read in
+// aligned words and shifted (65536 x 2001 bf16 with a residual in 180 us,
+// 4.4 TB/s: the shifts and the rows' ends); other strides take an element a
+// lane and step, where addresses and narrow accesses are the bound (429 us).
+#include <type_traits>
+
 #include "elem.cuh"
 #include "keep.cuh"
 #include "model.cuh"
@@ -114,6 +117,97 @@ __global__ void __launch_bounds__(kDropThreads) k_dropout_vec(const DropoutArgs 
   }
 }
 
+// Eight elements from memory of any alignment: the 16-byte words that they lie
+// in (each holds one of them at least), shifted into place.
+template <typename T>
+__device__ __forceinline__ void load_shifted(Eight<T>& to, const T* p) {
+  constexpr int N = sizeof(T) / 2;
+  const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u;
+  const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) - off);
+  uint32_t w[4 * N + 4];
+#pragma unroll
+  for (int i = 0; i <= N; ++i) {
+    const uint4 v = i < N || off ? q[i] : make_uint4(0, 0, 0, 0);
+    w[4 * i] = v.x;
+    w[4 * i + 1] = v.y;
+    w[4 * i + 2] = v.z;
+    w[4 * i + 3] = v.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 4 * N + 2; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 4 * N + 1; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
+  if (sizeof(T) == 2)
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], off * 8 & 16);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    to.a[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+// Into one aligned run from rows at any alignment (a slice of a wider buffer):
+// a thread takes an aligned eight of y (fp32 two, a block apart: 4099 x 1001
+// 7.6 -> 6.7 us; with 2-byte types two cost 65536 x 2001 6%).  Eights that lie
+// across a row's end are read one by one.
+template <typename T>
+constexpr int kRunEights = sizeof(T) / 2;
+template <typename T, bool RES>
+__global__ void __launch_bounds__(kDropThreads) k_dropout_run(const DropoutArgs a) {
+  constexpr int U = kRunEights<T>;
+  const uint64_t g0 = (uint64_t)blockIdx.x * (U * kDropThreads) + threadIdx.x;
+  float v[U][8], r[U][8];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint64_t e0 = 8 * (g0 + u * kDropThreads);
+    if (e0 >= a.n) break;
+    const uint64_t row = a.small ? __umul64hi(e0, a.magic) : e0 / a.cols;
+    uint64_t c = e0 - row * a.cols;
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx + c;
+    const T* res = RES ? static_cast<const T*>(a.residual) + row * a.ldr + c : nullptr;
+    if (c + 8 <= a.cols) {
+      Eight<T> xv, rv;
+      load_shifted(xv, x);
+      if (RES) load_shifted(rv, res);
+      xv.get(v[u]);
+      if (RES) rv.get(r[u]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[u][k] = r[u][k] = 0.0f;
+        if (e0 + k >= a.n) continue;
+        v[u][k] = to_f32(*x++);
+        if (RES) r[u][k] = to_f32(*res++);
+        if (++c == a.cols) {
+          c = 0;
+          x += a.ldx - a.cols;
+          if (RES) res += a.ldr - a.cols;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint64_t g = g0 + u * kDropThreads, e0 = 8 * g;
+    if (e0 >= a.n) break;
+    uint4 w = make_uint4(~0u, ~0u, ~0u, ~0u);
+    if (a.keep.T) w = keep_words(a.keep, g);
+    float o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      o[k] = drop1(v[u][k], RES ? r[u][k] : 0.0f, kept(w, k, a.keep.T), a.keep.scale);
+    T* y = static_cast<T*>(a.y) + e0;
+    if (e0 + 8 <= a.n) {
+      Eight<T> out;
+      out.set(o);
+      out.store(y);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (e0 + k < a.n) y[k] = from_f32<T>(o[k]);
+    }
+  }
+}
+
 // Any strides and alignment: a warp takes 256 elements, lane l draws the keep
 // bits of its l-th eight, and in step k the lanes handle elements 32k..32k+31
 // (consecutive addresses) with the bits fetched from the lane that drew them.
@@ -171,16 +265,26 @@ cudaError_t launch(const DropoutArgs& a, cudaStream_t s) {
   const bool vec = aligned(a.x, a.ldx) && aligned(a.y, a.ldy) &&
                    (!a.residual || aligned(a.residual, a.ldr)) &&
                    (a.rows == 1 || a.cols % 8 == 0);
-  const uint64_t per = vec ? 16ull * kDropThreads : 8ull * kDropThreads;
+  // Rows of less than eight make every eight cross one: 4000000 x 1 63 us, with
+  // the kernel for any stride 45.  From eight on: 4099 x 1001 fp16 6.6 us
+  // instead of 10.0, 65536 x 2001 bf16 with a residual 180 instead of 429.
+  const bool run = !vec && reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.cols >= 8 &&
+                   (a.rows == 1 || a.ldy == a.cols);
+  const uint64_t per = (vec ? 16ull : run ? 8ull * kRunEights<T> : 8ull) * kDropThreads;
   const dim3 grid((unsigned)((a.n + per - 1) / per));
-  if (vec && a.residual)
-    k_dropout_vec<T, true><<<grid, kDropThreads, 0, s>>>(a);
-  else if (vec)
-    k_dropout_vec<T, false><<<grid, kDropThreads, 0, s>>>(a);
-  else if (a.residual)
-    k_dropout_any<T, true><<<grid, kDropThreads, 0, s>>>(a);
+  auto go = [&](auto with) {
+    constexpr bool kRes = decltype(with)::value;
+    if (vec)
+      k_dropout_vec<T, kRes><<<grid, kDropThreads, 0, s>>>(a);
+    else if (run)
+      k_dropout_run<T, kRes><<<grid, kDropThreads, 0, s>>>(a);
+    else
+      k_dropout_any<T, kRes><<<grid, kDropThreads, 0, s>>>(a);
+  };
+  if (a.residual)
+    go(std::true_type());
   else
-    k_dropout_any<T, false><<<grid, kDropThreads, 0, s>>>(a);
+    go(std::false_type());
   return cudaGetLastError();
 }
 

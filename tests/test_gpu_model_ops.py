@@ -81,6 +81,23 @@ def test_dropout_at_any_alignment(shift):
     _within(y, want, bound, "y")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("shift", range(8))
+def test_dropout_of_rows_at_any_alignment_into_an_aligned_run(dtype, shift):
+    """x and the residual at their own offsets and strides; the last eight is short."""
+    mk = _gen(40 + shift)
+    for rows, cols, pad in ((37, 8, 1), (91, 9, 8), (53, 131, 3), (1, 1003, 0)):
+        n = rows * (cols + pad)
+        x = mk(n + shift, dtype=dtype)[shift:].view(rows, cols + pad)[:, :cols]
+        res = mk(n + 7 - shift, dtype=dtype)[7 - shift:].view(rows, cols + pad)[:, :cols]
+        y = torch.full((rows * cols + 8,), 7.0, device="cuda", dtype=dtype)
+        for r in (res, None):
+            ob.ob_dropout(x, y[:rows * cols].view(rows, cols), 0.3, 5, 6, residual=r)
+            want, bound = _dropout_ref(x, r, 0.3, 5, 6)
+            _within(y[:rows * cols].view(rows, cols), want, bound, "y")
+            assert (y[rows * cols:] == 7.0).all(), "wrote past the end"
+
+
 def test_dropout_probabilities_and_values_that_are_dropped():
     x = torch.full((64, 1024), math.nan, device="cuda")
     kb, up = R.keep(0, x.numel(), 0.75, 3, 4)
