@@ -54,6 +54,21 @@ __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
   return __half22float2(h);
 }
 
+// The 16 bytes that start `off` bytes (0..15, whole elements) into a.
+template <typename T>
+__device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, uint32_t off) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
+  if (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], off * 8 & 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // A value of any of the types, by a run-time code (small tables only).
 __device__ __forceinline__ float load_as_f32(const void* p, size_t i, int type) {
   if (type == OB_TYPE_F32) return static_cast<const float*>(p)[i];

@@ -124,25 +124,11 @@ __device__ __forceinline__ void load_shifted(Eight<T>& to, const T* p) {
   constexpr int N = sizeof(T) / 2;
   const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u;
   const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) - off);
-  uint32_t w[4 * N + 4];
+  uint4 w[N + 1];
 #pragma unroll
-  for (int i = 0; i <= N; ++i) {
-    const uint4 v = i < N || off ? q[i] : make_uint4(0, 0, 0, 0);
-    w[4 * i] = v.x;
-    w[4 * i + 1] = v.y;
-    w[4 * i + 2] = v.z;
-    w[4 * i + 3] = v.w;
-  }
+  for (int i = 0; i <= N; ++i) w[i] = i < N || off ? q[i] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-  for (int i = 0; i < 4 * N + 2; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
-#pragma unroll
-  for (int i = 0; i < 4 * N + 1; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
-  if (sizeof(T) == 2)
-#pragma unroll
-    for (int i = 0; i < 4 * N; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], off * 8 & 16);
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    to.a[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  for (int i = 0; i < N; ++i) to.a[i] = shifted<T>(w[i], w[i + 1], off);
 }
 
 // Into one aligned run from rows at any alignment (a slice of a wider buffer):

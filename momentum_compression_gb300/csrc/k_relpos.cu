@@ -7,7 +7,7 @@
 // along diagonals: a lane keeps the running sums of its columns' diagonals in
 // registers while it walks down the rows, and hands the one that leaves its
 // columns to the next lane, so an element costs one load and one addition
-// (bound: HBM reads; 32 x 12 x 512 x 512 bf16, 201 MB, in 42.5 us, 4.7 TB/s with
+// (bound: HBM reads; 32 x 12 x 512 x 512 bf16, 201 MB, in 39 us, 5.2 TB/s with
 // the launch of the second kernel).
 #include "elem.cuh"
 #include "model.cuh"
@@ -29,7 +29,8 @@ constexpr int kMapSpan = 2048;
 
 // Block (column chunk, row strip, head).  VEC: 8 columns a thread in 16-byte
 // stores (32 for fp32), one new value a row (the other seven move up); else
-// one column a thread and step, any alignment.
+// rows at any alignment, their aligned 16 bytes read from the values in two
+// words and shifted, the ends one by one.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kBiasThreads)
     k_relpos_bias(const __grid_constant__ RelposArgs a) {
@@ -37,7 +38,8 @@ __global__ void __launch_bounds__(kBiasThreads)
   __shared__ int first[OB_RELPOS_MAX_SIDE];
   __shared__ T head[2 * OB_RELPOS_MAX_SIDE];
   __shared__ uint8_t map[kMapSpan + 1];
-  __shared__ T val[kBiasRows + kCols];
+  constexpr int E = 16 / sizeof(T);
+  alignas(16) __shared__ T val[kBiasRows + kCols + 2 * E];
   const int last = a.rp.first[a.rp.side - 1], left = last, right = a.rp.two_sided ? last : 0;
   const bool mapped = left + right <= kMapSpan;
   for (int b = threadIdx.x; b < a.rp.side; b += kBiasThreads) first[b] = a.rp.first[b];
@@ -87,10 +89,26 @@ __global__ void __launch_bounds__(kBiasThreads)
           }
         }
       } else {
-        for (int r = 0; r < nrows; ++r) {
+        const uint4* words = reinterpret_cast<const uint4*>(val);
+        // thread and step: one of the `per` words that a row may touch
+        const int per = (ncols + 2 * E - 2) / E;
+        const int rows = kBiasThreads / per, rest = kBiasThreads % per;
+        int r = threadIdx.x / per, u = threadIdx.x % per;
+#pragma unroll 2
+        while (r < nrows) {
           T* p = out + (int64_t)r * a.stride_l;
-          const T* at = val + (nrows - 1 - r);
-          for (int c = threadIdx.x; c < ncols; c += kBiasThreads) p[c] = at[c];
+          const int at = nrows - 1 - r;  // of column c0
+          const int c = E * u - (int)(reinterpret_cast<uintptr_t>(p) & 15) / (int)sizeof(T);
+          if (c >= 0 && c + E <= ncols) {
+            const int t = at + c;
+            *reinterpret_cast<uint4*>(p + c) =
+                shifted<T>(words[t / E], words[t / E + 1], t % E * (uint32_t)sizeof(T));
+          } else {
+            for (int x = max(c, 0); x < min(c + E, ncols); ++x) p[x] = val[at + x];
+          }
+          r += rows;
+          u += rest;
+          if (u >= per) u -= per, ++r;
         }
       }
     }
@@ -119,21 +137,27 @@ cudaError_t launch_bias(const RelposArgs& a, cudaStream_t s) {
 constexpr int kGradWarps = 8;
 constexpr int kGradRows = 32;  // rows of a block's strip
 
-// V columns a lane: 8 where 16-byte loads are possible (32 bytes for fp32),
-// else 1.  A warp takes kGradRows rows of 32 V columns; a block's warps lie
-// side by side over warps_c column strips (a power of two, no more than the
-// columns fill) and one below the other in the rest, and add n_per entries.
+// A warp takes kGradRows rows of a strip of columns, a block eight such tiles
+// (the strips of a row strip first), and adds n_per entries.
 //
-// V = 8: the loads go through shared memory (each lane reads back what it
-// copied itself), kGradStages batches of four rows ahead, so that a warp
-// always has some 10 KB on the way; in registers there was room for one batch,
-// and its latency stood between every two (BERT-base, 201 MB: 61 us).
-// V = 1: a batch of eight rows in registers.
-template <int V>
-constexpr int kGradResident = V == 8 ? 2 : 5;  // blocks an SM
+// kAligned: eight columns a lane, from rows of whole 16 bytes.  The loads go
+// through shared memory (a lane reads back what it copied itself), kGradStages
+// batches of four rows ahead, so that a warp always has some 10 KB on the way;
+// in registers there was room for one batch, and its latency stood between
+// every two (BERT-base, 201 MB: 61 us).
+// kShifted: the same from rows at any alignment.  A warp copies the aligned
+// 16-byte words that its columns lie in (one more than they fill), and a lane
+// shifts its own out of them.
+// kNarrow: a column a lane, a batch of eight rows in registers.
+enum GradMode { kAligned, kShifted, kNarrow };
 constexpr int kGradBatch = 4;
+// columns a lane, and blocks an SM
+__host__ __device__ constexpr int grad_cols(GradMode m) { return m == kNarrow ? 1 : 8; }
+__host__ __device__ constexpr int grad_resident(GradMode m) { return m == kNarrow ? 5 : 2; }
 template <typename T>
 constexpr int kGradStages = sizeof(T) == 2 ? 6 : 3;
+template <typename T, GradMode M>
+constexpr int kGradWords = 32 * (int)sizeof(T) / 2 + (M == kShifted ? 1 : 0);  // a row in the ring
 
 __device__ __forceinline__ void copy16_async(void* dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
@@ -142,32 +166,30 @@ __device__ __forceinline__ void copy16_async(void* dst, const void* src, bool va
                : "memory");
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(32 * kGradWarps, kGradResident<V>)
+template <typename T, GradMode M>
+__global__ void __launch_bounds__(32 * kGradWarps, grad_resident(M))
     k_relpos_grad(const __grid_constant__ RelposBwdArgs a) {
-  constexpr int kWarpCols = 32 * V;
+  constexpr bool ALIGNED = M == kAligned;
+  constexpr int V = grad_cols(M), kWarpCols = 32 * V;
   constexpr int kDist = kGradRows + kWarpCols;  // distances of a warp's tile, and one spare
   __shared__ int first[OB_RELPOS_MAX_SIDE];
   __shared__ float by_d[kGradWarps][kDist];
-  extern __shared__ uint4 ring[];  // V = 8: [warp][stage][row][16-byte part][lane]
+  extern __shared__ uint4 ring[];  // [warp][stage][row][word]; ALIGNED: a lane's words 32 apart
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // A warp's sums by bucket: with V = 8 over its part of the ring, once that is
-  // read (else two blocks miss fitting an SM by a kilobyte).
-  __shared__ float apart[V == 8 ? 1 : kGradWarps * 2 * OB_RELPOS_MAX_SIDE];
-  constexpr int kPart = V == 8 ? kGradStages<T> * kGradBatch * (int)sizeof(T) / 2 * 32 * 4
-                               : 2 * OB_RELPOS_MAX_SIDE;  // floats
+  constexpr int kWords = kGradWords<T, M>;
+  constexpr int kRing = kGradStages<T> * kGradBatch * kWords;  // of a warp
+  // A warp's sums by bucket: where there is a ring over the warp's part of it,
+  // once that is read (else two blocks miss fitting an SM by a kilobyte).
+  __shared__ float apart[M == kNarrow ? kGradWarps * 2 * OB_RELPOS_MAX_SIDE : 1];
+  constexpr int kPart = M == kNarrow ? 2 * OB_RELPOS_MAX_SIDE : 4 * kRing;
   static_assert(kPart >= 2 * OB_RELPOS_MAX_SIDE, "");
-  float* by_b = V == 8 ? reinterpret_cast<float*>(ring) : apart;
+  float* by_b = M == kNarrow ? apart : reinterpret_cast<float*>(ring);
   grid_release();
   for (int b = threadIdx.x; b < a.rp.side; b += 32 * kGradWarps) first[b] = a.rp.first[b];
   __syncthreads();
-  int bl = blockIdx.x;
-  const int bn = bl % a.blocks_n;
-  bl /= a.blocks_n;
-  const int bc = bl % a.blocks_c;
-  const int wc = a.warps_c;
-  const int64_t i0 = ((int64_t)(bl / a.blocks_c) * (kGradWarps / wc) + warp / wc) * kGradRows;
-  const int64_t c0 = ((int64_t)bc * wc + warp % wc) * kWarpCols;
+  const int bn = blockIdx.x % a.blocks_n;
+  const int64_t tile = (int64_t)(blockIdx.x / a.blocks_n) * kGradWarps + warp;
+  const int64_t i0 = tile / a.strips * kGradRows, c0 = tile % a.strips * kWarpCols;
   const int64_t n0 = (int64_t)bn * a.n_per;
   const int h = blockIdx.y;
   const int nn = (int)min((int64_t)a.n_per, a.N - n0);
@@ -175,7 +197,9 @@ __global__ void __launch_bounds__(32 * kGradWarps, kGradResident<V>)
   const int64_t c = c0 + lane * V;
   const T* p = static_cast<const T*>(a.dout) + n0 * a.stride_n + h * a.stride_h +
                i0 * a.stride_l + c;
-  const bool in = c < a.Lk;  // V = 8: Lk % 8 == 0, so all eight or none
+  const bool in = c < a.Lk;  // ALIGNED: Lk % 8 == 0, so all eight or none
+  const int mine = (int)max((int64_t)0, min((int64_t)V, a.Lk - c));  // columns of the lane
+  const uint32_t bytes = (uint32_t)max((int64_t)0, min((int64_t)kWarpCols, a.Lk - c0)) * sizeof(T);
 
   const bool live = c0 < a.Lk && i0 < a.Lq;
   if (live) {
@@ -198,25 +222,43 @@ __global__ void __launch_bounds__(32 * kGradWarps, kGradResident<V>)
 #pragma unroll
       for (int k = 0; k < V; ++k) acc[k] += v[k];
     };
-    if constexpr (V == 8) {
+    if constexpr (M != kNarrow) {
       constexpr int kParts = sizeof(T) / 2, kStages = kGradStages<T>;
-      uint4* mine = ring + warp * (kStages * kGradBatch * kParts * 32) + lane;
+      uint4* mine_ring = ring + warp * kRing;
       const int steps = (nrows + kGradBatch - 1) / kGradBatch * nn;  // a batch of one entry each
       int fr = 0, fn = 0, fs = 0;  // row, entry and stage of the next copies
       auto fetch = [&] {
         if (fr < nrows) {
           const T* q = p + (int64_t)fr * a.stride_l + (int64_t)fn * a.stride_n;
-          uint4* to = mine + fs * (kGradBatch * kParts * 32);
+          uint4* to = mine_ring + fs * (kGradBatch * kWords) + lane;
 #pragma unroll
-          for (int i = 0; i < kGradBatch; ++i)
+          for (int i = 0; i < kGradBatch; ++i) {
+            if constexpr (ALIGNED) {
 #pragma unroll
-            for (int j = 0; j < kParts; ++j) {
-              const bool valid = in && fr + i < nrows;
-              copy16_async(to + (i * kParts + j) * 32,
-                           valid ? reinterpret_cast<const uint4*>(q + i * a.stride_l) + j
-                                 : static_cast<const void*>(a.dout),
-                           valid);
+              for (int j = 0; j < kParts; ++j) {
+                const bool valid = in && fr + i < nrows;
+                copy16_async(to + i * kWords + j * 32,
+                             valid ? reinterpret_cast<const uint4*>(q + i * a.stride_l) + j
+                                   : static_cast<const void*>(a.dout),
+                             valid);
+              }
+            } else {
+              // words of the warp's columns, each of which holds one byte of them at least
+              const char* line = reinterpret_cast<const char*>(q + i * a.stride_l - lane * V);
+              const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(line) & 15u;
+              const uint32_t end = fr + i < nrows ? off + bytes : 0;
+              const char* words = line - off;
+#pragma unroll
+              for (int j = 0; j <= kParts; ++j) {
+                if (j == kParts && lane) break;
+                const uint32_t at = 16 * (lane + 32 * j);
+                copy16_async(to + i * kWords + j * 32,
+                             at < end ? words + at : reinterpret_cast<const char*>(a.dout) -
+                                            (reinterpret_cast<uintptr_t>(a.dout) & 15u),
+                             at < end);
+              }
             }
+          }
           if (++fn == nn) fn = 0, fr += kGradBatch;
         }
         if (++fs == kStages) fs = 0;
@@ -227,22 +269,39 @@ __global__ void __launch_bounds__(32 * kGradWarps, kGradResident<V>)
       int r0 = 0, n = 0, st = 0;
       for (int step = 0; step < steps; ++step) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-        const uint4* from = mine + st * (kGradBatch * kParts * 32);
+        if (!ALIGNED) __syncwarp();  // the words are other lanes' copies
+        const uint4* from =
+            mine_ring + st * (kGradBatch * kWords) + (ALIGNED ? lane : lane * kParts);
 #pragma unroll
         for (int i = 0; i < kGradBatch; ++i) {
+          uint4 w[kParts];
+          if constexpr (ALIGNED) {
+#pragma unroll
+            for (int j = 0; j < kParts; ++j) w[j] = from[i * kWords + 32 * j];
+          } else {
+            const T* line = p + (int64_t)(r0 + i) * a.stride_l + (int64_t)n * a.stride_n - lane * V;
+            const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(line) & 15u;
+            uint4 u[kParts + 1];
+#pragma unroll
+            for (int j = 0; j <= kParts; ++j) u[j] = from[i * kWords + j];
+#pragma unroll
+            for (int j = 0; j < kParts; ++j) w[j] = shifted<T>(u[j], u[j + 1], off);
+          }
           float f[8];
           if constexpr (kParts == 2) {
-            const uint4 w[2] = {from[i * 64], from[i * 64 + 32]};
             memcpy(f, w, 32);
           } else {
-            const uint4 w = from[i * 32];
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float2 g = unpack2<T>(u[k]);
               f[2 * k] = g.x;
               f[2 * k + 1] = g.y;
             }
+          }
+          if (!ALIGNED && bytes < kWarpCols * sizeof(T)) {  // the last strip: what follows a row
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = k < mine ? f[k] : 0.0f;
           }
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[i][k] = n ? v[i][k] + f[k] : f[k];
@@ -342,23 +401,48 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-template <typename T>
-cudaError_t launch_grad(const RelposBwdArgs& a, bool aligned, cudaStream_t s) {
-  const dim3 grid((unsigned)(a.blocks_l * a.blocks_c * a.blocks_n), (unsigned)a.H);
-  if (aligned) {
-    constexpr int bytes =
-        kGradWarps * kGradStages<T> * kGradBatch * (int)(sizeof(T) / 2) * 32 * (int)sizeof(uint4);
-    static PerDeviceOnce once;
-    const cudaError_t e = once.run([] {
-      return cudaFuncSetAttribute(k_relpos_grad<T, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  bytes);
-    });
-    if (e != cudaSuccess) return e;
-    k_relpos_grad<T, 8><<<grid, 32 * kGradWarps, bytes, s>>>(a);
-  } else {
-    k_relpos_grad<T, 1><<<grid, 32 * kGradWarps, 0, s>>>(a);
-  }
+template <typename T, GradMode M>
+cudaError_t launch_grad(const RelposBwdArgs& a, cudaStream_t s) {
+  constexpr int bytes = M == kNarrow ? 0
+                                     : kGradWarps * kGradStages<T> * kGradBatch *
+                                           kGradWords<T, M> * (int)sizeof(uint4);
+  static PerDeviceOnce once;
+  const cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(k_relpos_grad<T, M>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                bytes);
+  });
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)(a.blocks_t * a.blocks_n), (unsigned)a.H);
+  k_relpos_grad<T, M><<<grid, 32 * kGradWarps, bytes, s>>>(a);
   return cudaGetLastError();
+}
+
+// The form of a call: by the rows' alignment and how much of a wide strip they
+// fill.  Aligned rows: 32 x 32 x 512 x 96 bf16 35 us, narrow 63; x 40 fp32 45
+// and 24 (a wide strip costs 3.6 (fp32) to 5 columns of the card's 10^12 a
+// second, a narrow one 0.9 (2-byte loads) to 1.3).  Shifted: 32 x 12 x 511 x 511
+// bf16 61 us, narrow 231; fp32 73 and 98; 20 x 20 x 401 x 251 as long as narrow;
+// 16 x 16 x 301 x 151 bf16 28 and 18.
+GradMode grad_mode(const RelposBwdArgs& a, int out_type) {
+  const int size = out_type == OB_TYPE_F32 ? 4 : 2, wide = 32 * grad_cols(kAligned);
+  if (reinterpret_cast<uintptr_t>(a.dout) % 16 == 0 && a.Lk % 8 == 0 && a.stride_n % 8 == 0 &&
+      a.stride_h % 8 == 0 && a.stride_l % 8 == 0)
+    return a.Lk >= 24 * size ? kAligned : kNarrow;
+  return 4 * a.Lk >= 3 * ((a.Lk + wide - 1) / wide * wide) ? kShifted : kNarrow;
+}
+
+void plan(RelposBwdArgs& a, GradMode m) {
+  const int64_t cols = 32 * grad_cols(m);
+  a.strips = (a.Lk + cols - 1) / cols;
+  const int64_t tiles = (a.Lq + kGradRows - 1) / kGradRows * a.strips;
+  a.blocks_t = (tiles + kGradWarps - 1) / kGradWarps;
+  // Entries are split over as many blocks as are resident at once on 152 SMs:
+  // more would start a second wave that leaves most of the card idle.
+  int64_t split = 152 * grad_resident(m) / (a.blocks_t * a.H);
+  if (split > a.N) split = a.N;
+  if (split < 1) split = 1;
+  a.n_per = (int)((a.N + split - 1) / split);
+  a.blocks_n = (int)((a.N + a.n_per - 1) / a.n_per);
 }
 
 }  // namespace
@@ -369,32 +453,32 @@ cudaError_t launch_relpos_bias(const RelposArgs& a, int out_type, cudaStream_t s
   return launch_bias<__half>(a, s);
 }
 
-void plan_relpos_bwd(RelposBwdArgs& a, bool aligned) {
-  const int64_t strips = (a.Lk + (aligned ? 255 : 31)) / (aligned ? 256 : 32);
-  a.warps_c = 1;
-  while (a.warps_c < kGradWarps && a.warps_c < strips) a.warps_c *= 2;
-  const int64_t rows = kGradRows * (kGradWarps / a.warps_c);
-  a.blocks_l = (int)((a.Lq + rows - 1) / rows);
-  a.blocks_c = (int)((strips + a.warps_c - 1) / a.warps_c);
-  // Entries are split over as many blocks as are resident at once on 152 SMs:
-  // more would start a second wave that leaves most of the card idle.
-  const int64_t tiles = (int64_t)a.blocks_l * a.blocks_c * a.H;
-  const int64_t resident = 152 * (aligned ? kGradResident<8> : kGradResident<1>);
-  int64_t split = resident / tiles;
-  if (split > a.N) split = a.N;
-  if (split < 1) split = 1;
-  a.n_per = (int)((a.N + split - 1) / split);
-  a.blocks_n = (int)((a.N + a.n_per - 1) / a.n_per);
+int64_t relpos_bwd_blocks(const RelposBwdArgs& of) {
+  RelposBwdArgs a = of;
+  int64_t most = 0;
+  for (GradMode m : {kAligned, kNarrow}) {  // kShifted's are kAligned's
+    plan(a, m);
+    if (a.blocks_t * a.blocks_n > most) most = a.blocks_t * a.blocks_n;
+  }
+  return most;
 }
 
-cudaError_t launch_relpos_bias_bwd(const RelposBwdArgs& a, int out_type, bool aligned,
-                                   cudaStream_t s) {
-  cudaError_t e = out_type == OB_TYPE_F32    ? launch_grad<float>(a, aligned, s)
-                  : out_type == OB_TYPE_BF16 ? launch_grad<__nv_bfloat16>(a, aligned, s)
-                                             : launch_grad<__half>(a, aligned, s);
+cudaError_t launch_relpos_bias_bwd(const RelposBwdArgs& of, int out_type, cudaStream_t s) {
+  RelposBwdArgs a = of;
+  const GradMode m = grad_mode(a, out_type);
+  plan(a, m);
+  auto go = [&](auto zero) {
+    using T = decltype(zero);
+    return m == kAligned   ? launch_grad<T, kAligned>(a, s)
+           : m == kShifted ? launch_grad<T, kShifted>(a, s)
+                           : launch_grad<T, kNarrow>(a, s);
+  };
+  const cudaError_t e = out_type == OB_TYPE_F32    ? go(0.0f)
+                        : out_type == OB_TYPE_BF16 ? go(__nv_bfloat16())
+                                                   : go(__half());
   if (e != cudaSuccess) return e;
-  return launch_bucket_sums(a.partial, a.blocks_l * a.blocks_c * a.blocks_n, a.H,
-                            a.rp.num_buckets, a.dtable, a.table_type, s);
+  return launch_bucket_sums(a.partial, (int)(a.blocks_t * a.blocks_n), a.H, a.rp.num_buckets,
+                            a.dtable, a.table_type, s);
 }
 
 cudaError_t launch_bucket_sums(const float* partial, int parts, int H, int num_buckets,

@@ -39,8 +39,9 @@ struct RelposBwdArgs {
   int64_t stride_n, stride_h, stride_l;
   int H;
   int n_per;        // entries of N a block adds
-  int warps_c;      // column strips of a block
-  int blocks_l, blocks_c, blocks_n;  // blocks a head: rows x columns x entries
+  int64_t strips;   // of columns
+  int64_t blocks_t; // blocks a head: tiles x entries
+  int blocks_n;
   float* partial;   // [H][blocks][num_buckets]
   void* dtable;
   int table_type;
@@ -48,10 +49,9 @@ struct RelposBwdArgs {
 
 cudaError_t launch_dropout(const DropoutArgs& a, int type, cudaStream_t s);
 cudaError_t launch_relpos_bias(const RelposArgs& a, int out_type, cudaStream_t s);
-// Fills the block counts of `a` from its sizes and alignment.
-void plan_relpos_bwd(RelposBwdArgs& a, bool aligned);
-cudaError_t launch_relpos_bias_bwd(const RelposBwdArgs& a, int out_type, bool aligned,
-                                   cudaStream_t s);
+// The most blocks a head that the gradient of these sizes may take.
+int64_t relpos_bwd_blocks(const RelposBwdArgs& a);
+cudaError_t launch_relpos_bias_bwd(const RelposBwdArgs& a, int out_type, cudaStream_t s);
 
 // Sums partial[h][0..parts)[b] in a fixed order into dtable[b][h].
 cudaError_t launch_bucket_sums(const float* partial, int parts, int H, int num_buckets,

@@ -88,13 +88,8 @@ ob_status check_lengths(int64_t Lq, int64_t Lk, int64_t q_offset, int64_t most) 
   return OB_OK;
 }
 
-bool relpos_bwd_aligned(const ob::RelposBwdArgs& a) {
-  return aligned(a.dout, 16) && a.Lk % 8 == 0 && a.stride_n % 8 == 0 && a.stride_h % 8 == 0 &&
-         a.stride_l % 8 == 0;
-}
-
 size_t relpos_partial_bytes(const ob::RelposBwdArgs& a) {
-  return (size_t)a.blocks_l * a.blocks_c * a.blocks_n * a.H * a.rp.num_buckets * sizeof(float);
+  return (size_t)ob::relpos_bwd_blocks(a) * a.H * a.rp.num_buckets * sizeof(float);
 }
 
 // What does not depend on the arrays.
@@ -287,10 +282,7 @@ ob_status ob_relpos_workspace_bytes(const ob_relpos* rp, int64_t N, int H, int64
   a.H = H;
   a.Lq = Lq;
   a.Lk = Lk;
-  for (int al = 0; al < 2; ++al) {  // whatever dout's alignment will be
-    ob::plan_relpos_bwd(a, al);
-    if (relpos_partial_bytes(a) > *bytes) *bytes = relpos_partial_bytes(a);
-  }
+  *bytes = relpos_partial_bytes(a);
   return OB_OK;
 }
 
@@ -327,16 +319,14 @@ ob_status ob_relpos_bias_bwd(const ob_relpos* rp, const void* dout, int out_type
   a.stride_l = Lq > 1 ? stride_l : 0;
   a.dtable = dtable;
   a.table_type = table_type;
-  const bool al = relpos_bwd_aligned(a);
-  ob::plan_relpos_bwd(a, al);
-  if ((double)a.blocks_l * a.blocks_c * a.blocks_n >= 2147483648.0)
+  if (ob::relpos_bwd_blocks(a) >= 2147483648ll)
     return failf(OB_ERR_UNSUPPORTED, "relpos_bias_bwd: too many blocks");
   OB_MODEL_PTR(workspace, 16, "workspace");
   if (workspace_bytes < relpos_partial_bytes(a))
     return failf(OB_ERR_INVALID, "workspace of %zu bytes, %zu are needed", workspace_bytes,
                  relpos_partial_bytes(a));
   a.partial = static_cast<float*>(workspace);
-  return launched(ob::launch_relpos_bias_bwd(a, out_type, al, s), "relpos_bias_bwd");
+  return launched(ob::launch_relpos_bias_bwd(a, out_type, s), "relpos_bias_bwd");
 }
 
 ob_status ob_attn_workspace_bytes(const ob_attn* at, size_t* bytes) {
