@@ -199,6 +199,30 @@ def test_relpos_bias_gradient(rp, N, H, Lq, Lk, off, dtype):
             _within(dt[:, h], want, bound, f"dtable of head {h}")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("shift", [0, 1, 5])
+@pytest.mark.parametrize("N,H,Lq,Lk", [(3, 2, 70, 251), (2, 3, 37, 509), (1, 2, 33, 1003),
+                                       (2, 1, 100, 77), (5, 1, 34, 255)])
+def test_relpos_bias_gradient_of_odd_rows(N, H, Lq, Lk, shift, dtype):
+    """Rows at every alignment, with NaN before, between and after them."""
+    p = ob.ob_relpos_init(32, 128, True)
+    b = torch.from_numpy(R.buckets(Lq, Lk, 3, 32, 128, True)).cuda()
+    for pad in (0, 3):
+        ld = Lk + pad
+        whole = torch.full((N * H * Lq * ld + shift + 9,), math.nan, device="cuda", dtype=dtype)
+        dout = whole[shift:shift + N * H * Lq * ld].view(N, H, Lq, ld)[..., :Lk]
+        dout.copy_(_gen(N)(N, H, Lq, Lk))
+        dt = torch.full((32, H), 9.0, device="cuda")
+        ob.ob_relpos_bias_bwd(p, dout, dt, q_offset=3)
+        for h in range(H):
+            x = dout[:, h].double()
+            want = R.bucket_sums(x.sum(0), b, 32)
+            # as in test_relpos_bias_gradient
+            bound = (32 * N + 120) * 2.0 ** -24 * R.bucket_sums(x.abs().sum(0), b, 32)
+            bound = bound + R.UNIT[F32] * (want.abs() + bound)
+            _within(dt[:, h], want, bound, f"dtable of head {h}")
+
+
 def test_relpos_gradient_of_nothing_is_zero():
     p = ob.ob_relpos_init(32, 128, True)
     dt = torch.full((32, 4), 9.0, device="cuda")
