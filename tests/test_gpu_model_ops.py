@@ -323,6 +323,25 @@ def test_attention(name):
     _attn_check(*_attn_case(**CASES[name]))
 
 
+# Few queries: two, four or eight blocks share the keys of the same ones, some
+# of them without any.
+SHARED_KEYS = {
+    "token": dict(H=2, Lq=1, Lk=3500, D=64, causal=True, bias=ONE),
+    "token_d128": dict(B=2, H=2, Hkv=1, Lq=1, Lk=3333, D=128, kv_len=[3333, 65]),
+    "lens": dict(B=3, H=2, Hkv=1, Lq=40, Lk=1700, D=128, p=0.1, bias=ONE, causal=True,
+                 kv_len=[1700, 100, 0]),
+    "causal_offset": dict(H=2, Lq=200, Lk=1600, D=40, causal=True, q_offset=-64, p=0.1),
+    "four": dict(B=2, H=8, Lq=300, Lk=900, D=72, p=0.1, bias=T5, kv_len=[900, 333]),
+    "two": dict(H=4, Lq=1000, Lk=800, D=64),
+    "peaked": dict(H=2, Lq=130, Lk=1600, spread=8.0, p=0.1),
+}
+
+
+@pytest.mark.parametrize("name", SHARED_KEYS)
+def test_attention_of_few_queries(name):
+    _attn_check(*_attn_case(**SHARED_KEYS[name]))
+
+
 def test_attention_repeats_bit_for_bit():
     c = _attn_case(B=3, H=4, Hkv=2, Lq=300, Lk=300, p=0.1, bias=T5, kv_len=[300, 17, 200])
     a = _attn_run(*c[:5])
