@@ -148,7 +148,8 @@ constexpr int kGradRows = 32;  // rows of a block's strip
 // kShifted: the same from rows at any alignment.  A warp copies the aligned
 // 16-byte words that its columns lie in (one more than they fill), and a lane
 // shifts its own out of them.
-// kNarrow: a column a lane, a batch of eight rows in registers.
+// kNarrow: a column a lane, a batch of eight rows in registers, for 2-byte types of
+// two entries (32 x 12 x 511 x 511 bf16 231 -> 78 us; for fp32 15 -> 21 at 77 columns).
 enum GradMode { kAligned, kShifted, kNarrow };
 constexpr int kGradBatch = 4;
 // columns a lane, and blocks an SM
@@ -323,8 +324,26 @@ __global__ void __launch_bounds__(32 * kGradWarps, grad_resident(M))
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) v[i][0] = 0.0f;
         const T* q = p + (int64_t)r0 * a.stride_l;
+        int n = 0;
+        if (sizeof(T) == 2) {
 #pragma unroll 1
-        for (int n = 0; n < nn; ++n, q += a.stride_n) {
+          for (; n + 1 < nn; n += 2, q += a.stride_n) {
+            T f[2][kBatch];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (e) q += a.stride_n;
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i)
+                f[e][i] = in && r0 + i < nrows ? q[i * a.stride_l] : from_f32<T>(0.0f);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) v[i][0] += to_f32(f[e][i]);
+          }
+        }
+#pragma unroll 1
+        for (; n < nn; ++n, q += a.stride_n) {
           float f[kBatch];
 #pragma unroll
           for (int i = 0; i < kBatch; ++i)
@@ -417,18 +436,18 @@ cudaError_t launch_grad(const RelposBwdArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// The form of a call: by the rows' alignment and how much of a wide strip they
+// The form of a call: by the rows' alignment and how much of the wide strips they
 // fill.  Aligned rows: 32 x 32 x 512 x 96 bf16 35 us, narrow 63; x 40 fp32 45
-// and 24 (a wide strip costs 3.6 (fp32) to 5 columns of the card's 10^12 a
-// second, a narrow one 0.9 (2-byte loads) to 1.3).  Shifted: 32 x 12 x 511 x 511
-// bf16 61 us, narrow 231; fp32 73 and 98; 20 x 20 x 401 x 251 as long as narrow;
-// 16 x 16 x 301 x 151 bf16 28 and 18.
+// and 24.  Shifted: 32 x 12 x 511 x 511 bf16 61 us, narrow 78 (fp32 72 and 98);
+// 32 x 1001 x 1301 bf16 40 and 66; but 20 x 16 x 701 x 389 bf16 68 and 58,
+// 20 x 20 x 401 x 251 37 and 30, 32 x 16 x 300 x 151 47 and 26.
 GradMode grad_mode(const RelposBwdArgs& a, int out_type) {
   const int size = out_type == OB_TYPE_F32 ? 4 : 2, wide = 32 * grad_cols(kAligned);
   if (reinterpret_cast<uintptr_t>(a.dout) % 16 == 0 && a.Lk % 8 == 0 && a.stride_n % 8 == 0 &&
       a.stride_h % 8 == 0 && a.stride_l % 8 == 0)
     return a.Lk >= 24 * size ? kAligned : kNarrow;
-  return 4 * a.Lk >= 3 * ((a.Lk + wide - 1) / wide * wide) ? kShifted : kNarrow;
+  const int64_t strips = (a.Lk + wide - 1) / wide;
+  return strips > 1 && 6 * a.Lk >= 5 * strips * wide ? kShifted : kNarrow;
 }
 
 void plan(RelposBwdArgs& a, GradMode m) {
