@@ -590,12 +590,16 @@ def _stream_of(t, stream):
 
 
 def _scratch(nbytes, like, stream):
-    """Device scratch of one call, kept by torch's allocator until `stream` is done with it."""
+    """Device scratch of one call on `stream` (None: torch's current one).  It is made on
+    that stream: torch's allocator hands a freed block on to the next call of the stream
+    that it was made on, at once, and only that stream is sure to be done with it."""
     import torch
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    if stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
-    return ws
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
 
 
 def _rows(t, name):

@@ -1,0 +1,137 @@
+"""What the binding of the model-side operators does around the library's
+calls, without a GPU: tensors that say they are on a device, and a library
+that records its calls instead of launching."""
+import contextlib
+
+import pytest
+import torch
+
+import momentum_compression_gb300 as ob
+
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from momentum_compression_gb300 import _build
+    _build.build()
+
+
+class _Fake(torch.Tensor):
+    """A tensor in host memory that says it is on CUDA device `at`."""
+    at = 0
+
+    @property
+    def is_cuda(self):
+        return True
+
+    @property
+    def device(self):
+        return torch.device("cuda", self.at)
+
+    def get_device(self):
+        return self.at
+
+
+def _on(t, at=0):
+    t = t.as_subclass(_Fake)
+    t.at = at
+    return t
+
+
+def _zeros(*shape, dtype=BF16, at=0):
+    n = 1
+    for s in shape:
+        n *= s
+    # on a 256-byte boundary, as device memory is
+    flat = torch.zeros(n + 256, dtype=dtype)
+    skip = -flat.data_ptr() % 256 // flat.element_size()
+    return _on(flat[skip:skip + n].view(shape), at)
+
+
+class _Library:
+    """The library, whose launching calls are recorded instead: (name, arguments,
+    current device)."""
+
+    def __init__(self, real):
+        self.real, self.calls, self.current = real, [], 0
+
+    def __getattr__(self, name):
+        if name not in ("ob_dropout", "ob_relpos_bias", "ob_relpos_bias_bwd", "ob_attn_fwd",
+                        "ob_attn_bwd"):
+            return getattr(self.real, name)
+
+        def call(*args):
+            self.calls.append((name, args, self.current))
+            return ob.OB_OK
+        return call
+
+
+class _Stream:
+    def __init__(self, handle, device_index=0):
+        self.cuda_stream, self.device_index = handle, device_index
+
+
+@pytest.fixture
+def library(monkeypatch):
+    """The recording library; torch's streams and device are its own."""
+    lib = _Library(ob.lib())
+    lib.entered = []  # streams made current, innermost last
+    lib.allocated = []  # (bytes, the stream that was current)
+
+    @contextlib.contextmanager
+    def stream(s):
+        lib.entered.append(s)
+        yield
+        lib.entered.pop()
+
+    @contextlib.contextmanager
+    def device(d):
+        before, lib.current = lib.current, d
+        yield
+        lib.current = before
+
+    def empty(*shape, **kw):
+        lib.allocated.append((shape, lib.entered[-1] if lib.entered else None))
+        return _zeros(*shape, dtype=kw["dtype"], at=kw["device"].index)
+
+    monkeypatch.setattr(ob, "lib", lambda: lib)
+    monkeypatch.setattr(ob, "_raw_stream", lambda d: 0x1000 + d)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: lib.current)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: _Stream(h))
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(_Fake, "record_stream", lambda self, s: None, raising=False)
+    return lib
+
+
+def _backward_calls(stream):
+    """The two calls that take scratch of torch's allocator."""
+    q, k = _zeros(2, 40, 4, 64), _zeros(2, 48, 2, 64)
+    lse = _zeros(2, 4, 40, dtype=torch.float32)
+    rp = ob.ob_relpos_init(32, 128, True)
+    table = _zeros(32, 4)
+    yield lambda: ob.ob_attn_bwd(q, q, k, k, q, lse, q, k, k, dtable=table, relpos=rp,
+                                 table=table, stream=stream)
+    dout, dtable = _zeros(3, 4, 40, 48), _zeros(32, 4, dtype=torch.float32)
+    yield lambda: ob.ob_relpos_bias_bwd(rp, dout, dtable, stream=stream)
+
+
+@pytest.mark.parametrize("stream", [_Stream(0x77), 0x77])
+def test_scratch_belongs_to_the_stream_of_its_call(library, stream):
+    """Torch's allocator hands a freed block on within the stream it was made on: scratch
+    made on another one may still be in use there."""
+    for call in _backward_calls(stream):
+        call()
+        (shape, of), = library.allocated
+        assert of is not None and of.cuda_stream == 0x77
+        assert library.calls[-1][1][-1] == 0x77
+        library.allocated.clear()
+
+
+def test_scratch_of_the_current_stream(library):
+    for call in _backward_calls(None):
+        call()
+        assert library.allocated.pop()[1] is None
+        assert library.calls[-1][1][-1] == 0x1000
