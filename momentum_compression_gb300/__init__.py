@@ -569,24 +569,42 @@ def _type(t, name):
     return code
 
 
-def _on_device(*named):
-    for name, t in named:
-        if t is not None and not t.is_cuda:
-            _refuse(f"{name} is not a CUDA tensor")
+def _device_of(name, t, *others):
+    """The number of the CUDA device that `t` and the `others` (name, tensor) are on."""
+    at = t.get_device()
+    if at < 0:
+        _refuse(f"{name} is not a CUDA tensor")
+    for name, t in others:
+        if t.get_device() != at:
+            _refuse(f"{name} is on {t.device}, not on CUDA device {at} as the others")
+    return at
 
 
-_raw_stream = None
+_raw_stream = _current_device = None
 
 
-def _stream_of(t, stream):
-    """The stream's handle; for None, torch's current one on the tensor's device."""
-    global _raw_stream
+def _launch(fn, at, stream, *args):
+    """fn(*args, stream's handle): a call whose tensors are on device `at`, which the library
+    wants to be the current one.  stream None: torch's current one of that device."""
+    global _raw_stream, _current_device
+    if _raw_stream is None:
+        import torch
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+        _current_device = torch.cuda.current_device
     if stream is None:
-        if _raw_stream is None:
-            import torch
-            _raw_stream = torch._C._cuda_getCurrentRawStream
-        return _raw_stream(t.get_device())
-    return _stream(stream)
+        handle = _raw_stream(at)
+    else:
+        if getattr(stream, "device_index", at) != at:
+            _refuse(f"stream is of CUDA device {stream.device_index}, the tensors are on {at}")
+        handle = _stream(stream)
+    if at == _current_device():
+        status = fn(*args, handle)
+    else:
+        import torch
+        with torch.cuda.device(at):
+            status = fn(*args, handle)
+    if status:
+        _check(status)
 
 
 def _scratch(nbytes, like, stream):
@@ -634,13 +652,12 @@ def ob_dropout(x, y, p, seed, offset, residual=None, stream=None):
     type_ = _type(x, "x")
     if y.shape != shape or y.dtype != dtype:
         _refuse("y must have the shape and the type of x")
-    if not (x.is_cuda and y.is_cuda):
-        _refuse("x and y must be CUDA tensors")
+    at = _device_of("x", x, ("y", y))
     pr = None
     whole = x.is_contiguous() and y.is_contiguous()
     if residual is not None:
-        if residual.shape != shape or residual.dtype != dtype or not residual.is_cuda:
-            _refuse("residual must be a CUDA tensor of the shape and the type of x")
+        if residual.shape != shape or residual.dtype != dtype or residual.get_device() != at:
+            _refuse("residual must have the shape, the type and the device of x")
         pr = residual.data_ptr()
         whole = whole and residual.is_contiguous()
     if whole:
@@ -650,10 +667,8 @@ def ob_dropout(x, y, p, seed, offset, residual=None, stream=None):
         rows, cols, ldx = _rows(x, "x")
         ldy = _rows(y, "y")[2]
         ldr = cols if residual is None else _rows(residual, "residual")[2]
-    status = lib().ob_dropout(x.data_ptr(), ldx, pr, ldr, y.data_ptr(), ldy, rows, cols, type_, p,
-                              seed, offset, _stream_of(x, stream))
-    if status:
-        _check(status)
+    _launch(lib().ob_dropout, at, stream, x.data_ptr(), ldx, pr, ldr, y.data_ptr(), ldy, rows, cols,
+            type_, p, seed, offset)
 
 
 @functools.lru_cache(256)
@@ -678,15 +693,15 @@ def _last_contiguous(t, name):
 
 def ob_relpos_bias(relpos, table, out, q_offset=0, stream=None):
     """out[h, i, j] = table[bucket(j - i - q_offset), h] for out [H, Lq, Lk]."""
-    _on_device(("table", table), ("out", out))
+    at = _device_of("out", out, ("table", table))
     if out.dim() != 3:
         _refuse("out must be [H, Lq, Lk]")
     H, Lq, Lk = out.shape
     _check_table(table, relpos, H)
     _last_contiguous(out, "out")
-    _check(lib().ob_relpos_bias(ct.byref(relpos), table.data_ptr(), _type(table, "table"), H, Lq,
-                                Lk, q_offset, out.data_ptr(), _type(out, "out"), out.stride(0),
-                                out.stride(1), _stream_of(out, stream)))
+    _launch(lib().ob_relpos_bias, at, stream, ct.byref(relpos), table.data_ptr(),
+            _type(table, "table"), H, Lq, Lk, q_offset, out.data_ptr(), _type(out, "out"),
+            out.stride(0), out.stride(1))
 
 
 def ob_relpos_workspace_bytes(relpos, N, H, Lq, Lk):
@@ -706,7 +721,7 @@ def ob_relpos_bias_bwd(relpos, dout, dtable, q_offset=0, workspace=None, stream=
     """dtable[b, h] = the sum of dout [N, H, Lq, Lk] (or [H, Lq, Lk]) over N and the
     pairs of bucket b.  workspace: a uint8 tensor, or None for one of torch's
     allocator."""
-    _on_device(("dout", dout), ("dtable", dtable))
+    at = _device_of("dout", dout, ("dtable", dtable))
     if dout.dim() == 3:
         dout = dout.unsqueeze(0)
     if dout.dim() != 4:
@@ -718,11 +733,10 @@ def ob_relpos_bias_bwd(relpos, dout, dtable, q_offset=0, workspace=None, stream=
         workspace = _scratch(_relpos_scratch(relpos.num_buckets, relpos.max_distance,
                                              bool(relpos.two_sided), N, H, Lq, Lk), dout, stream)
     sn, sh, sl = dout.stride()[:3]
-    _check(lib().ob_relpos_bias_bwd(ct.byref(relpos), dout.data_ptr(), _type(dout, "dout"), N, H,
-                                    Lq, Lk, sn, sh, sl, q_offset, dtable.data_ptr(),
-                                    _type(dtable, "dtable"), _ptr(workspace) or None,
-                                    workspace.numel() * workspace.element_size(),
-                                    _stream_of(dout, stream)))
+    _launch(lib().ob_relpos_bias_bwd, at, stream, ct.byref(relpos), dout.data_ptr(),
+            _type(dout, "dout"), N, H, Lq, Lk, sn, sh, sl, q_offset, dtable.data_ptr(),
+            _type(dtable, "dtable"), _ptr(workspace) or None,
+            workspace.numel() * workspace.element_size())
 
 
 # ob_attn and rows of ob_heads as they lie in memory: filled at once, which
@@ -735,19 +749,22 @@ _WORD = 2 ** 64 - 1
 
 def _attn(q, k, v, queries, keys, scale, causal, q_offset, relpos, table, kv_len, p, seed, offset):
     """The ob_attn of a call, the ob_heads of q, k, v, `queries` and `keys` (arrays shaped as
-    q or as k, with their names) in this order, and the sizes."""
+    q or as k, with their names) in this order, the sizes, and the number of the device."""
     qs, ks, dtype = q.shape, k.shape, q.dtype
     if len(qs) != 4 or len(ks) != 4 or ks[0] != qs[0] or ks[3] != qs[3]:
         _refuse(f"q {tuple(qs)} and k {tuple(ks)} must be [batch, length, heads, D] of one batch "
                 "and D")
     B, Lq, H, D = qs
     _, Lk, Hkv, _ = ks
+    at = q.get_device()
+    if at < 0:
+        _refuse("q is not a CUDA tensor")
     heads = []
     for shape, arrays in ((qs, (("q", q),)), (ks, (("k", k), ("v", v))), (qs, queries), (ks, keys)):
         for name, t in arrays:
-            if t.shape != shape or t.dtype != dtype or not t.is_cuda:
+            if t.shape != shape or t.dtype != dtype or t.get_device() != at:
                 _refuse(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device} does not go with q "
-                        f"{tuple(qs)} {dtype} and k {tuple(ks)} on a CUDA device")
+                        f"{tuple(qs)} {dtype} and k {tuple(ks)} on CUDA device {at}")
             strides = t.stride()
             if strides[3] != 1 and D > 1:
                 _refuse(f"{name}: the last dimension must be contiguous")
@@ -758,14 +775,15 @@ def _attn(q, k, v, queries, keys, scale, causal, q_offset, relpos, table, kv_len
     plan = bias = lens = 0
     if table is not None:
         _check_table(table, relpos, H)
-        if table.dtype != dtype or not table.is_cuda:
-            _refuse("table must be a CUDA tensor of the type of q")
+        if table.dtype != dtype or table.get_device() != at:
+            _refuse("table must have the type and the device of q")
         plan, bias = ct.addressof(relpos), table.data_ptr()
     if kv_len is not None:
         import torch
-        if kv_len.shape != (B,) or kv_len.dtype != torch.int32 or not kv_len.is_cuda \
+        if kv_len.shape != (B,) or kv_len.dtype != torch.int32 or kv_len.get_device() != at \
                 or not kv_len.is_contiguous():
-            _refuse("kv_len must be a contiguous int32 CUDA tensor of one length a batch entry")
+            _refuse("kv_len must be a contiguous int32 tensor on the device of q, of one length a "
+                    "batch entry")
         lens = kv_len.data_ptr()
     sizes = (_type(q, "q"), B, H, Hkv, D, Lq, Lk)
     try:
@@ -774,15 +792,15 @@ def _attn(q, k, v, queries, keys, scale, causal, q_offset, relpos, table, kv_len
                        seed & _WORD, offset & _WORD)
     except (struct.error, OverflowError) as e:
         _refuse(f"an argument or a size is out of range: {e}")
-    return a, _HEADS[len(heads) // 4](*heads), sizes
+    return a, _HEADS[len(heads) // 4](*heads), sizes, at
 
 
 def _check_lse(lse, q):
     import torch
     B, Lq, H, _ = q.shape
-    if lse.shape != (B, H, Lq) or lse.dtype != torch.float32 or not lse.is_cuda \
-            or not lse.is_contiguous():
-        _refuse("lse must be a contiguous float32 CUDA tensor [batch, heads, queries]")
+    if lse.shape != (B, H, Lq) or lse.dtype != torch.float32 \
+            or lse.get_device() != q.get_device() or not lse.is_contiguous():
+        _refuse("lse must be a contiguous float32 tensor [batch, heads, queries] on the device of q")
 
 
 @functools.lru_cache(1024)
@@ -802,15 +820,13 @@ def ob_attn_fwd(q, k, v, o, lse=None, scale=None, causal=False, q_offset=None, r
     """o = dropout(softmax(scale q k^T + bias)) v for q, o [B, Lq, H, D] and k, v
     [B, Lk, Hkv, D]; lse [B, H, Lq] is what the backward pass needs.  scale: D ** -0.5
     by default; q_offset: Lk - Lq."""
-    a, heads, _ = _attn(q, k, v, (("o", o),), (), scale, causal, q_offset, relpos, table, kv_len,
-                        p, seed, offset)
+    a, heads, _, dev = _attn(q, k, v, (("o", o),), (), scale, causal, q_offset, relpos, table,
+                             kv_len, p, seed, offset)
     if lse is not None:
         _check_lse(lse, q)
     at = ct.addressof(heads)
-    status = lib().ob_attn_fwd(a, at, at + 32, at + 64, at + 96,
-                               None if lse is None else lse.data_ptr(), _stream_of(q, stream))
-    if status:
-        _check(status)
+    _launch(lib().ob_attn_fwd, dev, stream, a, at, at + 32, at + 64, at + 96,
+            None if lse is None else lse.data_ptr())
 
 
 def ob_attn_bwd(grad_o, q, k, v, o, lse, dq, dk, dv, dtable=None, scale=None, causal=False,
@@ -818,28 +834,25 @@ def ob_attn_bwd(grad_o, q, k, v, o, lse, dq, dk, dv, dtable=None, scale=None, ca
                 workspace=None, stream=None):
     """dq, dk, dv and dtable from grad_o, with the forward call's arguments, o and
     lse.  workspace: a uint8 tensor, or None for one of torch's allocator."""
-    a, heads, sizes = _attn(q, k, v, (("grad_o", grad_o), ("o", o), ("dq", dq)),
-                            (("dk", dk), ("dv", dv)), scale, causal, q_offset, relpos, table,
-                            kv_len, p, seed, offset)
+    a, heads, sizes, dev = _attn(q, k, v, (("grad_o", grad_o), ("o", o), ("dq", dq)),
+                                 (("dk", dk), ("dv", dv)), scale, causal, q_offset, relpos, table,
+                                 kv_len, p, seed, offset)
     _check_lse(lse, q)
     if dtable is not None:
         if relpos is None:
             _refuse("dtable is given, but there is no bias")
         _check_table(dtable, relpos, q.shape[2], "dtable")
-        if dtable.dtype != q.dtype or not dtable.is_cuda:
-            _refuse("dtable must be a CUDA tensor of the type of q")
+        if dtable.dtype != q.dtype or dtable.get_device() != dev:
+            _refuse("dtable must have the type and the device of q")
     if workspace is None:
         workspace = _scratch(_attn_scratch(*sizes, None if relpos is None else
                                            (relpos.num_buckets, relpos.max_distance,
                                             bool(relpos.two_sided))), q, stream)
     at = ct.addressof(heads)  # of q, k, v, grad_o, o, dq, dk, dv
-    status = lib().ob_attn_bwd(a, at + 96, at, at + 32, at + 64, at + 128, lse.data_ptr(), at + 160,
-                               at + 192, at + 224, None if dtable is None else dtable.data_ptr(),
-                               workspace.data_ptr() or None,
-                               workspace.numel() * workspace.element_size(),
-                               _stream_of(q, stream))
-    if status:
-        _check(status)
+    _launch(lib().ob_attn_bwd, dev, stream, a, at + 96, at, at + 32, at + 64, at + 128,
+            lse.data_ptr(), at + 160, at + 192, at + 224,
+            None if dtable is None else dtable.data_ptr(), workspace.data_ptr() or None,
+            workspace.numel() * workspace.element_size())
 
 
 def ob_attn_device_error(stream=None):
@@ -851,7 +864,7 @@ def ob_attn_device_error(stream=None):
 
 def ob_attn_workspace_bytes(q, k, relpos=None, table=None):
     """Bytes of scratch ob_attn_bwd needs for these shapes."""
-    a, _, _ = _attn(q, k, k, (), (), None, False, 0, relpos, table, None, 0.0, 0, 0)
+    a, _, _, _ = _attn(q, k, k, (), (), None, False, 0, relpos, table, None, 0.0, 0, 0)
     b = ct.c_size_t()
     _check(lib().ob_attn_workspace_bytes(a, ct.byref(b)))
     return b.value

@@ -97,6 +97,7 @@ def library(monkeypatch):
 
     monkeypatch.setattr(ob, "lib", lambda: lib)
     monkeypatch.setattr(ob, "_raw_stream", lambda d: 0x1000 + d)
+    monkeypatch.setattr(ob, "_current_device", lambda: lib.current, raising=False)
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: lib.current)
@@ -135,3 +136,70 @@ def test_scratch_of_the_current_stream(library):
         call()
         assert library.allocated.pop()[1] is None
         assert library.calls[-1][1][-1] == 0x1000
+
+
+# ---------------------------------------------------------------------------
+# Devices
+# ---------------------------------------------------------------------------
+
+def _calls(at=0, change=None, other=None, **kw):
+    """(name, call) of every entry point on tensors of device `at`; the argument called
+    `change` is on device `other` instead."""
+    def z(name, *shape, dtype=BF16):
+        return _zeros(*shape, dtype=dtype, at=other if name == change else at)
+
+    rp = ob.ob_relpos_init(32, 128, True)
+    x = {n: z(n, 5, 24) for n in ("x", "y", "residual")}
+    yield "ob_dropout", lambda: ob.ob_dropout(x["x"], x["y"], 0.5, 1, 2, residual=x["residual"], **kw)
+    table, out = z("table", 32, 4), z("out", 4, 40, 48)
+    yield "ob_relpos_bias", lambda: ob.ob_relpos_bias(rp, table, out, **kw)
+    dout, dtable = z("dout", 3, 4, 40, 48), z("dtable", 32, 4)
+    scratch = z("workspace", 1 << 20, dtype=torch.uint8)
+    yield "ob_relpos_bias_bwd", lambda: ob.ob_relpos_bias_bwd(rp, dout, dtable, workspace=scratch, **kw)
+    t = {n: z(n, 2, 40, 4, 64) for n in ("q", "o", "grad_o", "dq")}
+    t.update({n: z(n, 2, 48, 2, 64) for n in ("k", "v", "dk", "dv")})
+    t["lse"], t["kv_len"] = z("lse", 2, 4, 40, dtype=torch.float32), z("kv_len", 2, dtype=torch.int32)
+    call = dict(relpos=rp, table=table, kv_len=t["kv_len"], **kw)
+    yield "ob_attn_fwd", lambda: ob.ob_attn_fwd(t["q"], t["k"], t["v"], t["o"], t["lse"], **call)
+    yield "ob_attn_bwd", lambda: ob.ob_attn_bwd(
+        t["grad_o"], t["q"], t["k"], t["v"], t["o"], t["lse"], t["dq"], t["dk"], t["dv"],
+        dtable=dtable, workspace=scratch, **call)
+
+
+def test_calls_run_on_the_device_of_their_tensors(library):
+    """The library launches on the current device: the binding makes the tensors' one
+    current for the call, and leaves the caller's as it was."""
+    for at in (0, 1):
+        for name, call in _calls(at):
+            call()
+            got, args, current = library.calls[-1]
+            assert (got, current, args[-1]) == (name, at, 0x1000 + at)
+            assert library.current == 0
+
+
+OPERANDS = {
+    "ob_dropout": ("x", "y", "residual"),
+    "ob_relpos_bias": ("table", "out"),
+    "ob_relpos_bias_bwd": ("dout", "dtable"),
+    "ob_attn_fwd": ("q", "k", "v", "o", "lse", "table", "kv_len"),
+    "ob_attn_bwd": ("grad_o", "q", "k", "v", "o", "lse", "dq", "dk", "dv", "dtable", "table",
+                    "kv_len"),
+}
+
+
+@pytest.mark.parametrize("name,change", [(n, c) for n in OPERANDS for c in OPERANDS[n]])
+def test_operands_of_two_devices_are_refused(library, name, change):
+    call = dict(_calls(0, change, 1))[name]
+    with pytest.raises(ob.OBError) as e:
+        call()
+    assert e.value.status == ob.OB_ERR_INVALID and not library.calls
+
+
+def test_a_stream_of_another_device_is_refused(library):
+    for name, call in _calls(0, stream=_Stream(0x77, 1)):
+        with pytest.raises(ob.OBError) as e:
+            call()
+        assert e.value.status == ob.OB_ERR_INVALID and not library.calls, name
+    for name, call in _calls(0, stream=_Stream(0x77, 0)):
+        call()
+        assert library.calls[-1][1][-1] == 0x77
