@@ -79,31 +79,32 @@ def _inner(t):
 
 class _Attention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, table, kw):
+    def forward(ctx, q, k, v, table, kv_len, kw):
         q, k, v = _inner(q), _inner(k), _inner(v)
         o = torch.empty(q.shape, device=q.device, dtype=q.dtype)
         B, Lq, H, _ = q.shape
         lse = torch.empty(B, H, Lq, device=q.device)
-        ob_attn_fwd(q, k, v, o, lse, table=table, **kw)
-        ctx.save_for_backward(q, k, v, o, lse, table)
+        ob_attn_fwd(q, k, v, o, lse, table=table, kv_len=kv_len, **kw)
+        ctx.save_for_backward(q, k, v, o, lse, table, kv_len)
         ctx.kw = kw
         return o
 
     @staticmethod
     def backward(ctx, grad_o):
-        q, k, v, o, lse, table = ctx.saved_tensors
+        q, k, v, o, lse, table, kv_len = ctx.saved_tensors
         dq, dk, dv = (torch.empty(t.shape, device=t.device, dtype=t.dtype) for t in (q, k, v))
         dtable = torch.empty_like(table) if ctx.needs_input_grad[3] else None
         ob_attn_bwd(_inner(grad_o), q, k, v, o, lse, dq, dk, dv, dtable=dtable, table=table,
-                    **ctx.kw)
-        return dq, dk, dv, dtable, None
+                    kv_len=kv_len, **ctx.kw)
+        return dq, dk, dv, dtable, None, None
 
 
 def attention(q, k, v, table=None, relpos=None, causal=False, kv_len=None, scale=None,
               q_offset=None, p=0.0, seed=0, offset=0):
     """dropout(softmax(scale q k^T + bias)) v for q [B, Lq, H, D] and k, v
     [B, Lk, Hkv, D] in bfloat16 or float16.  table [num_buckets, H] with relpos
-    (a RelPos) adds the learned bias; kv_len (int32 [B]) masks padded keys."""
-    kw = dict(causal=causal, kv_len=kv_len, scale=scale, q_offset=q_offset, p=p, seed=seed,
+    (a RelPos) adds the learned bias; kv_len (int32 [B]) masks padded keys and must not
+    change before the backward pass."""
+    kw = dict(causal=causal, scale=scale, q_offset=q_offset, p=p, seed=seed,
               offset=offset, relpos=None if relpos is None else relpos.plan)
-    return _Attention.apply(q, k, v, None if table is None else table.contiguous(), kw)
+    return _Attention.apply(q, k, v, None if table is None else table.contiguous(), kv_len, kw)

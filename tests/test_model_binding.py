@@ -203,3 +203,57 @@ def test_a_stream_of_another_device_is_refused(library):
     for name, call in _calls(0, stream=_Stream(0x77, 0)):
         call()
         assert library.calls[-1][1][-1] == 0x77
+
+
+# ---------------------------------------------------------------------------
+# autograd
+# ---------------------------------------------------------------------------
+
+@pytest.fixture
+def autograd(monkeypatch):
+    """model.py over entry points that fill their outputs on the host."""
+    from momentum_compression_gb300 import model as M
+    seen = []
+
+    def dropout(x, y, p, seed, offset, residual=None):
+        seen.append(("dropout", x))
+        y.copy_(x * 2 if residual is None else x * 2 + residual)
+
+    def bias(plan, table, out, q_offset=0):
+        out.copy_(table[0].view(-1, 1, 1).expand_as(out))
+
+    def bias_bwd(plan, dout, dtable, q_offset=0):
+        seen.append(("bias_bwd", dout))
+        dtable.zero_()
+        dtable[0] = dout.sum((1, 2))
+
+    def fwd(q, k, v, o, lse, kv_len=None, **kw):
+        seen.append(("fwd", None if kv_len is None else kv_len.tolist()))
+        o.copy_(q)
+
+    def bwd(grad_o, q, k, v, o, lse, dq, dk, dv, dtable=None, kv_len=None, **kw):
+        seen.append(("bwd", None if kv_len is None else kv_len.tolist()))
+        for t in (dq, dk, dv, dtable):
+            if t is not None:
+                t.fill_(1.0)
+
+    for name, f in (("ob_dropout", dropout), ("ob_relpos_bias", bias),
+                    ("ob_relpos_bias_bwd", bias_bwd), ("ob_attn_fwd", fwd), ("ob_attn_bwd", bwd)):
+        monkeypatch.setattr(M, name, f)
+    return M, seen
+
+
+def _qkv(B=2):
+    return [torch.zeros(B, 8, 2, 64, dtype=BF16).requires_grad_() for _ in range(3)]
+
+
+def test_lengths_changed_before_the_backward_pass_are_noticed(autograd):
+    M, seen = autograd
+    lengths = torch.tensor([8, 4], dtype=torch.int32)
+    o = M.attention(*_qkv(), kv_len=lengths)
+    o.sum().backward()
+    assert seen == [("fwd", [8, 4]), ("bwd", [8, 4])]
+    o = M.attention(*_qkv(), kv_len=lengths)
+    lengths.copy_(torch.tensor([3, 8], dtype=torch.int32))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        o.sum().backward()
