@@ -5,8 +5,10 @@ Each function calls the ob_* entry points of the same name (their CUDA
 kernels; there is no CPU fallback) on torch's current stream.  Random
 numbers are named by (seed, offset): the backward pass draws the forward
 pass's mask again instead of storing it, so calls that must be independent
-(another layer, another step) take another offset."""
+(another layer, another step) take another offset.  Gradients are of first
+order: a graph of them (create_graph) is refused when it is differentiated."""
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (ob_attn_bwd, ob_attn_fwd, ob_dropout, ob_relpos_bias, ob_relpos_bias_bwd,
                ob_relpos_init)
@@ -32,6 +34,7 @@ class _Dropout(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         dx = None
         if ctx.needs_input_grad[0]:
@@ -56,6 +59,7 @@ class _RelPosBias(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         shape, dtype = ctx.table
         dtable = torch.empty(shape, device=dout.device, dtype=dtype)
@@ -90,6 +94,7 @@ class _Attention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_o):
         q, k, v, o, lse, table, kv_len = ctx.saved_tensors
         dq, dk, dv = (torch.empty(t.shape, device=t.device, dtype=t.dtype) for t in (q, k, v))

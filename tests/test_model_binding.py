@@ -257,3 +257,23 @@ def test_lengths_changed_before_the_backward_pass_are_noticed(autograd):
     lengths.copy_(torch.tensor([3, 8], dtype=torch.int32))
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         o.sum().backward()
+
+
+def test_second_derivatives_are_refused(autograd):
+    """The gradients come from kernels that autograd does not see into: a graph of them
+    would be cut without a word."""
+    M, _ = autograd
+    x, res = torch.ones(4, 8, requires_grad=True), torch.ones(4, 8, requires_grad=True)
+    table = torch.ones(32, 2, requires_grad=True)
+    q, k, v = _qkv()
+    for y, of in ((M.dropout(x, 0.5, 1, 2, res), x),
+                  (M.relpos_bias(table, M.RelPos(), 4, 8), table),
+                  (M.attention(q, k, v), q)):
+        w = torch.ones_like(y).requires_grad_()
+        g, = torch.autograd.grad((y * w).sum(), of, create_graph=True)
+        assert g.requires_grad
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            g.sum().backward()
+        # a first derivative is what it was
+        y = M.dropout(x, 0.5, 1, 2, res)
+        assert torch.equal(torch.autograd.grad(y.sum(), x)[0], torch.full_like(x, 2.0))
