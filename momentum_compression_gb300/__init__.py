@@ -620,6 +620,11 @@ def _scratch(nbytes, like, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
 
 
+def _check_workspace(workspace, at):
+    if workspace.get_device() != at or not workspace.is_contiguous():
+        _refuse(f"workspace must be a contiguous tensor on CUDA device {at}")
+
+
 def _rows(t, name):
     """(rows, cols, elements between rows) of a tensor whose last dimension is
     contiguous and whose leading dimensions are one run of rows."""
@@ -732,6 +737,8 @@ def ob_relpos_bias_bwd(relpos, dout, dtable, q_offset=0, workspace=None, stream=
     if workspace is None:
         workspace = _scratch(_relpos_scratch(relpos.num_buckets, relpos.max_distance,
                                              bool(relpos.two_sided), N, H, Lq, Lk), dout, stream)
+    else:
+        _check_workspace(workspace, at)
     sn, sh, sl = dout.stride()[:3]
     _launch(lib().ob_relpos_bias_bwd, at, stream, ct.byref(relpos), dout.data_ptr(),
             _type(dout, "dout"), N, H, Lq, Lk, sn, sh, sl, q_offset, dtable.data_ptr(),
@@ -848,6 +855,8 @@ def ob_attn_bwd(grad_o, q, k, v, o, lse, dq, dk, dv, dtable=None, scale=None, ca
         workspace = _scratch(_attn_scratch(*sizes, None if relpos is None else
                                            (relpos.num_buckets, relpos.max_distance,
                                             bool(relpos.two_sided))), q, stream)
+    else:
+        _check_workspace(workspace, dev)
     at = ct.addressof(heads)  # of q, k, v, grad_o, o, dq, dk, dv
     _launch(lib().ob_attn_bwd, dev, stream, a, at + 96, at, at + 32, at + 64, at + 128,
             lse.data_ptr(), at + 160, at + 192, at + 224,

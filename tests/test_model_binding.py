@@ -277,3 +277,23 @@ def test_second_derivatives_are_refused(autograd):
         # a first derivative is what it was
         y = M.dropout(x, 0.5, 1, 2, res)
         assert torch.equal(torch.autograd.grad(y.sum(), x)[0], torch.full_like(x, 2.0))
+
+
+# ---------------------------------------------------------------------------
+# Scratch that the caller brings
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("workspace", ["host", "other device", "strided"])
+def test_scratch_that_kernels_cannot_use_is_refused(library, workspace):
+    ws = {"host": torch.zeros(1 << 20, dtype=torch.uint8),
+          "other device": _zeros(1 << 20, dtype=torch.uint8, at=1),
+          "strided": _zeros(1 << 20, 2, dtype=torch.uint8)[:, 0]}[workspace]
+    q, k = _zeros(2, 40, 4, 64), _zeros(2, 48, 2, 64)
+    lse = _zeros(2, 4, 40, dtype=torch.float32)
+    rp = ob.ob_relpos_init(32, 128, True)
+    for call in (lambda: ob.ob_attn_bwd(q, q, k, k, q, lse, q, k, k, workspace=ws),
+                 lambda: ob.ob_relpos_bias_bwd(rp, _zeros(3, 4, 40, 48), _zeros(32, 4),
+                                               workspace=ws)):
+        with pytest.raises(ob.OBError) as e:
+            call()
+        assert e.value.status == ob.OB_ERR_INVALID and not library.calls
