@@ -78,7 +78,8 @@ def _inner(t):
     ok = t.stride(-1) == 1 and t.data_ptr() % 16 == 0
     for size, stride in zip(t.shape[:3], t.stride()[:3]):
         ok = ok and (size == 1 or (stride % 8 == 0 and stride >= t.shape[3]))
-    return t if ok else t.contiguous()
+    # not contiguous(): a contiguous view that starts off 16 bytes would be returned as it is
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
 
 
 class _Attention(torch.autograd.Function):

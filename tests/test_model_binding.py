@@ -297,3 +297,28 @@ def test_scratch_that_kernels_cannot_use_is_refused(library, workspace):
         with pytest.raises(ob.OBError) as e:
             call()
         assert e.value.status == ob.OB_ERR_INVALID and not library.calls
+
+
+# ---------------------------------------------------------------------------
+# Views
+# ---------------------------------------------------------------------------
+
+def test_attention_of_views_that_start_anywhere(autograd):
+    """q, k, v and the gradient may be contiguous and yet start off a 16-byte boundary:
+    the kernels get a copy that does not."""
+    M, _ = autograd
+
+    def shifted(seed):
+        g = torch.Generator()
+        g.manual_seed(seed)
+        flat = torch.randn(2 * 8 * 2 * 64 + 16, generator=g).to(BF16)
+        skip = -flat.data_ptr() % 16 // 2 + 1
+        t = flat[skip:skip + 2 * 8 * 2 * 64].view(2, 8, 2, 64)
+        assert t.is_contiguous() and t.data_ptr() % 16
+        return t
+
+    for t in (shifted(1), shifted(2).transpose(1, 2), shifted(3)[:, ::2]):
+        u = M._inner(t)
+        assert u.data_ptr() % 16 == 0 and torch.equal(u, t)
+    t = torch.zeros(2, 8, 2, 64, dtype=BF16)
+    assert M._inner(t) is t or t.data_ptr() % 16
