@@ -38,6 +38,7 @@ size_t type_bytes(int t) { return t == OB_TYPE_F32 ? 4 : 2; }
   } while (0)
 
 constexpr int64_t kMaxLen = 1ll << 30;
+constexpr int kMaxDistance = 1 << 20;
 
 // A natural number in 32-bit limbs, least significant first: just what the
 // exact bucket edges need.
@@ -74,8 +75,13 @@ Natural power_product(uint32_t x, int a, uint32_t y, int b) {
 ob_status check_relpos(const ob_relpos* rp) {
   if (!rp) return failf(OB_ERR_INVALID, "relpos is NULL");
   const int side = rp->two_sided ? rp->num_buckets / 2 : rp->num_buckets;
-  if (rp->side != side || side < 2 || side > OB_RELPOS_MAX_SIDE || rp->first[0] != 0)
-    return failf(OB_ERR_INVALID, "relpos is not one that ob_relpos_init filled");
+  bool ok = rp->side == side && side >= 2 && side <= OB_RELPOS_MAX_SIDE &&
+            rp->num_buckets == (rp->two_sided ? 2 * side : side);
+  // The edges index shared memory: as ob_relpos_init leaves them, and none else.
+  for (int b = 0; ok && b < side; ++b)
+    ok = b < side / 2 ? rp->first[b] == b
+                      : rp->first[b] >= rp->first[b - 1] && rp->first[b] <= kMaxDistance;
+  if (!ok) return failf(OB_ERR_INVALID, "relpos is not one that ob_relpos_init filled");
   return OB_OK;
 }
 
@@ -214,7 +220,7 @@ ob_status ob_relpos_init(int num_buckets, int max_distance, int two_sided, ob_re
     return failf(OB_ERR_INVALID, "num_buckets = %d must be %sin [%d, %d]", num_buckets,
                  two_sided ? "even and " : "", least, most);
   const int side = two_sided ? num_buckets / 2 : num_buckets, E = side / 2, K = side - E;
-  if (max_distance <= E || max_distance > (1 << 20))
+  if (max_distance <= E || max_distance > kMaxDistance)
     return failf(OB_ERR_INVALID, "max_distance = %d must be in (%d, 2^20]", max_distance, E);
   *rp = ob_relpos{};
   rp->num_buckets = num_buckets;

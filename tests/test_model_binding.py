@@ -2,6 +2,7 @@
 calls, without a GPU: tensors that say they are on a device, and a library
 that records its calls instead of launching."""
 import contextlib
+import ctypes as ct
 
 import pytest
 import torch
@@ -322,3 +323,55 @@ def test_attention_of_views_that_start_anywhere(autograd):
         assert u.data_ptr() % 16 == 0 and torch.equal(u, t)
     t = torch.zeros(2, 8, 2, 64, dtype=BF16)
     assert M._inner(t) is t or t.data_ptr() % 16
+
+
+# ---------------------------------------------------------------------------
+# Buckets that ob_relpos_init did not fill
+# ---------------------------------------------------------------------------
+
+def _relpos(plan=(32, 128, True), edges=(), **fields):
+    rp = ob.ob_relpos.from_buffer_copy(ob.ob_relpos_init(*plan))
+    for name, value in fields.items():
+        setattr(rp, name, value)
+    for at, value in edges:
+        rp.first[at] = value
+    return rp
+
+
+@pytest.mark.parametrize("made", [
+    dict(num_buckets=33),                        # an odd number of two sides
+    dict(num_buckets=2, side=1),
+    dict(plan=(128, 300, False), num_buckets=129, side=129),
+    dict(edges=[(0, 1)]),
+    dict(edges=[(0, -5)]),
+    dict(edges=[(15, -70000)]),                  # would index in front of the staged values
+    dict(edges=[(15, 60)]),                      # below the edge before it
+    dict(edges=[(3, 9)]),
+    dict(edges=[(15, (1 << 20) + 1)]),
+    dict(edges=[(15, 1 << 30)]),                 # twice this is no int
+    dict(edges=[(15, (1 << 31) - 1)]),
+    dict(two_sided=0),
+], ids=range(12))
+def test_buckets_made_by_hand_are_checked(made):
+    rp, L = _relpos(**made), ob.lib()
+    n = ct.c_size_t()
+    p = ct.byref(rp)
+    a = ob.ob_attn(ob.OB_TYPE_BF16, 2, 4, 2, 64, 16, 24, 0.125, 0, 0, ct.pointer(rp), 0x5000, None,
+                   0.1, 1, 2)
+    for status in (L.ob_relpos_workspace_bytes(p, 2, 4, 8, 8, ct.byref(n)),
+                   L.ob_relpos_bias(p, 0x1000, 0, 4, 8, 8, 0, 0x2000, 0, 64, 8, None),
+                   L.ob_relpos_bias_bwd(p, 0x1000, 0, 2, 4, 8, 8, 256, 64, 8, 0, 0x2000, 0, 0x3000,
+                                        1 << 30, None),
+                   L.ob_attn_workspace_bytes(ct.byref(a), ct.byref(n))):
+        assert status == ob.OB_ERR_INVALID
+
+
+def test_every_plan_passes_its_check():
+    n = ct.c_size_t()
+    for two in (False, True):
+        for nb in range(4, 257 if two else 129, 2):
+            for D in (nb, 128, 1000, 1 << 20):
+                if D > (nb // 4 if two else nb // 2):
+                    rp = ob.ob_relpos_init(nb, D, two)
+                    assert ob.lib().ob_relpos_workspace_bytes(ct.byref(rp), 1, 1, 8, 8,
+                                                              ct.byref(n)) == ob.OB_OK
