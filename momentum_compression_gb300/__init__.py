@@ -569,35 +569,34 @@ def _type(t, name):
     return code
 
 
-def _device_of(name, t, *others):
-    """The number of the CUDA device that `t` and the `others` (name, tensor) are on."""
+def _device_of(name, t, other, u):
+    """The number of the CUDA device that tensors t and u, called `name` and `other`, are on."""
     at = t.get_device()
-    if at < 0:
-        _refuse(f"{name} is not a CUDA tensor")
-    for name, t in others:
-        if t.get_device() != at:
-            _refuse(f"{name} is on {t.device}, not on CUDA device {at} as the others")
+    if at < 0 or u.get_device() != at:
+        _refuse(f"{name} and {other} must be on one CUDA device")
     return at
 
 
 _raw_stream = _current_device = None
+_devices = 0
 
 
 def _launch(fn, at, stream, *args):
     """fn(*args, stream's handle): a call whose tensors are on device `at`, which the library
     wants to be the current one.  stream None: torch's current one of that device."""
-    global _raw_stream, _current_device
+    global _raw_stream, _current_device, _devices
     if _raw_stream is None:
         import torch
         _raw_stream = torch._C._cuda_getCurrentRawStream
-        _current_device = torch.cuda.current_device
+        _current_device = torch._C._cuda_getDevice
+        _devices = torch.cuda.device_count()
     if stream is None:
         handle = _raw_stream(at)
     else:
         if getattr(stream, "device_index", at) != at:
             _refuse(f"stream is of CUDA device {stream.device_index}, the tensors are on {at}")
         handle = _stream(stream)
-    if at == _current_device():
+    if _devices == 1 or at == _current_device():
         status = fn(*args, handle)
     else:
         import torch
@@ -657,7 +656,9 @@ def ob_dropout(x, y, p, seed, offset, residual=None, stream=None):
     type_ = _type(x, "x")
     if y.shape != shape or y.dtype != dtype:
         _refuse("y must have the shape and the type of x")
-    at = _device_of("x", x, ("y", y))
+    at = x.get_device()
+    if at < 0 or y.get_device() != at:
+        _refuse("x and y must be on one CUDA device")
     pr = None
     whole = x.is_contiguous() and y.is_contiguous()
     if residual is not None:
@@ -698,7 +699,7 @@ def _last_contiguous(t, name):
 
 def ob_relpos_bias(relpos, table, out, q_offset=0, stream=None):
     """out[h, i, j] = table[bucket(j - i - q_offset), h] for out [H, Lq, Lk]."""
-    at = _device_of("out", out, ("table", table))
+    at = _device_of("out", out, "table", table)
     if out.dim() != 3:
         _refuse("out must be [H, Lq, Lk]")
     H, Lq, Lk = out.shape
@@ -726,7 +727,7 @@ def ob_relpos_bias_bwd(relpos, dout, dtable, q_offset=0, workspace=None, stream=
     """dtable[b, h] = the sum of dout [N, H, Lq, Lk] (or [H, Lq, Lk]) over N and the
     pairs of bucket b.  workspace: a uint8 tensor, or None for one of torch's
     allocator."""
-    at = _device_of("dout", dout, ("dtable", dtable))
+    at = _device_of("dout", dout, "dtable", dtable)
     if dout.dim() == 3:
         dout = dout.unsqueeze(0)
     if dout.dim() != 4:

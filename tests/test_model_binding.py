@@ -98,10 +98,10 @@ def library(monkeypatch):
 
     monkeypatch.setattr(ob, "lib", lambda: lib)
     monkeypatch.setattr(ob, "_raw_stream", lambda d: 0x1000 + d)
-    monkeypatch.setattr(ob, "_current_device", lambda: lib.current, raising=False)
+    monkeypatch.setattr(ob, "_current_device", lambda: lib.current)
+    monkeypatch.setattr(ob, "_devices", 2)
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "device", device)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: lib.current)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: _Stream(h))
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(_Fake, "record_stream", lambda self, s: None, raising=False)
