@@ -680,8 +680,11 @@ ob_status ob_relpos_bias_bwd(const ob_relpos* rp, const void* dout, int out_type
  * and, given do:
  *   dv = Z^T do,  dS = P (kept-scaled do.v - rowsum(do o)),
  *   dq = scale dS k,  dk = scale dS^T q,  dtable = dS summed by buckets.
- * A row without keys gives o = 0 and adds nothing to any gradient.  K and V
- * past kv_len are never used, whatever they hold; their dk and dv are 0.
+ * A row without keys gives o = 0 and, where q and grad_o are finite, adds
+ * nothing to any gradient.  K and V that no query sees (past kv_len; if causal,
+ * from Lq + q_offset on) are never used, whatever they hold; their dk and dv
+ * are 0.  What is not finite in a key that some queries see may reach the
+ * others of the same 128, as zero weights times it.
  * The keep bits are those of an array [B][H][Lq][Lk rounded up to a multiple
  * of 8] (offset and seed as for ob_dropout).
  * Products take the inputs' type with fp32 accumulation; softmax statistics

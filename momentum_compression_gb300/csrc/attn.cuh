@@ -45,8 +45,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 #ifdef __CUDACC__
 
-__device__ __forceinline__ int key_count(const int32_t* kv_len, int Lk, int b) {
-  return kv_len ? max(0, min(Lk, kv_len[b])) : Lk;
+// Keys of batch entry b that any query sees.  The others may hold anything: what
+// comes after them in a tile is masked, and cleared where a zero weight meets it.
+template <typename Args>
+__device__ __forceinline__ int key_count(const Args& a, int b) {
+  int n = a.kv_len ? min(a.Lk, a.kv_len[b]) : a.Lk;
+  if (a.causal) n = min(n, a.Lq + a.q_offset);
+  return max(0, n);
 }
 
 // ---------------------------------------------------------------------------

@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
         const int x0 = (DQ ? a.blocks - 1 - blk : blk) * kRows, b = bh / heads_x, hx = bh % heads_x;
         unsigned n = 0;
         if (lane == 0) n = gridDim.x + atomicAdd(a.next, 1u);
-        const int keys = key_count(a.kv_len, a.Lk, b);
+        const int keys = key_count(a, b);
         int from = 0, per;
         if (DQ) {
           int last = keys;
@@ -972,7 +972,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
             if (!ok) break;
             tmem_wait_st();
             if (DQ && keys < a.Lk && c0 + 32 > keys) {
-              // Rows of K past the length have dS = 0, but may hold anything.
+              // Rows of K past the last key have dS = 0, but may hold anything.
               const int live = max(0, keys - c0);  // of the group's 32
               for (int k = threadIdx.x & 127; k < (32 - live) * 8 * (DP / 64); k += 128) {
                 const int r = 32 * half + live + (k >> 3) % (32 - live), y = (k >> 3) / (32 - live);

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
   const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H, hk = h / (a.H / a.Hkv);
   // The last queries see the most keys: they start first, those of all heads.
   const int q0 = ((int)gridDim.y - 1 - (int)blockIdx.y) * (kGroups * kRows);
-  const int keys = key_count(a.kv_len, a.Lk, b);
+  const int keys = key_count(a, b);
   int tiles[kGroups], most = 0;
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
       for (int c = 0; c < BN / 32; ++c) tmem_st16(ts + 16 * c, p + 16 * c);
       tmem_wait_st();
       if (keys < a.Lk && j0 + BN > keys) {
-        // Rows of V past the length have weight zero, but may hold anything.
+        // Rows of V past the last key have weight zero, but may hold anything.
         const int st = n % S::kStages;
         ok = warp_wait(&bar.v_full[st], (n / S::kStages) & 1, &g_attn_error);
         if (!ok) break;

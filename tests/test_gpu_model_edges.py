@@ -9,6 +9,7 @@ import torch
 
 import model_ref as R
 import momentum_compression_gb300 as ob
+import test_gpu_model_ops as G
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +71,27 @@ def test_backward_calls_on_two_streams(handle):
     for pair in work:
         for (out, _), w in zip(pair, want):
             assert all(torch.equal(a, b) for a, b in zip(out, w))
+
+
+# ---------------------------------------------------------------------------
+# Masked places
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Lq,Lk,off,lens", [(3, 200, 50, None), (1, 1600, 700, None),
+                                            (1, 1500, 1000, [1500, 600, 0]), (300, 500, 100, None),
+                                            (150, 333, -20, [333, 100, 50]), (40, 90, -60, None)])
+def test_attention_ignores_keys_behind_the_last_query(D, Lq, Lk, off, lens):
+    """Causal: a cache longer than what is filled.  Keys that no query sees may hold
+    anything, and get no gradient."""
+    B = len(lens) if lens else 2
+    q, k, v, do, kw, _ = G._attn_case(B=B, H=4, Hkv=2, Lq=Lq, Lk=Lk, D=D, causal=True, q_offset=off,
+                                      kv_len=lens, p=0.1, bias=G.ONE)
+    clean = G._attn_run(q, k, v, do, kw)
+    end = max(0, Lq + off)
+    for t, junk in ((k, math.nan), (v, math.inf), (k, -math.inf), (v, math.nan)):
+        t[:, end:] = junk
+        dirty = G._attn_run(q, k, v, do, kw)
+        for n in clean:
+            assert torch.equal(clean[n], dirty[n]), n
+    assert (dirty["dk"][:, end:] == 0).all() and (dirty["dv"][:, end:] == 0).all()
