@@ -680,6 +680,9 @@ ob_status ob_relpos_bias_bwd(const ob_relpos* rp, const void* dout, int out_type
  * and, given do:
  *   dv = Z^T do,  dS = P (kept-scaled do.v - rowsum(do o)),
  *   dq = scale dS k,  dk = scale dS^T q,  dtable = dS summed by buckets.
+ * Finite table values past 65536 either way count as 65536 (the type's lowest
+ * value masks a bucket, and a row where all are masked is one where none is);
+ * -inf masks, and a row where it leaves nothing is a row without keys.
  * A row without keys gives o = 0 and, where q and grad_o are finite, adds
  * nothing to any gradient.  K and V that no query sees (past kv_len; if causal,
  * from Lq + q_offset on) are never used, whatever they hold; their dk and dv

@@ -85,11 +85,20 @@ __device__ __forceinline__ void stage_buckets(uint8_t* map, const ob_relpos& rp,
   for (int t = tid; t < count; t += n)
     map[t] = (uint8_t)bucket_of(rp.first, rp.side, rp.two_sided, t - s.left - kBiasMargin);
 }
+// Finite values count up to 2^16 either way.  bf16's extremes times log2(e) would
+// be infinite, and a row whose keys all have one has to come out as if it had
+// none: the difference of such a value and the row's lse, both rounded near
+// 2^16, is off by 1% of a weight, and by all of it from 2^23 on.  -inf masks.
+constexpr float kBiasLimit = 65536.0f;
 template <typename T>
 __device__ __forceinline__ void stage_bias(float* tab, const uint8_t* map, int count,
                                            const T* table, int H, int h, int tid, int n) {
 #pragma unroll 8
-  for (int t = tid; t < count; t += n) tab[t] = to_f32(table[(size_t)map[t] * H + h]) * kLog2e;
+  for (int t = tid; t < count; t += n) {
+    const float x = to_f32(table[(size_t)map[t] * H + h]);
+    const float size = fabsf(x);
+    tab[t] = (size > kBiasLimit && size < INFINITY ? copysignf(kBiasLimit, x) : x) * kLog2e;
+  }
 }
 
 // ---------------------------------------------------------------------------

@@ -95,3 +95,67 @@ def test_attention_ignores_keys_behind_the_last_query(D, Lq, Lk, off, lens):
         for n in clean:
             assert torch.equal(clean[n], dirty[n]), n
     assert (dirty["dk"][:, end:] == 0).all() and (dirty["dv"][:, end:] == 0).all()
+
+
+def _masked_table(table, rows, value):
+    t = table.clone()
+    t[list(rows)] = value
+    return t
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D,Lq,Lk", [(64, 130, 200), (128, 130, 200), (64, 1, 1500)])
+@pytest.mark.parametrize("sign", [-1, 1])
+def test_attention_where_every_bias_is_the_types_extreme(dtype, D, Lq, Lk, sign):
+    """A bias that is the same for all keys of a row changes nothing, be it the type's
+    lowest or highest value."""
+    case = dict(B=2, H=2, D=D, Lq=Lq, Lk=Lk, dtype=dtype, bias=G.T5, p=0.1, q_offset=Lk + 300,
+                kv_len=[Lk, Lk // 3])
+    q, k, v, do, kw, ref = G._attn_case(**case)
+    far = 15  # the bucket of every distance here
+    extreme = sign * torch.finfo(dtype).max
+    kw["table"] = _masked_table(kw["table"], [far], extreme)
+    got = G._attn_run(q, k, v, do, kw)
+    ref["table"] = _masked_table(ref["table"].double(), [far], 0.0)
+    want, err = R.attention(q, k, v, do, bounds=True, **ref)
+    # The forward's weights are taken relative to a row's reference, whose difference from
+    # the bias is exact: o's bound is that without a bias.  The backward's go by lse, near
+    # 2^16: its rounding (2^-8) and that of its product with log2 e (2^-8), and the two
+    # constants' own errors (2^-25 each, of 94548), make one factor of a row's weights of
+    # 1 + 0.0105 at most.  The bounds hold `unit` times the magnitudes that it multiplies.
+    G._within(got["o"], want["o"], err["o"], "o")
+    for n in ("dq", "dk", "dv"):
+        G._within(got[n], want[n], err[n] * (1 + 0.0105 / R.UNIT[dtype]), n)
+    # every row's dS sums to zero: the factor multiplies what is left of that
+    G._within(got["dtable"], want["dtable"], err["dtable"] * 1.02, "dtable")
+    base = max(-65536.0, min(65536.0, extreme))
+    assert ((got["lse"].double() - base - want["lse"]).abs() <= 0.02).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("low", ["lowest", "infinite"])
+def test_attention_where_the_bias_masks(dtype, D, low):
+    """Far buckets of the type's lowest value, or of -inf: their keys get no weight."""
+    q, k, v, do, kw, ref = G._attn_case(B=2, H=3, D=D, Lq=230, Lk=260, dtype=dtype, bias=G.T5, p=0.1,
+                                        kv_len=[260, 200])
+    value = torch.finfo(dtype).min if low == "lowest" else -math.inf
+    kw["table"] = _masked_table(kw["table"], [15, 31], value)
+    # exp(-200) is no weight either, and keeps the bounds' magnitudes small
+    ref["table"] = _masked_table(ref["table"].double(), [15, 31], -200.0)
+    got = G._attn_run(q, k, v, do, kw)
+    want, err = R.attention(q, k, v, do, bounds=True, **ref)
+    for n in err:
+        G._within(got[n], want[n], err[n], n)
+
+
+def test_attention_where_every_bias_is_minus_infinity():
+    """As a row without keys."""
+    for D in (64, 128):
+        q, k, v, do, kw, _ = G._attn_case(B=2, H=2, D=D, Lq=130, Lk=200, bias=G.T5, p=0.1,
+                                          q_offset=500)
+        kw["table"] = _masked_table(kw["table"], [15], -math.inf)
+        got = G._attn_run(q, k, v, do, kw)
+        assert (got["lse"] == -math.inf).all()
+        for n in ("o", "dq", "dk", "dv", "dtable"):
+            assert (got[n] == 0).all(), n
