@@ -24,10 +24,25 @@ class RelPos:
         self.plan = ob_relpos_init(num_buckets, max_distance, bool(two_sided))
 
 
+def _as_rows(t):
+    """t itself if it is rows that the kernels can read (the last dimension contiguous, the
+    others one run of rows that do not overlap), else a contiguous copy."""
+    if t.is_contiguous():
+        return t
+    rows, ld = 1, None
+    ok = t.dim() > 0 and (t.stride(-1) == 1 or t.shape[-1] == 1)
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size > 1:
+            ld = stride if ld is None else ld
+            ok = ok and ld >= t.shape[-1] and stride == rows * ld
+            rows *= size
+    return t if ok else t.contiguous()
+
+
 class _Dropout(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, p, seed, offset):
-        y = torch.empty_like(x)
+        y = torch.empty(x.shape, device=x.device, dtype=x.dtype)
         ob_dropout(x, y, p, seed, offset, residual=residual)
         ctx.args = (p, seed, offset)
         ctx.has_residual = residual is not None
@@ -38,16 +53,15 @@ class _Dropout(torch.autograd.Function):
     def backward(ctx, dy):
         dx = None
         if ctx.needs_input_grad[0]:
-            dy = dy.contiguous()
-            dx = torch.empty_like(dy)
-            ob_dropout(dy, dx, *ctx.args)
+            dx = torch.empty(dy.shape, device=dy.device, dtype=dy.dtype)
+            ob_dropout(_as_rows(dy), dx, *ctx.args)
         return dx, dy if ctx.has_residual else None, None, None, None
 
 
 def dropout(x, p, seed, offset, residual=None):
     """residual + dropout(x), in one pass; the mask is never stored."""
-    return _Dropout.apply(x.contiguous(), None if residual is None else residual.contiguous(), p,
-                          seed, offset)
+    return _Dropout.apply(_as_rows(x), None if residual is None else _as_rows(residual), p, seed,
+                          offset)
 
 
 class _RelPosBias(torch.autograd.Function):
@@ -63,7 +77,9 @@ class _RelPosBias(torch.autograd.Function):
     def backward(ctx, dout):
         shape, dtype = ctx.table
         dtable = torch.empty(shape, device=dout.device, dtype=dtype)
-        ob_relpos_bias_bwd(ctx.plan, dout.contiguous(), dtable, q_offset=ctx.q_offset)
+        if dout.shape[-1] > 1 and dout.stride(-1) != 1:  # the kernels read any other strides
+            dout = dout.contiguous()
+        ob_relpos_bias_bwd(ctx.plan, dout, dtable, q_offset=ctx.q_offset)
         return dtable, None, None, None, None, None
 
 

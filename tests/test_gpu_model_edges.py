@@ -159,3 +159,20 @@ def test_attention_where_every_bias_is_minus_infinity():
         assert (got["lse"] == -math.inf).all()
         for n in ("o", "dq", "dk", "dv", "dtable"):
             assert (got[n] == 0).all(), n
+
+
+def test_dropout_of_strided_rows_through_autograd():
+    """The same bits as of a contiguous copy, forward and backward."""
+    from momentum_compression_gb300 import model as M
+    for dtype in (F32, BF16):
+        wide = _gen(21)(9, 4, 150, dtype=dtype)
+        for cut in (lambda t: t[..., 5:138], lambda t: t[..., :128], lambda t: t[:, 1, 3:8],
+                    lambda t: t.transpose(0, 1), lambda t: t[..., ::2]):
+            x, res, dy = cut(wide), cut(wide * 2), cut(wide * 3)
+            runs = []
+            for make in (lambda t: t, lambda t: t.contiguous()):
+                a, r = make(x).detach().requires_grad_(), make(res).detach().requires_grad_()
+                y = M.dropout(a, 0.3, 5, 6, r)
+                runs.append((y, *torch.autograd.grad(y, (a, r), make(dy))))
+            assert all(torch.equal(a, b) for a, b in zip(*runs))
+            assert runs[0][0].is_contiguous()

@@ -375,3 +375,32 @@ def test_every_plan_passes_its_check():
                     rp = ob.ob_relpos_init(nb, D, two)
                     assert ob.lib().ob_relpos_workspace_bytes(ct.byref(rp), 1, 1, 8, 8,
                                                               ct.byref(n)) == ob.OB_OK
+
+
+def test_strided_rows_reach_the_kernels_uncopied(autograd):
+    """The kernels read rows at any stride: a slice of a wider buffer is not copied first,
+    on the way back neither."""
+    M, seen = autograd
+    wide = torch.arange(6 * 20, dtype=torch.float32).view(6, 20)
+    for x in (wide[:, 3:14], wide.view(3, 2, 20)[..., 3:14], wide[::2, :8], wide[1, 2:7],
+              wide.view(3, 2, 20)[:, :1, :9]):
+        y = M.dropout(x, 0.5, 1, 2, x)
+        assert seen[-1][1].data_ptr() == x.data_ptr() and seen[-1][1].stride() == x.stride()
+        assert y.is_contiguous() and torch.equal(y, 3 * x)
+        leaf = torch.zeros_like(x, requires_grad=True)
+        y = M.dropout(leaf, 0.5, 1, 2)
+        y.backward(x)
+        assert seen[-1][1].data_ptr() == x.data_ptr()
+        assert torch.equal(leaf.grad, 2 * x)
+    # those that are not rows are
+    for x in (wide.t(), wide[:, ::2], wide[:1].expand(6, 20), wide.view(3, 2, 20)[:, :, :7].transpose(0, 1),
+              wide[0, ::3]):
+        y = M.dropout(x, 0.5, 1, 2, x)
+        assert seen[-1][1].is_contiguous()
+        assert y.is_contiguous() and torch.equal(y, 3 * x)
+    table = torch.ones(32, 2, requires_grad=True)
+    wide = torch.arange(2 * 4 * 12, dtype=torch.float32).view(2, 4, 12)
+    for g, copied in ((wide[..., :8], False), (torch.ones(()).expand(2, 4, 8), True),
+                      (torch.ones(2, 1, 8).expand(2, 4, 8), False)):
+        M.relpos_bias(table, M.RelPos(), 4, 8).backward(g)
+        assert (seen[-1][1].data_ptr() != g.data_ptr()) == copied
