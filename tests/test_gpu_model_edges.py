@@ -176,3 +176,62 @@ def test_dropout_of_strided_rows_through_autograd():
                 runs.append((y, *torch.autograd.grad(y, (a, r), make(dy))))
             assert all(torch.equal(a, b) for a, b in zip(*runs))
             assert runs[0][0].is_contiguous()
+
+
+# ---------------------------------------------------------------------------
+# Wide plans of the bias
+# ---------------------------------------------------------------------------
+
+def _plan_of_span(span, two):
+    """A plan whose outermost buckets are `span` distances apart."""
+    last = span // 2 if two else span
+    nb = 64 if two else 32
+    for D in range(last, 4 * last):
+        if ob.ob_relpos_init(nb, D, two).first[31] == last:
+            return nb, D, two
+    raise AssertionError("no such plan")
+
+
+# the forward looks buckets up in a map up to a span of 2048, and searches beyond
+WIDE = [(32, 5000, False), (64, 3000, True), (256, 1 << 20, True), (2048, False), (2049, False),
+        (2048, True), (2050, True)]
+
+
+def _plan(p):
+    return p if len(p) == 3 else _plan_of_span(*p)
+
+
+@pytest.mark.parametrize("plan", WIDE)
+@pytest.mark.parametrize("Lq,Lk,off", [(3, 9000, 6000), (70, 4100, 2000), (1, 2056, 5000), (40, 31, 2040)])
+def test_wide_relpos_bias(plan, Lq, Lk, off):
+    plan = _plan(plan)
+    p = ob.ob_relpos_init(*plan)
+    b = torch.from_numpy(R.buckets(Lq, Lk, off, *plan)).cuda()
+    for out_type in (F32, BF16):
+        table = _gen(9)(plan[0], 2)
+        want = table.t()[:, b].to(out_type)
+        for ld in (Lk, Lk + 3):
+            whole = torch.full((2, Lq, ld), 7.0, device="cuda", dtype=out_type)
+            ob.ob_relpos_bias(p, table, whole[..., :Lk], q_offset=off)
+            assert torch.equal(whole[..., :Lk], want), (out_type, ld)
+            assert (whole[..., Lk:] == 7.0).all(), "wrote past a row"
+
+
+@pytest.mark.parametrize("plan", WIDE)
+@pytest.mark.parametrize("Lq,Lk,off", [(3, 9000, 6000), (70, 4100, 2000), (40, 31, 2040)])
+def test_wide_relpos_bias_gradient(plan, Lq, Lk, off):
+    plan, N, H = _plan(plan), 3, 2
+    p = ob.ob_relpos_init(*plan)
+    b = torch.from_numpy(R.buckets(Lq, Lk, off, *plan)).cuda()
+    for dtype, ld in ((F32, Lk), (F32, Lk + 3), (BF16, Lk), (BF16, Lk + 3)):
+        dout = _gen(N)(N, H, Lq, ld, dtype=dtype)[..., :Lk]
+        dt = torch.full((plan[0], H), 9.0, device="cuda")
+        ob.ob_relpos_bias_bwd(p, dout, dt, q_offset=off)
+        for h in range(H):
+            x = dout[:, h].double()
+            want = R.bucket_sums(x.sum(0), b, plan[0])
+            # the longest chain of additions: 32 rows of N entries down a diagonal, a bucket's
+            # 287 distances in a tile, 8 warps, at most 5 parts in a row, 32 sums
+            bound = (32 * N + 332) * 2.0 ** -24 * R.bucket_sums(x.abs().sum(0), b, plan[0])
+            bound = bound + R.UNIT[F32] * (want.abs() + bound)
+            G._within(dt[:, h], want, bound, f"dtable of head {h}")
