@@ -404,3 +404,25 @@ def test_strided_rows_reach_the_kernels_uncopied(autograd):
                       (torch.ones(2, 1, 8).expand(2, 4, 8), False)):
         M.relpos_bias(table, M.RelPos(), 4, 8).backward(g)
         assert (seen[-1][1].data_ptr() != g.data_ptr()) == copied
+
+
+def test_the_readmes_example_draws_independent_masks(monkeypatch):
+    """Its calls of several steps, one (seed, offset) each."""
+    import os
+    import re
+    from momentum_compression_gb300 import model as M
+    readme = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
+    with open(readme) as f:
+        code, = [c for c in re.findall(r"```python\n(.*?)```", f.read(), re.S) if "M.attention" in c]
+    drawn = []
+    monkeypatch.setattr(M, "ob_attn_fwd", lambda q, k, v, o, lse, **kw: drawn.append(
+        (kw["seed"], kw["offset"])))
+    monkeypatch.setattr(M, "ob_dropout", lambda x, y, p, seed, offset, residual=None: drawn.append(
+        (seed, offset)))
+    q, k, v = _qkv()
+    names = dict(q=q, k=k, v=v, lengths=torch.tensor([8, 4], dtype=torch.int32), seed=7,
+                 table=torch.zeros(32, 2, dtype=BF16), w=torch.zeros(128, 16, dtype=BF16),
+                 x=torch.zeros(2, 8, 16, dtype=BF16))
+    for step in range(4):
+        exec(code, dict(names, step=step))
+    assert len(drawn) == 8 and len(set(drawn)) == 8, drawn
