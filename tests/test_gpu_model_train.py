@@ -80,3 +80,34 @@ def test_example_learns():
     assert all(math.isfinite(x) for x in losses)
     assert abs(losses[0] - math.log(64)) < 1.0
     assert sum(losses[-10:]) / 10 < sum(losses[50:60]) / 10 < losses[0] - 0.5
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D,causal,lens,p", [(64, False, [90, 0, 33], 0.1), (128, True, None, 0.2),
+                                             (128, False, [17, 90, 90], 0.0), (72, True, [90, 5, 64], 0.1)])
+def test_autograd_of_attention_in_its_forms(dtype, D, causal, lens, p):
+    """Lengths, causality, both types, every head size's kernels, views that start anywhere:
+    within the bounds of the 64-bit definition."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(D)
+
+    def make(L, H):
+        flat = torch.randn(3 * L * (3 * H) * D + 1, generator=g, device="cuda").to(dtype)
+        wide = flat[1:].view(3, L, 3 * H, D)  # off a 16-byte boundary
+        return wide, wide[:, :, H:2 * H]
+
+    views = [make(70, 4)[1], make(90, 2)[1], make(90, 2)[1]]
+    q, k, v = (t.detach().requires_grad_() for t in views)
+    plan = (32, 128, not causal)
+    table = torch.randn(32, 4, generator=g, device="cuda").to(dtype).requires_grad_()
+    lengths = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    kw = dict(causal=causal, p=p, seed=77, offset=(1 << 32) + 3)
+    o = M.attention(q, k, v, table=table, relpos=M.RelPos(*plan), kv_len=lengths, **kw)
+    do = make(70, 4)[1]
+    got = (o.detach(), *torch.autograd.grad(o, (q, k, v, table), do))
+    assert ob.ob_attn_device_error() == 0
+    want, err = R.attention(q.detach(), k.detach(), v.detach(), do, table=table.detach(), relpos=plan,
+                            kv_len=lens, bounds=True, **kw)
+    for x, n in zip(got, ("o", "dq", "dk", "dv", "dtable")):
+        d = (x.double() - want[n]).abs()
+        assert (d <= err[n]).all(), (n, (d - err[n]).max().item())
