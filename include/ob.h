@@ -617,7 +617,9 @@ ob_status ob_codec_step(ob_ctx* ctx, int bits, uint64_t t, const void* const* gr
  * number (ties to even): the element is dropped iff u < T, a kept one is
  * scaled by 32768 / (32768 - T), so the mean is exact for the probability
  * that is really applied.  p = 0 keeps, p = 1 drops everything.  Calls that
- * must be independent take different offsets. */
+ * must be independent take different offsets.  p, seed and offset are passed
+ * by value: a CUDA graph that captured a call draws the same bits on every
+ * replay. */
 
 /* y[r][c] = residual[r][c] + (kept ? x[r][c] * scale : 0), the keep bit that
  * of element r * cols + c; residual may be NULL (0).  One rounding to the
@@ -692,7 +694,8 @@ ob_status ob_relpos_bias_bwd(const ob_relpos* rp, const void* dout, int out_type
  * of 8] (offset and seed as for ob_dropout).
  * Products take the inputs' type with fp32 accumulation; softmax statistics
  * and dtable's sums are fp32; P and dS are rounded to the type as operands of
- * their products, as is o before rowsum(do o). */
+ * their products, as is o before rowsum(do o).  In fp16 what is below 2^-24 of
+ * them is lost. */
 typedef struct {
   int type;               /* OB_TYPE_BF16 or OB_TYPE_F16: q, k, v, o, their gradients, table */
   int B, H, Hkv, D;       /* H a multiple of Hkv; D a multiple of 8, 8..128 */

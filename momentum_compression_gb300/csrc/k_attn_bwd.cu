@@ -19,7 +19,10 @@
 //   Z, dS                   from them in registers, rounded over S and dP
 //   acc1 += Z W (dv), acc2 += dS U (dq or dk)    first operand from tensor memory
 // Z and dS are rounded to the inputs' type, as the matrix unit wants them; all
-// that is summed, and the bias table's sums, are fp32.  Two tiles are in work at
+// that is summed, and the bias table's sums, are fp32.  delta is of the o that
+// was stored, rounded: the exact one would want what that rounding left as
+// another array of o's size from the forward pass, and its error in dq and dk
+// is below that of dS's rounding.  Two tiles are in work at
 // a time, each by two warpgroups (a thread a row of 32 columns), so one's
 // arithmetic runs beside the other's products: sixteen warps that work, since a
 // single one's dependent instructions leave three of four issue slots empty.

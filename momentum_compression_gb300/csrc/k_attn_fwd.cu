@@ -16,8 +16,10 @@
 // the inputs' type, as the matrix unit wants it; its row sum is of the values
 // before that, in fp32.
 //
-// What bounds it: at d 128 the matrix unit and the softmax beside it (8192
-// keys 0.83 ms, 1330 TFLOP/s; 8 x 2048 causal 0.15 ms, 914), at d 64 the
+// What bounds it: at d 128 the matrix unit and the softmax beside it, each
+// waiting for the other (8192 keys 0.83 ms, 1320 TFLOP/s, 70% of cuBLAS's; 8 x
+// 2048 causal 0.15 ms, 910, 48%: the pipe is busy in 43% of the cycles, and
+// the start and end of each block are exposed), at d 64 the
 // exponentials and the rest of a row's arithmetic (2048 keys 860 TFLOP/s),
 // with dropout the drawing of the keep bits, 72 issue cycles of a scheduler
 // for 256 pairs (32 x 12 x 512 of d 64 96 us, without dropout 59).

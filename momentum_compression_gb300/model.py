@@ -5,7 +5,8 @@ Each function calls the ob_* entry points of the same name (their CUDA
 kernels; there is no CPU fallback) on torch's current stream.  Random
 numbers are named by (seed, offset): the backward pass draws the forward
 pass's mask again instead of storing it, so calls that must be independent
-(another layer, another step) take another offset.  Gradients are of first
+(another layer, another step) take another offset.  They are values of the
+host: a CUDA graph repeats the masks that it captured.  Gradients are of first
 order: a graph of them (create_graph) is refused when it is differentiated."""
 import torch
 from torch.autograd.function import once_differentiable
@@ -84,7 +85,9 @@ class _RelPosBias(torch.autograd.Function):
 
 
 def relpos_bias(table, relpos, Lq, Lk, q_offset=0, dtype=None):
-    """The bias [H, Lq, Lk] of table [num_buckets, H] (for use outside `attention`)."""
+    """The bias [H, Lq, Lk] of table [num_buckets, H] (for use outside `attention`).
+    q_offset: the position of query 0 among the keys, 0 by default; `attention`'s default
+    is Lk - Lq."""
     return _RelPosBias.apply(table.contiguous(), relpos.plan, Lq, Lk, q_offset,
                              table.dtype if dtype is None else dtype)
 
