@@ -587,9 +587,9 @@ def _launch(fn, at, stream, *args):
     global _raw_stream, _current_device, _devices
     if _raw_stream is None:
         import torch
-        _raw_stream = torch._C._cuda_getCurrentRawStream
-        _current_device = torch._C._cuda_getDevice
         _devices = torch.cuda.device_count()
+        _current_device = torch._C._cuda_getDevice
+        _raw_stream = torch._C._cuda_getCurrentRawStream  # last: another thread may look
     if stream is None:
         handle = _raw_stream(at)
     else:

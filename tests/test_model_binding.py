@@ -426,3 +426,17 @@ def test_the_readmes_example_draws_independent_masks(monkeypatch):
     for step in range(4):
         exec(code, dict(names, step=step))
     assert len(drawn) == 8 and len(set(drawn)) == 8, drawn
+
+
+def test_the_first_call_may_come_from_two_threads(library, monkeypatch):
+    """What a call looks up once is there in full when a second thread sees that it is."""
+    monkeypatch.setattr(ob, "_raw_stream", None)
+    monkeypatch.setattr(ob, "_current_device", None)
+    monkeypatch.setattr(ob, "_devices", 0)
+    seen = []
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: seen.append(ob._raw_stream) or 1)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0x1000 + d, raising=False)
+    x = _zeros(5, 24)
+    ob.ob_dropout(x, x, 0.5, 1, 2)
+    assert seen == [None] and ob._devices == 1 and ob._current_device is not None
+    assert library.calls[-1][1][-1] == 0x1000
