@@ -694,7 +694,9 @@ ob_status ob_relpos_bias_bwd(const ob_relpos* rp, const void* dout, int out_type
  * of 8] (offset and seed as for ob_dropout).
  * Products take the inputs' type with fp32 accumulation; softmax statistics
  * and dtable's sums are fp32; P and dS are rounded to the type as operands of
- * their products, as is o before rowsum(do o).  In fp16 what is below 2^-24 of
+ * their products, as is o before rowsum(do o) where a block of 128 queries has
+ * more than 256 keys (128 in a batch with kv_len and Lk over 256; with fewer,
+ * that sum is taken from dP).  In fp16 what is below 2^-24 of
  * them is lost. */
 typedef struct {
   int type;               /* OB_TYPE_BF16 or OB_TYPE_F16: q, k, v, o, their gradients, table */

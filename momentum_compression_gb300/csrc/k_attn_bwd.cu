@@ -5,8 +5,8 @@
 //   dv = keep scale Z^T do,  dq = scale keep scale dS K,  dk = ... dS^T Q
 //   dtable[n][h] = keep scale * the sum of dS over the pairs of bucket n
 //
-// Three kernels, and a fourth for shared heads.  k_rows: -lse and -delta of
-// every query.  k_attn_grad twice: for 128 queries at a time over the keys (dq
+// Three kernels, a fourth for few keys and a fifth for shared heads.  k_rows: -lse
+// and -delta of every query.  k_attn_grad twice: for 128 queries at a time over the keys (dq
 // and the bias table's sums), and for 128 keys at a time over the queries of
 // the heads that share them (dk, dv).  Both recompute S and dP on the tensor
 // cores and need no atomics: seven products instead of the five of a single
@@ -19,10 +19,16 @@
 //   Z, dS                   from them in registers, rounded over S and dP
 //   acc1 += Z W (dv), acc2 += dS U (dq or dk)    first operand from tensor memory
 // Z and dS are rounded to the inputs' type, as the matrix unit wants them; all
-// that is summed, and the bias table's sums, are fp32.  delta is of the o that
-// was stored, rounded: the exact one would want what that rounding left as
-// another array of o's size from the forward pass, and its error in dq and dk
-// is below that of dS's rounding.  Two tiles are in work at
+// that is summed, and the bias table's sums, are fp32.
+//
+// delta is of the o that was stored: rounded, and the sum of rounded weights.
+// Over many keys o is small, and its error in dq and dk well below that of dS's
+// rounding.  Over few it is as large or larger (dq at 27 keys 1.95 times as far
+// from 64 bits as with fp32 throughout, the bias table's gradient 2.4 times; two
+// roundings are 1.42): there k_attn_grad runs a third time before the others
+// (EXACT), for delta = sum of Z dP / sum of P, and drops the scores.
+//
+// Two tiles are in work at
 // a time, each by two warpgroups (a thread a row of 32 columns), so one's
 // arithmetic runs beside the other's products: sixteen warps that work, since a
 // single one's dependent instructions leave three of four issue slots empty.
@@ -43,8 +49,9 @@
 // bias and dropout 897 TFLOP/s (five products counted) at d 128 x 8192 in
 // 3.1 ms, 668 at d 64 x 2048 in 0.51 ms; with both, at 32 x 12 x 512 of
 // d 64, 0.26 ms full (the two passes' keep bits alone are 48 us of every
-// scheduler) and 0.23 ms over ragged lengths, where the start and the end of
+// scheduler) and 0.24 ms over ragged lengths, where the start and the end of
 // the many short pieces weigh more.
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -64,6 +71,7 @@ struct GradArgs {
   int B, H, Hkv, D, Lq, Lk, causal, q_offset, biased;
   int blocks, items;  // 128-row blocks of a head; blocks * batch * heads
   int sum_bufs;       // buffers of the bias table's sums, 0: none are wanted
+  int exact_tiles;    // EXACT: the most tiles of a piece
   float scale, scale2;  // scale2 = scale * log2(e)
   ob_relpos rp;
   const void* table;
@@ -177,6 +185,7 @@ struct GradShape {
   // tensor memory: S and dP of each slot, one or two sets of accumulators
   static constexpr uint32_t kAcc = 128 * kSlots, kAccCols = DQ ? DP : 2 * DP;
   static constexpr int kAccBufs = (512 - kAcc) / kAccCols >= 2 ? 2 : 1;
+  static constexpr int kExactFloats = 2 * kGroups * kRows;  // EXACT: a buffer of its sums
   // floats of one buffer of sums: by distance for each warp, and of each
   // group's rows eps, far left and right, mass left and right
   __host__ __device__ static constexpr int sum_floats(int ndist) {
@@ -196,6 +205,13 @@ __host__ __device__ constexpr int sum_dists(int n) {
 }
 
 constexpr int kItems = 4;  // pieces handed out at a time
+
+// Tiles of keys up to which a piece's delta is worked out from the scores.  Of 60
+// drawn training calls 37 were over 1.5 times as far from 64 bits as with fp32
+// throughout when none was, of 150 two with two tiles and none with four, which
+// cost 8 x 2048 causal of d 128 542 -> 552 us.  In a batch of longer and shorter
+// entries two: 32 x 12 x 512 with lengths from 128 on 227 -> 239 us, four 250.
+constexpr int kExactTiles = 4, kExactTilesRagged = 2;
 
 struct Item {
   int x0, b, hx, keys, from, per;  // x0 < 0: no more
@@ -265,9 +281,11 @@ __device__ __forceinline__ uint32_t keep_column(const Keep& keep, uint64_t call0
   return v;
 }
 
-template <typename T, int DP, bool DQ, bool DROP>
+// EXACT (with DQ): delta alone, for pieces of at most exact_tiles tiles of keys.
+template <typename T, int DP, bool DQ, bool DROP, bool EXACT>
 __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     k_attn_grad(const __grid_constant__ GradArgs a) {
+  static_assert(DQ || !EXACT, "");
   using S = GradShape<DP, DQ>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int G = S::kGroups, K = S::kSlots;
@@ -285,12 +303,13 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
   const bool single = DQ || a.join;
   const int heads_x = single ? a.H : a.Hkv, heads = single ? 1 : group;
   float* biases = reinterpret_cast<float*>(smem + S::kBias);
-  float* sums = biases + 2 * bias_step;  // sum_bufs buffers of S::sum_floats(ndist)
+  float* sums = biases + 2 * bias_step;  // sum_bufs buffers of sum_size
+  const int sum_size = EXACT ? S::kExactFloats : S::sum_floats(ndist);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bar.item_full[i], 1);
-      mbar_init(&bar.item_empty[i], 2 + S::kWarps + (a.biased ? 1 : 0));
+      mbar_init(&bar.item_empty[i], (EXACT ? 2 : 2 + (a.biased ? 1 : 0)) + S::kWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.x_full[i], 1);
@@ -309,7 +328,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     }
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&bar.full[i], 1);
-      mbar_init(&bar.empty[i], 1);
+      mbar_init(&bar.empty[i], EXACT ? S::kWarps / 2 : 1);
     }
     fence_barrier_init();
   }
@@ -317,8 +336,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
   if (a.biased) {
     for (int i = threadIdx.x; i < a.rp.side; i += S::kThreads) bar.first[i] = a.rp.first[i];
     stage_buckets(bar.bucket, a.rp, threadIdx.x, S::kThreads);
-    for (int i = threadIdx.x; i < a.sum_bufs * S::sum_floats(ndist); i += S::kThreads)
-      sums[i] = 0.0f;
+    for (int i = threadIdx.x; i < a.sum_bufs * sum_size; i += S::kThreads) sums[i] = 0.0f;
   }
   tc_fence_before();
   __syncthreads();
@@ -355,9 +373,13 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
       while (idx < a.items) {
         // Causal: the last queries see the most keys, the first keys the most queries.
         const int blk = idx / (a.B * heads_x), bh = idx % (a.B * heads_x);
-        const int x0 = (DQ ? a.blocks - 1 - blk : blk) * kRows, b = bh / heads_x, hx = bh % heads_x;
+        const int x0 = (DQ && !EXACT ? a.blocks - 1 - blk : blk) * kRows, b = bh / heads_x,
+                  hx = bh % heads_x;
         unsigned n = 0;
-        if (lane == 0) n = gridDim.x + atomicAdd(a.next, 1u);
+        if (EXACT)  // pieces much alike, most of which may be passed over: in turn
+          n = idx + gridDim.x;
+        else if (lane == 0)
+          n = gridDim.x + atomicAdd(a.next, 1u);
         const int keys = key_count(a, b);
         int from = 0, per;
         if (DQ) {
@@ -369,10 +391,11 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           per = x0 < keys ? max(0, (a.Lq + kTileRows - 1) / kTileRows - from) : 0;
         }
         idx = (int)__shfl_sync(0xffffffffu, n, 0);
-        if (per > 0) {
+        if (per > 0 && (!EXACT || per <= a.exact_tiles)) {
           it = Item{x0, b, hx, keys, from, per};
           break;
         }
+        if (EXACT) continue;
         // 16 bytes a lane, as many rows at a time as a warp has lanes for.
         const int chunks = a.D / 8, each = 32 / chunks, d = lane % chunks * 8;
         const int rows = lane < each * chunks ? min(kRows, (DQ ? a.Lq : a.Lk) - x0) : 0;
@@ -518,7 +541,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     // Nothing may arrive after the block's end.
     mma_commit(leader, &bar.drain[0]);
     mbar_wait(&bar.drain[0], 0, a.err, kErrDrain);
-  } else if (warp == kProducts) {
+  } else if (warp == kProducts && !EXACT) {
     // ----- the accumulators -----------------------------------------------------
     constexpr uint32_t kShapeA = mma_shape(kBf16, DP, true);
     const uint32_t leader = elect_lane();
@@ -558,7 +581,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
     mbar_wait(&bar.drain[1], 0, a.err, kErrDrain);
   } else if (warp > kCopies) {
     // ----- helper: the biases ahead, the bias table's sums behind -----------------
-    if (a.biased) {
+    if (EXACT || a.biased) {
       int k = 0, nb = 0;  // pieces taken, biases staged
       bool ok = true;
       Item it, prev;
@@ -572,11 +595,11 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
         return make_int2((int)lo, (int)hi);
       };
       int2 mine = make_int2(0, 0);
-      if (DQ && a.sum_bufs && lane < a.rp.num_buckets) mine = distances(lane);
+      if (DQ && !EXACT && a.sum_bufs && lane < a.rp.num_buckets) mine = distances(lane);
       while (ok && (have || had)) {
         if (have) {
           ++k;
-          for (int hh = 0; ok && hh < heads; ++hh, ++nb) {
+          for (int hh = 0; ok && a.biased && hh < heads; ++hh, ++nb) {
             if (nb >= 2)
               ok = warp_wait(&bar.bias_empty[nb & 1], (nb / 2 + 1) & 1, a.err, kErrWaitEmpty);
             if (!ok) break;
@@ -587,14 +610,33 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
             if (lane == 0) mbar_arrive(&bar.bias_full[nb & 1]);
           }
         }
-        if (had && ok && DQ && a.sum_bufs) {
+        if (EXACT && had && ok) {
           const int sb = done % a.sum_bufs;
           ok = warp_wait(&bar.sums_full[sb], (done / a.sum_bufs) & 1, a.err);
           if (!ok) break;
-          float* by_d = sums + sb * S::sum_floats(ndist);
+          const float* row = sums + sb * sum_size;  // [sum of P, of Z dP][G][kRows]
+          for (int r = lane; r < kRows; r += 32) {
+            float v[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int g = 0; g < G; ++g) v[i] += row[(i * G + g) * kRows + r];
+            // Rows of no weight (past Lq, without keys) keep the 0 of k_rows.
+            if (v[0] != 0.0f)
+              a.rows[row_at(prev.b * a.H + prev.hx, a.Lqp, prev.x0 + r) + kTileRows] = -v[1] / v[0];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.sums_empty[sb]);
+          ++done;
+        }
+        if (!EXACT && had && ok && DQ && a.sum_bufs) {
+          const int sb = done % a.sum_bufs;
+          ok = warp_wait(&bar.sums_full[sb], (done / a.sum_bufs) & 1, a.err);
+          if (!ok) break;
+          float* by_d = sums + sb * sum_size;
           float* row = by_d + S::kWarps * ndist;  // [5][G][kRows]
           // A row's dS sums to zero; what it sums to is the error of rowsum(do o),
-          // taken from the rounded o.  It is taken out of the far buckets, whose
+          // where that is of the rounded o.  It is taken out of the far buckets, whose
           // weight would multiply it.
           float far_l = 0.0f, far_r = 0.0f;
           for (int r = lane; r < kRows; r += 32) {
@@ -667,7 +709,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
                 from_f32<T>((sum[0] + sum[1]) + (sum[2] + sum[3]));
           }
     }
-  } else {
+  } else if (!EXACT || warp < kScores) {
     // ----- arithmetic: a thread a row of X ----------------------------------
     const int g = warp >> 2, half = g & 1, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -777,7 +819,7 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
           if (k >= a.sum_bufs)
             ok = warp_wait(&bar.sums_empty[sb], (k / a.sum_bufs + 1) & 1, a.err, kErrWaitEmpty);
           if (!ok) break;
-          by_d = sums + sb * S::sum_floats(ndist);
+          by_d = sums + sb * sum_size;
         }
         for (int hh = 0; ok && hh < heads; ++hh) {
           const float* bias = biases + (nb & 1) * bias_step;
@@ -900,10 +942,14 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
                   }
                   const uint64_t pp = pair(p[2 * k], p[2 * k + 1]);
                   float &d0 = ds[2 * k], &d1 = ds[2 * k + 1];
-                  unpair(fma2(pair(z[2 * k], z[2 * k + 1]), pair(vp[2 * k], vp[2 * k + 1]),
-                              mul2(pp, nd)),
-                         &d0, &d1);
-                  if (DQ && !kSeveral) mass = add2(mass, pp);
+                  if constexpr (EXACT)
+                    unpair(mul2(pair(z[2 * k], z[2 * k + 1]), pair(vp[2 * k], vp[2 * k + 1])), &d0,
+                           &d1);
+                  else
+                    unpair(fma2(pair(z[2 * k], z[2 * k + 1]), pair(vp[2 * k], vp[2 * k + 1]),
+                                mul2(pp, nd)),
+                           &d0, &d1);
+                  if (EXACT || (DQ && !kSeveral)) mass = add2(mass, pp);
                   if (kMask) {
                     const int n = col + 2 * k;
                     d0 = (DQ ? n < limit : n >= limit) ? d0 : 0.0f;
@@ -911,21 +957,26 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
                   }
                   if (DQ) sum2 = add2(sum2, pair(d0, d1));
                 }
-                uint32_t o[8];
-                if (!DQ) {
+                if (!EXACT) {
+                  uint32_t o[8];
+                  if (!DQ) {
 #pragma unroll
-                  for (int k = 0; k < 8; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
-                  tmem_st8(ts + 8 * c, o);
+                    for (int k = 0; k < 8; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
+                    tmem_st8(ts + 8 * c, o);
+                  }
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) o[k] = pack2<T>(ds[2 * k], ds[2 * k + 1]);
+                  tmem_st8(tp + 8 * c, o);
                 }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) o[k] = pack2<T>(ds[2 * k], ds[2 * k + 1]);
-                tmem_st8(tp + 8 * c, o);
                 if (DQ && a.sum_bufs) {
                   float s0, s1;
                   unpair(sum2, &s0, &s1);
                   const float sum = s0 + s1;
                   eps += sum;
-                  if (!kSeveral && !(kMask && near)) {
+                  if (EXACT) {
+                    unpair(mass, &s0, &s1);
+                    mass_l += s0 + s1;
+                  } else if (!kSeveral && !(kMask && near)) {
                     unpair(mass, &s0, &s1);
                     if (low >= span.right) {
                       far_r += sum;
@@ -973,6 +1024,12 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
               kept >>= 16;
             }
             if (!ok) break;
+            if constexpr (EXACT) {  // the scores have been read: their place and the stage are free
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bar.empty[st]);
+              continue;
+            }
             tmem_wait_st();
             if (DQ && keys < a.Lk && c0 + 32 > keys) {
               // Rows of K past the last key have dS = 0, but may hold anything.
@@ -1000,16 +1057,21 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
         }
         nt += heads * it.per;
         if (DQ && a.sum_bufs && ok) {
-          float* r = by_d + S::kWarps * ndist + g * kRows + row;
-          const float v[5] = {eps, far_l, far_r, mass_l, mass_r};
+          if constexpr (EXACT) {
+            by_d[g * kRows + row] = mass_l;
+            by_d[(G + g) * kRows + row] = eps;
+          } else {
+            float* r = by_d + S::kWarps * ndist + g * kRows + row;
+            const float v[5] = {eps, far_l, far_r, mass_l, mass_r};
 #pragma unroll
-          for (int i = 0; i < 5; ++i) r[i * G * kRows] = v[i];
+            for (int i = 0; i < 5; ++i) r[i * G * kRows] = v[i];
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.sums_full[k % a.sum_bufs]);
         }
       }
       if (ok && pending) finish(k - 1);
-      pending = have;
+      pending = have && !EXACT;
       if (!ok || !have) break;
       __syncwarp();
       if (lane == 0) bar.done[warp] = it;
@@ -1025,13 +1087,30 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
   if (!DQ) grid_wait();  // so that this grid's end is that of all before it
 }
 
-template <typename T, int DP, bool DQ, bool DROP>
+int blocks_of(int L) { return (L + kRows - 1) / kRows; }
+
+int exact_tiles(const AttnArgs& a) {
+  return a.kv_len && a.Lk > kExactTiles * kTileRows ? kExactTilesRagged : kExactTiles;
+}
+
+// The first blocks of 128 queries, those that may have pieces for EXACT: all,
+// where an entry may be short; else, with a causal mask, the first queries.
+int exact_blocks(const AttnArgs& a) {
+  const int most = exact_tiles(a) * kTileRows, blocks = a.Lk ? blocks_of(a.Lq) : 0;
+  if (a.Lk <= most || a.kv_len) return blocks;
+  if (!a.causal) return 0;
+  // block i ends at query min(128 (i + 1), Lq), which sees q_offset keys more
+  if (a.Lq + a.q_offset <= most) return blocks;
+  return a.q_offset < most ? std::min(blocks, (most - a.q_offset) / kRows) : 0;
+}
+
+template <typename T, int DP, bool DQ, bool DROP, bool EXACT>
 cudaError_t grad_of(const AttnArgs& a, GradArgs f, cudaStream_t s) {
   using S = GradShape<DP, DQ>;
   const int Lx = DQ ? a.Lq : a.Lk, Hx = DQ ? a.H : a.Hkv;
   f.out1 = DQ ? a.dq : a.dv;
   f.out2 = DQ ? a.dq : a.dk;
-  f.blocks = (Lx + kRows - 1) / kRows;
+  f.blocks = EXACT ? exact_blocks(a) : (Lx + kRows - 1) / kRows;
   f.items = f.blocks * a.B * (f.join ? a.H : Hx);
   f.next += DQ ? 0 : 1;
   constexpr size_t most = 227 * 1024 - 256 - sizeof(GradBars<S::kWarps, S::kStages>);
@@ -1039,7 +1118,7 @@ cudaError_t grad_of(const AttnArgs& a, GradArgs f, cudaStream_t s) {
   if (a.biased) {
     const int n = bias_floats(a.rp);
     bytes += 2 * bias_room(n) * sizeof(float);
-    if (DQ && f.dtable) {
+    if (DQ && !EXACT && f.dtable) {
       // Two buffers, so that the sums of a piece are added up beside the next
       // one; a wide bias may leave room for one.
       const size_t one = S::sum_floats(sum_dists(n)) * sizeof(float);
@@ -1047,12 +1126,18 @@ cudaError_t grad_of(const AttnArgs& a, GradArgs f, cudaStream_t s) {
       bytes += f.sum_bufs * one;
     }
   }
-  constexpr size_t widest = S::sum_floats(sum_dists(kBiasMost)) * sizeof(float);
+  if (EXACT) {
+    f.exact_tiles = exact_tiles(a);
+    f.sum_bufs = 2;
+    bytes += f.sum_bufs * S::kExactFloats * sizeof(float);
+  }
+  constexpr size_t widest = EXACT ? 2 * S::kExactFloats * sizeof(float)
+                                  : S::sum_floats(sum_dists(kBiasMost)) * sizeof(float);
   static_assert(1024 + S::kBias + 8 * bias_room(kBiasMost) + (DQ ? widest : 0) <= most,
                 "the widest bias must fit");
   static PerDeviceOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(k_attn_grad<T, DP, DQ, DROP>,
+    return cudaFuncSetAttribute(k_attn_grad<T, DP, DQ, DROP, EXACT>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   });
   if (e != cudaSuccess) return e;
@@ -1060,22 +1145,22 @@ cudaError_t grad_of(const AttnArgs& a, GradArgs f, cudaStream_t s) {
   e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  return launch_behind(k_attn_grad<T, DP, DQ, DROP>, dim3(f.items < sms ? f.items : sms),
+  return launch_behind(k_attn_grad<T, DP, DQ, DROP, EXACT>, dim3(f.items < sms ? f.items : sms),
                        dim3(S::kThreads), bytes, s, f);
 }
 
-template <typename T, bool DQ>
+template <typename T, bool DQ, bool EXACT = false>
 cudaError_t grad(const AttnArgs& a, const GradArgs& f, cudaStream_t s) {
   if (a.D <= 64)
-    return a.keep.T ? grad_of<T, 64, DQ, true>(a, f, s) : grad_of<T, 64, DQ, false>(a, f, s);
-  return a.keep.T ? grad_of<T, 128, DQ, true>(a, f, s) : grad_of<T, 128, DQ, false>(a, f, s);
+    return a.keep.T ? grad_of<T, 64, DQ, true, EXACT>(a, f, s)
+                    : grad_of<T, 64, DQ, false, EXACT>(a, f, s);
+  return a.keep.T ? grad_of<T, 128, DQ, true, EXACT>(a, f, s)
+                  : grad_of<T, 128, DQ, false, EXACT>(a, f, s);
 }
 
 constexpr size_t kCounterBytes = 256;
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-
-int blocks_of(int L) { return (L + kRows - 1) / kRows; }
 
 size_t rows_bytes(const AttnArgs& a) {
   return up256((size_t)a.B * a.H * blocks_of(a.Lq) * kRows * 2 * sizeof(float));
@@ -1182,6 +1267,7 @@ cudaError_t bwd(const AttnArgs& a, cudaStream_t s) {
   else
     k_rows<T, 16><<<grid_rows, kRowThreads, 0, s>>>(r);
   e = cudaGetLastError();
+  if (e == cudaSuccess && a.Lq && exact_blocks(a)) e = grad<T, true, true>(a, f, s);
   if (e == cudaSuccess && a.Lq) e = grad<T, true>(a, f, s);
   if (e != cudaSuccess || !a.Lk) return e;
   if (!a.Lq) f.dtable = nullptr;

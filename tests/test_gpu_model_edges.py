@@ -235,3 +235,34 @@ def test_wide_relpos_bias_gradient(plan, Lq, Lk, off):
             bound = (32 * N + 332) * 2.0 ** -24 * R.bucket_sums(x.abs().sum(0), b, plan[0])
             bound = bound + R.UNIT[F32] * (want.abs() + bound)
             G._within(dt[:, h], want, bound, f"dtable of head {h}")
+
+
+# ---------------------------------------------------------------------------
+# How near the gradients are
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("case", [
+    dict(B=8, H=4, Lq=27, Lk=27, D=64, causal=True), dict(B=8, H=4, Lq=200, Lk=27, D=80, causal=True, p=0.2),
+    dict(B=6, H=4, Lq=139, Lk=139, D=32), dict(B=6, H=4, Hkv=2, Lq=90, Lk=16, D=128, p=0.1),
+    dict(B=4, H=4, Lq=900, Lk=900, D=128, causal=True, p=0.1), dict(B=4, H=2, Hkv=1, Lq=300, Lk=256, D=64),
+    dict(B=6, H=4, Lq=150, Lk=700, D=64, kv_len=[700, 200, 20, 64, 0, 130], p=0.1),
+    dict(B=4, H=4, Lq=500, Lk=600, D=80, causal=True, q_offset=-60, kv_len=[600, 500, 70, 301]),
+    dict(B=4, H=4, Lq=400, Lk=1000, D=32, causal=True, q_offset=100),
+])
+@pytest.mark.parametrize("bias", [False, True])
+def test_gradients_are_as_near_as_two_roundings(dtype, case, bias):
+    """An output is rounded to the type, and so is dS, the operand of its product.  By norm
+    each is the error of rounding the exact gradient once (dS up to 1.1 times: its spread
+    over a binade is another), so both are under sqrt(1 + 1.1^2) < 1.5 times it: no third
+    error of that size, as rowsum(do o) of a rounded o would be where keys are few.  The
+    table's gradient is summed from dS before it is rounded."""
+    case = dict(case, dtype=dtype)
+    if bias:
+        case["bias"] = G.ONE if case.get("causal") else G.T5
+    q, k, v, do, kw, ref = G._attn_case(**case)
+    got = G._attn_run(q, k, v, do, kw)
+    want = R.attention(q, k, v, do, **ref)
+    for n in ("dq", "dk", "dv") + (("dtable",) if bias else ()):
+        once = (want[n].to(dtype).double() - want[n]).norm()
+        assert (got[n].double() - want[n]).norm() <= 1.5 * once, n
