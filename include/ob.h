@@ -695,8 +695,8 @@ ob_status ob_relpos_bias_bwd(const ob_relpos* rp, const void* dout, int out_type
  * Products take the inputs' type with fp32 accumulation; softmax statistics
  * and dtable's sums are fp32; P and dS are rounded to the type as operands of
  * their products, as is o before rowsum(do o) where a block of 128 queries has
- * more than 256 keys (128 in a batch with kv_len and Lk over 256; with fewer,
- * that sum is taken from dP).  In fp16 what is below 2^-24 of
+ * more than 128 keys (with dtable 256, but not with kv_len and a longer Lk);
+ * with fewer, that sum is taken from dP.  In fp16 what is below 2^-24 of
  * them is lost. */
 typedef struct {
   int type;               /* OB_TYPE_BF16 or OB_TYPE_F16: q, k, v, o, their gradients, table */

@@ -208,10 +208,13 @@ constexpr int kItems = 4;  // pieces handed out at a time
 
 // Tiles of keys up to which a piece's delta is worked out from the scores.  Of 60
 // drawn training calls 37 were over 1.5 times as far from 64 bits as with fp32
-// throughout when none was, of 150 two with two tiles and none with four, which
-// cost 8 x 2048 causal of d 128 542 -> 552 us.  In a batch of longer and shorter
-// entries two: 32 x 12 x 512 with lengths from 128 on 227 -> 239 us, four 250.
-constexpr int kExactTiles = 4, kExactTilesRagged = 2;
+// throughout when none was, of 450 ten with these, by up to 1.56.  The bias table's
+// gradient, which is not rounded on the way, wants more of them (256 keys: 1.9
+// times with two, 1 with four) but where a batch is of longer and shorter entries.
+// It costs the backward pass of 32 x 12 x 512, lengths from 128 on, 227 -> 239 us
+// (four tiles 250), 32 x 12 x 256 with a table 99 -> 131 (without one nothing),
+// 32 x 12 x 128 44 -> 55, 8 x 2048 causal of d 128 542 -> 551.
+constexpr int kExactTiles = 2, kExactTilesTable = 4;
 
 struct Item {
   int x0, b, hx, keys, from, per;  // x0 < 0: no more
@@ -1090,7 +1093,8 @@ __global__ void __launch_bounds__(GradShape<DP, DQ>::kThreads, 1)
 int blocks_of(int L) { return (L + kRows - 1) / kRows; }
 
 int exact_tiles(const AttnArgs& a) {
-  return a.kv_len && a.Lk > kExactTiles * kTileRows ? kExactTilesRagged : kExactTiles;
+  const bool ragged = a.kv_len && a.Lk > kExactTilesTable * kTileRows;
+  return a.dtable && !ragged ? kExactTilesTable : kExactTiles;
 }
 
 // The first blocks of 128 queries, those that may have pieces for EXACT: all,
