@@ -6,9 +6,9 @@
 //   dtable[n][h] = keep scale * the sum of dS over the pairs of bucket n
 //
 // Three kernels, a fourth for few keys and a fifth for shared heads.  k_rows: -lse
-// and -delta of every query.  k_attn_grad twice: for 128 queries at a time over the keys (dq
-// and the bias table's sums), and for 128 keys at a time over the queries of
-// the heads that share them (dk, dv).  Both recompute S and dP on the tensor
+// and -delta of every query.  k_attn_grad twice: for 128 queries at a time over
+// the keys (dq and the bias table's sums), and for 128 keys at a time over the
+// queries of the heads that share them (dk, dv).  Both recompute S and dP on the tensor
 // cores and need no atomics: seven products instead of the five of a single
 // pass, for results that are the same bits on every run.  k_join adds up heads
 // that share keys where they were worked out one by one.
@@ -212,8 +212,8 @@ constexpr int kItems = 4;  // pieces handed out at a time
 // gradient, which is not rounded on the way, wants more of them (256 keys: 1.9
 // times with two, 1 with four) but where a batch is of longer and shorter entries.
 // It costs the backward pass of 32 x 12 x 512, lengths from 128 on, 227 -> 239 us
-// (four tiles 250), 32 x 12 x 256 with a table 99 -> 131 (without one nothing),
-// 32 x 12 x 128 44 -> 55, 8 x 2048 causal of d 128 542 -> 551.
+// (four tiles 250), 32 x 12 x 256 with a table 99 -> 131 (without one nothing;
+// four tiles 87 -> 116), 32 x 12 x 128 44 -> 55, 8 x 2048 causal of d 128 542 -> 551.
 constexpr int kExactTiles = 2, kExactTilesTable = 4;
 
 struct Item {
