@@ -23,7 +23,7 @@ m and v are rounded after each of their operations.  In 8 bits they are held in
 blocks of 256 elements of a tensor, each with a power of two as its unit: one
 byte E a block, unit 2^(E - 127), 0 for a block of zeros.  With `a` the block's
 largest finite value, E = (a's biased exponent) - 8, plus 1 if a's significand
-is over 1.75, at least 1 (v: 3).  In that unit m is a float of 1 + 4 + 3 bits
+is over 1.75, at least 1 (v: 3), at most 246.  In that unit m is a float of 1 + 4 + 3 bits
 (sign, exponent with bias 7, significand; 127 = not a number) and v one of
 5 + 3 bits (exponent with bias 23; 255 = not a number).  A value between two
 codes takes the upper one with the probability of its place between them: the
@@ -354,7 +354,7 @@ def _pack(x, noise, bias):
     size = blocks.abs()
     top = torch.where(size < math.inf, size, 0).amax(1).view(torch.int32)
     e = (top >> 23) - 8 + ((top & 0x7FFFFF) > 0x600000).int()
-    exp = torch.where(top > 0, e.clamp(min=1 if bias == 7 else 3), 0)
+    exp = torch.where(top > 0, e.clamp(min=1 if bias == 7 else 3, max=246), 0)
     y = size * torch.where(exp > 0, (254 - exp) << 23, 0).view(torch.float32)[:, None]
     bits = y.view(torch.int32)
     noise = noise.view(-1, BLOCK)
