@@ -745,6 +745,145 @@ ob_status ob_attn_bwd(const ob_attn* a, const ob_heads* grad_o, const ob_heads* 
  * Synchronises `stream`. */
 ob_status ob_attn_device_error(unsigned* code, ob_stream_t stream);
 
+/* ----------------------------------------------------------------------
+ * What is left of a layer and of its step: layer norm, the dense layer's
+ * products with their epilogue, and AdamW over many tensors.  As the calls
+ * above they need no ctx and results are the same bits on every run.
+ * ---------------------------------------------------------------------- */
+
+/* Layer norm of rows of `cols` elements, for s = x + residual rounded to the
+ * type (residual NULL: s = x):
+ *   mean = sum(s) / cols,  rstd = 1 / sqrt(sum((s - mean)^2) / cols + eps),
+ *   y = (s - mean) rstd weight + bias
+ * weight, bias: [cols] of w_type, or NULL (1 and 0).  sum (with a residual
+ * only), mean and rstd [rows] (fp32): written where not NULL; s, mean and rstd
+ * are what the backward pass needs.  type: OB_TYPE_*, of the arrays of rows,
+ * which start ld elements apart (each >= cols); pointers aligned to the
+ * element, 16 bytes (and rows that are multiples of 16 bytes) for the fast
+ * path.  Sums are fp32, the variance that of the centred values.  y or sum may
+ * be x or residual itself, but they must not overlap otherwise, nor each
+ * other.  cols < 2^24, rows * cols < 2^40; either may be 0.  eps > 0. */
+ob_status ob_layernorm_fwd(const void* x, size_t ldx, const void* residual, size_t ldr,
+                           const void* weight, const void* bias, int w_type, void* y, size_t ldy,
+                           void* sum, size_t lds, float* mean, float* rstd, size_t rows,
+                           size_t cols, int type, double eps, ob_stream_t stream);
+
+/* Given dy, and x = the s of the forward pass with its mean and rstd:
+ *   xhat = (x - mean) rstd,  h = dy weight,
+ *   dx = rstd (h - mean(h) - xhat mean(h xhat)) + dsum
+ *   dweight = sum over rows of dy xhat,  dbias = sum over rows of dy
+ * dsum: the gradient that reaches s from elsewhere, or NULL (0); dx is that of
+ * x and of residual.  dx, dweight and dbias (w_type): NULL where not wanted;
+ * with 0 rows the latter two are 0.  Outputs must not overlap inputs.
+ * workspace: ob_layernorm_workspace_bytes(), 16-byte aligned, contents free. */
+ob_status ob_layernorm_workspace_bytes(size_t rows, size_t cols, size_t* bytes);
+ob_status ob_layernorm_bwd(const void* dy, size_t lddy, const void* x, size_t ldx,
+                           const float* mean, const float* rstd, const void* weight, int w_type,
+                           const void* dsum, size_t ldds, void* dx, size_t lddx, void* dweight,
+                           void* dbias, size_t rows, size_t cols, int type, void* workspace,
+                           size_t workspace_bytes, ob_stream_t stream);
+
+/* The dense layer of x [M][K] and weights [N][K] (stored [K][N] if w_kn):
+ *   z = x w^T + bias,  y = act(z) + residual
+ * and, given dy and the forward pass's z (none for OB_ACT_NONE):
+ *   dz = dy act'(z),  dx = dz w,  dw = dz^T x (stored as w),
+ *   dbias = sum over rows of dz;  the residual's gradient is dy
+ * Products take the inputs' type with fp32 accumulation.  y is rounded once;
+ * act is of the z before it is rounded to be stored, act' of the stored one;
+ * dz is rounded to the type as an operand of its products, dbias is summed in
+ * fp32 from the values before that.  GELU is z Phi(z), GELU_TANH
+ * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2. */
+#define OB_ACT_NONE 0
+#define OB_ACT_RELU 1
+#define OB_ACT_GELU 2
+#define OB_ACT_GELU_TANH 3
+typedef struct {
+  int type;          /* OB_TYPE_BF16 or OB_TYPE_F16: all arrays */
+  int act;           /* OB_ACT_* */
+  int w_kn;
+  int unaligned;     /* 0: every matrix is 16-byte aligned and its ld a multiple of 8; else
+                        any alignment to the element, at the cost of copies in the workspace */
+  int64_t M, N, K;   /* < 2^30 each; 0 is allowed */
+} ob_linear;
+/* A matrix of rows of contiguous elements, ld elements apart. */
+typedef struct {
+  void* data;
+  int64_t ld;
+} ob_matrix;
+
+/* bias [N], residual and z: NULL where there is none (z: not written).  y may
+ * be residual itself, and must not overlap it or another input otherwise.
+ * workspace: ob_linear_workspace_bytes(), 256-byte aligned, contents free. */
+ob_status ob_linear_workspace_bytes(const ob_linear* l, int backward, size_t* bytes);
+ob_status ob_linear_fwd(const ob_linear* l, const ob_matrix* x, const ob_matrix* w,
+                        const void* bias, const ob_matrix* residual, const ob_matrix* z,
+                        const ob_matrix* y, void* workspace, size_t workspace_bytes,
+                        ob_stream_t stream);
+/* dx, dw and dbias: NULL where not wanted (x is needed for dw only, w for dx
+ * only).  Outputs must not overlap inputs. */
+ob_status ob_linear_bwd(const ob_linear* l, const ob_matrix* dy, const ob_matrix* x,
+                        const ob_matrix* w, const ob_matrix* z, const ob_matrix* dx,
+                        const ob_matrix* dw, void* dbias, void* workspace,
+                        size_t workspace_bytes, ob_stream_t stream);
+
+/* One AdamW step over `count` tensors, with decoupled decay, at step t:
+ *   g = grad * grad_scale
+ *   m = b1 m + (1 - b1) g,  v = b2 v + ((1 - b2) g) g
+ *   p = p (1 - lr decay) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+ * in fp32; the products and sums of m and v are each rounded on their own, and
+ * the update takes them before they are rounded to 8 bits.  p and copy (a
+ * second array that gets the same values, or NULL) are rounded once to their
+ * types.
+ * State.  Tensor i's moments start at element 256 * (the sum over j < i of
+ * ceil(n_j / 256)) of m and v.  What follows a tensor's last element in its
+ * last block is written as 0.  state_bits 32: m and v are fp32, m_exp and v_exp
+ * unused.  state_bits 8: m and v hold a byte an element, m_exp and v_exp one
+ * byte E a block of 256: its unit is 2^(E - 127), or 0 for E = 0 (a block of
+ * zeros).  With a block's largest finite value of significand f and biased
+ * exponent e, E = e - 8 + (f > 1.75), at least 1 (v: 3), at most 246.  In that unit m's code
+ * is a float of one sign, 4 exponent (bias 7) and 3 significand bits, 127 or
+ * 255 not a number; v's one of 5 exponent (bias 23) and 3 significand bits, 255
+ * not a number (which an infinity becomes too).  Rounding to a code is
+ * stochastic: the low (m) or high (v) 16 bits of word i % 4 of Philox4x32-10
+ * with key = seed and counter = (i / 4, t), i the element's place in the
+ * state, are added below the significand's three bits, whose rest they extend to,
+ * and the sum is cut off; a positive v keeps at least its smallest code.
+ * All-zero buffers are moments of zero in either form.
+ * counter: 4 doubles on the device: t, b1^t, b2^t (0, 1, 1 before the first
+ * step) and one that the library uses and leaves 0.  The call advances it, so a
+ * graph that captured a call takes the next step on every replay.  Calls that
+ * share a state must not overlap on the GPU. */
+typedef struct {
+  int state_bits;           /* 8 or 32 */
+  int grad_type;            /* OB_TYPE_*, of every gradient */
+  double lr, b1, b2, eps;   /* lr >= 0; b1, b2 in [0, 1); eps in [1e-18, 1] */
+  uint64_t seed;            /* state_bits 8 */
+  const float* lr_device;   /* on the device, instead of lr; or NULL */
+  const float* grad_scale;  /* on the device, or NULL (1) */
+  const float* skip;        /* on the device, or NULL: the call changes nothing if it is not 0 */
+} ob_adamw;
+typedef struct {
+  void* p;
+  void* copy;       /* or NULL */
+  size_t n;         /* may be 0; 2^40 elements of state in all */
+  float decay;      /* >= 0 */
+  int p_type, copy_type;
+} ob_adamw_tensor;
+
+/* grads: `count` pointers; a tensor whose gradient is NULL is left as it is,
+ * its moments too.  p, copy and gradients are aligned to their element, 16
+ * bytes for the fast path, and must not overlap; m and v are 16-byte aligned,
+ * counter 8-byte. */
+ob_status ob_adamw_step(const ob_adamw* a, const ob_adamw_tensor* tensors,
+                        const void* const* grads, int count, void* m, void* v, uint8_t* m_exp,
+                        uint8_t* v_exp, double* counter, ob_stream_t stream);
+
+/* The values of `elements` (a multiple of 256) moments in 8 bits as bf16, which
+ * holds them exactly (below 2^-126: nearly). */
+ob_status ob_adamw_moments(const void* m, const void* v, const uint8_t* m_exp,
+                           const uint8_t* v_exp, size_t elements, void* m_out, void* v_out,
+                           ob_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

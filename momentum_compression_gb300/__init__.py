@@ -8,15 +8,18 @@ the path runs in the CUDA kernels of libob.so.  There is no CPU fallback:
 if libob.so is missing or cannot be loaded, `lib()` raises.
 
 The model's side of a training step -- dropout, the bucketed relative
-position bias and the attention that uses both -- is here under its C names
-too; model.py wraps it for torch's autograd.
+position bias and the attention that uses both, layer norm, the dense layer's
+products -- is here under its C names too; model.py wraps it for torch's
+autograd.  AdamW, over many tensors at once, is for parameters that are not
+compressed.
 
 Two layers:
   * `ob_*` functions with the C names, taking an `ob_ctx` handle, tensors
     (or lists of tensors) and an optional stream;
   * `OneBitOptimizer`, which owns the device buffers of one simulated
     data-parallel job (W workers on one GPU) and calls the `ob_*` functions
-    in the order of the method.
+    in the order of the method; `AdamW`, which owns the moments of a list of
+    tensors.
 """
 import ctypes as ct
 import functools
@@ -31,6 +34,7 @@ OB_GRAD_F32, OB_GRAD_BF16 = 0, 1
 OB_MODE_ADAM, OB_MODE_LAMB = 0, 1
 OB_MAX_WORKERS = 64
 OB_TYPE_F32, OB_TYPE_BF16, OB_TYPE_F16 = 0, 1, 2
+OB_ACT_NONE, OB_ACT_RELU, OB_ACT_GELU, OB_ACT_GELU_TANH = range(4)
 OB_RELPOS_MAX_SIDE = 128  # buckets a side of a relative position bias
 OB_ATTN_MAX_SPAN = 512  # distances between the outermost buckets of a bias inside the attention
 OB_NOALLOC_SCRATCH_BYTES = 4 << 20  # the static scratch of ob_compress_noalloc
@@ -52,6 +56,9 @@ EXPORTS = (
     "ob_dropout", "ob_relpos_init", "ob_relpos_bias", "ob_relpos_workspace_bytes",
     "ob_relpos_bias_bwd", "ob_attn_fwd", "ob_attn_workspace_bytes", "ob_attn_bwd",
     "ob_attn_device_error",
+    "ob_layernorm_fwd", "ob_layernorm_workspace_bytes", "ob_layernorm_bwd",
+    "ob_linear_workspace_bytes", "ob_linear_fwd", "ob_linear_bwd",
+    "ob_adamw_step", "ob_adamw_moments",
 )
 
 
@@ -108,6 +115,28 @@ class ob_attn(ct.Structure):
 class ob_heads(ct.Structure):
     _fields_ = [("data", ct.c_void_p), ("stride_b", ct.c_int64), ("stride_l", ct.c_int64),
                 ("stride_h", ct.c_int64)]
+
+
+class ob_linear(ct.Structure):
+    _fields_ = [("type", ct.c_int), ("act", ct.c_int), ("w_kn", ct.c_int),
+                ("unaligned", ct.c_int), ("M", ct.c_int64), ("N", ct.c_int64),
+                ("K", ct.c_int64)]
+
+
+class ob_matrix(ct.Structure):
+    _fields_ = [("data", ct.c_void_p), ("ld", ct.c_int64)]
+
+
+class ob_adamw(ct.Structure):
+    _fields_ = [("state_bits", ct.c_int), ("grad_type", ct.c_int), ("lr", ct.c_double),
+                ("b1", ct.c_double), ("b2", ct.c_double), ("eps", ct.c_double),
+                ("seed", ct.c_uint64), ("lr_device", ct.c_void_p), ("grad_scale", ct.c_void_p),
+                ("skip", ct.c_void_p)]
+
+
+class ob_adamw_tensor(ct.Structure):
+    _fields_ = [("p", ct.c_void_p), ("copy", ct.c_void_p), ("n", ct.c_size_t),
+                ("decay", ct.c_float), ("p_type", ct.c_int), ("copy_type", ct.c_int)]
 
 
 _lib = None
@@ -175,6 +204,16 @@ def lib():
         L.ob_attn_workspace_bytes.argtypes = [vp, ct.POINTER(sz)]
         L.ob_attn_device_error.argtypes = [ct.POINTER(ct.c_uint), vp]
         L.ob_attn_bwd.argtypes = [vp] * 12 + [sz, vp]
+        L.ob_layernorm_fwd.argtypes = [vp, sz, vp, sz, vp, vp, i32, vp, sz, vp, sz, vp, vp, sz, sz,
+                                       i32, f64, vp]
+        L.ob_layernorm_workspace_bytes.argtypes = [sz, sz, ct.POINTER(sz)]
+        L.ob_layernorm_bwd.argtypes = [vp, sz, vp, sz, vp, vp, vp, i32, vp, sz, vp, sz, vp, vp, sz,
+                                       sz, i32, vp, sz, vp]
+        L.ob_linear_workspace_bytes.argtypes = [vp, i32, ct.POINTER(sz)]
+        L.ob_linear_fwd.argtypes = [vp] * 8 + [sz, vp]
+        L.ob_linear_bwd.argtypes = [vp] * 9 + [sz, vp]
+        L.ob_adamw_step.argtypes = [vp, vp, vp, i32] + [vp] * 6
+        L.ob_adamw_moments.argtypes = [vp, vp, vp, vp, sz, vp, vp, vp]
         for name in EXPORTS:
             if name != "ob_last_error":
                 getattr(L, name).restype = ct.c_int
@@ -878,6 +917,395 @@ def ob_attn_workspace_bytes(q, k, relpos=None, table=None):
     b = ct.c_size_t()
     _check(lib().ob_attn_workspace_bytes(a, ct.byref(b)))
     return b.value
+
+
+# ---------------------------------------------------------------------------
+# Layer norm and the dense layer
+# ---------------------------------------------------------------------------
+
+def _like(name, t, shape, dtype, at, other="x"):
+    """Refuses t unless it has `other`'s shape, type and device."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != at:
+        _refuse(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device} must be {tuple(shape)} {dtype} "
+                f"on CUDA device {at}, as {other}")
+
+
+def _vectors(at, n, **vectors):
+    """(common type code, or that of float32; addresses) of vectors of n elements or None."""
+    dtype, ptrs = None, []
+    for name, t in vectors.items():
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.shape != (n,) or (n > 1 and t.stride(0) != 1) or t.get_device() != at:
+            _refuse(f"{name} must be a contiguous vector of {n} elements on CUDA device {at}")
+        if dtype is not None and t.dtype != dtype:
+            _refuse(f"{name}: {t.dtype}, but {dtype} before it")
+        dtype = t.dtype
+        ptrs.append(t.data_ptr())
+    return OB_TYPE_F32 if dtype is None else _types().get(dtype, -1), ptrs
+
+
+def _statistics(at, rows, **stats):
+    import torch
+    ptrs = []
+    for name, t in stats.items():
+        if t is not None and (t.numel() != rows or t.dtype != torch.float32 or not t.is_contiguous()
+                              or t.get_device() != at):
+            _refuse(f"{name} must be a contiguous float32 tensor of {rows} elements on CUDA device "
+                    f"{at}")
+        ptrs.append(None if t is None else t.data_ptr())
+    return ptrs
+
+
+def ob_layernorm_fwd(x, y, weight=None, bias=None, eps=1e-5, residual=None, sum=None, mean=None,
+                     rstd=None, stream=None):
+    """y = the layer norm of s = x + residual over the last dimension, times weight plus
+    bias; sum gets s (rounded to the type), mean and rstd what the backward pass needs."""
+    at, shape, dtype = x.get_device(), x.shape, x.dtype
+    if at < 0 or len(shape) == 0:
+        _refuse("x must be a tensor of rows on a CUDA device")
+    type_ = _type(x, "x")
+    rows, cols, ldx = _rows(x, "x")
+    _like("y", y, shape, dtype, at)
+    ldy = _rows(y, "y")[2]
+    pr = ps = None
+    ldr = lds = cols
+    if residual is not None:
+        _like("residual", residual, shape, dtype, at)
+        pr, ldr = residual.data_ptr(), _rows(residual, "residual")[2]
+    if sum is not None:
+        _like("sum", sum, shape, dtype, at)
+        ps, lds = sum.data_ptr(), _rows(sum, "sum")[2]
+    w_type, (pw, pb) = _vectors(at, cols, weight=weight, bias=bias)
+    pm, pd = _statistics(at, rows, mean=mean, rstd=rstd)
+    _launch(lib().ob_layernorm_fwd, at, stream, x.data_ptr(), ldx, pr, ldr, pw, pb, w_type,
+            y.data_ptr(), ldy, ps, lds, pm, pd, rows, cols, type_, eps)
+
+
+@functools.lru_cache(1024)
+def ob_layernorm_workspace_bytes(rows, cols):
+    """Bytes of scratch ob_layernorm_bwd needs where it computes dweight or dbias."""
+    b = ct.c_size_t()
+    _check(lib().ob_layernorm_workspace_bytes(rows, cols, ct.byref(b)))
+    return b.value
+
+
+def ob_layernorm_bwd(dy, x, mean, rstd, dx=None, weight=None, dweight=None, dbias=None, dsum=None,
+                     workspace=None, stream=None):
+    """dx, dweight and dbias from dy, with x the normalised s of the forward call; dsum is
+    added to dx.  workspace: a uint8 tensor, or None for one of torch's allocator."""
+    at, shape, dtype = x.get_device(), x.shape, x.dtype
+    if at < 0 or len(shape) == 0:
+        _refuse("x must be a tensor of rows on a CUDA device")
+    type_ = _type(x, "x")
+    rows, cols, ldx = _rows(x, "x")
+    _like("dy", dy, shape, dtype, at)
+    lddy = _rows(dy, "dy")[2]
+    px = ps = None
+    lddx = ldds = cols
+    if dx is not None:
+        _like("dx", dx, shape, dtype, at)
+        px, lddx = dx.data_ptr(), _rows(dx, "dx")[2]
+    if dsum is not None:
+        _like("dsum", dsum, shape, dtype, at)
+        ps, ldds = dsum.data_ptr(), _rows(dsum, "dsum")[2]
+    w_type, (pw, pdw, pdb) = _vectors(at, cols, weight=weight, dweight=dweight, dbias=dbias)
+    pm, pd = _statistics(at, rows, mean=mean, rstd=rstd)
+    if workspace is not None:
+        _check_workspace(workspace, at)
+    elif dweight is not None or dbias is not None:
+        workspace = _scratch(ob_layernorm_workspace_bytes(rows, cols), x, stream)
+    _launch(lib().ob_layernorm_bwd, at, stream, dy.data_ptr(), lddy, x.data_ptr(), ldx, pm, pd, pw,
+            w_type, ps, ldds, px, lddx, pdw, pdb, rows, cols, type_, _ptr(workspace) or None,
+            0 if workspace is None else workspace.numel() * workspace.element_size())
+
+
+_ACTIVATIONS = {"none": OB_ACT_NONE, "relu": OB_ACT_RELU, "gelu": OB_ACT_GELU,
+                "gelu_tanh": OB_ACT_GELU_TANH}
+_LINEAR = struct.Struct("4i3q")
+assert _LINEAR.size == ct.sizeof(ob_linear)
+_MATRIX = struct.Struct("Pq")
+assert _MATRIX.size == ct.sizeof(ob_matrix)
+
+
+def _weights(w, name):
+    """(N, K, whether it is stored [K, N], leading dimension) of weights w [N, K]."""
+    if w.dim() != 2:
+        _refuse(f"{name} must be [N, K], got {tuple(w.shape)}")
+    N, K = w.shape
+    sn, sk = w.stride()
+    if K <= 1 or sk == 1:
+        return N, K, False, sn if N > 1 else K
+    if N <= 1 or sn == 1:
+        return N, K, True, sk
+    _refuse(f"{name}: one of its dimensions must be contiguous")
+
+
+class _Matrices:
+    """The matrices of a call on device `at`, packed; `off` where one is off 16 bytes."""
+
+    def __init__(self, dtype, at):
+        self.dtype, self.at, self.off = dtype, at, False
+
+    def pack(self, name, t, rows, cols, ld):
+        if t.dtype != self.dtype or t.get_device() != self.at:
+            _refuse(f"{name}: {t.dtype} on {t.device} must be {self.dtype} on CUDA device {self.at}")
+        p = t.data_ptr()
+        if p % 16 or (rows > 1 and ld % 8):
+            self.off = True
+        return _MATRIX.pack(p, ld)
+
+    def rows(self, name, t, rows, cols):
+        """Packs t [..., cols] of `rows` rows; None stays None."""
+        if t is None:
+            return None
+        r, c, ld = _rows(t, name)
+        if r != rows or c != cols:
+            _refuse(f"{name}: {tuple(t.shape)} must be {rows} rows of {cols}")
+        return self.pack(name, t, rows, cols, ld)
+
+
+def _activation(name):
+    code = _ACTIVATIONS.get(name)
+    if code is None:
+        _refuse(f"activation {name!r} is not one of {', '.join(_ACTIVATIONS)}")
+    return code
+
+
+@functools.lru_cache(1024)
+def ob_linear_workspace_bytes(type, act, w_kn, unaligned, M, N, K, backward):
+    """Bytes of scratch ob_linear_fwd (or, with `backward`, ob_linear_bwd) needs."""
+    l, b = ob_linear(type, act, w_kn, unaligned, M, N, K), ct.c_size_t()
+    _check(lib().ob_linear_workspace_bytes(ct.byref(l), backward, ct.byref(b)))
+    return b.value
+
+
+def _linear_call(fn, m, l, backward, like, workspace, stream, *args):
+    if workspace is None:
+        nbytes = ob_linear_workspace_bytes(*l, backward)
+        workspace = _scratch(nbytes, like, stream) if nbytes else None
+    else:
+        _check_workspace(workspace, m.at)
+    _launch(fn, m.at, stream, _LINEAR.pack(*l), *args, _ptr(workspace) or None,
+            0 if workspace is None else workspace.numel() * workspace.element_size())
+
+
+def ob_linear_fwd(x, w, y, bias=None, residual=None, z=None, activation="none", workspace=None,
+                  stream=None):
+    """y = act(x w^T + bias) + residual for x [..., K], w [N, K] (either dimension
+    contiguous) and y [..., N] in bfloat16 or float16; z gets what act is of.
+    activation: none, relu, gelu or gelu_tanh."""
+    at, type_ = x.get_device(), _type(x, "x")
+    if at < 0 or x.dim() == 0:
+        _refuse("x must be a tensor of rows on a CUDA device")
+    m = _Matrices(x.dtype, at)
+    M, K, ldx = _rows(x, "x")
+    N, wk, kn, ldw = _weights(w, "w")
+    if wk != K or y.shape != x.shape[:-1] + (N,):
+        _refuse(f"x {tuple(x.shape)}, w {tuple(w.shape)} and y {tuple(y.shape)} do not go together")
+    px, pw = m.pack("x", x, M, K, ldx), m.pack("w", w, *((K, N) if kn else (N, K)), ldw)
+    py, pr, pz = (m.rows(n, t, M, N) for n, t in (("y", y), ("residual", residual), ("z", z)))
+    bt, (pb,) = _vectors(at, N, bias=bias)
+    if bias is not None and bt != type_:
+        _refuse("bias must have the type of x")
+    l = (type_, _activation(activation), int(kn), int(m.off), M, N, K)
+    _linear_call(lib().ob_linear_fwd, m, l, 0, x, workspace, stream, px, pw, pb, pr, pz, py)
+
+
+def ob_linear_bwd(dy, x, w, dx=None, dw=None, dbias=None, z=None, activation="none",
+                  workspace=None, stream=None):
+    """dx, dw (laid out as w) and dbias from dy, with the forward call's x, w, z and
+    activation; the residual's gradient is dy."""
+    at, type_ = dy.get_device(), _type(dy, "dy")
+    if at < 0 or dy.dim() == 0:
+        _refuse("dy must be a tensor of rows on a CUDA device")
+    m = _Matrices(dy.dtype, at)
+    M, N, ldy = _rows(dy, "dy")
+    wn, K, kn, ldw = _weights(w, "w")
+    if wn != N or x.shape != dy.shape[:-1] + (K,):
+        _refuse(f"dy {tuple(dy.shape)}, x {tuple(x.shape)} and w {tuple(w.shape)} do not go together")
+    act = _activation(activation)
+    if act and z is None:
+        _refuse(f"z is needed for activation {activation!r}")
+    wr, wc = (K, N) if kn else (N, K)
+    pdy, pz = m.pack("dy", dy, M, N, ldy), m.rows("z", z if act else None, M, N)
+    px, pdx = m.rows("x", x, M, K), m.rows("dx", dx, M, K)
+    pw, pdw = m.pack("w", w, wr, wc, ldw), None
+    if dw is not None:
+        if dw.shape != w.shape or (wr > 1 and wc > 1 and dw.stride(1 - kn) != 1):
+            _refuse(f"dw must be {tuple(w.shape)} with the contiguous dimension of w")
+        pdw = m.pack("dw", dw, wr, wc, dw.stride(int(kn)) if wr > 1 else wc)
+    bt, (pb,) = _vectors(at, N, dbias=dbias)
+    if dbias is not None and bt != type_:
+        _refuse("dbias must have the type of dy")
+    l = (type_, act, int(kn), int(m.off), M, N, K)
+    _linear_call(lib().ob_linear_bwd, m, l, 1, dy, workspace, stream, pdy, px, pw, pz, pdx, pdw, pb)
+
+
+# ---------------------------------------------------------------------------
+# AdamW over many tensors
+# ---------------------------------------------------------------------------
+
+OB_ADAMW_BLOCK = 256  # elements of a tensor that share a unit, and the state's grain
+
+
+def ob_adamw_step(config, tensors, grads, m, v, counter, m_exp=None, v_exp=None, at=None,
+                  stream=None):
+    """One AdamW step: `config` an ob_adamw, `tensors` an array of ob_adamw_tensor, `grads` as
+    many tensors or addresses (None: the tensor stays as it is), on CUDA device `at`."""
+    if len(grads) != len(tensors):
+        _refuse(f"{len(grads)} gradients for {len(tensors)} tensors")
+    _launch(lib().ob_adamw_step, counter.get_device() if at is None else at, stream,
+            ct.byref(config), tensors, _ptr_array(grads), len(grads), _ptr(m), _ptr(v), _ptr(m_exp),
+            _ptr(v_exp), counter.data_ptr())
+
+
+def ob_adamw_moments(m, v, m_exp, v_exp, m_out, v_out, stream=None):
+    """The values of 8-bit moments, as bfloat16."""
+    import torch
+    at, n = _device_of("m", m, "v", v), m.numel()
+    for name, t, dtype, count in (("m", m, torch.uint8, n), ("v", v, torch.uint8, n),
+                                  ("m_exp", m_exp, torch.uint8, n // OB_ADAMW_BLOCK),
+                                  ("v_exp", v_exp, torch.uint8, n // OB_ADAMW_BLOCK),
+                                  ("m_out", m_out, torch.bfloat16, n),
+                                  ("v_out", v_out, torch.bfloat16, n)):
+        if t.dtype != dtype or t.numel() != count or not t.is_contiguous() or t.get_device() != at:
+            _refuse(f"{name} must be a contiguous {dtype} tensor of {count} elements on CUDA device "
+                    f"{at}")
+    _launch(lib().ob_adamw_moments, at, stream, m.data_ptr(), v.data_ptr(), m_exp.data_ptr(),
+            v_exp.data_ptr(), n, m_out.data_ptr(), v_out.data_ptr())
+
+
+class AdamW:
+    """AdamW with decoupled weight decay over a list of tensors, which stay where they are:
+    the step of parameters that are not compressed (norms, biases, embeddings) or of a
+    whole model.  One launch updates up to 512 tensors.
+
+    params: contiguous tensors of float32, bfloat16 or float16 on one device.
+    weight_decay: a number, or one for each tensor.  state_bits: 32, or 8 for moments of a
+    byte an element, rounded stochastically with random numbers named by (seed, step).
+    copies: None, or a tensor (or None) for each parameter that gets its new value too, in
+    a type of its own.  state: None for moments of zero, or what state() returned; the
+    buffers are adopted, not copied.
+
+    Buffers: m, v (and m_exp, v_exp with 8 bits), counter.  A CUDA graph may capture
+    step(): the step's number is on the device, so replays are further steps."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+                 state_bits=32, seed=0, copies=None, state=None):
+        import torch
+        self.params = list(params)
+        self.lr, self.betas, self.eps, self.seed = lr, tuple(betas), eps, seed
+        self.state_bits = state_bits
+        if not self.params:
+            _refuse("params is empty")
+        if state_bits not in (8, 32):
+            _refuse(f"state_bits = {state_bits} must be 8 or 32")
+        n = len(self.params)
+        decay = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * n
+        self.copies = [None] * n if copies is None else list(copies)
+        if len(decay) != n or len(self.copies) != n:
+            _refuse(f"weight_decay and copies must have an entry for each of {n} tensors")
+        self.device = self.params[0].device
+        self._at = self.params[0].get_device()
+        if self._at < 0:
+            _refuse("params must be on a CUDA device")
+        self._sizes = [p.numel() for p in self.params]
+        self._table = (ob_adamw_tensor * n)()
+        for i, (p, c, d) in enumerate(zip(self.params, self.copies, decay)):
+            for name, t in (("parameter", p), ("copy", c)):
+                if t is None:
+                    continue
+                if t.get_device() != self._at or not t.is_contiguous() or t.shape != p.shape:
+                    _refuse(f"{name} {i} must be contiguous, on CUDA device {self._at} and of the "
+                            "parameter's shape")
+            self._table[i] = ob_adamw_tensor(p.data_ptr(), _ptr(c), self._sizes[i], d, _type(p, "params"),
+                                             0 if c is None else _type(c, "copies"))
+        blocks = [-(-k // OB_ADAMW_BLOCK) for k in self._sizes]
+        total = OB_ADAMW_BLOCK * sum(blocks)
+        dtype = torch.float32 if state_bits == 32 else torch.uint8
+        given = state or {}
+        step = int(given.get("step", 0))
+
+        def buffer(name, count, dtype):
+            t = given.get(name)
+            if t is None:
+                if state:
+                    _refuse(f"state has no {name}")
+                return torch.zeros(count, dtype=dtype, device=self.device)
+            if t.dtype != dtype or t.numel() != count or not t.is_contiguous() \
+                    or t.get_device() != self._at:
+                _refuse(f"state: {name} must be a contiguous {dtype} tensor of {count} elements on "
+                        f"CUDA device {self._at}")
+            return t
+
+        self.m, self.v = buffer("m", total, dtype), buffer("v", total, dtype)
+        self.m_exp = self.v_exp = None
+        if state_bits == 8:
+            self.m_exp = buffer("m_exp", total // OB_ADAMW_BLOCK, torch.uint8)
+            self.v_exp = buffer("v_exp", total // OB_ADAMW_BLOCK, torch.uint8)
+        b1, b2 = self.betas
+        self.counter = torch.tensor([step, b1 ** step, b2 ** step, 0.0], dtype=torch.float64,
+                                    device=self.device)
+
+    def _scalar(self, name, t):
+        import torch
+        if t is None:
+            return None
+        if t.dtype != torch.float32 or t.numel() != 1 or t.get_device() != self._at:
+            _refuse(f"{name} must be one float32 on CUDA device {self._at}")
+        return t.data_ptr()
+
+    def step(self, grads=None, lr=None, grad_scale=None, skip=None, stream=None):
+        """One step.  grads: a tensor for each parameter, all of one type (None: that
+        parameter and its moments stay as they are); None for the parameters' .grad.
+        lr: instead of the one given before, a number or one float32 on the device.
+        grad_scale: one float32 on the device that multiplies every gradient (a loss scale's
+        inverse, a clipping factor).  skip: one float32 on the device; nothing changes and
+        the step does not count where it is not 0."""
+        import torch
+        grads = [p.grad for p in self.params] if grads is None else grads
+        if len(grads) != len(self.params):
+            _refuse(f"{len(grads)} gradients for {len(self.params)} parameters")
+        some = grads
+        sizes = self._sizes
+        if any(g is None for g in grads):
+            some = [g for g in grads if g is not None]
+            sizes = [n for n, g in zip(self._sizes, grads) if g is not None]
+        T = torch.Tensor
+        dtypes = {g.dtype for g in some}
+        if len(dtypes) > 1 or list(map(T.numel, some)) != sizes or not all(map(T.is_contiguous, some)) \
+                or any(at != self._at for at in map(T.get_device, some)):
+            _refuse("grads must be contiguous, of one type, of the parameters' sizes and on CUDA "
+                    f"device {self._at}")
+        lr = self.lr if lr is None else lr
+        on_device = isinstance(lr, T)
+        config = ob_adamw(self.state_bits, _type(some[0], "grads") if some else OB_TYPE_F32,
+                          0.0 if on_device else lr, *self.betas, self.eps, self.seed & _WORD,
+                          self._scalar("lr", lr if on_device else None),
+                          self._scalar("grad_scale", grad_scale), self._scalar("skip", skip))
+        ob_adamw_step(config, self._table, grads, self.m, self.v, self.counter, self.m_exp,
+                      self.v_exp, self._at, stream)
+
+    def moments(self, stream=None):
+        """(m, v) of all tensors, each tensor's from a multiple of 256 elements on: the
+        buffers themselves in 32 bits, their values as bfloat16 in 8."""
+        import torch
+        if self.state_bits == 32:
+            return self.m, self.v
+        m, v = (torch.empty(self.m.numel(), dtype=torch.bfloat16, device=self.device)
+                for _ in range(2))
+        ob_adamw_moments(self.m, self.v, self.m_exp, self.v_exp, m, v, stream)
+        return m, v
+
+    def state(self):
+        """The moments' buffers and the number of steps taken, for `state=` of another
+        AdamW.  Waits for the device."""
+        out = dict(m=self.m, v=self.v, step=int(self.counter[0].item()))
+        if self.state_bits == 8:
+            out.update(m_exp=self.m_exp, v_exp=self.v_exp)
+        return out
 
 
 # ---------------------------------------------------------------------------

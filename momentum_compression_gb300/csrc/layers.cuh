@@ -1,0 +1,89 @@
+// Argument blocks and launchers of the operators of a layer (layer norm, the
+// dense layer's products) and of the AdamW step over many tensors.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "ob.h"
+
+namespace ob {
+
+struct LayerNormArgs {
+  const void *x, *residual;      // residual or null
+  const void *weight, *bias;     // or null
+  void *y, *sum;                 // sum or null
+  float *mean, *rstd;            // or null (forward)
+  uint64_t ldx, ldr, ldy, lds;
+  uint64_t rows;
+  int cols, w_type;
+  float eps;
+};
+
+struct LayerNormBwdArgs {
+  const void *dy, *x, *dsum;     // dsum or null
+  const void* weight;            // or null
+  const float *mean, *rstd;
+  void *dx, *dweight, *dbias;    // each or null
+  uint64_t lddy, ldx, ldds, lddx;
+  uint64_t rows;
+  int cols, w_type;
+  float* partial;                // [parts][2][cols]
+  int parts;
+};
+
+cudaError_t launch_layernorm_fwd(const LayerNormArgs& a, int type, cudaStream_t s);
+// Blocks whose partial sums the gradient of these sizes keeps.
+int layernorm_bwd_parts(uint64_t rows, int cols);
+cudaError_t launch_layernorm_bwd(const LayerNormBwdArgs& a, int type, cudaStream_t s);
+
+// A matrix of 16-bit elements: element (i, j) at data + i * ld + j.
+struct Mat {
+  void* data;
+  int64_t ld;
+};
+
+struct LinearArgs {
+  int type, act, w_kn, unaligned;
+  int64_t M, N, K;
+  Mat x, w, y, z, residual;      // z and residual: data or null
+  const void* bias;              // or null
+  Mat dy, dx, dw;                // backward; dx and dw: data or null
+  void* dbias;                   // or null
+  uint8_t* workspace;
+};
+
+size_t linear_workspace_bytes(const LinearArgs& a, bool backward);
+cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t s);
+cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t s);
+
+constexpr int kAdamBlock = 256;  // elements that share a unit, and the state's grain
+
+struct AdamTensor {
+  void* p;
+  const void* g;     // null: the tensor is left as it is
+  void* copy;        // or null
+  uint64_t n;
+  uint64_t first;    // its first block in the state
+  float decay;
+  int types;         // p_type | copy_type << 8
+};
+
+struct AdamArgs {
+  int bits, g_type;
+  double lr, b1, b2;
+  float eps;
+  uint64_t seed;
+  const float *lr_device, *grad_scale, *skip;
+  void *m, *v;
+  uint8_t *m_exp, *v_exp;
+  double* counter;
+};
+
+cudaError_t launch_adamw(const AdamArgs& a, const AdamTensor* t, int count, cudaStream_t s);
+cudaError_t launch_adamw_moments(const uint8_t* m, const uint8_t* v, const uint8_t* m_exp,
+                                 const uint8_t* v_exp, size_t elements, void* m_out, void* v_out,
+                                 cudaStream_t s);
+
+}  // namespace ob

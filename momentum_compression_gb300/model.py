@@ -1,5 +1,6 @@
 """The model-side operators for torch's autograd: dropout, the learned
-relative position bias by buckets, and the attention that uses both.
+relative position bias by buckets, the attention that uses both, layer norm and
+the dense layer with its epilogue.
 
 Each function calls the ob_* entry points of the same name (their CUDA
 kernels; there is no CPU fallback) on torch's current stream.  Random
@@ -11,8 +12,8 @@ order: a graph of them (create_graph) is refused when it is differentiated."""
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (ob_attn_bwd, ob_attn_fwd, ob_dropout, ob_relpos_bias, ob_relpos_bias_bwd,
-               ob_relpos_init)
+from . import (ob_attn_bwd, ob_attn_fwd, ob_dropout, ob_layernorm_bwd, ob_layernorm_fwd,
+               ob_linear_bwd, ob_linear_fwd, ob_relpos_bias, ob_relpos_bias_bwd, ob_relpos_init)
 
 
 class RelPos:
@@ -133,3 +134,102 @@ def attention(q, k, v, table=None, relpos=None, causal=False, kv_len=None, scale
     kw = dict(causal=causal, scale=scale, q_offset=q_offset, p=p, seed=seed,
               offset=offset, relpos=None if relpos is None else relpos.plan)
     return _Attention.apply(q, k, v, None if table is None else table.contiguous(), kv_len, kw)
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, bias, eps, return_sum, graph):
+        ctx.set_materialize_grads(False)
+        train = graph and any(ctx.needs_input_grad)
+        new = lambda: torch.empty(x.shape, device=x.device, dtype=x.dtype)
+        y = new()
+        s = new() if residual is not None and (train or return_sum) else None
+        mean = rstd = None
+        if train:
+            rows = x.numel() // x.shape[-1] if x.shape[-1] else 0
+            mean, rstd = (torch.empty(rows, device=x.device) for _ in range(2))
+        ob_layernorm_fwd(x, y, weight=weight, bias=bias, eps=eps, residual=residual, sum=s,
+                         mean=mean, rstd=rstd)
+        ctx.has_residual, ctx.bias = residual is not None, bias is not None
+        if train:
+            ctx.save_for_backward(x if s is None else s, weight, bias, mean, rstd)
+        return (y, s) if return_sum else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dsum=None):
+        x, weight, bias, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx = dw = db = None
+        if dy is None:  # only the sum was used
+            dx = dsum
+        else:
+            if need[0] or need[1]:
+                dx = torch.empty(x.shape, device=x.device, dtype=x.dtype)
+            if need[2]:
+                dw = torch.empty_like(weight)
+            if need[3]:
+                db = torch.empty_like(bias)
+            dsum = None if dx is None or dsum is None else _as_rows(dsum)
+            ob_layernorm_bwd(_as_rows(dy), x, mean, rstd, dx, weight=weight, dweight=dw, dbias=db,
+                             dsum=dsum)
+        return (dx if need[0] else None, dx if ctx.has_residual and need[1] else None, dw, db, None,
+                None, None)
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, return_sum=False):
+    """Layer norm of s = x + residual over the last dimension, times weight plus bias (both
+    of one type).  With return_sum (and a residual): (y, s), s the residual stream of the
+    layers after a pre-norm one; its gradient joins in the same pass."""
+    if return_sum and residual is None:
+        raise ValueError("layer_norm: return_sum needs a residual")
+    return _LayerNorm.apply(_as_rows(x), None if residual is None else _as_rows(residual),
+                            None if weight is None else weight.contiguous(),
+                            None if bias is None else bias.contiguous(), eps, return_sum,
+                            torch.is_grad_enabled())
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, activation, graph):
+        shape = x.shape[:-1] + (w.shape[0],)
+        y = torch.empty(shape, device=x.device, dtype=x.dtype)
+        z = None
+        if graph and activation != "none" and any(ctx.needs_input_grad[:3]):
+            z = torch.empty(shape, device=x.device, dtype=x.dtype)
+        ob_linear_fwd(x, w, y, bias=bias, residual=residual, z=z, activation=activation)
+        ctx.save_for_backward(x, w, z)
+        ctx.activation = activation
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, w, z = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx = torch.empty(x.shape, device=x.device, dtype=x.dtype) if need[0] else None
+        dw = torch.empty_like(w) if need[1] else None
+        db = torch.empty(w.shape[0], device=w.device, dtype=w.dtype) if need[2] else None
+        if any(need[:3]):
+            ob_linear_bwd(_as_rows(dy), x, w, dx=dx, dw=dw, dbias=db, z=z,
+                          activation=ctx.activation)
+        return dx, dw, db, dy if need[3] else None, None, None
+
+
+def _as_weights(w):
+    """w [N, K] itself if one of its dimensions is contiguous and its rows do not overlap,
+    else a contiguous copy."""
+    if w.dim() == 2:
+        for rows, cols in ((0, 1), (1, 0)):
+            if w.stride(cols) == 1 and (w.shape[rows] <= 1 or w.stride(rows) >= w.shape[cols]):
+                return w
+    return w.contiguous()
+
+
+def linear(x, w, bias=None, activation="none", residual=None):
+    """act(x w^T + bias) + residual for x [..., K] and w [N, K] in bfloat16 or float16, the
+    whole epilogue in the product's kernel.  w may be a transposed view ([K, N] in memory); its
+    gradient is laid out as it is.  activation: none, relu, gelu or gelu_tanh."""
+    return _Linear.apply(_as_rows(x), _as_weights(w), None if bias is None else bias.contiguous(),
+                         None if residual is None else _as_rows(residual), activation,
+                         torch.is_grad_enabled())
