@@ -803,7 +803,7 @@ typedef struct {
   int w_kn;
   int unaligned;     /* 0: every matrix is 16-byte aligned and its ld a multiple of 8; else
                         any alignment to the element, at the cost of copies in the workspace */
-  int64_t M, N, K;   /* < 2^30 each; 0 is allowed */
+  int64_t M, N, K;   /* < 2^30 each, no matrix over 2^40 elements; 0 is allowed */
 } ob_linear;
 /* A matrix of rows of contiguous elements, ld elements apart. */
 typedef struct {
@@ -825,6 +825,9 @@ ob_status ob_linear_bwd(const ob_linear* l, const ob_matrix* dy, const ob_matrix
                         const ob_matrix* w, const ob_matrix* z, const ob_matrix* dx,
                         const ob_matrix* dw, void* dbias, void* workspace,
                         size_t workspace_bytes, ob_stream_t stream);
+
+/* As ob_attn_device_error, for the waits of the dense layer's products. */
+ob_status ob_linear_device_error(unsigned* code, ob_stream_t stream);
 
 /* One AdamW step over `count` tensors, with decoupled decay, at step t:
  *   g = grad * grad_scale

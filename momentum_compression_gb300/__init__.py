@@ -57,7 +57,7 @@ EXPORTS = (
     "ob_relpos_bias_bwd", "ob_attn_fwd", "ob_attn_workspace_bytes", "ob_attn_bwd",
     "ob_attn_device_error",
     "ob_layernorm_fwd", "ob_layernorm_workspace_bytes", "ob_layernorm_bwd",
-    "ob_linear_workspace_bytes", "ob_linear_fwd", "ob_linear_bwd",
+    "ob_linear_workspace_bytes", "ob_linear_fwd", "ob_linear_bwd", "ob_linear_device_error",
     "ob_adamw_step", "ob_adamw_moments",
 )
 
@@ -212,6 +212,7 @@ def lib():
         L.ob_linear_workspace_bytes.argtypes = [vp, i32, ct.POINTER(sz)]
         L.ob_linear_fwd.argtypes = [vp] * 8 + [sz, vp]
         L.ob_linear_bwd.argtypes = [vp] * 9 + [sz, vp]
+        L.ob_linear_device_error.argtypes = [ct.POINTER(ct.c_uint), vp]
         L.ob_adamw_step.argtypes = [vp, vp, vp, i32] + [vp] * 6
         L.ob_adamw_moments.argtypes = [vp, vp, vp, vp, sz, vp, vp, vp]
         for name in EXPORTS:
@@ -1141,6 +1142,13 @@ def ob_linear_bwd(dy, x, w, dx=None, dw=None, dbias=None, z=None, activation="no
         _refuse("dbias must have the type of dy")
     l = (type_, act, int(kn), int(m.off), M, N, K)
     _linear_call(lib().ob_linear_bwd, m, l, 1, dy, workspace, stream, pdy, px, pw, pz, pdx, pdw, pb)
+
+
+def ob_linear_device_error(stream=None):
+    """Reads and clears the dense layer's device error word (0 = none)."""
+    v = ct.c_uint()
+    _check(lib().ob_linear_device_error(ct.byref(v), _stream(stream)))
+    return v.value
 
 
 # ---------------------------------------------------------------------------

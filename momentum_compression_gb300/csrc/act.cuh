@@ -1,0 +1,95 @@
+// The activations of the dense layer and their slopes, in fp32.
+//
+// GELU by Phi(z) = 1 - erfc(z / sqrt 2) / 2 with erfc(a) = e^(-a^2) (a1 t + ... + a5 t^5),
+// t = 1 / (1 + p a), for a >= 0: formula 7.1.26 of Abramowitz and Stegun's handbook,
+// off by at most 1.5e-7, where bf16 keeps 4e-3 of a value and fp16 5e-4.  One
+// exponential, one reciprocal and eight multiply-adds; its slope has the same
+// exponential.  The tanh form is z / (1 + e^(-2u)).
+#pragma once
+
+#include "ob.h"
+
+namespace ob {
+
+__device__ __forceinline__ float act_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float act_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// A NaN in either comes out.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+constexpr float kActLog2e = 1.44269504f;
+
+// e^(-z^2 / 2) in *bell, erfc(|z| / sqrt 2) / 2 returned; |z| <= 16.
+__device__ __forceinline__ float half_erfc(float size, float* bell) {
+  const float t = act_rcp(__fmaf_rn(0.3275911f * 0.70710678f, size, 1.0f));
+  float p = __fmaf_rn(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+  p = __fmaf_rn(p, t, 0.5f * 1.421413741f);
+  p = __fmaf_rn(p, t, 0.5f * -0.284496736f);
+  p = __fmaf_rn(p, t, 0.5f * 0.254829592f);
+  *bell = act_ex2(size * size * (-0.5f * kActLog2e));
+  return p * t * *bell;
+}
+
+constexpr float kTanhA = 0.7978845608f, kTanhB = 0.044715f;  // sqrt(2 / pi)
+
+template <int ACT>
+__device__ __forceinline__ float act_of(float z) {
+  if (ACT == OB_ACT_RELU) return max_nan(z, 0.0f);
+  if (ACT == OB_ACT_GELU) {
+    float bell;
+    const float size = fminf(fabsf(z), 16.0f);  // further out the weight is 0 (of infinity too)
+    return __fmaf_rn(-size, half_erfc(size, &bell), max_nan(z, 0.0f));
+  }
+  if (ACT == OB_ACT_GELU_TANH) {
+    const float c = max_nan(z, -16.0f);
+    const float u = c * __fmaf_rn(kTanhA * kTanhB, c * c, kTanhA);
+    return c * act_rcp(1.0f + act_ex2(u * (-2.0f * kActLog2e)));
+  }
+  return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if (ACT == OB_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+  if (ACT == OB_ACT_GELU) {
+    float bell;
+    const float size = fminf(fabsf(z), 16.0f), tail = half_erfc(size, &bell);
+    const float phi = z < 0.0f ? tail : 1.0f - tail;
+    // a NaN stays one; size = 16 of an infinity has no bell left
+    return z != z ? z : __fmaf_rn(copysignf(size, z) * 0.3989422804f, bell, phi);
+  }
+  if (ACT == OB_ACT_GELU_TANH) {
+    const float c = max_nan(fminf(z, 16.0f), -16.0f);
+    const float u = c * __fmaf_rn(kTanhA * kTanhB, c * c, kTanhA);
+    const float s = act_rcp(1.0f + act_ex2(u * (-2.0f * kActLog2e)));
+    const float du = __fmaf_rn(3.0f * kTanhA * kTanhB, c * c, kTanhA);
+    return z != z ? z : __fmaf_rn(2.0f * c * s * (1.0f - s), du, s);
+  }
+  return 1.0f;
+}
+
+// f(std::integral_constant<int, act>) for the run-time code.
+template <typename F>
+__device__ __forceinline__ void by_act(int act, F f) {
+  if (act == OB_ACT_NONE)
+    f(std::integral_constant<int, OB_ACT_NONE>());
+  else if (act == OB_ACT_RELU)
+    f(std::integral_constant<int, OB_ACT_RELU>());
+  else if (act == OB_ACT_GELU)
+    f(std::integral_constant<int, OB_ACT_GELU>());
+  else
+    f(std::integral_constant<int, OB_ACT_GELU_TANH>());
+}
+
+}  // namespace ob

@@ -1,164 +1,289 @@
-// The dense layer: y = act(x w^T + b) + residual and its gradients.
+// The dense layer: y = act(x w^T + b) + residual and its gradients.  The
+// products are k_gemm.cu's; here is what is around them.
+//
+// dz = dy act'(z) is made once, as the operand of both products of the backward
+// pass, and summed down the columns on the way: each block adds its share of
+// the rows, a second kernel the blocks' sums in their order.  HBM bounds it.
+//
+// Copies by TMA want 16-byte boundaries: matrices that lie elsewhere are first
+// copied into the workspace, their rows padded to multiples of 16 bytes (the
+// products' time is many times that of the copy).
+#include <type_traits>
+
+#include "act.cuh"
 #include "elem.cuh"
 #include "layers.cuh"
+#include "model.cuh"
 
 namespace ob {
 namespace {
 
-constexpr float kSqrtHalf = 0.70710678f, kInvSqrt2Pi = 0.39894228f;
-constexpr float kTanhA = 0.79788456f, kTanhB = 0.044715f;
+constexpr int kDzThreads = 128;
 
-__device__ __forceinline__ float act_of(float z, int act) {
-  if (act == OB_ACT_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays one
-  if (act == OB_ACT_GELU) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
-  if (act == OB_ACT_GELU_TANH)
-    return 0.5f * z * (1.0f + tanhf(kTanhA * __fmaf_rn(kTanhB * z * z, z, z)));
-  return z;
-}
-__device__ __forceinline__ float act_slope(float z, int act) {
-  if (act == OB_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-  if (act == OB_ACT_GELU)
-    return __fmaf_rn(z * kInvSqrt2Pi, expf(-0.5f * z * z), 0.5f * (1.0f + erff(z * kSqrtHalf)));
-  if (act == OB_ACT_GELU_TANH) {
-    const float t = tanhf(kTanhA * __fmaf_rn(kTanhB * z * z, z, z));
-    return __fmaf_rn(0.5f * z * (1.0f - t * t), kTanhA * __fmaf_rn(3.0f * kTanhB, z * z, 1.0f),
-                     0.5f * (1.0f + t));
-  }
-  return 1.0f;
-}
-
-struct Epilogue {
-  const void *bias, *residual;
-  int64_t ldr;
-  void* z;
-  int64_t ldz;
+struct DzArgs {
+  Mat dy, z, dz;      // dz: data or null
+  float* partial;     // [parts][N], or null
+  int64_t M, N;
+  int parts, tx;      // threads of a block along the columns, a power of two
   int act;
 };
 
-// c[i][j] = sum over k of a(i, k) b(k, j); a(i, k) at a + i * am + k * ak.
-template <typename T>
-__global__ void __launch_bounds__(256)
-    k_product(const T* a, int64_t am, int64_t ak, const T* b, int64_t bk, int64_t bn, T* c,
-              int64_t ldc, int64_t M, int64_t N, int64_t K, Epilogue ep) {
-  __shared__ float as[16][65], bs[16][65];
-  const int64_t i0 = (int64_t)blockIdx.y * 64, j0 = (int64_t)blockIdx.x * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < K; k0 += 16) {
-    for (int t = threadIdx.x; t < 64 * 16; t += 256) {
-      const int64_t i = i0 + t / 16, k = k0 + t % 16, j = j0 + t % 64, kb = k0 + t / 64;
-      as[t % 16][t / 16] = i < M && k < K ? to_f32(a[i * am + k * ak]) : 0.0f;
-      bs[t / 64][t % 64] = j < N && kb < K ? to_f32(b[kb * bk + j * bn]) : 0.0f;
-    }
-    __syncthreads();
+// V columns a thread (8: 16-byte loads).
+template <typename T, int V>
+__global__ void __launch_bounds__(kDzThreads) k_dz(const __grid_constant__ DzArgs a) {
+  __shared__ float sums[kDzThreads * V];
+  grid_wait();
+  const int x = threadIdx.x & (a.tx - 1), y = threadIdx.x / a.tx, ty = kDzThreads / a.tx;
+  const int64_t n = ((int64_t)blockIdx.x * a.tx + x) * V;
+  const int64_t per = (a.M + a.parts - 1) / a.parts;
+  const int64_t r0 = (int64_t)blockIdx.y * per, r1 = r0 + per < a.M ? r0 + per : a.M;
+  float acc[V];
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
+  for (int k = 0; k < V; ++k) acc[k] = 0.0f;
+  if (n < a.N)
+    by_act(a.act, [&](auto act) {
+      constexpr int kAct = decltype(act)::value;
+#pragma unroll 4
+      for (int64_t r = r0 + y; r < r1; r += ty) {
+        const T* dy = static_cast<const T*>(a.dy.data) + r * a.dy.ld + n;
+        const T* z = static_cast<const T*>(a.z.data) + r * a.z.ld + n;
+        float g[V];
+        if constexpr (V == 8) {
+          const uint4 u = *reinterpret_cast<const uint4*>(dy);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (kAct != OB_ACT_NONE) v = *reinterpret_cast<const uint4*>(z);
+          const uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+          for (int k = 0; k < 4; ++k) {
+            const float2 d = unpack2<T>(w[k]), s = unpack2<T>(q[k]);
+            g[2 * k] = d.x * act_slope<kAct>(s.x);
+            g[2 * k + 1] = d.y * act_slope<kAct>(s.y);
+          }
+        } else {
+          g[0] = to_f32(*dy);
+          if (kAct != OB_ACT_NONE) g[0] *= act_slope<kAct>(to_f32(*z));
+        }
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-          acc[u][w] = __fmaf_rn(as[k][ty * 4 + u], bs[k][tx + 16 * w], acc[u][w]);
-    __syncthreads();
-  }
-  for (int u = 0; u < 4; ++u)
-    for (int w = 0; w < 4; ++w) {
-      const int64_t i = i0 + ty * 4 + u, j = j0 + tx + 16 * w;
-      if (i >= M || j >= N) continue;
-      float z = acc[u][w];
-      if (ep.bias) z += to_f32(static_cast<const T*>(ep.bias)[j]);
-      if (ep.z) static_cast<T*>(ep.z)[i * ep.ldz + j] = from_f32<T>(z);
-      float y = act_of(z, ep.act);
-      if (ep.residual) y += to_f32(static_cast<const T*>(ep.residual)[i * ep.ldr + j]);
-      c[i * ldc + j] = from_f32<T>(y);
-    }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256)
-    k_dz(const T* dy, int64_t lddy, const T* z, int64_t ldz, T* dz, int64_t M, int64_t N, int act) {
-  const int64_t i = blockIdx.y, j = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (j >= N) return;
-  for (int64_t r = i; r < M; r += gridDim.y)
-    dz[r * N + j] = from_f32<T>(to_f32(dy[r * lddy + j]) * act_slope(to_f32(z[r * ldz + j]), act));
-}
-
-template <typename T>
-__global__ void __launch_bounds__(1024)
-    k_dbias(const T* dy, int64_t lddy, const T* z, int64_t ldz, T* db, int64_t M, int64_t N,
-            int act) {
-  __shared__ float sum[32][33];
-  const int64_t j = (int64_t)blockIdx.x * 32 + threadIdx.x;
-  float t = 0.0f;
-  if (j < N)
-    for (int64_t r = threadIdx.y; r < M; r += 32) {
-      const float g = to_f32(dy[r * lddy + j]);
-      t += z ? g * act_slope(to_f32(z[r * ldz + j]), act) : g;
-    }
-  sum[threadIdx.y][threadIdx.x] = t;
+        for (int k = 0; k < V; ++k) acc[k] += g[k];
+        if (!a.dz.data) continue;
+        T* out = static_cast<T*>(a.dz.data) + r * a.dz.ld + n;
+        if constexpr (V == 8)
+          *reinterpret_cast<uint4*>(out) = make_uint4(pack2<T>(g[0], g[1]), pack2<T>(g[2], g[3]),
+                                                      pack2<T>(g[4], g[5]), pack2<T>(g[6], g[7]));
+        else
+          *out = from_f32<T>(g[0]);
+      }
+    });
+  if (!a.partial) return;
+#pragma unroll
+  for (int k = 0; k < V; ++k) sums[threadIdx.x * V + k] = acc[k];
   __syncthreads();
-  if (threadIdx.y == 0 && j < N) {
-    t = 0.0f;
-    for (int r = 0; r < 32; ++r) t += sum[r][threadIdx.x];
-    db[j] = from_f32<T>(t);
+  // a column a thread; its rows' sums in their order
+  for (int c = threadIdx.x; c < a.tx * V; c += kDzThreads) {
+    const int64_t col = (int64_t)blockIdx.x * a.tx * V + c;
+    if (col >= a.N) break;
+    float t = 0.0f;
+    for (int q = 0; q < ty; ++q) t += sums[q * a.tx * V + c];
+    a.partial[(int64_t)blockIdx.y * a.N + col] = t;
   }
 }
 
+// dbias from the parts: 32 columns a block, a warp every eighth part.
 template <typename T>
-void product(const T* a, int64_t am, int64_t ak, const T* b, int64_t bk, int64_t bn, T* c,
-             int64_t ldc, int64_t M, int64_t N, int64_t K, const Epilogue& ep, cudaStream_t s) {
-  const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 63) / 64));
-  k_product<T><<<grid, 256, 0, s>>>(a, am, ak, b, bk, bn, c, ldc, M, N, K, ep);
+__global__ void __launch_bounds__(256) k_dbias(const float* partial, int parts, int64_t N, T* out) {
+  __shared__ float sums[8][32];
+  grid_wait();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t n = (int64_t)blockIdx.x * 32 + lane;
+  float t = 0.0f;
+  if (n < N)
+#pragma unroll 8
+    for (int p = w; p < parts; p += 8) t += partial[(int64_t)p * N + n];
+  sums[w][lane] = t;
+  __syncthreads();
+  if (w || n >= N) return;
+  t = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) t += sums[k][lane];
+  out[n] = from_f32<T>(t);
+}
+
+__global__ void __launch_bounds__(256) k_realign(const uint16_t* from, int64_t ld, uint16_t* to,
+                                                 int64_t to_ld, int64_t rows, int64_t cols) {
+  grid_wait();
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c < cols)
+#pragma unroll 4
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) to[r * to_ld + c] = from[r * ld + c];
+}
+
+int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+bool on(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+bool by_tma(const Mat& m) { return on(m.data, 16) && m.ld % 8 == 0; }
+
+// How far the epilogue's rows are aligned: 2, 1 or 0.
+int wide_of(const Epilogue& e) {
+  int w = e.bias && !on(e.bias, 16) ? 0 : 2;
+  for (const Mat* m : {&e.out, &e.z, &e.residual}) {
+    if (!m->data) continue;
+    if (!by_tma(*m))
+      w = 0;
+    else if (w == 2 && !(on(m->data, 32) && m->ld % 16 == 0))
+      w = 1;
+  }
+  return w;
+}
+
+int power_of_two(int64_t n, int most) {
+  int p = 1;
+  while (p < n && p < most) p *= 2;
+  return p;
+}
+
+// Blocks along the rows of dz, by sizes alone (the workspace goes by it): eight
+// rows a thread at least, and 8 blocks an SM.
+int dz_parts(int64_t M, int64_t N) {
+  const int tx = power_of_two((N + 7) / 8, kDzThreads);
+  const int64_t columns = (N + 8 * tx - 1) / (8 * tx), rows = 8 * (kDzThreads / tx);
+  int64_t most = 8 * 152 / columns;
+  if (most < 1) most = 1;
+  const int64_t parts = (M + rows - 1) / rows;
+  return (int)(parts < 1 ? 1 : parts < most ? parts : most);
+}
+
+struct Area {  // the workspace, handed out in order
+  uint8_t* base;
+  size_t used;
+  void* take(size_t bytes) {
+    void* p = base + used;
+    used += up256(bytes);
+    return p;
+  }
+};
+
+size_t mat_bytes(int64_t rows, int64_t cols) { return up256((size_t)(rows * padded(cols)) * 2); }
+
+cudaError_t realign(Mat* m, int64_t rows, int64_t cols, Area* area, cudaStream_t s) {
+  if (rows == 0 || cols == 0 || by_tma(*m)) return cudaSuccess;
+  uint16_t* to = static_cast<uint16_t*>(area->take(mat_bytes(rows, cols)));
+  const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)(rows < 2048 ? rows : 2048));
+  const cudaError_t e = launch_behind(k_realign, grid, dim3(256), 0, s,
+                                      static_cast<const uint16_t*>(m->data), m->ld, to,
+                                      padded(cols), rows, cols);
+  *m = Mat{to, padded(cols)};
+  return e;
+}
+
+template <typename T>
+cudaError_t make_dz(const DzArgs& d, bool wide, cudaStream_t s) {
+  DzArgs a = d;
+  const int V = wide ? 8 : 1;
+  a.tx = power_of_two((a.N + V - 1) / V, kDzThreads);
+  const dim3 grid((unsigned)((a.N + (int64_t)a.tx * V - 1) / ((int64_t)a.tx * V)), a.parts);
+  return wide ? launch_behind(k_dz<T, 8>, grid, dim3(kDzThreads), 0, s, a)
+              : launch_behind(k_dz<T, 1>, grid, dim3(kDzThreads), 0, s, a);
 }
 
 }  // namespace
 
 size_t linear_workspace_bytes(const LinearArgs& a, bool backward) {
-  return backward && a.act != OB_ACT_NONE ? (size_t)(a.M * a.N) * 2 : 0;
+  const int64_t M = a.M, N = a.N, K = a.K, wr = a.w_kn ? K : N, wc = a.w_kn ? N : K;
+  size_t b = a.unaligned ? mat_bytes(M, K) + mat_bytes(wr, wc) : 0;
+  if (!backward) return b + up256(gemm_partial_bytes(M, N, K));
+  if (a.act != OB_ACT_NONE || a.unaligned) b += mat_bytes(M, N);
+  b += up256((size_t)dz_parts(M, N) * N * sizeof(float));
+  const size_t p = gemm_partial_bytes(M, K, N), q = gemm_partial_bytes(wr, wc, M);
+  return b + up256(p > q ? p : q);
 }
 
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t s) {
-  auto go = [&](auto zero) {
-    using T = decltype(zero);
-    const Epilogue ep{a.bias, a.residual.data, a.residual.ld, a.z.data, a.z.ld, a.act};
-    product<T>(static_cast<const T*>(a.x.data), a.x.ld, 1, static_cast<const T*>(a.w.data),
-               a.w_kn ? a.w.ld : 1, a.w_kn ? 1 : a.w.ld, static_cast<T*>(a.y.data), a.y.ld, a.M,
-               a.N, a.K, ep, s);
-    return cudaGetLastError();
-  };
-  return a.type == OB_TYPE_BF16 ? go(__nv_bfloat16()) : go(__half());
+  Area area{a.workspace, 0};
+  Gemm g{};
+  g.a = a.x;
+  g.b = a.w;
+  cudaError_t e = realign(&g.a, a.M, a.K, &area, s);
+  if (e == cudaSuccess) e = realign(&g.b, a.w_kn ? a.K : a.N, a.w_kn ? a.N : a.K, &area, s);
+  if (e != cudaSuccess) return e;
+  g.b_mn = a.w_kn;
+  g.M = a.M;
+  g.N = a.N;
+  g.K = a.K;
+  g.ep.bias = a.bias;
+  g.ep.residual = a.residual;
+  g.ep.z = a.z;
+  g.ep.out = a.y;
+  g.ep.act = a.act;
+  g.ep.type = a.type;
+  g.ep.wide = wide_of(g.ep);
+  g.partial = static_cast<float*>(area.take(0));
+  return launch_gemm(g, s);
 }
 
 cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t s) {
-  auto go = [&](auto zero) {
-    using T = decltype(zero);
-    const T* dz = static_cast<const T*>(a.dy.data);
-    int64_t lddz = a.dy.ld;
-    const T* z = a.act != OB_ACT_NONE ? static_cast<const T*>(a.z.data) : nullptr;
-    const T* dy = dz;
-    if (z && (a.dx.data || a.dw.data) && a.M > 0) {
-      T* to = reinterpret_cast<T*>(a.workspace);
-      const dim3 grid((unsigned)((a.N + 255) / 256), (unsigned)(a.M < 65535 ? a.M : 65535));
-      k_dz<T><<<grid, 256, 0, s>>>(dy, a.dy.ld, z, a.z.ld, to, a.M, a.N, a.act);
-      dz = to;
-      lddz = a.N;
+  Area area{a.workspace, 0};
+  const int64_t M = a.M, N = a.N, K = a.K, wr = a.w_kn ? K : N, wc = a.w_kn ? N : K;
+  const bool products = a.dx.data || a.dw.data;
+  cudaError_t e = cudaSuccess;
+  Mat dz = a.dy;
+  DzArgs d{};
+  const bool make = products && M > 0 && N > 0 && (a.act != OB_ACT_NONE || !by_tma(a.dy));
+  if (make) {
+    dz = Mat{area.take(mat_bytes(M, N)), padded(N)};
+    d.dz = dz;
+  }
+  if (a.dbias) d.partial = static_cast<float*>(area.take((size_t)dz_parts(M, N) * N * sizeof(float)));
+  if (make || a.dbias) {
+    d.dy = a.dy;
+    d.z = a.z;
+    d.M = M;
+    d.N = N;
+    d.act = a.act;
+    d.parts = dz_parts(M, N);
+    const bool wide = N % 8 == 0 && by_tma(a.dy) && (a.act == OB_ACT_NONE || by_tma(a.z));
+    e = a.type == OB_TYPE_BF16 ? make_dz<__nv_bfloat16>(d, wide, s) : make_dz<__half>(d, wide, s);
+    if (e == cudaSuccess && a.dbias) {
+      const dim3 grid((unsigned)((N + 31) / 32));
+      e = a.type == OB_TYPE_BF16
+              ? launch_behind(k_dbias<__nv_bfloat16>, grid, dim3(256), 0, s, d.partial, d.parts, N,
+                              static_cast<__nv_bfloat16*>(a.dbias))
+              : launch_behind(k_dbias<__half>, grid, dim3(256), 0, s, d.partial, d.parts, N,
+                              static_cast<__half*>(a.dbias));
     }
-    const Epilogue none{nullptr, nullptr, 0, nullptr, 0, OB_ACT_NONE};
-    const T *x = static_cast<const T*>(a.x.data), *w = static_cast<const T*>(a.w.data);
-    if (a.dx.data && a.M > 0)
-      product<T>(dz, lddz, 1, w, a.w_kn ? 1 : a.w.ld, a.w_kn ? a.w.ld : 1,
-                 static_cast<T*>(a.dx.data), a.dx.ld, a.M, a.K, a.N, none, s);
-    if (a.dw.data && a.w_kn)
-      product<T>(x, 1, a.x.ld, dz, lddz, 1, static_cast<T*>(a.dw.data), a.dw.ld, a.K, a.N, a.M,
-                 none, s);
-    else if (a.dw.data)
-      product<T>(dz, 1, lddz, x, a.x.ld, 1, static_cast<T*>(a.dw.data), a.dw.ld, a.N, a.K, a.M,
-                 none, s);
-    if (a.dbias)
-      k_dbias<T><<<(unsigned)((a.N + 31) / 32), dim3(32, 32), 0, s>>>(
-          dy, a.dy.ld, z, a.z.ld, static_cast<T*>(a.dbias), a.M, a.N, a.act);
-    return cudaGetLastError();
-  };
-  return a.type == OB_TYPE_BF16 ? go(__nv_bfloat16()) : go(__half());
+  }
+  Mat x = a.x, w = a.w;
+  if (e == cudaSuccess && a.dw.data) e = realign(&x, M, K, &area, s);
+  if (e == cudaSuccess && a.dx.data) e = realign(&w, wr, wc, &area, s);
+  if (e != cudaSuccess) return e;
+  Gemm g{};
+  g.ep.type = a.type;
+  g.ep.act = OB_ACT_NONE;
+  g.partial = static_cast<float*>(area.take(0));
+  if (a.dw.data) {  // dw[n][k] = sum over m of dz(m, n) x(m, k), or turned
+    g.a = a.w_kn ? x : dz;
+    g.b = a.w_kn ? dz : x;
+    g.a_mn = g.b_mn = 1;
+    g.M = wr;
+    g.N = wc;
+    g.K = M;
+    g.ep.out = a.dw;
+    g.ep.wide = wide_of(g.ep);
+    e = launch_gemm(g, s);
+  }
+  if (e == cudaSuccess && a.dx.data) {  // dx[m][k] = sum over n of dz(m, n) w(n, k)
+    g.a = dz;
+    g.b = w;
+    g.a_mn = 0;
+    g.b_mn = !a.w_kn;
+    g.M = M;
+    g.N = K;
+    g.K = N;
+    g.ep.out = a.dx;
+    g.ep.wide = wide_of(g.ep);
+    e = launch_gemm(g, s);
+  }
+  return e;
 }
 
 }  // namespace ob

@@ -4,6 +4,7 @@
 
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "ob.h"
@@ -44,6 +45,11 @@ struct Mat {
   int64_t ld;
 };
 
+// A map of `rows` rows of `cols` elements whose boxes are box_rows rows of 64
+// elements in 128-byte swizzle; what is outside reads as zero.
+cudaError_t matrix_tensor_map(CUtensorMap* map, const Mat& m, int type, int64_t rows, int64_t cols,
+                              int box_rows);
+
 struct LinearArgs {
   int type, act, w_kn, unaligned;
   int64_t M, N, K;
@@ -57,6 +63,31 @@ struct LinearArgs {
 size_t linear_workspace_bytes(const LinearArgs& a, bool backward);
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t s);
+// The device word where a wait that ran out leaves its code.
+cudaError_t linear_error_word(unsigned** word);
+
+// ---------------------------------------------------------------------------
+// One product C[M][N] = sum over k of A(m, k) B(n, k) with the dense layer's
+// epilogue (k_gemm.cu).
+// ---------------------------------------------------------------------------
+
+struct Epilogue {
+  const void* bias;          // [N], or null
+  Mat residual, z, out;      // residual and z: data or null
+  int act, type;
+  int wide;                  // rows, and bias, are aligned to 2: 32, 1: 16 bytes, 0: less
+};
+
+struct Gemm {
+  Mat a, b;
+  int a_mn, b_mn;            // stored [K][M] or [K][N] instead of [M][K] or [N][K]
+  int64_t M, N, K;
+  Epilogue ep;
+  float* partial;            // gemm_partial_bytes
+};
+
+size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K);
+cudaError_t launch_gemm(const Gemm& g, cudaStream_t s);
 
 constexpr int kAdamBlock = 256;  // elements that share a unit, and the state's grain
 

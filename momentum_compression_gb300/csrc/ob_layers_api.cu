@@ -70,6 +70,10 @@ ob_status check_linear(const ob_linear* l) {
   if (l->M < 0 || l->N < 0 || l->K < 0 || l->M >= kMost || l->N >= kMost || l->K >= kMost)
     return failf(OB_ERR_INVALID, "M = %lld, N = %lld, K = %lld must be in [0, 2^30)",
                  (long long)l->M, (long long)l->N, (long long)l->K);
+  const int64_t most = 1ll << 40;
+  if (l->M * l->N > most || l->M * l->K > most || l->N * l->K > most)
+    return failf(OB_ERR_INVALID, "M = %lld, N = %lld, K = %lld: a matrix is over 2^40 elements",
+                 (long long)l->M, (long long)l->N, (long long)l->K);
   return OB_OK;
 }
 
@@ -282,6 +286,21 @@ ob_status ob_linear_bwd(const ob_linear* l, const ob_matrix* dy, const ob_matrix
   OB_TRY(check_workspace(workspace, workspace_bytes, ob::linear_workspace_bytes(a, true), 256));
   a.workspace = static_cast<uint8_t*>(workspace);
   return launched(ob::launch_linear_bwd(a, reinterpret_cast<cudaStream_t>(stream)), "linear_bwd");
+}
+
+ob_status ob_linear_device_error(unsigned* code, ob_stream_t stream) {
+  OB_TRACE();
+  if (!code) return failf(OB_ERR_INVALID, "linear_device_error: code is NULL");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  unsigned* word = nullptr;
+  unsigned v = 0;
+  cudaError_t e = ob::linear_error_word(&word);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&v, word, sizeof v, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof v, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return launched(e, "linear_device_error");
+  *code = v;
+  return OB_OK;
 }
 
 ob_status ob_adamw_step(const ob_adamw* a, const ob_adamw_tensor* tensors,

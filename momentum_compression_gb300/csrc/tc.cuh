@@ -127,10 +127,11 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t stride) {
          (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// kind::f16, fp32 accumulation, M = 128, both operands bf16 or both f16.
-__host__ __device__ constexpr uint32_t mma_shape(bool bf16, int N, bool b_mn) {
-  return 1u << 4 | (bf16 ? 1u : 0u) << 7 | (bf16 ? 1u : 0u) << 10 | (b_mn ? 1u : 0u) << 16 |
-         (uint32_t)(N >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+// kind::f16, fp32 accumulation, both operands bf16 or both f16; M = 256 by a pair of blocks.
+__host__ __device__ constexpr uint32_t mma_shape(bool bf16, int N, bool b_mn, bool a_mn = false,
+                                                 int M = 128) {
+  return 1u << 4 | (bf16 ? 1u : 0u) << 7 | (bf16 ? 1u : 0u) << 10 | (a_mn ? 1u : 0u) << 15 |
+         (b_mn ? 1u : 0u) << 16 | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
 }
 
 // One lane of a whole warp, the same one every time.  The products are issued
@@ -184,6 +185,14 @@ __device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, int
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
+__device__ __forceinline__ void tma_load2(void* dst, const CUtensorMap* map, int x, int y,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
 // A cluster's blocks wait for one another here, and see what was written
 // before; every thread of every block takes part.
 __device__ __forceinline__ void cluster_sync() {
@@ -211,6 +220,60 @@ __device__ __forceinline__ float4 cluster_ld4(uint32_t addr, uint32_t rank) {
                : "r"(cluster_addr(addr, rank))
                : "memory");
   return v;
+}
+
+
+// ---------------------------------------------------------------------------
+// A pair of blocks (a cluster of two) on one product: D has 256 rows, each block
+// holds 128 of A's and of D's and half of B's.  The block of rank 0 issues.
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Into this block's shared memory; the bytes are counted on the barrier at cluster
+// address `bar`, of either block.
+__device__ __forceinline__ void pair_load2(void* dst, const CUtensorMap* map, int x, int y,
+                                           uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+// By one whole warp of each of the two.
+__device__ __forceinline__ void pair_alloc(uint32_t* dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(dst)),
+               "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void pair_free(uint32_t base, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
+}
+__device__ __forceinline__ void pair_mma(uint32_t leader, uint32_t d, uint64_t a, uint64_t b,
+                                         uint32_t shape, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add), "r"(leader)
+      : "memory");
+}
+// Arrives on `bar`, at the same place of both blocks, when the products are done.
+__device__ __forceinline__ void pair_commit(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t.reg .b16 m;\n\tsetp.ne.u32 q, %1, 0;\n\tmov.b16 m, 3;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], m;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+// On a barrier at a cluster address.
+__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {

@@ -23,6 +23,8 @@ def _cuda():
     torch.cuda.set_device(0)
     from momentum_compression_gb300 import _build
     _build.build()
+    yield
+    assert ob.ob_linear_device_error() == 0
 
 
 def _gen(seed):
@@ -217,6 +219,39 @@ def test_dense_gradient(dtype, Mr, N, K, kn, pad, shift):
     ob.ob_linear_bwd(dy, x, w, dw=dw2, **kw)
     ob.ob_linear_bwd(dy, x, w, dbias=db2, **kw)
     assert torch.equal(dx, dx2) and torch.equal(dw.t() if kn else dw, dw2) and torch.equal(db, db2)
+
+
+# sizes that take pairs of blocks, whole and cut along the sum, forward or backward
+LARGE = [(2560, 1024, 256), (2570, 1030, 1000), (2816, 2304, 4096), (9000, 1100, 1300), (5000, 2048, 136),
+         (600, 5000, 2100)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("Mr,N,K", LARGE)
+@pytest.mark.parametrize("kn", [False, True])
+def test_dense_of_large_sizes(dtype, Mr, N, K, kn):
+    mk, x, w, b, r = _dense_case(Mr, N, K, dtype, kn, 0, 0, 3)
+    y, clean = _guarded(Mr, N, 0, 0, dtype)
+    z, z_clean = _guarded(Mr, N, 0, 0, dtype)
+    ob.ob_linear_fwd(x, w, y, b, r, z, "gelu")
+    clean()
+    z_clean()
+    (z64, y64), (ez, ey) = L.dense(x, w, b, r, "gelu")
+    L.within(y, y64, ey, "y")
+    L.within(z, z64, ez, "z")
+    for got, want in ((y, y64), (z, z64)):
+        assert (got.double() - want).norm() <= 1.02 * (want.to(dtype).double() - want).norm()
+    dx, x_clean = _guarded(Mr, K, 0, 0, dtype)
+    dw, w_clean = _guarded(*((K, N) if kn else (N, K)), 0, 0, dtype)
+    dwt, db = dw.t() if kn else dw, torch.empty_like(b)
+    ob.ob_linear_bwd(r, x, w, dx, dwt, db, z=z, activation="gelu")
+    x_clean()
+    w_clean()
+    want, err = L.dense_grad(r, x, w, z, "gelu")
+    for got, a, e, n in zip((dx, dwt, db), want, err, ("dx", "dw", "db")):
+        L.within(got, a, e, n)
+        once = (a.to(dtype).double() - a).norm()
+        assert (got.double() - a).norm() <= math.sqrt(1 + 1.1 ** 2) * once, n
 
 
 @pytest.mark.parametrize("Mr,N,K", [(0, 5, 7), (5, 0, 7), (5, 7, 0), (0, 0, 0), (130, 9, 0)])

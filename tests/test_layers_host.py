@@ -70,7 +70,7 @@ def test_dense_refuses():
     ok = [lin(), mat(0x1000, 64), mat(0x2000, 64), 0x3000, mat(0x4000, 32), mat(0x5000, 32), mat(0x6000, 32),
           0x7000, 1 << 30, None]
     _refuses(f, ok, [(0, None, BAD), (0, lin(type=0), UNSUPPORTED), (0, lin(act=4), BAD), (0, lin(act=-1), BAD),
-                     (0, lin(M=-1), BAD), (0, lin(N=1 << 30), BAD), (0, lin(K=1 << 30), BAD), (1, None, BAD),
+                     (0, lin(M=-1), BAD), (0, lin(N=1 << 30), BAD), (0, lin(K=1 << 30), BAD), (0, lin(M=1 << 29, N=1 << 29), BAD), (1, None, BAD),
                      (2, None, BAD), (6, None, BAD), (1, mat(0x1002, 64), ALIGN), (1, mat(0x1000, 65), ALIGN),
                      (1, mat(0x1000, 56), BAD), (2, mat(0x2000, 56), BAD), (2, mat(0x2008, 64), ALIGN),
                      (4, mat(0x4008, 32), ALIGN), (5, mat(0x5000, 33), ALIGN), (6, mat(0x6002, 32), ALIGN),
