@@ -4,10 +4,13 @@
 //   dw = sum over rows of dy xhat,  db = sum over rows of dy
 // The variance is that of the centred values (a second pass over the row),
 // never a difference of squares.  All sums are fp32.
+#include <type_traits>
+
 #include "elem.cuh"
 #include "layers.cuh"
 #include "model.cuh"
 #include "ob_internal.cuh"
+#include "ptx.cuh"
 
 namespace ob {
 namespace {
@@ -116,16 +119,345 @@ __global__ void __launch_bounds__(kStrip * kStripRows) k_ln_dw_wide(const LayerN
   }
 }
 
-// dweight and dbias from the parts, in a fixed order.
-__global__ void __launch_bounds__(256) k_ln_sums(const LayerNormBwdArgs a) {
+// ---------------------------------------------------------------------------
+// Rows in registers.  A thread has CH chunks of eight columns: consecutive ones
+// where everything lies on 16 bytes (VEC), else every `threads`-th, so that
+// narrow accesses of a warp still lie side by side.
+// ---------------------------------------------------------------------------
+
+template <bool VEC>
+__device__ __forceinline__ int column(int c, int j, int t, int threads) {
+  return VEC ? (c * threads + t) * 8 + j : (c * 8 + j) * threads + t;
+}
+
+// Chunk c as it lies in memory; what is past the row stays 0.
+template <typename T, bool VEC>
+struct Chunk {
+  uint4 raw[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* row, int c, int t, int threads, int cols) {
+    constexpr int kWords = sizeof(T) / 2;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+    if constexpr (VEC) {
+      const int at = column<true>(c, 0, t, threads);
+      if (at < cols) {
+        const uint4* p = reinterpret_cast<const uint4*>(row + at);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) raw[i] = p[i];
+      }
+    } else {
+      T v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = column<false>(c, j, t, threads);
+        v[j] = from_f32<T>(0.0f);
+        if (at < cols) v[j] = row[at];
+      }
+      memcpy(raw, v, sizeof raw);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    if constexpr (sizeof(T) == 4) {
+      memcpy(v, raw, 32);
+    } else {
+      const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2<T>(w[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void put(const float (&v)[8]) {
+    if constexpr (sizeof(T) == 4)
+      memcpy(raw, v, 32);
+    else
+      raw[0] = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]),
+                          pack2<T>(v[6], v[7]));
+  }
+  __device__ __forceinline__ void store(T* row, int c, int t, int threads, int cols) const {
+    if constexpr (VEC) {
+      const int at = column<true>(c, 0, t, threads);
+      if (at < cols) {
+        uint4* p = reinterpret_cast<uint4*>(row + at);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) p[i] = raw[i];
+      }
+    } else {
+      T v[8];
+      memcpy(v, raw, sizeof raw);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = column<false>(c, j, t, threads);
+        if (at < cols) row[at] = v[j];
+      }
+    }
+  }
+};
+
+// Eight weights of the thread's chunk, by their run-time type.
+template <bool VEC>
+__device__ __forceinline__ void load_weights(float (&w)[8], const void* p, int type, float none,
+                                             int c, int t, int threads, int cols) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = none;
+  if (!p) return;
+  if (type == OB_TYPE_F32) {
+    Chunk<float, VEC> k;
+    k.load(static_cast<const float*>(p), c, t, threads, cols);
+    k.get(w);
+  } else if (type == OB_TYPE_BF16) {
+    Chunk<__nv_bfloat16, VEC> k;
+    k.load(static_cast<const __nv_bfloat16*>(p), c, t, threads, cols);
+    k.get(w);
+  } else {
+    Chunk<__half, VEC> k;
+    k.load(static_cast<const __half*>(p), c, t, threads, cols);
+    k.get(w);
+  }
+}
+
+// A row a warp (MULTI false, eight rows a block) or a row a block.
+template <typename T, int CH, bool VEC, bool MULTI>
+__global__ void __launch_bounds__(MULTI ? 1024 : 256) k_ln_fwd(const __grid_constant__ LayerNormArgs a) {
+  __shared__ float buf[33];
+  const int threads = MULTI ? blockDim.x : 32, t = MULTI ? threadIdx.x : threadIdx.x & 31;
+  const uint64_t first = MULTI ? blockIdx.x : (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const uint64_t step = MULTI ? gridDim.x : (uint64_t)gridDim.x * 8;
+  auto row_sum = [&](float v) { return MULTI ? block_sum(v, buf) : warp_butterfly_sum(v); };
   grid_wait();
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= 2 * a.cols) return;
-  void* to = i < a.cols ? a.dweight : a.dbias;
-  if (!to) return;
+  for (uint64_t row = first; row < a.rows; row += step) {
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    float v[CH][8];
+    Chunk<T, VEC> in[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) in[c].load(x, c, t, threads, a.cols);
+    if (a.residual) {
+      const T* r = static_cast<const T*>(a.residual) + row * a.ldr;
+      Chunk<T, VEC> k[CH];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) k[c].load(r, c, t, threads, a.cols);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        float p[8], q[8];
+        in[c].get(p);
+        k[c].get(q);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] += q[j];
+        in[c].put(p);  // the sum as it is kept
+        if (a.sum) in[c].store(static_cast<T*>(a.sum) + row * a.lds, c, t, threads, a.cols);
+      }
+    }
+    float total = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      in[c].get(v[c]);
+      total += ((v[c][0] + v[c][1]) + (v[c][2] + v[c][3])) + ((v[c][4] + v[c][5]) + (v[c][6] + v[c][7]));
+    }
+    const float mean = row_sum(total) / (float)a.cols;
+    float square = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[c][j] -= mean;
+        if (column<VEC>(c, j, t, threads) < a.cols) square = __fmaf_rn(v[c][j], v[c][j], square);
+      }
+    const float rstd = 1.0f / sqrtf(row_sum(square) / (float)a.cols + a.eps);
+    T* y = static_cast<T*>(a.y) + row * a.ldy;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float w[8], b[8];
+      load_weights<VEC>(w, a.weight, a.w_type, 1.0f, c, t, threads, a.cols);
+      load_weights<VEC>(b, a.bias, a.w_type, 0.0f, c, t, threads, a.cols);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[c][j] = __fmaf_rn(v[c][j] * rstd, w[j], b[j]);
+      Chunk<T, VEC> out;
+      out.put(v[c]);
+      out.store(y, c, t, threads, a.cols);
+    }
+    if (t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+  }
+}
+
+// The sums over a warp of N = 2 R values each lane has, N a power of two up to 8: halves
+// of the values change sides first, so that N + log2(32 / N) - 1 exchanges do.  Value
+// lane / (32 / N) is returned.
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+  int o = 16;
+#pragma unroll
+  for (int n = N / 2; n >= 1; n /= 2, o /= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      const float send = up ? v[k] : v[k + n], keep = up ? v[k + n] : v[k];
+      v[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  float r = v[0];
+#pragma unroll
+  for (; o >= 1; o /= 2) r += __shfl_xor_sync(0xffffffffu, r, o);
+  return r;
+}
+
+constexpr int kBwdThreads = 256;
+
+// dx and the block's sums of dy xhat and dy.  A group of threads has a row's
+// columns, the same ones for every row, and takes R rows at a time.
+template <typename T, int CH, int R, bool VEC>
+__global__ void __launch_bounds__(kBwdThreads, 2)
+    k_ln_bwd(const __grid_constant__ LayerNormBwdArgs a, int threads) {
+  constexpr int N = 2 * R;
+  __shared__ __align__(16) float part[2][kBwdThreads / 32][N];
+  __shared__ float merge[kBwdThreads * 8];
+  const int t = threadIdx.x & (threads - 1), group = threadIdx.x / threads;
+  const int groups = kBwdThreads / threads, warps = threads / 32, warp = threadIdx.x >> 5;
+  const float inv = 1.0f / (float)a.cols;
+  grid_wait();
+  float w[CH][8], dw[CH][8], db[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    load_weights<VEC>(w[c], a.weight, a.w_type, 1.0f, c, t, threads, a.cols);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[c][j] = db[c][j] = 0.0f;
+  }
+  int flip = 0;
+  const uint64_t step = (uint64_t)gridDim.x * groups * R;
+  for (uint64_t r0 = ((uint64_t)blockIdx.x * groups + group) * R; r0 < a.rows; r0 += step) {
+    Chunk<T, VEC> x[R][CH], g[R][CH], s[R][CH];
+    float mean[R], rstd[R], sums[N];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool in = r0 + r < a.rows;
+      const uint64_t row = in ? r0 + r : a.rows - 1;
+      const int cols = in ? a.cols : 0;
+      mean[r] = a.mean[row];
+      rstd[r] = a.rstd[row];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        x[r][c].load(static_cast<const T*>(a.x) + row * a.ldx, c, t, threads, cols);
+        g[r][c].load(static_cast<const T*>(a.dy) + row * a.lddy, c, t, threads, cols);
+      }
+    }
+    if (a.dsum)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r0 + r < a.rows)
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+            s[r][c].load(static_cast<const T*>(a.dsum) + (r0 + r) * a.ldds, c, t, threads, a.cols);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      sums[2 * r] = sums[2 * r + 1] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        float xv[8], gv[8];
+        x[r][c].get(xv);
+        g[r][c].get(gv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {  // a column past the row has no dy
+          const float h = gv[j] * w[c][j];
+          const float xhat = (xv[j] - mean[r]) * rstd[r];
+          sums[2 * r] += h;
+          if (VEC || column<VEC>(c, j, t, threads) < a.cols)
+            sums[2 * r + 1] = __fmaf_rn(h, xhat, sums[2 * r + 1]);
+          if (r0 + r < a.rows) {
+            dw[c][j] = __fmaf_rn(gv[j], xhat, dw[c][j]);
+            db[c][j] += gv[j];
+          }
+        }
+      }
+    }
+    if (!a.dx) continue;
+    const float mine = warp_sums<N>(sums);
+    float m[N];
+    if (threads == 32) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) m[k] = __shfl_sync(0xffffffffu, mine, k * (32 / N)) * inv;
+    } else {
+      if ((threadIdx.x & (32 / N - 1)) == 0) part[flip][warp][(threadIdx.x & 31) / (32 / N)] = mine;
+      named_sync(1 + group, threads);
+#pragma unroll
+      for (int k = 0; k < N; ++k) m[k] = 0.0f;
+      for (int q = 0; q < warps; ++q)
+#pragma unroll
+        for (int k = 0; k < N; ++k) m[k] += part[flip][group * warps + q][k];
+#pragma unroll
+      for (int k = 0; k < N; ++k) m[k] *= inv;
+      flip ^= 1;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r0 + r >= a.rows) break;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        float xv[8], gv[8];
+        x[r][c].get(xv);
+        g[r][c].get(gv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float xhat = (xv[j] - mean[r]) * rstd[r];
+          gv[j] = rstd[r] * __fmaf_rn(-xhat, m[2 * r + 1], gv[j] * w[c][j] - m[2 * r]);
+        }
+        if (a.dsum) {
+          s[r][c].get(xv);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) gv[j] += xv[j];
+        }
+        g[r][c].put(gv);
+        g[r][c].store(static_cast<T*>(a.dx) + (r0 + r) * a.lddx, c, t, threads, a.cols);
+      }
+    }
+  }
+  if (!a.partial) return;
+  // the groups' sums in their order
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      if (groups > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) merge[j * kBwdThreads + threadIdx.x] = which ? db[c][j] : dw[c][j];
+        __syncthreads();
+      }
+      if (group) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = column<VEC>(c, j, t, threads);
+        if (at >= a.cols) continue;
+        float v = which ? db[c][j] : dw[c][j];
+        for (int q = 1; q < groups; ++q) v += merge[j * kBwdThreads + q * threads + t];
+        a.partial[((size_t)blockIdx.x * 2 + which) * a.cols + at] = v;
+      }
+    }
+}
+
+// dweight and dbias from the parts, in a fixed order: 32 sums a block, a warp every
+// eighth part.
+__global__ void __launch_bounds__(256) k_ln_sums(const __grid_constant__ LayerNormBwdArgs a) {
+  __shared__ float sums[8][32];
+  grid_wait();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int i = blockIdx.x * 32 + lane;
   float t = 0.0f;
-  for (int p = 0; p < a.parts; ++p) t += a.partial[(size_t)p * 2 * a.cols + i];
-  store_from_f32(to, i < a.cols ? i : i - a.cols, a.w_type, t);
+  if (i < 2 * a.cols)
+#pragma unroll 8
+    for (int p = w; p < a.parts; p += 8) t += a.partial[(size_t)p * 2 * a.cols + i];
+  sums[w][lane] = t;
+  __syncthreads();
+  if (w || i >= 2 * a.cols) return;
+  t = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) t += sums[k][lane];
+  void* to = i < a.cols ? a.dweight : a.dbias;
+  if (to) store_from_f32(to, i < a.cols ? i : i - a.cols, a.w_type, t);
 }
 
 template <typename F>
@@ -137,32 +469,102 @@ cudaError_t by_type(int type, F f) {
 
 int row_blocks(uint64_t rows) { return (int)(rows < 65535 ? rows : 65535); }
 
+bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+constexpr int kSms = 152;
+constexpr int kFwdMost = 1024 * 8 * 4;  // columns that a block's registers hold
+constexpr int kBwdMost = kBwdThreads * 8 * 2;
+
+template <typename T, bool VEC>
+cudaError_t fwd(const LayerNormArgs& a, cudaStream_t s) {
+  const int chunks = (a.cols + 7) / 8;
+  // A row a warp needs no barrier, a row a block more of them at a time: the latter
+  // where the rows alone do not fill the card.
+  if (chunks <= 256 && (chunks <= 32 || a.rows >= (uint64_t)kSms * 8)) {
+    const uint64_t blocks = (a.rows + 7) / 8;
+    const int grid = (int)(blocks < (uint64_t)kSms * 32 ? blocks : kSms * 32);
+    auto go = [&](auto ch) {
+      return launch_behind(k_ln_fwd<T, decltype(ch)::value, VEC, false>, dim3(grid), dim3(256), 0, s, a);
+    };
+    if (chunks <= 32) return go(std::integral_constant<int, 1>());
+    if (chunks <= 64) return go(std::integral_constant<int, 2>());
+    if (chunks <= 128) return go(std::integral_constant<int, 4>());
+    return go(std::integral_constant<int, 8>());
+  }
+  const int grid = (int)(a.rows < (uint64_t)kSms * 16 ? a.rows : kSms * 16);
+  const bool few = a.rows < kSms && chunks <= 1024;
+  const int threads = few ? (chunks + 31) / 32 * 32 : (chunks + 127) / 128 * 32;
+  return few ? launch_behind(k_ln_fwd<T, 1, VEC, true>, dim3(grid), dim3(threads), 0, s, a)
+             : launch_behind(k_ln_fwd<T, 4, VEC, true>, dim3(grid), dim3(threads), 0, s, a);
+}
+
+// Threads of a group: a power of two from 32, so that CH chunks each hold the row.
+int group_threads(int cols, int ch) {
+  int t = 32;
+  while (t * 8 * ch < cols) t *= 2;
+  return t;
+}
+
+template <typename T, bool VEC>
+cudaError_t bwd(const LayerNormBwdArgs& a, cudaStream_t s) {
+  constexpr int R = sizeof(T) == 4 ? 2 : 4;
+  if (a.cols <= kBwdThreads * 8)
+    return launch_behind(k_ln_bwd<T, 1, R, VEC>, dim3(a.parts), dim3(kBwdThreads), 0, s, a,
+                         group_threads(a.cols, 1));
+  return launch_behind(k_ln_bwd<T, 2, R / 2, VEC>, dim3(a.parts), dim3(kBwdThreads), 0, s, a,
+                       group_threads(a.cols, 2));
+}
+
 }  // namespace
 
 cudaError_t launch_layernorm_fwd(const LayerNormArgs& a, int type, cudaStream_t s) {
   return by_type(type, [&](auto zero) {
     using T = decltype(zero);
-    k_ln_fwd_wide<T><<<row_blocks(a.rows), kWide, 0, s>>>(a);
-    return cudaGetLastError();
+    if (a.cols > kFwdMost) {
+      k_ln_fwd_wide<T><<<row_blocks(a.rows), kWide, 0, s>>>(a);
+      return cudaGetLastError();
+    }
+    bool vec = a.cols % 8 == 0 && on16(a.weight) && on16(a.bias);
+    const void* p[4] = {a.x, a.residual, a.y, a.sum};
+    const uint64_t ld[4] = {a.ldx, a.ldr, a.ldy, a.lds};
+    for (int i = 0; i < 4; ++i)
+      if (p[i]) vec = vec && on16(p[i]) && (a.rows == 1 || ld[i] * sizeof(T) % 16 == 0);
+    return vec ? fwd<T, true>(a, s) : fwd<T, false>(a, s);
   });
 }
 
-int layernorm_bwd_parts(uint64_t rows, int) {
-  return (int)(rows < 64 ? 1 : rows / 64 < 64 ? rows / 64 : 64);
+int layernorm_bwd_parts(uint64_t rows, int cols) {
+  if (cols > kBwdMost) return (int)(rows < 64 ? 1 : rows / 64 < 64 ? rows / 64 : 64);
+  // two blocks an SM, as far as there are rows for them
+  const uint64_t per = kBwdThreads / group_threads(cols, cols <= kBwdThreads * 8 ? 1 : 2);
+  const uint64_t want = (rows + per - 1) / per;
+  return (int)(want < 2 * kSms ? want : 2 * kSms);
 }
 
-cudaError_t launch_layernorm_bwd(const LayerNormBwdArgs& a, int type, cudaStream_t s) {
+cudaError_t launch_layernorm_bwd(const LayerNormBwdArgs& b, int type, cudaStream_t s) {
   return by_type(type, [&](auto zero) {
     using T = decltype(zero);
-    if (a.dx) k_ln_dx_wide<T><<<row_blocks(a.rows), kWide, 0, s>>>(a);
-    if (a.dweight || a.dbias) {
-      const dim3 grid((a.cols + kStrip - 1) / kStrip, a.parts);
-      k_ln_dw_wide<T><<<grid, dim3(kStrip, kStripRows), 0, s>>>(a);
-      cudaError_t e = cudaGetLastError();
-      if (e != cudaSuccess) return e;
-      return launch_behind(k_ln_sums, (2 * a.cols + 255) / 256, 256, 0, s, a);
+    LayerNormBwdArgs a = b;
+    const bool sums = a.dweight || a.dbias;
+    if (!sums) a.partial = nullptr;
+    cudaError_t e = cudaSuccess;
+    if (a.cols > kBwdMost) {
+      if (a.dx) k_ln_dx_wide<T><<<row_blocks(a.rows), kWide, 0, s>>>(a);
+      if (sums) {
+        const dim3 grid((a.cols + kStrip - 1) / kStrip, a.parts);
+        k_ln_dw_wide<T><<<grid, dim3(kStrip, kStripRows), 0, s>>>(a);
+      }
+      e = cudaGetLastError();
+    } else {
+      bool vec = a.cols % 8 == 0 && on16(a.weight);
+      const void* p[4] = {a.x, a.dy, a.dx, a.dsum};
+      const uint64_t ld[4] = {a.ldx, a.lddy, a.lddx, a.ldds};
+      for (int i = 0; i < 4; ++i)
+        if (p[i]) vec = vec && on16(p[i]) && (a.rows == 1 || ld[i] * sizeof(T) % 16 == 0);
+      e = vec ? bwd<T, true>(a, s) : bwd<T, false>(a, s);
     }
-    return cudaGetLastError();
+    if (e != cudaSuccess || !sums) return e;
+    return launch_behind(k_ln_sums, dim3((2 * a.cols + 31) / 32), dim3(256), 0, s, a);
   });
 }
 
