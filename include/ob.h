@@ -859,7 +859,7 @@ ob_status ob_linear_device_error(unsigned* code, ob_stream_t stream);
 typedef struct {
   int state_bits;           /* 8 or 32 */
   int grad_type;            /* OB_TYPE_*, of every gradient */
-  double lr, b1, b2, eps;   /* lr >= 0; b1, b2 in [0, 1); eps in [1e-18, 1] */
+  double lr, b1, b2, eps;   /* lr >= 0; b1, b2 in [0, 1); eps in [1e-12, 1] */
   uint64_t seed;            /* state_bits 8 */
   const float* lr_device;   /* on the device, instead of lr; or NULL */
   const float* grad_scale;  /* on the device, or NULL (1) */
@@ -874,9 +874,9 @@ typedef struct {
 } ob_adamw_tensor;
 
 /* grads: `count` pointers; a tensor whose gradient is NULL is left as it is,
- * its moments too.  p, copy and gradients are aligned to their element, 16
- * bytes for the fast path, and must not overlap; m and v are 16-byte aligned,
- * counter 8-byte. */
+ * its moments too.  p, copy and gradients are aligned to their element, 32
+ * bytes (16 of 2-byte types) for the fast path, and must not overlap; m and v are
+ * 32-byte aligned, counter 8-byte. */
 ob_status ob_adamw_step(const ob_adamw* a, const ob_adamw_tensor* tensors,
                         const void* const* grads, int count, void* m, void* v, uint8_t* m_exp,
                         uint8_t* v_exp, double* counter, ob_stream_t stream);

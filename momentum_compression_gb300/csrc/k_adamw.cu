@@ -18,6 +18,7 @@ namespace ob {
 namespace {
 
 constexpr int kAdamThreads = 256;
+constexpr int kAdamGrid = 3 * 152;  // all that run at a time
 
 template <int CAP>
 struct AdamTable {
@@ -38,17 +39,50 @@ struct AdamStep {  // of the whole call
   int skip;
 };
 
-// Codes of a moment: an exponent field with bias BIAS, three bits of significand.
-template <int BIAS>
-__device__ __forceinline__ float decode(uint32_t c, float unit) {
-  constexpr uint32_t nan = BIAS == 7 ? 127u : 255u;
-  const uint32_t size = BIAS == 7 ? c & 127u : c;
-  // as fp32 bits it is the value times 2^(BIAS - 127), below the normal range too
-  const float v = __uint_as_float(size << 20) * __uint_as_float((uint32_t)(254 - BIAS) << 23) * unit;
-  if (size == nan) return __uint_as_float(0x7fffffffu);
-  return BIAS == 7 && (c & 128u) ? -v : v;
+// ---------------------------------------------------------------------------
+// Moments in 8 bits
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ float power_of_two(int e) {  // biased, 1..254
+  return __uint_as_float((uint32_t)e << 23);
 }
-__device__ __forceinline__ float unit_of(uint32_t e) { return __uint_as_float(e << 23); }
+
+// Four codes of m, which are floats of a type that the hardware converts.
+__device__ __forceinline__ void decode_m(uint32_t w, float unit, float* m) {
+  uint32_t h[2];
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(h[0]), "=r"(h[1])
+      : "r"(w));
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float2 f = unpack2<__half>(h[k]);
+    m[2 * k] = f.x * unit;
+    m[2 * k + 1] = f.y * unit;
+  }
+}
+// Four of v: as fp32 bits, twenty places up, a code is its value times 2^-104, below the
+// normal range too.  `up` is 2^104 times the unit as far as fp32 goes, `more` the rest.
+struct VUnit {
+  float up, more;
+  __device__ __forceinline__ explicit VUnit(int e) {
+    up = e ? power_of_two(min(e + 104, 254)) : 0.0f;
+    more = power_of_two(max(e + 104 - 254, 0) + 127);
+  }
+};
+__device__ __forceinline__ void decode_v(uint32_t w, const VUnit& u, float* v) {
+  v[0] = __uint_as_float((w << 20) & 0x0ff00000u) * u.up;
+  v[1] = __uint_as_float((w << 12) & 0x0ff00000u) * u.up;
+  v[2] = __uint_as_float((w << 4) & 0x0ff00000u) * u.up;
+  v[3] = __uint_as_float((w >> 4) & 0x0ff00000u) * u.up;
+  if (u.more != 1.0f)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] *= u.more;
+  if (__vcmpeq4(w, 0xffffffffu))
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if ((w >> (8 * k) & 255u) == 255u) v[k] = __uint_as_float(0x7fffffffu);
+}
 
 // E of a block whose largest finite value has bits `top`.
 template <int BIAS>
@@ -57,21 +91,101 @@ __device__ __forceinline__ int block_exp(uint32_t top) {
   return top == 0 ? 0 : min(max(e, BIAS == 7 ? 1 : 3), 246);
 }
 
+// The code of size >= 0, finite, in the unit 1 / up, `noise` the random bits four places
+// up: below the normal codes the smallest normal one is added first, toward zero, which
+// makes the same steps of the float's bits.  No value of a block passes the largest
+// code, whose unit goes by them all.
 template <int BIAS>
-__device__ __forceinline__ uint32_t encode(float x, float up, uint32_t noise) {
-  constexpr int most = BIAS == 7 ? 126 : 254;
-  const float size = fabsf(x), y = size * up;
-  int c = (int)((__float_as_uint(y) + (noise << 4)) >> 20) - ((127 - BIAS) << 3);
-  const int low = (int)((uint32_t)__float2int_rz(y * (float)(1ull << (18 + BIAS))) + noise) >> 16;
-  if (y < __uint_as_float((uint32_t)(128 - BIAS) << 23)) c = low;
-  c = min(c, most);
-  if (BIAS != 7 && size > 0.0f) c = max(c, 1);
-  if (!(size < INFINITY)) c = most + 1;
-  return (uint32_t)c | (BIAS == 7 ? __float_as_uint(x) >> 24 & 128u : 0u);
+__device__ __forceinline__ uint32_t encode(float size, float up, uint32_t noise) {
+  constexpr uint32_t kBase = (uint32_t)(127 - BIAS) << 23;  // bits of half the smallest normal code
+  const float y = size * up, least = __uint_as_float(kBase + (1u << 23));
+  const uint32_t bits =
+      y < least ? __float_as_uint(__fadd_rz(y, least)) - (1u << 23) : __float_as_uint(y);
+  uint32_t c = (bits + noise - kBase) >> 20;
+  if (BIAS != 7) c = max(c, min(__float_as_uint(size), 1u));
+  return c;
+}
+// The same for any x: what is not finite has the code after the last.
+template <int BIAS>
+__device__ __forceinline__ uint32_t encode_any(float size, float up, uint32_t noise) {
+  constexpr uint32_t most = BIAS == 7 ? 126 : 254;
+  return size < INFINITY ? min(encode<BIAS>(size, up, noise), most) : most + 1;
+}
+
+// ---------------------------------------------------------------------------
+// Eight elements of a lane
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void load_f32x8(const float* p, float (&v)[8]) {
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+                 "=f"(v[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void store_f32x8(float* p, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = unpack2<T>(w[k]);
+    v[2 * k] = f.x;
+    v[2 * k + 1] = f.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]),
+                    pack2<T>(v[6], v[7]));
+}
+
+// n of the eight from element `at` of p; whole: all eight, aligned.
+__device__ __forceinline__ void load8(const void* p, uint64_t at, int type, bool whole, int n,
+                                      float (&v)[8]) {
+  if (!whole) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = k < n ? load_as_f32(p, at + k, type) : 0.0f;
+  } else if (type == OB_TYPE_F32) {
+    load_f32x8(static_cast<const float*>(p) + at, v);
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    if (type == OB_TYPE_BF16)
+      unpack8<__nv_bfloat16>(u, v);
+    else
+      unpack8<__half>(u, v);
+  }
+}
+__device__ __forceinline__ void store8(void* p, uint64_t at, int type, bool whole, int n,
+                                       const float (&v)[8]) {
+  if (!whole) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) store_from_f32(p, at + k, type, v[k]);
+  } else if (type == OB_TYPE_F32) {
+    store_f32x8(static_cast<float*>(p) + at, v);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) =
+        type == OB_TYPE_BF16 ? pack8<__nv_bfloat16>(v) : pack8<__half>(v);
+  }
+}
+
+__device__ __forceinline__ float sqrt_near(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_near(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 template <int CAP, bool EIGHT>
-__global__ void __launch_bounds__(kAdamThreads)
+__global__ void __launch_bounds__(kAdamThreads, 3)
     k_adamw(const __grid_constant__ AdamCall c, const __grid_constant__ AdamTable<CAP> table) {
   __shared__ AdamStep shared_step;
   const AdamArgs& a = c.a;
@@ -106,66 +220,91 @@ __global__ void __launch_bounds__(kAdamThreads)
       }
       const AdamTensor& t = table.t[lo];
       if (!t.g) continue;
-      const uint64_t at = (b - t.first) * kAdamBlock + lane * 8;  // in the tensor
-      const uint64_t st = b * kAdamBlock + lane * 8;              // in the state
+      const uint64_t begin = (b - t.first) * kAdamBlock, at = begin + lane * 8;  // in the tensor
+      const uint64_t st = b * kAdamBlock + lane * 8;                             // in the state
       const int n = at < t.n ? (int)min((uint64_t)8, t.n - at) : 0;
-      float m[8], v[8];
+      const bool full = begin + kAdamBlock <= t.n;
+      const bool whole = full && (t.types >> 16);
+      const int p_type = t.types & 255, copy_type = t.types >> 8 & 255;
+      float g[8], p[8], m[8], v[8];
+      load8(t.g, at, a.g_type, whole, n, g);
+      load8(t.p, at, p_type, whole, n, p);
       if constexpr (EIGHT) {
         const uint2 mc = *reinterpret_cast<const uint2*>(static_cast<uint8_t*>(a.m) + st);
         const uint2 vc = *reinterpret_cast<const uint2*>(static_cast<uint8_t*>(a.v) + st);
-        const float um = unit_of(a.m_exp[b]), uv = unit_of(a.v_exp[b]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          m[k] = decode<7>((k < 4 ? mc.x : mc.y) >> (8 * (k & 3)) & 255u, um);
-          v[k] = decode<23>((k < 4 ? vc.x : vc.y) >> (8 * (k & 3)) & 255u, uv);
-        }
+        const int em = a.m_exp[b];
+        const float um = em ? power_of_two(em) : 0.0f;
+        const VUnit uv(a.v_exp[b]);
+        decode_m(mc.x, um, m);
+        decode_m(mc.y, um, m + 4);
+        decode_v(vc.x, uv, v);
+        decode_v(vc.y, uv, v + 4);
       } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          m[k] = static_cast<float*>(a.m)[st + k];
-          v[k] = static_cast<float*>(a.v)[st + k];
-        }
+        load_f32x8(static_cast<float*>(a.m) + st, m);
+        load_f32x8(static_cast<float*>(a.v) + st, v);
       }
       const float keep = 1.0f - s.lr * t.decay;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        if (k >= n) {
-          m[k] = v[k] = 0.0f;
-          continue;
-        }
-        const float g = load_as_f32(t.g, at + k, a.g_type) * s.scale;
-        m[k] = __fadd_rn(__fmul_rn(m[k], c.b1), __fmul_rn(g, c.c1));
-        v[k] = __fadd_rn(__fmul_rn(v[k], c.b2), __fmul_rn(__fmul_rn(g, c.c2), g));
-        const float p = load_as_f32(t.p, at + k, t.types & 255);
-        const float den = __fmaf_rn(sqrtf(v[k]), s.root, a.eps);
-        const float q = __fmaf_rn(-s.size, m[k] / den, p * keep);
-        store_from_f32(t.p, at + k, t.types & 255, q);
-        if (t.copy) store_from_f32(t.copy, at + k, t.types >> 8, q);
+        g[k] *= s.scale;
+        m[k] = __fadd_rn(__fmul_rn(m[k], c.b1), __fmul_rn(g[k], c.c1));
+        v[k] = __fadd_rn(__fmul_rn(v[k], c.b2), __fmul_rn(__fmul_rn(g[k], c.c2), g[k]));
+        const float den = __fmaf_rn(sqrt_near(v[k]), s.root, a.eps);
+        p[k] = __fmaf_rn(-s.size, m[k] * rcp_near(den), p[k] * keep);
       }
+      if (!full)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k >= n) m[k] = v[k] = 0.0f;  // whatever a state that was handed in had there
+      store8(t.p, at, p_type, whole, n, p);
+      if (t.copy) store8(t.copy, at, copy_type, whole, n, p);
       if constexpr (EIGHT) {
         uint32_t tm = 0, tv = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint32_t x = __float_as_uint(m[k]) & 0x7fffffffu, y = __float_as_uint(v[k]);
-          if (x < 0x7f800000u) tm = max(tm, x);
-          if (y < 0x7f800000u) tv = max(tv, y);
+          tm = max(tm, __float_as_uint(m[k]) & 0x7fffffffu);
+          tv = max(tv, __float_as_uint(v[k]) & 0x7fffffffu);
         }
-        const int em = block_exp<7>(__reduce_max_sync(0xffffffffu, tm));
-        const int ev = block_exp<23>(__reduce_max_sync(0xffffffffu, tv));
-        const float upm = em ? __uint_as_float((uint32_t)(254 - em) << 23) : 0.0f;
-        const float upv = ev ? __uint_as_float((uint32_t)(254 - ev) << 23) : 0.0f;
+        tm = __reduce_max_sync(0xffffffffu, tm);
+        tv = __reduce_max_sync(0xffffffffu, tv);
+        // Nothing infinite, not a number or near the largest fp32 value: the usual case.
+        const bool usual = max(tm, tv) < 0x7f000000u;
+        if (!usual) {
+          tm = tv = 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t x = __float_as_uint(m[k]) & 0x7fffffffu, y = __float_as_uint(v[k]) & 0x7fffffffu;
+            if (x < 0x7f800000u) tm = max(tm, x);
+            if (y < 0x7f800000u) tv = max(tv, y);
+          }
+          tm = __reduce_max_sync(0xffffffffu, tm);
+          tv = __reduce_max_sync(0xffffffffu, tv);
+        }
+        const int em = block_exp<7>(tm), ev = block_exp<23>(tv);
+        const float upm = em ? power_of_two(254 - em) : 0.0f;
+        const float upv = ev ? power_of_two(254 - ev) : 0.0f;
         uint32_t mo[2] = {0, 0}, vo[2] = {0, 0};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint64_t call = st / 4 + h;
           const uint4 w = philox4x32_10(
               make_uint4((uint32_t)call, (uint32_t)(call >> 32), s.lo, s.hi), c.keys);
+          uint32_t cm[4], cv[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint32_t r = word_of(w, k);
-            mo[h] |= encode<7>(m[4 * h + k], upm, r & 0xffffu) << (8 * k);
-            vo[h] |= encode<23>(v[4 * h + k], upv, r >> 16) << (8 * k);
+            const uint32_t r = word_of(w, k), nm = (r << 4) & 0xffff0u, nv = (r >> 12) & 0xffff0u;
+            const float x = m[4 * h + k];
+            if (usual) {
+              cm[k] = encode<7>(fabsf(x), upm, nm);
+              cv[k] = encode<23>(v[4 * h + k], upv, nv);
+            } else {
+              cm[k] = encode_any<7>(fabsf(x), upm, nm);
+              cv[k] = encode_any<23>(v[4 * h + k], upv, nv);
+            }
+            cm[k] |= (__float_as_uint(x) & 0x80000000u) >> 24;
           }
+          mo[h] = __byte_perm(__byte_perm(cm[0], cm[1], 0x0040), __byte_perm(cm[2], cm[3], 0x0040), 0x5410);
+          vo[h] = __byte_perm(__byte_perm(cv[0], cv[1], 0x0040), __byte_perm(cv[2], cv[3], 0x0040), 0x5410);
         }
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + st) = make_uint2(mo[0], mo[1]);
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + st) = make_uint2(vo[0], vo[1]);
@@ -174,11 +313,8 @@ __global__ void __launch_bounds__(kAdamThreads)
           a.v_exp[b] = (uint8_t)ev;
         }
       } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          static_cast<float*>(a.m)[st + k] = m[k];
-          static_cast<float*>(a.v)[st + k] = v[k];
-        }
+        store_f32x8(static_cast<float*>(a.m) + st, m);
+        store_f32x8(static_cast<float*>(a.v) + st, v);
       }
     }
   // The block that ends last has seen all others read the counter.
@@ -203,27 +339,35 @@ __global__ void __launch_bounds__(256)
   const uint64_t b = (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (b >= blocks) return;
   const uint64_t st = b * kAdamBlock + lane * 8;
-  auto one = [&](const uint8_t* codes, const uint8_t* exps, uint32_t* out, auto bias) {
-    const uint2 c = *reinterpret_cast<const uint2*>(codes + st);
-    const float u = unit_of(exps[b]);
-    float x[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      x[k] = decode<decltype(bias)::value>((k < 4 ? c.x : c.y) >> (8 * (k & 3)) & 255u, u);
-    using B = __nv_bfloat16;
-    *reinterpret_cast<uint4*>(out + st / 2) = make_uint4(
-        pack2<B>(x[0], x[1]), pack2<B>(x[2], x[3]), pack2<B>(x[4], x[5]), pack2<B>(x[6], x[7]));
-  };
-  one(m, m_exp, m_out, std::integral_constant<int, 7>());
-  one(v, v_exp, v_out, std::integral_constant<int, 23>());
+  using B = __nv_bfloat16;
+  const uint2 mc = *reinterpret_cast<const uint2*>(m + st);
+  const uint2 vc = *reinterpret_cast<const uint2*>(v + st);
+  const int em = m_exp[b];
+  const float um = em ? power_of_two(em) : 0.0f;
+  const VUnit uv(v_exp[b]);
+  float x[8];
+  decode_m(mc.x, um, x);
+  decode_m(mc.y, um, x + 4);
+  *reinterpret_cast<uint4*>(m_out + st / 2) = pack8<B>(x);
+  decode_v(vc.x, uv, x);
+  decode_v(vc.y, uv, x + 4);
+  *reinterpret_cast<uint4*>(v_out + st / 2) = pack8<B>(x);
 }
 
 template <int CAP>
 cudaError_t launch(const AdamCall& c, const AdamTensor* t, cudaStream_t s) {
   AdamTable<CAP> table;
-  for (int i = 0; i < c.count; ++i) table.t[i] = t[i];
+  auto lies = [](const void* p, int type) {
+    return reinterpret_cast<uintptr_t>(p) % (type == OB_TYPE_F32 ? 32 : 16) == 0;
+  };
+  for (int i = 0; i < c.count; ++i) {
+    table.t[i] = t[i];
+    const bool whole = lies(t[i].p, t[i].types & 255) && lies(t[i].g, c.a.g_type) &&
+                       lies(t[i].copy, t[i].types >> 8);
+    table.t[i].types |= (int)whole << 16;
+  }
   const uint64_t want = (c.blocks + kAdamThreads / 32 - 1) / (kAdamThreads / 32);
-  const int grid = (int)(want < 1 ? 1 : want < 1216 ? want : 1216);
+  const int grid = (int)(want < 1 ? 1 : want < kAdamGrid ? want : kAdamGrid);
   if (c.a.bits == 8)
     k_adamw<CAP, true><<<grid, kAdamThreads, 0, s>>>(c, table);
   else

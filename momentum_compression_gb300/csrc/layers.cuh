@@ -98,7 +98,7 @@ struct AdamTensor {
   uint64_t n;
   uint64_t first;    // its first block in the state
   float decay;
-  int types;         // p_type | copy_type << 8
+  int types;         // p_type | copy_type << 8; from bit 16 on, all lie on 16 (32) bytes
 };
 
 struct AdamArgs {

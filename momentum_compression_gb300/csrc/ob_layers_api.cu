@@ -316,8 +316,8 @@ ob_status ob_adamw_step(const ob_adamw* a, const ob_adamw_tensor* tensors,
     return failf(OB_ERR_INVALID, "lr = %g must not be negative", a->lr);
   if (!(a->b1 >= 0.0 && a->b1 < 1.0 && a->b2 >= 0.0 && a->b2 < 1.0))
     return failf(OB_ERR_INVALID, "b1 = %g, b2 = %g must be in [0, 1)", a->b1, a->b2);
-  if (!(a->eps >= 1e-18 && a->eps <= 1.0))
-    return failf(OB_ERR_INVALID, "eps = %g must be in [1e-18, 1]", a->eps);
+  if (!(a->eps >= 1e-12 && a->eps <= 1.0))
+    return failf(OB_ERR_INVALID, "eps = %g must be in [1e-12, 1]", a->eps);
   if (count < 0) return failf(OB_ERR_INVALID, "count = %d is negative", count);
   if (count && (!tensors || !grads)) return failf(OB_ERR_INVALID, "tensors or grads is NULL");
   OB_TRY(check_ptr(counter, 8, "counter"));
@@ -355,8 +355,8 @@ ob_status ob_adamw_step(const ob_adamw* a, const ob_adamw_tensor* tensors,
       return failf(OB_ERR_INVALID, "the tensors are over 2^40 elements");
   }
   if (blocks) {
-    OB_TRY(check_ptr(m, 16, "m"));
-    OB_TRY(check_ptr(v, 16, "v"));
+    OB_TRY(check_ptr(m, 32, "m"));
+    OB_TRY(check_ptr(v, 32, "v"));
     if (a->state_bits == 8) {
       OB_TRY(check_ptr(m_exp, 1, "m_exp"));
       OB_TRY(check_ptr(v_exp, 1, "v_exp"));
