@@ -826,8 +826,9 @@ ob_status ob_linear_bwd(const ob_linear* l, const ob_matrix* dy, const ob_matrix
                         const ob_matrix* dw, void* dbias, void* workspace,
                         size_t workspace_bytes, ob_stream_t stream);
 
-/* As ob_attn_device_error, for the waits of the dense layer's products. */
-ob_status ob_linear_device_error(unsigned* code, ob_stream_t stream);
+/* As ob_attn_device_error, for the waits of the dense layer's products and of
+ * layer norm's backward pass. */
+ob_status ob_layer_device_error(unsigned* code, ob_stream_t stream);
 
 /* One AdamW step over `count` tensors, with decoupled decay, at step t:
  *   g = grad * grad_scale

@@ -57,7 +57,7 @@ EXPORTS = (
     "ob_relpos_bias_bwd", "ob_attn_fwd", "ob_attn_workspace_bytes", "ob_attn_bwd",
     "ob_attn_device_error",
     "ob_layernorm_fwd", "ob_layernorm_workspace_bytes", "ob_layernorm_bwd",
-    "ob_linear_workspace_bytes", "ob_linear_fwd", "ob_linear_bwd", "ob_linear_device_error",
+    "ob_linear_workspace_bytes", "ob_linear_fwd", "ob_linear_bwd", "ob_layer_device_error",
     "ob_adamw_step", "ob_adamw_moments",
 )
 
@@ -212,7 +212,7 @@ def lib():
         L.ob_linear_workspace_bytes.argtypes = [vp, i32, ct.POINTER(sz)]
         L.ob_linear_fwd.argtypes = [vp] * 8 + [sz, vp]
         L.ob_linear_bwd.argtypes = [vp] * 9 + [sz, vp]
-        L.ob_linear_device_error.argtypes = [ct.POINTER(ct.c_uint), vp]
+        L.ob_layer_device_error.argtypes = [ct.POINTER(ct.c_uint), vp]
         L.ob_adamw_step.argtypes = [vp, vp, vp, i32] + [vp] * 6
         L.ob_adamw_moments.argtypes = [vp, vp, vp, vp, sz, vp, vp, vp]
         for name in EXPORTS:
@@ -1144,10 +1144,10 @@ def ob_linear_bwd(dy, x, w, dx=None, dw=None, dbias=None, z=None, activation="no
     _linear_call(lib().ob_linear_bwd, m, l, 1, dy, workspace, stream, pdy, px, pw, pz, pdx, pdw, pb)
 
 
-def ob_linear_device_error(stream=None):
-    """Reads and clears the dense layer's device error word (0 = none)."""
+def ob_layer_device_error(stream=None):
+    """Reads and clears the device error word of layer norm and the dense layer (0 = none)."""
     v = ct.c_uint()
-    _check(lib().ob_linear_device_error(ct.byref(v), _stream(stream)))
+    _check(lib().ob_layer_device_error(ct.byref(v), _stream(stream)))
     return v.value
 
 
@@ -1188,7 +1188,7 @@ def ob_adamw_moments(m, v, m_exp, v_exp, m_out, v_out, stream=None):
 class AdamW:
     """AdamW with decoupled weight decay over a list of tensors, which stay where they are:
     the step of parameters that are not compressed (norms, biases, embeddings) or of a
-    whole model.  One launch updates up to 512 tensors.
+    whole model.  One launch updates up to 128 tensors.
 
     params: contiguous tensors of float32, bfloat16 or float16 on one device.
     weight_decay: a number, or one for each tensor.  state_bits: 32, or 8 for moments of a

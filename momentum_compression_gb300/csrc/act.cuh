@@ -7,6 +7,8 @@
 // exponential.  The tanh form is z / (1 + e^(-2u)).
 #pragma once
 
+#include <type_traits>
+
 #include "ob.h"
 
 namespace ob {

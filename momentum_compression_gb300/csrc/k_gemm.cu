@@ -13,6 +13,7 @@
 // takes an equal share of all their steps, parts of a tile go to the
 // workspace in fp32, and a second kernel adds a tile's parts in their order and
 // runs the epilogue.
+#include <atomic>
 #include <type_traits>
 
 #include "act.cuh"
@@ -25,7 +26,7 @@
 namespace ob {
 namespace {
 
-__device__ unsigned g_linear_error;
+__device__ unsigned g_layer_error;
 
 constexpr int BK = 64;            // of the sum a step
 constexpr int kEpWarps = 8;
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       tile_at(u.tile, a.tiles_m, a.tiles_n, &tm, &tn);
       const int m0 = tm * S::kRows + (int)rank * 128, n0 = tn * S::kCols + (int)rank * 128 * (CG - 1);
       for (int k = u.k0; k < u.k1; ++k) {
-        if (n >= S::kStages) ok = warp_wait(&bar.empty[st], par, &g_linear_error, kErrWaitEmpty);
+        if (n >= S::kStages) ok = warp_wait(&bar.empty[st], par, &g_layer_error, kErrWaitEmpty);
         if (!ok) break;
         if (lane == 0) {
           uint8_t* to = smem + st * S::kStage;
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
     }
     if (!ok && rank == 0)  // a wait ran out: let what is in flight land before the block ends
       for (int64_t i = n > S::kStages ? n - S::kStages : 0; i < n; ++i)
-        mbar_wait(&bar.full[i % S::kStages], (i / S::kStages) & 1, &g_linear_error, kErrDrain);
+        mbar_wait(&bar.full[i % S::kStages], (i / S::kStages) & 1, &g_layer_error, kErrDrain);
   } else if (warp == 1) {
     // ----- products --------------------------------------------------------
     if (rank == 0) {
@@ -336,12 +337,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       int64_t n = 0;
       int64_t units = 0;
       while (ok && u.next(a)) {
-        if (units >= 2) ok = warp_wait(&bar.sum_empty[buf], sum_par, &g_linear_error, kErrWaitEmpty);
+        if (units >= 2) ok = warp_wait(&bar.sum_empty[buf], sum_par, &g_layer_error, kErrWaitEmpty);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + buf * S::kCols;
         for (int k = u.k0; k < u.k1; ++k) {
-          ok = warp_wait(&bar.full[st], par, &g_linear_error);
+          ok = warp_wait(&bar.full[st], par, &g_layer_error);
           if (!ok) break;
           tc_fence_after();
           const uint64_t ad = a_desc + (uint32_t)st * (S::kStage >> 4);
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
           pair_commit(leader, &bar.drain);
         else
           mma_commit(leader, &bar.drain);
-        mbar_wait(&bar.drain, 0, &g_linear_error, kErrDrain);
+        mbar_wait(&bar.drain, 0, &g_layer_error, kErrDrain);
       }
     }
   } else {
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
     bool ok = true;
     int buf = 0, par = 0;
     while (ok && u.next(a)) {
-      ok = warp_wait(&bar.sum_full[buf], par, &g_linear_error);
+      ok = warp_wait(&bar.sum_full[buf], par, &g_layer_error);
       if (!ok) break;
       tc_fence_after();
       int tm, tn;
@@ -594,8 +595,16 @@ cudaError_t launch_gemm(const Gemm& g, cudaStream_t s) {
   return p.cg == 2 ? run<2>(g, p, s) : run<1>(g, p, s);
 }
 
-cudaError_t linear_error_word(unsigned** word) {
-  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_linear_error);
+cudaError_t layer_error_word(unsigned** word) {
+  static std::atomic<unsigned*> known[64];  // by device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  *word = known[dev & 63].load(std::memory_order_acquire);
+  if (*word) return cudaSuccess;
+  e = cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_layer_error);
+  if (e == cudaSuccess) known[dev & 63].store(*word, std::memory_order_release);
+  return e;
 }
 
 }  // namespace ob

@@ -10,7 +10,7 @@
 #include "layers.cuh"
 #include "model.cuh"
 #include "ob_internal.cuh"
-#include "ptx.cuh"
+#include "tc.cuh"
 
 namespace ob {
 namespace {
@@ -220,7 +220,7 @@ __device__ __forceinline__ void load_weights(float (&w)[8], const void* p, int t
 
 // A row a warp (MULTI false, eight rows a block) or a row a block.
 template <typename T, int CH, bool VEC, bool MULTI>
-__global__ void __launch_bounds__(MULTI ? 1024 : 256) k_ln_fwd(const __grid_constant__ LayerNormArgs a) {
+__global__ void __launch_bounds__(MULTI ? 512 : 256, MULTI || CH == 8 ? 2 : 3) k_ln_fwd(const __grid_constant__ LayerNormArgs a) {
   __shared__ float buf[33];
   const int threads = MULTI ? blockDim.x : 32, t = MULTI ? threadIdx.x : threadIdx.x & 31;
   const uint64_t first = MULTI ? blockIdx.x : (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -229,7 +229,6 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 256) k_ln_fwd(const __grid_cons
   grid_wait();
   for (uint64_t row = first; row < a.rows; row += step) {
     const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-    float v[CH][8];
     Chunk<T, VEC> in[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) in[c].load(x, c, t, threads, a.cols);
@@ -249,33 +248,39 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 256) k_ln_fwd(const __grid_cons
         if (a.sum) in[c].store(static_cast<T*>(a.sum) + row * a.lds, c, t, threads, a.cols);
       }
     }
+    // The row stays as it lies in memory, two elements a register, and is unpacked again
+    // for each pass.
     float total = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      in[c].get(v[c]);
-      total += ((v[c][0] + v[c][1]) + (v[c][2] + v[c][3])) + ((v[c][4] + v[c][5]) + (v[c][6] + v[c][7]));
+      float v[8];
+      in[c].get(v);
+      total += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
     }
     const float mean = row_sum(total) / (float)a.cols;
     float square = 0.0f;
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
+    for (int c = 0; c < CH; ++c) {
+      float v[8];
+      in[c].get(v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[c][j] -= mean;
-        if (column<VEC>(c, j, t, threads) < a.cols) square = __fmaf_rn(v[c][j], v[c][j], square);
+        v[j] -= mean;
+        if (column<VEC>(c, VEC ? 0 : j, t, threads) < a.cols) square = __fmaf_rn(v[j], v[j], square);
       }
+    }
     const float rstd = 1.0f / sqrtf(row_sum(square) / (float)a.cols + a.eps);
     T* y = static_cast<T*>(a.y) + row * a.ldy;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      float w[8], b[8];
+      float v[8], w[8], b[8];
+      in[c].get(v);
       load_weights<VEC>(w, a.weight, a.w_type, 1.0f, c, t, threads, a.cols);
       load_weights<VEC>(b, a.bias, a.w_type, 0.0f, c, t, threads, a.cols);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[c][j] = __fmaf_rn(v[c][j] * rstd, w[j], b[j]);
-      Chunk<T, VEC> out;
-      out.put(v[c]);
-      out.store(y, c, t, threads, a.cols);
+      for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn((v[j] - mean) * rstd, w[j], b[j]);
+      in[c].put(v);
+      in[c].store(y, c, t, threads, a.cols);
     }
     if (t == 0) {
       if (a.mean) a.mean[row] = mean;
@@ -306,20 +311,94 @@ __device__ __forceinline__ float warp_sums(float (&v)[N]) {
   return r;
 }
 
-constexpr int kBwdThreads = 256;
+// ---------------------------------------------------------------------------
+// Backward.  One warp of a block copies rows of x, dy and dsum into shared memory,
+// units of G R rows, several ahead; the others, G groups that each share a row's
+// columns, the same ones for every row, walk over a unit twice: for the row's two
+// sums and the columns' own, and for dx.  So what is under way to an SM does not
+// hang on its registers, and rows at any alignment are copied in whole 16-byte
+// words.  HBM bounds it.
+// ---------------------------------------------------------------------------
 
-// dx and the block's sums of dy xhat and dy.  A group of threads has a row's
-// columns, the same ones for every row, and takes R rows at a time.
-template <typename T, int CH, int R, bool VEC>
-__global__ void __launch_bounds__(kBwdThreads, 2)
-    k_ln_bwd(const __grid_constant__ LayerNormBwdArgs a, int threads) {
+// Threads of a block (and a warp for the copies): 256, or 512 for wide rows.
+constexpr int kBwdStages = 4;     // at most
+
+struct LnBwdPlan {
+  int threads;     // of a group
+  int rows;        // of a unit: R for each group
+  int stages, arrays;
+  uint32_t pitch;  // bytes of a row in shared memory
+  bool runs;       // a unit's rows of each array are one run of 16-byte words
+};
+
+template <typename T, int kBwdThreads, int CH, int R, bool VEC>
+__global__ void __launch_bounds__(kBwdThreads + 32, kBwdThreads == 256 ? 2 : 1)
+    k_ln_bwd(const __grid_constant__ LayerNormBwdArgs a, const __grid_constant__ LnBwdPlan p) {
   constexpr int N = 2 * R;
+  extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(16) float part[2][kBwdThreads / 32][N];
   __shared__ float merge[kBwdThreads * 8];
-  const int t = threadIdx.x & (threads - 1), group = threadIdx.x / threads;
-  const int groups = kBwdThreads / threads, warps = threads / 32, warp = threadIdx.x >> 5;
-  const float inv = 1.0f / (float)a.cols;
+  __shared__ uint64_t full[kBwdStages], empty[kBwdStages];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kBwdThreads / 32);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
   grid_wait();
+  const uint64_t units = (a.rows + p.rows - 1) / p.rows;
+  const uint32_t array_bytes = p.rows * p.pitch, stage_bytes = array_bytes * p.arrays;
+  const char* from[3] = {static_cast<const char*>(a.x), static_cast<const char*>(a.dy),
+                         static_cast<const char*>(a.dsum)};
+  const uint64_t ld[3] = {a.ldx * sizeof(T), a.lddy * sizeof(T), a.ldds * sizeof(T)};
+
+  if (warp == kBwdThreads / 32) {
+    // ----- copies ----------------------------------------------------------
+    int st = 0, par = 1;
+    uint32_t n = 0;
+    bool ok = true;
+    for (uint64_t u = blockIdx.x; u < units; u += gridDim.x, ++n) {
+      if (n >= (uint32_t)p.stages) ok = warp_wait(&empty[st], par, a.error, kErrWaitEmpty);
+      if (!ok) break;
+      const uint64_t r0 = u * p.rows;
+      const int rows = (int)(a.rows - r0 < (uint64_t)p.rows ? a.rows - r0 : p.rows);
+      uint8_t* to = ring + st * stage_bytes;
+      const int copies = p.runs ? p.arrays : rows * p.arrays;
+      // of copy i: the 16-byte words that hold its bytes
+      auto words = [&](int i, const char** src, uint8_t** dst) {
+        const int k = p.runs ? i : i % p.arrays, r = p.runs ? 0 : i / p.arrays;
+        const char* q = from[k] + (r0 + r) * ld[k];
+        const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(q) & 15);
+        const uint32_t bytes = (p.runs ? rows : 1) * a.cols * (uint32_t)sizeof(T);
+        *src = q - off;
+        *dst = to + k * array_bytes + r * p.pitch;
+        return (off + bytes + 15) & ~15u;
+      };
+      const char* src;
+      uint8_t* dst;
+      uint32_t bytes = 0;
+      for (int i = lane; i < copies; i += 32) bytes += words(i, &src, &dst);
+      bytes = __reduce_add_sync(0xffffffffu, bytes);
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
+      __syncwarp();
+      for (int i = lane; i < copies; i += 32) {
+        const uint32_t size = words(i, &src, &dst);
+        bulk_g2s(dst, src, size, &full[st]);
+      }
+      if (++st == p.stages) st = 0, par ^= 1;
+    }
+    if (!ok)  // a wait ran out: let what is in flight land before the block ends
+      for (uint32_t i = n > (uint32_t)p.stages ? n - p.stages : 0; i < n; ++i)
+        mbar_wait(&full[i % p.stages], (i / p.stages) & 1, a.error, kErrDrain);
+    return;
+  }
+
+  const int threads = p.threads, t = threadIdx.x & (threads - 1), group = threadIdx.x / threads;
+  const int groups = kBwdThreads / threads, warps = threads / 32;
+  const float inv = 1.0f / (float)a.cols;
   float w[CH][8], dw[CH][8], db[CH][8];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -327,93 +406,100 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[c][j] = db[c][j] = 0.0f;
   }
-  int flip = 0;
-  const uint64_t step = (uint64_t)gridDim.x * groups * R;
-  for (uint64_t r0 = ((uint64_t)blockIdx.x * groups + group) * R; r0 < a.rows; r0 += step) {
-    Chunk<T, VEC> x[R][CH], g[R][CH], s[R][CH];
+  int st = 0, par = 0, flip = 0;
+  for (uint64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const uint64_t r0 = u * p.rows + (uint64_t)group * R;
+    const int rows = r0 < a.rows ? (int)(a.rows - r0 < R ? a.rows - r0 : R) : 0;
     float mean[R], rstd[R], sums[N];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const bool in = r0 + r < a.rows;
-      const uint64_t row = in ? r0 + r : a.rows - 1;
-      const int cols = in ? a.cols : 0;
-      mean[r] = a.mean[row];
-      rstd[r] = a.rstd[row];
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        x[r][c].load(static_cast<const T*>(a.x) + row * a.ldx, c, t, threads, cols);
-        g[r][c].load(static_cast<const T*>(a.dy) + row * a.lddy, c, t, threads, cols);
-      }
-    }
-    if (a.dsum)
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (r0 + r < a.rows)
-#pragma unroll
-          for (int c = 0; c < CH; ++c)
-            s[r][c].load(static_cast<const T*>(a.dsum) + (r0 + r) * a.ldds, c, t, threads, a.cols);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
+      mean[r] = r < rows ? a.mean[r0 + r] : 0.0f;
+      rstd[r] = r < rows ? a.rstd[r0 + r] : 0.0f;
       sums[2 * r] = sums[2 * r + 1] = 0.0f;
+    }
+    const bool ok = warp_wait(&full[st], par, a.error);
+    auto row_of = [&](int k, int r) {
+      uint32_t at = st * stage_bytes + k * array_bytes + (group * R + r) * p.pitch;
+      if (!VEC) at += (uint32_t)(reinterpret_cast<uintptr_t>(from[k] + (r0 + r) * ld[k]) & 15);
+      return reinterpret_cast<const T*>(ring + at);
+    };
+    if (ok)
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        float xv[8], gv[8];
-        x[r][c].get(xv);
-        g[r][c].get(gv);
+      for (int r = 0; r < R; ++r) {
+        if (r >= rows) break;
+        const T *xr = row_of(0, r), *gr = row_of(1, r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {  // a column past the row has no dy
-          const float h = gv[j] * w[c][j];
-          const float xhat = (xv[j] - mean[r]) * rstd[r];
-          sums[2 * r] += h;
-          if (VEC || column<VEC>(c, j, t, threads) < a.cols)
+        for (int c = 0; c < CH; ++c) {
+          Chunk<T, VEC> x, g;
+          x.load(xr, c, t, threads, a.cols);
+          g.load(gr, c, t, threads, a.cols);
+          float xv[8], gv[8];
+          x.get(xv);
+          g.get(gv);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {  // a column past the row has no dy
+            const float h = gv[j] * w[c][j];
+            const float xhat = (xv[j] - mean[r]) * rstd[r];
+            sums[2 * r] += h;
             sums[2 * r + 1] = __fmaf_rn(h, xhat, sums[2 * r + 1]);
-          if (r0 + r < a.rows) {
             dw[c][j] = __fmaf_rn(gv[j], xhat, dw[c][j]);
             db[c][j] += gv[j];
           }
         }
       }
-    }
-    if (!a.dx) continue;
-    const float mine = warp_sums<N>(sums);
-    float m[N];
-    if (threads == 32) {
+    bool fine = ok;
+    if (a.dx) {
+      const float mine = warp_sums<N>(sums);
+      float m[N];
+      if (threads == 32) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) m[k] = __shfl_sync(0xffffffffu, mine, k * (32 / N)) * inv;
-    } else {
-      if ((threadIdx.x & (32 / N - 1)) == 0) part[flip][warp][(threadIdx.x & 31) / (32 / N)] = mine;
-      named_sync(1 + group, threads);
+        for (int k = 0; k < N; ++k) m[k] = __shfl_sync(0xffffffffu, mine, k * (32 / N)) * inv;
+      } else {
+        if ((lane & (32 / N - 1)) == 0) part[flip][warp][lane / (32 / N)] = mine;
+        fine = !named_sync_or(1 + group, threads, !ok);
 #pragma unroll
-      for (int k = 0; k < N; ++k) m[k] = 0.0f;
-      for (int q = 0; q < warps; ++q)
+        for (int k = 0; k < N; ++k) m[k] = 0.0f;
+        for (int q = 0; q < warps; ++q)
 #pragma unroll
-        for (int k = 0; k < N; ++k) m[k] += part[flip][group * warps + q][k];
+          for (int k = 0; k < N; ++k) m[k] += part[flip][group * warps + q][k];
 #pragma unroll
-      for (int k = 0; k < N; ++k) m[k] *= inv;
-      flip ^= 1;
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (r0 + r >= a.rows) break;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        float xv[8], gv[8];
-        x[r][c].get(xv);
-        g[r][c].get(gv);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float xhat = (xv[j] - mean[r]) * rstd[r];
-          gv[j] = rstd[r] * __fmaf_rn(-xhat, m[2 * r + 1], gv[j] * w[c][j] - m[2 * r]);
-        }
-        if (a.dsum) {
-          s[r][c].get(xv);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) gv[j] += xv[j];
-        }
-        g[r][c].put(gv);
-        g[r][c].store(static_cast<T*>(a.dx) + (r0 + r) * a.lddx, c, t, threads, a.cols);
+        for (int k = 0; k < N; ++k) m[k] *= inv;
+        flip ^= 1;
       }
+      if (fine)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if (r >= rows) break;
+          const T *xr = row_of(0, r), *gr = row_of(1, r), *sr = row_of(2, r);
+          T* out = static_cast<T*>(a.dx) + (r0 + r) * a.lddx;
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            Chunk<T, VEC> x, g;
+            x.load(xr, c, t, threads, a.cols);
+            g.load(gr, c, t, threads, a.cols);
+            float xv[8], gv[8];
+            x.get(xv);
+            g.get(gv);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float xhat = (xv[j] - mean[r]) * rstd[r];
+              gv[j] = rstd[r] * __fmaf_rn(-xhat, m[2 * r + 1], gv[j] * w[c][j] - m[2 * r]);
+            }
+            if (a.dsum) {
+              x.load(sr, c, t, threads, a.cols);
+              x.get(xv);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) gv[j] += xv[j];
+            }
+            g.put(gv);
+            g.store(out, c, t, threads, a.cols);
+          }
+        }
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+    if (!fine) break;
+    if (++st == p.stages) st = 0, par ^= 1;
   }
   if (!a.partial) return;
   // the groups' sums in their order
@@ -422,10 +508,10 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       if (groups > 1) {
-        __syncthreads();
+        named_sync(15, kBwdThreads);
 #pragma unroll
         for (int j = 0; j < 8; ++j) merge[j * kBwdThreads + threadIdx.x] = which ? db[c][j] : dw[c][j];
-        __syncthreads();
+        named_sync(15, kBwdThreads);
       }
       if (group) continue;
 #pragma unroll
@@ -472,15 +558,16 @@ int row_blocks(uint64_t rows) { return (int)(rows < 65535 ? rows : 65535); }
 bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 constexpr int kSms = 152;
-constexpr int kFwdMost = 1024 * 8 * 4;  // columns that a block's registers hold
-constexpr int kBwdMost = kBwdThreads * 8 * 2;
+constexpr int kFwdMost = 512 * 8 * 4;  // columns that a block's registers hold
+constexpr int kBwdMost = 512 * 8 * 2;
 
 template <typename T, bool VEC>
 cudaError_t fwd(const LayerNormArgs& a, cudaStream_t s) {
   const int chunks = (a.cols + 7) / 8;
   // A row a warp needs no barrier, a row a block more of them at a time: the latter
-  // where the rows alone do not fill the card.
-  if (chunks <= 256 && (chunks <= 32 || a.rows >= (uint64_t)kSms * 8)) {
+  // where the rows alone do not fill the card, or a warp's registers do not last.
+  constexpr int kWarpMost = !VEC ? 2 : sizeof(T) == 4 ? 4 : 8;  // chunks of a lane
+  if (chunks <= 32 * kWarpMost && (chunks <= 32 || a.rows >= (uint64_t)kSms * 8)) {
     const uint64_t blocks = (a.rows + 7) / 8;
     const int grid = (int)(blocks < (uint64_t)kSms * 32 ? blocks : kSms * 32);
     auto go = [&](auto ch) {
@@ -488,31 +575,59 @@ cudaError_t fwd(const LayerNormArgs& a, cudaStream_t s) {
     };
     if (chunks <= 32) return go(std::integral_constant<int, 1>());
     if (chunks <= 64) return go(std::integral_constant<int, 2>());
-    if (chunks <= 128) return go(std::integral_constant<int, 4>());
-    return go(std::integral_constant<int, 8>());
+    if (chunks <= 128) return go(std::integral_constant<int, kWarpMost < 4 ? kWarpMost : 4>());
+    return go(std::integral_constant<int, kWarpMost>());
   }
   const int grid = (int)(a.rows < (uint64_t)kSms * 16 ? a.rows : kSms * 16);
-  const bool few = a.rows < kSms && chunks <= 1024;
+  const bool few = chunks <= 512 && (a.rows < kSms * 2 || chunks <= 128);
   const int threads = few ? (chunks + 31) / 32 * 32 : (chunks + 127) / 128 * 32;
   return few ? launch_behind(k_ln_fwd<T, 1, VEC, true>, dim3(grid), dim3(threads), 0, s, a)
              : launch_behind(k_ln_fwd<T, 4, VEC, true>, dim3(grid), dim3(threads), 0, s, a);
 }
 
-// Threads of a group: a power of two from 32, so that CH chunks each hold the row.
-int group_threads(int cols, int ch) {
+// Threads of a block and of a group (a power of two from 32), and chunks a thread.
+int block_threads(int cols) { return cols <= 256 * 8 ? 256 : 512; }
+int row_chunks(int cols) { return cols <= 512 * 8 ? 1 : 2; }
+int group_threads(int cols) {
   int t = 32;
-  while (t * 8 * ch < cols) t *= 2;
+  while (t * 8 * row_chunks(cols) < cols) t *= 2;
   return t;
+}
+
+template <typename T, int kBwdThreads, int CH, int R, bool VEC>
+cudaError_t bwd_launch(const LayerNormBwdArgs& a, cudaStream_t s) {
+  LnBwdPlan p{};
+  p.threads = group_threads(a.cols);
+  p.rows = kBwdThreads / p.threads * R;
+  p.arrays = a.dsum ? 3 : 2;
+  const uint32_t row = a.cols * (uint32_t)sizeof(T);
+  p.pitch = VEC ? row : (row + 30) / 16 * 16;
+  p.runs = VEC && a.ldx == (uint64_t)a.cols && a.lddy == a.ldx && (!a.dsum || a.ldds == a.ldx);
+  const uint32_t stage = p.rows * p.pitch * p.arrays;
+  const uint32_t most = kBwdThreads == 256 ? 96 * 1024 : 192 * 1024;  // two blocks an SM, or one
+  p.stages = (int)(most / stage < kBwdStages ? most / stage : kBwdStages);
+  static PerDeviceOnce once;
+  const cudaError_t e = once.run([&] {
+    return cudaFuncSetAttribute(k_ln_bwd<T, kBwdThreads, CH, R, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)most);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_behind(k_ln_bwd<T, kBwdThreads, CH, R, VEC>, dim3(a.parts), dim3(kBwdThreads + 32),
+                       (size_t)(p.stages * stage), s, a, p);
 }
 
 template <typename T, bool VEC>
 cudaError_t bwd(const LayerNormBwdArgs& a, cudaStream_t s) {
-  constexpr int R = sizeof(T) == 4 ? 2 : 4;
-  if (a.cols <= kBwdThreads * 8)
-    return launch_behind(k_ln_bwd<T, 1, R, VEC>, dim3(a.parts), dim3(kBwdThreads), 0, s, a,
-                         group_threads(a.cols, 1));
-  return launch_behind(k_ln_bwd<T, 2, R / 2, VEC>, dim3(a.parts), dim3(kBwdThreads), 0, s, a,
-                       group_threads(a.cols, 2));
+  if (a.cols <= 256 * 8) {
+    // Four rows of a group share a barrier, where there are units enough for every
+    // block and two of them fit.
+    const int groups = 256 / group_threads(a.cols);
+    const size_t unit = (size_t)groups * 4 * (a.cols * sizeof(T) + 30) * (a.dsum ? 3 : 2);
+    const bool four = a.rows >= (uint64_t)a.parts * groups * 16 && unit <= 48 * 1024;
+    return four ? bwd_launch<T, 256, 1, 4, VEC>(a, s) : bwd_launch<T, 256, 1, 1, VEC>(a, s);
+  }
+  return a.cols <= 512 * 8 ? bwd_launch<T, 512, 1, 1, VEC>(a, s)
+                           : bwd_launch<T, 512, 2, 1, VEC>(a, s);
 }
 
 }  // namespace
@@ -535,10 +650,11 @@ cudaError_t launch_layernorm_fwd(const LayerNormArgs& a, int type, cudaStream_t 
 
 int layernorm_bwd_parts(uint64_t rows, int cols) {
   if (cols > kBwdMost) return (int)(rows < 64 ? 1 : rows / 64 < 64 ? rows / 64 : 64);
-  // two blocks an SM, as far as there are rows for them
-  const uint64_t per = kBwdThreads / group_threads(cols, cols <= kBwdThreads * 8 ? 1 : 2);
+  // all blocks that run at a time, as far as there are rows for them
+  const int threads = block_threads(cols);
+  const uint64_t most = threads == 256 ? 2 * kSms : kSms, per = threads / group_threads(cols);
   const uint64_t want = (rows + per - 1) / per;
-  return (int)(want < 2 * kSms ? want : 2 * kSms);
+  return (int)(want < most ? want : most);
 }
 
 cudaError_t launch_layernorm_bwd(const LayerNormBwdArgs& b, int type, cudaStream_t s) {
@@ -561,7 +677,8 @@ cudaError_t launch_layernorm_bwd(const LayerNormBwdArgs& b, int type, cudaStream
       const uint64_t ld[4] = {a.ldx, a.lddy, a.lddx, a.ldds};
       for (int i = 0; i < 4; ++i)
         if (p[i]) vec = vec && on16(p[i]) && (a.rows == 1 || ld[i] * sizeof(T) % 16 == 0);
-      e = vec ? bwd<T, true>(a, s) : bwd<T, false>(a, s);
+      e = layer_error_word(&a.error);
+      if (e == cudaSuccess) e = vec ? bwd<T, true>(a, s) : bwd<T, false>(a, s);
     }
     if (e != cudaSuccess || !sums) return e;
     return launch_behind(k_ln_sums, dim3((2 * a.cols + 31) / 32), dim3(256), 0, s, a);

@@ -288,17 +288,17 @@ ob_status ob_linear_bwd(const ob_linear* l, const ob_matrix* dy, const ob_matrix
   return launched(ob::launch_linear_bwd(a, reinterpret_cast<cudaStream_t>(stream)), "linear_bwd");
 }
 
-ob_status ob_linear_device_error(unsigned* code, ob_stream_t stream) {
+ob_status ob_layer_device_error(unsigned* code, ob_stream_t stream) {
   OB_TRACE();
-  if (!code) return failf(OB_ERR_INVALID, "linear_device_error: code is NULL");
+  if (!code) return failf(OB_ERR_INVALID, "layer_device_error: code is NULL");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   unsigned* word = nullptr;
   unsigned v = 0;
-  cudaError_t e = ob::linear_error_word(&word);
+  cudaError_t e = ob::layer_error_word(&word);
   if (e == cudaSuccess) e = cudaMemcpyAsync(&v, word, sizeof v, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof v, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return launched(e, "linear_device_error");
+  if (e != cudaSuccess) return launched(e, "layer_device_error");
   *code = v;
   return OB_OK;
 }

@@ -24,7 +24,7 @@ def _cuda():
     from momentum_compression_gb300 import _build
     _build.build()
     yield
-    assert ob.ob_linear_device_error() == 0
+    assert ob.ob_layer_device_error() == 0
 
 
 def _gen(seed):
