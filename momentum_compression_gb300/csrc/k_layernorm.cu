@@ -121,26 +121,42 @@ __global__ void __launch_bounds__(kStrip * kStripRows) k_ln_dw_wide(const LayerN
 
 // ---------------------------------------------------------------------------
 // Rows in registers.  A thread has CH chunks of eight columns: consecutive ones
-// where everything lies on 16 bytes (VEC), else every `threads`-th, so that
-// narrow accesses of a warp still lie side by side.
+// where everything lies on 16 bytes (LIES 1; 2: and the chunks are the row exactly),
+// else (0) every `threads`-th, so that narrow accesses of a warp still lie side by side.
+// The arithmetic takes two columns an instruction.
 // ---------------------------------------------------------------------------
 
-template <bool VEC>
+template <int LIES>
 __device__ __forceinline__ int column(int c, int j, int t, int threads) {
-  return VEC ? (c * threads + t) * 8 + j : (c * 8 + j) * threads + t;
+  return LIES ? (c * threads + t) * 8 + j : (c * 8 + j) * threads + t;
 }
 
-// Chunk c as it lies in memory; what is past the row stays 0.
-template <typename T, bool VEC>
+__device__ __forceinline__ uint64_t twice(float x) { return pair(x, x); }
+
+template <typename T>
+__device__ __forceinline__ uint64_t unpack_pair(uint32_t w);
+template <>
+__device__ __forceinline__ uint64_t unpack_pair<__nv_bfloat16>(uint32_t w) {
+  return pair(w << 16, w & 0xffff0000u);
+}
+template <>
+__device__ __forceinline__ uint64_t unpack_pair<__half>(uint32_t w) {
+  const float2 f = unpack2<__half>(w);
+  return pair(f.x, f.y);
+}
+
+// Chunk c as it lies in memory; what is past the row is 0.
+template <typename T, int LIES>
 struct Chunk {
-  uint4 raw[sizeof(T) / 2];
+  static constexpr int kWords = sizeof(T) / 2;
+  uint4 raw[kWords];
   __device__ __forceinline__ void load(const T* row, int c, int t, int threads, int cols) {
-    constexpr int kWords = sizeof(T) / 2;
+    if constexpr (LIES > 0) {
+      const int at = column<1>(c, 0, t, threads);
+      if (LIES == 1)
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-    if constexpr (VEC) {
-      const int at = column<true>(c, 0, t, threads);
-      if (at < cols) {
+        for (int i = 0; i < kWords; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+      if (LIES == 2 || at < cols) {
         const uint4* p = reinterpret_cast<const uint4*>(row + at);
 #pragma unroll
         for (int i = 0; i < kWords; ++i) raw[i] = p[i];
@@ -149,139 +165,159 @@ struct Chunk {
       T v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int at = column<false>(c, j, t, threads);
+        const int at = column<0>(c, j, t, threads);
         v[j] = from_f32<T>(0.0f);
         if (at < cols) v[j] = row[at];
       }
       memcpy(raw, v, sizeof raw);
     }
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
+  // Pairs of columns in fp32.
+  __device__ __forceinline__ void get(uint64_t (&v)[4]) const {
     if constexpr (sizeof(T) == 4) {
-      memcpy(v, raw, 32);
+      v[0] = pair(raw[0].x, raw[0].y);
+      v[1] = pair(raw[0].z, raw[0].w);
+      v[2] = pair(raw[1].x, raw[1].y);
+      v[3] = pair(raw[1].z, raw[1].w);
     } else {
-      const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2<T>(w[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-      }
+      v[0] = unpack_pair<T>(raw[0].x);
+      v[1] = unpack_pair<T>(raw[0].y);
+      v[2] = unpack_pair<T>(raw[0].z);
+      v[3] = unpack_pair<T>(raw[0].w);
     }
   }
-  __device__ __forceinline__ void put(const float (&v)[8]) {
+  __device__ __forceinline__ void put(const uint64_t (&v)[4]) {
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) unpair(v[k], &f[2 * k], &f[2 * k + 1]);
     if constexpr (sizeof(T) == 4)
-      memcpy(raw, v, 32);
+      memcpy(raw, f, 32);
     else
-      raw[0] = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]),
-                          pack2<T>(v[6], v[7]));
+      raw[0] = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]),
+                          pack2<T>(f[6], f[7]));
   }
   __device__ __forceinline__ void store(T* row, int c, int t, int threads, int cols) const {
-    if constexpr (VEC) {
-      const int at = column<true>(c, 0, t, threads);
-      if (at < cols) {
+    if constexpr (LIES > 0) {
+      const int at = column<1>(c, 0, t, threads);
+      if (LIES == 2 || at < cols) {
         uint4* p = reinterpret_cast<uint4*>(row + at);
 #pragma unroll
-        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) p[i] = raw[i];
+        for (int i = 0; i < kWords; ++i) p[i] = raw[i];
       }
     } else {
       T v[8];
       memcpy(v, raw, sizeof raw);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int at = column<false>(c, j, t, threads);
+        const int at = column<0>(c, j, t, threads);
         if (at < cols) row[at] = v[j];
       }
     }
   }
 };
 
-// Eight weights of the thread's chunk, by their run-time type.
-template <bool VEC>
-__device__ __forceinline__ void load_weights(float (&w)[8], const void* p, int type, float none,
-                                             int c, int t, int threads, int cols) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = none;
-  if (!p) return;
-  if (type == OB_TYPE_F32) {
-    Chunk<float, VEC> k;
-    k.load(static_cast<const float*>(p), c, t, threads, cols);
-    k.get(w);
-  } else if (type == OB_TYPE_BF16) {
-    Chunk<__nv_bfloat16, VEC> k;
-    k.load(static_cast<const __nv_bfloat16*>(p), c, t, threads, cols);
-    k.get(w);
-  } else {
-    Chunk<__half, VEC> k;
-    k.load(static_cast<const __half*>(p), c, t, threads, cols);
-    k.get(w);
-  }
+// f(zero of the type) for a run-time type.
+template <typename F>
+__device__ __forceinline__ void with_type(int type, F f) {
+  if (type == OB_TYPE_F32)
+    f(0.0f);
+  else if (type == OB_TYPE_BF16)
+    f(__nv_bfloat16());
+  else
+    f(__half());
 }
 
-// A row a warp (MULTI false, eight rows a block) or a row a block.
-template <typename T, int CH, bool VEC, bool MULTI>
-__global__ void __launch_bounds__(MULTI ? 512 : 256, MULTI || CH == 8 ? 2 : 3) k_ln_fwd(const __grid_constant__ LayerNormArgs a) {
+// A row a warp (MULTI false, eight rows a block) or a row a block.  The row stays as it
+// lies in memory, two elements a register, and is unpacked again for each pass.
+template <typename T, int CH, int LIES, bool MULTI>
+__global__ void __launch_bounds__(MULTI ? 512 : 256, MULTI || CH == 8 ? 2 : 3)
+    k_ln_fwd(const __grid_constant__ LayerNormArgs a) {
   __shared__ float buf[33];
   const int threads = MULTI ? blockDim.x : 32, t = MULTI ? threadIdx.x : threadIdx.x & 31;
   const uint64_t first = MULTI ? blockIdx.x : (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const uint64_t step = MULTI ? gridDim.x : (uint64_t)gridDim.x * 8;
-  auto row_sum = [&](float v) { return MULTI ? block_sum(v, buf) : warp_butterfly_sum(v); };
+  auto row_sum = [&](uint64_t v) {
+    float lo, hi;
+    unpair(v, &lo, &hi);
+    return MULTI ? block_sum(lo + hi, buf) : warp_butterfly_sum(lo + hi);
+  };
   grid_wait();
   for (uint64_t row = first; row < a.rows; row += step) {
     const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-    Chunk<T, VEC> in[CH];
+    Chunk<T, LIES> in[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) in[c].load(x, c, t, threads, a.cols);
     if (a.residual) {
       const T* r = static_cast<const T*>(a.residual) + row * a.ldr;
-      Chunk<T, VEC> k[CH];
+      Chunk<T, LIES> k[CH];
 #pragma unroll
       for (int c = 0; c < CH; ++c) k[c].load(r, c, t, threads, a.cols);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        float p[8], q[8];
+        uint64_t p[4], q[4];
         in[c].get(p);
         k[c].get(q);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] += q[j];
+        for (int j = 0; j < 4; ++j) p[j] = add2(p[j], q[j]);
         in[c].put(p);  // the sum as it is kept
         if (a.sum) in[c].store(static_cast<T*>(a.sum) + row * a.lds, c, t, threads, a.cols);
       }
     }
-    // The row stays as it lies in memory, two elements a register, and is unpacked again
-    // for each pass.
-    float total = 0.0f;
+    uint64_t total = 0;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      float v[8];
+      uint64_t v[4];
       in[c].get(v);
-      total += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+      total = add2(total, add2(add2(v[0], v[1]), add2(v[2], v[3])));
     }
     const float mean = row_sum(total) / (float)a.cols;
-    float square = 0.0f;
+    const uint64_t less = twice(-mean);
+    uint64_t square = 0;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      float v[8];
+      if (LIES == 1 && column<1>(c, 0, t, threads) >= a.cols) break;
+      uint64_t v[4];
       in[c].get(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] -= mean;
-        if (column<VEC>(c, VEC ? 0 : j, t, threads) < a.cols) square = __fmaf_rn(v[j], v[j], square);
+      for (int j = 0; j < 4; ++j) {
+        v[j] = add2(v[j], less);
+        if (LIES == 0) {
+          float lo, hi;
+          unpair(v[j], &lo, &hi);
+          v[j] = pair(column<0>(c, 2 * j, t, threads) < a.cols ? lo : 0.0f,
+                      column<0>(c, 2 * j + 1, t, threads) < a.cols ? hi : 0.0f);
+        }
+        square = fma2(v[j], v[j], square);
       }
     }
     const float rstd = 1.0f / sqrtf(row_sum(square) / (float)a.cols + a.eps);
+    const uint64_t rstd2 = twice(rstd);
     T* y = static_cast<T*>(a.y) + row * a.ldy;
+    with_type(a.w_type, [&](auto zero) {
+      using W = decltype(zero);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      float v[8], w[8], b[8];
-      in[c].get(v);
-      load_weights<VEC>(w, a.weight, a.w_type, 1.0f, c, t, threads, a.cols);
-      load_weights<VEC>(b, a.bias, a.w_type, 0.0f, c, t, threads, a.cols);
+      for (int c = 0; c < CH; ++c) {
+        uint64_t v[4], w[4];
+        in[c].get(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn((v[j] - mean) * rstd, w[j], b[j]);
-      in[c].put(v);
-      in[c].store(y, c, t, threads, a.cols);
-    }
+        for (int j = 0; j < 4; ++j) v[j] = mul2(add2(v[j], less), rstd2);
+        Chunk<W, LIES> k;
+        if (a.weight) {
+          k.load(static_cast<const W*>(a.weight), c, t, threads, a.cols);
+          k.get(w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], w[j]);
+        }
+        if (a.bias) {
+          k.load(static_cast<const W*>(a.bias), c, t, threads, a.cols);
+          k.get(w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = add2(v[j], w[j]);
+        }
+        in[c].put(v);
+        in[c].store(y, c, t, threads, a.cols);
+      }
+    });
     if (t == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -331,7 +367,7 @@ struct LnBwdPlan {
   bool runs;       // a unit's rows of each array are one run of 16-byte words
 };
 
-template <typename T, int kBwdThreads, int CH, int R, bool VEC>
+template <typename T, int kBwdThreads, int CH, int R, int LIES>
 __global__ void __launch_bounds__(kBwdThreads + 32, kBwdThreads == 256 ? 2 : 1)
     k_ln_bwd(const __grid_constant__ LayerNormBwdArgs a, const __grid_constant__ LnBwdPlan p) {
   constexpr int N = 2 * R;
@@ -399,13 +435,32 @@ __global__ void __launch_bounds__(kBwdThreads + 32, kBwdThreads == 256 ? 2 : 1)
   const int threads = p.threads, t = threadIdx.x & (threads - 1), group = threadIdx.x / threads;
   const int groups = kBwdThreads / threads, warps = threads / 32;
   const float inv = 1.0f / (float)a.cols;
-  float w[CH][8], dw[CH][8], db[CH][8];
+  uint64_t w[CH][4], dw[CH][4], db[CH][4];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    load_weights<VEC>(w[c], a.weight, a.w_type, 1.0f, c, t, threads, a.cols);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[c][j] = db[c][j] = 0.0f;
+    for (int j = 0; j < 4; ++j) {
+      w[c][j] = twice(1.0f);
+      dw[c][j] = db[c][j] = 0;
+    }
+    if (a.weight)
+      with_type(a.w_type, [&](auto zero) {
+        using W = decltype(zero);
+        Chunk<W, LIES> k;
+        k.load(static_cast<const W*>(a.weight), c, t, threads, a.cols);
+        k.get(w[c]);
+      });
   }
+  float ahead_mean[R], ahead_rstd[R];  // of the next unit's rows
+  auto statistics = [&](uint64_t u) {
+    const uint64_t r0 = u * p.rows + (uint64_t)group * R;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      ahead_mean[r] = r0 + r < a.rows ? a.mean[r0 + r] : 0.0f;
+      ahead_rstd[r] = r0 + r < a.rows ? a.rstd[r0 + r] : 0.0f;
+    }
+  };
+  statistics(blockIdx.x);
   int st = 0, par = 0, flip = 0;
   for (uint64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const uint64_t r0 = u * p.rows + (uint64_t)group * R;
@@ -413,14 +468,15 @@ __global__ void __launch_bounds__(kBwdThreads + 32, kBwdThreads == 256 ? 2 : 1)
     float mean[R], rstd[R], sums[N];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      mean[r] = r < rows ? a.mean[r0 + r] : 0.0f;
-      rstd[r] = r < rows ? a.rstd[r0 + r] : 0.0f;
+      mean[r] = ahead_mean[r];
+      rstd[r] = ahead_rstd[r];
       sums[2 * r] = sums[2 * r + 1] = 0.0f;
     }
+    statistics(u + gridDim.x);
     const bool ok = warp_wait(&full[st], par, a.error);
     auto row_of = [&](int k, int r) {
       uint32_t at = st * stage_bytes + k * array_bytes + (group * R + r) * p.pitch;
-      if (!VEC) at += (uint32_t)(reinterpret_cast<uintptr_t>(from[k] + (r0 + r) * ld[k]) & 15);
+      if (LIES == 0) at += (uint32_t)(reinterpret_cast<uintptr_t>(from[k] + (r0 + r) * ld[k]) & 15);
       return reinterpret_cast<const T*>(ring + at);
     };
     if (ok)
@@ -428,24 +484,30 @@ __global__ void __launch_bounds__(kBwdThreads + 32, kBwdThreads == 256 ? 2 : 1)
       for (int r = 0; r < R; ++r) {
         if (r >= rows) break;
         const T *xr = row_of(0, r), *gr = row_of(1, r);
+        const uint64_t less = twice(-mean[r]), scale = twice(rstd[r]);
+        uint64_t s1 = 0, s2 = 0;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          Chunk<T, VEC> x, g;
+          Chunk<T, LIES> x, g;
           x.load(xr, c, t, threads, a.cols);
           g.load(gr, c, t, threads, a.cols);
-          float xv[8], gv[8];
+          uint64_t xv[4], gv[4];
           x.get(xv);
           g.get(gv);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {  // a column past the row has no dy
-            const float h = gv[j] * w[c][j];
-            const float xhat = (xv[j] - mean[r]) * rstd[r];
-            sums[2 * r] += h;
-            sums[2 * r + 1] = __fmaf_rn(h, xhat, sums[2 * r + 1]);
-            dw[c][j] = __fmaf_rn(gv[j], xhat, dw[c][j]);
-            db[c][j] += gv[j];
+          for (int j = 0; j < 4; ++j) {  // a column past the row has no dy
+            const uint64_t h = mul2(gv[j], w[c][j]), xhat = mul2(add2(xv[j], less), scale);
+            s1 = add2(s1, h);
+            s2 = fma2(h, xhat, s2);
+            dw[c][j] = fma2(gv[j], xhat, dw[c][j]);
+            db[c][j] = add2(db[c][j], gv[j]);
           }
         }
+        float lo, hi;
+        unpair(s1, &lo, &hi);
+        sums[2 * r] = lo + hi;
+        unpair(s2, &lo, &hi);
+        sums[2 * r + 1] = lo + hi;
       }
     bool fine = ok;
     if (a.dx) {
@@ -472,24 +534,26 @@ __global__ void __launch_bounds__(kBwdThreads + 32, kBwdThreads == 256 ? 2 : 1)
           if (r >= rows) break;
           const T *xr = row_of(0, r), *gr = row_of(1, r), *sr = row_of(2, r);
           T* out = static_cast<T*>(a.dx) + (r0 + r) * a.lddx;
+          const uint64_t less = twice(-mean[r]), scale = twice(rstd[r]);
+          const uint64_t m1 = twice(-m[2 * r]), m2 = twice(-m[2 * r + 1]);
 #pragma unroll
           for (int c = 0; c < CH; ++c) {
-            Chunk<T, VEC> x, g;
+            Chunk<T, LIES> x, g;
             x.load(xr, c, t, threads, a.cols);
             g.load(gr, c, t, threads, a.cols);
-            float xv[8], gv[8];
+            uint64_t xv[4], gv[4];
             x.get(xv);
             g.get(gv);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float xhat = (xv[j] - mean[r]) * rstd[r];
-              gv[j] = rstd[r] * __fmaf_rn(-xhat, m[2 * r + 1], gv[j] * w[c][j] - m[2 * r]);
+            for (int j = 0; j < 4; ++j) {
+              const uint64_t xhat = mul2(add2(xv[j], less), scale);
+              gv[j] = mul2(scale, fma2(xhat, m2, add2(mul2(gv[j], w[c][j]), m1)));
             }
             if (a.dsum) {
               x.load(sr, c, t, threads, a.cols);
               x.get(xv);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) gv[j] += xv[j];
+              for (int j = 0; j < 4; ++j) gv[j] = add2(gv[j], xv[j]);
             }
             g.put(gv);
             g.store(out, c, t, threads, a.cols);
@@ -510,15 +574,19 @@ __global__ void __launch_bounds__(kBwdThreads + 32, kBwdThreads == 256 ? 2 : 1)
       if (groups > 1) {
         named_sync(15, kBwdThreads);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) merge[j * kBwdThreads + threadIdx.x] = which ? db[c][j] : dw[c][j];
+        for (int j = 0; j < 4; ++j)
+          unpair(which ? db[c][j] : dw[c][j], &merge[2 * j * kBwdThreads + threadIdx.x],
+                 &merge[(2 * j + 1) * kBwdThreads + threadIdx.x]);
         named_sync(15, kBwdThreads);
       }
       if (group) continue;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int at = column<VEC>(c, j, t, threads);
+        const int at = column<LIES>(c, j, t, threads);
         if (at >= a.cols) continue;
-        float v = which ? db[c][j] : dw[c][j];
+        float two[2];
+        unpair(which ? db[c][j / 2] : dw[c][j / 2], &two[0], &two[1]);
+        float v = two[j & 1];
         for (int q = 1; q < groups; ++q) v += merge[j * kBwdThreads + q * threads + t];
         a.partial[((size_t)blockIdx.x * 2 + which) * a.cols + at] = v;
       }
@@ -561,28 +629,32 @@ constexpr int kSms = 152;
 constexpr int kFwdMost = 512 * 8 * 4;  // columns that a block's registers hold
 constexpr int kBwdMost = 512 * 8 * 2;
 
-template <typename T, bool VEC>
+template <typename T, int LIES>
 cudaError_t fwd(const LayerNormArgs& a, cudaStream_t s) {
   const int chunks = (a.cols + 7) / 8;
   // A row a warp needs no barrier, a row a block more of them at a time: the latter
   // where the rows alone do not fill the card, or a warp's registers do not last.
-  constexpr int kWarpMost = !VEC ? 2 : sizeof(T) == 4 ? 4 : 8;  // chunks of a lane
+  constexpr int kWarpMost = !LIES ? 2 : sizeof(T) == 4 ? 4 : 8;  // chunks of a lane
   if (chunks <= 32 * kWarpMost && (chunks <= 32 || a.rows >= (uint64_t)kSms * 8)) {
     const uint64_t blocks = (a.rows + 7) / 8;
     const int grid = (int)(blocks < (uint64_t)kSms * 32 ? blocks : kSms * 32);
     auto go = [&](auto ch) {
-      return launch_behind(k_ln_fwd<T, decltype(ch)::value, VEC, false>, dim3(grid), dim3(256), 0, s, a);
+      constexpr int CH = decltype(ch)::value <= kWarpMost ? decltype(ch)::value : kWarpMost;
+      if (LIES && a.cols == CH * 256)
+        return launch_behind(k_ln_fwd<T, CH, LIES ? 2 : 0, false>, dim3(grid), dim3(256), 0, s, a);
+      return launch_behind(k_ln_fwd<T, CH, LIES, false>, dim3(grid), dim3(256), 0, s, a);
     };
     if (chunks <= 32) return go(std::integral_constant<int, 1>());
     if (chunks <= 64) return go(std::integral_constant<int, 2>());
-    if (chunks <= 128) return go(std::integral_constant<int, kWarpMost < 4 ? kWarpMost : 4>());
-    return go(std::integral_constant<int, kWarpMost>());
+    if (chunks <= 96 && LIES) return go(std::integral_constant<int, 3>());
+    if (chunks <= 128) return go(std::integral_constant<int, 4>());
+    return go(std::integral_constant<int, 8>());
   }
   const int grid = (int)(a.rows < (uint64_t)kSms * 16 ? a.rows : kSms * 16);
   const bool few = chunks <= 512 && (a.rows < kSms * 2 || chunks <= 128);
   const int threads = few ? (chunks + 31) / 32 * 32 : (chunks + 127) / 128 * 32;
-  return few ? launch_behind(k_ln_fwd<T, 1, VEC, true>, dim3(grid), dim3(threads), 0, s, a)
-             : launch_behind(k_ln_fwd<T, 4, VEC, true>, dim3(grid), dim3(threads), 0, s, a);
+  return few ? launch_behind(k_ln_fwd<T, 1, LIES, true>, dim3(grid), dim3(threads), 0, s, a)
+             : launch_behind(k_ln_fwd<T, 4, LIES, true>, dim3(grid), dim3(threads), 0, s, a);
 }
 
 // Threads of a block and of a group (a power of two from 32), and chunks a thread.
@@ -594,40 +666,46 @@ int group_threads(int cols) {
   return t;
 }
 
-template <typename T, int kBwdThreads, int CH, int R, bool VEC>
+// Bytes of shared memory for the rows: two blocks an SM, or one.
+constexpr uint32_t ring_most(int threads) { return threads == 256 ? 98304 : 196608; }
+
+template <typename T, int kBwdThreads, int CH, int R, int LIES>
 cudaError_t bwd_launch(const LayerNormBwdArgs& a, cudaStream_t s) {
   LnBwdPlan p{};
   p.threads = group_threads(a.cols);
   p.rows = kBwdThreads / p.threads * R;
   p.arrays = a.dsum ? 3 : 2;
   const uint32_t row = a.cols * (uint32_t)sizeof(T);
-  p.pitch = VEC ? row : (row + 30) / 16 * 16;
-  p.runs = VEC && a.ldx == (uint64_t)a.cols && a.lddy == a.ldx && (!a.dsum || a.ldds == a.ldx);
-  const uint32_t stage = p.rows * p.pitch * p.arrays;
-  const uint32_t most = kBwdThreads == 256 ? 96 * 1024 : 192 * 1024;  // two blocks an SM, or one
+  p.pitch = LIES ? row : (row + 30) / 16 * 16;
+  p.runs = LIES && a.ldx == (uint64_t)a.cols && a.lddy == a.ldx && (!a.dsum || a.ldds == a.ldx);
+  const uint32_t stage = p.rows * p.pitch * p.arrays, most = ring_most(kBwdThreads);
   p.stages = (int)(most / stage < kBwdStages ? most / stage : kBwdStages);
   static PerDeviceOnce once;
   const cudaError_t e = once.run([&] {
-    return cudaFuncSetAttribute(k_ln_bwd<T, kBwdThreads, CH, R, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)most);
+    return cudaFuncSetAttribute(k_ln_bwd<T, kBwdThreads, CH, R, LIES>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   });
   if (e != cudaSuccess) return e;
-  return launch_behind(k_ln_bwd<T, kBwdThreads, CH, R, VEC>, dim3(a.parts), dim3(kBwdThreads + 32),
+  return launch_behind(k_ln_bwd<T, kBwdThreads, CH, R, LIES>, dim3(a.parts), dim3(kBwdThreads + 32),
                        (size_t)(p.stages * stage), s, a, p);
 }
 
-template <typename T, bool VEC>
+template <typename T, int LIES>
 cudaError_t bwd(const LayerNormBwdArgs& a, cudaStream_t s) {
   if (a.cols <= 256 * 8) {
     // Four rows of a group share a barrier, where there are units enough for every
     // block and two of them fit.
     const int groups = 256 / group_threads(a.cols);
-    const size_t unit = (size_t)groups * 4 * (a.cols * sizeof(T) + 30) * (a.dsum ? 3 : 2);
-    const bool four = a.rows >= (uint64_t)a.parts * groups * 16 && unit <= 48 * 1024;
-    return four ? bwd_launch<T, 256, 1, 4, VEC>(a, s) : bwd_launch<T, 256, 1, 1, VEC>(a, s);
+    const size_t row = LIES ? a.cols * sizeof(T) : a.cols * sizeof(T) + 30;
+    const size_t unit = (size_t)groups * 4 * row * (a.dsum ? 3 : 2);
+    const bool four = a.rows >= (uint64_t)a.parts * groups * 16 && unit <= ring_most(256) / 2;
+    if (LIES && a.cols == group_threads(a.cols) * 8)
+      return four ? bwd_launch<T, 256, 1, 4, LIES ? 2 : 0>(a, s)
+                  : bwd_launch<T, 256, 1, 1, LIES ? 2 : 0>(a, s);
+    return four ? bwd_launch<T, 256, 1, 4, LIES>(a, s) : bwd_launch<T, 256, 1, 1, LIES>(a, s);
   }
-  return a.cols <= 512 * 8 ? bwd_launch<T, 512, 1, 1, VEC>(a, s)
-                           : bwd_launch<T, 512, 2, 1, VEC>(a, s);
+  return a.cols <= 512 * 8 ? bwd_launch<T, 512, 1, 1, LIES>(a, s)
+                           : bwd_launch<T, 512, 2, 1, LIES>(a, s);
 }
 
 }  // namespace
@@ -644,7 +722,7 @@ cudaError_t launch_layernorm_fwd(const LayerNormArgs& a, int type, cudaStream_t 
     const uint64_t ld[4] = {a.ldx, a.ldr, a.ldy, a.lds};
     for (int i = 0; i < 4; ++i)
       if (p[i]) vec = vec && on16(p[i]) && (a.rows == 1 || ld[i] * sizeof(T) % 16 == 0);
-    return vec ? fwd<T, true>(a, s) : fwd<T, false>(a, s);
+    return vec ? fwd<T, 1>(a, s) : fwd<T, 0>(a, s);
   });
 }
 
@@ -678,7 +756,7 @@ cudaError_t launch_layernorm_bwd(const LayerNormBwdArgs& b, int type, cudaStream
       for (int i = 0; i < 4; ++i)
         if (p[i]) vec = vec && on16(p[i]) && (a.rows == 1 || ld[i] * sizeof(T) % 16 == 0);
       e = layer_error_word(&a.error);
-      if (e == cudaSuccess) e = vec ? bwd<T, true>(a, s) : bwd<T, false>(a, s);
+      if (e == cudaSuccess) e = vec ? bwd<T, 1>(a, s) : bwd<T, 0>(a, s);
     }
     if (e != cudaSuccess || !sums) return e;
     return launch_behind(k_ln_sums, dim3((2 * a.cols + 31) / 32), dim3(256), 0, s, a);
