@@ -4,9 +4,9 @@
 // of 256 x 256 (each holds 128 rows of A and of the sum, and half of B), or, where
 // that leaves most of the card idle, a block a tile of 128 x 128.  In a block one
 // warp issues the copies (tiles of 64 along the sum, 128-byte swizzle, either
-// operand stored along the sum or across it), one the products, and eight take
-// the sums out of tensor memory, 32 columns of a row a thread: bias, activation,
-// residual, one rounding.  Tensor memory holds two sums, so that the epilogue
+// operand stored along the sum or across it), one the products, and sixteen
+// take the sums out of tensor memory, 16 columns of a row a thread: bias,
+// activation, residual, one rounding.  Tensor memory holds two sums, so that the epilogue
 // runs beside the next unit's products.
 //
 // Tiles that do not fill the workers evenly are cut along the sum: worker p of P
@@ -29,7 +29,9 @@ namespace {
 __device__ unsigned g_layer_error;
 
 constexpr int BK = 64;            // of the sum a step
-constexpr int kEpWarps = 8;
+constexpr int kEpWarps = 16;
+constexpr int kEpCols = 16;       // columns of a row that a lane takes at a time
+constexpr int kTurn = 16 * (kEpCols + 1);  // floats of a warp's own area: half of its rows
 constexpr int kGemmThreads = 64 + 32 * kEpWarps;
 
 template <int CG>
@@ -39,10 +41,10 @@ struct Shape {
   static constexpr int kStages = 6;
   static constexpr uint32_t kA = 128 * BK * 2, kB = 128 * BK * 2, kStage = kA + kB;
   static constexpr uint32_t kAlloc = 2 * kCols;  // columns of tensor memory
-  static constexpr uint32_t kTurn = kStages * kStage;  // offset of the warps' own areas
-  static constexpr uint32_t kBytes = 1024 + kTurn + kEpWarps * 32 * 33 * 4;
+  static constexpr uint32_t kArea = kStages * kStage;  // offset of the warps' own areas
+  static constexpr uint32_t kBytes = 1024 + kArea + kEpWarps * kTurn * 4;
 };
-static_assert(Shape<2>::kBytes <= 227 * 1024, "");
+static_assert(Shape<2>::kBytes <= 226 * 1024, "with the barriers, an SM's 227 KB");
 
 struct GemmArgs {
   CUtensorMap a, b;
@@ -132,90 +134,87 @@ __device__ __forceinline__ void load32(const void* p, uint32_t* v, int wide = 2)
                : "memory");
 }
 
-// z without bias -> outputs, for 32 columns from n on of row m, a row a lane.
+// z without bias -> outputs, for 16 columns from n on of row m, a row a lane.
 template <typename T>
-__device__ __forceinline__ void epilogue_wide(const Epilogue& e, float (&z)[32], int64_t m,
+__device__ __forceinline__ void epilogue_wide(const Epilogue& e, float (&z)[kEpCols], int64_t m,
                                               int64_t n, bool row) {
+  uint32_t o[8];
   if (e.bias) {
     const uint4* b = reinterpret_cast<const uint4*>(static_cast<const T*>(e.bias) + n);
+    const uint4 x = b[0], y = b[1];
+    o[0] = x.x, o[1] = x.y, o[2] = x.z, o[3] = x.w;
+    o[4] = y.x, o[5] = y.y, o[6] = y.z, o[7] = y.w;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint4 w = b[q];
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = unpack2<T>(u[k]);
-        z[8 * q + 2 * k] += f.x;
-        z[8 * q + 2 * k + 1] += f.y;
-      }
+    for (int k = 0; k < 8; ++k) {
+      const float2 f = unpack2<T>(o[k]);
+      z[2 * k] += f.x;
+      z[2 * k + 1] += f.y;
     }
   }
-  uint32_t o[16];
   if (e.z.data && row) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
-    T* p = static_cast<T*>(e.z.data) + m * e.z.ld + n;
-    store32(p, o, e.wide);
-    store32(p + 16, o + 8, e.wide);
+    for (int k = 0; k < 8; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
+    store32(static_cast<T*>(e.z.data) + m * e.z.ld + n, o, e.wide);
   }
-  if (e.residual.data && row) {
-    const T* p = static_cast<const T*>(e.residual.data) + m * e.residual.ld + n;
-    load32(p, o, e.wide);
-    load32(p + 16, o + 8, e.wide);
-  }
+  if (e.residual.data && row)
+    load32(static_cast<const T*>(e.residual.data) + m * e.residual.ld + n, o, e.wide);
   by_act(e.act, [&](auto act) {
 #pragma unroll
-    for (int k = 0; k < 32; ++k) z[k] = act_of<decltype(act)::value>(z[k]);
+    for (int k = 0; k < kEpCols; k += 2) act_of2<decltype(act)::value>(z[k], z[k + 1]);
   });
   if (e.residual.data)
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
+    for (int k = 0; k < 8; ++k) {
       const float2 f = unpack2<T>(o[k]);
       z[2 * k] += f.x;
       z[2 * k + 1] += f.y;
     }
   if (!row) return;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
-  T* p = static_cast<T*>(e.out.data) + m * e.out.ld + n;
-  store32(p, o, e.wide);
-  store32(p + 16, o + 8, e.wide);
+  for (int k = 0; k < 8; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
+  store32(static_cast<T*>(e.out.data) + m * e.out.ld + n, o, e.wide);
 }
 
 // The same at any alignment and at the matrix's edges: turned through the
-// warp's own shared memory, a column a lane.
+// warp's own shared memory, a column of every second row a lane.
 template <typename T>
-__device__ __forceinline__ void epilogue_edge(const Epilogue& e, const float (&z)[32], int64_t m0,
-                                              int64_t n0, int64_t M, int64_t N, float* turn) {
-  const int lane = threadIdx.x & 31;
-  __syncwarp();
+__device__ __forceinline__ void epilogue_edge(const Epilogue& e, const float (&z)[kEpCols],
+                                              int64_t m0, int64_t n0, int64_t M, int64_t N,
+                                              float* turn) {
+  const int lane = threadIdx.x & 31, col = lane & (kEpCols - 1);
+  const int64_t n = n0 + col;
+  const float bias = e.bias && n < N ? to_f32(static_cast<const T*>(e.bias)[n]) : 0.0f;
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    __syncwarp();
+    if (lane / 16 == h)
 #pragma unroll
-  for (int k = 0; k < 32; ++k) turn[lane * 33 + k] = z[k];
-  __syncwarp();
-  const int64_t n = n0 + lane;
-  if (n >= N) return;
-  const int rows = M - m0 < 32 ? (int)(M - m0) : 32;
-  const float bias = e.bias ? to_f32(static_cast<const T*>(e.bias)[n]) : 0.0f;
-  by_act(e.act, [&](auto act) {
+      for (int k = 0; k < kEpCols; ++k) turn[lane % 16 * (kEpCols + 1) + k] = z[k];
+    __syncwarp();
+    if (n >= N) continue;
+    const int64_t m = m0 + 16 * h;
+    const int rows = M - m < 16 ? (int)(M - m) : 16;
+    by_act(e.act, [&](auto act) {
 #pragma unroll 4
-    for (int r = 0; r < rows; ++r) {
-      const float x = e.bias ? turn[r * 33 + lane] + bias : turn[r * 33 + lane];
-      if (e.z.data) static_cast<T*>(e.z.data)[(m0 + r) * e.z.ld + n] = from_f32<T>(x);
-      float y = act_of<decltype(act)::value>(x);
-      if (e.residual.data)
-        y += to_f32(static_cast<const T*>(e.residual.data)[(m0 + r) * e.residual.ld + n]);
-      static_cast<T*>(e.out.data)[(m0 + r) * e.out.ld + n] = from_f32<T>(y);
-    }
-  });
+      for (int r = lane / kEpCols; r < rows; r += 32 / kEpCols) {
+        const float v = turn[r * (kEpCols + 1) + col], x = e.bias ? v + bias : v;
+        if (e.z.data) static_cast<T*>(e.z.data)[(m + r) * e.z.ld + n] = from_f32<T>(x);
+        float y = act_of<decltype(act)::value>(x);
+        if (e.residual.data)
+          y += to_f32(static_cast<const T*>(e.residual.data)[(m + r) * e.residual.ld + n]);
+        static_cast<T*>(e.out.data)[(m + r) * e.out.ld + n] = from_f32<T>(y);
+      }
+    });
+  }
 }
 
 // m0, n0: the warp's first row and column.
 template <typename T>
-__device__ __forceinline__ void epilogue(const Epilogue& e, float (&z)[32], int64_t m0, int64_t n0,
-                                         int64_t M, int64_t N, float* turn) {
+__device__ __forceinline__ void epilogue(const Epilogue& e, float (&z)[kEpCols], int64_t m0,
+                                         int64_t n0, int64_t M, int64_t N, float* turn) {
   if (n0 >= N || m0 >= M) return;
   const int64_t m = m0 + (threadIdx.x & 31);
-  if (e.wide && n0 + 32 <= N)
+  if (e.wide && n0 + kEpCols <= N)
     epilogue_wide<T>(e, z, m, n0, m < M);
   else
     epilogue_edge<T>(e, z, m0, n0, M, N, turn);
@@ -383,9 +382,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
     }
   } else {
     // ----- epilogue --------------------------------------------------------
-    const int w = warp - 2, quarter = warp & 3, half = w >> 2;
-    float* turn = reinterpret_cast<float*>(smem + S::kTurn) + w * 32 * 33;
-    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    // A warp reaches 32 lanes of tensor memory, by its number; four share them, a quarter
+    // of the columns each.
+    constexpr int kCols = S::kCols / (kEpWarps / 4);
+    const int w = warp - 2, lanes0 = (warp & 3) * 32, col0 = (w >> 2) * kCols;
+    float* turn = reinterpret_cast<float*>(smem + S::kArea) + w * kTurn;
+    const uint32_t lanes = (uint32_t)lanes0 << 16;
     const uint32_t empty = CG == 2 ? cluster_addr(smem_u32(&bar.sum_empty[0]), 0) : 0;
     Units u(a, worker);
     bool ok = true;
@@ -396,15 +398,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       tc_fence_after();
       int tm, tn;
       tile_at(u.tile, a.tiles_m, a.tiles_n, &tm, &tn);
-      const int row0 = (int)rank * 128 + quarter * 32;  // in the tile
+      const int row0 = (int)rank * 128 + lanes0;  // in the tile
       const int64_t m0 = (int64_t)tm * S::kRows + row0;
 #pragma unroll 1
-      for (int c = half * (S::kCols / 2); c < (half + 1) * (S::kCols / 2); c += 32) {
-        uint32_t r[32];
+      for (int c = col0; c < col0 + kCols; c += kEpCols) {
+        uint32_t r[kEpCols];
         __syncwarp();  // the last columns' lanes may have parted at an edge
-        tmem_ld32(r, tmem + lanes + buf * S::kCols + c);
+        tmem_ld16(r, tmem + lanes + buf * S::kCols + c);
         tmem_wait_ld(r);
-        if (c + 32 == (half + 1) * (S::kCols / 2)) {  // the last: the next sum may come
+        if (c + kEpCols == col0 + kCols) {  // the last: the next sum may come
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -416,12 +418,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
         }
         if (u.part) {
           float* p = a.partial + (((int64_t)worker * 2 + u.slot) * S::kRows + row0 + lane) * S::kCols + c;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) store32(p + 8 * q, r + 8 * q);
+          store32(p, r);
+          store32(p + 8, r + 8);
         } else {
-          float z[32];
+          float z[kEpCols];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) z[k] = __uint_as_float(r[k]);
+          for (int k = 0; k < kEpCols; ++k) z[k] = __uint_as_float(r[k]);
           const int64_t n0 = (int64_t)tn * S::kCols + c;
           if (a.ep.type == OB_TYPE_BF16)
             epilogue<__nv_bfloat16>(a.ep, z, m0, n0, a.M, a.N, turn);
@@ -446,16 +448,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
   }
 }
 
-// The cut tiles: a warp 32 rows of 32 columns, its parts in their order.
+// The cut tiles: a warp 32 rows of 16 columns, its parts in their order.
 template <int CG>
 __global__ void __launch_bounds__(256) k_gemm_parts(const __grid_constant__ GemmArgs a) {
   using S = Shape<CG>;
-  __shared__ float turn[8][32 * 33];
+  __shared__ float turn[8][kTurn];
   grid_wait();
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kPer = (S::kRows / 32) * (S::kCols / 32);  // warps a tile
+  constexpr int kAcross = S::kCols / kEpCols, kPer = (S::kRows / 32) * kAcross;  // warps a tile
   const int unit = blockIdx.x * 8 + w, t = unit / kPer, in = unit % kPer;
-  const int row0 = in / (S::kCols / 32) * 32, c = in % (S::kCols / 32) * 32;
+  const int row0 = in / kAcross * 32, c = in % kAcross * kEpCols;
   int tm, tn;
   tile_at(a.whole + t, a.tiles_m, a.tiles_n, &tm, &tn);
   const int64_t m0 = (int64_t)tm * S::kRows + row0, n0 = (int64_t)tn * S::kCols + c;
@@ -469,9 +471,9 @@ __global__ void __launch_bounds__(256) k_gemm_parts(const __grid_constant__ Gemm
     while (share(total, p, a.workers) > step) --p;
     return p;
   };
-  float z[32];
+  float z[kEpCols];
 #pragma unroll
-  for (int k = 0; k < 32; ++k) z[k] = 0.0f;
+  for (int k = 0; k < kEpCols; ++k) z[k] = 0.0f;
   int p0 = 0, p1 = -1;
   if (total > 0) {  // else the sums are empty
     p0 = owner(first);
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(256) k_gemm_parts(const __grid_constant__ Gemm
     const float* q =
         a.partial + (((int64_t)p * 2 + slot) * S::kRows + row0 + lane) * S::kCols + c;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kEpCols / 8; ++k) {
       uint32_t v[8];
       load32(q + 8 * k, v);
 #pragma unroll
@@ -554,7 +556,7 @@ cudaError_t run(const Gemm& g, const Plan& p, cudaStream_t s) {
   a.ep = g.ep;
   a.partial = g.partial;
   const int rest = p.tiles_m * p.tiles_n - p.whole;
-  const dim3 parts(rest * ((S::kRows / 32) * (S::kCols / 32) / 8));
+  const dim3 parts(rest * ((S::kRows / 32) * (S::kCols / kEpCols) / 8));
   if (!p.steps) return launch_behind(k_gemm_parts<CG>, parts, dim3(256), 0, s, a);
   static PerDeviceOnce once;
   e = once.run([] {

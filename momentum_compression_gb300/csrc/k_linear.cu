@@ -28,6 +28,37 @@ struct DzArgs {
   int act;
 };
 
+// V elements as they lie in memory (8: 16 bytes).
+template <typename T, int V>
+struct Cell {
+  T v[V];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (V == 8) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      memcpy(v, &u, 16);
+    } else {
+      v[0] = *p;
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (V == 8) {
+      uint4 u;
+      memcpy(&u, v, 16);
+      *reinterpret_cast<uint4*>(p) = u;
+    } else {
+      *p = v[0];
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[V]) const {
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[k] = to_f32(v[k]);
+  }
+  __device__ __forceinline__ void put(const float (&f)[V]) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = from_f32<T>(f[k]);
+  }
+};
+
 // V columns a thread (8: 16-byte loads).
 template <typename T, int V>
 __global__ void __launch_bounds__(kDzThreads) k_dz(const __grid_constant__ DzArgs a) {
@@ -43,36 +74,35 @@ __global__ void __launch_bounds__(kDzThreads) k_dz(const __grid_constant__ DzArg
   if (n < a.N)
     by_act(a.act, [&](auto act) {
       constexpr int kAct = decltype(act)::value;
-#pragma unroll 4
-      for (int64_t r = r0 + y; r < r1; r += ty) {
-        const T* dy = static_cast<const T*>(a.dy.data) + r * a.dy.ld + n;
-        const T* z = static_cast<const T*>(a.z.data) + r * a.z.ld + n;
-        float g[V];
-        if constexpr (V == 8) {
-          const uint4 u = *reinterpret_cast<const uint4*>(dy);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (kAct != OB_ACT_NONE) v = *reinterpret_cast<const uint4*>(z);
-          const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+      // Several rows' loads are on their way at once: the stores, which may touch anything as
+      // far as the compiler knows, come behind them.
+      constexpr int B = 4;
+      for (int64_t r = r0 + y; r < r1; r += B * ty) {
+        Cell<T, V> dy[B], z[B];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 d = unpack2<T>(w[k]), s = unpack2<T>(q[k]);
-            g[2 * k] = d.x * act_slope<kAct>(s.x);
-            g[2 * k + 1] = d.y * act_slope<kAct>(s.y);
+        for (int b = 0; b < B; ++b)
+          if (r + b * ty < r1) {
+            dy[b].load(static_cast<const T*>(a.dy.data) + (r + b * ty) * a.dy.ld + n);
+            if (kAct != OB_ACT_NONE)
+              z[b].load(static_cast<const T*>(a.z.data) + (r + b * ty) * a.z.ld + n);
           }
-        } else {
-          g[0] = to_f32(*dy);
-          if (kAct != OB_ACT_NONE) g[0] *= act_slope<kAct>(to_f32(*z));
-        }
 #pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] += g[k];
-        if (!a.dz.data) continue;
-        T* out = static_cast<T*>(a.dz.data) + r * a.dz.ld + n;
-        if constexpr (V == 8)
-          *reinterpret_cast<uint4*>(out) = make_uint4(pack2<T>(g[0], g[1]), pack2<T>(g[2], g[3]),
-                                                      pack2<T>(g[4], g[5]), pack2<T>(g[6], g[7]));
-        else
-          *out = from_f32<T>(g[0]);
+        for (int b = 0; b < B; ++b) {
+          if (r + b * ty >= r1) break;
+          float g[V], s[V];
+          dy[b].get(g);
+          if (kAct != OB_ACT_NONE) {
+            z[b].get(s);
+#pragma unroll
+            for (int k = 0; k < V; ++k) g[k] *= act_slope<kAct>(s[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < V; ++k) acc[k] += g[k];
+          if (a.dz.data) {
+            dy[b].put(g);
+            dy[b].store(static_cast<T*>(a.dz.data) + (r + b * ty) * a.dz.ld + n);
+          }
+        }
       }
     });
   if (!a.partial) return;
