@@ -49,15 +49,16 @@ cudaError_t attn_tensor_map(CUtensorMap* map, const Heads& t, int type, int D, i
 }
 
 cudaError_t matrix_tensor_map(CUtensorMap* map, const Mat& m, int type, int64_t rows, int64_t cols,
-                              int box_rows) {
+                              int box_cols, int box_rows) {
   Encode encode = nullptr;
   const cudaError_t e = encoder(&encode);
   if (e != cudaSuccess) return e;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)m.ld * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, step[2] = {1, 1};
   const CUresult r = encode(map, map_type(type), 2, m.data, dims, strides, box, step,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

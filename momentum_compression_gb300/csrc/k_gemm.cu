@@ -5,8 +5,10 @@
 // that leaves most of the card idle, a block a tile of 128 x 128.  In a block one
 // warp issues the copies (tiles of 64 along the sum, 128-byte swizzle, either
 // operand stored along the sum or across it), one the products, and sixteen
-// take the sums out of tensor memory, 16 columns of a row a thread: bias,
-// activation, residual, one rounding.  Tensor memory holds two sums, so that the epilogue
+// take the sums out of tensor memory, a row a lane: bias, activation, residual, one
+// rounding.  They store through shared memory and TMA, 32 x 32 at a time, and
+// read the residual the same way: lanes that store rows of their own cost up to half of
+// the time (16384 x 768 x 768 with a residual 34 us).  Tensor memory holds two sums, so that the epilogue
 // runs beside the next unit's products.
 //
 // Tiles that do not fill the workers evenly are cut along the sum: worker p of P
@@ -30,24 +32,24 @@ __device__ unsigned g_layer_error;
 
 constexpr int BK = 64;            // of the sum a step
 constexpr int kEpWarps = 16;
-constexpr int kEpCols = 16;       // columns of a row that a lane takes at a time
-constexpr int kTurn = 16 * (kEpCols + 1);  // floats of a warp's own area: half of its rows
+constexpr int kGroup = 32;        // columns of a warp's 32 rows that it stores at a time
+constexpr uint32_t kBuf = 32 * kGroup * 2;  // bytes of them; a warp has two, or one in fp32
 constexpr int kGemmThreads = 64 + 32 * kEpWarps;
 
 template <int CG>
 struct Shape {
   static constexpr int kRows = 128 * CG;       // of a tile
   static constexpr int kCols = 128 * CG;
-  static constexpr int kStages = 6;
+  static constexpr int kStages = 5;
   static constexpr uint32_t kA = 128 * BK * 2, kB = 128 * BK * 2, kStage = kA + kB;
   static constexpr uint32_t kAlloc = 2 * kCols;  // columns of tensor memory
   static constexpr uint32_t kArea = kStages * kStage;  // offset of the warps' own areas
-  static constexpr uint32_t kBytes = 1024 + kArea + kEpWarps * kTurn * 4;
+  static constexpr uint32_t kBytes = 1024 + kArea + kEpWarps * 2 * kBuf;
 };
 static_assert(Shape<2>::kBytes <= 226 * 1024, "with the barriers, an SM's 227 KB");
 
 struct GemmArgs {
-  CUtensorMap a, b;
+  CUtensorMap a, b, out, z, residual;  // the last three where ep.tiled and there is one
   int a_mn, b_mn;
   int64_t M, N;
   int steps;             // of the sum
@@ -109,119 +111,170 @@ struct Units {
   }
 };
 
-// Eight 4-byte words at once, or (`wide` 1) twice four where a row is only 16-byte aligned.
-__device__ __forceinline__ void store32(void* p, const uint32_t* v, int wide = 2) {
-  if (wide == 1) {
-    static_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    static_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-    return;
-  }
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
+// ---------------------------------------------------------------------------
+// Epilogue of a warp's 32 rows and 32 columns, a row a lane, sixteen columns at a time.
+// ---------------------------------------------------------------------------
+
+// Where 16-byte piece c (0..3) of a row of 64 bytes lies: as TMA's 64-byte swizzle has it, and
+// the pieces of a warp's rows in different banks.
+__device__ __forceinline__ uint4* piece(uint8_t* buf, int row, int c) {
+  return reinterpret_cast<uint4*>(buf + row * 64 + ((c ^ (row >> 1 & 3)) << 4));
 }
-__device__ __forceinline__ void load32(const void* p, uint32_t* v, int wide = 2) {
-  if (wide == 1) {
-    const uint4 x = static_cast<const uint4*>(p)[0], y = static_cast<const uint4*>(p)[1];
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-    return;
+template <typename T>
+__device__ __forceinline__ void put16(uint8_t* buf, int row, int half, const float (&z)[16]) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    *piece(buf, row, 2 * half + q) =
+        make_uint4(pack2<T>(z[8 * q], z[8 * q + 1]), pack2<T>(z[8 * q + 2], z[8 * q + 3]),
+                   pack2<T>(z[8 * q + 4], z[8 * q + 5]), pack2<T>(z[8 * q + 6], z[8 * q + 7]));
+}
+template <typename T>
+__device__ __forceinline__ void add16(const uint4& x, const uint4& y, float (&z)[16]) {
+  const uint32_t o[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float2 f = unpack2<T>(o[k]);
+    z[2 * k] += f.x;
+    z[2 * k + 1] += f.y;
   }
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-                 "=r"(v[7])
-               : "l"(p)
-               : "memory");
 }
 
-// z without bias -> outputs, for 16 columns from n on of row m, a row a lane.
+// Tiled: columns n0 + 16 half .. of the group, into the buffers of z and y; the latter
+// holds the residual.
 template <typename T>
-__device__ __forceinline__ void epilogue_wide(const Epilogue& e, float (&z)[kEpCols], int64_t m,
-                                              int64_t n, bool row) {
-  uint32_t o[8];
+__device__ __forceinline__ void finish16(const Epilogue& e, float (&z)[16], int64_t n, int64_t N,
+                                         int half, uint8_t* zbuf, uint8_t* ybuf) {
+  const int lane = threadIdx.x & 31;
   if (e.bias) {
-    const uint4* b = reinterpret_cast<const uint4*>(static_cast<const T*>(e.bias) + n);
-    const uint4 x = b[0], y = b[1];
-    o[0] = x.x, o[1] = x.y, o[2] = x.z, o[3] = x.w;
-    o[4] = y.x, o[5] = y.y, o[6] = y.z, o[7] = y.w;
+    const T* b = static_cast<const T*>(e.bias) + n;
+    if (n + 16 <= N) {
+      add16<T>(reinterpret_cast<const uint4*>(b)[0], reinterpret_cast<const uint4*>(b)[1], z);
+    } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 f = unpack2<T>(o[k]);
-      z[2 * k] += f.x;
-      z[2 * k + 1] += f.y;
+      for (int k = 0; k < 16; ++k)
+        if (n + k < N) z[k] += to_f32(b[k]);
     }
   }
-  if (e.z.data && row) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
-    store32(static_cast<T*>(e.z.data) + m * e.z.ld + n, o, e.wide);
-  }
-  if (e.residual.data && row)
-    load32(static_cast<const T*>(e.residual.data) + m * e.residual.ld + n, o, e.wide);
+  if (e.z.data) put16<T>(zbuf, lane, half, z);
   by_act(e.act, [&](auto act) {
 #pragma unroll
-    for (int k = 0; k < kEpCols; k += 2) act_of2<decltype(act)::value>(z[k], z[k + 1]);
+    for (int k = 0; k < 16; k += 2) act_of2<decltype(act)::value>(z[k], z[k + 1]);
   });
-  if (e.residual.data)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 f = unpack2<T>(o[k]);
-      z[2 * k] += f.x;
-      z[2 * k + 1] += f.y;
-    }
-  if (!row) return;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) o[k] = pack2<T>(z[2 * k], z[2 * k + 1]);
-  store32(static_cast<T*>(e.out.data) + m * e.out.ld + n, o, e.wide);
+  if (e.residual.data) add16<T>(*piece(ybuf, lane, 2 * half), *piece(ybuf, lane, 2 * half + 1), z);
+  put16<T>(ybuf, lane, half, z);
 }
 
-// The same at any alignment and at the matrix's edges: turned through the
-// warp's own shared memory, a column of every second row a lane.
-template <typename T>
-__device__ __forceinline__ void epilogue_edge(const Epilogue& e, const float (&z)[kEpCols],
-                                              int64_t m0, int64_t n0, int64_t M, int64_t N,
-                                              float* turn) {
-  const int lane = threadIdx.x & 31, col = lane & (kEpCols - 1);
-  const int64_t n = n0 + col;
-  const float bias = e.bias && n < N ? to_f32(static_cast<const T*>(e.bias)[n]) : 0.0f;
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    __syncwarp();
-    if (lane / 16 == h)
+// At any alignment: the group has been put into `turn` in fp32 (turned), and a lane takes a
+// column, row by row.
+__device__ __forceinline__ float4* turned(float* turn, int row, int c) {  // piece c of 8 of a row
+  return reinterpret_cast<float4*>(turn + row * 32 + ((c ^ (row & 7)) << 2));
+}
+__device__ __forceinline__ void put_turned(float* turn, int half, const float (&z)[16]) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-      for (int k = 0; k < kEpCols; ++k) turn[lane % 16 * (kEpCols + 1) + k] = z[k];
-    __syncwarp();
-    if (n >= N) continue;
-    const int64_t m = m0 + 16 * h;
-    const int rows = M - m < 16 ? (int)(M - m) : 16;
-    by_act(e.act, [&](auto act) {
+  for (int q = 0; q < 4; ++q)
+    *turned(turn, lane, 4 * half + q) = make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
+}
+template <typename T>
+__device__ __forceinline__ void finish_turned(const Epilogue& e, const float* turn, int64_t m0,
+                                              int64_t n0, int64_t M, int64_t N) {
+  const int lane = threadIdx.x & 31;
+  const int64_t n = n0 + lane;
+  if (n >= N) return;
+  const int rows = M - m0 < 32 ? (int)(M - m0) : 32;
+  const float bias = e.bias ? to_f32(static_cast<const T*>(e.bias)[n]) : 0.0f;
+  by_act(e.act, [&](auto act) {
 #pragma unroll 4
-      for (int r = lane / kEpCols; r < rows; r += 32 / kEpCols) {
-        const float v = turn[r * (kEpCols + 1) + col], x = e.bias ? v + bias : v;
-        if (e.z.data) static_cast<T*>(e.z.data)[(m + r) * e.z.ld + n] = from_f32<T>(x);
-        float y = act_of<decltype(act)::value>(x);
-        if (e.residual.data)
-          y += to_f32(static_cast<const T*>(e.residual.data)[(m + r) * e.residual.ld + n]);
-        static_cast<T*>(e.out.data)[(m + r) * e.out.ld + n] = from_f32<T>(y);
-      }
-    });
-  }
+    for (int r = 0; r < rows; ++r) {
+      const float v = turn[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)];
+      const float x = e.bias ? v + bias : v;
+      if (e.z.data) static_cast<T*>(e.z.data)[(m0 + r) * e.z.ld + n] = from_f32<T>(x);
+      float y = act_of<decltype(act)::value>(x);
+      if (e.residual.data)
+        y += to_f32(static_cast<const T*>(e.residual.data)[(m0 + r) * e.residual.ld + n]);
+      static_cast<T*>(e.out.data)[(m0 + r) * e.out.ld + n] = from_f32<T>(y);
+    }
+  });
 }
 
-// m0, n0: the warp's first row and column.
-template <typename T>
-__device__ __forceinline__ void epilogue(const Epilogue& e, float (&z)[kEpCols], int64_t m0,
-                                         int64_t n0, int64_t M, int64_t N, float* turn) {
-  if (n0 >= N || m0 >= M) return;
-  const int64_t m = m0 + (threadIdx.x & 31);
-  if (e.wide && n0 + kEpCols <= N)
-    epilogue_wide<T>(e, z, m, n0, m < M);
-  else
-    epilogue_edge<T>(e, z, m0, n0, M, N, turn);
+// Whether the group of columns from n on is stored by TMA, which writes whole pieces of 16
+// bytes: the last ones may have to end inside one.
+__device__ __forceinline__ bool tiled_at(const GemmArgs& a, int64_t n) {
+  return a.ep.tiled && (n + kGroup <= a.N || a.N % 8 == 0);
+}
+
+// What a warp of the epilogue keeps: two buffers of 32 x 32, and a barrier for each, on which
+// the residual's bytes are counted.
+struct Out {
+  uint8_t* buf;
+  uint64_t* bar;
+  uint32_t par;  // bit b: of buffer b's next phase
+
+  // Buffer of a group's y; z, if there is one, has the other.
+  __device__ __forceinline__ int of(const Epilogue& e, int g) const { return e.z.data ? 1 : g & 1; }
+  // By lane 0: both buffers are free.
+  __device__ __forceinline__ void load(const GemmArgs& a, int b, int64_t m0, int64_t n0) {
+    mbar_arrive_expect_tx(&bar[b], kBuf);
+    tma_load2(buf + b * kBuf, &a.residual, (int)n0, (int)m0, &bar[b]);
+  }
+  // Before a unit's (parts of) GROUPS groups from (m0, n0) on: the buffers' last stores have
+  // been read, and the residual is on its way.
+  template <int GROUPS>
+  __device__ __forceinline__ void begin(const GemmArgs& a, int64_t m0, int64_t n0) {
+    if ((threadIdx.x & 31) == 0) {
+      store_wait_read<0>();
+      if (a.ep.residual.data && m0 < a.M)
+        for (int g = 0; g < (a.ep.z.data ? 1 : GROUPS); ++g)
+          if (n0 + g * kGroup < a.N && tiled_at(a, n0 + g * kGroup))
+            load(a, of(a.ep, g), m0, n0 + g * kGroup);
+    }
+    __syncwarp();
+  }
+  // Group g, whose sums come by get(half, z); whole warps, inside the matrix.
+  template <typename T, typename F>
+  __device__ __forceinline__ bool group(const GemmArgs& a, int g, int64_t m0, int64_t n0, F get) {
+    const Epilogue& e = a.ep;
+    const int lane = threadIdx.x & 31, b = of(e, g);
+    uint8_t *ybuf = buf + b * kBuf, *zbuf = buf;
+    if (e.z.data && g > 0) {  // one pair of buffers for all groups
+      if (lane == 0) {
+        store_wait_read<0>();
+        if (e.residual.data) load(a, b, m0, n0);
+      }
+      __syncwarp();
+    }
+    if (e.residual.data) {
+      const bool ok = warp_wait(&bar[b], par >> b & 1, &g_layer_error);
+      par ^= 1u << b;
+      if (!ok) return false;
+    }
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      float z[16];
+      get(half, z);
+      finish16<T>(e, z, n0 + 16 * half, a.N, half, zbuf, ybuf);
+    }
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      if (e.z.data) tma_store2(&a.z, (int)n0, (int)m0, zbuf);
+      tma_store2(&a.out, (int)n0, (int)m0, ybuf);
+      store_commit();
+    }
+    return true;
+  }
+};
+
+// Sums of 32 rows and 16 columns in the workspace: four columns of a lane side by side, the
+// lanes' behind one another.
+__device__ __forceinline__ float4* part_at(float* partial, int64_t slot, int rows, int cols, int row0,
+                                           int c) {
+  return reinterpret_cast<float4*>(partial + slot * rows * cols + (int64_t)row0 * cols + c * 32) +
+         (threadIdx.x & 31);
 }
 
 struct GemmBars {
-  uint64_t full[8], empty[8], sum_full[2], sum_empty[2], drain;
+  uint64_t full[8], empty[8], sum_full[2], sum_empty[2], drain, residual[kEpWarps][2];
   uint32_t tmem;
 };
 
@@ -245,6 +298,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       mbar_init(&bar.sum_empty[i], kEpWarps * CG);
     }
     mbar_init(&bar.drain, 1);
+    for (int i = 0; i < 2 * kEpWarps; ++i) mbar_init(&bar.residual[0][0] + i, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -386,53 +440,79 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
     // of the columns each.
     constexpr int kCols = S::kCols / (kEpWarps / 4);
     const int w = warp - 2, lanes0 = (warp & 3) * 32, col0 = (w >> 2) * kCols;
-    float* turn = reinterpret_cast<float*>(smem + S::kArea) + w * kTurn;
+    Out out{smem + S::kArea + w * 2 * kBuf, bar.residual[w], 0};
+    float* turn = reinterpret_cast<float*>(out.buf);
     const uint32_t lanes = (uint32_t)lanes0 << 16;
     const uint32_t empty = CG == 2 ? cluster_addr(smem_u32(&bar.sum_empty[0]), 0) : 0;
     Units u(a, worker);
     bool ok = true;
     int buf = 0, par = 0;
     while (ok && u.next(a)) {
-      ok = warp_wait(&bar.sum_full[buf], par, &g_layer_error);
-      if (!ok) break;
-      tc_fence_after();
       int tm, tn;
       tile_at(u.tile, a.tiles_m, a.tiles_n, &tm, &tn);
       const int row0 = (int)rank * 128 + lanes0;  // in the tile
-      const int64_t m0 = (int64_t)tm * S::kRows + row0;
-#pragma unroll 1
-      for (int c = col0; c < col0 + kCols; c += kEpCols) {
-        uint32_t r[kEpCols];
-        __syncwarp();  // the last columns' lanes may have parted at an edge
-        tmem_ld16(r, tmem + lanes + buf * S::kCols + c);
+      const int64_t m0 = (int64_t)tm * S::kRows + row0, n0 = (int64_t)tn * S::kCols + col0;
+      if (a.ep.tiled && !u.part) out.begin<kCols / kGroup>(a, m0, n0);
+      ok = warp_wait(&bar.sum_full[buf], par, &g_layer_error);
+      if (!ok) break;
+      tc_fence_after();
+      int taken = 0;  // columns
+      auto get = [&](int, float (&z)[16]) {
+        uint32_t r[16];
+        __syncwarp();  // one lane may come from a copy of its own
+        tmem_ld16(r, tmem + lanes + buf * S::kCols + col0 + taken);
         tmem_wait_ld(r);
-        if (c + kEpCols == col0 + kCols) {  // the last: the next sum may come
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (CG == 2)
-              cluster_arrive(empty + 8 * buf);
-            else
-              mbar_arrive(&bar.sum_empty[buf]);
-          }
-        }
-        if (u.part) {
-          float* p = a.partial + (((int64_t)worker * 2 + u.slot) * S::kRows + row0 + lane) * S::kCols + c;
-          store32(p, r);
-          store32(p + 8, r + 8);
-        } else {
-          float z[kEpCols];
+        taken += 16;
 #pragma unroll
-          for (int k = 0; k < kEpCols; ++k) z[k] = __uint_as_float(r[k]);
-          const int64_t n0 = (int64_t)tn * S::kCols + c;
-          if (a.ep.type == OB_TYPE_BF16)
-            epilogue<__nv_bfloat16>(a.ep, z, m0, n0, a.M, a.N, turn);
+        for (int k = 0; k < 16; ++k) z[k] = __uint_as_float(r[k]);
+        if (taken < kCols) return;
+        tc_fence_before();  // the last: the next sum may come
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2)
+            cluster_arrive(empty + 8 * buf);
           else
-            epilogue<__half>(a.ep, z, m0, n0, a.M, a.N, turn);
+            mbar_arrive(&bar.sum_empty[buf]);
+        }
+      };
+#pragma unroll 1
+      for (int g = 0; g < kCols / kGroup; ++g) {
+        const int64_t n = n0 + g * kGroup;
+        const bool inside = m0 < a.M && n < a.N;
+        if (u.part || !inside || !tiled_at(a, n)) {
+          if (lane == 0) store_wait_read<0>();
+          __syncwarp();  // the groups before have been read
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            float z[16];
+            get(half, z);
+            if (u.part) {
+              float4* p = part_at(a.partial, (int64_t)worker * 2 + u.slot, S::kRows, S::kCols, row0,
+                                  col0 + g * kGroup + 16 * half);
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                p[32 * q] = make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
+            } else if (inside) {
+              put_turned(turn, half, z);
+            }
+          }
+          if (u.part || !inside) continue;
+          __syncwarp();
+          if (a.ep.type == OB_TYPE_BF16)
+            finish_turned<__nv_bfloat16>(a.ep, turn, m0, n, a.M, a.N);
+          else
+            finish_turned<__half>(a.ep, turn, m0, n, a.M, a.N);
+        } else if (a.ep.type == OB_TYPE_BF16) {
+          ok = out.group<__nv_bfloat16>(a, g, m0, n, get) && ok;
+        } else {
+          ok = out.group<__half>(a, g, m0, n, get) && ok;
         }
       }
+      __syncwarp();
       if (++buf == 2) buf = 0, par ^= 1;
     }
+    if (lane == 0) store_wait();
+    __syncwarp();
     tc_fence_before();
   }
   if (CG == 2)
@@ -448,16 +528,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
   }
 }
 
-// The cut tiles: a warp 32 rows of 16 columns, its parts in their order.
+// The cut tiles: a warp 32 rows of 32 columns, its parts in their order.
 template <int CG>
 __global__ void __launch_bounds__(256) k_gemm_parts(const __grid_constant__ GemmArgs a) {
   using S = Shape<CG>;
-  __shared__ float turn[8][kTurn];
-  grid_wait();
+  __shared__ __align__(1024) uint8_t bufs[8][2 * kBuf];
+  __shared__ uint64_t bars[8][2];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kAcross = S::kCols / kEpCols, kPer = (S::kRows / 32) * kAcross;  // warps a tile
+  if (lane == 0) {
+    mbar_init(&bars[w][0], 1);
+    mbar_init(&bars[w][1], 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  grid_wait();
+  constexpr int kAcross = S::kCols / kGroup, kPer = (S::kRows / 32) * kAcross;  // warps a tile
   const int unit = blockIdx.x * 8 + w, t = unit / kPer, in = unit % kPer;
-  const int row0 = in / kAcross * 32, c = in % kAcross * kEpCols;
+  const int row0 = in / kAcross * 32, c = in % kAcross * kGroup;
   int tm, tn;
   tile_at(a.whole + t, a.tiles_m, a.tiles_n, &tm, &tn);
   const int64_t m0 = (int64_t)tm * S::kRows + row0, n0 = (int64_t)tn * S::kCols + c;
@@ -471,32 +558,51 @@ __global__ void __launch_bounds__(256) k_gemm_parts(const __grid_constant__ Gemm
     while (share(total, p, a.workers) > step) --p;
     return p;
   };
-  float z[kEpCols];
-#pragma unroll
-  for (int k = 0; k < kEpCols; ++k) z[k] = 0.0f;
   int p0 = 0, p1 = -1;
   if (total > 0) {  // else the sums are empty
     p0 = owner(first);
     p1 = owner(last);
     if (p0 == p1) return;  // one worker had it whole
   }
-  for (int p = p0; p <= p1; ++p) {
-    if (share(total, p, a.workers) == share(total, p + 1, a.workers)) continue;  // no step at all
-    const int slot = share(total, p, a.workers) > first ? 0 : 1;
-    const float* q =
-        a.partial + (((int64_t)p * 2 + slot) * S::kRows + row0 + lane) * S::kCols + c;
+  Out out{bufs[w], bars[w], 0};
+  auto get = [&](int half, float (&z)[16]) {
 #pragma unroll
-    for (int k = 0; k < kEpCols / 8; ++k) {
-      uint32_t v[8];
-      load32(q + 8 * k, v);
+    for (int k = 0; k < 16; ++k) z[k] = 0.0f;
+    for (int p = p0; p <= p1; ++p) {
+      if (share(total, p, a.workers) == share(total, p + 1, a.workers)) continue;  // no step at all
+      const int slot = share(total, p, a.workers) > first ? 0 : 1;
+      const float4* q = part_at(a.partial, (int64_t)p * 2 + slot, S::kRows, S::kCols, row0, c + 16 * half);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) z[8 * k + x] += __uint_as_float(v[x]);
+      for (int k = 0; k < 4; ++k) {
+        const float4 v = q[32 * k];
+        z[4 * k] += v.x;
+        z[4 * k + 1] += v.y;
+        z[4 * k + 2] += v.z;
+        z[4 * k + 3] += v.w;
+      }
     }
+  };
+  if (tiled_at(a, n0)) {
+    out.begin<1>(a, m0, n0);
+    if (a.ep.type == OB_TYPE_BF16)
+      out.group<__nv_bfloat16>(a, 0, m0, n0, get);
+    else
+      out.group<__half>(a, 0, m0, n0, get);
+    if (lane == 0) store_wait();
+    return;
   }
+  float* turn = reinterpret_cast<float*>(out.buf);
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+    float z[16];
+    get(half, z);
+    put_turned(turn, half, z);
+  }
+  __syncwarp();
   if (a.ep.type == OB_TYPE_BF16)
-    epilogue<__nv_bfloat16>(a.ep, z, m0, n0, a.M, a.N, turn[w]);
+    finish_turned<__nv_bfloat16>(a.ep, turn, m0, n0, a.M, a.N);
   else
-    epilogue<__half>(a.ep, z, m0, n0, a.M, a.N, turn[w]);
+    finish_turned<__half>(a.ep, turn, m0, n0, a.M, a.N);
 }
 
 constexpr int kSms = 152;
@@ -537,11 +643,24 @@ cudaError_t run(const Gemm& g, const Plan& p, cudaStream_t s) {
   using S = Shape<CG>;
   GemmArgs a{};
   cudaError_t e = cudaSuccess;
-  if (p.steps) e = g.a_mn ? matrix_tensor_map(&a.a, g.a, g.ep.type, g.K, g.M, BK)
-                         : matrix_tensor_map(&a.a, g.a, g.ep.type, g.M, g.K, 128);
-  if (p.steps && e == cudaSuccess)
-    e = g.b_mn ? matrix_tensor_map(&a.b, g.b, g.ep.type, g.K, g.N, BK)
-               : matrix_tensor_map(&a.b, g.b, g.ep.type, g.N, g.K, 128);
+  auto map = [&](CUtensorMap* to, const Mat& m, int64_t rows, int64_t cols, int bc, int br) {
+    if (e == cudaSuccess) e = matrix_tensor_map(to, m, g.ep.type, rows, cols, bc, br);
+  };
+  if (p.steps) {
+    if (g.a_mn)
+      map(&a.a, g.a, g.K, g.M, 64, BK);
+    else
+      map(&a.a, g.a, g.M, g.K, 64, 128);
+    if (g.b_mn)
+      map(&a.b, g.b, g.K, g.N, 64, BK);
+    else
+      map(&a.b, g.b, g.N, g.K, 64, 128);
+  }
+  if (g.ep.tiled) {
+    map(&a.out, g.ep.out, g.M, g.N, kGroup, 32);
+    if (g.ep.z.data) map(&a.z, g.ep.z, g.M, g.N, kGroup, 32);
+    if (g.ep.residual.data) map(&a.residual, g.ep.residual, g.M, g.N, kGroup, 32);
+  }
   if (e != cudaSuccess) return e;
   a.a_mn = g.a_mn;
   a.b_mn = g.b_mn;
@@ -556,7 +675,7 @@ cudaError_t run(const Gemm& g, const Plan& p, cudaStream_t s) {
   a.ep = g.ep;
   a.partial = g.partial;
   const int rest = p.tiles_m * p.tiles_n - p.whole;
-  const dim3 parts(rest * ((S::kRows / 32) * (S::kCols / kEpCols) / 8));
+  const dim3 parts(rest * ((S::kRows / 32) * (S::kCols / kGroup) / 8));
   if (!p.steps) return launch_behind(k_gemm_parts<CG>, parts, dim3(256), 0, s, a);
   static PerDeviceOnce once;
   e = once.run([] {

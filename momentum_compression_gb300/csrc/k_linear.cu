@@ -153,17 +153,10 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 bool on(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool by_tma(const Mat& m) { return on(m.data, 16) && m.ld % 8 == 0; }
 
-// How far the epilogue's rows are aligned: 2, 1 or 0.
-int wide_of(const Epilogue& e) {
-  int w = e.bias && !on(e.bias, 16) ? 0 : 2;
-  for (const Mat* m : {&e.out, &e.z, &e.residual}) {
-    if (!m->data) continue;
-    if (!by_tma(*m))
-      w = 0;
-    else if (w == 2 && !(on(m->data, 32) && m->ld % 16 == 0))
-      w = 1;
-  }
-  return w;
+int tiled(const Epilogue& e) {
+  bool all = !e.bias || on(e.bias, 16);
+  for (const Mat* m : {&e.out, &e.z, &e.residual}) all = all && (!m->data || by_tma(*m));
+  return all;
 }
 
 int power_of_two(int64_t n, int most) {
@@ -246,7 +239,7 @@ cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t s) {
   g.ep.out = a.y;
   g.ep.act = a.act;
   g.ep.type = a.type;
-  g.ep.wide = wide_of(g.ep);
+  g.ep.tiled = tiled(g.ep);
   g.partial = static_cast<float*>(area.take(0));
   return launch_gemm(g, s);
 }
@@ -298,7 +291,7 @@ cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t s) {
     g.N = wc;
     g.K = M;
     g.ep.out = a.dw;
-    g.ep.wide = wide_of(g.ep);
+    g.ep.tiled = tiled(g.ep);
     e = launch_gemm(g, s);
   }
   if (e == cudaSuccess && a.dx.data) {  // dx[m][k] = sum over n of dz(m, n) w(n, k)
@@ -310,7 +303,7 @@ cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t s) {
     g.N = K;
     g.K = N;
     g.ep.out = a.dx;
-    g.ep.wide = wide_of(g.ep);
+    g.ep.tiled = tiled(g.ep);
     e = launch_gemm(g, s);
   }
   return e;

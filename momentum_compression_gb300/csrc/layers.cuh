@@ -46,10 +46,10 @@ struct Mat {
   int64_t ld;
 };
 
-// A map of `rows` rows of `cols` elements whose boxes are box_rows rows of 64
-// elements in 128-byte swizzle; what is outside reads as zero.
+// A map of `rows` rows of `cols` elements whose boxes are box_rows rows of 64 or 32
+// elements, swizzled as far as they are wide; what is outside reads as zero.
 cudaError_t matrix_tensor_map(CUtensorMap* map, const Mat& m, int type, int64_t rows, int64_t cols,
-                              int box_rows);
+                              int box_cols, int box_rows);
 
 struct LinearArgs {
   int type, act, w_kn, unaligned;
@@ -77,7 +77,7 @@ struct Epilogue {
   const void* bias;          // [N], or null
   Mat residual, z, out;      // residual and z: data or null
   int act, type;
-  int wide;                  // rows, and bias, are aligned to 2: 32, 1: 16 bytes, 0: less
+  int tiled;                 // every matrix, and bias, lies on 16 bytes
 };
 
 struct Gemm {

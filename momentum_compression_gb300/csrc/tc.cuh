@@ -193,6 +193,24 @@ __device__ __forceinline__ void tma_load2(void* dst, const CUtensorMap* map, int
       "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
 }
+// Shared memory to the box at (x, y); what is outside the matrix is not written.  The copies
+// of a thread are counted in groups; store_wait_read<N>: all but the N newest groups have
+// read their shared memory.
+__device__ __forceinline__ void tma_store2(const CUtensorMap* map, int x, int y, const void* src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+               "r"(x), "r"(y), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ void store_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void store_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
 // A cluster's blocks wait for one another here, and see what was written
 // before; every thread of every block takes part.
 __device__ __forceinline__ void cluster_sync() {
@@ -271,9 +289,10 @@ __device__ __forceinline__ void pair_commit(uint32_t leader, uint64_t* bar) {
       "r"(leader)
       : "memory");
 }
-// On a barrier at a cluster address.
+// On a barrier at a cluster address; orders nothing but what tensor-memory fences order (a
+// release would wait for every store that is under way).
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
