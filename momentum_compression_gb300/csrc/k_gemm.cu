@@ -181,20 +181,29 @@ __device__ __forceinline__ void finish_turned(const Epilogue& e, const float* tu
   const int lane = threadIdx.x & 31;
   const int64_t n = n0 + lane;
   if (n >= N) return;
-  const int rows = M - m0 < 32 ? (int)(M - m0) : 32;
   const float bias = e.bias ? to_f32(static_cast<const T*>(e.bias)[n]) : 0.0f;
-  by_act(e.act, [&](auto act) {
-#pragma unroll 4
-    for (int r = 0; r < rows; ++r) {
-      const float v = turn[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)];
-      const float x = e.bias ? v + bias : v;
-      if (e.z.data) static_cast<T*>(e.z.data)[(m0 + r) * e.z.ld + n] = from_f32<T>(x);
-      float y = act_of<decltype(act)::value>(x);
-      if (e.residual.data)
-        y += to_f32(static_cast<const T*>(e.residual.data)[(m0 + r) * e.residual.ld + n]);
-      static_cast<T*>(e.out.data)[(m0 + r) * e.out.ld + n] = from_f32<T>(y);
-    }
-  });
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32 && m0 + r0 < M; r0 += 16) {
+    T residual[16];  // sixteen rows' loads at once
+    if (e.residual.data)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (m0 + r0 + r < M)
+          residual[r] = static_cast<const T*>(e.residual.data)[(m0 + r0 + r) * e.residual.ld + n];
+    by_act(e.act, [&](auto act) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int row = r0 + r;
+        if (m0 + row >= M) break;
+        const float v = turn[row * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)];
+        const float x = e.bias ? v + bias : v;
+        if (e.z.data) static_cast<T*>(e.z.data)[(m0 + row) * e.z.ld + n] = from_f32<T>(x);
+        float y = act_of<decltype(act)::value>(x);
+        if (e.residual.data) y += to_f32(residual[r]);
+        static_cast<T*>(e.out.data)[(m0 + row) * e.out.ld + n] = from_f32<T>(y);
+      }
+    });
+  }
 }
 
 // Whether the group of columns from n on is stored by TMA, which writes whole pieces of 16
@@ -705,13 +714,16 @@ cudaError_t run(const Gemm& g, const Plan& p, cudaStream_t s) {
 
 size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K) {
   if (M == 0 || N == 0) return 0;
+  const size_t few = M <= kGemvRows ? gemv_partial_bytes(M, N, K) : 0;
   const Plan p = plan_of(M, N, K);
-  if (p.whole == p.tiles_m * p.tiles_n || !p.steps) return 0;
-  return (size_t)p.workers * 2 * (128 * p.cg) * (128 * p.cg) * sizeof(float);
+  if (p.whole == p.tiles_m * p.tiles_n || !p.steps) return few;
+  const size_t parts = (size_t)p.workers * 2 * (128 * p.cg) * (128 * p.cg) * sizeof(float);
+  return parts > few ? parts : few;
 }
 
 cudaError_t launch_gemm(const Gemm& g, cudaStream_t s) {
   if (g.M == 0 || g.N == 0) return cudaSuccess;
+  if (g.M <= kGemvRows && !g.a_mn) return launch_gemv(g, s);
   const Plan p = plan_of(g.M, g.N, g.K);
   return p.cg == 2 ? run<2>(g, p, s) : run<1>(g, p, s);
 }

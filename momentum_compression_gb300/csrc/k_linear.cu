@@ -19,6 +19,7 @@ namespace ob {
 namespace {
 
 constexpr int kDzThreads = 128;
+constexpr int kDzBlocks = 5;  // of an SM at a time
 
 struct DzArgs {
   Mat dy, z, dz;      // dz: data or null
@@ -61,7 +62,7 @@ struct Cell {
 
 // V columns a thread (8: 16-byte loads).
 template <typename T, int V>
-__global__ void __launch_bounds__(kDzThreads) k_dz(const __grid_constant__ DzArgs a) {
+__global__ void __launch_bounds__(kDzThreads, kDzBlocks) k_dz(const __grid_constant__ DzArgs a) {
   __shared__ float sums[kDzThreads * V];
   grid_wait();
   const int x = threadIdx.x & (a.tx - 1), y = threadIdx.x / a.tx, ty = kDzThreads / a.tx;
@@ -139,13 +140,35 @@ __global__ void __launch_bounds__(256) k_dbias(const float* partial, int parts, 
   out[n] = from_f32<T>(t);
 }
 
-__global__ void __launch_bounds__(256) k_realign(const uint16_t* from, int64_t ld, uint16_t* to,
-                                                 int64_t to_ld, int64_t rows, int64_t cols) {
+// Copies of matrices that lie anywhere, rows padded to whole 16-byte words: a word a thread,
+// from the two words that hold its bytes.
+struct Realign {
+  const char* from;
+  char* to;
+  int64_t rows, cols, ld, words;  // words of a padded row
+  int64_t first;                  // its first thread
+};
+struct Realigns {
+  Realign m[2];
+  int count;
+  int64_t threads;
+};
+__global__ void __launch_bounds__(256) k_realign(const __grid_constant__ Realigns a) {
   grid_wait();
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c < cols)
-#pragma unroll 4
-    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) to[r * to_ld + c] = from[r * ld + c];
+  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < a.threads; t += (int64_t)gridDim.x * 256) {
+    const Realign& m = a.m[a.count > 1 && t >= a.m[1].first ? 1 : 0];
+    const int64_t i = t - m.first, row = i / m.words, w = i - row * m.words;
+    const char* begin = m.from + row * m.ld * 2;
+    const char* p = begin + 16 * w;
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+    const uint4* q = reinterpret_cast<const uint4*>(p - off);
+    uint4 x = q[0];
+    if (off) {
+      const bool more = reinterpret_cast<const char*>(q + 1) < begin + 2 * m.cols;
+      x = shifted<__half>(x, more ? q[1] : make_uint4(0, 0, 0, 0), off);
+    }
+    *reinterpret_cast<uint4*>(m.to + (row * m.words + w) * 16) = x;
+  }
 }
 
 int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
@@ -166,11 +189,11 @@ int power_of_two(int64_t n, int most) {
 }
 
 // Blocks along the rows of dz, by sizes alone (the workspace goes by it): eight
-// rows a thread at least, and 8 blocks an SM.
+// rows a thread at least, and all that run at a time.
 int dz_parts(int64_t M, int64_t N) {
   const int tx = power_of_two((N + 7) / 8, kDzThreads);
   const int64_t columns = (N + 8 * tx - 1) / (8 * tx), rows = 8 * (kDzThreads / tx);
-  int64_t most = 8 * 152 / columns;
+  int64_t most = kDzBlocks * 152 / columns;
   if (most < 1) most = 1;
   const int64_t parts = (M + rows - 1) / rows;
   return (int)(parts < 1 ? 1 : parts < most ? parts : most);
@@ -188,15 +211,20 @@ struct Area {  // the workspace, handed out in order
 
 size_t mat_bytes(int64_t rows, int64_t cols) { return up256((size_t)(rows * padded(cols)) * 2); }
 
-cudaError_t realign(Mat* m, int64_t rows, int64_t cols, Area* area, cudaStream_t s) {
-  if (rows == 0 || cols == 0 || by_tma(*m)) return cudaSuccess;
-  uint16_t* to = static_cast<uint16_t*>(area->take(mat_bytes(rows, cols)));
-  const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)(rows < 2048 ? rows : 2048));
-  const cudaError_t e = launch_behind(k_realign, grid, dim3(256), 0, s,
-                                      static_cast<const uint16_t*>(m->data), m->ld, to,
-                                      padded(cols), rows, cols);
+// Has m copied where its rows do not lie on 16 bytes.
+void realign(Realigns* all, Mat* m, int64_t rows, int64_t cols, Area* area) {
+  if (rows == 0 || cols == 0 || by_tma(*m)) return;
+  void* to = area->take(mat_bytes(rows, cols));
+  all->m[all->count++] = Realign{static_cast<const char*>(m->data), static_cast<char*>(to), rows, cols,
+                                 m->ld, padded(cols) / 8, all->threads};
+  all->threads += rows * (padded(cols) / 8);
   *m = Mat{to, padded(cols)};
-  return e;
+}
+cudaError_t launch(const Realigns& all, cudaStream_t s) {
+  if (!all.count) return cudaSuccess;
+  const int64_t blocks = (all.threads + 255) / 256;
+  return launch_behind(k_realign, dim3((unsigned)(blocks < 152 * 16 ? blocks : 152 * 16)), dim3(256), 0,
+                       s, all);
 }
 
 template <typename T>
@@ -226,8 +254,10 @@ cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t s) {
   Gemm g{};
   g.a = a.x;
   g.b = a.w;
-  cudaError_t e = realign(&g.a, a.M, a.K, &area, s);
-  if (e == cudaSuccess) e = realign(&g.b, a.w_kn ? a.K : a.N, a.w_kn ? a.N : a.K, &area, s);
+  Realigns all{};
+  realign(&all, &g.a, a.M, a.K, &area);
+  realign(&all, &g.b, a.w_kn ? a.K : a.N, a.w_kn ? a.N : a.K, &area);
+  const cudaError_t e = launch(all, s);
   if (e != cudaSuccess) return e;
   g.b_mn = a.w_kn;
   g.M = a.M;
@@ -276,8 +306,10 @@ cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t s) {
     }
   }
   Mat x = a.x, w = a.w;
-  if (e == cudaSuccess && a.dw.data) e = realign(&x, M, K, &area, s);
-  if (e == cudaSuccess && a.dx.data) e = realign(&w, wr, wc, &area, s);
+  Realigns all{};
+  if (a.dw.data) realign(&all, &x, M, K, &area);
+  if (a.dx.data) realign(&all, &w, wr, wc, &area);
+  if (e == cudaSuccess) e = launch(all, s);
   if (e != cudaSuccess) return e;
   Gemm g{};
   g.ep.type = a.type;
