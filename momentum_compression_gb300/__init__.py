@@ -21,8 +21,10 @@ Two layers:
     in the order of the method; `AdamW`, which owns the moments of a list of
     tensors.
 """
+import array
 import ctypes as ct
 import functools
+import operator
 import os
 import struct
 
@@ -924,11 +926,34 @@ def ob_attn_workspace_bytes(q, k, relpos=None, table=None):
 # Layer norm and the dense layer
 # ---------------------------------------------------------------------------
 
-def _like(name, t, shape, dtype, at, other="x"):
-    """Refuses t unless it has `other`'s shape, type and device."""
-    if t.shape != shape or t.dtype != dtype or t.get_device() != at:
-        _refuse(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device} must be {tuple(shape)} {dtype} "
-                f"on CUDA device {at}, as {other}")
+def _row_arrays(x, others):
+    """(device, type code, rows, cols, [address, elements between rows, ...]) of x and of the
+    other (name, tensor or None) pairs, which have its shape, type and device."""
+    at, shape, dtype = x.get_device(), x.shape, x.dtype
+    if at < 0 or not shape:
+        _refuse("x must be a tensor of rows on a CUDA device")
+    type_ = (_type_codes or _types()).get(dtype)
+    if type_ is None:
+        _type(x, "x")
+    whole = x.is_contiguous()
+    for name, t in others:
+        if t is not None:
+            if t.shape != shape or t.dtype != dtype or t.get_device() != at:
+                _refuse(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device} must be {tuple(shape)} "
+                        f"{dtype} on CUDA device {at}, as x")
+            whole = whole and t.is_contiguous()
+    cols = shape[-1]
+    if whole:
+        rows = x.numel() // cols if cols else 0
+        out = [x.data_ptr(), cols]
+        for _, t in others:
+            out += (None, cols) if t is None else (t.data_ptr(), cols)
+    else:
+        rows, cols, ld = _rows(x, "x")
+        out = [x.data_ptr(), ld]
+        for name, t in others:
+            out += (None, cols) if t is None else (t.data_ptr(), _rows(t, name)[2])
+    return at, type_, rows, cols, out
 
 
 def _vectors(at, n, **vectors):
@@ -938,13 +963,14 @@ def _vectors(at, n, **vectors):
         if t is None:
             ptrs.append(None)
             continue
-        if t.shape != (n,) or (n > 1 and t.stride(0) != 1) or t.get_device() != at:
+        if t.numel() != n or t.dim() != 1 or t.get_device() != at or not t.is_contiguous():
             _refuse(f"{name} must be a contiguous vector of {n} elements on CUDA device {at}")
-        if dtype is not None and t.dtype != dtype:
+        if dtype is None:
+            dtype = t.dtype
+        elif t.dtype != dtype:
             _refuse(f"{name}: {t.dtype}, but {dtype} before it")
-        dtype = t.dtype
         ptrs.append(t.data_ptr())
-    return OB_TYPE_F32 if dtype is None else _types().get(dtype, -1), ptrs
+    return OB_TYPE_F32 if dtype is None else (_type_codes or _types()).get(dtype, -1), ptrs
 
 
 def _statistics(at, rows, **stats):
@@ -963,25 +989,14 @@ def ob_layernorm_fwd(x, y, weight=None, bias=None, eps=1e-5, residual=None, sum=
                      rstd=None, stream=None):
     """y = the layer norm of s = x + residual over the last dimension, times weight plus
     bias; sum gets s (rounded to the type), mean and rstd what the backward pass needs."""
-    at, shape, dtype = x.get_device(), x.shape, x.dtype
-    if at < 0 or len(shape) == 0:
-        _refuse("x must be a tensor of rows on a CUDA device")
-    type_ = _type(x, "x")
-    rows, cols, ldx = _rows(x, "x")
-    _like("y", y, shape, dtype, at)
-    ldy = _rows(y, "y")[2]
-    pr = ps = None
-    ldr = lds = cols
-    if residual is not None:
-        _like("residual", residual, shape, dtype, at)
-        pr, ldr = residual.data_ptr(), _rows(residual, "residual")[2]
-    if sum is not None:
-        _like("sum", sum, shape, dtype, at)
-        ps, lds = sum.data_ptr(), _rows(sum, "sum")[2]
+    at, type_, rows, cols, (px, ldx, py, ldy, pr, ldr, ps, lds) = _row_arrays(
+        x, (("y", y), ("residual", residual), ("sum", sum)))
     w_type, (pw, pb) = _vectors(at, cols, weight=weight, bias=bias)
-    pm, pd = _statistics(at, rows, mean=mean, rstd=rstd)
-    _launch(lib().ob_layernorm_fwd, at, stream, x.data_ptr(), ldx, pr, ldr, pw, pb, w_type,
-            y.data_ptr(), ldy, ps, lds, pm, pd, rows, cols, type_, eps)
+    pm = pd = None
+    if mean is not None or rstd is not None:
+        pm, pd = _statistics(at, rows, mean=mean, rstd=rstd)
+    _launch(lib().ob_layernorm_fwd, at, stream, px, ldx, pr, ldr, pw, pb, w_type, py, ldy, ps, lds,
+            pm, pd, rows, cols, type_, eps)
 
 
 @functools.lru_cache(1024)
@@ -996,29 +1011,16 @@ def ob_layernorm_bwd(dy, x, mean, rstd, dx=None, weight=None, dweight=None, dbia
                      workspace=None, stream=None):
     """dx, dweight and dbias from dy, with x the normalised s of the forward call; dsum is
     added to dx.  workspace: a uint8 tensor, or None for one of torch's allocator."""
-    at, shape, dtype = x.get_device(), x.shape, x.dtype
-    if at < 0 or len(shape) == 0:
-        _refuse("x must be a tensor of rows on a CUDA device")
-    type_ = _type(x, "x")
-    rows, cols, ldx = _rows(x, "x")
-    _like("dy", dy, shape, dtype, at)
-    lddy = _rows(dy, "dy")[2]
-    px = ps = None
-    lddx = ldds = cols
-    if dx is not None:
-        _like("dx", dx, shape, dtype, at)
-        px, lddx = dx.data_ptr(), _rows(dx, "dx")[2]
-    if dsum is not None:
-        _like("dsum", dsum, shape, dtype, at)
-        ps, ldds = dsum.data_ptr(), _rows(dsum, "dsum")[2]
+    at, type_, rows, cols, (p, ldx, pdy, lddy, px, lddx, ps, ldds) = _row_arrays(
+        x, (("dy", dy), ("dx", dx), ("dsum", dsum)))
     w_type, (pw, pdw, pdb) = _vectors(at, cols, weight=weight, dweight=dweight, dbias=dbias)
     pm, pd = _statistics(at, rows, mean=mean, rstd=rstd)
     if workspace is not None:
         _check_workspace(workspace, at)
     elif dweight is not None or dbias is not None:
         workspace = _scratch(ob_layernorm_workspace_bytes(rows, cols), x, stream)
-    _launch(lib().ob_layernorm_bwd, at, stream, dy.data_ptr(), lddy, x.data_ptr(), ldx, pm, pd, pw,
-            w_type, ps, ldds, px, lddx, pdw, pdb, rows, cols, type_, _ptr(workspace) or None,
+    _launch(lib().ob_layernorm_bwd, at, stream, pdy, lddy, p, ldx, pm, pd, pw, w_type, ps, ldds, px,
+            lddx, pdw, pdb, rows, cols, type_, _ptr(workspace) or None,
             0 if workspace is None else workspace.numel() * workspace.element_size())
 
 
@@ -1026,8 +1028,7 @@ _ACTIVATIONS = {"none": OB_ACT_NONE, "relu": OB_ACT_RELU, "gelu": OB_ACT_GELU,
                 "gelu_tanh": OB_ACT_GELU_TANH}
 _LINEAR = struct.Struct("4i3q")
 assert _LINEAR.size == ct.sizeof(ob_linear)
-_MATRIX = struct.Struct("Pq")
-assert _MATRIX.size == ct.sizeof(ob_matrix)
+assert ct.sizeof(ob_matrix) == 16
 
 
 def _weights(w, name):
@@ -1037,34 +1038,34 @@ def _weights(w, name):
     N, K = w.shape
     sn, sk = w.stride()
     if K <= 1 or sk == 1:
-        return N, K, False, sn if N > 1 else K
+        return N, K, 0, sn if N > 1 else K
     if N <= 1 or sn == 1:
-        return N, K, True, sk
+        return N, K, 1, sk
     _refuse(f"{name}: one of its dimensions must be contiguous")
 
 
-class _Matrices:
-    """The matrices of a call on device `at`, packed; `off` where one is off 16 bytes."""
-
-    def __init__(self, dtype, at):
-        self.dtype, self.at, self.off = dtype, at, False
-
-    def pack(self, name, t, rows, cols, ld):
-        if t.dtype != self.dtype or t.get_device() != self.at:
-            _refuse(f"{name}: {t.dtype} on {t.device} must be {self.dtype} on CUDA device {self.at}")
-        p = t.data_ptr()
-        if p % 16 or (rows > 1 and ld % 8):
-            self.off = True
-        return _MATRIX.pack(p, ld)
-
-    def rows(self, name, t, rows, cols):
-        """Packs t [..., cols] of `rows` rows; None stays None."""
+def _matrices(at, dtype, rows):
+    """([address, leading dimension, ...], whether one is off 16 bytes) of the (name, tensor or
+    None, rows, cols, leading dimension or None) in `rows`."""
+    out, off = [], 0
+    for name, t, r, c, ld in rows:
         if t is None:
-            return None
-        r, c, ld = _rows(t, name)
-        if r != rows or c != cols:
-            _refuse(f"{name}: {tuple(t.shape)} must be {rows} rows of {cols}")
-        return self.pack(name, t, rows, cols, ld)
+            out += (0, 0)
+            continue
+        if t.dtype != dtype or t.get_device() != at:
+            _refuse(f"{name}: {t.dtype} on {t.device} must be {dtype} on CUDA device {at}")
+        if ld is None:
+            strides = t.stride()
+            if len(strides) == 2 and t.shape == (r, c) and (strides[1] == 1 or c == 1):
+                ld = strides[0] if r > 1 else c
+            else:
+                r1, c1, ld = _rows(t, name)
+                if r1 != r or c1 != c:
+                    _refuse(f"{name}: {tuple(t.shape)} must be {r} rows of {c}")
+        p = t.data_ptr()
+        off |= p & 15 | (ld & 7 if r > 1 else 0)
+        out += (p, ld)
+    return out, int(off != 0)
 
 
 def _activation(name):
@@ -1082,13 +1083,22 @@ def ob_linear_workspace_bytes(type, act, w_kn, unaligned, M, N, K, backward):
     return b.value
 
 
-def _linear_call(fn, m, l, backward, like, workspace, stream, *args):
+_PAIRS = {n: ct.c_int64 * (2 * n) for n in (5, 6)}
+
+
+def _linear_call(fn, at, l, backward, like, workspace, stream, pairs, order):
+    """fn with the matrices of `pairs` (by their place, None: no matrix) and vectors in `order`."""
     if workspace is None:
         nbytes = ob_linear_workspace_bytes(*l, backward)
         workspace = _scratch(nbytes, like, stream) if nbytes else None
     else:
-        _check_workspace(workspace, m.at)
-    _launch(fn, m.at, stream, _LINEAR.pack(*l), *args, _ptr(workspace) or None,
+        _check_workspace(workspace, at)
+    mats = _PAIRS[len(pairs) // 2](*pairs)
+    base = ct.addressof(mats)
+    _launch(fn, at, stream, _LINEAR.pack(*l),
+            *[i[0] if i.__class__ is tuple else base + 16 * i if pairs[2 * i + 1] else None
+              for i in order],
+            _ptr(workspace) or None,
             0 if workspace is None else workspace.numel() * workspace.element_size())
 
 
@@ -1097,51 +1107,65 @@ def ob_linear_fwd(x, w, y, bias=None, residual=None, z=None, activation="none", 
     """y = act(x w^T + bias) + residual for x [..., K], w [N, K] (either dimension
     contiguous) and y [..., N] in bfloat16 or float16; z gets what act is of.
     activation: none, relu, gelu or gelu_tanh."""
-    at, type_ = x.get_device(), _type(x, "x")
-    if at < 0 or x.dim() == 0:
+    at, dtype, shape = x.get_device(), x.dtype, x.shape
+    if at < 0 or not shape:
         _refuse("x must be a tensor of rows on a CUDA device")
-    m = _Matrices(x.dtype, at)
-    M, K, ldx = _rows(x, "x")
-    N, wk, kn, ldw = _weights(w, "w")
-    if wk != K or y.shape != x.shape[:-1] + (N,):
-        _refuse(f"x {tuple(x.shape)}, w {tuple(w.shape)} and y {tuple(y.shape)} do not go together")
-    px, pw = m.pack("x", x, M, K, ldx), m.pack("w", w, *((K, N) if kn else (N, K)), ldw)
-    py, pr, pz = (m.rows(n, t, M, N) for n, t in (("y", y), ("residual", residual), ("z", z)))
-    bt, (pb,) = _vectors(at, N, bias=bias)
-    if bias is not None and bt != type_:
-        _refuse("bias must have the type of x")
-    l = (type_, _activation(activation), int(kn), int(m.off), M, N, K)
-    _linear_call(lib().ob_linear_fwd, m, l, 0, x, workspace, stream, px, pw, pb, pr, pz, py)
+    type_ = _type(x, "x")
+    N, K, kn, ldw = _weights(w, "w")
+    if shape[-1] != K or y.shape[-1:] != (N,) or y.shape[:-1] != shape[:-1]:
+        _refuse(f"x {tuple(shape)}, w {tuple(w.shape)} and y {tuple(y.shape)} do not go together")
+    M = x.numel() // K if K else _rows(x, "x")[0]
+    pairs, off = _matrices(at, dtype, (("x", x, M, K, None), ("w", w, *((K, N) if kn else (N, K)), ldw),
+                                       ("y", y, M, N, None), ("residual", residual, M, N, None),
+                                       ("z", z, M, N, None)))
+    pb = None
+    if bias is not None:
+        bt, (pb,) = _vectors(at, N, bias=bias)
+        if bt != type_:
+            _refuse("bias must have the type of x")
+    l = (type_, _activation(activation), kn, off, M, N, K)
+    if not M or not N:
+        return
+    if not K:
+        pairs[1] = pairs[3] = 1  # empty, but there
+    _linear_call(lib().ob_linear_fwd, at, l, 0, x, workspace, stream, pairs, (0, 1, (pb,), 3, 4, 2))
 
 
 def ob_linear_bwd(dy, x, w, dx=None, dw=None, dbias=None, z=None, activation="none",
                   workspace=None, stream=None):
     """dx, dw (laid out as w) and dbias from dy, with the forward call's x, w, z and
     activation; the residual's gradient is dy."""
-    at, type_ = dy.get_device(), _type(dy, "dy")
-    if at < 0 or dy.dim() == 0:
+    at, dtype, shape = dy.get_device(), dy.dtype, dy.shape
+    if at < 0 or not shape:
         _refuse("dy must be a tensor of rows on a CUDA device")
-    m = _Matrices(dy.dtype, at)
-    M, N, ldy = _rows(dy, "dy")
-    wn, K, kn, ldw = _weights(w, "w")
-    if wn != N or x.shape != dy.shape[:-1] + (K,):
-        _refuse(f"dy {tuple(dy.shape)}, x {tuple(x.shape)} and w {tuple(w.shape)} do not go together")
+    type_ = _type(dy, "dy")
+    N, K, kn, ldw = _weights(w, "w")
+    if shape[-1] != N or x.shape[-1:] != (K,) or x.shape[:-1] != shape[:-1]:
+        _refuse(f"dy {tuple(shape)}, x {tuple(x.shape)} and w {tuple(w.shape)} do not go together")
     act = _activation(activation)
     if act and z is None:
         _refuse(f"z is needed for activation {activation!r}")
+    M = dy.numel() // N if N else _rows(dy, "dy")[0]
     wr, wc = (K, N) if kn else (N, K)
-    pdy, pz = m.pack("dy", dy, M, N, ldy), m.rows("z", z if act else None, M, N)
-    px, pdx = m.rows("x", x, M, K), m.rows("dx", dx, M, K)
-    pw, pdw = m.pack("w", w, wr, wc, ldw), None
+    lddw = None
     if dw is not None:
         if dw.shape != w.shape or (wr > 1 and wc > 1 and dw.stride(1 - kn) != 1):
             _refuse(f"dw must be {tuple(w.shape)} with the contiguous dimension of w")
-        pdw = m.pack("dw", dw, wr, wc, dw.stride(int(kn)) if wr > 1 else wc)
-    bt, (pb,) = _vectors(at, N, dbias=dbias)
-    if dbias is not None and bt != type_:
-        _refuse("dbias must have the type of dy")
-    l = (type_, act, int(kn), int(m.off), M, N, K)
-    _linear_call(lib().ob_linear_bwd, m, l, 1, dy, workspace, stream, pdy, px, pw, pz, pdx, pdw, pb)
+        lddw = dw.stride(kn) if wr > 1 else wc
+    pairs, off = _matrices(at, dtype, (("dy", dy, M, N, None), ("x", x, M, K, None), ("w", w, wr, wc, ldw),
+                                       ("z", z if act else None, M, N, None),
+                                       ("dx", dx, M, K, None), ("dw", dw, wr, wc, lddw)))
+    pb = None
+    if dbias is not None:
+        bt, (pb,) = _vectors(at, N, dbias=dbias)
+        if bt != type_:
+            _refuse("dbias must have the type of dy")
+    l = (type_, act, kn, off, M, N, K)
+    for i, t in enumerate((dy, x, w, z if act else None, dx, dw)):
+        if t is not None and not pairs[2 * i + 1]:
+            pairs[2 * i + 1] = 1  # empty, but there
+    _linear_call(lib().ob_linear_bwd, at, l, 1, dy, workspace, stream, pairs,
+                 (0, 1, 2, 3, 4, 5, (pb,)))
 
 
 def ob_layer_device_error(stream=None):
@@ -1155,6 +1179,7 @@ def ob_layer_device_error(stream=None):
 # AdamW over many tensors
 # ---------------------------------------------------------------------------
 
+_dtype_of = operator.attrgetter("dtype")
 OB_ADAMW_BLOCK = 256  # elements of a tensor that share a unit, and the state's grain
 
 
@@ -1256,6 +1281,7 @@ class AdamW:
         b1, b2 = self.betas
         self.counter = torch.tensor([step, b1 ** step, b2 ** step, 0.0], dtype=torch.float64,
                                     device=self.device)
+        self._buffers = tuple(map(_ptr, (self.m, self.v, self.m_exp, self.v_exp, self.counter)))
 
     def _scalar(self, name, t):
         import torch
@@ -1276,15 +1302,16 @@ class AdamW:
         grads = [p.grad for p in self.params] if grads is None else grads
         if len(grads) != len(self.params):
             _refuse(f"{len(grads)} gradients for {len(self.params)} parameters")
-        some = grads
-        sizes = self._sizes
-        if any(g is None for g in grads):
+        T = torch.Tensor
+        some, sizes = grads, self._sizes
+        try:
+            pointers = list(map(T.data_ptr, grads))
+        except TypeError:  # some have none
             some = [g for g in grads if g is not None]
             sizes = [n for n, g in zip(self._sizes, grads) if g is not None]
-        T = torch.Tensor
-        dtypes = {g.dtype for g in some}
-        if len(dtypes) > 1 or list(map(T.numel, some)) != sizes or not all(map(T.is_contiguous, some)) \
-                or any(at != self._at for at in map(T.get_device, some)):
+            pointers = [0 if g is None else g.data_ptr() for g in grads]
+        if some and (set(map(T.get_device, some)) != {self._at} or len(set(map(_dtype_of, some))) > 1
+                     or list(map(T.numel, some)) != sizes or not all(map(T.is_contiguous, some))):
             _refuse("grads must be contiguous, of one type, of the parameters' sizes and on CUDA "
                     f"device {self._at}")
         lr = self.lr if lr is None else lr
@@ -1293,8 +1320,9 @@ class AdamW:
                           0.0 if on_device else lr, *self.betas, self.eps, self.seed & _WORD,
                           self._scalar("lr", lr if on_device else None),
                           self._scalar("grad_scale", grad_scale), self._scalar("skip", skip))
-        ob_adamw_step(config, self._table, grads, self.m, self.v, self.counter, self.m_exp,
-                      self.v_exp, self._at, stream)
+        pointers = array.array("Q", pointers)
+        _launch(lib().ob_adamw_step, self._at, stream, ct.byref(config), self._table,
+                pointers.buffer_info()[0], len(pointers), *self._buffers)
 
     def moments(self, stream=None):
         """(m, v) of all tensors, each tensor's from a multiple of 256 elements on: the

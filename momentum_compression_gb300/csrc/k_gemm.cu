@@ -495,13 +495,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
           for (int half = 0; half < 2; ++half) {
             float z[16];
             get(half, z);
-            if (u.part) {
+            if (u.part && m0 < a.M) {
               float4* p = part_at(a.partial, (int64_t)worker * 2 + u.slot, S::kRows, S::kCols, row0,
                                   col0 + g * kGroup + 16 * half);
 #pragma unroll
               for (int q = 0; q < 4; ++q)
                 p[32 * q] = make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
-            } else if (inside) {
+            } else if (!u.part && inside) {
               put_turned(turn, half, z);
             }
           }
@@ -636,12 +636,17 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
   p.whole = steps ? (int)tiles : 0;
   if (!steps) return p;
   // Cutting the last tiles saves steps, and costs the second kernel and its traffic.
+  // With no whole tile a worker may have as few as four steps, or the parts of a tile
+  // are more than their sum is worth.
   const int64_t rest = tiles % most;
   if (rest) {
-    const int64_t saved = p.steps - (rest * p.steps + most - 1) / most;
+    int64_t workers = most;
+    if (rest == tiles && rest * p.steps / 4 < most) workers = rest * p.steps / 4;
+    if (workers < rest) workers = rest;
+    const int64_t saved = p.steps - (rest * p.steps + workers - 1) / workers;
     if (saved > 16) {
       p.whole = (int)(tiles - rest);
-      p.workers = most;
+      p.workers = (int)workers;
     }
   }
   return p;

@@ -339,15 +339,10 @@ ob_status ob_adamw_step(const ob_adamw* a, const ob_adamw_tensor* tensors,
       return failf(OB_ERR_INVALID, "tensor %d: decay = %g must not be negative", i,
                    (double)t.decay);
     if (t.n > (1ull << 40)) return failf(OB_ERR_INVALID, "tensor %d is over 2^40 elements", i);
-    if (t.n) {
-      char name[32];
-      snprintf(name, sizeof name, "p of tensor %d", i);
-      OB_TRY(check_ptr(t.p, type_bytes(t.p_type), name));
-      snprintf(name, sizeof name, "copy of tensor %d", i);
-      if (t.copy) OB_TRY(check_ptr(t.copy, type_bytes(t.copy_type), name));
-      snprintf(name, sizeof name, "gradient of tensor %d", i);
-      if (grads[i]) OB_TRY(check_ptr(grads[i], type_bytes(a->grad_type), name));
-    }
+    auto lies = [](const void* p, int type) { return reinterpret_cast<uintptr_t>(p) % type_bytes(type) == 0; };
+    if (t.n && !t.p) return failf(OB_ERR_INVALID, "tensor %d: p is NULL", i);
+    if (t.n && !(lies(t.p, t.p_type) && (!t.copy || lies(t.copy, t.copy_type)) && lies(grads[i], a->grad_type)))
+      return failf(OB_ERR_ALIGN, "tensor %d: p, copy or gradient is not aligned to its element", i);
     list[i] = ob::AdamTensor{t.p, grads[i], t.copy, t.n, blocks, t.decay,
                              t.p_type | (t.copy ? t.copy_type : 0) << 8};
     blocks += (t.n + ob::kAdamBlock - 1) / ob::kAdamBlock;
