@@ -717,13 +717,12 @@ cudaError_t run(const Gemm& g, const Plan& p, cudaStream_t s) {
 
 }  // namespace
 
-size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K) {
+size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool a_mn, bool b_mn) {
   if (M == 0 || N == 0) return 0;
-  const size_t few = M <= kGemvRows ? gemv_partial_bytes(M, N, K) : 0;
+  if (M <= kGemvRows && !a_mn) return gemv_partial_bytes(M, N, K, b_mn);
   const Plan p = plan_of(M, N, K);
-  if (p.whole == p.tiles_m * p.tiles_n || !p.steps) return few;
-  const size_t parts = (size_t)p.workers * 2 * (128 * p.cg) * (128 * p.cg) * sizeof(float);
-  return parts > few ? parts : few;
+  if (p.whole == p.tiles_m * p.tiles_n || !p.steps) return 0;
+  return (size_t)p.workers * 2 * (128 * p.cg) * (128 * p.cg) * sizeof(float);
 }
 
 cudaError_t launch_gemm(const Gemm& g, cudaStream_t s) {

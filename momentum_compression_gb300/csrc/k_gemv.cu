@@ -253,8 +253,8 @@ cudaError_t go(const Gemm& g, cudaStream_t s) {
 
 }  // namespace
 
-size_t gemv_partial_bytes(int64_t M, int64_t N, int64_t K) {
-  const int parts = gemv_parts(N, K);
+size_t gemv_partial_bytes(int64_t M, int64_t N, int64_t K, bool b_mn) {
+  const int parts = b_mn ? gemv_parts(N, K) : 1;
   return parts > 1 ? (size_t)parts * M * N * sizeof(float) : 0;
 }
 

@@ -88,12 +88,12 @@ struct Gemm {
   float* partial;            // gemm_partial_bytes
 };
 
-// Of either product of these sizes, however the operands are stored.
-size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K);
+// By sizes and a_mn, b_mn alone.
+size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool a_mn, bool b_mn);
 // Up to this many rows of A, stored [M][K], a product is bound by B's way through the memory
 // and has kernels of its own (k_gemv.cu).
 constexpr int kGemvRows = 8;
-size_t gemv_partial_bytes(int64_t M, int64_t N, int64_t K);
+size_t gemv_partial_bytes(int64_t M, int64_t N, int64_t K, bool b_mn);
 cudaError_t launch_gemv(const Gemm& g, cudaStream_t s);
 cudaError_t launch_gemm(const Gemm& g, cudaStream_t s);
 
