@@ -57,6 +57,7 @@ struct GemmArgs {
   int whole;             // tiles that one worker takes whole; the others are cut
   int workers;
   uint32_t shape;
+  uint32_t stage;        // bytes of a step's copies to a block
   Epilogue ep;
   float* partial;        // [worker][2][rows][cols]
 };
@@ -298,6 +299,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
   const int worker = blockIdx.x / CG;
 
   if (threadIdx.x == 0) {
+    map_prefetch(&a.a);
+    map_prefetch(&a.b);
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&bar.full[i], 1);
       mbar_init(&bar.empty[i], 1);
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
           uint8_t* to = smem + st * S::kStage;
           if (CG == 2) {
             const uint32_t full = cluster_addr(smem_u32(&bar.full[st]), 0);
-            if (rank == 0) mbar_arrive_expect_tx(&bar.full[st], 2 * S::kStage);
+            if (rank == 0) mbar_arrive_expect_tx(&bar.full[st], 2 * a.stage);
             if (a.a_mn) {
               pair_load2(to, &a.a, m0, k * BK, full);
               pair_load2(to + S::kA / 2, &a.a, m0 + 64, k * BK, full);
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
               pair_load2(to + S::kA, &a.b, k * BK, n0, full);
             }
           } else {
-            mbar_arrive_expect_tx(&bar.full[st], S::kStage);
+            mbar_arrive_expect_tx(&bar.full[st], a.stage);
             if (a.a_mn) {
               tma_load2(to, &a.a, m0, k * BK, &bar.full[st]);
               tma_load2(to + S::kA / 2, &a.a, m0 + 64, k * BK, &bar.full[st]);
@@ -520,7 +523,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       __syncwarp();
       if (++buf == 2) buf = 0, par ^= 1;
     }
-    if (lane == 0) store_wait();
+    if (lane == 0) store_wait_read<0>();
     __syncwarp();
     tc_fence_before();
   }
@@ -577,17 +580,29 @@ __global__ void __launch_bounds__(256) k_gemm_parts(const __grid_constant__ Gemm
   auto get = [&](int half, float (&z)[16]) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) z[k] = 0.0f;
-    for (int p = p0; p <= p1; ++p) {
-      if (share(total, p, a.workers) == share(total, p + 1, a.workers)) continue;  // no step at all
-      const int slot = share(total, p, a.workers) > first ? 0 : 1;
-      const float4* q = part_at(a.partial, (int64_t)p * 2 + slot, S::kRows, S::kCols, row0, c + 16 * half);
+    // Every worker between has a step; the first alone may have begun before this tile.
+    constexpr int B = 4;  // parts on their way at once
+    for (int p = p0; p <= p1; p += B) {
+      float4 v[B][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 v = q[32 * k];
-        z[4 * k] += v.x;
-        z[4 * k + 1] += v.y;
-        z[4 * k + 2] += v.z;
-        z[4 * k + 3] += v.w;
+      for (int b = 0; b < B; ++b) {
+        if (p + b > p1) break;
+        const int slot = p + b == p0 && share(total, p0, a.workers) <= first ? 1 : 0;
+        const float4* q =
+            part_at(a.partial, (int64_t)(p + b) * 2 + slot, S::kRows, S::kCols, row0, c + 16 * half);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[b][k] = q[32 * k];
+      }
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        if (p + b > p1) break;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          z[4 * k] += v[b][k].x;
+          z[4 * k + 1] += v[b][k].y;
+          z[4 * k + 2] += v[b][k].z;
+          z[4 * k + 3] += v[b][k].w;
+        }
       }
     }
   };
@@ -597,7 +612,7 @@ __global__ void __launch_bounds__(256) k_gemm_parts(const __grid_constant__ Gemm
       out.group<__nv_bfloat16>(a, 0, m0, n0, get);
     else
       out.group<__half>(a, 0, m0, n0, get);
-    if (lane == 0) store_wait();
+    if (lane == 0) store_wait_read<0>();
     return;
   }
   float* turn = reinterpret_cast<float*>(out.buf);
@@ -620,36 +635,45 @@ struct Plan {
   int cg, tiles_m, tiles_n, steps, workers, whole;
 };
 
-// What a product is cut into.  By sizes alone: the workspace goes by it.
-Plan plan_of(int64_t M, int64_t N, int64_t K) {
-  Plan p{};
+// Rows of A that a block copies: few rows are copied as they are, and what the other rows of
+// the tile hold gives sums that nobody reads.
+int copied_rows(int64_t M, bool a_mn) { return M < 128 && !a_mn ? (int)((M + 7) / 8 * 8) : 128; }
+
+// What a product is cut into.  By sizes and a_mn alone: the workspace goes by it.
+Plan plan_of(int64_t M, int64_t N, int64_t K, bool a_mn) {
   const int64_t steps = (K + BK - 1) / BK;
-  const int64_t tm2 = (M + 255) / 256, tn2 = (N + 255) / 256;
-  p.cg = tm2 * tn2 >= kSms / 4 ? 2 : 1;
-  const int edge = 128 * p.cg;
-  p.tiles_m = (int)((M + edge - 1) / edge);
-  p.tiles_n = (int)((N + edge - 1) / edge);
-  p.steps = (int)steps;
-  const int most = kSms / p.cg;
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-  p.workers = (int)(tiles < most ? tiles : most);
-  p.whole = steps ? (int)tiles : 0;
-  if (!steps) return p;
-  // Cutting the last tiles saves steps, and costs the second kernel and its traffic.
-  // With no whole tile a worker may have as few as four steps, or the parts of a tile
-  // are more than their sum is worth.
-  const int64_t rest = tiles % most;
-  if (rest) {
+  // A step takes about 0.27 us in either form: a block's copies of 32 KB, which a pair needs
+  // for four times the products.  Cutting the last tiles costs the second kernel and its
+  // traffic, about 4.5 us (16 steps); a pair's epilogue is the longer one.
+  auto form = [&](int cg, int64_t* time) {
+    Plan p{};
+    p.cg = cg;
+    const int edge = 128 * cg, most = kSms / cg;
+    p.tiles_m = (int)((M + edge - 1) / edge);
+    p.tiles_n = (int)((N + edge - 1) / edge);
+    p.steps = (int)steps;
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, rest = tiles % most;
+    const int64_t cost = cg == 1 ? 16 * 256 / (copied_rows(M, a_mn) + 128) : 16;
+    p.workers = (int)(tiles < most ? tiles : most);
+    p.whole = steps ? (int)tiles : 0;
+    *time = (tiles + most - 1) / most * steps + 4 * cg;
+    // A worker has four steps at least (the others' parts of a tile are summed as if every
+    // one between had some), or the parts are more than their sum is worth.
     int64_t workers = most;
-    if (rest == tiles && rest * p.steps / 4 < most) workers = rest * p.steps / 4;
-    if (workers < rest) workers = rest;
-    const int64_t saved = p.steps - (rest * p.steps + workers - 1) / workers;
-    if (saved > 16) {
-      p.whole = (int)(tiles - rest);
-      p.workers = (int)workers;
+    if (rest == tiles && rest * steps / 4 < most) workers = rest * steps / 4;
+    if (rest && workers > rest && rest * steps >= 4 * workers) {
+      const int64_t share = (rest * steps + workers - 1) / workers;
+      if (steps - share > cost) {
+        p.whole = (int)(tiles - rest);
+        p.workers = (int)workers;
+        *time = tiles / most * steps + share + cost + 4 * cg;
+      }
     }
-  }
-  return p;
+    return p;
+  };
+  int64_t t1, t2;
+  const Plan p1 = form(1, &t1), p2 = form(2, &t2);
+  return t2 < t1 ? p2 : p1;
 }
 
 template <int CG>
@@ -660,11 +684,13 @@ cudaError_t run(const Gemm& g, const Plan& p, cudaStream_t s) {
   auto map = [&](CUtensorMap* to, const Mat& m, int64_t rows, int64_t cols, int bc, int br) {
     if (e == cudaSuccess) e = matrix_tensor_map(to, m, g.ep.type, rows, cols, bc, br);
   };
+  const int a_rows = CG == 1 ? copied_rows(g.M, g.a_mn) : 128;
+  a.stage = a_rows * BK * 2 + S::kB;
   if (p.steps) {
     if (g.a_mn)
       map(&a.a, g.a, g.K, g.M, 64, BK);
     else
-      map(&a.a, g.a, g.M, g.K, 64, 128);
+      map(&a.a, g.a, g.M, g.K, 64, a_rows);
     if (g.b_mn)
       map(&a.b, g.b, g.K, g.N, 64, BK);
     else
@@ -720,7 +746,7 @@ cudaError_t run(const Gemm& g, const Plan& p, cudaStream_t s) {
 size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool a_mn, bool b_mn) {
   if (M == 0 || N == 0) return 0;
   if (M <= kGemvRows && !a_mn) return gemv_partial_bytes(M, N, K, b_mn);
-  const Plan p = plan_of(M, N, K);
+  const Plan p = plan_of(M, N, K, a_mn);
   if (p.whole == p.tiles_m * p.tiles_n || !p.steps) return 0;
   return (size_t)p.workers * 2 * (128 * p.cg) * (128 * p.cg) * sizeof(float);
 }
@@ -728,7 +754,7 @@ size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool a_mn, bool b_mn)
 cudaError_t launch_gemm(const Gemm& g, cudaStream_t s) {
   if (g.M == 0 || g.N == 0) return cudaSuccess;
   if (g.M <= kGemvRows && !g.a_mn) return launch_gemv(g, s);
-  const Plan p = plan_of(g.M, g.N, g.K);
+  const Plan p = plan_of(g.M, g.N, g.K, g.a_mn);
   return p.cg == 2 ? run<2>(g, p, s) : run<1>(g, p, s);
 }
 

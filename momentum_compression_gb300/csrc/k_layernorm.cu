@@ -694,15 +694,15 @@ template <typename T, int LIES>
 cudaError_t bwd(const LayerNormBwdArgs& a, cudaStream_t s) {
   if (a.cols <= 256 * 8) {
     // Four rows of a group share a barrier, where there are units enough for every
-    // block and two of them fit.
+    // block and two of them fit; else two.
     const int groups = 256 / group_threads(a.cols);
     const size_t row = LIES ? a.cols * sizeof(T) : a.cols * sizeof(T) + 30;
     const size_t unit = (size_t)groups * 4 * row * (a.dsum ? 3 : 2);
     const bool four = a.rows >= (uint64_t)a.parts * groups * 16 && unit <= ring_most(256) / 2;
     if (LIES && a.cols == group_threads(a.cols) * 8)
       return four ? bwd_launch<T, 256, 1, 4, LIES ? 2 : 0>(a, s)
-                  : bwd_launch<T, 256, 1, 1, LIES ? 2 : 0>(a, s);
-    return four ? bwd_launch<T, 256, 1, 4, LIES>(a, s) : bwd_launch<T, 256, 1, 1, LIES>(a, s);
+                  : bwd_launch<T, 256, 1, 2, LIES ? 2 : 0>(a, s);
+    return four ? bwd_launch<T, 256, 1, 4, LIES>(a, s) : bwd_launch<T, 256, 1, 2, LIES>(a, s);
   }
   return a.cols <= 512 * 8 ? bwd_launch<T, 512, 1, 1, LIES>(a, s)
                            : bwd_launch<T, 512, 2, 1, LIES>(a, s);

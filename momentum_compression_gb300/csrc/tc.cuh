@@ -185,6 +185,10 @@ __device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, int
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
+// Asks for a tensor map that copies will soon go by.
+__device__ __forceinline__ void map_prefetch(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void tma_load2(void* dst, const CUtensorMap* map, int x, int y,
                                           uint64_t* bar) {
   asm volatile(
@@ -207,9 +211,6 @@ __device__ __forceinline__ void store_commit() {
 template <int N>
 __device__ __forceinline__ void store_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void store_wait() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 // A cluster's blocks wait for one another here, and see what was written
 // before; every thread of every block takes part.
