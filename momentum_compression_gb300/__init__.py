@@ -1255,6 +1255,11 @@ class AdamW:
                             "parameter's shape")
             self._table[i] = ob_adamw_tensor(p.data_ptr(), _ptr(c), self._sizes[i], d, _type(p, "params"),
                                              0 if c is None else _type(c, "copies"))
+        # what is written twice in a step is in no order
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                       for t in self.params + [c for c in self.copies if c is not None] if t.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            _refuse("params and copies must not overlap, nor be the same tensor twice")
         blocks = [-(-k // OB_ADAMW_BLOCK) for k in self._sizes]
         total = OB_ADAMW_BLOCK * sum(blocks)
         dtype = torch.float32 if state_bits == 32 else torch.uint8

@@ -15,7 +15,6 @@
 // takes an equal share of all their steps, parts of a tile go to the
 // workspace in fp32, and a second kernel adds a tile's parts in their order and
 // runs the epilogue.
-#include <atomic>
 #include <type_traits>
 
 #include "act.cuh"
@@ -28,7 +27,7 @@
 namespace ob {
 namespace {
 
-__device__ unsigned g_layer_error;
+__device__ unsigned g_linear_error;
 
 constexpr int BK = 64;            // of the sum a step
 constexpr int kEpWarps = 16;
@@ -254,7 +253,7 @@ struct Out {
       __syncwarp();
     }
     if (e.residual.data) {
-      const bool ok = warp_wait(&bar[b], par >> b & 1, &g_layer_error);
+      const bool ok = warp_wait(&bar[b], par >> b & 1, &g_linear_error);
       par ^= 1u << b;
       if (!ok) return false;
     }
@@ -346,7 +345,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       tile_at(u.tile, a.tiles_m, a.tiles_n, &tm, &tn);
       const int m0 = tm * S::kRows + (int)rank * 128, n0 = tn * S::kCols + (int)rank * 128 * (CG - 1);
       for (int k = u.k0; k < u.k1; ++k) {
-        if (n >= S::kStages) ok = warp_wait(&bar.empty[st], par, &g_layer_error, kErrWaitEmpty);
+        if (n >= S::kStages) ok = warp_wait(&bar.empty[st], par, &g_linear_error, kErrWaitEmpty);
         if (!ok) break;
         if (lane == 0) {
           uint8_t* to = smem + st * S::kStage;
@@ -387,7 +386,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
     }
     if (!ok && rank == 0)  // a wait ran out: let what is in flight land before the block ends
       for (int64_t i = n > S::kStages ? n - S::kStages : 0; i < n; ++i)
-        mbar_wait(&bar.full[i % S::kStages], (i / S::kStages) & 1, &g_layer_error, kErrDrain);
+        mbar_wait(&bar.full[i % S::kStages], (i / S::kStages) & 1, &g_linear_error, kErrDrain);
   } else if (warp == 1) {
     // ----- products --------------------------------------------------------
     if (rank == 0) {
@@ -402,12 +401,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       int64_t n = 0;
       int64_t units = 0;
       while (ok && u.next(a)) {
-        if (units >= 2) ok = warp_wait(&bar.sum_empty[buf], sum_par, &g_layer_error, kErrWaitEmpty);
+        if (units >= 2) ok = warp_wait(&bar.sum_empty[buf], sum_par, &g_linear_error, kErrWaitEmpty);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + buf * S::kCols;
         for (int k = u.k0; k < u.k1; ++k) {
-          ok = warp_wait(&bar.full[st], par, &g_layer_error);
+          ok = warp_wait(&bar.full[st], par, &g_linear_error);
           if (!ok) break;
           tc_fence_after();
           const uint64_t ad = a_desc + (uint32_t)st * (S::kStage >> 4);
@@ -443,7 +442,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
           pair_commit(leader, &bar.drain);
         else
           mma_commit(leader, &bar.drain);
-        mbar_wait(&bar.drain, 0, &g_layer_error, kErrDrain);
+        mbar_wait(&bar.drain, 0, &g_linear_error, kErrDrain);
       }
     }
   } else {
@@ -465,7 +464,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       const int row0 = (int)rank * 128 + lanes0;  // in the tile
       const int64_t m0 = (int64_t)tm * S::kRows + row0, n0 = (int64_t)tn * S::kCols + col0;
       if (a.ep.tiled && !u.part) out.begin<kCols / kGroup>(a, m0, n0);
-      ok = warp_wait(&bar.sum_full[buf], par, &g_layer_error);
+      ok = warp_wait(&bar.sum_full[buf], par, &g_linear_error);
       if (!ok) break;
       tc_fence_after();
       int taken = 0;  // columns
@@ -758,16 +757,8 @@ cudaError_t launch_gemm(const Gemm& g, cudaStream_t s) {
   return p.cg == 2 ? run<2>(g, p, s) : run<1>(g, p, s);
 }
 
-cudaError_t layer_error_word(unsigned** word) {
-  static std::atomic<unsigned*> known[64];  // by device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  *word = known[dev & 63].load(std::memory_order_acquire);
-  if (*word) return cudaSuccess;
-  e = cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_layer_error);
-  if (e == cudaSuccess) known[dev & 63].store(*word, std::memory_order_release);
-  return e;
+cudaError_t linear_error_word(unsigned** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_linear_error);
 }
 
 }  // namespace ob

@@ -15,6 +15,8 @@
 namespace ob {
 namespace {
 
+__device__ unsigned g_layernorm_error;
+
 constexpr int kWide = 512;       // threads of a block that walks over its row
 constexpr int kStrip = 32;       // columns of a block of the weights' gradient
 constexpr int kStripRows = 32;
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(kBwdThreads + 32, kBwdThreads == 256 ? 2 : 1)
     uint32_t n = 0;
     bool ok = true;
     for (uint64_t u = blockIdx.x; u < units; u += gridDim.x, ++n) {
-      if (n >= (uint32_t)p.stages) ok = warp_wait(&empty[st], par, a.error, kErrWaitEmpty);
+      if (n >= (uint32_t)p.stages) ok = warp_wait(&empty[st], par, &g_layernorm_error, kErrWaitEmpty);
       if (!ok) break;
       const uint64_t r0 = u * p.rows;
       const int rows = (int)(a.rows - r0 < (uint64_t)p.rows ? a.rows - r0 : p.rows);
@@ -428,7 +430,7 @@ __global__ void __launch_bounds__(kBwdThreads + 32, kBwdThreads == 256 ? 2 : 1)
     }
     if (!ok)  // a wait ran out: let what is in flight land before the block ends
       for (uint32_t i = n > (uint32_t)p.stages ? n - p.stages : 0; i < n; ++i)
-        mbar_wait(&full[i % p.stages], (i / p.stages) & 1, a.error, kErrDrain);
+        mbar_wait(&full[i % p.stages], (i / p.stages) & 1, &g_layernorm_error, kErrDrain);
     return;
   }
 
@@ -473,7 +475,7 @@ __global__ void __launch_bounds__(kBwdThreads + 32, kBwdThreads == 256 ? 2 : 1)
       sums[2 * r] = sums[2 * r + 1] = 0.0f;
     }
     statistics(u + gridDim.x);
-    const bool ok = warp_wait(&full[st], par, a.error);
+    const bool ok = warp_wait(&full[st], par, &g_layernorm_error);
     auto row_of = [&](int k, int r) {
       uint32_t at = st * stage_bytes + k * array_bytes + (group * R + r) * p.pitch;
       if (LIES == 0) at += (uint32_t)(reinterpret_cast<uintptr_t>(from[k] + (r0 + r) * ld[k]) & 15);
@@ -594,22 +596,22 @@ __global__ void __launch_bounds__(kBwdThreads + 32, kBwdThreads == 256 ? 2 : 1)
 }
 
 // dweight and dbias from the parts, in a fixed order: 32 sums a block, a warp every
-// eighth part.
-__global__ void __launch_bounds__(256) k_ln_sums(const __grid_constant__ LayerNormBwdArgs a) {
-  __shared__ float sums[8][32];
+// 32nd part.
+__global__ void __launch_bounds__(1024) k_ln_sums(const __grid_constant__ LayerNormBwdArgs a) {
+  __shared__ float sums[32][32];
   grid_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane;
   float t = 0.0f;
   if (i < 2 * a.cols)
 #pragma unroll 8
-    for (int p = w; p < a.parts; p += 8) t += a.partial[(size_t)p * 2 * a.cols + i];
+    for (int p = w; p < a.parts; p += 32) t += a.partial[(size_t)p * 2 * a.cols + i];
   sums[w][lane] = t;
   __syncthreads();
   if (w || i >= 2 * a.cols) return;
   t = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) t += sums[k][lane];
+  for (int k = 0; k < 32; ++k) t += sums[k][lane];
   void* to = i < a.cols ? a.dweight : a.dbias;
   if (to) store_from_f32(to, i < a.cols ? i : i - a.cols, a.w_type, t);
 }
@@ -710,6 +712,10 @@ cudaError_t bwd(const LayerNormBwdArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+cudaError_t layernorm_error_word(unsigned** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_layernorm_error);
+}
+
 cudaError_t launch_layernorm_fwd(const LayerNormArgs& a, int type, cudaStream_t s) {
   return by_type(type, [&](auto zero) {
     using T = decltype(zero);
@@ -755,11 +761,10 @@ cudaError_t launch_layernorm_bwd(const LayerNormBwdArgs& b, int type, cudaStream
       const uint64_t ld[4] = {a.ldx, a.lddy, a.lddx, a.ldds};
       for (int i = 0; i < 4; ++i)
         if (p[i]) vec = vec && on16(p[i]) && (a.rows == 1 || ld[i] * sizeof(T) % 16 == 0);
-      e = layer_error_word(&a.error);
-      if (e == cudaSuccess) e = vec ? bwd<T, 1>(a, s) : bwd<T, 0>(a, s);
+      e = vec ? bwd<T, 1>(a, s) : bwd<T, 0>(a, s);
     }
     if (e != cudaSuccess || !sums) return e;
-    return launch_behind(k_ln_sums, dim3((2 * a.cols + 31) / 32), dim3(256), 0, s, a);
+    return launch_behind(k_ln_sums, dim3((2 * a.cols + 31) / 32), dim3(1024), 0, s, a);
   });
 }
 

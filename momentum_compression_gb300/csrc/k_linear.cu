@@ -120,23 +120,23 @@ __global__ void __launch_bounds__(kDzThreads, kDzBlocks) k_dz(const __grid_const
   }
 }
 
-// dbias from the parts: 32 columns a block, a warp every eighth part.
+// dbias from the parts: 32 columns a block, a warp every 32nd part.
 template <typename T>
-__global__ void __launch_bounds__(256) k_dbias(const float* partial, int parts, int64_t N, T* out) {
-  __shared__ float sums[8][32];
+__global__ void __launch_bounds__(1024) k_dbias(const float* partial, int parts, int64_t N, T* out) {
+  __shared__ float sums[32][32];
   grid_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t n = (int64_t)blockIdx.x * 32 + lane;
   float t = 0.0f;
   if (n < N)
 #pragma unroll 8
-    for (int p = w; p < parts; p += 8) t += partial[(int64_t)p * N + n];
+    for (int p = w; p < parts; p += 32) t += partial[(int64_t)p * N + n];
   sums[w][lane] = t;
   __syncthreads();
   if (w || n >= N) return;
   t = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) t += sums[k][lane];
+  for (int k = 0; k < 32; ++k) t += sums[k][lane];
   out[n] = from_f32<T>(t);
 }
 
@@ -300,9 +300,9 @@ cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t s) {
     if (e == cudaSuccess && a.dbias) {
       const dim3 grid((unsigned)((N + 31) / 32));
       e = a.type == OB_TYPE_BF16
-              ? launch_behind(k_dbias<__nv_bfloat16>, grid, dim3(256), 0, s, d.partial, d.parts, N,
+              ? launch_behind(k_dbias<__nv_bfloat16>, grid, dim3(1024), 0, s, d.partial, d.parts, N,
                               static_cast<__nv_bfloat16*>(a.dbias))
-              : launch_behind(k_dbias<__half>, grid, dim3(256), 0, s, d.partial, d.parts, N,
+              : launch_behind(k_dbias<__half>, grid, dim3(1024), 0, s, d.partial, d.parts, N,
                               static_cast<__half*>(a.dbias));
     }
   }

@@ -31,7 +31,6 @@ struct LayerNormBwdArgs {
   uint64_t rows;
   int cols, w_type;
   float* partial;                // [parts][2][cols]
-  unsigned* error;               // where a wait that runs out leaves its code
   int parts;
 };
 
@@ -64,9 +63,9 @@ struct LinearArgs {
 size_t linear_workspace_bytes(const LinearArgs& a, bool backward);
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t s);
-// The device word where a wait of layer norm or the dense layer that ran out
-// leaves its code.
-cudaError_t layer_error_word(unsigned** word);
+// The device words where a wait that ran out leaves its code.
+cudaError_t linear_error_word(unsigned** word);
+cudaError_t layernorm_error_word(unsigned** word);
 
 // ---------------------------------------------------------------------------
 // One product C[M][N] = sum over k of A(m, k) B(n, k) with the dense layer's

@@ -292,14 +292,17 @@ ob_status ob_layer_device_error(unsigned* code, ob_stream_t stream) {
   OB_TRACE();
   if (!code) return failf(OB_ERR_INVALID, "layer_device_error: code is NULL");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  unsigned* word = nullptr;
-  unsigned v = 0;
-  cudaError_t e = ob::layer_error_word(&word);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(&v, word, sizeof v, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof v, s);
+  unsigned* words[2] = {nullptr, nullptr};
+  unsigned v[2] = {0, 0};
+  cudaError_t e = ob::linear_error_word(&words[0]);
+  if (e == cudaSuccess) e = ob::layernorm_error_word(&words[1]);
+  for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+    e = cudaMemcpyAsync(&v[i], words[i], sizeof v[i], cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(words[i], 0, sizeof v[i], s);
+  }
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return launched(e, "layer_device_error");
-  *code = v;
+  *code = v[0] ? v[0] : v[1];
   return OB_OK;
 }
 

@@ -165,7 +165,7 @@ def test_layer_norm_of_constant_far_and_special_rows():
 DENSE = [(1, 1, 1), (1, 64, 64), (1, 1000, 333), (2, 40, 8), (3, 129, 257), (8, 512, 1024),
          (9, 300, 70), (16, 8, 16), (17, 256, 512), (33, 65, 1), (64, 1, 100), (100, 200, 300),
          (127, 128, 129), (128, 256, 64), (129, 257, 65), (250, 768, 96), (256, 256, 256),
-         (257, 511, 513), (300, 64, 2000), (513, 1024, 320), (1000, 136, 1000), (777, 1301, 1001)]
+         (257, 511, 513), (300, 64, 2000), (513, 1024, 320), (19500, 100, 1100), (1000, 136, 1000), (777, 1301, 1001)]
 
 
 def _dense_case(Mr, N, K, dtype, kn, pad, shift, seed=0):
@@ -493,6 +493,158 @@ def test_adamw_state_goes_on_and_graphs_step():
             assert torch.equal(x, y)
         # powers of b1 and b2 by products: five roundings of 2^-53
         assert torch.allclose(a.counter, b.counter, rtol=1e-15, atol=0)
+
+
+# ---------------------------------------------------------------------------
+# Streams and graphs
+# ---------------------------------------------------------------------------
+
+def _pass(seed, dtype=BF16, rows=520, d=320, f=768):
+    """(inputs, a function that runs layer norm and a dense layer both ways, into new tensors)"""
+    mk = _gen(seed)
+    x, r, ds, w1, b1 = mk(rows, d, dtype=dtype), mk(rows, d, dtype=dtype), mk(rows, d, dtype=dtype), mk(d), mk(d)
+    w, b, dy = mk(f, d, dtype=dtype), mk(f, dtype=dtype), mk(rows, f, dtype=dtype)
+    E = lambda *s, dt=dtype: torch.empty(*s, device="cuda", dtype=dt)
+    h, s, mean, rstd = E(rows, d), E(rows, d), E(rows, dt=F32), E(rows, dt=F32)
+    y, z, dh, dw, db = E(rows, f), E(rows, f), E(rows, d), E(f, d), E(f)
+    dx, dw1, db1 = E(rows, d), E(d, dt=F32), E(d, dt=F32)
+
+    def run(stream=None):
+        kw = dict(stream=stream)
+        ob.ob_layernorm_fwd(x, h, w1, b1, 1e-5, r, s, mean, rstd, **kw)
+        ob.ob_linear_fwd(h, w, y, b, None, z, "gelu", **kw)
+        ob.ob_linear_bwd(dy, h, w, dh, dw, db, z, "gelu", **kw)
+        ob.ob_layernorm_bwd(dh, s, mean, rstd, dx, w1, dw1, db1, ds, **kw)
+        return (y, z, s, dw, db, dx, dw1, db1)
+    return run
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_layers_on_two_streams(handle):
+    """In turn on two streams and without waiting: the same bits as one after another."""
+    runs = [_pass(1), _pass(2, rows=3000)]
+    want = []
+    for r in runs:
+        want.append([t.clone() for t in r()])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        got = [runs[0](), runs[1](side.cuda_stream if handle else side)]
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
+def test_layers_in_a_graph():
+    """Captured and replayed on new inputs: the same bits as called."""
+    mk = _gen(31)
+    x, w1 = mk(300, 256, dtype=BF16), mk(256, dtype=BF16)
+    up, down = mk(512, 256, dtype=BF16), mk(256, 512, dtype=BF16)
+    dy = mk(300, 256, dtype=BF16)
+
+    def step(x):
+        leaves = [t.detach().requires_grad_() for t in (x, w1, up, down)]
+        y, s = M.layer_norm(leaves[0], leaves[1], residual=leaves[0], return_sum=True)
+        h = M.linear(y, leaves[2], activation="gelu")
+        out = M.linear(h, leaves[3], residual=s)
+        return [out.detach(), *torch.autograd.grad(out, leaves, dy)]
+
+    held = x.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(held)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(held)
+    for k in range(3):
+        held.copy_(mk(300, 256, dtype=BF16))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, step(held)))
+
+
+FIRST = """
+import torch, momentum_compression_gb300 as ob
+mk = lambda *s: torch.ones(*s, device="cuda", dtype=torch.bfloat16)
+x, w, y, z, dx, dw, db = mk(300, 64), mk(96, 64), mk(300, 96), mk(300, 96), mk(300, 64), mk(96, 64), mk(96)
+m, d, p = torch.zeros(300, device="cuda"), torch.zeros(300, device="cuda"), torch.ones(500, device="cuda")
+g, opt = torch.ones_like(p), ob.AdamW([p], state_bits=8)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    ob.ob_layernorm_fwd(x, dx, mean=m, rstd=d)
+    ob.ob_layernorm_bwd(x, x, m, d, dx, dweight=db[:64])
+    ob.ob_linear_fwd(x, w, y, db, None, z, "gelu")
+    ob.ob_linear_bwd(y, x, w, dx, dw, db, z, "gelu")
+    opt.step([g])
+graph.replay()
+torch.cuda.synchronize()
+assert (y[0, 95] - 65).abs() < 1 and ob.ob_layer_device_error() == 0
+print("fine")
+"""
+
+
+@pytest.mark.parametrize("what", ["dense", "attention"])
+def test_first_call_of_a_thread(what):
+    """A thread that has done nothing on the GPU yet, as autograd's."""
+    import threading
+    mk = _gen(12)
+    x, w, y = mk(300, 64, dtype=BF16), mk(96, 64, dtype=BF16), torch.zeros(300, 96, device="cuda", dtype=BF16)
+    q, o = mk(1, 70, 2, 64, dtype=BF16), torch.zeros(1, 70, 2, 64, device="cuda", dtype=BF16)
+    call = (lambda out: ob.ob_linear_fwd(x, w, out)) if what == "dense" else \
+        (lambda out: ob.ob_attn_fwd(q, q, q, out))
+    out = y if what == "dense" else o
+    got, errors = torch.zeros_like(out), []
+
+    def body():
+        try:
+            call(got)
+        except Exception as e:
+            errors.append(e)
+    t = threading.Thread(target=body)
+    t.start()
+    t.join()
+    call(out)
+    torch.cuda.synchronize()
+    assert not errors and torch.equal(got, out)
+
+
+def test_first_calls_are_in_a_capture():
+    """A process whose first calls are captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "fine", r.stderr[-2000:]
+
+
+def test_model_functions_are_the_entry_points():
+    """Views that kernels cannot read are copied; without gradients nothing is kept."""
+    mk = _gen(41)
+    x, w, b = mk(6, 40, 2 * 96, dtype=BF16)[..., ::2], mk(96, 200, dtype=BF16), mk(200, dtype=BF16)
+    assert torch.equal(M.linear(x, w.t(), b, "gelu"), M.linear(x.contiguous(), w.t().contiguous(), b, "gelu"))
+    res = mk(6, 200, 40, dtype=BF16).transpose(1, 2)
+    got = M.linear(x, w.t(), b, "relu", res)
+    assert torch.equal(got, M.linear(x, w.t(), b, "relu", res.contiguous()))
+    weight = mk(192)[::2]
+    assert torch.equal(M.layer_norm(x, weight), M.layer_norm(x.contiguous(), weight.contiguous()))
+    a, r = (mk(50, 96, dtype=BF16).requires_grad_() for _ in range(2))
+    y, s = M.layer_norm(a, residual=r, return_sum=True)
+    dy, ds = mk(50, 96, dtype=BF16), mk(50, 96, dtype=BF16)
+    both = torch.autograd.grad((y, s), (a, r), (dy, ds), retain_graph=True)
+    assert torch.equal(*both)
+    only_y, = torch.autograd.grad(y, a, dy, retain_graph=True)
+    only_s, = torch.autograd.grad(s, a, ds)
+    assert torch.equal(only_s, ds)
+    near = (both[0].double() - only_y.double() - ds.double()).abs()
+    assert (near <= 2.0 ** -8 * (both[0].double().abs() + only_y.double().abs())).all()
+    with pytest.raises(ValueError):
+        M.layer_norm(a, return_sum=True)
+    with pytest.raises(RuntimeError):
+        g, = torch.autograd.grad(M.layer_norm(a).sum(), a, create_graph=True)
+        g.sum().backward()
 
 
 # ---------------------------------------------------------------------------

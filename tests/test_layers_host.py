@@ -151,6 +151,7 @@ def test_binding_refuses():
         lambda: ob.AdamW([]), lambda: ob.AdamW([torch.zeros(3)]), lambda: ob.AdamW([p], state_bits=16),
         lambda: ob.AdamW([p], weight_decay=[0.1, 0.2]), lambda: ob.AdamW([p], copies=[x]),
         lambda: ob.AdamW([p, _zeros(5, dtype=F32, at=1)]), lambda: ob.AdamW([_zeros(4, 8).t()]),
+        lambda: ob.AdamW([p, p]), lambda: ob.AdamW([p], copies=[p]), lambda: ob.AdamW([p, p[:5]]),
         lambda: ob.AdamW([p], state=dict(m=p, v=p, step=1)), lambda: ob.AdamW([p], state=dict(step=1)),
     ]
     for i, call in enumerate(calls):
