@@ -59,6 +59,19 @@ struct GemmArgs {
   uint32_t stage;        // bytes of a step's copies to a block
   Epilogue ep;
   float* partial;        // [worker][2][rows][cols]
+  __device__ __forceinline__ bool second(unsigned) const { return false; }
+  __device__ __forceinline__ const GemmArgs& of(bool) const { return *this; }
+  __device__ __forceinline__ int from(bool) const { return 0; }
+};
+
+// One product, or two that together leave no block without one: those from `first` on work
+// at the second.
+struct GemmPair {
+  GemmArgs g[2];
+  int first;
+  __device__ __forceinline__ bool second(unsigned block) const { return (int)block >= first; }
+  __device__ __forceinline__ const GemmArgs& of(bool second) const { return g[second]; }
+  __device__ __forceinline__ int from(bool second) const { return second ? first : 0; }
 };
 
 // Tile t in an order in which tiles that run at one time share operands: strips
@@ -287,15 +300,18 @@ struct GemmBars {
   uint32_t tmem;
 };
 
-template <int CG>
-__global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant__ GemmArgs a) {
+// Args: GemmArgs, or GemmPair.
+template <int CG, typename Args>
+__global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant__ Args args) {
   using S = Shape<CG>;
+  const bool second = args.second(blockIdx.x);
+  const GemmArgs& a = args.of(second);
   extern __shared__ uint8_t raw[];
   __shared__ GemmBars bar;
   uint8_t* smem = align_shared(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-  const int worker = blockIdx.x / CG;
+  const int worker = ((int)blockIdx.x - args.from(second)) / CG;
 
   if (threadIdx.x == 0) {
     map_prefetch(&a.a);
@@ -676,9 +692,9 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, bool a_mn) {
 }
 
 template <int CG>
-cudaError_t run(const Gemm& g, const Plan& p, cudaStream_t s) {
+cudaError_t fill(const Gemm& g, const Plan& p, GemmArgs* out) {
   using S = Shape<CG>;
-  GemmArgs a{};
+  GemmArgs& a = *out;
   cudaError_t e = cudaSuccess;
   auto map = [&](CUtensorMap* to, const Mat& m, int64_t rows, int64_t cols, int bc, int br) {
     if (e == cudaSuccess) e = matrix_tensor_map(to, m, g.ep.type, rows, cols, bc, br);
@@ -700,7 +716,6 @@ cudaError_t run(const Gemm& g, const Plan& p, cudaStream_t s) {
     if (g.ep.z.data) map(&a.z, g.ep.z, g.M, g.N, kGroup, 32);
     if (g.ep.residual.data) map(&a.residual, g.ep.residual, g.M, g.N, kGroup, 32);
   }
-  if (e != cudaSuccess) return e;
   a.a_mn = g.a_mn;
   a.b_mn = g.b_mn;
   a.M = g.M;
@@ -713,17 +728,20 @@ cudaError_t run(const Gemm& g, const Plan& p, cudaStream_t s) {
   a.shape = mma_shape(g.ep.type == OB_TYPE_BF16, S::kCols, g.b_mn, g.a_mn, S::kRows);
   a.ep = g.ep;
   a.partial = g.partial;
-  const int rest = p.tiles_m * p.tiles_n - p.whole;
-  const dim3 parts(rest * ((S::kRows / 32) * (S::kCols / kGroup) / 8));
-  if (!p.steps) return launch_behind(k_gemm_parts<CG>, parts, dim3(256), 0, s, a);
+  return e;
+}
+
+template <int CG, typename Args>
+cudaError_t run_products(const Args& args, int blocks, cudaStream_t s) {
+  using S = Shape<CG>;
   static PerDeviceOnce once;
-  e = once.run([] {
-    return cudaFuncSetAttribute(k_gemm<CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(k_gemm<CG, Args>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)S::kBytes);
   });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3(p.workers * CG);
+  c.gridDim = dim3(blocks);
   c.blockDim = dim3(kGemmThreads);
   c.dynamicSmemBytes = S::kBytes;
   c.stream = s;
@@ -735,9 +753,24 @@ cudaError_t run(const Gemm& g, const Plan& p, cudaStream_t s) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   c.attrs = at;
   c.numAttrs = CG == 2 ? 2 : 1;
-  e = cudaLaunchKernelEx(&c, k_gemm<CG>, a);
-  if (e != cudaSuccess || rest == 0) return e;
-  return launch_behind(k_gemm_parts<CG>, parts, dim3(256), 0, s, a);
+  return cudaLaunchKernelEx(&c, k_gemm<CG, Args>, args);
+}
+// The second kernel of a product that is cut.
+template <int CG>
+cudaError_t run_parts(const GemmArgs& a, cudaStream_t s) {
+  using S = Shape<CG>;
+  const int rest = a.tiles_m * a.tiles_n - a.whole;
+  if (!rest) return cudaSuccess;
+  return launch_behind(k_gemm_parts<CG>, dim3(rest * ((S::kRows / 32) * (S::kCols / kGroup) / 8)),
+                       dim3(256), 0, s, a);
+}
+
+template <int CG>
+cudaError_t run_one(const Gemm& g, const Plan& p, cudaStream_t s) {
+  GemmArgs a{};
+  cudaError_t e = fill<CG>(g, p, &a);
+  if (e == cudaSuccess && p.steps) e = run_products<CG>(a, a.workers * CG, s);
+  return e == cudaSuccess ? run_parts<CG>(a, s) : e;
 }
 
 }  // namespace
@@ -754,7 +787,26 @@ cudaError_t launch_gemm(const Gemm& g, cudaStream_t s) {
   if (g.M == 0 || g.N == 0) return cudaSuccess;
   if (g.M <= kGemvRows && !g.a_mn) return launch_gemv(g, s);
   const Plan p = plan_of(g.M, g.N, g.K, g.a_mn);
-  return p.cg == 2 ? run<2>(g, p, s) : run<1>(g, p, s);
+  return p.cg == 2 ? run_one<2>(g, p, s) : run_one<1>(g, p, s);
+}
+
+cudaError_t launch_gemms(const Gemm& g, const Gemm& h, cudaStream_t s) {
+  const bool both = g.M > 0 && g.N > 0 && h.M > 0 && h.N > 0 && (g.M > kGemvRows || g.a_mn) &&
+                    (h.M > kGemvRows || h.a_mn);
+  if (both) {
+    const Plan p = plan_of(g.M, g.N, g.K, g.a_mn), q = plan_of(h.M, h.N, h.K, h.a_mn);
+    if (p.cg == 1 && q.cg == 1 && p.steps && q.steps && p.workers + q.workers <= kSms) {
+      GemmPair pair{};
+      pair.first = p.workers;
+      cudaError_t e = fill<1>(g, p, &pair.g[0]);
+      if (e == cudaSuccess) e = fill<1>(h, q, &pair.g[1]);
+      if (e == cudaSuccess) e = run_products<1>(pair, p.workers + q.workers, s);
+      if (e == cudaSuccess) e = run_parts<1>(pair.g[0], s);
+      return e == cudaSuccess ? run_parts<1>(pair.g[1], s) : e;
+    }
+  }
+  const cudaError_t e = launch_gemm(g, s);
+  return e == cudaSuccess ? launch_gemm(h, s) : e;
 }
 
 cudaError_t linear_error_word(unsigned** word) {

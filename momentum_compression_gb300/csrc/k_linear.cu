@@ -247,7 +247,7 @@ size_t linear_workspace_bytes(const LinearArgs& a, bool backward) {
   b += up256((size_t)dz_parts(M, N) * N * sizeof(float));
   const size_t p = gemm_partial_bytes(M, K, N, false, !a.w_kn);
   const size_t q = gemm_partial_bytes(wr, wc, M, true, true);
-  return b + up256(p > q ? p : q);
+  return b + up256(p) + up256(q);
 }
 
 cudaError_t launch_linear_fwd(const LinearArgs& a, cudaStream_t s) {
@@ -312,10 +312,7 @@ cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t s) {
   if (a.dx.data) realign(&all, &w, wr, wc, &area);
   if (e == cudaSuccess) e = launch(all, s);
   if (e != cudaSuccess) return e;
-  Gemm g{};
-  g.ep.type = a.type;
-  g.ep.act = OB_ACT_NONE;
-  g.partial = static_cast<float*>(area.take(0));
+  Gemm g{}, h{};
   if (a.dw.data) {  // dw[n][k] = sum over m of dz(m, n) x(m, k), or turned
     g.a = a.w_kn ? x : dz;
     g.b = a.w_kn ? dz : x;
@@ -324,22 +321,23 @@ cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t s) {
     g.N = wc;
     g.K = M;
     g.ep.out = a.dw;
-    g.ep.tiled = tiled(g.ep);
-    e = launch_gemm(g, s);
   }
-  if (e == cudaSuccess && a.dx.data) {  // dx[m][k] = sum over n of dz(m, n) w(n, k)
-    g.a = dz;
-    g.b = w;
-    g.a_mn = 0;
-    g.b_mn = !a.w_kn;
-    g.M = M;
-    g.N = K;
-    g.K = N;
-    g.ep.out = a.dx;
-    g.ep.tiled = tiled(g.ep);
-    e = launch_gemm(g, s);
+  if (a.dx.data) {  // dx[m][k] = sum over n of dz(m, n) w(n, k)
+    h.a = dz;
+    h.b = w;
+    h.b_mn = !a.w_kn;
+    h.M = M;
+    h.N = K;
+    h.K = N;
+    h.ep.out = a.dx;
   }
-  return e;
+  for (Gemm* p : {&g, &h}) {
+    p->ep.type = a.type;
+    p->ep.act = OB_ACT_NONE;
+    p->ep.tiled = tiled(p->ep);
+    p->partial = static_cast<float*>(area.take(gemm_partial_bytes(p->M, p->N, p->K, p->a_mn, p->b_mn)));
+  }
+  return launch_gemms(g, h, s);
 }
 
 }  // namespace ob

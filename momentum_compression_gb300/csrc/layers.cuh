@@ -95,6 +95,8 @@ constexpr int kGemvRows = 8;
 size_t gemv_partial_bytes(int64_t M, int64_t N, int64_t K, bool b_mn);
 cudaError_t launch_gemv(const Gemm& g, cudaStream_t s);
 cudaError_t launch_gemm(const Gemm& g, cudaStream_t s);
+// Two products, in one launch where the card has room for both; their partials are apart.
+cudaError_t launch_gemms(const Gemm& g, const Gemm& h, cudaStream_t s);
 
 constexpr int kAdamBlock = 256;  // elements that share a unit, and the state's grain
 
