@@ -5,6 +5,9 @@
 //                     lane and step, eight of them on their way at once
 //   B stored [K][N]   a lane eight columns; the sum is cut among a block's warps and
 //                     among blocks, whose parts a second kernel adds in their order
+// One row of 2048 by [8192][2048] bf16 takes 9 us (33.5 MB at 3.7 TB/s: half of it the
+// launch and the ramp of one wave), four rows 12, eight 18 (the multiply-adds and what
+// unpacks their operands); [K][N] 10 and 18.  From nine rows on the matrix unit is quicker.
 #include <type_traits>
 
 #include "act.cuh"

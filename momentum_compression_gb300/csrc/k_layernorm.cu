@@ -4,6 +4,13 @@
 //   dw = sum over rows of dy xhat,  db = sum over rows of dy
 // The variance is that of the centred values (a second pass over the row),
 // never a difference of squares.  All sums are fp32.
+//
+// HBM bounds both: 65536 x 2048 bf16 forward 90 us (5.95 TB/s), backward 144 us (5.6
+// TB/s); 16384 x 1024 with a residual, whose arrays partly stay in L2, 23.5 and 31.4 us.
+// One row of 2048 takes 2.4 us forward, the launch.  Rows at odd starts are read and
+// written an element at a time: 4099 x 1001 fp16 9.8 and 20 us, bound by instructions
+// (IPC 2.1 of 4) and the second launch.  Rows wider than the registers hold (forward
+// 16384, backward 8192 columns) are read again for each pass.
 #include <type_traits>
 
 #include "elem.cuh"
