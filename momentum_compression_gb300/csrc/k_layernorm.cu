@@ -9,7 +9,8 @@
 // TB/s); 16384 x 1024 with a residual, whose arrays partly stay in L2, 23.5 and 31.4 us.
 // One row of 2048 takes 2.4 us forward, the launch.  Rows at odd starts are read and
 // written an element at a time: 4099 x 1001 fp16 9.8 and 20 us, bound by instructions
-// (IPC 2.1 of 4) and the second launch.  Rows wider than the registers hold (forward
+// (IPC 2.1 of 4) and the second launch; whole words of global memory shifted into place
+// were no quicker (65536 x 1001 bf16: 132 for 144 us forward, 255 for 167 backward).  Rows wider than the registers hold (forward
 // 16384, backward 8192 columns) are read again for each pass.
 #include <type_traits>
 
@@ -660,10 +661,16 @@ cudaError_t fwd(const LayerNormArgs& a, cudaStream_t s) {
     return go(std::integral_constant<int, 8>());
   }
   const int grid = (int)(a.rows < (uint64_t)kSms * 16 ? a.rows : kSms * 16);
-  const bool few = chunks <= 512 && (a.rows < kSms * 2 || chunks <= 128);
-  const int threads = few ? (chunks + 31) / 32 * 32 : (chunks + 127) / 128 * 32;
-  return few ? launch_behind(k_ln_fwd<T, 1, LIES, true>, dim3(grid), dim3(threads), 0, s, a)
-             : launch_behind(k_ln_fwd<T, 4, LIES, true>, dim3(grid), dim3(threads), 0, s, a);
+  // Chunks a thread: four where there are rows enough (aligned words of a wide row in
+  // flight), as few as the row allows where there are not, and where rows lie anywhere:
+  // element loads want threads (16384 x 2049 bf16: 191 us with four, 82 with one).
+  const bool few = !LIES || a.rows < kSms * 2;
+  const int ch = chunks <= (few ? 512 : 128) ? 1 : !LIES && chunks <= 1024 ? 2 : 4;
+  const dim3 threads((chunks + 32 * ch - 1) / (32 * ch) * 32);
+  if (ch == 1) return launch_behind(k_ln_fwd<T, 1, LIES, true>, dim3(grid), threads, 0, s, a);
+  if constexpr (!LIES)
+    if (ch == 2) return launch_behind(k_ln_fwd<T, 2, LIES, true>, dim3(grid), threads, 0, s, a);
+  return launch_behind(k_ln_fwd<T, 4, LIES, true>, dim3(grid), threads, 0, s, a);
 }
 
 // Threads of a block and of a group (a power of two from 32), and chunks a thread.
