@@ -1187,9 +1187,29 @@ def ob_adamw_step(config, tensors, grads, m, v, counter, m_exp=None, v_exp=None,
                   stream=None):
     """One AdamW step: `config` an ob_adamw, `tensors` an array of ob_adamw_tensor, `grads` as
     many tensors or addresses (None: the tensor stays as it is), on CUDA device `at`."""
+    import torch
+    at = counter.get_device() if at is None else at
     if len(grads) != len(tensors):
         _refuse(f"{len(grads)} gradients for {len(tensors)} tensors")
-    _launch(lib().ob_adamw_step, counter.get_device() if at is None else at, stream,
+    for i, (t, g) in enumerate(zip(tensors, grads)):
+        if hasattr(g, "data_ptr") and (g.numel() != t.n or g.get_device() != at
+                                       or not g.is_contiguous() or _type(g, "grads") != config.grad_type):
+            _refuse(f"grads[{i}] must be a contiguous tensor of {t.n} elements on CUDA device {at} "
+                    "and of the type that config names")
+    blocks = sum(-(-t.n // OB_ADAMW_BLOCK) for t in tensors)
+    bits = config.state_bits
+    dtype = torch.float32 if bits == 32 else torch.uint8
+    for name, t, dtype, n in (("m", m, dtype, blocks * OB_ADAMW_BLOCK),
+                              ("v", v, dtype, blocks * OB_ADAMW_BLOCK),
+                              ("m_exp", m_exp, torch.uint8, blocks), ("v_exp", v_exp, torch.uint8, blocks),
+                              ("counter", counter, torch.float64, 4)):
+        if t is None and bits == 32 and name.endswith("_exp"):
+            continue
+        if t is None or t.dtype != dtype or t.numel() < n or not t.is_contiguous() \
+                or t.get_device() != at:
+            _refuse(f"{name} must be a contiguous {dtype} tensor of {n} elements at least on CUDA "
+                    f"device {at}")
+    _launch(lib().ob_adamw_step, at, stream,
             ct.byref(config), tensors, _ptr_array(grads), len(grads), _ptr(m), _ptr(v), _ptr(m_exp),
             _ptr(v_exp), counter.data_ptr())
 
@@ -1210,12 +1230,23 @@ def ob_adamw_moments(m, v, m_exp, v_exp, m_out, v_out, stream=None):
             v_exp.data_ptr(), n, m_out.data_ptr(), v_out.data_ptr())
 
 
+def _power(b, n):
+    """b^n by the products the device's counter takes, so that a resumed run has its bits."""
+    p = 1.0
+    for _ in range(n):
+        if p * b == p:
+            break
+        p *= b
+    return p
+
+
 class AdamW:
     """AdamW with decoupled weight decay over a list of tensors, which stay where they are:
     the step of parameters that are not compressed (norms, biases, embeddings) or of a
     whole model.  One launch updates up to 128 tensors.
 
-    params: contiguous tensors of float32, bfloat16 or float16 on one device.
+    params: contiguous tensors of float32, bfloat16 or float16 on one device.  Steps go to
+    the memory they have now: assigning other memory to one (`.data`) takes it out.
     weight_decay: a number, or one for each tensor.  state_bits: 32, or 8 for moments of a
     byte an element, rounded stochastically with random numbers named by (seed, step).
     copies: None, or a tensor (or None) for each parameter that gets its new value too, in
@@ -1255,6 +1286,8 @@ class AdamW:
                             "parameter's shape")
             self._table[i] = ob_adamw_tensor(p.data_ptr(), _ptr(c), self._sizes[i], d, _type(p, "params"),
                                              0 if c is None else _type(c, "copies"))
+        # their memory, whatever becomes of the tensors: the table has its addresses
+        self._kept = [t.detach() for t in self.params + self.copies if t is not None]
         # what is written twice in a step is in no order
         spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
                        for t in self.params + [c for c in self.copies if c is not None] if t.numel())
@@ -1284,8 +1317,8 @@ class AdamW:
             self.m_exp = buffer("m_exp", total // OB_ADAMW_BLOCK, torch.uint8)
             self.v_exp = buffer("v_exp", total // OB_ADAMW_BLOCK, torch.uint8)
         b1, b2 = self.betas
-        self.counter = torch.tensor([step, b1 ** step, b2 ** step, 0.0], dtype=torch.float64,
-                                    device=self.device)
+        self.counter = torch.tensor([step, _power(b1, step), _power(b2, step), 0.0],
+                                    dtype=torch.float64, device=self.device)
         self._buffers = tuple(map(_ptr, (self.m, self.v, self.m_exp, self.v_exp, self.counter)))
 
     def _scalar(self, name, t):

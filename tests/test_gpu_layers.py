@@ -496,6 +496,28 @@ def test_adamw_state_goes_on_and_graphs_step():
         assert torch.allclose(a.counter, b.counter, rtol=1e-15, atol=0)
 
 
+def test_adamw_of_a_late_state_and_of_replaced_memory():
+    """A state of some steps goes on with the counter's own bits; a parameter that got other
+    memory keeps it, and the step goes to the memory it was made with."""
+    g = [_gen(8)(700, dtype=BF16)]
+    ps, qs = [torch.ones(700, device="cuda")], [torch.ones(700, device="cuda")]
+    a, b = ob.AdamW(ps, lr=1e-2), ob.AdamW(qs, lr=1e-2)
+    for t in range(50):
+        if t == 43:
+            b = ob.AdamW(qs, lr=1e-2, state=b.state())
+        a.step(g)
+        b.step(g)
+    assert torch.equal(a.counter, b.counter) and torch.equal(ps[0], qs[0])
+    old, new = qs[0].detach(), torch.full((700,), 3.0, device="cuda")
+    at = old.data_ptr()
+    qs[0].data = new
+    del old
+    a.step(g)
+    b.step(g)
+    assert b._kept[0].data_ptr() == at and torch.equal(b._kept[0], ps[0])
+    assert (qs[0] == 3.0).all()
+
+
 # ---------------------------------------------------------------------------
 # Streams and graphs
 # ---------------------------------------------------------------------------

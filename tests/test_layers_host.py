@@ -154,10 +154,34 @@ def test_binding_refuses():
         lambda: ob.AdamW([p, p]), lambda: ob.AdamW([p], copies=[p]), lambda: ob.AdamW([p, p[:5]]),
         lambda: ob.AdamW([p], state=dict(m=p, v=p, step=1)), lambda: ob.AdamW([p], state=dict(step=1)),
     ]
+    # the step's arrays: 300 elements are two blocks of state
+    m, m8, e, c = _zeros(512, dtype=F32), _zeros(512, dtype=torch.uint8), _zeros(2, dtype=torch.uint8), _zeros(4, dtype=torch.float64)
+    table = (ob.ob_adamw_tensor * 1)(ob.ob_adamw_tensor(256, 0, 300, 0.0, ob.OB_TYPE_F32, 0))
+    config = {bits: ob.ob_adamw(bits, ob.OB_TYPE_F32, 0.1, 0.9, 0.99, 1e-8) for bits in (8, 32)}
+
+    def step(bits=32, g=g, m=m, v=m, c=c, **exp):
+        return lambda: ob.ob_adamw_step(config[bits], table, [g], m, v, c, at=0, **exp)
+    calls += [
+        lambda: ob.ob_adamw_step(config[32], table, [g, g], m, m, c), step(g=g[:299]), step(g=g.bfloat16()),
+        step(g=_zeros(300, dtype=F32, at=1)), step(g=_zeros(600, dtype=F32)[::2]), step(m=m[:511]), step(v=m[:511]),
+        step(m=m8), step(v=None), step(c=c[:3]), step(c=m), step(c=_zeros(4, dtype=torch.float64, at=1)),
+        step(8, m=m, v=m8, m_exp=e, v_exp=e), step(8, m=m8, v=m8, m_exp=e), step(8, m=m8, v=m8, m_exp=e[:1], v_exp=e),
+    ]
     for i, call in enumerate(calls):
         with pytest.raises(ob.OBError) as e:
             call()
         assert e.value.status in (BAD, UNSUPPORTED), i
+
+
+@pytest.mark.parametrize("b", [0.0, 0.5, 0.9, 0.95, 0.999, 1 - 2 ** -40])
+def test_powers_are_products(b):
+    """A resumed optimizer starts from the bits that the device's products have come to."""
+    want, powers = 1.0, {}
+    for t in range(20001):
+        powers[t] = want
+        want *= b
+    for t in (0, 1, 2, 4, 43, 1000, 6600, 7200, 20000):
+        assert ob._power(b, t) == powers[t], t
 
 
 def test_reference_gradients_against_differences():
