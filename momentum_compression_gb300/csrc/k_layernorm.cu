@@ -237,22 +237,31 @@ __device__ __forceinline__ void with_type(int type, F f) {
     f(__half());
 }
 
-// A row a warp (MULTI false, eight rows a block) or a row a block.  The row stays as it
-// lies in memory, two elements a register, and is unpacked again for each pass.
-template <typename T, int CH, int LIES, bool MULTI>
-__global__ void __launch_bounds__(MULTI ? 512 : 256, MULTI || CH == 8 ? 2 : 3)
+// A row to LANES lanes of a warp (256 threads a block), or to a block (LANES 0).  The row
+// stays as it lies in memory, two elements a register, and is unpacked again for each pass.
+template <typename T, int CH, int LIES, int LANES>
+__global__ void __launch_bounds__(LANES ? 256 : 512, !LANES || CH == 8 ? 2 : 3)
     k_ln_fwd(const __grid_constant__ LayerNormArgs a) {
   __shared__ float buf[33];
-  const int threads = MULTI ? blockDim.x : 32, t = MULTI ? threadIdx.x : threadIdx.x & 31;
-  const uint64_t first = MULTI ? blockIdx.x : (uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const uint64_t step = MULTI ? gridDim.x : (uint64_t)gridDim.x * 8;
+  constexpr int kRows = LANES ? 32 / LANES : 1;  // of a warp
+  const int threads = LANES ? LANES : blockDim.x, t = threadIdx.x & (LANES ? LANES - 1 : ~0);
+  const uint64_t first = LANES ? ((uint64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kRows : blockIdx.x;
+  const uint64_t step = LANES ? (uint64_t)gridDim.x * 8 * kRows : gridDim.x;
   auto row_sum = [&](uint64_t v) {
     float lo, hi;
     unpair(v, &lo, &hi);
-    return MULTI ? block_sum(lo + hi, buf) : warp_butterfly_sum(lo + hi);
+    if (!LANES) return block_sum(lo + hi, buf);
+    float sum = lo + hi;
+#pragma unroll
+    for (int o = LANES / 2; o >= 1; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
   };
   grid_wait();
-  for (uint64_t row = first; row < a.rows; row += step) {
+  for (uint64_t from = first; from < a.rows; from += step) {
+    // lanes without a row go through the last one, and keep nothing
+    uint64_t row = from + (kRows > 1 ? (threadIdx.x & 31) / LANES : 0);
+    const bool real = kRows == 1 || row < a.rows;
+    if (!real) row = a.rows - 1;
     const T* x = static_cast<const T*>(a.x) + row * a.ldx;
     Chunk<T, LIES> in[CH];
 #pragma unroll
@@ -270,7 +279,7 @@ __global__ void __launch_bounds__(MULTI ? 512 : 256, MULTI || CH == 8 ? 2 : 3)
 #pragma unroll
         for (int j = 0; j < 4; ++j) p[j] = add2(p[j], q[j]);
         in[c].put(p);  // the sum as it is kept
-        if (a.sum) in[c].store(static_cast<T*>(a.sum) + row * a.lds, c, t, threads, a.cols);
+        if (a.sum && real) in[c].store(static_cast<T*>(a.sum) + row * a.lds, c, t, threads, a.cols);
       }
     }
     uint64_t total = 0;
@@ -325,23 +334,23 @@ __global__ void __launch_bounds__(MULTI ? 512 : 256, MULTI || CH == 8 ? 2 : 3)
           for (int j = 0; j < 4; ++j) v[j] = add2(v[j], w[j]);
         }
         in[c].put(v);
-        in[c].store(y, c, t, threads, a.cols);
+        if (real) in[c].store(y, c, t, threads, a.cols);
       }
     });
-    if (t == 0) {
+    if (t == 0 && real) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
     }
   }
 }
 
-// The sums over a warp of N = 2 R values each lane has, N a power of two up to 8: halves
-// of the values change sides first, so that N + log2(32 / N) - 1 exchanges do.  Value
-// lane / (32 / N) is returned.
-template <int N>
-__device__ __forceinline__ float warp_sums(float (&v)[N]) {
+// The sums over LANES lanes of N = 2 R values each lane has, N a power of two up to 8:
+// halves of the values change sides first, so that N + log2(LANES / N) - 1 exchanges do.
+// Value lane % LANES / (LANES / N) is returned.
+template <int N, int LANES>
+__device__ __forceinline__ float lane_sums(float (&v)[N]) {
   const int lane = threadIdx.x & 31;
-  int o = 16;
+  int o = LANES / 2;
 #pragma unroll
   for (int n = N / 2; n >= 1; n /= 2, o /= 2) {
     const bool up = lane & o;
@@ -521,12 +530,22 @@ __global__ void __launch_bounds__(kBwdThreads + 32, kBwdThreads == 256 ? 2 : 1)
       }
     bool fine = ok;
     if (a.dx) {
-      const float mine = warp_sums<N>(sums);
       float m[N];
-      if (threads == 32) {
+      auto within = [&](auto lanes) {  // a group of lanes of one warp
+        constexpr int LANES = decltype(lanes)::value;
+        const float mine = lane_sums<N, LANES>(sums);
 #pragma unroll
-        for (int k = 0; k < N; ++k) m[k] = __shfl_sync(0xffffffffu, mine, k * (32 / N)) * inv;
+        for (int k = 0; k < N; ++k)
+          m[k] = __shfl_sync(0xffffffffu, mine, (lane & ~(LANES - 1)) + k * (LANES / N)) * inv;
+      };
+      if (kBwdThreads == 256 && threads == 8) {
+        within(std::integral_constant<int, 8>());
+      } else if (kBwdThreads == 256 && threads == 16) {
+        within(std::integral_constant<int, 16>());
+      } else if (threads == 32) {
+        within(std::integral_constant<int, 32>());
       } else {
+        const float mine = lane_sums<N, 32>(sums);
         if ((lane & (32 / N - 1)) == 0) part[flip][warp][lane / (32 / N)] = mine;
         fine = !named_sync_or(1 + group, threads, !ok);
 #pragma unroll
@@ -646,19 +665,25 @@ cudaError_t fwd(const LayerNormArgs& a, cudaStream_t s) {
   // where the rows alone do not fill the card, or a warp's registers do not last.
   constexpr int kWarpMost = !LIES ? 2 : sizeof(T) == 4 ? 4 : 8;  // chunks of a lane
   if (chunks <= 32 * kWarpMost && (chunks <= 32 || a.rows >= (uint64_t)kSms * 8)) {
-    const uint64_t blocks = (a.rows + 7) / 8;
-    const int grid = (int)(blocks < (uint64_t)kSms * 32 ? blocks : kSms * 32);
-    auto go = [&](auto ch) {
+    auto go = [&](auto ch, auto lanes) {
       constexpr int CH = decltype(ch)::value <= kWarpMost ? decltype(ch)::value : kWarpMost;
-      if (LIES && a.cols == CH * 256)
-        return launch_behind(k_ln_fwd<T, CH, LIES ? 2 : 0, false>, dim3(grid), dim3(256), 0, s, a);
-      return launch_behind(k_ln_fwd<T, CH, LIES, false>, dim3(grid), dim3(256), 0, s, a);
+      constexpr int LANES = decltype(lanes)::value;
+      const uint64_t per = 256 / LANES, blocks = (a.rows + per - 1) / per;
+      const dim3 grid((unsigned)(blocks < (uint64_t)kSms * 32 ? blocks : kSms * 32));
+      if (LIES && a.cols == CH * LANES * 8)
+        return launch_behind(k_ln_fwd<T, CH, LIES ? 2 : 0, LANES>, grid, dim3(256), 0, s, a);
+      return launch_behind(k_ln_fwd<T, CH, LIES, LANES>, grid, dim3(256), 0, s, a);
     };
-    if (chunks <= 32) return go(std::integral_constant<int, 1>());
-    if (chunks <= 64) return go(std::integral_constant<int, 2>());
-    if (chunks <= 96 && LIES) return go(std::integral_constant<int, 3>());
-    if (chunks <= 128) return go(std::integral_constant<int, 4>());
-    return go(std::integral_constant<int, 8>());
+    constexpr auto all = std::integral_constant<int, 32>();
+    // Narrow rows, a head's for one, share a warp (400000 x 64 bf16: 93 us with a warp each,
+    // 30 so; backward 98 and 36).
+    if (chunks <= 8) return go(std::integral_constant<int, 1>(), std::integral_constant<int, 8>());
+    if (chunks <= 16) return go(std::integral_constant<int, 1>(), std::integral_constant<int, 16>());
+    if (chunks <= 32) return go(std::integral_constant<int, 1>(), all);
+    if (chunks <= 64) return go(std::integral_constant<int, 2>(), all);
+    if (chunks <= 96 && LIES) return go(std::integral_constant<int, 3>(), all);
+    if (chunks <= 128) return go(std::integral_constant<int, 4>(), all);
+    return go(std::integral_constant<int, 8>(), all);
   }
   const int grid = (int)(a.rows < (uint64_t)kSms * 16 ? a.rows : kSms * 16);
   // Chunks a thread: four where there are rows enough (aligned words of a wide row in
@@ -667,23 +692,23 @@ cudaError_t fwd(const LayerNormArgs& a, cudaStream_t s) {
   const bool few = !LIES || a.rows < kSms * 2;
   const int ch = chunks <= (few ? 512 : 128) ? 1 : !LIES && chunks <= 1024 ? 2 : 4;
   const dim3 threads((chunks + 32 * ch - 1) / (32 * ch) * 32);
-  if (ch == 1) return launch_behind(k_ln_fwd<T, 1, LIES, true>, dim3(grid), threads, 0, s, a);
+  if (ch == 1) return launch_behind(k_ln_fwd<T, 1, LIES, 0>, dim3(grid), threads, 0, s, a);
   if constexpr (!LIES)
-    if (ch == 2) return launch_behind(k_ln_fwd<T, 2, LIES, true>, dim3(grid), threads, 0, s, a);
-  return launch_behind(k_ln_fwd<T, 4, LIES, true>, dim3(grid), threads, 0, s, a);
+    if (ch == 2) return launch_behind(k_ln_fwd<T, 2, LIES, 0>, dim3(grid), threads, 0, s, a);
+  return launch_behind(k_ln_fwd<T, 4, LIES, 0>, dim3(grid), threads, 0, s, a);
 }
 
-// Threads of a block and of a group (a power of two from 32), and chunks a thread.
+// Threads of a block and of a group (a power of two from 8), and chunks a thread.
 int block_threads(int cols) { return cols <= 256 * 8 ? 256 : 512; }
 int row_chunks(int cols) { return cols <= 512 * 8 ? 1 : 2; }
 int group_threads(int cols) {
-  int t = 32;
+  int t = 8;
   while (t * 8 * row_chunks(cols) < cols) t *= 2;
   return t;
 }
 
 // Bytes of shared memory for the rows: two blocks an SM, or one.
-constexpr uint32_t ring_most(int threads) { return threads == 256 ? 98304 : 196608; }
+constexpr uint32_t ring_most(int threads) { return threads == 256 ? 104448 : 196608; }
 
 template <typename T, int kBwdThreads, int CH, int R, int LIES>
 cudaError_t bwd_launch(const LayerNormBwdArgs& a, cudaStream_t s) {
