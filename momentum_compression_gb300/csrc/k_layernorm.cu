@@ -666,24 +666,29 @@ cudaError_t fwd(const LayerNormArgs& a, cudaStream_t s) {
   constexpr int kWarpMost = !LIES ? 2 : sizeof(T) == 4 ? 4 : 8;  // chunks of a lane
   if (chunks <= 32 * kWarpMost && (chunks <= 32 || a.rows >= (uint64_t)kSms * 8)) {
     auto go = [&](auto ch, auto lanes) {
-      constexpr int CH = decltype(ch)::value <= kWarpMost ? decltype(ch)::value : kWarpMost;
-      constexpr int LANES = decltype(lanes)::value;
+      constexpr int CH = decltype(ch)::value, LANES = decltype(lanes)::value;
       const uint64_t per = 256 / LANES, blocks = (a.rows + per - 1) / per;
       const dim3 grid((unsigned)(blocks < (uint64_t)kSms * 32 ? blocks : kSms * 32));
       if (LIES && a.cols == CH * LANES * 8)
         return launch_behind(k_ln_fwd<T, CH, LIES ? 2 : 0, LANES>, grid, dim3(256), 0, s, a);
       return launch_behind(k_ln_fwd<T, CH, LIES, LANES>, grid, dim3(256), 0, s, a);
     };
-    constexpr auto all = std::integral_constant<int, 32>();
-    // Narrow rows, a head's for one, share a warp (400000 x 64 bf16: 93 us with a warp each,
-    // 30 so; backward 98 and 36).
-    if (chunks <= 8) return go(std::integral_constant<int, 1>(), std::integral_constant<int, 8>());
-    if (chunks <= 16) return go(std::integral_constant<int, 1>(), std::integral_constant<int, 16>());
-    if (chunks <= 32) return go(std::integral_constant<int, 1>(), all);
-    if (chunks <= 64) return go(std::integral_constant<int, 2>(), all);
-    if (chunks <= 96 && LIES) return go(std::integral_constant<int, 3>(), all);
-    if (chunks <= 128) return go(std::integral_constant<int, 4>(), all);
-    return go(std::integral_constant<int, 8>(), all);
+#define LN_ROWS(CH, LANES) go(std::integral_constant<int, CH>(), std::integral_constant<int, LANES>())
+    // Narrow rows share a warp, so that a lane has two or three loads under way: 400000 x
+    // 64 bf16 takes 93 us with a warp each, 30 with eight lanes and 22 with four; 200000 x
+    // 256 50 and 40, 100000 x 384 42 and 32.  Four loads take longer where rows are few.
+    if (chunks <= 8) return LN_ROWS(2, 4);
+    if (chunks <= 16) return LN_ROWS(2, 8);
+    if (chunks <= 32) return LN_ROWS(2, 16);
+    if constexpr (LIES != 0)
+      if (chunks <= 48) return LN_ROWS(3, 16);
+    if (chunks <= 64) return LN_ROWS(2, 32);
+    if constexpr (LIES != 0) {
+      if (chunks <= 96) return LN_ROWS(3, 32);
+      if (chunks <= 128) return LN_ROWS(4, 32);
+      if constexpr (kWarpMost == 8) return LN_ROWS(8, 32);
+    }
+#undef LN_ROWS
   }
   const int grid = (int)(a.rows < (uint64_t)kSms * 16 ? a.rows : kSms * 16);
   // Chunks a thread: four where there are rows enough (aligned words of a wide row in

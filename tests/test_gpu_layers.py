@@ -60,7 +60,8 @@ def _guarded(rows, cols, pad, shift, dtype):
 SHAPES = [(1, 1), (1, 8), (3, 7), (2, 33), (5, 64), (1, 768), (37, 768), (9, 1001), (300, 1024),
           (2, 2048), (1, 2048), (65, 2050), (7, 4096), (4, 5000), (3, 8192), (2, 12345), (1, 16384),
           (2, 40000), (700, 128), (5000, 24), (1300, 520), (400, 1500),
-          (305, 4096), (310, 9000), (3001, 64), (1001, 100)]
+          (305, 4096), (310, 9000), (3001, 64), (1001, 100),
+          (901, 384), (1300, 300)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
