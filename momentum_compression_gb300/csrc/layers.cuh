@@ -87,13 +87,12 @@ struct Gemm {
   float* partial;            // gemm_partial_bytes
 };
 
-// By sizes and a_mn, b_mn alone.
-size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool a_mn, bool b_mn);
-// Up to this many rows of A, stored [M][K], a product is bound by B's way through the memory
-// and has kernels of its own (k_gemv.cu).
-constexpr int kGemvRows = 8;
-size_t gemv_partial_bytes(int64_t M, int64_t N, int64_t K, bool b_mn);
-cudaError_t launch_gemv(const Gemm& g, cudaStream_t s);
+// By sizes and a_mn alone.
+size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool a_mn);
+// Whether a product has so few rows of A, stored [M][K], that B's way through the memory
+// bounds it: it has a kernel of its own (k_few.cu).
+bool few_rows(int64_t M, int64_t N, int64_t K, bool a_mn);
+cudaError_t launch_few(const Gemm& g, cudaStream_t s);
 cudaError_t launch_gemm(const Gemm& g, cudaStream_t s);
 // Two products, in one launch where the card has room for both; their partials are apart.
 cudaError_t launch_gemms(const Gemm& g, const Gemm& h, cudaStream_t s);

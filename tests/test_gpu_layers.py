@@ -167,7 +167,8 @@ def test_layer_norm_of_constant_far_and_special_rows():
 DENSE = [(1, 1, 1), (1, 64, 64), (1, 1000, 333), (2, 40, 8), (3, 129, 257), (8, 512, 1024),
          (9, 300, 70), (16, 8, 16), (17, 256, 512), (33, 65, 1), (64, 1, 100), (100, 200, 300),
          (127, 128, 129), (128, 256, 64), (129, 257, 65), (250, 768, 96), (256, 256, 256),
-         (257, 511, 513), (300, 64, 2000), (513, 1024, 320), (19500, 100, 1100), (1000, 136, 1000), (777, 1301, 1001)]
+         (257, 511, 513), (300, 64, 2000), (513, 1024, 320), (19500, 100, 1100), (1000, 136, 1000), (777, 1301, 1001),
+         (1, 300, 5003), (5, 300, 2100), (16, 1000, 5003), (30, 264, 4104), (32, 40, 8195)]
 
 
 def _dense_case(Mr, N, K, dtype, kn, pad, shift, seed=0):
