@@ -256,10 +256,15 @@ cudaError_t go(const Gemm& g, cudaStream_t s) {
 }  // namespace
 
 // Up to 16 rows this is the quicker way for any B (16 x 8192 x 2048 bf16: 10.5 us, 13.4 on
-// tiles of the matrix unit; 32: 17.8 and 13.5), up to 32 for a B of 16 MB at most (32 x 4096
-// x 1024: 5.8 and 8.6).
-bool few_rows(int64_t M, int64_t N, int64_t K, bool a_mn) {
-  return !a_mn && (M <= 16 || (M <= 32 && N * K <= 1 << 23));
+// tiles of the matrix unit), up to 128 where what is read, B for every 16 rows, is less than
+// the tiles' start and end are worth: 64 x 2048 x 1024 5.4 and 8.3 us, 48 x 4096 x 1024
+// 9.6 and 8.3; and twice as much along a long sum, which the tiles cut and join: 64 x 1024 x
+// 4096 10.7 and 16.2, 32 x 2048 x 4096 11.3 and 18.2.
+// Where a backward pass can put both products in one launch, those with a short sum stay on
+// the tiles from 17 rows on (128 x 768 x 768: 12.2 us together, 15.6 apart).
+bool few_rows(int64_t M, int64_t N, int64_t K, bool a_mn, bool pair) {
+  if (a_mn || M > 128 || (M > 16 && pair && K < 2048)) return false;
+  return M <= 16 || (M + 15) / 16 * N * K <= (K < 2048 ? 1 << 23 : 1 << 24);
 }
 
 cudaError_t launch_few(const Gemm& g, cudaStream_t s) {

@@ -784,9 +784,9 @@ cudaError_t run_one(const Gemm& g, const Plan& p, cudaStream_t s) {
 
 }  // namespace
 
-size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool a_mn) {
+size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool a_mn, bool pair) {
   if (M == 0 || N == 0) return 0;
-  if (few_rows(M, N, K, a_mn)) return 0;
+  if (few_rows(M, N, K, a_mn, pair)) return 0;
   const Plan p = plan_of(M, N, K, a_mn);
   if (p.whole == p.tiles_m * p.tiles_n || !p.steps) return 0;
   return (size_t)p.workers * 2 * (128 * p.cg) * (128 * p.cg) * sizeof(float);
@@ -794,13 +794,13 @@ size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool a_mn) {
 
 cudaError_t launch_gemm(const Gemm& g, cudaStream_t s) {
   if (g.M == 0 || g.N == 0) return cudaSuccess;
-  if (few_rows(g.M, g.N, g.K, g.a_mn)) return launch_few(g, s);
+  if (few_rows(g.M, g.N, g.K, g.a_mn, g.pair)) return launch_few(g, s);
   const Plan p = plan_of(g.M, g.N, g.K, g.a_mn);
   return p.cg == 2 ? run_one<2>(g, p, s) : run_one<1>(g, p, s);
 }
 
 cudaError_t launch_gemms(const Gemm& g, const Gemm& h, cudaStream_t s) {
-  auto tiled = [](const Gemm& p) { return p.M > 0 && p.N > 0 && !few_rows(p.M, p.N, p.K, p.a_mn); };
+  auto tiled = [](const Gemm& p) { return p.M > 0 && p.N > 0 && !few_rows(p.M, p.N, p.K, p.a_mn, p.pair); };
   const bool both = tiled(g) && tiled(h);
   if (both) {
     const Plan p = plan_of(g.M, g.N, g.K, g.a_mn), q = plan_of(h.M, h.N, h.K, h.a_mn);

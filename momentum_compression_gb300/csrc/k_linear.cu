@@ -244,11 +244,11 @@ cudaError_t make_dz(const DzArgs& d, bool wide, cudaStream_t s) {
 size_t linear_workspace_bytes(const LinearArgs& a, bool backward) {
   const int64_t M = a.M, N = a.N, K = a.K, wr = a.w_kn ? K : N, wc = a.w_kn ? N : K;
   size_t b = a.unaligned ? mat_bytes(M, K) + mat_bytes(wr, wc) : 0;
-  if (!backward) return b + up256(gemm_partial_bytes(M, N, K, false));
+  if (!backward) return b + up256(gemm_partial_bytes(M, N, K, false, false));
   if (a.act != OB_ACT_NONE || a.unaligned) b += mat_bytes(M, N);
   b += up256((size_t)dz_parts(M, N) * N * sizeof(float));
-  const size_t p = gemm_partial_bytes(M, K, N, false);
-  const size_t q = gemm_partial_bytes(wr, wc, M, true);
+  const size_t p = gemm_partial_bytes(M, K, N, false, true);
+  const size_t q = gemm_partial_bytes(wr, wc, M, true, true);
   return b + up256(p) + up256(q);
 }
 
@@ -336,8 +336,9 @@ cudaError_t launch_linear_bwd(const LinearArgs& a, cudaStream_t s) {
   for (Gemm* p : {&g, &h}) {
     p->ep.type = a.type;
     p->ep.act = OB_ACT_NONE;
+    p->pair = 1;
     p->ep.tiled = tiled(p->ep);
-    p->partial = static_cast<float*>(area.take(gemm_partial_bytes(p->M, p->N, p->K, p->a_mn)));
+    p->partial = static_cast<float*>(area.take(gemm_partial_bytes(p->M, p->N, p->K, p->a_mn, p->pair)));
   }
   return launch_gemms(g, h, s);
 }

@@ -83,15 +83,16 @@ struct Gemm {
   Mat a, b;
   int a_mn, b_mn;            // stored [K][M] or [K][N] instead of [M][K] or [N][K]
   int64_t M, N, K;
+  int pair;                  // one of launch_gemms' two
   Epilogue ep;
   float* partial;            // gemm_partial_bytes
 };
 
-// By sizes and a_mn alone.
-size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool a_mn);
+// By sizes, a_mn and pair alone.
+size_t gemm_partial_bytes(int64_t M, int64_t N, int64_t K, bool a_mn, bool pair);
 // Whether a product has so few rows of A, stored [M][K], that B's way through the memory
 // bounds it: it has a kernel of its own (k_few.cu).
-bool few_rows(int64_t M, int64_t N, int64_t K, bool a_mn);
+bool few_rows(int64_t M, int64_t N, int64_t K, bool a_mn, bool pair);
 cudaError_t launch_few(const Gemm& g, cudaStream_t s);
 cudaError_t launch_gemm(const Gemm& g, cudaStream_t s);
 // Two products, in one launch where the card has room for both; their partials are apart.
