@@ -610,6 +610,29 @@ print("fine")
 """
 
 
+@pytest.mark.parametrize("kn", [False, True])
+def test_few_rows_in_a_graph_and_on_two_streams(kn):
+    """Products whose blocks share a sum: replays and calls side by side give the call's bits."""
+    mk = _gen(12)
+    x, w, b = mk(5, 4096, dtype=BF16), mk(4096, 1024, dtype=BF16), mk(1024, dtype=BF16)
+    w = w if kn else w.t().contiguous().t()
+    want = torch.empty(5, 1024, device="cuda", dtype=BF16)
+    ob.ob_linear_fwd(x, w.t(), want, b, activation="gelu")
+    y = [torch.zeros_like(want) for _ in range(3)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ob.ob_linear_fwd(x, w.t(), y[0], b, activation="gelu")
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        graph.replay()
+        for s, out in zip(streams, y[1:]):
+            ob.ob_linear_fwd(x, w.t(), out, b, activation="gelu", stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want) for t in y)
+    assert ob.ob_layer_device_error() == 0
+
+
 @pytest.mark.parametrize("what", ["dense", "attention"])
 def test_first_call_of_a_thread(what):
     """A thread that has done nothing on the GPU yet, as autograd's."""
