@@ -193,6 +193,7 @@ int power_of_two(int64_t n, int most) {
 // Blocks along the rows of dz, by sizes alone (the workspace goes by it): eight
 // rows a thread at least, and all that run at a time.
 int dz_parts(int64_t M, int64_t N) {
+  if (N == 0) return 1;
   const int tx = power_of_two((N + 7) / 8, kDzThreads);
   const int64_t columns = (N + 8 * tx - 1) / (8 * tx), rows = 8 * (kDzThreads / tx);
   int64_t most = kDzBlocks * 152 / columns;
