@@ -1087,7 +1087,7 @@ _PAIRS = {n: ct.c_int64 * (2 * n) for n in (5, 6)}
 
 
 def _linear_call(fn, at, l, backward, like, workspace, stream, pairs, order):
-    """fn with the matrices of `pairs` (by their place, None: no matrix) and vectors in `order`."""
+    """fn with the matrices of `pairs` by their place (None: there is none) and vectors in `order`."""
     if workspace is None:
         nbytes = ob_linear_workspace_bytes(*l, backward)
         workspace = _scratch(nbytes, like, stream) if nbytes else None
@@ -1096,8 +1096,7 @@ def _linear_call(fn, at, l, backward, like, workspace, stream, pairs, order):
     mats = _PAIRS[len(pairs) // 2](*pairs)
     base = ct.addressof(mats)
     _launch(fn, at, stream, _LINEAR.pack(*l),
-            *[i[0] if i.__class__ is tuple else base + 16 * i if pairs[2 * i + 1] else None
-              for i in order],
+            *[None if i is None else i[0] if i.__class__ is tuple else base + 16 * i for i in order],
             _ptr(workspace) or None,
             0 if workspace is None else workspace.numel() * workspace.element_size())
 
@@ -1126,9 +1125,8 @@ def ob_linear_fwd(x, w, y, bias=None, residual=None, z=None, activation="none", 
     l = (type_, _activation(activation), kn, off, M, N, K)
     if not M or not N:
         return
-    if not K:
-        pairs[1] = pairs[3] = 1  # empty, but there
-    _linear_call(lib().ob_linear_fwd, at, l, 0, x, workspace, stream, pairs, (0, 1, (pb,), 3, 4, 2))
+    _linear_call(lib().ob_linear_fwd, at, l, 0, x, workspace, stream, pairs,
+                 (0, 1, (pb,), None if residual is None else 3, None if z is None else 4, 2))
 
 
 def ob_linear_bwd(dy, x, w, dx=None, dw=None, dbias=None, z=None, activation="none",
@@ -1165,7 +1163,7 @@ def ob_linear_bwd(dy, x, w, dx=None, dw=None, dbias=None, z=None, activation="no
         if t is not None and not pairs[2 * i + 1]:
             pairs[2 * i + 1] = 1  # empty, but there
     _linear_call(lib().ob_linear_bwd, at, l, 1, dy, workspace, stream, pairs,
-                 (0, 1, 2, 3, 4, 5, (pb,)))
+                 (0, 1, 2, 3 if act else None, None if dx is None else 4, None if dw is None else 5, (pb,)))
 
 
 def ob_layer_device_error(stream=None):

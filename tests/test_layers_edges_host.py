@@ -5,9 +5,13 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 import momentum_compression_gb300 as ob
+from test_model_binding import _zeros, library  # noqa: F401
 
+BF16, F32 = torch.bfloat16, torch.float32
+BAD = ob.OB_ERR_INVALID
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -36,3 +40,32 @@ def test_workspaces_of_sizes_of_zero():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", SIZES], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "fine", (r.returncode, r.stderr[-2000:])
+
+
+def _refused(call, name):
+    with pytest.raises(ob.OBError) as e:
+        call()
+    assert e.value.status == BAD and name in str(e.value), str(e.value)
+
+
+def test_dense_forward_refuses_strides_of_zero(library):  # noqa: F811
+    """A residual that is one row for all of them is not left out, nor a z."""
+    x, w, y = _zeros(4, 64), _zeros(32, 64), _zeros(4, 32)
+    for row in (_zeros(32), _zeros(1, 32)):
+        _refused(lambda: ob.ob_linear_fwd(x, w, y, residual=row.expand(4, 32)), "residual")
+        _refused(lambda: ob.ob_linear_fwd(x, w, y, z=row.expand(4, 32)), "z")
+        _refused(lambda: ob.ob_linear_fwd(x, w, row.expand(4, 32)), "y")
+    _refused(lambda: ob.ob_linear_fwd(_zeros(64).expand(4, 64), w, y), "x")
+    _refused(lambda: ob.ob_linear_fwd(x, _zeros(64).expand(32, 64), y), "w")
+    _refused(lambda: ob.ob_linear_fwd(x, _zeros(32).expand(64, 32).t(), y), "w")
+    one = _zeros(4, 1)
+    _refused(lambda: ob.ob_linear_fwd(x, w[:1], one, residual=_zeros(1, 1).expand(4, 1)), "residual")
+    # of one row the stride is no matter
+    calls = []
+    library.ob_linear_fwd = lambda *a: calls.append(a) or ob.OB_OK
+    ob.ob_linear_fwd(x[:1], w, y[:1], residual=_zeros(32).expand(1, 32))
+    ob.ob_linear_fwd(x, w, y)
+    ob.ob_linear_fwd(x[:, :0], w[:, :0], y, z=_zeros(4, 32))
+    given = [[p is not None for p in c[1:7]] for c in calls]  # x, w, bias, residual, z, y
+    assert given == [[True, True, False, True, False, True], [True, True, False, False, False, True],
+                     [True, True, False, False, True, True]]
