@@ -1159,9 +1159,6 @@ def ob_linear_bwd(dy, x, w, dx=None, dw=None, dbias=None, z=None, activation="no
         if bt != type_:
             _refuse("dbias must have the type of dy")
     l = (type_, act, kn, off, M, N, K)
-    for i, t in enumerate((dy, x, w, z if act else None, dx, dw)):
-        if t is not None and not pairs[2 * i + 1]:
-            pairs[2 * i + 1] = 1  # empty, but there
     _linear_call(lib().ob_linear_bwd, at, l, 1, dy, workspace, stream, pairs,
                  (0, 1, 2, 3 if act else None, None if dx is None else 4, None if dw is None else 5, (pb,)))
 

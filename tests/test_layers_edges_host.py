@@ -69,3 +69,33 @@ def test_dense_forward_refuses_strides_of_zero(library):  # noqa: F811
     given = [[p is not None for p in c[1:7]] for c in calls]  # x, w, bias, residual, z, y
     assert given == [[True, True, False, True, False, True], [True, True, False, False, False, True],
                      [True, True, False, False, True, True]]
+
+
+@pytest.mark.parametrize("at", ["2", "3"])
+def test_dense_backward_refuses_strides_of_zero(library, at):  # noqa: F811
+    """One element that stands for a column of them is not read as if they lay there."""
+    def column(n):
+        one = _zeros(1, 1)
+        return one.expand(n, 1) if at == "2" else one.view(1, 1, 1).expand(2, n // 2, 1)
+    x, w, dy = _zeros(4, 64), _zeros(1, 64), _zeros(4, 1)
+    x, dy = (x, dy) if at == "2" else (x.view(2, 2, 64), dy.view(2, 2, 1))
+    dx, dw, act = torch.zeros_like(x), torch.zeros_like(w), dict(z=dy, activation="gelu")
+    bwd = ob.ob_linear_bwd
+    _refused(lambda: bwd(column(4), x, w, dx=dx), "dy")
+    _refused(lambda: bwd(column(4), x, w, dbias=_zeros(1)), "dy")
+    _refused(lambda: bwd(dy, x, w, dx=dx, z=column(4), activation="gelu"), "z")
+    x, w = dy, _zeros(1, 1)  # one column of x
+    _refused(lambda: bwd(dy, column(4), w, dw=w, **act), "x")
+    _refused(lambda: bwd(dy, x, w, dx=column(4), **act), "dx")
+    w, dy = _zeros(8, 1), (_zeros(4, 8) if at == "2" else _zeros(2, 2, 8))
+    _refused(lambda: bwd(dy, x, _zeros(1, 1).expand(8, 1), dx=x), "w")
+    _refused(lambda: bwd(dy, x, w, dw=_zeros(1, 1).expand(8, 1)), "dw")
+    wide = _zeros(8)
+    wide = wide.expand(4, 8) if at == "2" else wide.expand(2, 2, 8)
+    _refused(lambda: bwd(wide, x, w, dx=x), "dy")
+    # what is empty has no rows to be apart
+    calls = []
+    library.ob_linear_bwd = lambda *a: calls.append(a) or ob.OB_OK
+    bwd(dy, dy[..., :0], _zeros(8, 0), dx=dy[..., :0], dw=_zeros(8, 0), dbias=_zeros(8))
+    bwd(dy[..., :0], x, _zeros(0, 1), dx=x, dw=_zeros(0, 1), dbias=_zeros(0))
+    assert all([p is not None for p in c[1:7]] == [True, True, True, False, True, True] for c in calls) and calls
