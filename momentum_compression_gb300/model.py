@@ -108,7 +108,7 @@ class _Attention(torch.autograd.Function):
         q, k, v = _inner(q), _inner(k), _inner(v)
         o = torch.empty(q.shape, device=q.device, dtype=q.dtype)
         B, Lq, H, _ = q.shape
-        lse = torch.empty(B, H, Lq, device=q.device)
+        lse = torch.empty(B, H, Lq, device=q.device, dtype=torch.float32)
         ob_attn_fwd(q, k, v, o, lse, table=table, kv_len=kv_len, **kw)
         ctx.save_for_backward(q, k, v, o, lse, table, kv_len)
         ctx.kw = kw
@@ -147,7 +147,7 @@ class _LayerNorm(torch.autograd.Function):
         mean = rstd = None
         if train:
             rows = x.numel() // x.shape[-1] if x.shape[-1] else 0
-            mean, rstd = (torch.empty(rows, device=x.device) for _ in range(2))
+            mean, rstd = (torch.empty(rows, device=x.device, dtype=torch.float32) for _ in range(2))
         ob_layernorm_fwd(x, y, weight=weight, bias=bias, eps=eps, residual=residual, sum=s,
                          mean=mean, rstd=rstd)
         ctx.has_residual, ctx.bias = residual is not None, bias is not None

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import momentum_compression_gb300 as ob
+from momentum_compression_gb300 import model as M
 from test_model_binding import _zeros, library  # noqa: F401
 
 BF16, F32 = torch.bfloat16, torch.float32
@@ -99,3 +100,32 @@ def test_dense_backward_refuses_strides_of_zero(library, at):  # noqa: F811
     bwd(dy, dy[..., :0], _zeros(8, 0), dx=dy[..., :0], dw=_zeros(8, 0), dbias=_zeros(8))
     bwd(dy[..., :0], x, _zeros(0, 1), dx=x, dw=_zeros(0, 1), dbias=_zeros(0))
     assert all([p is not None for p in c[1:7]] == [True, True, True, False, True, True] for c in calls) and calls
+
+
+@pytest.fixture
+def recorded(library, monkeypatch):  # noqa: F811
+    """The recording library for model.py: its calls by name, and tensors of torch's default type
+    where none is asked for."""
+    calls = {}
+    for n in ("ob_layernorm_fwd", "ob_layernorm_bwd", "ob_linear_fwd", "ob_linear_bwd", "ob_adamw_step",
+              "ob_adamw_moments", "ob_attn_fwd"):
+        setattr(library, n, lambda *a, n=n: calls.setdefault(n, []).append(a) or ob.OB_OK)
+
+    def empty(*shape, dtype=None, device=None):
+        shape = shape[0] if shape and not isinstance(shape[0], int) else shape
+        return _zeros(*shape, dtype=dtype or torch.get_default_dtype(), at=device.index)
+    monkeypatch.setattr(torch, "empty", empty)
+    return calls
+
+
+@pytest.mark.parametrize("default", [torch.float64, BF16])
+def test_statistics_are_float32_whatever_torch_makes(recorded, default):
+    x, q = _zeros(4, 64).requires_grad_(), _zeros(1, 8, 2, 64).requires_grad_()
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(default)
+    try:
+        M.layer_norm(x)
+        M.attention(q, q, q)
+    finally:
+        torch.set_default_dtype(before)
+    assert len(recorded["ob_layernorm_fwd"]) == len(recorded["ob_attn_fwd"]) == 1
