@@ -1147,7 +1147,7 @@ def ob_linear_bwd(dy, x, w, dx=None, dw=None, dbias=None, z=None, activation="no
     wr, wc = (K, N) if kn else (N, K)
     lddw = None
     if dw is not None:
-        if dw.shape != w.shape or (wr > 1 and wc > 1 and dw.stride(1 - kn) != 1):
+        if dw.shape != w.shape or (wc > 1 and dw.stride(1 - kn) != 1):
             _refuse(f"dw must be {tuple(w.shape)} with the contiguous dimension of w")
         lddw = dw.stride(kn) if wr > 1 else wc
     pairs, off = _matrices(at, dtype, (("dy", dy, M, N, None), ("x", x, M, K, None), ("w", w, wr, wc, ldw),

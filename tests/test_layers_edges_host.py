@@ -129,3 +129,12 @@ def test_statistics_are_float32_whatever_torch_makes(recorded, default):
     finally:
         torch.set_default_dtype(before)
     assert len(recorded["ob_layernorm_fwd"]) == len(recorded["ob_attn_fwd"]) == 1
+
+
+def test_gradient_of_one_row_of_weights_is_contiguous(recorded):
+    """Else what lies between its elements would be written."""
+    x, w, dy = _zeros(4, 64), _zeros(1, 64), _zeros(4, 1)
+    _refused(lambda: ob.ob_linear_bwd(dy, x, w, dw=_zeros(1, 128)[:, ::2]), "dw")
+    ob.ob_linear_bwd(dy, x, w, dw=_zeros(1, 128)[:, :64])
+    ob.ob_linear_bwd(dy, x, _zeros(1, 128)[:, ::2], dw=_zeros(1, 192)[:, ::3])  # stored [K, N]: 64 rows of one
+    assert len(recorded["ob_linear_bwd"]) == 2
