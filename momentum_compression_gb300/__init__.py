@@ -1363,8 +1363,7 @@ class AdamW:
         import torch
         if self.state_bits == 32:
             return self.m, self.v
-        m, v = (torch.empty(self.m.numel(), dtype=torch.bfloat16, device=self.device)
-                for _ in range(2))
+        m, v = (_scratch(2 * self.m.numel(), self.m, stream).view(torch.bfloat16) for _ in range(2))
         ob_adamw_moments(self.m, self.v, self.m_exp, self.v_exp, m, v, stream)
         return m, v
 

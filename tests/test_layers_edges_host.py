@@ -138,3 +138,36 @@ def test_gradient_of_one_row_of_weights_is_contiguous(recorded):
     ob.ob_linear_bwd(dy, x, w, dw=_zeros(1, 128)[:, :64])
     ob.ob_linear_bwd(dy, x, _zeros(1, 128)[:, ::2], dw=_zeros(1, 192)[:, ::3])  # stored [K, N]: 64 rows of one
     assert len(recorded["ob_linear_bwd"]) == 2
+
+
+@pytest.fixture
+def adamw(recorded, monkeypatch):
+    """AdamW of a tensor of 300 elements, two blocks of state."""
+    real = torch.tensor
+
+    def tensor(data, dtype=None, device=None):
+        t = _zeros(len(data), dtype=dtype, at=device.index)
+        t.copy_(real(data, dtype=dtype))
+        return t
+    monkeypatch.setattr(torch, "tensor", tensor)
+
+    def make(bits=8, **state):
+        t = F32 if bits == 32 else torch.uint8
+        given = dict(m=_zeros(512, dtype=t), v=_zeros(512, dtype=t), step=0)
+        if bits == 8:
+            given.update(m_exp=_zeros(2, dtype=t), v_exp=_zeros(2, dtype=t))
+        given.update(state)
+        return ob.AdamW([_zeros(300, dtype=F32)], state_bits=bits, state={k: v for k, v in given.items() if v is not None})
+    return make
+
+
+@pytest.mark.parametrize("stream", [None, 77])
+def test_moments_values_are_made_on_their_stream(adamw, library, recorded, monkeypatch, stream):  # noqa: F811
+    """What torch's allocator hands out belongs to the stream that is current then."""
+    made = []
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: made.append(library.entered[-1:]) or empty(*a, **kw))
+    m, v = adamw().moments(stream=stream)
+    assert [t.cuda_stream for s in made for t in s] == ([] if stream is None else [77, 77])
+    assert m.dtype == v.dtype == BF16 and m.shape == v.shape == (512,) and m.data_ptr() != v.data_ptr()
+    assert recorded["ob_adamw_moments"][0][-1] == (0x1000 if stream is None else 77)
