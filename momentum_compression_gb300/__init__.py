@@ -1369,7 +1369,9 @@ class AdamW:
 
     def state(self):
         """The moments' buffers and the number of steps taken, for `state=` of another
-        AdamW.  Waits for the device."""
+        AdamW.  Waits for the device: steps may be under way on any stream."""
+        import torch
+        torch.cuda.synchronize(self.device)
         out = dict(m=self.m, v=self.v, step=int(self.counter[0].item()))
         if self.state_bits == 8:
             out.update(m_exp=self.m_exp, v_exp=self.v_exp)

@@ -171,3 +171,10 @@ def test_moments_values_are_made_on_their_stream(adamw, library, recorded, monke
     assert [t.cuda_stream for s in made for t in s] == ([] if stream is None else [77, 77])
     assert m.dtype == v.dtype == BF16 and m.shape == v.shape == (512,) and m.data_ptr() != v.data_ptr()
     assert recorded["ob_adamw_moments"][0][-1] == (0x1000 if stream is None else 77)
+
+
+def test_state_waits_for_steps_on_every_stream(adamw, monkeypatch):
+    """Steps may be under way on a stream that is not the current one."""
+    opt = adamw(32)
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: opt.counter[0].fill_(5.0))
+    assert opt.state()["step"] == 5
