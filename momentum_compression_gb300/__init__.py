@@ -1291,13 +1291,16 @@ class AdamW:
         blocks = [-(-k // OB_ADAMW_BLOCK) for k in self._sizes]
         total = OB_ADAMW_BLOCK * sum(blocks)
         dtype = torch.float32 if state_bits == 32 else torch.uint8
-        given = state or {}
-        step = int(given.get("step", 0))
+        given = dict(step=0) if state is None else state
+        step = given.get("step")
+        if step is None or isinstance(step, str) or not step >= 0 or step % 1:
+            _refuse(f"state: step = {step!r} must be the number of steps taken")
+        step = int(step)
 
         def buffer(name, count, dtype):
             t = given.get(name)
             if t is None:
-                if state:
+                if state is not None:
                     _refuse(f"state has no {name}")
                 return torch.zeros(count, dtype=dtype, device=self.device)
             if t.dtype != dtype or t.numel() != count or not t.is_contiguous() \

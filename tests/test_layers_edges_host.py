@@ -1,5 +1,6 @@
 """Calls of layer norm, the dense layer and AdamW at the edge of what they allow, without a
 GPU: sizes of zero, strides of zero, arrays that are not where they seem."""
+import math
 import os
 import subprocess
 import sys
@@ -178,3 +179,13 @@ def test_state_waits_for_steps_on_every_stream(adamw, monkeypatch):
     opt = adamw(32)
     monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: opt.counter[0].fill_(5.0))
     assert opt.state()["step"] == 5
+
+
+def test_a_state_that_is_not_whole_is_refused(adamw):
+    """Else moments would go on as if no step had been taken, or none had been handed over."""
+    assert all(adamw(32, step=s).counter[0] == 7 for s in (7, 7.0, torch.full((), 7)))
+    for missing in ("m", "v", "m_exp", "v_exp", "step"):
+        _refused(lambda: adamw(8, **{missing: None}), missing)
+    for step in (-1, 2.5, math.nan, "3"):
+        _refused(lambda: adamw(32, step=step), "step")
+    _refused(lambda: ob.AdamW([_zeros(300, dtype=F32)], state={}), "state")
