@@ -1184,6 +1184,8 @@ def ob_adamw_step(config, tensors, grads, m, v, counter, m_exp=None, v_exp=None,
     many tensors or addresses (None: the tensor stays as it is), on CUDA device `at`."""
     import torch
     at = counter.get_device() if at is None else at
+    if at < 0:
+        _refuse("the step's arrays must be on a CUDA device")
     if len(grads) != len(tensors):
         _refuse(f"{len(grads)} gradients for {len(tensors)} tensors")
     for i, (t, g) in enumerate(zip(tensors, grads)):

@@ -189,3 +189,14 @@ def test_a_state_that_is_not_whole_is_refused(adamw):
     for step in (-1, 2.5, math.nan, "3"):
         _refused(lambda: adamw(32, step=step), "step")
     _refused(lambda: ob.AdamW([_zeros(300, dtype=F32)], state={}), "state")
+
+
+def test_adamw_step_refuses_host_memory(recorded):
+    """Arrays that all lie on the host are on one device, but not on one that kernels run on."""
+    host = lambda n, t=F32: torch.zeros(n, dtype=t)
+    p, c = host(256), host(4, torch.float64)
+    table = (ob.ob_adamw_tensor * 1)(ob.ob_adamw_tensor(p.data_ptr(), 0, 256, 0.0, ob.OB_TYPE_F32, 0))
+    config = ob.ob_adamw(32, ob.OB_TYPE_F32, 0.1, 0.9, 0.99, 1e-8)
+    for kw in ({}, dict(at=-1)):
+        _refused(lambda: ob.ob_adamw_step(config, table, [host(256)], host(256), host(256), c, **kw), "CUDA")
+    assert "ob_adamw_step" not in recorded
