@@ -199,7 +199,7 @@ class _Linear(torch.autograd.Function):
             z = torch.empty(shape, device=x.device, dtype=x.dtype)
         ob_linear_fwd(x, w, y, bias=bias, residual=residual, z=z, activation=activation)
         ctx.save_for_backward(x, w, z)
-        ctx.activation = activation
+        ctx.activation, ctx.residual_shape = activation, None if residual is None else residual.shape
         return y
 
     @staticmethod
@@ -213,7 +213,7 @@ class _Linear(torch.autograd.Function):
         if any(need[:3]):
             ob_linear_bwd(_as_rows(dy), x, w, dx=dx, dw=dw, dbias=db, z=z,
                           activation=ctx.activation)
-        return dx, dw, db, dy if need[3] else None, None, None
+        return dx, dw, db, dy.reshape(ctx.residual_shape) if need[3] else None, None, None
 
 
 def _as_weights(w):

@@ -200,3 +200,16 @@ def test_adamw_step_refuses_host_memory(recorded):
     for kw in ({}, dict(at=-1)):
         _refused(lambda: ob.ob_adamw_step(config, table, [host(256)], host(256), host(256), c, **kw), "CUDA")
     assert "ob_adamw_step" not in recorded
+
+
+def test_gradient_of_a_residual_has_its_shape(recorded):
+    """The forward pass takes rows in any leading shape; so does the backward pass."""
+    x, w, dy = _zeros(2, 2, 64), _zeros(32, 64), _zeros(2, 2, 32)
+    dy.copy_(torch.arange(128).view(2, 2, 32))
+    for shape in ((4, 32), (2, 2, 32), (4, 1, 32)):
+        r = _zeros(*shape).requires_grad_()
+        got, = torch.autograd.grad(M.linear(x, w, residual=r), r, dy)
+        assert got.shape == r.shape and torch.equal(got.reshape(-1), dy.reshape(-1))
+    r = _zeros(32).requires_grad_()
+    got, = torch.autograd.grad(M.linear(x[0, :1], w, residual=r), r, dy[0, :1])
+    assert torch.equal(got, dy[0, 0])
