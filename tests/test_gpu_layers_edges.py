@@ -88,3 +88,133 @@ def test_gelu_slope_is_near_relative_to_itself(dtype, act, cols):
     ob.ob_linear_bwd(torch.ones_like(wide), torch.zeros_like(wide), w, dx=dx, z=wide, activation=act)
     _, want = _act64(z.double(), act)
     L.within(dx[:, 0], want, 2.0 ** -14 * want.abs() + 2.0 ** -19 * (z.double() > -2), act)
+
+
+# ---------------------------------------------------------------------------
+# Layer norm
+# ---------------------------------------------------------------------------
+
+# rows that share a warp, a warp's, a block's (few and many), rows read again; odd widths
+ROWS = [(3, 7), (1001, 64), (1001, 100), (300, 384), (37, 768), (1300, 768), (9, 1001), (300, 1024), (65, 2050),
+        (305, 4096), (3, 8192), (310, 9000), (3, 20000)]
+
+
+def _rows(rows, cols, dtype, seed, shift):
+    """Rows at an aligned or an odd start, away from 0."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    flat = torch.empty(rows * cols + shift, device="cuda", dtype=dtype)
+    t = flat[shift:].view(rows, cols)
+    t.copy_(torch.randn(rows, cols, generator=g, device="cuda") * 1.5 + 0.7)
+    return t
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("rows,cols", ROWS)
+@pytest.mark.parametrize("shift", [0, 1])
+def test_layer_norm_statistics(dtype, rows, cols, shift):
+    """mean and rstd themselves, within the errors that layers_ref derives for y from them."""
+    x = _rows(rows, cols, dtype, 3, shift)
+    mean, rstd = (torch.full((rows,), math.nan, device="cuda") for _ in range(2))
+    ob.ob_layernorm_fwd(x, torch.empty_like(x), mean=mean, rstd=rstd)
+    _, _, m, r = L.layer_norm(x, None, None, 1e-5)
+    c, x = L.row_sums(cols), x.double()
+    em = c * x.abs().mean(1) + L.U32 * m.abs()
+    var = (x - m[:, None]).square().mean(1)
+    er = 0.5 * (2 * var.sqrt() * em + em * em + (c + 4 * L.U32) * var) / (var + 1e-5) + 4 * L.U32
+    assert ((mean.double() - m).abs() <= em + L.U32 * m.abs()).all()
+    assert ((rstd.double() - r).abs() <= er * r).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,cols", ROWS)
+@pytest.mark.parametrize("shift", [0, 1])
+def test_layer_norm_in_place(dtype, rows, cols, shift):
+    """y and sum may be x and residual: the same bits."""
+    make = lambda: (_rows(rows, cols, dtype, 5, shift), _rows(rows, cols, dtype, 6, shift))
+    w = _rows(1, cols, dtype, 7, 0)[0]
+    x, r = make()
+    y, s = torch.empty_like(x), torch.empty_like(x)
+    ob.ob_layernorm_fwd(x, y, w, w, residual=r, sum=s)
+    for of_y, of_s in (("x", "r"), ("r", "x"), ("x", None), (None, "x"), ("r", None), (None, "r")):
+        a, b = make()
+        at = dict(x=a, r=b)
+        y2, s2 = at.get(of_y, torch.empty_like(a)), at.get(of_s, torch.empty_like(a))
+        ob.ob_layernorm_fwd(a, y2, w, w, residual=b, sum=s2)
+        assert torch.equal(y2, y) and torch.equal(s2, s), (of_y, of_s)
+    x, _ = make()
+    ob.ob_layernorm_fwd(x, y, w)
+    ob.ob_layernorm_fwd(x, x, w)
+    assert torch.equal(x, y)
+
+
+# ---------------------------------------------------------------------------
+# The dense layer
+# ---------------------------------------------------------------------------
+
+# few rows (whole and cut among a cluster), tiles, tiles cut along the sum, pairs of blocks; odd sizes
+SIZES = [(1, 40, 8), (8, 512, 4096), (128, 768, 768), (300, 200, 300), (257, 511, 513), (250, 768, 96),
+         (300, 64, 2000), (2816, 2304, 4096), (2570, 1030, 1000)]
+
+
+@pytest.mark.parametrize("Mr,N,K", SIZES)
+@pytest.mark.parametrize("kn", [False, True])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("keep", [False, True])
+def test_dense_adds_to_its_residual_in_place(Mr, N, K, kn, shift, keep):
+    """y may be residual: the same bits."""
+    x, r = _rows(Mr, K, BF16, 1, shift), _rows(Mr, N, BF16, 2, shift)
+    w = _rows(*((K, N) if kn else (N, K)), BF16, 3, shift).div_(K ** 0.5)
+    w, b = w.t() if kn else w, _rows(1, N, BF16, 4, 0)[0]
+    y, z, z2 = torch.empty_like(r), *(torch.empty_like(r) if keep else None for _ in range(2))
+    ob.ob_linear_fwd(x, w, y, b, r, z, "gelu")
+    ob.ob_linear_fwd(x, w, r, b, r, z2, "gelu")
+    assert torch.equal(y, r)
+    if keep:
+        assert torch.equal(z, z2)
+
+
+def test_broadcast_inputs_and_gradients():
+    """model.layer_norm and model.linear take views whose elements are shared, and gradients that are;
+    autograd sums them over what was broadcast."""
+    mk = lambda *s: _rows(1, math.prod(s), BF16, sum(s), 0).view(*s)
+    x, w, b, res = mk(64), mk(96, 64), mk(96), mk(96)
+    lnw = mk(1).expand(64)
+    leaves = [t.detach().requires_grad_() for t in (x, w, b, res, lnw[:1])]
+    full = [x.expand(5, 7, 64).contiguous(), w, b, res.expand(5, 7, 96).contiguous(), lnw.contiguous()]
+    full = [t.detach().requires_grad_() for t in full]
+
+    def out(x, w, b, res, lnw):
+        return M.linear(M.layer_norm(x, lnw), w, b, "gelu", res)
+    a, c = leaves, full
+    y = out(a[0].expand(5, 7, 64), a[1], a[2], a[3].expand(5, 7, 96), a[4].expand(64))
+    y2 = out(*c)
+    assert torch.equal(y, y2)
+    dy = mk(1).expand(5, 7, 96)
+    got, want = torch.autograd.grad(y, a, dy), torch.autograd.grad(y2, c, dy.contiguous())
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+    for g, f, shape in ((got[0], want[0], (35, 64)), (got[3], want[3], (35, 96)), (got[4], want[4], (64, 1))):
+        f = f.double().view(shape)
+        # autograd's sums over the broadcast dimensions, each rounded to bf16
+        assert ((g.double().view(-1) - f.sum(0)).abs() <= 3 * 2.0 ** -8 * f.abs().sum(0)).all()
+
+
+# ---------------------------------------------------------------------------
+# AdamW
+# ---------------------------------------------------------------------------
+
+def test_adamw_on_another_stream():
+    """Steps and the moments' values on a stream that is not the current one, and state() after them."""
+    def run(stream):
+        p = torch.ones(1 << 22, device="cuda")
+        g = torch.full_like(p, 0.5)
+        opt = ob.AdamW([p], lr=1e-2, state_bits=8, seed=2)
+        torch.cuda.synchronize()
+        for _ in range(20):
+            opt.step([g], stream=stream)
+        values = opt.moments(stream=stream)
+        return opt.state(), p, values
+    (s, p, v), (s2, p2, v2) = run(None), run(torch.cuda.Stream())
+    assert s["step"] == s2["step"] == 20 and torch.equal(p, p2)
+    assert all(torch.equal(a, b) for a, b in zip(v, v2))
+    assert all(torch.equal(s[n], s2[n]) for n in ("m", "v", "m_exp", "v_exp"))
