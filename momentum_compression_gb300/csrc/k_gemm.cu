@@ -239,7 +239,8 @@ __device__ __forceinline__ bool tiled_at(const GemmArgs& a, int64_t n) {
 struct Out {
   uint8_t* buf;
   uint64_t* bar;
-  uint32_t par;  // bit b: of buffer b's next phase
+  uint32_t par;    // bit b: of buffer b's next phase
+  uint32_t asked;  // lane 0; bit b differs from par's while a load of buffer b is on its way
 
   // Buffer of a group's y; z, if there is one, has the other.
   __device__ __forceinline__ int of(const Epilogue& e, int g) const { return e.z.data ? 1 : g & 1; }
@@ -247,6 +248,14 @@ struct Out {
   __device__ __forceinline__ void load(const GemmArgs& a, int b, int64_t m0, int64_t n0) {
     mbar_arrive_expect_tx(&bar[b], kBuf);
     tma_load2(buf + b * kBuf, &a.residual, (int)n0, (int)m0, &bar[b]);
+    asked ^= 1u << b;
+  }
+  // A wait ran out: lets the loads that are on their way land before the block ends.
+  __device__ __forceinline__ void drain() {
+    if ((threadIdx.x & 31) == 0)
+      for (int b = 0; b < 2; ++b)
+        if ((asked ^ par) >> b & 1) mbar_wait(&bar[b], par >> b & 1, &g_linear_error, kErrDrain);
+    __syncwarp();
   }
   // Before a unit's (parts of) GROUPS groups from (m0, n0) on: the buffers' last stores have
   // been read, and the residual is on its way.
@@ -275,9 +284,8 @@ struct Out {
       __syncwarp();
     }
     if (e.residual.data) {
-      const bool ok = warp_wait(&bar[b], par >> b & 1, &g_linear_error);
+      if (!warp_wait(&bar[b], par >> b & 1, &g_linear_error)) return false;
       par ^= 1u << b;
-      if (!ok) return false;
     }
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
@@ -463,8 +471,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
         if (++buf == 2) buf = 0, sum_par ^= 1;
       }
       if (!ok) {
-        if (CG == 2)
-          pair_commit(leader, &bar.drain);
+        // the copies, which were asked for as far as the stages go, and the products
+        for (int64_t i = n; i < n + S::kStages && i < mine; ++i)
+          mbar_wait(&bar.full[i % S::kStages], (i / S::kStages) & 1, &g_linear_error, kErrDrain);
+        if (CG == 2)  // the other block waits for no such arrival, and may have ended
+          pair_commit_here(leader, &bar.drain);
         else
           mma_commit(leader, &bar.drain);
         mbar_wait(&bar.drain, 0, &g_linear_error, kErrDrain);
@@ -476,7 +487,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
     // of the columns each.
     constexpr int kCols = S::kCols / (kEpWarps / 4);
     const int w = warp - 2, lanes0 = (warp & 3) * 32, col0 = (w >> 2) * kCols;
-    Out out{smem + S::kArea + w * 2 * kBuf, bar.residual[w], 0};
+    Out out{smem + S::kArea + w * 2 * kBuf, bar.residual[w], 0, 0};
     float* turn = reinterpret_cast<float*>(out.buf);
     const uint32_t lanes = (uint32_t)lanes0 << 16;
     const uint32_t empty = CG == 2 ? cluster_addr(smem_u32(&bar.sum_empty[0]), 0) : 0;
@@ -512,7 +523,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
         }
       };
 #pragma unroll 1
-      for (int g = 0; g < kCols / kGroup; ++g) {
+      for (int g = 0; ok && g < kCols / kGroup; ++g) {
         const int64_t n = n0 + g * kGroup;
         const bool inside = m0 < a.M && n < a.N;
         if (u.part || !inside || !tiled_at(a, n)) {
@@ -539,14 +550,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
           else
             finish_turned<__half>(a.ep, turn, m0, n, a.M, a.N);
         } else if (a.ep.type == OB_TYPE_BF16) {
-          ok = out.group<__nv_bfloat16>(a, g, m0, n, get) && ok;
+          ok = out.group<__nv_bfloat16>(a, g, m0, n, get);
         } else {
-          ok = out.group<__half>(a, g, m0, n, get) && ok;
+          ok = out.group<__half>(a, g, m0, n, get);
         }
       }
       __syncwarp();
       if (++buf == 2) buf = 0, par ^= 1;
     }
+    if (!ok) out.drain();
     if (lane == 0) store_wait_read<0>();
     __syncwarp();
     tc_fence_before();
@@ -600,7 +612,7 @@ __global__ void __launch_bounds__(256) k_gemm_parts(const __grid_constant__ Gemm
     p1 = owner(last);
     if (p0 == p1) return;  // one worker had it whole
   }
-  Out out{bufs[w], bars[w], 0};
+  Out out{bufs[w], bars[w], 0, 0};
   auto get = [&](int half, float (&z)[16]) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) z[k] = 0.0f;
@@ -632,10 +644,9 @@ __global__ void __launch_bounds__(256) k_gemm_parts(const __grid_constant__ Gemm
   };
   if (tiled_at(a, n0)) {
     out.begin<1>(a, m0, n0);
-    if (a.ep.type == OB_TYPE_BF16)
-      out.group<__nv_bfloat16>(a, 0, m0, n0, get);
-    else
-      out.group<__half>(a, 0, m0, n0, get);
+    const bool ok = a.ep.type == OB_TYPE_BF16 ? out.group<__nv_bfloat16>(a, 0, m0, n0, get)
+                                              : out.group<__half>(a, 0, m0, n0, get);
+    if (!ok) out.drain();
     if (lane == 0) store_wait_read<0>();
     return;
   }

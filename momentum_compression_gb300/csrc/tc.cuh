@@ -290,6 +290,15 @@ __device__ __forceinline__ void pair_commit(uint32_t leader, uint64_t* bar) {
       "r"(leader)
       : "memory");
 }
+// The same on this block's `bar` alone.
+__device__ __forceinline__ void pair_commit_here(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
 // On a barrier at a cluster address; orders nothing but what tensor-memory fences order (a
 // release would wait for every store that is under way).
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
