@@ -320,7 +320,13 @@ __global__ void __launch_bounds__(kBwdThreads + 32, kBwdThreads == 256 ? 2 : 1)
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
-    if (!fine) break;
+    if (!fine) {  // let what was asked for land before the block ends
+      for (int i = 0; i < p.stages && u + (uint64_t)i * gridDim.x < units; ++i) {
+        mbar_wait(&full[st], par, &g_layernorm_error, kErrDrain);
+        if (++st == p.stages) st = 0, par ^= 1;
+      }
+      break;
+    }
     if (++st == p.stages) st = 0, par ^= 1;
   }
   if (!a.partial) return;
