@@ -218,3 +218,76 @@ def test_adamw_on_another_stream():
     assert s["step"] == s2["step"] == 20 and torch.equal(p, p2)
     assert all(torch.equal(a, b) for a, b in zip(v, v2))
     assert all(torch.equal(s[n], s2[n]) for n in ("m", "v", "m_exp", "v_exp"))
+
+
+# ---------------------------------------------------------------------------
+# Arrays of more than 2^32 elements
+# ---------------------------------------------------------------------------
+
+LONG = 512 * 4099  # rows; of 2056 columns they hold 4.3e9 elements
+
+
+def _long(cols, seed):
+    """LONG rows, the same 4099 again and again."""
+    return _rows(4099, cols, BF16, seed, 0).expand(512, 4099, cols).reshape(LONG, cols)
+
+
+def test_layer_norm_of_long_arrays():
+    """The last rows are right, and equal rows have equal bits."""
+    cols, tail = 2056, slice(LONG - 300, LONG)
+    x, w = _long(cols, 1), _rows(1, cols, BF16, 2, 0)[0]
+    y = torch.empty_like(x)
+    mean, rstd = (torch.empty(LONG, device="cuda") for _ in range(2))
+    ob.ob_layernorm_fwd(x, y, w, w, mean=mean, rstd=rstd)
+    want, err, _, _ = L.layer_norm(x[tail], w, w, 1e-5)
+    L.within(y[tail], want, err, "y")
+    assert torch.equal(y[tail], y[4099 - 300:4099])
+    dx = torch.empty_like(x)
+    ob.ob_layernorm_bwd(y, x, mean, rstd, dx, w)
+    (want, _, _), (err, _, _) = L.layer_norm_grad(y[tail], x[tail], mean[tail], rstd[tail], w, None)
+    L.within(dx[tail], want, err, "dx")
+    assert torch.equal(dx[tail], dx[4099 - 300:4099])
+
+
+@pytest.mark.parametrize("kn", [False, True])
+def test_dense_of_long_arrays(kn):
+    N, K, tail = 2056, 64, slice(LONG - 300, LONG)
+    x, b = _long(K, 3), _rows(1, N, BF16, 4, 0)[0]
+    w = _rows(*((K, N) if kn else (N, K)), BF16, 5, 0).div_(8)
+    w = w.t() if kn else w
+    y, z = (torch.empty(LONG, N, device="cuda", dtype=BF16) for _ in range(2))
+    ob.ob_linear_fwd(x, w, y, b, None, z, "gelu")
+    (z64, y64), (ez, ey) = L.dense(x[tail], w, b, None, "gelu")
+    L.within(y[tail], y64, ey, "y")
+    L.within(z[tail], z64, ez, "z")
+    dx = torch.empty_like(x)
+    ob.ob_linear_bwd(y, x, w, dx=dx, z=z, activation="gelu")
+    (want, _, _), (err, _, _) = L.dense_grad(y[tail], x[tail], w, z[tail], "gelu")
+    L.within(dx[tail], want, err, "dx")
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_of_a_long_tensor(bits):
+    """The last elements take the step that they take by themselves, the random numbers of their own place."""
+    n = (1 << 32) + 1000
+    p = torch.full((n,), 0.5, device="cuda", dtype=BF16)
+    small = _rows(1, 5000, BF16, 6, 0)[0]
+    g = torch.zeros(n, device="cuda", dtype=BF16)
+    g[-5000:] = small
+    opt = ob.AdamW([p], lr=1e-2, weight_decay=0.0, state_bits=bits, seed=9)
+    opt.step([g])
+    first = (n - 5000) // 256 * 256
+    k = n - first
+    pad = -k % 256
+    np_ = lambda t: torch.nn.functional.pad(t[first:].float(), (0, pad)).cpu().numpy()
+    zero = torch.zeros(k + pad, dtype=torch.uint8 if bits == 8 else F32).numpy()
+    exps = torch.zeros((k + pad) // 256, dtype=torch.uint8).numpy()
+    q, size, new = L.adamw(np_(torch.full_like(p, 0.5)), np_(g), zero, zero, 1, 9, first, 1e-2, 0.9, 0.999, 1e-8, 0.0,
+                           1.0, bits, exps, exps)
+    L.within(p[first:], torch.from_numpy(q[:k]).cuda(), torch.from_numpy(size[:k]).cuda() * 2.0 ** -20 + 2 * L.U32, "p")
+    got = [opt.m[first:], opt.v[first:]]
+    if bits == 8:
+        got += [opt.m_exp[first // 256:], opt.v_exp[first // 256:]]
+    for a, b in zip(got, new):
+        assert torch.equal(a.cpu(), torch.from_numpy(b))
+    assert (p[:first] == 0.5).all()
