@@ -174,9 +174,9 @@ __global__ void __launch_bounds__(kBwdThreads + 32, kBwdThreads == 256 ? 2 : 1)
       }
       if (++st == p.stages) st = 0, par ^= 1;
     }
-    if (!ok)  // a wait ran out: let what is in flight land before the block ends
-      for (uint32_t i = n > (uint32_t)p.stages ? n - p.stages : 0; i < n; ++i)
-        mbar_wait(&full[i % p.stages], (i / p.stages) & 1, &g_layernorm_error, kErrDrain);
+    // What is in flight lands before the block ends, whoever's wait ran out.
+    for (uint32_t i = n > (uint32_t)p.stages ? n - p.stages : 0; i < n; ++i)
+      mbar_wait(&full[i % p.stages], (i / p.stages) & 1, &g_layernorm_error, kErrDrain);
     return;
   }
 
@@ -320,13 +320,7 @@ __global__ void __launch_bounds__(kBwdThreads + 32, kBwdThreads == 256 ? 2 : 1)
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
-    if (!fine) {  // let what was asked for land before the block ends
-      for (int i = 0; i < p.stages && u + (uint64_t)i * gridDim.x < units; ++i) {
-        mbar_wait(&full[st], par, &g_layernorm_error, kErrDrain);
-        if (++st == p.stages) st = 0, par ^= 1;
-      }
-      break;
-    }
+    if (!fine) break;
     if (++st == p.stages) st = 0, par ^= 1;
   }
   if (!a.partial) return;
