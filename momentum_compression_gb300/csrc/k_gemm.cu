@@ -239,8 +239,7 @@ __device__ __forceinline__ bool tiled_at(const GemmArgs& a, int64_t n) {
 struct Out {
   uint8_t* buf;
   uint64_t* bar;
-  uint32_t par;    // bit b: of buffer b's next phase
-  uint32_t asked;  // lane 0; bit b differs from par's while a load of buffer b is on its way
+  uint32_t par;  // bit b: of buffer b's next phase
 
   // Buffer of a group's y; z, if there is one, has the other.
   __device__ __forceinline__ int of(const Epilogue& e, int g) const { return e.z.data ? 1 : g & 1; }
@@ -248,14 +247,11 @@ struct Out {
   __device__ __forceinline__ void load(const GemmArgs& a, int b, int64_t m0, int64_t n0) {
     mbar_arrive_expect_tx(&bar[b], kBuf);
     tma_load2(buf + b * kBuf, &a.residual, (int)n0, (int)m0, &bar[b]);
-    asked ^= 1u << b;
   }
-  // A wait ran out: lets the loads that are on their way land before the block ends.
-  __device__ __forceinline__ void drain() {
-    if ((threadIdx.x & 31) == 0)
-      for (int b = 0; b < 2; ++b)
-        if ((asked ^ par) >> b & 1) mbar_wait(&bar[b], par >> b & 1, &g_linear_error, kErrDrain);
-    __syncwarp();
+  // A wait ran out: lets loads that may be on their way land before the block ends.
+  __device__ __forceinline__ void drain(const Epilogue& e) {
+    for (int b = 0; e.residual.data && b < 2; ++b)
+      mbar_wait(&bar[b], par >> b & 1, &g_linear_error, kErrDrain);
   }
   // Before a unit's (parts of) GROUPS groups from (m0, n0) on: the buffers' last stores have
   // been read, and the residual is on its way.
@@ -487,7 +483,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
     // of the columns each.
     constexpr int kCols = S::kCols / (kEpWarps / 4);
     const int w = warp - 2, lanes0 = (warp & 3) * 32, col0 = (w >> 2) * kCols;
-    Out out{smem + S::kArea + w * 2 * kBuf, bar.residual[w], 0, 0};
+    Out out{smem + S::kArea + w * 2 * kBuf, bar.residual[w], 0};
     float* turn = reinterpret_cast<float*>(out.buf);
     const uint32_t lanes = (uint32_t)lanes0 << 16;
     const uint32_t empty = CG == 2 ? cluster_addr(smem_u32(&bar.sum_empty[0]), 0) : 0;
@@ -558,7 +554,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       __syncwarp();
       if (++buf == 2) buf = 0, par ^= 1;
     }
-    if (!ok) out.drain();
+    if (!ok) out.drain(a.ep);
     if (lane == 0) store_wait_read<0>();
     __syncwarp();
     tc_fence_before();
@@ -612,7 +608,7 @@ __global__ void __launch_bounds__(256) k_gemm_parts(const __grid_constant__ Gemm
     p1 = owner(last);
     if (p0 == p1) return;  // one worker had it whole
   }
-  Out out{bufs[w], bars[w], 0, 0};
+  Out out{bufs[w], bars[w], 0};
   auto get = [&](int half, float (&z)[16]) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) z[k] = 0.0f;
@@ -646,7 +642,7 @@ __global__ void __launch_bounds__(256) k_gemm_parts(const __grid_constant__ Gemm
     out.begin<1>(a, m0, n0);
     const bool ok = a.ep.type == OB_TYPE_BF16 ? out.group<__nv_bfloat16>(a, 0, m0, n0, get)
                                               : out.group<__half>(a, 0, m0, n0, get);
-    if (!ok) out.drain();
+    if (!ok) out.drain(a.ep);
     if (lane == 0) store_wait_read<0>();
     return;
   }
