@@ -792,7 +792,8 @@ ob_status ob_layernorm_bwd(const void* dy, size_t lddy, const void* x, size_t ld
  * act is of the z before it is rounded to be stored, act' of the stored one;
  * dz is rounded to the type as an operand of its products, dbias is summed in
  * fp32 from the values before that.  GELU is z Phi(z), GELU_TANH
- * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2. */
+ * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2; both are within 2^-15 of
+ * themselves before they are rounded, down to z = -12.5 and -9.9. */
 #define OB_ACT_NONE 0
 #define OB_ACT_RELU 1
 #define OB_ACT_GELU 2

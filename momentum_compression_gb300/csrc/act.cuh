@@ -4,11 +4,11 @@
 // q(a) e^(a^2 / 2) falls slowly from 1/2 to 1/40 at a = 16; it is t P(t), t = 1 / (1 + 0.35 a),
 // the form of Abramowitz and Stegun's 7.1.26.  That formula is off by 1.5e-7 whatever the
 // value, which is 2% of q(10); P here was fitted (linear programming over 3000 points of
-// [0, 16]) to be off by at most 4e-8 and 5e-6 of q(a) itself, so that a small y has its
-// digits too: a step of bf16 is 4e-3 of a value, of fp16 5e-4.  One exponential, one reciprocal
-// and ten multiply-adds; its slope has the same exponential.  The two multiply-adds more than
-// 7.1.26 cost 16384 x 4096 bf16 nothing forward (107 us) and dz 4 of 70 us.  The tanh form is
-// z / (1 + e^(-2u)).
+// [0, 16]) to be off by at most 4e-8 and 5e-6 of q(a) itself, fp32's roundings apart, so that
+// a small y has its digits too: a step of bf16 is 4e-3 of a value, of fp16 5e-4.  One
+// exponential, one reciprocal and ten multiply-adds; its slope has the same exponential.  The
+// two multiply-adds more than 7.1.26's cost 16384 x 4096 x 1024 bf16 nothing forward (107 us)
+// and make dz 74 us from 70.  The tanh form is z / (1 + e^(-2u)).
 #pragma once
 
 #include <type_traits>

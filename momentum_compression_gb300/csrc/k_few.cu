@@ -7,10 +7,11 @@
 // The sum is cut among a block's eight warps and among a cluster's blocks, which add what
 // they have through shared memory, in their order.
 // One row of 2048 by [8192][2048] bf16 takes 7.6 us (33.5 MB at 4.4 TB/s, the launch and the
-// ramp of one wave among it), eight 7.8, sixteen 10.5 (A's words take as many registers as
-// B's); [K][N] 9.2, 9.9 and 12.5.  8 x 4096 x 1024 takes 2.8 us, 8 x 768 x 768 2.3.  A in
-// shared memory, staged for two steps of all warps at a time, took 10.3 and 14.6 us for
-// eight and sixteen rows.
+// ramp of one wave among it), eight 7.7, sixteen 10.2 (A's words take as many registers as
+// B's); [K][N] 9.4, 9.7 and 12.5, where sixteen rows read B twice.  Those are weights from HBM,
+// 600 MB of them in turn; where L2 holds B, 4.2, 4.6 and 8.3 us.  8 x 4096 x 1024 takes 4.0 us
+// (2.8 from L2), 8 x 768 x 768 3.2 (2.3).  A in shared memory, staged for two steps of all
+// warps at a time, took 10.3 and 14.6 us for eight and sixteen rows.
 #include <type_traits>
 
 #include "act.cuh"
@@ -255,13 +256,16 @@ cudaError_t go(const Gemm& g, cudaStream_t s) {
 
 }  // namespace
 
-// Up to 16 rows this is the quicker way for any B (16 x 8192 x 2048 bf16: 10.5 us, 13.4 on
-// tiles of the matrix unit), up to 128 where what is read, B for every 16 rows, is less than
-// the tiles' start and end are worth: 64 x 2048 x 1024 5.4 and 8.3 us, 48 x 4096 x 1024
-// 9.6 and 8.3; and twice as much along a long sum, which the tiles cut and join: 64 x 1024 x
-// 4096 10.7 and 16.2, 32 x 2048 x 4096 11.3 and 18.2.
+// Up to 16 rows this is the quicker way for any B (weights from HBM, us here and on tiles of
+// the matrix unit: 16 x 8192 x 2048 bf16 10.2 and 13.4, by [K][N] weights 12.5 and 14.2; 16 x
+// 2048 x 8192 11.8 and 19.9, 13.8 and 19.6).  Up to 128 where what is read, B for every 16 rows
+// (by [K][N] weights for every eight), is less than the tiles' start and end are worth: 64 x 2048
+// x 1024 5.7 and 8.9, [K][N] 7.0 and 9.4; 48 x 4096 x 1024 would take 9.9 and 9.0, 10.6 and 9.5.
+// Twice as much along a long sum, which the tiles cut and join: 64 x 1024 x 4096 10.9 and 17.5,
+// 13.0 and 17.3; 128 x 1024 x 2048 8.6 and 12.6, 11.7 and 12.6.  One limit holds for both layouts.
 // Where a backward pass can put both products in one launch, those with a short sum stay on
-// the tiles from 17 rows on (128 x 768 x 768: 12.2 us together, 15.6 apart).
+// the tiles from 17 rows on (128 x 768 x 768: 12.2 us together, 15.6 apart); dx alone does too,
+// as the workspace's size is asked for without knowing which are wanted.
 bool few_rows(int64_t M, int64_t N, int64_t K, bool a_mn, bool pair) {
   if (a_mn || M > 128 || (M > 16 && pair && K < 2048)) return false;
   return M <= 16 || (M + 15) / 16 * N * K <= (K < 2048 ? 1 << 23 : 1 << 24);

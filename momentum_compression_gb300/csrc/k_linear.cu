@@ -3,9 +3,9 @@
 //
 // dz = dy act'(z) is made once, as the operand of both products of the backward
 // pass, and summed down the columns on the way: each block adds its share of
-// the rows, a second kernel the blocks' sums in their order.  HBM bounds it (16384 x 4096
-// bf16 with GELU 70 us for 403 MB, 5.7 TB/s; making it inside the products would do its
-// arithmetic once for every 256 columns of dx).
+// the rows, a second kernel the blocks' sums in their order.  HBM bounds it, and the
+// slope's arithmetic near to it (16384 x 4096 bf16 with GELU 74 us for 403 MB, 5.4 TB/s; making it
+// inside the products would do its arithmetic once for every 256 columns of dx).
 //
 // Copies by TMA want 16-byte boundaries: matrices that lie elsewhere are first
 // copied into the workspace, their rows padded to multiples of 16 bytes (the

@@ -8,7 +8,10 @@ numbers are named by (seed, offset): the backward pass draws the forward
 pass's mask again instead of storing it, so calls that must be independent
 (another layer, another step) take another offset.  They are values of the
 host: a CUDA graph repeats the masks that it captured.  Gradients are of first
-order: a graph of them (create_graph) is refused when it is differentiated."""
+order: a graph of them (create_graph) is refused when it is differentiated.
+A backward pass is captured into a CUDA graph by torch.autograd.grad, or by
+.backward() while no eager graph of the same leaves lives: torch adds to a
+leaf's .grad on the stream of the graph that was made first."""
 import torch
 from torch.autograd.function import once_differentiable
 
